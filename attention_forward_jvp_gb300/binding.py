@@ -1,10 +1,12 @@
-"""ctypes binding of the C ABI in include/attn_jvp.h.
+"""ctypes binding of the C ABI in include/attn_jvp.h and include/attn_paged.h.
 
 Argument marshalling only: shapes, strides and raw pointers of torch
 tensors are handed to ``libattn_jvp.so``; every arithmetic step runs in its
 CUDA kernels.  Outputs are allocated with torch (device memory plumbing).
-CPU (host) inputs are staged through the device: the host->device copies,
-the kernel and the device->host copies all run on the current stream.
+CPU (host) inputs of the attention entry points are staged through the
+device: the host->device copies, the kernel and the device->host copies all
+run on the current stream.  (The rotation and the paged cache take CUDA
+tensors only.)
 
 There is no fallback: if the library is missing or the GPU is absent the
 call raises.
@@ -12,6 +14,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -34,10 +37,20 @@ EXPORTS = (
     "attn_launch_count",
     "attn_set_wait_timeout_ns",
     "attn_debug_skip_first_load",
+    "attn_rope",
+    "attn_rope_f16",
+    "attn_rope_freqs",
+    "attn_rope_steps",
+    "attn_paged_append",
+    "attn_paged_append_f16",
+    "attn_paged_decode",
+    "attn_paged_decode_f16",
+    "attn_paged_decode_workspace",
 )
 
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED",
-          3: "ATTN_ERR_MISALIGNED", 4: "ATTN_ERR_CUDA", 5: "ATTN_ERR_TIMEOUT"}
+          3: "ATTN_ERR_MISALIGNED", 4: "ATTN_ERR_CUDA", 5: "ATTN_ERR_TIMEOUT",
+          6: "ATTN_ERR_PAGE"}
 
 
 class AttnShape(ctypes.Structure):
@@ -49,6 +62,37 @@ class AttnShape(ctypes.Structure):
 class AttnBias(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p), ("bias_stride", ctypes.c_int64 * 4),
                 ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64 * 4)]
+
+
+class AttnRopeSpec(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("out_scale", ctypes.c_float)]
+
+
+class AttnRopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("H", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
+
+
+class AttnRopeFreq(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("orig_len", ctypes.c_double), ("low_turns", ctypes.c_double),
+                ("high_turns", ctypes.c_double)]
+
+
+class AttnPagedCache(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("Dqk", ctypes.c_int32),
+                ("Dv", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p)]
+
+
+class AttnPagedNew(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("Hq", ctypes.c_int32),
+                ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2), ("q_stride", ctypes.c_int64 * 2),
+                ("q_out_stride", ctypes.c_int64 * 2)]
 
 
 class AttnError(RuntimeError):
@@ -103,6 +147,23 @@ def lib() -> ctypes.CDLL:
     L.attn_set_wait_timeout_ns.argtypes = [ctypes.c_uint64]
     L.attn_debug_skip_first_load.restype = None
     L.attn_debug_skip_first_load.argtypes = [i32]
+    i64, sz = ctypes.c_int64, ctypes.c_size_t
+    for f in (L.attn_rope, L.attn_rope_f16):
+        f.restype = i32
+        f.argtypes = [ctypes.c_int32, i64, ctypes.c_int32, ctypes.POINTER(AttnRopeSpec), vp, ctypes.c_int32, vp, vp,
+                      vp, ctypes.c_int32, i32, vp]
+    L.attn_rope_freqs.restype = i32
+    L.attn_rope_freqs.argtypes = [ctypes.POINTER(AttnRopeFreq), vp]
+    L.attn_rope_steps.restype = i32
+    L.attn_rope_steps.argtypes = [vp, ctypes.c_int32, vp]
+    for f in (L.attn_paged_append, L.attn_paged_append_f16):
+        f.restype = i32
+        f.argtypes = [ctypes.POINTER(AttnPagedCache), ctypes.POINTER(AttnPagedNew), ctypes.POINTER(AttnRopeSpec), vp]
+    L.attn_paged_decode_workspace.restype = sz
+    L.attn_paged_decode_workspace.argtypes = [ctypes.POINTER(AttnPagedCache), ctypes.c_int32]
+    for f in (L.attn_paged_decode, L.attn_paged_decode_f16):
+        f.restype = i32
+        f.argtypes = [ctypes.POINTER(AttnPagedCache), ctypes.c_int32, vp, vp, f32, vp, vp, vp, sz, vp]
     _LIB = L
     return L
 
@@ -490,3 +551,287 @@ def _host_call(fn, tensors, kw, n_out):
         for st in streams:
             st.synchronize()
     return tuple(h_out[:n_out])
+
+
+# ------------------------------------------- rotary positions, paged cache
+
+
+def _need_cuda(t: torch.Tensor, name: str, dtype, dev=None):
+    """A CUDA tensor of this type (on this device), its last dimension contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _call_on(dev, fn, *args):
+    """fn(*args, stream) with `dev` current; its status raised."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != 0:
+        _check(st)
+
+
+_ROPE_SCALING = {None: 0, "linear": 1, "base": 2, "by_parts": 3}
+
+
+class Rope:
+    """A rotation by position: what a program keeps of its position encoding.
+
+    Pair i of the first ``rot_dim`` elements of a head turns by
+    ``p * inv_freq[i]`` at position p, with ``inv_freq[i] = base ** (-2 i /
+    rot_dim)``; pairs are (i, i + rot_dim / 2), or (2i, 2i + 1) when
+    ``interleaved``; the result is multiplied by ``out_scale``.  ``scaling``
+    stretches the frequencies for contexts longer than those trained on:
+
+      None        as they are
+      "linear"    all divided by ``factor``
+      "base"      the base times ``factor ** (rot_dim / (rot_dim - 2))``
+      "by_parts"  divided by ``factor`` where a pair makes fewer than
+                  ``low_turns`` turns over ``orig_len`` positions, kept where
+                  it makes more than ``high_turns``, blended in between
+
+    or ``inv_freq`` (rot_dim / 2 numbers, float64) gives them outright.
+    ``inv_freq`` holds the frequencies (float64, CPU) and ``steps`` the
+    device array of the kernels (turns per position times 2^64)."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: Optional[str] = None,
+                 factor: float = 1.0, orig_len: float = 0, low_turns: float = 1.0, high_turns: float = 32.0,
+                 out_scale: float = 1.0, inv_freq=None, device=None):
+        rot_dim = int(rot_dim)
+        if rot_dim <= 0 or rot_dim % 2:
+            raise ValueError("rot_dim must be even and positive")
+        if scaling not in _ROPE_SCALING:
+            raise ValueError(f"scaling must be one of {list(_ROPE_SCALING)}, got {scaling!r}")
+        if not math.isfinite(out_scale):
+            raise ValueError("out_scale must be finite")
+        if inv_freq is None:
+            freq = AttnRopeFreq(rot_dim, _ROPE_SCALING[scaling], base, factor, orig_len, low_turns, high_turns)
+            f = torch.empty(rot_dim // 2, dtype=torch.float64)
+            _check(lib().attn_rope_freqs(ctypes.byref(freq), f.data_ptr()))
+        else:
+            if scaling is not None:
+                raise ValueError("inv_freq gives the frequencies outright: no scaling with it")
+            f = torch.as_tensor(inv_freq, dtype=torch.float64).detach().cpu().contiguous().clone()
+            if tuple(f.shape) != (rot_dim // 2,):
+                raise ValueError(f"inv_freq must hold {rot_dim // 2} numbers")
+        steps = torch.empty(rot_dim // 2, dtype=torch.int64)
+        _check(lib().attn_rope_steps(f.data_ptr(), rot_dim // 2, steps.data_ptr()))
+        dev = torch.device("cuda" if device is None else device)
+        if dev.type != "cuda":
+            raise ValueError(f"the rotation runs on a CUDA device, got {dev}")
+        self.rot_dim, self.interleaved, self.out_scale = rot_dim, bool(interleaved), float(out_scale)
+        self.inv_freq = f
+        self.steps = steps.to(dev)
+        self._spec = AttnRopeSpec(self.steps.data_ptr(), rot_dim, 1 if interleaved else 0, out_scale)
+        self._ref = ctypes.byref(self._spec)
+
+
+def attn_rope(tensors, rope: Rope, positions: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+              inverse: bool = False, out=None):
+    """Rotate up to four tensors by position, in one launch.  Returns a tuple
+    of them.
+
+    Dense: [B, H, N, D], equal but for H (q, k, their tangents, or gradients
+    with ``inverse``, which turns back: the transpose of the rotation).
+    ``positions`` int32 [B, N] or [N], default 0 .. N - 1.  Jagged:
+    [H, T, D] with int32 ``offsets`` [B + 1]; ``positions`` int32 [T],
+    default the place in the sequence; rows at offsets[B] and behind are not
+    written.  Any strides with contiguous rows of D (a transposed view of a
+    [B, N, H, D] projection); rows on 16-byte boundaries with D and rot_dim
+    multiples of 16 run at speed, others element by element.  ``out``: one
+    tensor for each, the input itself to rotate in place; by default new
+    contiguous ones."""
+    tensors = tuple(tensors)
+    n = len(tensors)
+    if not 1 <= n <= 4:
+        raise ValueError("attn_rope takes one to four tensors")
+    x0 = tensors[0]
+    dev, dt, nd = x0.device, _elem_type(x0), x0.dim()
+    jagged = offsets is not None
+    if nd != (3 if jagged else 4):
+        raise ValueError("tensors must be [B, H, N, D], or [H, T, D] with offsets")
+    B = 1 if jagged else x0.shape[0]
+    N, D = x0.shape[-2], x0.shape[-1]
+    if rope.rot_dim > D:
+        raise ValueError(f"rot_dim {rope.rot_dim} exceeds the head dim {D}")
+    if rope.steps.device != dev:
+        raise ValueError(f"the rotation is on {rope.steps.device}, the tensors on {dev}")
+    if out is None:
+        out = tuple(torch.empty(t.shape, dtype=dt, device=dev) for t in tensors)
+    else:
+        out = tuple(out)
+        if len(out) != n:
+            raise ValueError("out must hold one tensor for each input")
+    arr = (AttnRopeTensor * n)()
+    for i in range(n):
+        x, y, a = tensors[i], out[i], arr[i]
+        _need_cuda(x, "every tensor", dt, dev)
+        _need_cuda(y, "out", dt, dev)
+        sx, sy = x.shape, y.shape
+        if x.dim() != nd or sx[-2] != N or sx[-1] != D or (not jagged and sx[0] != B):
+            raise ValueError("the tensors must agree in all but their heads")
+        if sy != sx:
+            raise ValueError(f"out must have shape {tuple(sx)}, got {tuple(sy)}")
+        a.x, a.y, a.H = x.data_ptr(), y.data_ptr(), sx[-3]
+        if jagged:
+            a.x_stride[1:] = x.stride()[:2]
+            a.y_stride[1:] = y.stride()[:2]
+        else:
+            a.x_stride[:] = x.stride()[:3]
+            a.y_stride[:] = y.stride()[:3]
+    pos = ps = off = None
+    n_seq = 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.device != dev:
+            raise TypeError("positions must be int32 on the tensors' device")
+        want = (N,) if jagged or positions.dim() == 1 else (B, N)
+        if tuple(positions.shape) != want:
+            raise ValueError(f"positions must have shape {want}, got {tuple(positions.shape)}")
+        st = positions.stride()
+        ps = (ctypes.c_int64 * 2)(*(st if len(st) == 2 else (0, st[0])))
+        pos = positions.data_ptr()
+    if jagged:
+        _need(offsets, "offsets", torch.int32, dev)
+        if offsets.dim() != 1 or offsets.numel() < 1:
+            raise ValueError("offsets must be [B + 1]")
+        off, n_seq = offsets.data_ptr(), offsets.numel() - 1
+    L = lib()
+    _call_on(dev, L.attn_rope_f16 if dt == torch.float16 else L.attn_rope, B, N, D, rope._ref, arr, n, pos, ps, off,
+             n_seq, 1 if inverse else 0)
+    return out
+
+
+class PagedCache:
+    """A paged key-value cache, as a serving program holds it: pools
+    ``k`` [pages, Hkv, page_size, Dqk] and ``v`` [pages, Hkv, page_size, Dv]
+    (any strides with contiguous rows: pass ``pool.transpose(1, 2)`` of a
+    token-major one), int32 ``page_table`` [B, max_pages] and ``seq_lens``
+    [B].  Position p of sequence b is token p % page_size of page
+    page_table[b, p // page_size]; seq_lens[b] counts the tokens of sequence
+    b, those being appended in the same step included, and is 0 for an idle
+    place of the batch.  The tensors are the caller's, read by the kernels
+    when they run: change their contents between calls, not the tensors."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor):
+        dt, dev = _elem_type(k), k.device
+        _need_cuda(k, "k", dt)
+        _need_cuda(v, "v", dt, dev)
+        _need_cuda(page_table, "page_table", torch.int32, dev)
+        _need_cuda(seq_lens, "seq_lens", torch.int32, dev)
+        if k.dim() != 4 or v.dim() != 4 or k.shape[:3] != v.shape[:3]:
+            raise ValueError("k must be [pages, Hkv, page_size, Dqk] and v [pages, Hkv, page_size, Dv]")
+        if page_table.dim() != 2 or seq_lens.dim() != 1 or seq_lens.shape[0] != page_table.shape[0]:
+            raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
+        self.k, self.v, self.page_table, self.seq_lens = k, v, page_table, seq_lens
+        self.B, self.max_pages = page_table.shape
+        self.n_pages, self.Hkv, self.page_size, self.Dqk = k.shape
+        self.Dv = v.shape[3]
+        self.device, self.dtype = dev, dt
+        c = AttnPagedCache()
+        c.B, c.max_pages, c.n_pages, c.page_size = self.B, self.max_pages, self.n_pages, self.page_size
+        c.Hkv, c.Dqk, c.Dv = self.Hkv, self.Dqk, self.Dv
+        c.k, c.v = k.data_ptr(), v.data_ptr()
+        c.k_stride[:], c.v_stride[:] = k.stride()[:3], v.stride()[:3]
+        c.page_table, c.table_stride, c.seq_lens = page_table.data_ptr(), page_table.stride(0), seq_lens.data_ptr()
+        self._struct, self._ref = c, ctypes.byref(c)
+        self._workspace = {}  # bytes a decode needs, by query heads
+
+    def _workspace_bytes(self, Hq: int) -> int:
+        n = self._workspace.get(Hq)
+        if n is None:
+            with torch.cuda.device(self.device):
+                n = self._workspace[Hq] = int(lib().attn_paged_decode_workspace(self._ref, Hq))
+        return n
+
+
+def attn_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, rope: Optional[Rope] = None,
+                      q: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None):
+    """Write the keys k [T, Hkv, Dqk] and values v [T, Hkv, Dv] of new tokens
+    into their pages, the keys rotated to their positions by ``rope``, and
+    return the queries q [T, Hq, Dqk] rotated beside them (in ``out``, which
+    may be q itself; None without q).
+
+    Without ``offsets`` T = B and token b is the last of sequence b; with
+    int32 offsets [B + 1], tokens offsets[b] .. offsets[b + 1] are the last
+    of sequence b (rows behind offsets[B] are left alone).  An idle place
+    writes nothing to the cache and zeros to its query row.  Any strides with
+    contiguous rows; a jagged [H, T, D] tensor goes in as its transpose(0, 1)."""
+    dev, dt = cache.device, cache.dtype
+    _need_cuda(k, "k", dt, dev)
+    _need_cuda(v, "v", dt, dev)
+    T = k.shape[0]
+    if tuple(k.shape) != (T, cache.Hkv, cache.Dqk) or tuple(v.shape) != (T, cache.Hkv, cache.Dv):
+        raise ValueError(f"k must be [T, {cache.Hkv}, {cache.Dqk}] and v [T, {cache.Hkv}, {cache.Dv}]")
+    a = AttnPagedNew()
+    a.T, a.k, a.v = T, k.data_ptr(), v.data_ptr()
+    a.k_stride[:], a.v_stride[:] = k.stride()[:2], v.stride()[:2]
+    if offsets is not None:
+        _need(offsets, "offsets", torch.int32, dev)
+        if tuple(offsets.shape) != (cache.B + 1,):
+            raise ValueError(f"offsets must be [{cache.B + 1}]")
+        a.offsets = offsets.data_ptr()
+    elif T != cache.B:
+        raise ValueError(f"without offsets there is one token for each of the {cache.B} sequences, got {T}")
+    if q is not None:
+        _need_cuda(q, "q", dt, dev)
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != cache.Dqk:
+            raise ValueError(f"q must be [{T}, Hq, {cache.Dqk}]")
+        if out is None:
+            out = torch.empty(q.shape, dtype=dt, device=dev)
+        else:
+            _need_cuda(out, "out", dt, dev)
+            if out.shape != q.shape:
+                raise ValueError(f"out must have shape {tuple(q.shape)}, got {tuple(out.shape)}")
+        a.q, a.q_out, a.Hq = q.data_ptr(), out.data_ptr(), q.shape[1]
+        a.q_stride[:], a.q_out_stride[:] = q.stride()[:2], out.stride()[:2]
+    elif out is not None:
+        raise ValueError("out holds the rotated q: there is none without q")
+    if rope is not None:
+        if rope.rot_dim > cache.Dqk:
+            raise ValueError(f"rot_dim {rope.rot_dim} exceeds the head dim {cache.Dqk}")
+        if rope.steps.device != dev:
+            raise ValueError(f"the rotation is on {rope.steps.device}, the cache on {dev}")
+    L = lib()
+    _call_on(dev, L.attn_paged_append_f16 if dt == torch.float16 else L.attn_paged_append, cache._ref,
+             ctypes.byref(a), rope._ref if rope is not None else None)
+    return out
+
+
+def attn_paged_decode(cache: PagedCache, q: torch.Tensor, sm_scale: Optional[float] = None, out=None):
+    """Attention of one query token per sequence over the paged cache:
+    q [B, Hq, Dqk], Hq a multiple of the cache's key heads (query head h
+    reads key head h // (Hq / Hkv)).  Returns (o [B, Hq, Dv], lse [B, Hq]
+    float32, natural log).  An idle place (length 0) gets o = 0, lse = -inf."""
+    dev, dt = cache.device, cache.dtype
+    _need_cuda(q, "q", dt, dev)
+    if q.dim() != 3 or q.shape[0] != cache.B or q.shape[2] != cache.Dqk:
+        raise ValueError(f"q must be [{cache.B}, Hq, {cache.Dqk}]")
+    B, Hq = cache.B, q.shape[1]
+    if cache.Hkv == 0 or Hq % cache.Hkv:
+        raise ValueError(f"the cache's {cache.Hkv} key heads must divide the {Hq} query heads")
+    if out is None:
+        o = torch.empty((B, Hq, cache.Dv), dtype=dt, device=dev)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    else:
+        o, lse = out
+        _need_out(o, "o", (B, Hq, cache.Dv), dt, dev)
+        _need_out(lse, "lse", (B, Hq), torch.float32, dev)
+    n = cache._workspace_bytes(Hq)
+    # of this call alone: a graph's is its own, calls on two streams have two
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    qs = q.stride()
+    L = lib()
+    _call_on(dev, L.attn_paged_decode_f16 if dt == torch.float16 else L.attn_paged_decode, cache._ref, Hq,
+             q.data_ptr(), (ctypes.c_int64 * 2)(qs[0], qs[1]), _scale(sm_scale), o.data_ptr(), lse.data_ptr(),
+             ws.data_ptr(), n)
+    return o, lse

@@ -14,6 +14,7 @@
 
 #include "attn_jvp.h"
 #include "attn_bwd_kernel.cuh"
+#include "attn_paged_kernels.h"
 #include "attn_plan.h"
 
 static_assert(attn::kPlanBM == attn::kBM && attn::kPlanBN == attn::kBN,
@@ -791,6 +792,10 @@ attn_status noalloc_state(DeviceState* out) {
 
 }  // namespace
 
+namespace attn {
+void count_launch(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
+}  // namespace attn
+
 extern "C" {
 
 attn_status attn_fwd_jvp(const attn_shape* shape, const void* q, const void* k, const void* v,
@@ -878,7 +883,17 @@ attn_status attn_sync_check(void* stream) {
       timed_out = true;
     }
   }
-  return timed_out ? ATTN_ERR_TIMEOUT : ATTN_OK;
+  // and the word of the paged cache's entry points
+  bool bad_page = false;
+  if (int* w = attn::page_error_word(dev)) {
+    int word = 0;
+    if (cudaMemcpy(&word, w, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (word != 0) {
+      if (cudaMemset(w, 0, sizeof(int)) != cudaSuccess) return ATTN_ERR_CUDA;
+      bad_page = true;
+    }
+  }
+  return timed_out ? ATTN_ERR_TIMEOUT : bad_page ? ATTN_ERR_PAGE : ATTN_OK;
 }
 
 const char* attn_status_string(attn_status s) {
@@ -891,6 +906,8 @@ const char* attn_status_string(attn_status s) {
     case ATTN_ERR_MISALIGNED: return "a device pointer is not 16-byte aligned";
     case ATTN_ERR_CUDA: return "CUDA error (no device, launch failure or driver entry point missing)";
     case ATTN_ERR_TIMEOUT: return "a device pipeline wait ran out of time; outputs are undefined";
+    case ATTN_ERR_PAGE:
+      return "a page number, sequence length or token position was out of range in the paged cache";
   }
   return "unknown status";
 }

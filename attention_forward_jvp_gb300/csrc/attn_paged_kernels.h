@@ -1,0 +1,102 @@
+// Rotary positions and the paged cache: what the host side (attn_paged.cu)
+// hands to the kernels (attn_rope.cu, attn_decode_kernel.cuh).
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace attn {
+
+// ------------------------------------------------------------- rope, append
+struct RopeSpec {
+  const unsigned long long* steps;  // turn per position, 2^64 = a full turn
+  int rot;                          // rotated elements of a head (0: none)
+  int interleaved;
+  float scale;
+  int inverse;
+};
+
+struct RopeTensor {
+  const uint16_t* x;
+  uint16_t* y;
+  long long xs[3], ys[3];  // batch, head, token
+  int H;
+};
+
+constexpr int kRopeTensors = 4;
+
+struct RopeParams {
+  RopeTensor t[kRopeTensors];
+  RopeSpec r;
+  int n_tensors, heads;      // heads: of all tensors together
+  int heads_per_split;       // heads of one blockIdx.y
+  int D;
+  long long N, rows;         // tokens of a batch entry, of all
+  const int* positions;      // or null
+  long long ps[2];
+  const int* offsets;        // or null
+  int n_seq;
+};
+
+struct AppendParams {
+  RopeSpec r;
+  const uint16_t *k, *v, *q;
+  uint16_t *k_pool, *v_pool, *q_out;
+  long long ks[2], vs[2], qs[2], qos[2];  // token, head
+  long long kp[3], vp[3];                 // page, head, token
+  int Hq, Hkv, Dqk, Dv;                   // Hq = 0: no queries
+  int heads_per_split;
+  long long T;
+  const int* offsets;                     // or null: token b is of sequence b
+  const int* page_table;
+  long long table_stride;
+  const int* seq_lens;
+  int B, max_pages, n_pages, page_size;
+  int* err;
+};
+
+// vec: every row 16-byte aligned, head dims and rotated width multiples of 16
+cudaError_t launch_rope(const RopeParams& p, bool vec, bool f16, int splits, cudaStream_t stream);
+cudaError_t launch_append(const AppendParams& p, bool vec, bool f16, int splits, cudaStream_t stream);
+
+// -------------------------------------------------------------------- decode
+constexpr int kDecodeBN = 64;        // keys of a tile
+constexpr int kDecodeMaxRows = 64;   // query heads of one work unit
+
+struct DecodeParams {
+  const uint16_t *q, *k, *v;
+  long long qs[2];             // sequence, head
+  long long kp[3], vp[3];      // page, head, token
+  const int* page_table;
+  long long table_stride;
+  const int* seq_lens;
+  int B, n_pages, page_size, page_shift;  // page_shift: log2, or -1
+  int capacity;                // keys a table row can hold
+  int Hkv, G;                  // key heads, query heads of each
+  int rows, chunks;            // query heads of a work unit, units of a key head
+  int wr;                      // 16-row groups of a unit (1, 2 or 4)
+  int min_tiles;               // tiles a CTA takes at least
+  int dqk, dv;                 // true head dims (<= the kernel's)
+  float scale_log2;
+  uint16_t* o;
+  float* lse;
+  int4* desc;                  // [CTA]: the unit that starts in it and ends in a later one
+  float2* part_ml;             // [CTA][2][rows]
+  float* part_o;               // [CTA][2][rows][kernel Dv]
+  int* err;
+  int split;                   // 0: no sequence can have more than one tile
+};
+
+// CTAs the decode kernel of these head dims runs with, and its launch
+// (followed, when p.split, by the joining kernel).  nw: 4 or 8 warps.
+constexpr int decode_ctas_per_sm(int dq, int dv, int nw) { return nw == 4 && dq + dv <= 256 ? 2 : 1; }
+template <int DQ, int DV, bool F16>
+cudaError_t launch_decode(const DecodeParams& p, int nw, int ctas, cudaStream_t stream);
+
+// Device word that append and decode set on a bad page number or length;
+// null where no call has set it up on this device.
+int* page_error_word(int dev);
+
+void count_launch(int n);
+
+}  // namespace attn

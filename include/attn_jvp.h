@@ -82,7 +82,9 @@ typedef enum {
   ATTN_ERR_UNSUPPORTED = 2,   /* head dim outside the entry point's set, option not supported */
   ATTN_ERR_MISALIGNED = 3,    /* a pointer is not 16-byte aligned */
   ATTN_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed (no GPU, launch error) */
-  ATTN_ERR_TIMEOUT = 5        /* a device pipeline wait ran out of time; outputs undefined */
+  ATTN_ERR_TIMEOUT = 5,       /* a device pipeline wait ran out of time; outputs undefined */
+  ATTN_ERR_PAGE = 6           /* paged cache (attn_paged.h): a page number, a length or a
+                                 position out of range; that access was left out */
 } attn_status;
 
 /* Problem shape.  Dense: B, H, M (query length), N (key length), Dqk, Dv;
@@ -268,9 +270,10 @@ attn_status attn_bwd_stages(const attn_shape* shape,
 /* Synchronises `stream`, then reads and clears the error words of the
  * current device: the scratch of the allocating entry points and the fixed
  * array of attn_fwd_jvp_noalloc, each once a call on the device has set it
- * up (nothing is allocated here).  Returns ATTN_ERR_TIMEOUT if a launch
- * since the last check reported a timed-out wait, ATTN_ERR_CUDA on a CUDA
- * error, else ATTN_OK. */
+ * up (nothing is allocated here), and the word of attn_paged.h's entry
+ * points.  Returns ATTN_ERR_TIMEOUT if a launch since the last check
+ * reported a timed-out wait, else ATTN_ERR_PAGE if one met a page, length
+ * or position out of range, ATTN_ERR_CUDA on a CUDA error, else ATTN_OK. */
 attn_status attn_sync_check(void* stream);
 
 /* Static description of a status code; never NULL. */
