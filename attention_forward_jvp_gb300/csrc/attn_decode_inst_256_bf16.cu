@@ -2,7 +2,7 @@
 #include "attn_decode_kernel.cuh"
 
 namespace attn {
-template cudaError_t launch_decode<256, 64, false>(const DecodeParams&, int, int, cudaStream_t);
-template cudaError_t launch_decode<256, 128, false>(const DecodeParams&, int, int, cudaStream_t);
-template cudaError_t launch_decode<256, 256, false>(const DecodeParams&, int, int, cudaStream_t);
+template cudaError_t launch_decode<256, 64, false>(DecodeParams&, int, int, cudaStream_t);
+template cudaError_t launch_decode<256, 128, false>(DecodeParams&, int, int, cudaStream_t);
+template cudaError_t launch_decode<256, 256, false>(DecodeParams&, int, int, cudaStream_t);
 }  // namespace attn

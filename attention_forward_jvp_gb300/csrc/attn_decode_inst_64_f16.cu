@@ -2,7 +2,7 @@
 #include "attn_decode_kernel.cuh"
 
 namespace attn {
-template cudaError_t launch_decode<64, 64, true>(const DecodeParams&, int, int, cudaStream_t);
-template cudaError_t launch_decode<64, 128, true>(const DecodeParams&, int, int, cudaStream_t);
-template cudaError_t launch_decode<64, 256, true>(const DecodeParams&, int, int, cudaStream_t);
+template cudaError_t launch_decode<64, 64, true>(DecodeParams&, int, int, cudaStream_t);
+template cudaError_t launch_decode<64, 128, true>(DecodeParams&, int, int, cudaStream_t);
+template cudaError_t launch_decode<64, 256, true>(DecodeParams&, int, int, cudaStream_t);
 }  // namespace attn

@@ -1,28 +1,36 @@
 // Attention of one query token per sequence over a paged key-value cache.
 //
-// Mathematics: S = s q K^T, O = softmax(S) V, LSE, for the G query heads of
-// one key head together.  One pass over the keys with a running maximum m
-// and sum l per row: P = exp2(S' - m), O <- O exp2(m_old - m) + P V,
-// l <- l exp2(m_old - m) + rowsum(P), with S' = S log2(e).  Parts of a
+// Mathematics: S = s q K^T, O = softmax(S) V, LSE, for the query heads of one
+// key head together.  One pass over the keys with a running maximum m and
+// sum l per head: P = exp2(S' - m), O <- O exp2(m_old - m) + P V,
+// l <- l exp2(m_old - m) + sum(P), with S' = S log2(e).  m moves only when a
+// score passes it by more than 8 (P then stays below 2^8), so that most steps
+// need neither the maximum over the lanes nor the rescale.  Parts of a
 // sequence are joined by the same rule.
 //
 // What bounds it: memory.  Every key and value is read once and used by G
-// rows, 2 G flops a byte; at G <= 16 the 16-row mma.sync steps below need a
-// sixth of their issue rate to keep up with memory, so the 128-row
-// tcgen05 tiles (64 rows at least, all but G of them padding) and their
-// trips through tensor memory would buy nothing here.
+// query heads, G flops a byte; tcgen05's 64 or 128 rows would be padding but
+// for G of them, and the trip through tensor memory latency.  mma.sync with
+// the keys (for O: the value columns) as the 16 rows and the query heads as
+// the 8 columns has no padding from G = 8 on.
 //
-// Layout of the work: the 64-key tiles of all (sequence, key head) pairs
-// form one list, cut into equal ranges, one for each resident CTA, whatever
-// the lengths; a CTA walks its range, unit after unit.  A unit that lies
-// within one CTA is finished there; parts of the others go to the workspace
-// and attn_decode_join joins them, in order.  The warps of a CTA share a
-// tile's keys (16 or 32 each) and, above 16 rows, its rows.
+//   S^T (16 keys x 8 heads)    = K (16 x Dqk) Q^T
+//   O^T (Dv x 8 heads)        += V^T (Dv x 16 keys) P^T
 //
-// Tiles come by 16-byte asynchronous copies, row by row through the page
-// table, into a ring that keeps two to five tiles in flight; rows behind the
-// sequence's end are filled with zeros, so that whatever a page holds there
-// never enters a product.
+// K and V^T come from shared memory by ldmatrix (V^T by its transposing
+// form), Q^T stays in registers, P^T is turned from S^T's accumulator layout
+// to the operand's by movmatrix.  NT groups of 8 heads share a key's loads.
+//
+// Layout of the work: the 16-key steps of all (sequence, key head) pairs form
+// one list, cut into equal ranges, one for each resident warp, whatever the
+// lengths.  A warp walks its range alone, unit after unit, with a ring of its
+// own in shared memory that it fills by 16-byte asynchronous copies, row by
+// row through the page table: no block-wide barrier until the end.  A unit
+// that lies within one warp is finished there; the warps of a CTA that lies
+// within one unit join their parts in shared memory; parts of the others go
+// to the workspace and attn_decode_join joins them, in order.  Rows behind
+// the sequence's end are filled with zeros, so that whatever a page holds
+// there never enters a product.
 #pragma once
 #include "attn_paged_kernels.h"
 #include "ptx.cuh"
@@ -89,49 +97,53 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = pack2<F16>(x - hx, y - hy);
 }
 
-constexpr int decode_pow2_floor(int x) {
-  int r = 1;
-  while (2 * r <= x) r *= 2;
-  return r;
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
-template <int DQ, int DV, int NW>
+// Shared memory and registers of a warp decide how many fit on an SM: three
+// stages of 16 keys where that leaves six warps or more (two thirds of the
+// ring in flight while a stage is read), else two; Q in registers unless it
+// and the accumulators would pass 176.
+template <int DQ, int DV, int NT>
 struct DecodePlan {
   static constexpr int BN = kDecodeBN;
-  static constexpr int THREADS = NW * 32;
-  static constexpr int CTAS = decode_ctas_per_sm(DQ, DV, NW);
-  static constexpr int ROWS = NW == 4 ? 16 : kDecodeMaxRows;
-  static constexpr int Q_BYTES = ROWS * DQ * 2;
+  static constexpr int STAGE = BN * (DQ + DV) * 2;
   static constexpr int K_BYTES = BN * DQ * 2;
-  static constexpr int TILE_BYTES = BN * (DQ + DV) * 2;
-  // per-warp row statistics, scan words
-  static constexpr int MISC_BYTES = NW * 16 * 8 + 256;
-  // (the row table beside the ring: page and slot of each key in flight)
-  static constexpr int BUDGET = (CTAS == 2 ? 113 : 226) * 1024 - Q_BYTES - MISC_BYTES;
-  static constexpr int STAGES_FIT = BUDGET / (TILE_BYTES + BN * 8);
-  static constexpr int STAGES = STAGES_FIT > 6 ? 6 : STAGES_FIT;
-  static constexpr int TAB = STAGES;  // table entries: a tile's is free once its copies are issued
-  static constexpr int SMEM = Q_BYTES + STAGES * TILE_BYTES + TAB * BN * 8 + MISC_BYTES;
-  // columns of O that the warps exchange at a time through one stage
-  static constexpr int CW_FIT = decode_pow2_floor(TILE_BYTES / (NW * 64));
-  static constexpr int CW = CW_FIT < DV ? CW_FIT : DV;
-  static_assert(STAGES >= 2 && CW >= 32, "decode plan");
+  static constexpr int ACC_REGS = DV / 4 * NT, Q_REGS = DQ / 8 * NT;
+  static constexpr bool QREG = ACC_REGS + Q_REGS <= 176;
+  static constexpr int Q_BYTES = QREG ? 0 : DQ / 16 * NT * 256;
+  static constexpr int MISC_BYTES = 1024;
+  static constexpr int FIT = 226 * 1024 - MISC_BYTES;
+  static constexpr int S = FIT / (3 * STAGE + Q_BYTES) >= 6 ? 3 : 2;
+  static constexpr int WARP_BYTES = S * STAGE + Q_BYTES;
+  static constexpr int REGS = ACC_REGS + (QREG ? Q_REGS : 0) + 72;
+  static constexpr int NW_REGS = REGS <= 128 ? 16 : (REGS <= 168 ? 12 : 8);
+  static constexpr int NW_SMEM = FIT / WARP_BYTES;
+  static constexpr int NW = NW_SMEM < NW_REGS ? NW_SMEM : NW_REGS;
+  static_assert(NW <= kDecodeMaxWarps, "decode plan");
+  static constexpr int SMEM = NW * WARP_BYTES + MISC_BYTES;
+  // O of 8 heads on its way out, rows padded against bank conflicts
+  static constexpr int PITCH = DV + 4;
+  static_assert(NW >= 4 && 8 * PITCH * 4 <= STAGE && NT * 8 * (PITCH * 4 + 8) <= S * STAGE, "decode plan");
 };
 
-template <int DQ, int DV, bool F16, int NW>
-__global__ void __launch_bounds__(NW * 32, decode_ctas_per_sm(DQ, DV, NW))
+template <int DQ, int DV, bool F16, int NT>
+__global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     attn_decode_kernel(const __grid_constant__ DecodeParams p) {
-  using P = DecodePlan<DQ, DV, NW>;
-  constexpr int BN = P::BN, S = P::STAGES, THREADS = P::THREADS;
-  constexpr int QPITCH = DQ * 2, KPITCH = DQ * 2, VPITCH = DV * 2;
-  constexpr bool QREG = DQ <= 128;  // Q fragments stay in registers
+  using P = DecodePlan<DQ, DV, NT>;
+  constexpr int BN = P::BN, S = P::S, NW = P::NW, THREADS = NW * 32, PITCH = P::PITCH;
+  constexpr int KPITCH = DQ * 2, VPITCH = DV * 2;
   extern __shared__ __align__(128) char smem[];
-  const uint32_t sq = smem_u32(smem);
-  const uint32_t ring = sq + P::Q_BYTES;
-  int2* tab = reinterpret_cast<int2*>(smem + P::Q_BYTES + S * P::TILE_BYTES);
-  float2* ml = reinterpret_cast<float2*>(tab + P::TAB * BN);
-  long long* scan = reinterpret_cast<long long*>(ml + NW * 16);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  char* mine = smem + warp * P::WARP_BYTES;  // this warp's ring, then its Q
+  const uint32_t ring = smem_u32(mine);
+  uint2* qs = reinterpret_cast<uint2*>(mine + S * P::STAGE) + lane;
+  char* misc = smem + NW * P::WARP_BYTES;
+  long long* scan = reinterpret_cast<long long*>(misc);          // [NW]
+  int3* start = reinterpret_cast<int3*>(misc + 8 * 16);          // [NW]: b, unit, step
   const int HU = p.Hkv * p.chunks;  // units of a sequence
 
   griddep_wait();
@@ -141,14 +153,14 @@ __global__ void __launch_bounds__(NW * 32, decode_ctas_per_sm(DQ, DV, NW))
     const int n = __ldg(p.seq_lens + b);
     return n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
   };
-  auto tiles_of = [](int len) { return (len + BN - 1) / BN; };
+  auto steps_of = [](int len) { return (len + BN - 1) / BN; };
 
-  // ---- this CTA's range [lo, hi) of the tile list
+  // ---- the ranges of the warps: warp x takes steps [total x / warps, total (x + 1) / warps)
   long long sum = 0;
   for (int b = tid; b < p.B; b += THREADS) {
     const int raw = __ldg(p.seq_lens + b), n = length(b);
     if (raw != n && blockIdx.x == 0) *p.err = 1;
-    sum += tiles_of(n);
+    sum += steps_of(n);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -158,37 +170,33 @@ __global__ void __launch_bounds__(NW * 32, decode_ctas_per_sm(DQ, DV, NW))
 #pragma unroll
   for (int w = 0; w < NW; ++w) total += scan[w];
   total *= HU;
-  long long ctas = (total + p.min_tiles - 1) / p.min_tiles;
-  if (ctas > gridDim.x) ctas = gridDim.x;
-  const int c = blockIdx.x;
-  const long long lo = c < ctas ? total * c / ctas : 0;
-  const long long hi = c < ctas ? total * (c + 1) / ctas : 0;
+  long long warps = (total + p.min_steps - 1) / p.min_steps;
+  if (warps > static_cast<long long>(gridDim.x) * NW) warps = static_cast<long long>(gridDim.x) * NW;
+  auto range_start = [&](long long x) { return x < warps ? total * x / warps : total; };
+  const int first = blockIdx.x * NW;  // this CTA's first warp
+  const int me = first + warp;
+  const long long lo = range_start(me), hi = range_start(me + 1);
+  const int count = static_cast<int>(hi - lo);
 
   // ---- sequences without keys: O = 0, LSE = -inf
-  for (int b = c; b < p.B; b += gridDim.x) {
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (length(b) != 0) continue;
     const int Hq = p.Hkv * p.G;
     for (int i = tid; i < Hq * (p.dv / 8); i += THREADS)
       reinterpret_cast<uint4*>(p.o + static_cast<long long>(b) * Hq * p.dv)[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = tid; i < Hq; i += THREADS) p.lse[static_cast<long long>(b) * Hq + i] = -INFINITY;
   }
-  if (p.split && tid == 0) p.desc[c] = make_int4(-1, 0, 0, 0);
-  const int count = static_cast<int>(hi - lo);
-  if (count == 0) return;
+  if (p.split && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
+  if (first >= warps) return;
 
-  // ---- the sequence that tile lo belongs to
-  struct Cursor {
-    int b, hu, t, nt, len;
-  };
-  Cursor cur;
+  // ---- the sequence, unit and step that each warp's range starts with
   {
     long long before = 0;
-    int b0 = 0;
-    long long r = 0;
-    for (;; b0 += THREADS) {  // ends: lo < total
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
       const int b = b0 + tid;
-      const long long mine = b < p.B ? static_cast<long long>(tiles_of(length(b))) * HU : 0;
-      long long inc = mine;
+      const int n = b < p.B ? steps_of(length(b)) : 0;
+      const long long own = static_cast<long long>(n) * HU;
+      long long inc = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, inc, o);
@@ -196,7 +204,6 @@ __global__ void __launch_bounds__(NW * 32, decode_ctas_per_sm(DQ, DV, NW))
       }
       __syncthreads();
       if (lane == 31) scan[warp] = inc;
-      if (tid == 0) scan[NW] = -1;
       __syncthreads();
       long long base = before, all = before;
 #pragma unroll
@@ -204,26 +211,23 @@ __global__ void __launch_bounds__(NW * 32, decode_ctas_per_sm(DQ, DV, NW))
         if (w < warp) base += scan[w];
         all += scan[w];
       }
-      const long long start = base + inc - mine;
-      if (mine > 0 && start <= lo && lo < start + mine) {
-        scan[NW] = b;
-        scan[NW + 1] = lo - start;
+      const long long begin = base + inc - own;
+      if (own > 0) {
+#pragma unroll 1
+        for (int w = 0; w < NW; ++w) {
+          const long long x = range_start(first + w) - begin;
+          if (0 <= x && x < own) start[w] = make_int3(b, static_cast<int>(x / n), static_cast<int>(x % n));
+        }
       }
-      __syncthreads();
-      if (scan[NW] >= 0) {
-        cur.b = static_cast<int>(scan[NW]);
-        r = scan[NW + 1];
-        break;
-      }
-      if (b0 + THREADS >= p.B) return;  // (never: the lengths changed under the kernel)
       before = all;
+      if (range_start(first + NW - 1) < all) break;
     }
-    cur.len = length(cur.b);
-    cur.nt = max(tiles_of(cur.len), 1);
-    cur.hu = static_cast<int>(r / cur.nt);
-    cur.t = static_cast<int>(r - static_cast<long long>(cur.hu) * cur.nt);
+    __syncthreads();
   }
-  // the next tile of the list; the caller knows that there is one
+  struct Cursor {
+    int b, hu, t, nt, len;
+  };
+  // the next step of the list; the caller knows that there is one
   auto advance = [&](Cursor& a) {
     if (++a.t < a.nt) return;
     a.t = 0;
@@ -232,389 +236,444 @@ __global__ void __launch_bounds__(NW * 32, decode_ctas_per_sm(DQ, DV, NW))
     do {
       ++a.b;
       a.len = length(a.b);
-      a.nt = tiles_of(a.len);
+      a.nt = steps_of(a.len);
     } while (a.nt == 0 && a.b + 1 < p.B);
   };
 
-  // ---- page table look-ups, tiles ahead of the copies
-  auto lookup = [&](const Cursor& a, int key_in_tile) -> int2 {
-    const int key = a.t * BN + key_in_tile;
-    if (key >= a.len) return make_int2(-1, 0);
-    const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-    const int slot = key - e * p.page_size;
-    int page = __ldg(p.page_table + a.b * p.table_stride + e);
-    if (page < 0 || page >= p.n_pages) {
-      *p.err = 1;
-      page = -1;
-    }
-    return make_int2(page, slot);
-  };
-  // ---- copies of one tile
-  auto issue = [&](int hu, int stage, int entry) {
-    const int h = hu / p.chunks;
-    const int2* row = tab + entry * BN;
-    constexpr int KC = DQ / 8, VC = DV / 8;  // 16-byte pieces of a row
-    const uint32_t kd = ring + stage * P::TILE_BYTES, vd = kd + P::K_BYTES;
-    {
-      const int piece = tid % KC;
-      const bool in = piece * 8 < p.dqk;
-      const uint16_t* base = p.k + h * p.kp[1] + piece * 8;
-#pragma unroll
-      for (int r = tid / KC; r < BN; r += THREADS / KC) {
-        const int2 e = row[r];
-        const bool live = in && e.x >= 0;
-        const uint16_t* src = live ? base + e.x * p.kp[0] + e.y * p.kp[2] : p.q;
-        cp_async16(kd + r * KPITCH + ((piece ^ (r & 7)) << 4), src, live);
-      }
-    }
-    {
-      const int piece = tid % VC;
-      const bool in = piece * 8 < p.dv;
-      const uint16_t* base = p.v + h * p.vp[1] + piece * 8;
-#pragma unroll
-      for (int r = tid / VC; r < BN; r += THREADS / VC) {
-        const int2 e = row[r];
-        const bool live = in && e.x >= 0;
-        const uint16_t* src = live ? base + e.x * p.vp[0] + e.y * p.vp[2] : p.q;
-        cp_async16(vd + r * VPITCH + ((piece ^ (r & 7)) << 4), src, live);
-      }
-    }
-  };
-  // ---- query rows of a unit, 16-byte pieces
-  constexpr int QC = DQ / 8;
-  constexpr int QN = (P::ROWS * QC + THREADS - 1) / THREADS;  // pieces of a thread
-  auto load_q = [&](const Cursor& a, uint4 (&reg)[QN]) {
-    const int h = a.hu / p.chunks, chunk = a.hu - h * p.chunks;
-    const int g0 = chunk * p.rows, n = min(p.rows, p.G - g0);
-    const uint16_t* base = p.q + a.b * p.qs[0] + static_cast<long long>(h * p.G + g0) * p.qs[1];
-#pragma unroll
-    for (int i = 0; i < QN; ++i) {
-      const int x = tid + i * THREADS, r = x / QC, piece = x % QC;
-      reg[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < n && piece * 8 < p.dqk) reg[i] = *reinterpret_cast<const uint4*>(base + r * p.qs[1] + piece * 8);
-    }
-  };
-  auto store_q = [&](const uint4 (&reg)[QN]) {
-#pragma unroll
-    for (int i = 0; i < QN; ++i) {
-      const int x = tid + i * THREADS, r = x / QC, piece = x % QC;
-      if (r < P::ROWS) *reinterpret_cast<uint4*>(smem + r * QPITCH + ((piece ^ (r & 7)) << 4)) = reg[i];
-    }
-  };
-
-  Cursor ahead = cur;     // the tile whose page numbers are looked up next
-  int looked = 0;         // tiles looked up
-  int2 next_row;          // row `tid` of tile `looked`, on its way (tid < BN)
-  // rows of the first S tiles at once
-  {
-    constexpr int GROUPS = THREADS / BN;
-    int2 rows[(S + GROUPS - 1) / GROUPS];
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      if (j < count) {
-        if (tid / BN == j % GROUPS) rows[j / GROUPS] = lookup(ahead, tid % BN);
-        if (j + 1 < count) advance(ahead);
-        looked = j + 1;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < S; ++j)
-      if (j < count && tid / BN == j % GROUPS) tab[j % P::TAB * BN + tid % BN] = rows[j / GROUPS];
-  }
-  uint4 qreg[QN];
-  load_q(cur, qreg);
-  store_q(qreg);
-  __syncthreads();
-  Cursor fill = cur;  // the tile whose copies are issued next
-#pragma unroll
-  for (int j = 0; j < S - 1; ++j) {
-    if (j < count) {
-      issue(fill.hu, j, j);
-      if (j + 1 < count) advance(fill);
-    }
-    cp_async_commit();
-  }
-  if (tid < BN && looked < count) next_row = lookup(ahead, tid);
-
-  // ---- accumulators
-  const int wr = warp % p.wr, wk = warp / p.wr, WK = NW / p.wr;
-  const int keys_w = BN / WK;  // keys of this warp in a tile
   const int mi = lane >> 3, l8 = lane & 7, g = lane >> 2, q4 = lane & 3;
-  uint32_t qf[QREG ? DQ / 16 : 1][4];
-  const uint32_t q_row = sq + (wr * 16 + (mi & 1) * 8 + l8) * QPITCH;
-  auto q_frag = [&](int ks, uint32_t (&f)[4]) { ldsm4(f, q_row + (((ks * 2 + (mi >> 1)) ^ l8) << 4)); };
-  float acc[DV / 8][4];
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows g and g + 8
-#pragma unroll
-  for (int i = 0; i < DV / 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-  if constexpr (QREG) {
-#pragma unroll
-    for (int ks = 0; ks < DQ / 16; ++ks) q_frag(ks, qf[ks]);
+  float acc[NT][DV / 16][4];
+  float m[NT][2], l[NT][2];  // heads 2 q4, 2 q4 + 1 of each group
+  uint32_t qr[P::QREG ? DQ / 16 : 1][NT][2];
+  Cursor cur;
+  bool same_unit = false;  // the whole CTA lies within one unit
+  {
+    const int3 a = start[0];
+    const int nt = steps_of(length(a.x));
+    same_unit = a.z + (range_start(first + NW) - range_start(first)) <= nt;
   }
-  int seg_t0 = cur.t;  // first tile of the unit in this CTA
-
-  int stage = 0;
-#pragma unroll 1
-  for (int i = 0; i < count; ++i) {
-    cp_async_wait<S - 2>();
-    __syncthreads();
-    // refill the stage of the tile before this one
-    const int j = i + S - 1;
-    if (j < count) {
-      issue(fill.hu, stage == 0 ? S - 1 : stage - 1, j % P::TAB);
-      if (j + 1 < count) advance(fill);
+  auto clear = [&]() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int d = 0; d < DV / 16; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][d][e] = 0.f;
     }
-    cp_async_commit();
-    // rows of tile i + S: its entry was that of tile i, read S - 1 tiles ago
-    if (looked < count) {
-      if (tid < BN) tab[looked % P::TAB * BN + tid] = next_row;
-      if (looked + 1 < count) {
-        advance(ahead);
-        if (tid < BN) next_row = lookup(ahead, tid);
-      }
-      ++looked;
-    }
-
-    const uint32_t sk = ring + stage * P::TILE_BYTES, sv = sk + P::K_BYTES;
-    const int live = cur.len - cur.t * BN;  // keys of this tile
-#pragma unroll 1
-    for (int k0 = wk * keys_w; k0 < (wk + 1) * keys_w; k0 += 16) {
-      if (k0 >= live) break;  // (warp-uniform)
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint32_t k_row = sk + (k0 + (mi >> 1) * 8 + l8) * KPITCH;
+  };
+  // Q^T of a unit as the product's second operand: pairs of neighbouring
+  // elements of head g of each group
+  auto load_q = [&](const Cursor& a) {
+    const int h = a.hu / p.chunks, g0 = (a.hu - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
+    const uint16_t* base = p.q + a.b * p.qs[0] + (static_cast<long long>(h) * p.G + g0) * p.qs[1];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const bool in = 8 * n + g < n_rows;
+      const uint16_t* row = base + (in ? 8 * n + g : 0) * p.qs[1];
 #pragma unroll
       for (int ks = 0; ks < DQ / 16; ++ks) {
-        uint32_t kb[4];
-        ldsm4(kb, k_row + (((ks * 2 + (mi & 1)) ^ l8) << 4));
-        if constexpr (QREG) {
-          mma16816<F16>(s0, qf[ks], kb[0], kb[1]);
-          mma16816<F16>(s1, qf[ks], kb[2], kb[3]);
+        uint32_t v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int d = 16 * ks + 8 * e + 2 * q4;
+          v[e] = in && d < p.dqk ? *reinterpret_cast<const uint32_t*>(row + d) : 0u;
+        }
+        if constexpr (P::QREG) {
+          qr[ks][n][0] = v[0];
+          qr[ks][n][1] = v[1];
         } else {
-          uint32_t f[4];
-          q_frag(ks, f);
-          mma16816<F16>(s0, f, kb[0], kb[1]);
-          mma16816<F16>(s1, f, kb[2], kb[3]);
+          qs[(ks * NT + n) * 32] = make_uint2(v[0], v[1]);  // read back by this lane alone
         }
       }
-      if (k0 + 16 > live) {
-        const int k = k0 + 2 * q4;
-        if (k >= live) s0[0] = s0[2] = -INFINITY;
-        if (k + 1 >= live) s0[1] = s0[3] = -INFINITY;
-        if (k + 8 >= live) s1[0] = s1[2] = -INFINITY;
-        if (k + 9 >= live) s1[1] = s1[3] = -INFINITY;
-      }
-      float x0 = fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s1[0], s1[1]));
-      float x1 = fmaxf(fmaxf(s0[2], s0[3]), fmaxf(s1[2], s1[3]));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-      const float n0 = fmaxf(m0, x0 * p.scale_log2), n1 = fmaxf(m1, x1 * p.scale_log2);
-      // a row whose scores are all -inf keeps weights of 0
-      const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
-      if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1)) {
-        const float a0 = exp2_fast(m0 - u0), a1 = exp2_fast(m1 - u1);
-        l0 *= a0;
-        l1 *= a1;
+    }
+  };
+  // O of group n to [head][Dv] in shared memory, scaled by f[head of the lane]
+  auto spill = [&](float* to, int n, float f0, float f1) {
 #pragma unroll
-        for (int d = 0; d < DV / 8; ++d) {
-          acc[d][0] *= a0;
-          acc[d][1] *= a0;
-          acc[d][2] *= a1;
-          acc[d][3] *= a1;
+    for (int d = 0; d < DV / 16; ++d) {
+      float* x = to + 2 * q4 * PITCH + 16 * d + g;
+      x[0] = acc[n][d][0] * f0;
+      x[PITCH] = acc[n][d][1] * f1;
+      x[8] = acc[n][d][2] * f0;
+      x[PITCH + 8] = acc[n][d][3] * f1;
+    }
+  };
+  // four columns of a row that is complete
+  auto write_row = [&](long long row, int col, float4 o, float mm, float ll) {
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    if (col < p.dv)
+      *reinterpret_cast<uint2*>(p.o + row * p.dv + col) =
+          make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
+    if (col == 0) p.lse[row] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
+  };
+
+  clear();
+  if (count > 0) {
+    cur.b = start[warp].x;
+    cur.hu = start[warp].y;
+    cur.t = start[warp].z;
+    cur.len = length(cur.b);
+    cur.nt = steps_of(cur.len);
+
+    // ---- copies: a lane brings 16-byte pieces q4, q4 + 4, .. of rows g and
+    // g + 8 of a step, so that one instruction moves 64 bytes of 8 rows
+    int page[2], slot[2], next_h;  // of the step whose copies are next
+    auto lookup = [&](const Cursor& a) {
+      next_h = a.hu / p.chunks;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int key = a.t * BN + g + 8 * r;
+        page[r] = -1;
+        slot[r] = 0;
+        if (key < a.len) {
+          const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+          slot[r] = key - e * p.page_size;
+          page[r] = __ldg(p.page_table + a.b * p.table_stride + e);
         }
-        m0 = n0;
-        m1 = n1;
       }
+    };
+    auto issue = [&](int stage) {
+      const uint32_t kd = ring + stage * P::STAGE + g * KPITCH + ((q4 ^ g) << 4);
+      const uint32_t vd = ring + stage * P::STAGE + P::K_BYTES + g * VPITCH + ((q4 ^ g) << 4);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s0[e] = exp2_fast(fmaf(s0[e], p.scale_log2, -u0));
-        s1[e] = exp2_fast(fmaf(s1[e], p.scale_log2, -u0));
-        s0[2 + e] = exp2_fast(fmaf(s0[2 + e], p.scale_log2, -u1));
-        s1[2 + e] = exp2_fast(fmaf(s1[2 + e], p.scale_log2, -u1));
-      }
-      l0 += (s0[0] + s0[1]) + (s1[0] + s1[1]);
-      l1 += (s0[2] + s0[3]) + (s1[2] + s1[3]);
-      uint32_t ph[4], pl[4];
-      split2<F16>(s0[0], s0[1], ph[0], pl[0]);
-      split2<F16>(s0[2], s0[3], ph[1], pl[1]);
-      split2<F16>(s1[0], s1[1], ph[2], pl[2]);
-      split2<F16>(s1[2], s1[3], ph[3], pl[3]);
-      const uint32_t v_row = sv + (k0 + (mi & 1) * 8 + l8) * VPITCH;
+      for (int r = 0; r < 2; ++r) {
+        const bool live = page[r] >= 0 && page[r] < p.n_pages;
+        // (a row behind the end of the sequence has slot 0 and page -1 too)
+        const uint16_t* k = live ? p.k + page[r] * p.kp[0] + next_h * p.kp[1] + slot[r] * p.kp[2] + 8 * q4 : p.q;
+        const uint16_t* v = live ? p.v + page[r] * p.vp[0] + next_h * p.vp[1] + slot[r] * p.vp[2] + 8 * q4 : p.q;
 #pragma unroll
-      for (int d = 0; d < DV / 16; ++d) {
-        uint32_t vb[4];
-        ldsm4t(vb, v_row + (((d * 2 + (mi >> 1)) ^ l8) << 4));
-        mma16816<F16>(acc[2 * d], ph, vb[0], vb[1]);
-        mma16816<F16>(acc[2 * d + 1], ph, vb[2], vb[3]);
-        mma16816<F16>(acc[2 * d], pl, vb[0], vb[1]);
-        mma16816<F16>(acc[2 * d + 1], pl, vb[2], vb[3]);
+        for (int j = 0; j < DQ / 32; ++j) {
+          const bool in = live && 32 * j + 8 * q4 < p.dqk;
+          cp_async16((kd ^ ((j & 1) << 6)) + r * 8 * KPITCH + (j >> 1) * 128, in ? k + 32 * j : p.q, in);
+        }
+#pragma unroll
+        for (int j = 0; j < DV / 32; ++j) {
+          const bool in = live && 32 * j + 8 * q4 < p.dv;
+          cp_async16((vd ^ ((j & 1) << 6)) + r * 8 * VPITCH + (j >> 1) * 128, in ? v + 32 * j : p.q, in);
+        }
       }
+    };
+    // reported when its copies are issued (by then the number has arrived)
+    auto check_pages = [&](const Cursor& a) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (a.t * BN + g + 8 * r < a.len && (page[r] < 0 || page[r] >= p.n_pages)) *p.err = 1;
+    };
+    Cursor ahead = cur;  // the step that page[], slot[] are of
+    lookup(ahead);
+    load_q(cur);
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j) {
+      if (j < count) {
+        check_pages(ahead);
+        issue(j);
+        if (j + 1 < count) {
+          advance(ahead);
+          lookup(ahead);
+        }
+      }
+      cp_async_commit();
     }
 
-    // ---- end of the unit, or of the range: join the warps, write
-    if (cur.t + 1 == cur.nt || i + 1 == count) {
-      const Cursor done = cur;
-      const bool more = i + 1 < count;
-      if (more) {
-        advance(cur);
-        load_q(cur, qreg);
-      }
-      const bool begins = seg_t0 == 0, ends = done.t + 1 == done.nt;
-      const int h = done.hu / p.chunks, chunk = done.hu - h * p.chunks;
-      const int g0 = chunk * p.rows, n_rows = min(p.rows, p.G - g0);
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-      if (q4 == 0) {
-        ml[warp * 16 + g] = make_float2(m0, l0);
-        ml[warp * 16 + g + 8] = make_float2(m1, l1);
-      }
-      __syncthreads();  // statistics written; nobody reads this stage or Q any more
-      if (more) store_q(qreg);
-      // maximum and sum of row r of this CTA's part
-      auto row_stat = [&](int r) -> float2 {
-        const int w0 = r >> 4, rr = r & 15;
-        float m = -INFINITY, l = 0.f;
-        for (int w = 0; w < WK; ++w) m = fmaxf(m, ml[(w * p.wr + w0) * 16 + rr].x);
-        const float u = m == -INFINITY ? 0.f : m;
-        for (int w = 0; w < WK; ++w) {
-          const float2 x = ml[(w * p.wr + w0) * 16 + rr];
-          l += exp2_fast(x.x - u) * x.y;
+    int t0 = cur.t;  // first step of the unit in this warp
+    int stage = 0;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      // refill the stage of the step before this one, which every lane has read
+      __syncwarp();
+      if (i + S - 1 < count) {
+        check_pages(ahead);
+        issue(stage == 0 ? S - 1 : stage - 1);
+        if (i + S < count) {
+          advance(ahead);
+          lookup(ahead);
         }
-        return make_float2(m, l);
-      };
-      const float2 st0 = row_stat(wr * 16 + g), st1 = row_stat(wr * 16 + g + 8);
-      const float f0 = exp2_fast(m0 - (st0.x == -INFINITY ? 0.f : st0.x));
-      const float f1 = exp2_fast(m1 - (st1.x == -INFINITY ? 0.f : st1.x));
-      const bool whole = begins && ends;
-      const long long slot = 2LL * c + (begins ? 1 : 0);
-      float* buf = reinterpret_cast<float*>(smem + P::Q_BYTES + stage * P::TILE_BYTES);
-      constexpr int CW = P::CW, NB = CW / 8;  // 8-column blocks, swizzled by the row
-      constexpr int SW = NB < 8 ? NB - 1 : 7;
+      }
+      cp_async_commit();
+      cp_async_wait<S - 1>();
+      __syncwarp();
+
+      const uint32_t sk = ring + stage * P::STAGE, sv = sk + P::K_BYTES;
+      const int live = cur.len - cur.t * BN;  // keys of this step
+      constexpr int CH = NT == 1 ? 2 : 1;     // chains of products
+      float s[CH][NT][4];
 #pragma unroll
-      for (int c0 = 0; c0 < DV; c0 += CW) {
-        if (c0 > 0) __syncthreads();
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int d = 0; d < NB; ++d) {
-          float* x = buf + (warp * 16 + g) * CW + ((d ^ (g & SW)) * 8) + 2 * q4;
-          const float* a = acc[c0 / 8 + d];
-          *reinterpret_cast<float2*>(x) = make_float2(a[0] * f0, a[1] * f0);
-          *reinterpret_cast<float2*>(x + 8 * CW) = make_float2(a[2] * f1, a[3] * f1);
-        }
-        __syncthreads();
-        for (int x = tid; x < n_rows * (CW / 4); x += THREADS) {
-          const int r = x / (CW / 4), c4 = x % (CW / 4);
-          const int w0 = r >> 4, rr = r & 15;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int w = 0; w < WK; ++w) {
-            const float4 y = *reinterpret_cast<const float4*>(
-                buf + ((w * p.wr + w0) * 16 + rr) * CW + (((c4 >> 1) ^ (rr & SW)) * 8) + (c4 & 1) * 4);
-            o.x += y.x;
-            o.y += y.y;
-            o.z += y.z;
-            o.w += y.w;
-          }
-          const int col = c0 + 4 * c4;
-          if (whole) {
-            const float2 st = row_stat(r);
-            const float inv = st.y == 0.f ? 0.f : 1.f / st.y;
-            const long long row = (static_cast<long long>(done.b) * p.Hkv + h) * p.G + g0 + r;
-            if (col < p.dv)
-              *reinterpret_cast<uint2*>(p.o + row * p.dv + col) =
-                  make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
-            if (col == 0) p.lse[row] = st.y == 0.f ? -INFINITY : st.x * 0.6931471805599453f + logf(st.y);
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[c][n][e] = 0.f;
+      const uint32_t k_row = sk + ((mi & 1) * 8 + l8) * KPITCH;
+#pragma unroll
+      for (int ks = 0; ks < DQ / 16; ++ks) {
+        uint32_t ka[4];
+        ldsm4(ka, k_row + (((2 * ks + (mi >> 1)) ^ l8) << 4));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (P::QREG) {
+            mma16816<F16>(s[ks % CH][n], ka, qr[ks][n][0], qr[ks][n][1]);
           } else {
-            *reinterpret_cast<float4*>(p.part_o + (slot * p.rows + r) * DV + col) = o;
-            if (col == 0) p.part_ml[slot * p.rows + r] = row_stat(r);
+            const uint2 q = qs[(ks * NT + n) * 32];
+            mma16816<F16>(s[ks % CH][n], ka, q.x, q.y);
           }
         }
       }
-      if (begins && !ends && tid == 0) {
-        // the CTA that the unit's last tile falls to
-        const long long last = lo + i + (done.nt - 1 - done.t);
-        const int parts = static_cast<int>(((last + 1) * ctas - 1) / total) - c + 1;
-        p.desc[c] = make_int4(done.b, done.hu, parts, 0);
-      }
-      if (more) {
-        seg_t0 = 0;
-        m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
+      bool grows = false;
 #pragma unroll
-        for (int d = 0; d < DV / 8; ++d)
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[d][e] = 0.f;
-        // (store_q is ordered before this by the barriers of the exchange)
-        if constexpr (QREG) {
-#pragma unroll
-          for (int ks = 0; ks < DQ / 16; ++ks) q_frag(ks, qf[ks]);
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (CH == 2) s[0][n][e] += s[1][n][e];
+          s[0][n][e] *= p.scale_log2;
+          if (g + (e >> 1) * 8 >= live) s[0][n][e] = -INFINITY;
+          grows = grows || s[0][n][e] > m[n][e & 1] + 8.f;
         }
       }
-    } else {
-      ++cur.t;
+      if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(s[0][n][e], s[0][n][2 + e]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            x = fmaxf(x, m[n][e]);
+            const float a = exp2_fast(m[n][e] - (x == -INFINITY ? 0.f : x));
+            m[n][e] = x;
+            l[n][e] *= a;
+#pragma unroll
+            for (int d = 0; d < DV / 16; ++d) {
+              acc[n][d][e] *= a;
+              acc[n][d][2 + e] *= a;
+            }
+          }
+      }
+      uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        // a head whose scores are all -inf keeps weights of 0
+        const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0], u1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float a = exp2_fast(s[0][n][2 * e] - u0), b = exp2_fast(s[0][n][2 * e + 1] - u1);
+          l[n][0] += a;
+          l[n][1] += b;
+          split2<F16>(a, b, ph[n][e], pl[n][e]);
+          ph[n][e] = movmatrix_t(ph[n][e]);
+          pl[n][e] = movmatrix_t(pl[n][e]);
+        }
+      }
+      const uint32_t v_row = sv + ((mi >> 1) * 8 + l8) * VPITCH;
+#pragma unroll
+      for (int d = 0; d < DV / 16; ++d) {
+        uint32_t va[4];
+        ldsm4t(va, v_row + (((2 * d + (mi & 1)) ^ l8) << 4));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma16816<F16>(acc[n][d], va, ph[n][0], ph[n][1]);
+          mma16816<F16>(acc[n][d], va, pl[n][0], pl[n][1]);
+        }
+      }
+
+      // ---- the unit ends here, or the range does
+      const bool last = i + 1 == count;
+      if (cur.t + 1 == cur.nt || last) {
+        const bool begins = t0 == 0, ends = cur.t + 1 == cur.nt;
+        const int h = cur.hu / p.chunks, g0 = (cur.hu - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+            l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+          }
+        if (!same_unit) {
+          const long long part = 2LL * me + (begins ? 1 : 0);
+          const long long row0 = (static_cast<long long>(cur.b) * p.Hkv + h) * p.G + g0;
+          float* scratch = reinterpret_cast<float*>(mine + stage * P::STAGE);  // read; refilled in the next step
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            __syncwarp();
+            spill(scratch, n, 1.f, 1.f);
+            __syncwarp();
+#pragma unroll
+            for (int x = lane; x < 8 * (DV / 4); x += 32) {
+              const int r = x / (DV / 4), c4 = x % (DV / 4);
+              const float ma = __shfl_sync(0xffffffffu, m[n][0], r >> 1), mb = __shfl_sync(0xffffffffu, m[n][1], r >> 1);
+              const float la = __shfl_sync(0xffffffffu, l[n][0], r >> 1), lb = __shfl_sync(0xffffffffu, l[n][1], r >> 1);
+              const float mm = r & 1 ? mb : ma, ll = r & 1 ? lb : la;
+              const float4 o = *reinterpret_cast<const float4*>(scratch + r * PITCH + 4 * c4);
+              const int row = 8 * n + r;
+              if (row < n_rows) {
+                if (begins && ends) {
+                  write_row(row0 + row, 4 * c4, o, mm, ll);
+                } else {
+                  *reinterpret_cast<float4*>(p.part_o + (part * p.rows + row) * DV + 4 * c4) = o;
+                  if (c4 == 0) p.part_ml[part * p.rows + row] = make_float2(mm, ll);
+                }
+              }
+            }
+          }
+          if (begins && !ends && lane == 0) {
+            // parts: up to the warp that the unit's last step falls to
+            const long long end = lo + i + (cur.nt - 1 - cur.t);
+            p.desc[me] = make_int4(cur.b, cur.hu, static_cast<int>(((end + 1) * warps - 1) / total) - me + 1, 0);
+          }
+        }
+        if (!last) {
+          clear();
+          advance(cur);
+          t0 = 0;
+          load_q(cur);
+        }
+      } else {
+        ++cur.t;
+      }
+      stage = stage + 1 == S ? 0 : stage + 1;
     }
-    stage = stage + 1 == S ? 0 : stage + 1;
+  }
+
+  // ---- a CTA within one unit: its warps' parts joined here
+  if (!same_unit) return;
+  float* parts = reinterpret_cast<float*>(mine);
+  cp_async_wait<0>();
+  // statistics of every warp and head, behind its spilled O
+  constexpr int ROWS = NT * 8;
+  float2* my_ml = reinterpret_cast<float2*>(parts + ROWS * PITCH);
+  __syncwarp();
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    spill(parts + 8 * n * PITCH, n, 1.f, 1.f);
+    if (g == 0) {
+      my_ml[8 * n + 2 * q4] = make_float2(m[n][0], l[n][0]);
+      my_ml[8 * n + 2 * q4 + 1] = make_float2(m[n][1], l[n][1]);
+    }
+  }
+  __syncthreads();
+  const int3 a = start[0];
+  const int nt = steps_of(length(a.x));
+  const int n_steps = static_cast<int>(range_start(first + NW) - range_start(first));
+  const bool begins = a.z == 0, ends = a.z + n_steps == nt;
+  const int h = a.y / p.chunks, g0 = (a.y - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
+  const long long part = 2LL * first + (begins ? 1 : 0);
+  const long long row0 = (static_cast<long long>(a.x) * p.Hkv + h) * p.G + g0;
+  for (int x = tid; x < n_rows * (DV / 4); x += THREADS) {
+    const int r = x / (DV / 4), c4 = x % (DV / 4);
+    float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+      mm = fmaxf(mm, reinterpret_cast<const float2*>(smem + w * P::WARP_BYTES + ROWS * PITCH * 4)[r].x);
+    const float u = mm == -INFINITY ? 0.f : mm;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const char* from = smem + w * P::WARP_BYTES;
+      const float2 s = reinterpret_cast<const float2*>(from + ROWS * PITCH * 4)[r];
+      const float f = exp2_fast(s.x - u);
+      const float4 y = *reinterpret_cast<const float4*>(from + (r * PITCH + 4 * c4) * 4);
+      ll = fmaf(f, s.y, ll);
+      o.x = fmaf(f, y.x, o.x);
+      o.y = fmaf(f, y.y, o.y);
+      o.z = fmaf(f, y.z, o.z);
+      o.w = fmaf(f, y.w, o.w);
+    }
+    if (begins && ends) {
+      write_row(row0 + r, 4 * c4, o, mm, ll);
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (part * p.rows + r) * DV + 4 * c4) = o;
+      if (c4 == 0) p.part_ml[part * p.rows + r] = make_float2(mm, ll);
+    }
+  }
+  if (begins && ends) return;
+  // the other warps' parts are in it: empty
+  for (int x = tid; x < (NW - 1) * n_rows; x += THREADS)
+    p.part_ml[2LL * (first + 1 + x / n_rows) * p.rows + x % n_rows] = make_float2(-INFINITY, 0.f);
+  if (begins && tid == 0) {
+    const long long end = range_start(first) + (nt - 1);
+    p.desc[first] = make_int4(a.x, a.y, static_cast<int>(((end + 1) * warps - 1) / total) - first + 1, 0);
   }
 }
 
-// Joins the parts of a unit that several CTAs of the kernel above share:
-// block c takes the unit that starts in CTA c and ends in a later one, if
-// there is one.  A warp takes a row, or a row's parts together with other
-// warps when there are fewer rows than warps.
+// Joins the parts of the units that several warps of the kernel above share:
+// block c takes the units that start in a warp of CTA c and end in a later
+// one.  A warp takes a head of one of them, or its parts together with other
+// warps when there are fewer heads than warps.
 template <int DV, bool F16>
 __global__ void __launch_bounds__(512) attn_decode_join(const __grid_constant__ DecodeParams p) {
   constexpr int NW = 16, VPL = DV / 32;  // values of a lane
-  __shared__ float part[NW][DV];
+  __shared__ float sum[NW][DV];
+  __shared__ int4 units[NW];
+  __shared__ int n_units;
+  __shared__ float2 list[NW][32];  // parts that hold something: number, weight
   griddep_wait();
   griddep_launch_dependents();
-  const int c = blockIdx.x;
-  const int4 d = p.desc[c];
-  if (d.x < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = d.y / p.chunks, chunk = d.y - h * p.chunks;
-  const int g0 = chunk * p.rows, n_rows = min(p.rows, p.G - g0);
-  const int per_row = n_rows >= NW ? 1 : NW / n_rows;  // warps of a row
-  const int parts = d.z;
-  auto slot = [&](int i) { return 2LL * (c + i) + (i == 0 ? 1 : 0); };
-  for (int r0 = 0; r0 < n_rows; r0 += NW / per_row) {
-    const int r = r0 + warp / per_row, s = warp % per_row;
-    const bool on = warp < NW / per_row * per_row && r < n_rows;
+  if (warp == 0) {
+    int4 d = make_int4(-1, 0, 0, 0);
+    if (lane < p.cta_warps) d = p.desc[blockIdx.x * p.cta_warps + lane];
+    const unsigned have = __ballot_sync(0xffffffffu, d.x >= 0);
+    if (d.x >= 0) units[__popc(have & ((1u << lane) - 1))] = make_int4(d.x, d.y, d.z, blockIdx.x * p.cta_warps + lane);
+    if (lane == 0) n_units = __popc(have);
+  }
+  __syncthreads();
+  const int items = n_units * p.rows;  // (the rows of a short last chunk are skipped)
+  if (items == 0) return;
+  const int per = items >= NW ? 1 : NW / items;  // warps of an item
+  for (int i0 = 0; i0 < items; i0 += NW / per) {
+    const int it = i0 + warp / per, s = warp % per;
+    bool on = warp < NW / per * per && it < items;
+    const int4 d = units[on ? it / p.rows : 0];
+    const int r = on ? it % p.rows : 0;
+    const int h = d.y / p.chunks, g0 = (d.y - h * p.chunks) * p.rows;
+    on = on && g0 + r < p.G;
+    auto part = [&](int i) { return 2LL * (d.w + i) + (i == 0 ? 1 : 0); };
     float m = -INFINITY, l = 0.f, acc[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) acc[v] = 0.f;
     if (on) {
-      for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[slot(i) * p.rows + r].x);
+      for (int i = lane; i < d.z; i += 32) m = fmaxf(m, p.part_ml[part(i) * p.rows + r].x);
 #pragma unroll
       for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float u = m == -INFINITY ? 0.f : m;
-      for (int i = lane; i < parts; i += 32) {
-        const float2 x = p.part_ml[slot(i) * p.rows + r];
-        l += exp2_fast(x.x - u) * x.y;
+      int seen = 0;
+      for (int i0p = 0; i0p < d.z; i0p += 32) {
+        const int i = i0p + lane;
+        const float2 x = i < d.z ? p.part_ml[part(i) * p.rows + r] : make_float2(-INFINITY, 0.f);
+        const float w = exp2_fast(x.x - u);
+        l = fmaf(w, x.y, l);
+        // (a part of NaN scores has no maximum but a sum)
+        const unsigned have = __ballot_sync(0xffffffffu, !(x.y == 0.f));
+        __syncwarp();
+        if (!(x.y == 0.f)) list[warp][__popc(have & ((1u << lane) - 1))] = make_float2(__int_as_float(i), w);
+        __syncwarp();
+        const int n = __popc(have);
+        const int k0 = (s + per - seen % per) % per;
+#pragma unroll 4
+        for (int k = k0; k < n; k += per) {
+          const float2 e = list[warp][k];
+          const float* y = p.part_o + (part(__float_as_int(e.x)) * p.rows + r) * DV + lane * VPL;
+#pragma unroll
+          for (int v = 0; v < VPL; v += 2) {
+            const float2 z = *reinterpret_cast<const float2*>(y + v);
+            acc[v] = fmaf(e.y, z.x, acc[v]);
+            acc[v + 1] = fmaf(e.y, z.y, acc[v + 1]);
+          }
+        }
+        seen += n;
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-#pragma unroll 4
-      for (int i = s; i < parts; i += per_row) {
-        const float w = exp2_fast(p.part_ml[slot(i) * p.rows + r].x - u);
-        const float* x = p.part_o + (slot(i) * p.rows + r) * DV + lane * VPL;
-#pragma unroll
-        for (int v = 0; v < VPL; v += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(x + v);
-          acc[v] = fmaf(w, y.x, acc[v]);
-          acc[v + 1] = fmaf(w, y.y, acc[v + 1]);
-        }
-      }
     }
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) part[warp][lane * VPL + v] = acc[v];
+    for (int v = 0; v < VPL; ++v) sum[warp][lane * VPL + v] = acc[v];
     __syncthreads();
     if (on && s == 0) {
-      for (int k = 1; k < per_row; ++k)
+      for (int k = 1; k < per; ++k)
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) acc[v] += part[warp + k][lane * VPL + v];
+        for (int v = 0; v < VPL; ++v) acc[v] += sum[warp + k][lane * VPL + v];
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const long long row = (static_cast<long long>(d.x) * p.Hkv + h) * p.G + g0 + r;
 #pragma unroll
@@ -643,27 +702,33 @@ cudaError_t decode_launch_one(K kernel, const DecodeParams& p, int grid, int thr
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int DQ, int DV, bool F16, int NW>
-cudaError_t launch_decode_nw(const DecodeParams& p, int ctas, cudaStream_t stream) {
-  constexpr int smem = DecodePlan<DQ, DV, NW>::SMEM;
+template <int DQ, int DV, bool F16, int NT>
+cudaError_t launch_decode_nt(DecodeParams& p, int ctas, cudaStream_t stream) {
+  using P = DecodePlan<DQ, DV, NT>;
   static bool attr_done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(attn_decode_kernel<DQ, DV, F16, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(attn_decode_kernel<DQ, DV, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
-  e = decode_launch_one(attn_decode_kernel<DQ, DV, F16, NW>, p, ctas, NW * 32, smem, stream);
+  p.cta_warps = P::NW;
+  e = decode_launch_one(attn_decode_kernel<DQ, DV, F16, NT>, p, ctas, P::NW * 32, P::SMEM, stream);
   if (e != cudaSuccess || !p.split) return e;
   return decode_launch_one(attn_decode_join<DV, F16>, p, ctas, 512, 0, stream);
 }
 
 template <int DQ, int DV, bool F16>
-cudaError_t launch_decode(const DecodeParams& p, int nw, int ctas, cudaStream_t stream) {
-  return nw == 4 ? launch_decode_nw<DQ, DV, F16, 4>(p, ctas, stream) : launch_decode_nw<DQ, DV, F16, 8>(p, ctas, stream);
+cudaError_t launch_decode(DecodeParams& p, int nt, int ctas, cudaStream_t stream) {
+  if (nt == 1) return launch_decode_nt<DQ, DV, F16, 1>(p, ctas, stream);
+  if (nt == 2) return launch_decode_nt<DQ, DV, F16, 2>(p, ctas, stream);
+  if constexpr (decode_max_rows(DV) == 32)
+    return launch_decode_nt<DQ, DV, F16, 4>(p, ctas, stream);
+  else
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace attn

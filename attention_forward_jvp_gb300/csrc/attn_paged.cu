@@ -12,8 +12,8 @@
 namespace attn {
 
 #define ATTN_DECODE_DECL(DQ, DV)                                                                         \
-  extern template cudaError_t launch_decode<DQ, DV, false>(const DecodeParams&, int, int, cudaStream_t); \
-  extern template cudaError_t launch_decode<DQ, DV, true>(const DecodeParams&, int, int, cudaStream_t);
+  extern template cudaError_t launch_decode<DQ, DV, false>(DecodeParams&, int, int, cudaStream_t);       \
+  extern template cudaError_t launch_decode<DQ, DV, true>(DecodeParams&, int, int, cudaStream_t);
 ATTN_DECODE_DECL(64, 64)
 ATTN_DECODE_DECL(64, 128)
 ATTN_DECODE_DECL(64, 256)
@@ -233,7 +233,7 @@ attn_status run_append(const attn_paged_cache* c, const attn_paged_new* n, const
 struct Layout {
   int dq, dv;          // kernel head dims
   int rows, chunks;    // query heads of a unit, units of a key head
-  int nw, wr;          // warps, 16-row groups
+  int nt;              // groups of 8 query heads
   int ctas;
   size_t desc, ml, total;  // workspace: bytes of the first two parts, of all
 };
@@ -241,31 +241,31 @@ Layout layout_of(const attn_paged_cache* c, int Hq, int sms) {
   Layout l;
   l.dq = c->Dqk < 64 ? 64 : c->Dqk;
   l.dv = c->Dv < 64 ? 64 : c->Dv;
-  const int G = Hq / c->Hkv;
-  l.chunks = (G + kDecodeMaxRows - 1) / kDecodeMaxRows;
+  const int G = Hq / c->Hkv, most = decode_max_rows(l.dv);
+  l.chunks = (G + most - 1) / most;
   l.rows = (G + l.chunks - 1) / l.chunks;
-  l.nw = l.rows <= 16 ? 4 : 8;
-  l.wr = l.rows <= 16 ? 1 : (l.rows <= 32 ? 2 : 4);
-  l.ctas = sms * decode_ctas_per_sm(l.dq, l.dv, l.nw);
+  l.nt = l.rows <= 8 ? 1 : (l.rows <= 16 ? 2 : 4);
+  l.ctas = sms;
+  const size_t warps = static_cast<size_t>(sms) * kDecodeMaxWarps;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  l.desc = up(sizeof(int4) * l.ctas);
-  l.ml = up(sizeof(float2) * 2 * l.ctas * l.rows);
-  l.total = l.desc + l.ml + sizeof(float) * 2 * l.ctas * static_cast<size_t>(l.rows) * l.dv;
+  l.desc = up(sizeof(int4) * warps);
+  l.ml = up(sizeof(float2) * 2 * warps * l.rows);
+  l.total = l.desc + l.ml + sizeof(float) * 2 * warps * static_cast<size_t>(l.rows) * l.dv;
   return l;
 }
 
 template <bool F16>
-cudaError_t dispatch_decode(const Layout& l, const DecodeParams& p, cudaStream_t s) {
+cudaError_t dispatch_decode(const Layout& l, DecodeParams& p, cudaStream_t s) {
   switch (l.dq * 1000 + l.dv) {
-    case 64064: return launch_decode<64, 64, F16>(p, l.nw, l.ctas, s);
-    case 64128: return launch_decode<64, 128, F16>(p, l.nw, l.ctas, s);
-    case 64256: return launch_decode<64, 256, F16>(p, l.nw, l.ctas, s);
-    case 128064: return launch_decode<128, 64, F16>(p, l.nw, l.ctas, s);
-    case 128128: return launch_decode<128, 128, F16>(p, l.nw, l.ctas, s);
-    case 128256: return launch_decode<128, 256, F16>(p, l.nw, l.ctas, s);
-    case 256064: return launch_decode<256, 64, F16>(p, l.nw, l.ctas, s);
-    case 256128: return launch_decode<256, 128, F16>(p, l.nw, l.ctas, s);
-    case 256256: return launch_decode<256, 256, F16>(p, l.nw, l.ctas, s);
+    case 64064: return launch_decode<64, 64, F16>(p, l.nt, l.ctas, s);
+    case 64128: return launch_decode<64, 128, F16>(p, l.nt, l.ctas, s);
+    case 64256: return launch_decode<64, 256, F16>(p, l.nt, l.ctas, s);
+    case 128064: return launch_decode<128, 64, F16>(p, l.nt, l.ctas, s);
+    case 128128: return launch_decode<128, 128, F16>(p, l.nt, l.ctas, s);
+    case 128256: return launch_decode<128, 256, F16>(p, l.nt, l.ctas, s);
+    case 256064: return launch_decode<256, 64, F16>(p, l.nt, l.ctas, s);
+    case 256128: return launch_decode<256, 128, F16>(p, l.nt, l.ctas, s);
+    case 256256: return launch_decode<256, 256, F16>(p, l.nt, l.ctas, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -313,8 +313,7 @@ attn_status run_decode(const attn_paged_cache* c, int32_t Hq, const void* q, con
   p.G = Hq / c->Hkv;
   p.rows = l.rows;
   p.chunks = l.chunks;
-  p.wr = l.wr;
-  p.min_tiles = 1;
+  p.min_steps = 2;
   p.dqk = c->Dqk;
   p.dv = c->Dv;
   const float scale = std::isnan(sm_scale) ? 1.0f / std::sqrt(static_cast<float>(c->Dqk)) : sm_scale;

@@ -60,8 +60,10 @@ cudaError_t launch_rope(const RopeParams& p, bool vec, bool f16, int splits, cud
 cudaError_t launch_append(const AppendParams& p, bool vec, bool f16, int splits, cudaStream_t stream);
 
 // -------------------------------------------------------------------- decode
-constexpr int kDecodeBN = 64;        // keys of a tile
-constexpr int kDecodeMaxRows = 64;   // query heads of one work unit
+constexpr int kDecodeBN = 16;        // keys of a step
+constexpr int kDecodeMaxWarps = 16;  // warps of a CTA, at most
+// query heads of a work unit, at most: what the accumulators leave room for
+constexpr int decode_max_rows(int dv) { return dv <= 128 ? 32 : 16; }
 
 struct DecodeParams {
   const uint16_t *q, *k, *v;
@@ -74,24 +76,23 @@ struct DecodeParams {
   int capacity;                // keys a table row can hold
   int Hkv, G;                  // key heads, query heads of each
   int rows, chunks;            // query heads of a work unit, units of a key head
-  int wr;                      // 16-row groups of a unit (1, 2 or 4)
-  int min_tiles;               // tiles a CTA takes at least
+  int min_steps;               // steps a warp takes at least
   int dqk, dv;                 // true head dims (<= the kernel's)
   float scale_log2;
   uint16_t* o;
   float* lse;
-  int4* desc;                  // [CTA]: the unit that starts in it and ends in a later one
-  float2* part_ml;             // [CTA][2][rows]
-  float* part_o;               // [CTA][2][rows][kernel Dv]
+  int4* desc;                  // [warp]: the unit that starts in it and ends in a later one
+  float2* part_ml;             // [warp][2][rows]
+  float* part_o;               // [warp][2][rows][kernel Dv]
   int* err;
-  int split;                   // 0: no sequence can have more than one tile
+  int split;                   // 0: no sequence can have more than one step
+  int cta_warps;               // warps of a CTA (set by the launch)
 };
 
-// CTAs the decode kernel of these head dims runs with, and its launch
-// (followed, when p.split, by the joining kernel).  nw: 4 or 8 warps.
-constexpr int decode_ctas_per_sm(int dq, int dv, int nw) { return nw == 4 && dq + dv <= 256 ? 2 : 1; }
+// The decode kernel for kernel head dims DQ, DV and nt (1, 2 or 4) groups of
+// 8 query heads, followed, when p.split, by the joining kernel.
 template <int DQ, int DV, bool F16>
-cudaError_t launch_decode(const DecodeParams& p, int nw, int ctas, cudaStream_t stream);
+cudaError_t launch_decode(DecodeParams& p, int nt, int ctas, cudaStream_t stream);
 
 // Device word that append and decode set on a bad page number or length;
 // null where no call has set it up on this device.
