@@ -103,6 +103,11 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
   return d;
 }
 
+// a / b of whole numbers >= 0, b > 0: in 32 bits where both fit
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
 // Shared memory and registers of a warp decide how many fit on an SM: three
 // stages of 16 keys where that leaves six warps or more (two thirds of the
 // ring in flight while a stage is read), else two; Q in registers unless it
@@ -142,8 +147,8 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   const uint32_t ring = smem_u32(mine);
   uint2* qs = reinterpret_cast<uint2*>(mine + S * P::STAGE) + lane;
   char* misc = smem + NW * P::WARP_BYTES;
-  long long* scan = reinterpret_cast<long long*>(misc);          // [NW]
-  int3* start = reinterpret_cast<int3*>(misc + 8 * 16);          // [NW]: b, unit, step
+  long long* scan = reinterpret_cast<long long*>(misc);      // [2][16]
+  int4* start = reinterpret_cast<int4*>(misc + 2 * 8 * 16);  // [NW]: b, unit, step, length
   const int HU = p.Hkv * p.chunks;  // units of a sequence
 
   griddep_wait();
@@ -155,28 +160,62 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   };
   auto steps_of = [](int len) { return (len + BN - 1) / BN; };
 
-  // ---- the ranges of the warps: warp x takes steps [total x / warps, total (x + 1) / warps)
-  long long sum = 0;
-  for (int b = tid; b < p.B; b += THREADS) {
-    const int raw = __ldg(p.seq_lens + b), n = length(b);
-    if (raw != n && blockIdx.x == 0) *p.err = 1;
-    sum += steps_of(n);
+  // ---- the ranges of the warps: `total` steps over `warps` warps, one more
+  // for the first total % warps.  Thread x holds sequence x (and adds up those
+  // THREADS apart behind it).
+  const int n_mine = tid < p.B ? length(tid) : 0;
+  long long inc = steps_of(n_mine), rest = 0;  // steps up to this sequence, of later ones
+  bool odd = tid < p.B && __ldg(p.seq_lens + tid) != n_mine;
+  for (int b = tid + THREADS; b < p.B; b += THREADS) {
+    const int n = length(b);
+    odd = odd || __ldg(p.seq_lens + b) != n;
+    rest += steps_of(n);
   }
+  if (odd && blockIdx.x == 0) *p.err = 1;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) scan[warp] = sum;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (p.B > THREADS) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+  }
+  if (lane == 31) scan[warp] = inc;
+  if (lane == 0) scan[16 + warp] = rest;
   __syncthreads();
-  long long total = 0;
+  long long before = 0, chunk = 0, total = 0;  // steps of the warps before, of this chunk, of all
 #pragma unroll
-  for (int w = 0; w < NW; ++w) total += scan[w];
-  total *= HU;
-  long long warps = (total + p.min_steps - 1) / p.min_steps;
-  if (warps > static_cast<long long>(gridDim.x) * NW) warps = static_cast<long long>(gridDim.x) * NW;
-  auto range_start = [&](long long x) { return x < warps ? total * x / warps : total; };
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += scan[w];
+    chunk += scan[w];
+    total += scan[16 + w];
+  }
+  total = (total + chunk) * HU;
+  const long long most = static_cast<long long>(gridDim.x) * NW;
+  long long warps = total / p.min_steps + 1;
+  if (warps > most) warps = most;
+  if (warps > total) warps = total;
+  if (warps < 1) warps = 1;
+  const long long each = divide(total, warps), more = total - each * warps;
+  auto range_start = [&](long long x) { return x < warps ? each * x + (x < more ? x : more) : total; };
+  // the warp that step x falls to
+  auto owner = [&](long long x) -> long long {
+    return x < more * (each + 1) ? divide(x, each + 1) : more + divide(x - more * (each + 1), each);
+  };
+  // What joins a unit that begins in warp w and has its last step at `end`:
+  // the parts of w's CTA from w on (`here` of them), one for each CTA that
+  // lies within the unit, and those of the CTA where it ends.
+  auto describe = [&](int b, int hu, int w, int here, long long end) -> int4 {
+    const int z = static_cast<int>(owner(end)), c = w / NW, e = z / NW;
+    if (e == c) return make_int4(b, hu, z - w + 1, 0);
+    const bool joined = range_start((e + 1LL) * NW) == end + 1;  // CTA e lies within the unit too
+    return make_int4(b, hu, here | (joined ? 1 : z - e * NW + 1) << 8, e - c - 1);
+  };
   const int first = blockIdx.x * NW;  // this CTA's first warp
   const int me = first + warp;
-  const long long lo = range_start(me), hi = range_start(me + 1);
-  const int count = static_cast<int>(hi - lo);
+  const long long lo = range_start(me);
+  const int count = static_cast<int>(range_start(me + 1) - lo);
 
   // ---- sequences without keys: O = 0, LSE = -inf
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -187,16 +226,31 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     for (int i = tid; i < Hq; i += THREADS) p.lse[static_cast<long long>(b) * Hq + i] = -INFINITY;
   }
   if (p.split && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
-  if (first >= warps) return;
+  if (range_start(first) >= total) return;
 
   // ---- the sequence, unit and step that each warp's range starts with
   {
-    long long before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
-      const int b = b0 + tid;
-      const int n = b < p.B ? steps_of(length(b)) : 0;
-      const long long own = static_cast<long long>(n) * HU;
-      long long inc = own;
+    long long base = 0;  // steps of the chunks before
+    int n = n_mine;
+    for (int b0 = 0;;) {
+      const int steps = steps_of(n);
+      const long long begin = (base + before + inc - steps) * HU;
+      if (steps > 0) {
+        const long long own = static_cast<long long>(steps) * HU;
+#pragma unroll 1
+        for (int w = 0; w < NW; ++w) {
+          const long long x = range_start(first + w) - begin;
+          if (0 <= x && x < own) {
+            const long long u = divide(x, steps);
+            start[w] = make_int4(b0 + tid, static_cast<int>(u), static_cast<int>(x - u * steps), n);
+          }
+        }
+      }
+      base += chunk;
+      b0 += THREADS;
+      if (b0 >= p.B || range_start(first + NW - 1) < base * HU) break;
+      n = b0 + tid < p.B ? length(b0 + tid) : 0;
+      inc = steps_of(n);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, inc, o);
@@ -205,22 +259,12 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
       __syncthreads();
       if (lane == 31) scan[warp] = inc;
       __syncthreads();
-      long long base = before, all = before;
+      before = chunk = 0;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        if (w < warp) base += scan[w];
-        all += scan[w];
+        if (w < warp) before += scan[w];
+        chunk += scan[w];
       }
-      const long long begin = base + inc - own;
-      if (own > 0) {
-#pragma unroll 1
-        for (int w = 0; w < NW; ++w) {
-          const long long x = range_start(first + w) - begin;
-          if (0 <= x && x < own) start[w] = make_int3(b, static_cast<int>(x / n), static_cast<int>(x % n));
-        }
-      }
-      before = all;
-      if (range_start(first + NW - 1) < all) break;
     }
     __syncthreads();
   }
@@ -247,8 +291,8 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   Cursor cur;
   bool same_unit = false;  // the whole CTA lies within one unit
   {
-    const int3 a = start[0];
-    const int nt = steps_of(length(a.x));
+    const int4 a = start[0];
+    const int nt = steps_of(a.w);
     same_unit = a.z + (range_start(first + NW) - range_start(first)) <= nt;
   }
   auto clear = [&]() {
@@ -313,7 +357,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     cur.b = start[warp].x;
     cur.hu = start[warp].y;
     cur.t = start[warp].z;
-    cur.len = length(cur.b);
+    cur.len = start[warp].w;
     cur.nt = steps_of(cur.len);
 
     // ---- copies: a lane brings 16-byte pieces q4, q4 + 4, .. of rows g and
@@ -517,11 +561,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
               }
             }
           }
-          if (begins && !ends && lane == 0) {
-            // parts: up to the warp that the unit's last step falls to
-            const long long end = lo + i + (cur.nt - 1 - cur.t);
-            p.desc[me] = make_int4(cur.b, cur.hu, static_cast<int>(((end + 1) * warps - 1) / total) - me + 1, 0);
-          }
+          if (begins && !ends && lane == 0) p.desc[me] = describe(cur.b, cur.hu, me, NW - warp, lo + i + (cur.nt - 1 - cur.t));
         }
         if (!last) {
           clear();
@@ -553,8 +593,8 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     }
   }
   __syncthreads();
-  const int3 a = start[0];
-  const int nt = steps_of(length(a.x));
+  const int4 a = start[0];
+  const int nt = steps_of(a.w);
   const int n_steps = static_cast<int>(range_start(first + NW) - range_start(first));
   const bool begins = a.z == 0, ends = a.z + n_steps == nt;
   const int h = a.y / p.chunks, g0 = (a.y - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
@@ -587,89 +627,98 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
       if (c4 == 0) p.part_ml[part * p.rows + r] = make_float2(mm, ll);
     }
   }
-  if (begins && ends) return;
-  // the other warps' parts are in it: empty
-  for (int x = tid; x < (NW - 1) * n_rows; x += THREADS)
-    p.part_ml[2LL * (first + 1 + x / n_rows) * p.rows + x % n_rows] = make_float2(-INFINITY, 0.f);
-  if (begins && tid == 0) {
-    const long long end = range_start(first) + (nt - 1);
-    p.desc[first] = make_int4(a.x, a.y, static_cast<int>(((end + 1) * warps - 1) / total) - first + 1, 0);
-  }
+  if (begins && !ends && tid == 0) p.desc[first] = describe(a.x, a.y, first, 1, range_start(first) + (nt - 1));
 }
 
 // Joins the parts of the units that several warps of the kernel above share:
-// block c takes the units that start in a warp of CTA c and end in a later
-// one.  A warp takes a head of one of them, or its parts together with other
-// warps when there are fewer heads than warps.
+// block (c, y) takes heads kJoinRows y .. of the units that begin in CTA c and
+// end elsewhere.  A warp takes a head of one of them, or its parts together
+// with other warps when there are fewer heads than warps.
+constexpr int kJoinRows = 4, kJoinWarps = 8;
+
 template <int DV, bool F16>
-__global__ void __launch_bounds__(512) attn_decode_join(const __grid_constant__ DecodeParams p) {
-  constexpr int NW = 16, VPL = DV / 32;  // values of a lane
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid_constant__ DecodeParams p) {
+  constexpr int NW = kJoinWarps, VPL = DV / 32;  // values of a lane
   __shared__ float sum[NW][DV];
-  __shared__ int4 units[NW];
+  __shared__ int4 units[kDecodeMaxWarps];
+  __shared__ int from[kDecodeMaxWarps];
   __shared__ int n_units;
-  __shared__ float2 list[NW][32];  // parts that hold something: number, weight
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cw = p.cta_warps;
   if (warp == 0) {
     int4 d = make_int4(-1, 0, 0, 0);
-    if (lane < p.cta_warps) d = p.desc[blockIdx.x * p.cta_warps + lane];
+    if (lane < cw) d = p.desc[blockIdx.x * cw + lane];
     const unsigned have = __ballot_sync(0xffffffffu, d.x >= 0);
-    if (d.x >= 0) units[__popc(have & ((1u << lane) - 1))] = make_int4(d.x, d.y, d.z, blockIdx.x * p.cta_warps + lane);
+    if (d.x >= 0) {
+      const int at = __popc(have & ((1u << lane) - 1));
+      units[at] = d;
+      from[at] = blockIdx.x * cw + lane;
+    }
     if (lane == 0) n_units = __popc(have);
   }
   __syncthreads();
-  const int items = n_units * p.rows;  // (the rows of a short last chunk are skipped)
+  const int r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, p.rows - r0);
+  const int items = n_units * rows;
   if (items == 0) return;
   const int per = items >= NW ? 1 : NW / items;  // warps of an item
   for (int i0 = 0; i0 < items; i0 += NW / per) {
     const int it = i0 + warp / per, s = warp % per;
     bool on = warp < NW / per * per && it < items;
-    const int4 d = units[on ? it / p.rows : 0];
-    const int r = on ? it % p.rows : 0;
+    const int u = on ? it / rows : 0, r = on ? r0 + it % rows : 0;
+    const int4 d = units[u];
     const int h = d.y / p.chunks, g0 = (d.y - h * p.chunks) * p.rows;
-    on = on && g0 + r < p.G;
-    auto part = [&](int i) { return 2LL * (d.w + i) + (i == 0 ? 1 : 0); };
+    on = on && g0 + r < p.G;  // (the last units of a key head may have fewer)
+    // parts: here, one of each CTA between, there
+    const int here = d.z & 255, there = d.z >> 8, parts = here + d.w + there;
+    auto row_of = [&](int i) -> long long {
+      int w = from[u] + i;
+      if (i >= here) w = (blockIdx.x + 1 + min(i - here, d.w)) * cw + max(i - here - d.w, 0);
+      return (2LL * w + (i == 0 ? 1 : 0)) * p.rows + r;
+    };
     float m = -INFINITY, l = 0.f, acc[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) acc[v] = 0.f;
     if (on) {
-      for (int i = lane; i < d.z; i += 32) m = fmaxf(m, p.part_ml[part(i) * p.rows + r].x);
+      float2 x = lane < parts ? p.part_ml[row_of(lane)] : make_float2(-INFINITY, 0.f);
+      m = x.x;
+      for (int i = 32 + lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[row_of(i)].x);
 #pragma unroll
       for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float u = m == -INFINITY ? 0.f : m;
-      int seen = 0;
-      for (int i0p = 0; i0p < d.z; i0p += 32) {
-        const int i = i0p + lane;
-        const float2 x = i < d.z ? p.part_ml[part(i) * p.rows + r] : make_float2(-INFINITY, 0.f);
-        const float w = exp2_fast(x.x - u);
+      const float base = m == -INFINITY ? 0.f : m;
+      for (int i0p = 0; i0p < parts; i0p += 32) {
+        if (i0p > 0) x = i0p + lane < parts ? p.part_ml[row_of(i0p + lane)] : make_float2(-INFINITY, 0.f);
+        const float w = exp2_fast(x.x - base);
         l = fmaf(w, x.y, l);
-        // (a part of NaN scores has no maximum but a sum)
-        const unsigned have = __ballot_sync(0xffffffffu, !(x.y == 0.f));
-        __syncwarp();
-        if (!(x.y == 0.f)) list[warp][__popc(have & ((1u << lane) - 1))] = make_float2(__int_as_float(i), w);
-        __syncwarp();
-        const int n = __popc(have);
-        const int k0 = (s + per - seen % per) % per;
-#pragma unroll 4
-        for (int k = k0; k < n; k += per) {
-          const float2 e = list[warp][k];
-          const float* y = p.part_o + (part(__float_as_int(e.x)) * p.rows + r) * DV + lane * VPL;
+        const int n = min(32, parts - i0p);
+        constexpr int U = VPL <= 4 ? 8 : 4;  // parts in flight
+        for (int k0 = s; k0 < n; k0 += U * per) {
+          float y[U][VPL], f[U];
 #pragma unroll
-          for (int v = 0; v < VPL; v += 2) {
-            const float2 z = *reinterpret_cast<const float2*>(y + v);
-            acc[v] = fmaf(e.y, z.x, acc[v]);
-            acc[v + 1] = fmaf(e.y, z.y, acc[v + 1]);
+          for (int j = 0; j < U; ++j) {
+            const int k = k0 + j * per;
+            f[j] = __shfl_sync(0xffffffffu, w, k & 31);
+            if (k >= n) continue;
+            const float* z = p.part_o + row_of(i0p + k) * DV + lane * VPL;
+#pragma unroll
+            for (int v = 0; v < VPL; v += 2) *reinterpret_cast<float2*>(&y[j][v]) = *reinterpret_cast<const float2*>(z + v);
           }
+#pragma unroll
+          for (int j = 0; j < U; ++j)
+            if (k0 + j * per < n) {
+#pragma unroll
+              for (int v = 0; v < VPL; ++v) acc[v] = fmaf(f[j], y[j][v], acc[v]);
+            }
         }
-        seen += n;
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     }
+    if (per > 1) {
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) sum[warp][lane * VPL + v] = acc[v];
-    __syncthreads();
+      for (int v = 0; v < VPL; ++v) sum[warp][lane * VPL + v] = acc[v];
+      __syncthreads();
+    }
     if (on && s == 0) {
       for (int k = 1; k < per; ++k)
 #pragma unroll
@@ -683,14 +732,14 @@ __global__ void __launch_bounds__(512) attn_decode_join(const __grid_constant__ 
               pack2<F16>(acc[v] * inv, acc[v + 1] * inv);
       if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
     }
-    __syncthreads();
+    if (per > 1) __syncthreads();
   }
 }
 
 template <class K>
-cudaError_t decode_launch_one(K kernel, const DecodeParams& p, int grid, int threads, int smem, cudaStream_t stream) {
+cudaError_t decode_launch_one(K kernel, const DecodeParams& p, dim3 grid, int threads, int smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -713,12 +762,18 @@ cudaError_t launch_decode_nt(DecodeParams& p, int ctas, cudaStream_t stream) {
   if (!attr_done[dev]) {
     e = cudaFuncSetAttribute(attn_decode_kernel<DQ, DV, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
     if (e != cudaSuccess) return e;
+    // the same division of the SM's memory as the kernel before it: changing
+    // it would have to wait for the SM to drain
+    e = cudaFuncSetAttribute(attn_decode_join<DV, F16>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
   p.cta_warps = P::NW;
-  e = decode_launch_one(attn_decode_kernel<DQ, DV, F16, NT>, p, ctas, P::NW * 32, P::SMEM, stream);
+  e = decode_launch_one(attn_decode_kernel<DQ, DV, F16, NT>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
   if (e != cudaSuccess || !p.split) return e;
-  return decode_launch_one(attn_decode_join<DV, F16>, p, ctas, 512, 0, stream);
+  return decode_launch_one(attn_decode_join<DV, F16>, p, dim3(ctas, (p.rows + kJoinRows - 1) / kJoinRows), kJoinWarps * 32, 0,
+                           stream);
 }
 
 template <int DQ, int DV, bool F16>
