@@ -108,6 +108,125 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
   return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
 }
 
+// The list of steps cut into ranges: `total` steps over `warps` warps, one
+// more for the first `extra` of them; and the place of this warp's range.
+struct DecodeRange {
+  long long total, warps, each, extra;
+  long long lo, cta_lo, cta_hi;  // first step of the warp, of its CTA, behind the CTA's last
+  int count;                     // steps of the warp
+  int b, hu, t, len;             // sequence, unit and step of lo, the sequence's length
+  __device__ long long start(long long x) const { return x < warps ? each * x + (x < extra ? x : extra) : total; }
+  // the warp that step x falls to
+  __device__ long long owner(long long x) const {
+    return x < extra * (each + 1) ? divide(x, each + 1) : extra + divide(x - extra * (each + 1), each);
+  }
+};
+struct DecodeWords {
+  int* lens;          // [threads]
+  uint32_t* sums;     // [threads]
+  long long* totals;  // [2][16]
+};
+
+// Thread x holds sequence x (and adds up those behind it, a block's width
+// apart): its length, and the steps up to it within its warp.  I: int where
+// no list of this shape can pass 2^31 steps, else long long.
+template <class I, int NW>
+__device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const DecodeWords& s) {
+  constexpr int THREADS = NW * 32;
+  constexpr unsigned ALL = 0xffffffffu;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const I HU = p.Hkv * p.chunks;
+  auto length = [&](int b, bool& odd) {
+    const int n = __ldg(p.seq_lens + b);
+    odd = odd || n < 0 || n > p.capacity;
+    return n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
+  };
+  auto scan = [&](I x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const I y = __shfl_up_sync(ALL, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  bool odd = false;
+  int n = tid < p.B ? length(tid, odd) : 0;
+  I inc = scan((n + kDecodeBN - 1) / kDecodeBN), rest = 0;
+  if (p.B > THREADS) {
+    for (int b = tid + THREADS; b < p.B; b += THREADS) rest += (length(b, odd) + kDecodeBN - 1) / kDecodeBN;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(ALL, rest, o);
+  }
+  if (odd && blockIdx.x == 0) *p.err = 1;
+  // (a sum within a warp fits 32 bits: 32 sequences of at most 2^26 steps)
+  s.lens[tid] = n;
+  s.sums[tid] = static_cast<uint32_t>(inc);
+  if (lane == 31) s.totals[warp] = inc;
+  if (lane == 0) s.totals[16 + warp] = rest;
+  __syncthreads();
+  I cum = scan(lane < NW ? static_cast<I>(s.totals[lane]) : 0);  // steps up to warp `lane`
+  I steps = __shfl_sync(ALL, cum, NW - 1);
+  if (p.B > THREADS) {
+    I r = lane < NW ? static_cast<I>(s.totals[16 + lane]) : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) r += __shfl_xor_sync(ALL, r, o);
+    steps += r;
+  }
+  const I total = steps * HU, most = static_cast<I>(gridDim.x) * NW;
+  I warps = static_cast<I>(divide(total, p.min_steps)) + 1;
+  warps = warps > most ? most : warps;
+  warps = warps > total ? total : warps;
+  warps = warps < 1 ? 1 : warps;
+  DecodeRange w;
+  w.total = total;
+  w.warps = warps;
+  w.each = divide(total, warps);
+  w.extra = total - w.each * warps;
+  const int first = blockIdx.x * NW;
+  w.lo = w.start(first + warp);
+  w.count = static_cast<int>(w.start(first + warp + 1) - w.lo);
+  w.cta_lo = w.start(first);
+  w.cta_hi = w.start(first + NW);
+  if (w.count == 0) w.lo = w.cta_lo;
+  w.b = w.hu = w.t = w.len = 0;
+  if (w.cta_lo >= total) return w;
+  // the sequence: the first whose steps, with those before it, pass x; the
+  // warps' places may lie in several blocks' widths of sequences
+  const I x = static_cast<I>(divide(w.lo, HU)), last_x = static_cast<I>(divide(w.cta_hi - 1, HU));
+  I base = 0;
+  for (int b0 = 0;;) {
+    const I all = __shfl_sync(ALL, cum, NW - 1);
+    if (base <= x && x < base + all) {
+      I y = x - base;
+      const int chunk = __popc(__ballot_sync(ALL, lane < NW && cum <= y));
+      if (chunk > 0) y -= __shfl_sync(ALL, cum, chunk - 1);
+      const uint32_t v = s.sums[chunk * 32 + lane];
+      const int k = __popc(__ballot_sync(ALL, v <= static_cast<uint32_t>(y)));
+      if (k > 0) y -= __shfl_sync(ALL, v, k - 1);
+      // y: place of x within the sequence's steps; in the list, each step
+      // counts once for every unit
+      w.b = b0 + chunk * 32 + k;
+      w.len = s.lens[chunk * 32 + k];
+      const int nt = (w.len + kDecodeBN - 1) / kDecodeBN;
+      const long long r = static_cast<long long>(y) * HU + (w.lo - static_cast<long long>(x) * HU);
+      w.hu = static_cast<int>(divide(r, nt));
+      w.t = static_cast<int>(r - static_cast<long long>(w.hu) * nt);
+    }
+    base += all;
+    b0 += THREADS;
+    if (b0 >= p.B || last_x < base) break;
+    n = b0 + tid < p.B ? length(b0 + tid, odd) : 0;
+    inc = scan((n + kDecodeBN - 1) / kDecodeBN);
+    __syncthreads();
+    s.lens[tid] = n;
+    s.sums[tid] = static_cast<uint32_t>(inc);
+    if (lane == 31) s.totals[warp] = inc;
+    __syncthreads();
+    cum = scan(lane < NW ? static_cast<I>(s.totals[lane]) : 0);
+  }
+  return w;
+}
+
 // Shared memory and registers of a warp decide how many fit on an SM: three
 // stages of 16 keys where that leaves six warps or more (two thirds of the
 // ring in flight while a stage is read), else two; Q in registers unless it
@@ -120,7 +239,7 @@ struct DecodePlan {
   static constexpr int ACC_REGS = DV / 4 * NT, Q_REGS = DQ / 8 * NT;
   static constexpr bool QREG = ACC_REGS + Q_REGS <= 176;
   static constexpr int Q_BYTES = QREG ? 0 : DQ / 16 * NT * 256;
-  static constexpr int MISC_BYTES = 1024;
+  static constexpr int MISC_BYTES = 4608;  // words of the planning: 8 bytes a thread, 16 a warp
   static constexpr int FIT = 226 * 1024 - MISC_BYTES;
   static constexpr int S = FIT / (3 * STAGE + Q_BYTES) >= 6 ? 3 : 2;
   static constexpr int WARP_BYTES = S * STAGE + Q_BYTES;
@@ -147,8 +266,8 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   const uint32_t ring = smem_u32(mine);
   uint2* qs = reinterpret_cast<uint2*>(mine + S * P::STAGE) + lane;
   char* misc = smem + NW * P::WARP_BYTES;
-  long long* scan = reinterpret_cast<long long*>(misc);      // [2][16]
-  int4* start = reinterpret_cast<int4*>(misc + 2 * 8 * 16);  // [NW]: b, unit, step, length
+  const DecodeWords words{reinterpret_cast<int*>(misc), reinterpret_cast<uint32_t*>(misc) + THREADS,
+                          reinterpret_cast<long long*>(misc + 8 * THREADS)};
   const int HU = p.Hkv * p.chunks;  // units of a sequence
 
   griddep_wait();
@@ -159,63 +278,19 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     return n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
   };
   auto steps_of = [](int len) { return (len + BN - 1) / BN; };
-
-  // ---- the ranges of the warps: `total` steps over `warps` warps, one more
-  // for the first total % warps.  Thread x holds sequence x (and adds up those
-  // THREADS apart behind it).
-  const int n_mine = tid < p.B ? length(tid) : 0;
-  long long inc = steps_of(n_mine), rest = 0;  // steps up to this sequence, of later ones
-  bool odd = tid < p.B && __ldg(p.seq_lens + tid) != n_mine;
-  for (int b = tid + THREADS; b < p.B; b += THREADS) {
-    const int n = length(b);
-    odd = odd || __ldg(p.seq_lens + b) != n;
-    rest += steps_of(n);
-  }
-  if (odd && blockIdx.x == 0) *p.err = 1;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  if (p.B > THREADS) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
-  }
-  if (lane == 31) scan[warp] = inc;
-  if (lane == 0) scan[16 + warp] = rest;
-  __syncthreads();
-  long long before = 0, chunk = 0, total = 0;  // steps of the warps before, of this chunk, of all
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    if (w < warp) before += scan[w];
-    chunk += scan[w];
-    total += scan[16 + w];
-  }
-  total = (total + chunk) * HU;
-  const long long most = static_cast<long long>(gridDim.x) * NW;
-  long long warps = total / p.min_steps + 1;
-  if (warps > most) warps = most;
-  if (warps > total) warps = total;
-  if (warps < 1) warps = 1;
-  const long long each = divide(total, warps), more = total - each * warps;
-  auto range_start = [&](long long x) { return x < warps ? each * x + (x < more ? x : more) : total; };
-  // the warp that step x falls to
-  auto owner = [&](long long x) -> long long {
-    return x < more * (each + 1) ? divide(x, each + 1) : more + divide(x - more * (each + 1), each);
-  };
-  // What joins a unit that begins in warp w and has its last step at `end`:
-  // the parts of w's CTA from w on (`here` of them), one for each CTA that
-  // lies within the unit, and those of the CTA where it ends.
-  auto describe = [&](int b, int hu, int w, int here, long long end) -> int4 {
-    const int z = static_cast<int>(owner(end)), c = w / NW, e = z / NW;
-    if (e == c) return make_int4(b, hu, z - w + 1, 0);
-    const bool joined = range_start((e + 1LL) * NW) == end + 1;  // CTA e lies within the unit too
-    return make_int4(b, hu, here | (joined ? 1 : z - e * NW + 1) << 8, e - c - 1);
-  };
   const int first = blockIdx.x * NW;  // this CTA's first warp
   const int me = first + warp;
-  const long long lo = range_start(me);
-  const int count = static_cast<int>(range_start(me + 1) - lo);
+  const DecodeRange w = p.wide ? decode_plan<long long, NW>(p, words) : decode_plan<int, NW>(p, words);
+
+  // What joins a unit that begins in warp x and has its last step at `end`:
+  // the parts of x's CTA from x on (`here` of them), one for each CTA that
+  // lies within the unit, and those of the CTA where it ends.
+  auto describe = [&](int b, int hu, int x, int here, long long end) -> int4 {
+    const int z = static_cast<int>(w.owner(end)), c = x / NW, e = z / NW;
+    if (e == c) return make_int4(b, hu, z - x + 1, 0);
+    const bool joined = w.start((e + 1LL) * NW) == end + 1;  // CTA e lies within the unit too
+    return make_int4(b, hu, here | (joined ? 1 : z - e * NW + 1) << 8, e - c - 1);
+  };
 
   // ---- sequences without keys: O = 0, LSE = -inf
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -226,48 +301,8 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     for (int i = tid; i < Hq; i += THREADS) p.lse[static_cast<long long>(b) * Hq + i] = -INFINITY;
   }
   if (p.split && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
-  if (range_start(first) >= total) return;
+  if (w.cta_lo >= w.total) return;
 
-  // ---- the sequence, unit and step that each warp's range starts with
-  {
-    long long base = 0;  // steps of the chunks before
-    int n = n_mine;
-    for (int b0 = 0;;) {
-      const int steps = steps_of(n);
-      const long long begin = (base + before + inc - steps) * HU;
-      if (steps > 0) {
-        const long long own = static_cast<long long>(steps) * HU;
-#pragma unroll 1
-        for (int w = 0; w < NW; ++w) {
-          const long long x = range_start(first + w) - begin;
-          if (0 <= x && x < own) {
-            const long long u = divide(x, steps);
-            start[w] = make_int4(b0 + tid, static_cast<int>(u), static_cast<int>(x - u * steps), n);
-          }
-        }
-      }
-      base += chunk;
-      b0 += THREADS;
-      if (b0 >= p.B || range_start(first + NW - 1) < base * HU) break;
-      n = b0 + tid < p.B ? length(b0 + tid) : 0;
-      inc = steps_of(n);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      __syncthreads();
-      if (lane == 31) scan[warp] = inc;
-      __syncthreads();
-      before = chunk = 0;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += scan[w];
-        chunk += scan[w];
-      }
-    }
-    __syncthreads();
-  }
   struct Cursor {
     int b, hu, t, nt, len;
   };
@@ -289,12 +324,16 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   float m[NT][2], l[NT][2];  // heads 2 q4, 2 q4 + 1 of each group
   uint32_t qr[P::QREG ? DQ / 16 : 1][NT][2];
   Cursor cur;
-  bool same_unit = false;  // the whole CTA lies within one unit
-  {
-    const int4 a = start[0];
-    const int nt = steps_of(a.w);
-    same_unit = a.z + (range_start(first + NW) - range_start(first)) <= nt;
-  }
+  cur.b = w.b;
+  cur.hu = w.hu;
+  cur.t = w.t;
+  cur.len = w.len;
+  cur.nt = steps_of(w.len);
+  const int count = w.count;
+  // does the whole CTA lie within one unit?  (a warp without steps has the
+  // place of the CTA's first step)
+  const long long unit_lo = w.lo - w.t;
+  const bool same_unit = unit_lo <= w.cta_lo && w.cta_hi <= unit_lo + cur.nt;
   auto clear = [&]() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -354,12 +393,6 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
 
   clear();
   if (count > 0) {
-    cur.b = start[warp].x;
-    cur.hu = start[warp].y;
-    cur.t = start[warp].z;
-    cur.len = start[warp].w;
-    cur.nt = steps_of(cur.len);
-
     // ---- copies: a lane brings 16-byte pieces q4, q4 + 4, .. of rows g and
     // g + 8 of a step, so that one instruction moves 64 bytes of 8 rows
     int page[2], slot[2], next_h;  // of the step whose copies are next
@@ -561,7 +594,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
               }
             }
           }
-          if (begins && !ends && lane == 0) p.desc[me] = describe(cur.b, cur.hu, me, NW - warp, lo + i + (cur.nt - 1 - cur.t));
+          if (begins && !ends && lane == 0) p.desc[me] = describe(cur.b, cur.hu, me, NW - warp, w.lo + i + (cur.nt - 1 - cur.t));
         }
         if (!last) {
           clear();
@@ -593,32 +626,30 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     }
   }
   __syncthreads();
-  const int4 a = start[0];
-  const int nt = steps_of(a.w);
-  const int n_steps = static_cast<int>(range_start(first + NW) - range_start(first));
-  const bool begins = a.z == 0, ends = a.z + n_steps == nt;
-  const int h = a.y / p.chunks, g0 = (a.y - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
+  const int nt = steps_of(w.len);
+  const bool begins = unit_lo == w.cta_lo, ends = w.cta_hi == unit_lo + nt;
+  const int h = w.hu / p.chunks, g0 = (w.hu - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
   const long long part = 2LL * first + (begins ? 1 : 0);
-  const long long row0 = (static_cast<long long>(a.x) * p.Hkv + h) * p.G + g0;
-  for (int x = tid; x < n_rows * (DV / 4); x += THREADS) {
-    const int r = x / (DV / 4), c4 = x % (DV / 4);
+  const long long row0 = (static_cast<long long>(w.b) * p.Hkv + h) * p.G + g0;
+  for (int y = tid; y < n_rows * (DV / 4); y += THREADS) {
+    const int r = y / (DV / 4), c4 = y % (DV / 4);
     float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w)
-      mm = fmaxf(mm, reinterpret_cast<const float2*>(smem + w * P::WARP_BYTES + ROWS * PITCH * 4)[r].x);
+    for (int x = 0; x < NW; ++x)
+      mm = fmaxf(mm, reinterpret_cast<const float2*>(smem + x * P::WARP_BYTES + ROWS * PITCH * 4)[r].x);
     const float u = mm == -INFINITY ? 0.f : mm;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const char* from = smem + w * P::WARP_BYTES;
+    for (int x = 0; x < NW; ++x) {
+      const char* from = smem + x * P::WARP_BYTES;
       const float2 s = reinterpret_cast<const float2*>(from + ROWS * PITCH * 4)[r];
       const float f = exp2_fast(s.x - u);
-      const float4 y = *reinterpret_cast<const float4*>(from + (r * PITCH + 4 * c4) * 4);
+      const float4 z = *reinterpret_cast<const float4*>(from + (r * PITCH + 4 * c4) * 4);
       ll = fmaf(f, s.y, ll);
-      o.x = fmaf(f, y.x, o.x);
-      o.y = fmaf(f, y.y, o.y);
-      o.z = fmaf(f, y.z, o.z);
-      o.w = fmaf(f, y.w, o.w);
+      o.x = fmaf(f, z.x, o.x);
+      o.y = fmaf(f, z.y, o.y);
+      o.z = fmaf(f, z.z, o.z);
+      o.w = fmaf(f, z.w, o.w);
     }
     if (begins && ends) {
       write_row(row0 + r, 4 * c4, o, mm, ll);
@@ -627,18 +658,21 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
       if (c4 == 0) p.part_ml[part * p.rows + r] = make_float2(mm, ll);
     }
   }
-  if (begins && !ends && tid == 0) p.desc[first] = describe(a.x, a.y, first, 1, range_start(first) + (nt - 1));
+  if (begins && !ends && tid == 0) p.desc[first] = describe(w.b, w.hu, first, 1, unit_lo + nt - 1);
 }
 
 // Joins the parts of the units that several warps of the kernel above share:
-// block (c, y) takes heads kJoinRows y .. of the units that begin in CTA c and
-// end elsewhere.  A warp takes a head of one of them, or its parts together
-// with other warps when there are fewer heads than warps.
-constexpr int kJoinRows = 4, kJoinWarps = 8;
+// block (c, y) takes some heads (the y-th part of them) of the units that
+// begin in CTA c and end in another warp.  A warp takes a head of one unit,
+// or its parts together with other warps when there are fewer heads than
+// warps; U parts' rows are on their way at a time.
+constexpr int kJoinWarps = 16;
 
 template <int DV, bool F16>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid_constant__ DecodeParams p) {
   constexpr int NW = kJoinWarps, VPL = DV / 32;  // values of a lane
+  constexpr int U = VPL > 4 ? 4 : 8;             // parts on their way
+  constexpr unsigned ALL = 0xffffffffu;
   __shared__ float sum[NW][DV];
   __shared__ int4 units[kDecodeMaxWarps];
   __shared__ int from[kDecodeMaxWarps];
@@ -649,7 +683,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
   if (warp == 0) {
     int4 d = make_int4(-1, 0, 0, 0);
     if (lane < cw) d = p.desc[blockIdx.x * cw + lane];
-    const unsigned have = __ballot_sync(0xffffffffu, d.x >= 0);
+    const unsigned have = __ballot_sync(ALL, d.x >= 0);
     if (d.x >= 0) {
       const int at = __popc(have & ((1u << lane) - 1));
       units[at] = d;
@@ -658,9 +692,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
     if (lane == 0) n_units = __popc(have);
   }
   __syncthreads();
-  const int r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, p.rows - r0);
+  const int per_block = (p.rows + gridDim.y - 1) / gridDim.y;
+  const int r0 = blockIdx.y * per_block, rows = min(per_block, p.rows - r0);
   const int items = n_units * rows;
-  if (items == 0) return;
+  if (items <= 0) return;
   const int per = items >= NW ? 1 : NW / items;  // warps of an item
   for (int i0 = 0; i0 < items; i0 += NW / per) {
     const int it = i0 + warp / per, s = warp % per;
@@ -670,49 +705,57 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
     const int h = d.y / p.chunks, g0 = (d.y - h * p.chunks) * p.rows;
     on = on && g0 + r < p.G;  // (the last units of a key head may have fewer)
     // parts: here, one of each CTA between, there
-    const int here = d.z & 255, there = d.z >> 8, parts = here + d.w + there;
-    auto row_of = [&](int i) -> long long {
-      int w = from[u] + i;
-      if (i >= here) w = (blockIdx.x + 1 + min(i - here, d.w)) * cw + max(i - here - d.w, 0);
-      return (2LL * w + (i == 0 ? 1 : 0)) * p.rows + r;
+    const int here = d.z & 255, parts = here + d.w + (d.z >> 8);
+    auto row_of = [&](int i) {
+      const int j = i - here;
+      const int w = j < 0 ? from[u] + i : (blockIdx.x + 1 + min(j, d.w)) * cw + max(j - d.w, 0);
+      return (2 * w + (i == 0 ? 1 : 0)) * p.rows + r;
     };
     float m = -INFINITY, l = 0.f, acc[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) acc[v] = 0.f;
     if (on) {
-      float2 x = lane < parts ? p.part_ml[row_of(lane)] : make_float2(-INFINITY, 0.f);
+      int at = row_of(min(lane, parts - 1));
+      float2 x = p.part_ml[at];
+      if (lane >= parts) x = make_float2(-INFINITY, 0.f);
       m = x.x;
       for (int i = 32 + lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[row_of(i)].x);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float base = m == -INFINITY ? 0.f : m;
-      for (int i0p = 0; i0p < parts; i0p += 32) {
-        if (i0p > 0) x = i0p + lane < parts ? p.part_ml[row_of(i0p + lane)] : make_float2(-INFINITY, 0.f);
-        const float w = exp2_fast(x.x - base);
-        l = fmaf(w, x.y, l);
-        const int n = min(32, parts - i0p);
-        constexpr int U = VPL <= 4 ? 8 : 4;  // parts in flight
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(ALL, m, o));
+      const float top = m == -INFINITY ? 0.f : m;
+      for (int base = 0;;) {
+        const float f = exp2_fast(x.x - top);
+        l = fmaf(f, x.y, l);
+        const int n = min(32, parts - base);
+#pragma unroll 1
         for (int k0 = s; k0 < n; k0 += U * per) {
-          float y[U][VPL], f[U];
+          float y[U][VPL];
+#pragma unroll
+          for (int j = 0; j < U; ++j) {
+            const int k = min(k0 + j * per, n - 1);
+            const float* z = p.part_o + static_cast<long long>(__shfl_sync(ALL, at, k)) * DV + lane * VPL;
+#pragma unroll
+            for (int v = 0; v < VPL; v += 2)
+              *reinterpret_cast<float2*>(&y[j][v]) = *reinterpret_cast<const float2*>(z + v);
+          }
 #pragma unroll
           for (int j = 0; j < U; ++j) {
             const int k = k0 + j * per;
-            f[j] = __shfl_sync(0xffffffffu, w, k & 31);
-            if (k >= n) continue;
-            const float* z = p.part_o + row_of(i0p + k) * DV + lane * VPL;
+            const float g = __shfl_sync(ALL, f, k & 31);
+            if (k < n) {
 #pragma unroll
-            for (int v = 0; v < VPL; v += 2) *reinterpret_cast<float2*>(&y[j][v]) = *reinterpret_cast<const float2*>(z + v);
-          }
-#pragma unroll
-          for (int j = 0; j < U; ++j)
-            if (k0 + j * per < n) {
-#pragma unroll
-              for (int v = 0; v < VPL; ++v) acc[v] = fmaf(f[j], y[j][v], acc[v]);
+              for (int v = 0; v < VPL; ++v) acc[v] = fmaf(g, y[j][v], acc[v]);
             }
+          }
         }
+        base += 32;
+        if (base >= parts) break;
+        at = row_of(min(base + lane, parts - 1));
+        x = p.part_ml[at];
+        if (base + lane >= parts) x = make_float2(-INFINITY, 0.f);
       }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(ALL, l, o);
     }
     if (per > 1) {
 #pragma unroll
@@ -772,8 +815,8 @@ cudaError_t launch_decode_nt(DecodeParams& p, int ctas, cudaStream_t stream) {
   p.cta_warps = P::NW;
   e = decode_launch_one(attn_decode_kernel<DQ, DV, F16, NT>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
   if (e != cudaSuccess || !p.split) return e;
-  return decode_launch_one(attn_decode_join<DV, F16>, p, dim3(ctas, (p.rows + kJoinRows - 1) / kJoinRows), kJoinWarps * 32, 0,
-                           stream);
+  return decode_launch_one(attn_decode_join<DV, F16>, p, dim3(ctas, p.rows < 8 ? (p.rows + 1) / 2 : 4),
+                           kJoinWarps * 32, 0, stream);
 }
 
 template <int DQ, int DV, bool F16>

@@ -326,6 +326,8 @@ attn_status run_decode(const attn_paged_cache* c, int32_t Hq, const void* q, con
   p.part_o = reinterpret_cast<float*>(ws + l.desc + l.ml);
   p.err = d.err;
   p.split = p.capacity > kDecodeBN ? 1 : 0;
+  const double steps = (p.capacity / kDecodeBN + 1.0) * p.B * p.Hkv * p.chunks;
+  p.wide = steps + l.ctas * kDecodeMaxWarps < 2147483648.0 ? 0 : 1;
   const cudaError_t e = f16 ? dispatch_decode<true>(l, p, static_cast<cudaStream_t>(stream))
                             : dispatch_decode<false>(l, p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return ATTN_ERR_CUDA;

@@ -86,6 +86,7 @@ struct DecodeParams {
   float* part_o;               // [warp][2][rows][kernel Dv]
   int* err;
   int split;                   // 0: no sequence can have more than one step
+  int wide;                    // 1: the list of steps might pass 2^31
   int cta_warps;               // warps of a CTA (set by the launch)
 };
 
