@@ -32,6 +32,8 @@
 // the sequence's end are filled with zeros, so that whatever a page holds
 // there never enters a product.
 #pragma once
+#include <climits>
+
 #include "attn_paged_kernels.h"
 #include "ptx.cuh"
 
@@ -103,7 +105,8 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
   return d;
 }
 
-// a / b of whole numbers >= 0, b > 0: in 32 bits where both fit
+// a / b of whole numbers >= 0, b > 0
+__device__ __forceinline__ int divide(int a, int b) { return static_cast<uint32_t>(a) / static_cast<uint32_t>(b); }
 __device__ __forceinline__ long long divide(long long a, long long b) {
   return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
 }
@@ -115,6 +118,7 @@ struct DecodeRange {
   long long lo, cta_lo, cta_hi;  // first step of the warp, of its CTA, behind the CTA's last
   int count;                     // steps of the warp
   int b, hu, t, len;             // sequence, unit and step of lo, the sequence's length
+  bool idle;                     // some sequence may be empty
   __device__ long long start(long long x) const { return x < warps ? each * x + (x < extra ? x : extra) : total; }
   // the warp that step x falls to
   __device__ long long owner(long long x) const {
@@ -163,7 +167,7 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
   s.sums[tid] = static_cast<uint32_t>(inc);
   if (lane == 31) s.totals[warp] = inc;
   if (lane == 0) s.totals[16 + warp] = rest;
-  __syncthreads();
+  const bool idle = __syncthreads_or((tid < p.B && n == 0) || p.B > THREADS);
   I cum = scan(lane < NW ? static_cast<I>(s.totals[lane]) : 0);  // steps up to warp `lane`
   I steps = __shfl_sync(ALL, cum, NW - 1);
   if (p.B > THREADS) {
@@ -173,15 +177,17 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
     steps += r;
   }
   const I total = steps * HU, most = static_cast<I>(gridDim.x) * NW;
-  I warps = static_cast<I>(divide(total, p.min_steps)) + 1;
+  I warps = (total >> kDecodeMinStepsLog) + 1;
   warps = warps > most ? most : warps;
   warps = warps > total ? total : warps;
   warps = warps < 1 ? 1 : warps;
   DecodeRange w;
+  const I each = divide(total, warps);
+  w.idle = idle;
   w.total = total;
   w.warps = warps;
-  w.each = divide(total, warps);
-  w.extra = total - w.each * warps;
+  w.each = each;
+  w.extra = total - each * warps;
   const int first = blockIdx.x * NW;
   w.lo = w.start(first + warp);
   w.count = static_cast<int>(w.start(first + warp + 1) - w.lo);
@@ -192,7 +198,7 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
   if (w.cta_lo >= total) return w;
   // the sequence: the first whose steps, with those before it, pass x; the
   // warps' places may lie in several blocks' widths of sequences
-  const I x = static_cast<I>(divide(w.lo, HU)), last_x = static_cast<I>(divide(w.cta_hi - 1, HU));
+  const I x = divide(static_cast<I>(w.lo), HU);
   I base = 0;
   for (int b0 = 0;;) {
     const I all = __shfl_sync(ALL, cum, NW - 1);
@@ -208,13 +214,14 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
       w.b = b0 + chunk * 32 + k;
       w.len = s.lens[chunk * 32 + k];
       const int nt = (w.len + kDecodeBN - 1) / kDecodeBN;
-      const long long r = static_cast<long long>(y) * HU + (w.lo - static_cast<long long>(x) * HU);
-      w.hu = static_cast<int>(divide(r, nt));
-      w.t = static_cast<int>(r - static_cast<long long>(w.hu) * nt);
+      const I r = y * HU + (static_cast<I>(w.lo) - x * HU);
+      const I hu = divide(r, static_cast<I>(nt));
+      w.hu = static_cast<int>(hu);
+      w.t = static_cast<int>(r - hu * nt);
     }
     base += all;
     b0 += THREADS;
-    if (b0 >= p.B || last_x < base) break;
+    if (b0 >= p.B || w.cta_hi <= static_cast<long long>(base) * HU) break;
     n = b0 + tid < p.B ? length(b0 + tid, odd) : 0;
     inc = scan((n + kDecodeBN - 1) / kDecodeBN);
     __syncthreads();
@@ -293,7 +300,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   };
 
   // ---- sequences without keys: O = 0, LSE = -inf
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+  for (int b = blockIdx.x; w.idle && b < p.B; b += gridDim.x) {
     if (length(b) != 0) continue;
     const int Hq = p.Hkv * p.G;
     for (int i = tid; i < Hq * (p.dv / 8); i += THREADS)
@@ -395,30 +402,36 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   if (count > 0) {
     // ---- copies: a lane brings 16-byte pieces q4, q4 + 4, .. of rows g and
     // g + 8 of a step, so that one instruction moves 64 bytes of 8 rows
-    int page[2], slot[2], next_h;  // of the step whose copies are next
-    auto lookup = [&](const Cursor& a) {
-      next_h = a.hu / p.chunks;
+    struct Place {
+      int page[2], slot[2], h;
+    };
+    auto lookup = [&](const Cursor& a) -> Place {
+      Place x;
+      x.h = p.chunks == 1 ? a.hu : a.hu / p.chunks;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int key = a.t * BN + g + 8 * r;
-        page[r] = -1;
-        slot[r] = 0;
+        x.page[r] = -1;
+        x.slot[r] = 0;
         if (key < a.len) {
           const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-          slot[r] = key - e * p.page_size;
-          page[r] = __ldg(p.page_table + a.b * p.table_stride + e);
+          x.slot[r] = key - e * p.page_size;
+          const int page = __ldg(p.page_table + a.b * p.table_stride + e);
+          x.page[r] = page < 0 ? INT_MIN : page;
         }
       }
+      return x;
     };
-    auto issue = [&](int stage) {
+    // (a row behind the end of the sequence has page -1, a bad one is reported)
+    auto issue = [&](const Place& x, int stage) {
       const uint32_t kd = ring + stage * P::STAGE + g * KPITCH + ((q4 ^ g) << 4);
       const uint32_t vd = ring + stage * P::STAGE + P::K_BYTES + g * VPITCH + ((q4 ^ g) << 4);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const bool live = page[r] >= 0 && page[r] < p.n_pages;
-        // (a row behind the end of the sequence has slot 0 and page -1 too)
-        const uint16_t* k = live ? p.k + page[r] * p.kp[0] + next_h * p.kp[1] + slot[r] * p.kp[2] + 8 * q4 : p.q;
-        const uint16_t* v = live ? p.v + page[r] * p.vp[0] + next_h * p.vp[1] + slot[r] * p.vp[2] + 8 * q4 : p.q;
+        const bool live = x.page[r] >= 0 && x.page[r] < p.n_pages;
+        if (!live && x.page[r] != -1) *p.err = 1;
+        const uint16_t* k = live ? p.k + x.page[r] * p.kp[0] + x.h * p.kp[1] + x.slot[r] * p.kp[2] + 8 * q4 : p.q;
+        const uint16_t* v = live ? p.v + x.page[r] * p.vp[0] + x.h * p.vp[1] + x.slot[r] * p.vp[2] + 8 * q4 : p.q;
 #pragma unroll
         for (int j = 0; j < DQ / 32; ++j) {
           const bool in = live && 32 * j + 8 * q4 < p.dqk;
@@ -431,25 +444,19 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
         }
       }
     };
-    // reported when its copies are issued (by then the number has arrived)
-    auto check_pages = [&](const Cursor& a) {
+    Cursor ahead = cur;  // the step that `next` is of
+    Place next, now[S - 1];
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        if (a.t * BN + g + 8 * r < a.len && (page[r] < 0 || page[r] >= p.n_pages)) *p.err = 1;
-    };
-    Cursor ahead = cur;  // the step that page[], slot[] are of
-    lookup(ahead);
+    for (int j = 0; j < S; ++j) {  // the first steps' page numbers all at once
+      if (j < count) {
+        (j < S - 1 ? now[j < S - 1 ? j : 0] : next) = lookup(ahead);
+        if (j + 1 < count && j + 1 < S) advance(ahead);
+      }
+    }
     load_q(cur);
 #pragma unroll
     for (int j = 0; j < S - 1; ++j) {
-      if (j < count) {
-        check_pages(ahead);
-        issue(j);
-        if (j + 1 < count) {
-          advance(ahead);
-          lookup(ahead);
-        }
-      }
+      if (j < count) issue(now[j], j);
       cp_async_commit();
     }
 
@@ -460,11 +467,10 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
       // refill the stage of the step before this one, which every lane has read
       __syncwarp();
       if (i + S - 1 < count) {
-        check_pages(ahead);
-        issue(stage == 0 ? S - 1 : stage - 1);
+        issue(next, stage == 0 ? S - 1 : stage - 1);
         if (i + S < count) {
           advance(ahead);
-          lookup(ahead);
+          next = lookup(ahead);
         }
       }
       cp_async_commit();
@@ -674,6 +680,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
   constexpr int U = VPL > 4 ? 4 : 8;             // parts on their way
   constexpr unsigned ALL = 0xffffffffu;
   __shared__ float sum[NW][DV];
+  __shared__ float2 stat[NW];
   __shared__ int4 units[kDecodeMaxWarps];
   __shared__ int from[kDecodeMaxWarps];
   __shared__ int n_units;
@@ -714,58 +721,46 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
     float m = -INFINITY, l = 0.f, acc[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) acc[v] = 0.f;
+    // adds a part: its rows' scale (fa for what is held, fb for the part)
+    auto add = [&](float mb, float lb, const float (&y)[VPL]) {
+      const float n = fmaxf(m, mb), u = n == -INFINITY ? 0.f : n;
+      const float fa = exp2_fast(m - u), fb = exp2_fast(mb - u);
+      m = n;
+      l = l * fa + lb * fb;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) acc[v] = acc[v] * fa + y[v] * fb;
+    };
     if (on) {
-      int at = row_of(min(lane, parts - 1));
-      float2 x = p.part_ml[at];
-      if (lane >= parts) x = make_float2(-INFINITY, 0.f);
-      m = x.x;
-      for (int i = 32 + lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[row_of(i)].x);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(ALL, m, o));
-      const float top = m == -INFINITY ? 0.f : m;
-      for (int base = 0;;) {
-        const float f = exp2_fast(x.x - top);
-        l = fmaf(f, x.y, l);
-        const int n = min(32, parts - base);
 #pragma unroll 1
-        for (int k0 = s; k0 < n; k0 += U * per) {
-          float y[U][VPL];
+      for (int k0 = s; k0 < parts; k0 += U * per) {
+        float y[U][VPL];
+        float2 st[U];
 #pragma unroll
-          for (int j = 0; j < U; ++j) {
-            const int k = min(k0 + j * per, n - 1);
-            const float* z = p.part_o + static_cast<long long>(__shfl_sync(ALL, at, k)) * DV + lane * VPL;
+        for (int j = 0; j < U; ++j) {
+          const int at = row_of(min(k0 + j * per, parts - 1));
+          st[j] = p.part_ml[at];
+          const float* z = p.part_o + static_cast<long long>(at) * DV + lane * VPL;
 #pragma unroll
-            for (int v = 0; v < VPL; v += 2)
-              *reinterpret_cast<float2*>(&y[j][v]) = *reinterpret_cast<const float2*>(z + v);
-          }
-#pragma unroll
-          for (int j = 0; j < U; ++j) {
-            const int k = k0 + j * per;
-            const float g = __shfl_sync(ALL, f, k & 31);
-            if (k < n) {
-#pragma unroll
-              for (int v = 0; v < VPL; ++v) acc[v] = fmaf(g, y[j][v], acc[v]);
-            }
-          }
+          for (int v = 0; v < VPL; v += 2) *reinterpret_cast<float2*>(&y[j][v]) = *reinterpret_cast<const float2*>(z + v);
         }
-        base += 32;
-        if (base >= parts) break;
-        at = row_of(min(base + lane, parts - 1));
-        x = p.part_ml[at];
-        if (base + lane >= parts) x = make_float2(-INFINITY, 0.f);
-      }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(ALL, l, o);
+        for (int j = 0; j < U; ++j)
+          if (k0 + j * per < parts) add(st[j].x, st[j].y, y[j]);
+      }
     }
     if (per > 1) {
 #pragma unroll
       for (int v = 0; v < VPL; ++v) sum[warp][lane * VPL + v] = acc[v];
+      if (lane == 0) stat[warp] = make_float2(m, l);
       __syncthreads();
     }
     if (on && s == 0) {
-      for (int k = 1; k < per; ++k)
+      for (int k = 1; k < per; ++k) {
+        float y[VPL];
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) acc[v] += sum[warp + k][lane * VPL + v];
+        for (int v = 0; v < VPL; ++v) y[v] = sum[warp + k][lane * VPL + v];
+        add(stat[warp + k].x, stat[warp + k].y, y);
+      }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const long long row = (static_cast<long long>(d.x) * p.Hkv + h) * p.G + g0 + r;
 #pragma unroll

@@ -313,7 +313,6 @@ attn_status run_decode(const attn_paged_cache* c, int32_t Hq, const void* q, con
   p.G = Hq / c->Hkv;
   p.rows = l.rows;
   p.chunks = l.chunks;
-  p.min_steps = 2;
   p.dqk = c->Dqk;
   p.dv = c->Dv;
   const float scale = std::isnan(sm_scale) ? 1.0f / std::sqrt(static_cast<float>(c->Dqk)) : sm_scale;

@@ -61,6 +61,7 @@ cudaError_t launch_append(const AppendParams& p, bool vec, bool f16, int splits,
 
 // -------------------------------------------------------------------- decode
 constexpr int kDecodeBN = 16;        // keys of a step
+constexpr int kDecodeMinStepsLog = 1;  // a warp takes two steps at least, where there are two
 constexpr int kDecodeMaxWarps = 16;  // warps of a CTA, at most
 // query heads of a work unit, at most: what the accumulators leave room for
 constexpr int decode_max_rows(int dv) { return dv <= 128 ? 32 : 16; }
@@ -76,7 +77,6 @@ struct DecodeParams {
   int capacity;                // keys a table row can hold
   int Hkv, G;                  // key heads, query heads of each
   int rows, chunks;            // query heads of a work unit, units of a key head
-  int min_steps;               // steps a warp takes at least
   int dqk, dv;                 // true head dims (<= the kernel's)
   float scale_log2;
   uint16_t* o;
