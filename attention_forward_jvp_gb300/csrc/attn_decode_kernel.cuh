@@ -32,8 +32,6 @@
 // the sequence's end are filled with zeros, so that whatever a page holds
 // there never enters a product.
 #pragma once
-#include <climits>
-
 #include "attn_paged_kernels.h"
 #include "ptx.cuh"
 
@@ -141,7 +139,7 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const I HU = p.Hkv * p.chunks;
   auto length = [&](int b, bool& odd) {
-    const int n = __ldg(p.seq_lens + b);
+    const int n = p.seq_lens[b];
     odd = odd || n < 0 || n > p.capacity;
     return n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
   };
@@ -281,13 +279,65 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   griddep_launch_dependents();
 
   auto length = [&](int b) {
-    const int n = __ldg(p.seq_lens + b);
+    const int n = p.seq_lens[b];
     return n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
   };
   auto steps_of = [](int len) { return (len + BN - 1) / BN; };
+  struct Cursor {
+    int b, hu, t, nt, len;
+  };
+  // the next step of the list (the caller knows that there is one)
+  auto advance = [&](Cursor& a) {
+    if (++a.t < a.nt) return;
+    a.t = 0;
+    if (++a.hu < HU) return;
+    a.hu = 0;
+    while (a.b + 1 < p.B) {
+      ++a.b;
+      a.len = length(a.b);
+      a.nt = steps_of(a.len);
+      if (a.nt > 0) break;
+    }
+  };
+  const int mi = lane >> 3, l8 = lane & 7, g = lane >> 2, q4 = lane & 3;
+  // where rows g and g + 8 of a step lie: page, token in it (-1: behind the
+  // end of the sequence), key head
+  struct Place {
+    int page[2], slot[2], h;
+  };
+  auto lookup = [&](const Cursor& a) -> Place {
+    Place x;
+    x.h = p.chunks == 1 ? a.hu : a.hu / p.chunks;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int key = a.t * BN + g + 8 * r;
+      x.page[r] = 0;
+      x.slot[r] = -1;
+      if (key < a.len) {
+        const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+        x.slot[r] = key - e * p.page_size;
+        x.page[r] = p.page_table[a.b * p.table_stride + e];
+      }
+    }
+    return x;
+  };
+
+  // ---- this warp's range, and the places of its first steps, looked up all
+  // at once
   const int first = blockIdx.x * NW;  // this CTA's first warp
   const int me = first + warp;
   const DecodeRange w = p.wide ? decode_plan<long long, NW>(p, words) : decode_plan<int, NW>(p, words);
+  const int count = w.count;
+  Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len};  // the step computed next
+  Cursor ahead = cur;                                  // the step that `next` is of
+  Place next, now[S - 1];
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    if (j < count) {
+      (j < S - 1 ? now[j < S - 1 ? j : 0] : next) = lookup(ahead);
+      if (j + 1 < count && j + 1 < S) advance(ahead);
+    }
+  }
 
   // What joins a unit that begins in warp x and has its last step at `end`:
   // the parts of x's CTA from x on (`here` of them), one for each CTA that
@@ -310,33 +360,9 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   if (p.split && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
   if (w.cta_lo >= w.total) return;
 
-  struct Cursor {
-    int b, hu, t, nt, len;
-  };
-  // the next step of the list; the caller knows that there is one
-  auto advance = [&](Cursor& a) {
-    if (++a.t < a.nt) return;
-    a.t = 0;
-    if (++a.hu < HU) return;
-    a.hu = 0;
-    do {
-      ++a.b;
-      a.len = length(a.b);
-      a.nt = steps_of(a.len);
-    } while (a.nt == 0 && a.b + 1 < p.B);
-  };
-
-  const int mi = lane >> 3, l8 = lane & 7, g = lane >> 2, q4 = lane & 3;
   float acc[NT][DV / 16][4];
   float m[NT][2], l[NT][2];  // heads 2 q4, 2 q4 + 1 of each group
   uint32_t qr[P::QREG ? DQ / 16 : 1][NT][2];
-  Cursor cur;
-  cur.b = w.b;
-  cur.hu = w.hu;
-  cur.t = w.t;
-  cur.len = w.len;
-  cur.nt = steps_of(w.len);
-  const int count = w.count;
   // does the whole CTA lie within one unit?  (a warp without steps has the
   // place of the CTA's first step)
   const long long unit_lo = w.lo - w.t;
@@ -402,34 +428,14 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   if (count > 0) {
     // ---- copies: a lane brings 16-byte pieces q4, q4 + 4, .. of rows g and
     // g + 8 of a step, so that one instruction moves 64 bytes of 8 rows
-    struct Place {
-      int page[2], slot[2], h;
-    };
-    auto lookup = [&](const Cursor& a) -> Place {
-      Place x;
-      x.h = p.chunks == 1 ? a.hu : a.hu / p.chunks;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int key = a.t * BN + g + 8 * r;
-        x.page[r] = -1;
-        x.slot[r] = 0;
-        if (key < a.len) {
-          const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-          x.slot[r] = key - e * p.page_size;
-          const int page = __ldg(p.page_table + a.b * p.table_stride + e);
-          x.page[r] = page < 0 ? INT_MIN : page;
-        }
-      }
-      return x;
-    };
-    // (a row behind the end of the sequence has page -1, a bad one is reported)
+    // (a row behind the end of the sequence has slot -1)
     auto issue = [&](const Place& x, int stage) {
       const uint32_t kd = ring + stage * P::STAGE + g * KPITCH + ((q4 ^ g) << 4);
       const uint32_t vd = ring + stage * P::STAGE + P::K_BYTES + g * VPITCH + ((q4 ^ g) << 4);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const bool live = x.page[r] >= 0 && x.page[r] < p.n_pages;
-        if (!live && x.page[r] != -1) *p.err = 1;
+        const bool live = x.slot[r] >= 0 && x.page[r] >= 0 && x.page[r] < p.n_pages;
+        if (!live && x.slot[r] >= 0) *p.err = 1;
         const uint16_t* k = live ? p.k + x.page[r] * p.kp[0] + x.h * p.kp[1] + x.slot[r] * p.kp[2] + 8 * q4 : p.q;
         const uint16_t* v = live ? p.v + x.page[r] * p.vp[0] + x.h * p.vp[1] + x.slot[r] * p.vp[2] + 8 * q4 : p.q;
 #pragma unroll
@@ -444,15 +450,6 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
         }
       }
     };
-    Cursor ahead = cur;  // the step that `next` is of
-    Place next, now[S - 1];
-#pragma unroll
-    for (int j = 0; j < S; ++j) {  // the first steps' page numbers all at once
-      if (j < count) {
-        (j < S - 1 ? now[j < S - 1 ? j : 0] : next) = lookup(ahead);
-        if (j + 1 < count && j + 1 < S) advance(ahead);
-      }
-    }
     load_q(cur);
 #pragma unroll
     for (int j = 0; j < S - 1; ++j) {
@@ -672,7 +669,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
 // begin in CTA c and end in another warp.  A warp takes a head of one unit,
 // or its parts together with other warps when there are fewer heads than
 // warps; U parts' rows are on their way at a time.
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 8;
 
 template <int DV, bool F16>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid_constant__ DecodeParams p) {
@@ -684,9 +681,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
   __shared__ int4 units[kDecodeMaxWarps];
   __shared__ int from[kDecodeMaxWarps];
   __shared__ int n_units;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cw = p.cta_warps;
+  const int r0 = blockIdx.y * p.join_rows, rows = min(p.join_rows, p.rows - r0);
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cw = p.cta_warps;
   if (warp == 0) {
     int4 d = make_int4(-1, 0, 0, 0);
     if (lane < cw) d = p.desc[blockIdx.x * cw + lane];
@@ -699,17 +697,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
     if (lane == 0) n_units = __popc(have);
   }
   __syncthreads();
-  const int per_block = (p.rows + gridDim.y - 1) / gridDim.y;
-  const int r0 = blockIdx.y * per_block, rows = min(per_block, p.rows - r0);
   const int items = n_units * rows;
-  if (items <= 0) return;
-  const int per = items >= NW ? 1 : NW / items;  // warps of an item
-  for (int i0 = 0; i0 < items; i0 += NW / per) {
-    const int it = i0 + warp / per, s = warp % per;
-    bool on = warp < NW / per * per && it < items;
-    const int u = on ? it / rows : 0, r = on ? r0 + it % rows : 0;
+  int sh = 0;  // log2 of the warps of an item
+  while (items << (sh + 1) <= NW && sh < 3) ++sh;
+  for (int i0 = 0; i0 < items; i0 += NW >> sh) {
+    const int it = i0 + (warp >> sh), s = warp & ((1 << sh) - 1);
+    bool on = it < items;
+    const int u = on ? it / rows : 0, r = on ? r0 + it - u * rows : 0;
     const int4 d = units[u];
-    const int h = d.y / p.chunks, g0 = (d.y - h * p.chunks) * p.rows;
+    const int h = p.chunks == 1 ? d.y : d.y / p.chunks, g0 = (d.y - h * p.chunks) * p.rows;
     on = on && g0 + r < p.G;  // (the last units of a key head may have fewer)
     // parts: here, one of each CTA between, there
     const int here = d.z & 255, parts = here + d.w + (d.z >> 8);
@@ -721,10 +717,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
     float m = -INFINITY, l = 0.f, acc[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) acc[v] = 0.f;
-    // adds a part: its rows' scale (fa for what is held, fb for the part)
+    // adds a part: fa scales what is held, fb the part
     auto add = [&](float mb, float lb, const float (&y)[VPL]) {
-      const float n = fmaxf(m, mb), u = n == -INFINITY ? 0.f : n;
-      const float fa = exp2_fast(m - u), fb = exp2_fast(mb - u);
+      const float n = fmaxf(m, mb), top = n == -INFINITY ? 0.f : n;
+      const float fa = exp2_fast(m - top), fb = exp2_fast(mb - top);
       m = n;
       l = l * fa + lb * fb;
 #pragma unroll
@@ -732,30 +728,34 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
     };
     if (on) {
 #pragma unroll 1
-      for (int k0 = s; k0 < parts; k0 += U * per) {
+      for (int k0 = s; k0 < parts; k0 += U << sh) {
         float y[U][VPL];
         float2 st[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-          const int at = row_of(min(k0 + j * per, parts - 1));
+          const int at = row_of(min(k0 + (j << sh), parts - 1));
           st[j] = p.part_ml[at];
           const float* z = p.part_o + static_cast<long long>(at) * DV + lane * VPL;
 #pragma unroll
-          for (int v = 0; v < VPL; v += 2) *reinterpret_cast<float2*>(&y[j][v]) = *reinterpret_cast<const float2*>(z + v);
+          for (int v = 0; v < VPL; v += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(z + v);
+            y[j][v] = x.x;
+            y[j][v + 1] = x.y;
+          }
         }
 #pragma unroll
         for (int j = 0; j < U; ++j)
-          if (k0 + j * per < parts) add(st[j].x, st[j].y, y[j]);
+          if (k0 + (j << sh) < parts) add(st[j].x, st[j].y, y[j]);
       }
     }
-    if (per > 1) {
+    if (sh > 0) {
 #pragma unroll
       for (int v = 0; v < VPL; ++v) sum[warp][lane * VPL + v] = acc[v];
       if (lane == 0) stat[warp] = make_float2(m, l);
       __syncthreads();
     }
     if (on && s == 0) {
-      for (int k = 1; k < per; ++k) {
+      for (int k = 1; k < 1 << sh; ++k) {
         float y[VPL];
 #pragma unroll
         for (int v = 0; v < VPL; ++v) y[v] = sum[warp + k][lane * VPL + v];
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
               pack2<F16>(acc[v] * inv, acc[v + 1] * inv);
       if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
     }
-    if (per > 1) __syncthreads();
+    if (sh > 0) __syncthreads();
   }
 }
 
@@ -808,9 +808,10 @@ cudaError_t launch_decode_nt(DecodeParams& p, int ctas, cudaStream_t stream) {
     attr_done[dev] = true;
   }
   p.cta_warps = P::NW;
+  p.join_rows = (p.rows + 7) / 8;  // eight blocks at most share the heads of a CTA's units
   e = decode_launch_one(attn_decode_kernel<DQ, DV, F16, NT>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
   if (e != cudaSuccess || !p.split) return e;
-  return decode_launch_one(attn_decode_join<DV, F16>, p, dim3(ctas, p.rows < 8 ? (p.rows + 1) / 2 : 4),
+  return decode_launch_one(attn_decode_join<DV, F16>, p, dim3(ctas, (p.rows + p.join_rows - 1) / p.join_rows),
                            kJoinWarps * 32, 0, stream);
 }
 

@@ -87,7 +87,7 @@ struct DecodeParams {
   int* err;
   int split;                   // 0: no sequence can have more than one step
   int wide;                    // 1: the list of steps might pass 2^31
-  int cta_warps;               // warps of a CTA (set by the launch)
+  int cta_warps, join_rows;    // warps of a CTA, heads of a joining block (set by the launch)
 };
 
 // The decode kernel for kernel head dims DQ, DV and nt (1, 2 or 4) groups of

@@ -49,7 +49,7 @@ __device__ __forceinline__ uint16_t narrow(float f) {
 // cos and sin (times the output scale) of pair `pair` at position pos
 __device__ __forceinline__ float2 turn(const RopeSpec& r, int pair, int pos) {
   const unsigned long long ph =
-      __ldg(r.steps + pair) * static_cast<unsigned long long>(static_cast<long long>(pos));
+      r.steps[pair] * static_cast<unsigned long long>(static_cast<long long>(pos));
   float s, c;
   sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
   if (r.inverse) s = -s;
@@ -137,7 +137,7 @@ __device__ __forceinline__ int sequence_of(const int* offsets, int n_seq, long l
   int lo = 0, hi = n_seq;  // offsets[lo] <= t < offsets[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(offsets + mid) <= t) lo = mid;
+    if (offsets[mid] <= t) lo = mid;
     else hi = mid;
   }
   return lo;
@@ -165,10 +165,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const long long n = row - b * p.N;
   int pos = static_cast<int>(n);
   if (p.offsets != nullptr) {
-    if (n >= __ldg(p.offsets + p.n_seq)) return;
-    pos -= __ldg(p.offsets + sequence_of(p.offsets, p.n_seq, n));
+    if (n >= p.offsets[p.n_seq]) return;
+    pos -= p.offsets[sequence_of(p.offsets, p.n_seq, n)];
   }
-  if (p.positions != nullptr) pos = __ldg(p.positions + b * p.ps[0] + n * p.ps[1]);
+  if (p.positions != nullptr) pos = p.positions[b * p.ps[0] + n * p.ps[1]];
 
   for (int item = threadIdx.x - row_in_block * per_row; item < items; item += per_row) {
     float2 cs[8];
@@ -229,11 +229,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   long long b = t, pos = 0;
   bool idle = false;
   if (p.offsets != nullptr) {
-    if (t >= __ldg(p.offsets + p.B)) return;
+    if (t >= p.offsets[p.B]) return;
     b = sequence_of(p.offsets, p.B, t);
-    pos = __ldg(p.seq_lens + b) - static_cast<long long>(__ldg(p.offsets + b + 1)) + t;
+    pos = p.seq_lens[b] - static_cast<long long>(p.offsets[b + 1]) + t;
   } else {
-    pos = static_cast<long long>(__ldg(p.seq_lens + b)) - 1;
+    pos = static_cast<long long>(p.seq_lens[b]) - 1;
     idle = pos == -1;
   }
   // its place in the pool
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   if (pos >= 0 && pos < static_cast<long long>(p.max_pages) * p.page_size) {
     const int e = static_cast<int>(pos / p.page_size);
     slot = pos - static_cast<long long>(e) * p.page_size;
-    page = __ldg(p.page_table + b * p.table_stride + e);
+    page = p.page_table[b * p.table_stride + e];
   }
   const bool placed = page >= 0 && page < p.n_pages;
   if (!placed && !idle && item == 0 && blockIdx.y == 0) *p.err = 1;
