@@ -84,16 +84,18 @@ attn_status spec_of(const attn_rope_spec* r, int D, bool inverse, RopeSpec* out)
   return ATTN_OK;
 }
 
-// Into how many blockIdx.y the heads are split: threads enough for the card
-// (`want`) while there are heads to give them; beyond that a thread walks
-// over several heads with the angles it has computed.
+// Into how many blockIdx.y the heads are split: four rounds of threads over
+// the card while there are heads to give them, so that the last round is a
+// small share (one round: 48 us where four take 45; eight: the angles, taken
+// once for a thread's heads, tell); whole batches of heads for each.
 int head_splits(long long row_threads, int heads, int sms, int* per_split) {
-  const long long want = static_cast<long long>(sms) * 1024;
-  long long splits = row_threads > 0 ? (want + row_threads - 1) / row_threads : 1;
+  const long long want = static_cast<long long>(sms) * 4096;
+  long long splits = (want + row_threads - 1) / row_threads;
   if (splits > heads) splits = heads;
-  if (splits < 1) splits = 1;
-  *per_split = static_cast<int>((heads + splits - 1) / splits);
-  return (heads + *per_split - 1) / *per_split;
+  int per = static_cast<int>((heads + splits - 1) / splits);
+  if (per > 1) per = (per + kRopeUnroll - 1) / kRopeUnroll * kRopeUnroll;
+  *per_split = per;
+  return (heads + per - 1) / per;
 }
 
 attn_status run_rope(int32_t B, int64_t N, int32_t D, const attn_rope_spec* rope, const attn_rope_tensor* tensors,

@@ -24,6 +24,7 @@ struct RopeTensor {
 };
 
 constexpr int kRopeTensors = 4;
+constexpr int kRopeUnroll = 2;  // heads of a thread in flight
 
 struct RopeParams {
   RopeTensor t[kRopeTensors];

@@ -5,16 +5,20 @@
 // hold w_i as a 64-bit fraction of a full turn, so that p * step modulo 2^64
 // is the angle modulo a full turn exactly, at any position, in three integer
 // multiplications; its upper 32 bits, taken as a signed fraction of half a
-// turn, go to sincospif.  (p * w_i in fp32 is off by 2^-24 p: 0.008 rad at
-// position 131072.)  The one rounding is that of the fraction to fp32,
-// 2^-25 of half a turn at most.
+// turn and multiplied by pi, go to __sincosf.  (p * w_i in fp32 is off by
+// 2^-24 p: 0.008 rad at position 131072.)  The fraction and the product are
+// rounded to fp32, 3 10^-7 together, and __sincosf is within 2^-21.1 on
+// [-pi, pi]: 8 10^-7, against the 2^-12 relative of the finer of the two
+// storage types.  (sincospif, exact to 10^-7 but five times the
+// instructions, cost 1 to 4 % at the sizes below.)
 //
 // Both are bound by memory: an element is read once and written once.  A
 // thread owns one 16-element piece of one token (for half-split pairs the
-// two 8-element pieces that turn together), computes its eight angles once
-// and walks over the heads with them in registers, four heads of 16-byte
-// loads in flight; a table of cos and sin, the alternative, is a second
-// stream to read and has to end at some position.
+// two 8-element pieces that turn together), computes its eight angles once,
+// behind the first loads, and walks over the heads with them in registers,
+// two heads of 16-byte loads in flight and four blocks on an SM (four heads
+// and two blocks were slower: 47 us for 45); a table of cos and sin, the
+// alternative, is a second stream to read and has to end at some position.
 #include "attn_paged_kernels.h"
 #include "ptx.cuh"
 
@@ -22,7 +26,7 @@ namespace attn {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kBlocks = 4;
 
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -51,7 +55,7 @@ __device__ __forceinline__ float2 turn(const RopeSpec& r, int pair, int pos) {
   const unsigned long long ph =
       r.steps[pair] * static_cast<unsigned long long>(static_cast<long long>(pos));
   float s, c;
-  sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+  __sincosf(static_cast<float>(static_cast<int>(ph >> 32)) * 1.462918079267160e-9f, &s, &c);  // pi 2^-31
   if (r.inverse) s = -s;
   return make_float2(c * r.scale, s * r.scale);
 }
@@ -91,28 +95,46 @@ __device__ __forceinline__ void rotate_piece(Piece& v, const float2 (&cs)[8]) {
   }
 }
 
+// The angles of a thread's piece, computed when first needed: behind loads
+struct Angles {
+  float2 cs[8];
+  bool have = false;
+  __device__ __forceinline__ void need(const RopeSpec& r, int first, int pos) {
+    if (have) return;
+    have = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = turn(r, first + i, pos);
+  }
+};
+
 // n heads of one piece: rotated, or copied
 template <bool F16, bool INTER>
 __device__ __forceinline__ void walk_heads(const uint16_t* x, long long xh, uint16_t* y, long long yh, int n, int d1,
-                                           bool turned, const float2 (&cs)[8]) {
-  constexpr int U = 4;
+                                           bool turned, Angles& a, const RopeSpec& r, int first, int pos) {
+  constexpr int U = kRopeUnroll;
   int h = 0;
+#pragma unroll 1
   for (; h + U <= n; h += U) {
     Piece v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = load_piece(x + u * xh, d1);
     if (turned) {
+      a.need(r, first, pos);
 #pragma unroll
-      for (int u = 0; u < U; ++u) rotate_piece<F16, INTER>(v[u], cs);
+      for (int u = 0; u < U; ++u) rotate_piece<F16, INTER>(v[u], a.cs);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) store_piece(y + u * yh, d1, v[u]);
     x += U * xh;
     y += U * yh;
   }
+#pragma unroll 1
   for (; h < n; ++h, x += xh, y += yh) {
     Piece v = load_piece(x, d1);
-    if (turned) rotate_piece<F16, INTER>(v, cs);
+    if (turned) {
+      a.need(r, first, pos);
+      rotate_piece<F16, INTER>(v, a.cs);
+    }
     store_piece(y, d1, v);
   }
 }
@@ -132,15 +154,22 @@ __device__ __forceinline__ void walk_heads_scalar(const uint16_t* x, long long x
   }
 }
 
-// The sequence of packed token t: the last b with offsets[b] <= t
+// The sequence of packed token t, the last b < n_seq with offsets[b] <= t,
+// for a whole warp whose first lane has its first token: 32 offsets at a
+// time for that token, then step by step.  All lanes take part.
 __device__ __forceinline__ int sequence_of(const int* offsets, int n_seq, long long t) {
-  int lo = 0, hi = n_seq;  // offsets[lo] <= t < offsets[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (offsets[mid] <= t) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 31;
+  const long long t0 = __shfl_sync(0xffffffffu, t, 0);
+  int b = 0, n = n_seq;  // the one sought is in [b, b + n)
+  while (n > 1) {
+    const int k = (n + 31) / 32;
+    const bool below = lane * k < n && offsets[b + lane * k] <= t0;
+    const int c = max(__popc(__ballot_sync(0xffffffffu, below)) - 1, 0);
+    b += c * k;
+    n = min(k, n - c * k);
   }
-  return lo;
+  while (b + 1 < n_seq && offsets[b + 1] <= t) ++b;
+  return b;
 }
 
 // pieces (VEC) or pairs and single elements (scalar) of a row of d elements
@@ -150,7 +179,7 @@ __device__ __forceinline__ int items_of(int d, int rot) {
 }
 
 template <bool F16, bool INTER, bool VEC>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int items = items_of<VEC>(p.D, p.r.rot);
@@ -158,20 +187,22 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   // than it has threads
   const int per_row = items < kThreads ? items : kThreads;
   const int row_in_block = threadIdx.x / per_row;
-  if (row_in_block >= kThreads / per_row) return;
-  const long long row = static_cast<long long>(blockIdx.x) * (kThreads / per_row) + row_in_block;
-  if (row >= p.rows) return;
+  long long row = static_cast<long long>(blockIdx.x) * (kThreads / per_row) + row_in_block;
+  const bool idle = row_in_block >= kThreads / per_row || row >= p.rows;
+  if (idle) row = p.rows - 1;  // (takes part in the search)
   const long long b = p.N == p.rows ? 0 : row / p.N;
   const long long n = row - b * p.N;
   int pos = static_cast<int>(n);
   if (p.offsets != nullptr) {
+    const int seq = sequence_of(p.offsets, p.n_seq, n);
     if (n >= p.offsets[p.n_seq]) return;
-    pos -= p.offsets[sequence_of(p.offsets, p.n_seq, n)];
+    pos -= p.offsets[seq];
   }
+  if (idle) return;
   if (p.positions != nullptr) pos = p.positions[b * p.ps[0] + n * p.ps[1]];
 
   for (int item = threadIdx.x - row_in_block * per_row; item < items; item += per_row) {
-    float2 cs[8];
+    Angles angles;
     bool turned;
     int d0, d1;
     if constexpr (VEC) {
@@ -183,14 +214,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
           d0 = 8 * item;
           d1 = p.r.rot / 2;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = turn(p.r, 8 * item + i, pos);
       }
     } else {
       turned = item < p.r.rot / 2;
       d0 = turned ? (INTER ? 2 * item : item) : item + p.r.rot / 2;
       d1 = INTER ? d0 + 1 : d0 + p.r.rot / 2;
-      if (turned) cs[0] = turn(p.r, item, pos);
+      if (turned) angles.cs[0] = turn(p.r, item, pos);
     }
     const int first = blockIdx.y * p.heads_per_split;
     const int last = min(first + p.heads_per_split, p.heads);
@@ -205,37 +234,38 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       uint16_t* y = a.y + b * a.ys[0] + lo * a.ys[1] + n * a.ys[2];
       if (!turned && x == y) continue;  // in place: nothing to copy
       if constexpr (VEC)
-        walk_heads<F16, INTER>(x + d0, a.xs[1], y + d0, a.ys[1], hi - lo, d1, turned, cs);
+        walk_heads<F16, INTER>(x + d0, a.xs[1], y + d0, a.ys[1], hi - lo, d1, turned, angles, p.r, 8 * item, pos);
       else
-        walk_heads_scalar<F16>(x, a.xs[1], y, a.ys[1], hi - lo, d0, d1, turned, cs[0]);
+        walk_heads_scalar<F16>(x, a.xs[1], y, a.ys[1], hi - lo, d0, d1, turned, angles.cs[0]);
     }
   }
 }
 
 template <bool F16, bool INTER, bool VEC>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const __grid_constant__ AppendParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int items_qk = items_of<VEC>(p.Dqk, p.r.rot), items_v = items_of<VEC>(p.Dv, 0);
   const int items = max(items_qk, items_v);
   const int per_row = items < kThreads ? items : kThreads;
   const int row_in_block = threadIdx.x / per_row;
-  if (row_in_block >= kThreads / per_row) return;
-  const long long t = static_cast<long long>(blockIdx.x) * (kThreads / per_row) + row_in_block;
-  if (t >= p.T) return;
+  long long t = static_cast<long long>(blockIdx.x) * (kThreads / per_row) + row_in_block;
+  const bool none = row_in_block >= kThreads / per_row || t >= p.T;
+  if (none) t = p.T - 1;  // (takes part in the search)
   const int item = threadIdx.x - row_in_block * per_row;  // items <= 256: every one has its thread
 
   // the token's sequence and position
   long long b = t, pos = 0;
   bool idle = false;
   if (p.offsets != nullptr) {
-    if (t >= p.offsets[p.B]) return;
     b = sequence_of(p.offsets, p.B, t);
+    if (t >= p.offsets[p.B]) return;
     pos = p.seq_lens[b] - static_cast<long long>(p.offsets[b + 1]) + t;
   } else {
     pos = static_cast<long long>(p.seq_lens[b]) - 1;
     idle = pos == -1;
   }
+  if (none) return;
   // its place in the pool
   long long page = -1, slot = 0;
   if (pos >= 0 && pos < static_cast<long long>(p.max_pages) * p.page_size) {
@@ -246,20 +276,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const bool placed = page >= 0 && page < p.n_pages;
   if (!placed && !idle && item == 0 && blockIdx.y == 0) *p.err = 1;
 
-  float2 cs[8];
+  Angles angles;
   const bool turned = item < (VEC ? p.r.rot / 16 : p.r.rot / 2);
   int d0, d1;
   if constexpr (VEC) {
     d0 = turned && !INTER ? 8 * item : 16 * item;
     d1 = turned && !INTER ? p.r.rot / 2 : 8;
-    if (turned && pos >= 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) cs[i] = turn(p.r, 8 * item + i, static_cast<int>(pos));
-    }
   } else {
     d0 = turned ? (INTER ? 2 * item : item) : item + p.r.rot / 2;
     d1 = INTER ? d0 + 1 : d0 + p.r.rot / 2;
-    if (turned && pos >= 0) cs[0] = turn(p.r, item, static_cast<int>(pos));
+    if (turned && pos >= 0) angles.cs[0] = turn(p.r, item, static_cast<int>(pos));
   }
 
   // heads of q, of k and of v, one after the other
@@ -281,9 +307,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         }
       } else if (turned || x != y) {
         if constexpr (VEC)
-          walk_heads<F16, INTER>(x + d0, p.qs[1], y + d0, p.qos[1], hi - lo, d1, turned, cs);
+          walk_heads<F16, INTER>(x + d0, p.qs[1], y + d0, p.qos[1], hi - lo, d1, turned, angles, p.r, 8 * item, static_cast<int>(pos));
         else
-          walk_heads_scalar<F16>(x, p.qs[1], y, p.qos[1], hi - lo, d0, d1, turned, cs[0]);
+          walk_heads_scalar<F16>(x, p.qs[1], y, p.qos[1], hi - lo, d0, d1, turned, angles.cs[0]);
       }
     }
   }
@@ -294,9 +320,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       const uint16_t* x = p.k + t * p.ks[0] + lo * p.ks[1];
       uint16_t* y = p.k_pool + page * p.kp[0] + lo * p.kp[1] + slot * p.kp[2];
       if constexpr (VEC)
-        walk_heads<F16, INTER>(x + d0, p.ks[1], y + d0, p.kp[1], hi - lo, d1, turned, cs);
+        walk_heads<F16, INTER>(x + d0, p.ks[1], y + d0, p.kp[1], hi - lo, d1, turned, angles, p.r, 8 * item, static_cast<int>(pos));
       else
-        walk_heads_scalar<F16>(x, p.ks[1], y, p.kp[1], hi - lo, d0, d1, turned, cs[0]);
+        walk_heads_scalar<F16>(x, p.ks[1], y, p.kp[1], hi - lo, d0, d1, turned, angles.cs[0]);
     }
   }
   {
@@ -305,9 +331,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       const uint16_t* x = p.v + t * p.vs[0] + lo * p.vs[1];
       uint16_t* y = p.v_pool + page * p.vp[0] + lo * p.vp[1] + slot * p.vp[2];
       if constexpr (VEC)
-        walk_heads<F16, INTER>(x + 16 * item, p.vs[1], y + 16 * item, p.vp[1], hi - lo, 8, false, cs);
+        walk_heads<F16, INTER>(x + 16 * item, p.vs[1], y + 16 * item, p.vp[1], hi - lo, 8, false, angles, p.r, 0, 0);
       else
-        walk_heads_scalar<F16>(x, p.vs[1], y, p.vp[1], hi - lo, item, item, false, cs[0]);
+        walk_heads_scalar<F16>(x, p.vs[1], y, p.vp[1], hi - lo, item, item, false, angles.cs[0]);
     }
   }
 }
