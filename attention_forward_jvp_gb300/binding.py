@@ -74,6 +74,12 @@ class AttnRopeTensor(ctypes.Structure):
                 ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
 
 
+# an array of AttnRopeTensor as 64-bit words, one constructor call instead of
+# nine assignments a tensor (H's upper half is padding; the hosts are little-endian)
+_ROPE_WORDS = [ctypes.c_int64 * (9 * n) for n in range(5)]
+assert ctypes.sizeof(AttnRopeTensor) == 72
+
+
 class AttnRopeFreq(ctypes.Structure):
     _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
                 ("factor", ctypes.c_double), ("orig_len", ctypes.c_double), ("low_turns", ctypes.c_double),
@@ -570,12 +576,12 @@ def _need_cuda(t: torch.Tensor, name: str, dtype, dev=None):
 
 def _call_on(dev, fn, *args):
     """fn(*args, stream) with `dev` current; its status raised."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, stream)
+    i = dev.index
+    if torch.cuda.current_device() == i:
+        st = fn(*args, torch.cuda.current_stream().cuda_stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream)
+            st = fn(*args, torch.cuda.current_stream().cuda_stream)
     if st != 0:
         _check(st)
 
@@ -665,29 +671,36 @@ def attn_rope(tensors, rope: Rope, positions: Optional[torch.Tensor] = None, off
         raise ValueError(f"rot_dim {rope.rot_dim} exceeds the head dim {D}")
     if rope.steps.device != dev:
         raise ValueError(f"the rotation is on {rope.steps.device}, the tensors on {dev}")
-    if out is None:
-        out = tuple(torch.empty(t.shape, dtype=dt, device=dev) for t in tensors)
-    else:
+    given = out is not None
+    if given:
         out = tuple(out)
         if len(out) != n:
             raise ValueError("out must hold one tensor for each input")
-    arr = (AttnRopeTensor * n)()
+    else:
+        out = []
+    words = []
     for i in range(n):
-        x, y, a = tensors[i], out[i], arr[i]
+        x = tensors[i]
         _need_cuda(x, "every tensor", dt, dev)
-        _need_cuda(y, "out", dt, dev)
-        sx, sy = x.shape, y.shape
-        if x.dim() != nd or sx[-2] != N or sx[-1] != D or (not jagged and sx[0] != B):
+        sx = x.shape
+        if len(sx) != nd or sx[-2] != N or sx[-1] != D or (not jagged and sx[0] != B):
             raise ValueError("the tensors must agree in all but their heads")
-        if sy != sx:
-            raise ValueError(f"out must have shape {tuple(sx)}, got {tuple(sy)}")
-        a.x, a.y, a.H = x.data_ptr(), y.data_ptr(), sx[-3]
-        if jagged:
-            a.x_stride[1:] = x.stride()[:2]
-            a.y_stride[1:] = y.stride()[:2]
+        if given:
+            y = out[i]
+            _need_cuda(y, "out", dt, dev)
+            if y.shape != sx:
+                raise ValueError(f"out must have shape {tuple(sx)}, got {tuple(y.shape)}")
         else:
-            a.x_stride[:] = x.stride()[:3]
-            a.y_stride[:] = y.stride()[:3]
+            y = torch.empty(sx, dtype=dt, device=dev)
+            out.append(y)
+        xs, ys = x.stride(), y.stride()
+        words += (x.data_ptr(), y.data_ptr(), sx[-3])
+        if jagged:
+            words += (0, xs[0], xs[1], 0, ys[0], ys[1])
+        else:
+            words += (xs[0], xs[1], xs[2], ys[0], ys[1], ys[2])
+    out = tuple(out)
+    arr = _ROPE_WORDS[n](*words)
     pos = ps = off = None
     n_seq = 0
     if positions is not None:

@@ -13,9 +13,10 @@
 // instructions, cost 1 to 4 % at the sizes below.)
 //
 // Both are bound by memory: an element is read once and written once.  A
-// thread owns one 16-element piece of one token (for half-split pairs the
-// two 8-element pieces that turn together), computes its eight angles once,
-// behind the first loads, and walks over the heads with them in registers,
+// thread owns two 16-byte pieces of one token, half a row (of the rotated
+// part, or of the rest) apart: the pieces that turn together where pairs are
+// half-split, and neighbouring threads on neighbouring pieces in any case.
+// It computes its eight angles once, behind the first loads, and walks over the heads with them in registers,
 // two heads of 16-byte loads in flight and four blocks on an SM (four heads
 // and two blocks were slower: 47 us for 45); a table of cos and sin, the
 // alternative, is a second stream to read and has to end at some position.
@@ -72,7 +73,7 @@ __device__ __forceinline__ void store_piece(uint16_t* y, int d1, const Piece& v)
 }
 
 // Eight pairs.  Half-split: element j of a with element j of b;
-// interleaved: neighbours of a, then of b.
+// interleaved: the four pairs of neighbours of a, then those of b.
 template <bool F16, bool INTER>
 __device__ __forceinline__ void rotate_piece(Piece& v, const float2 (&cs)[8]) {
   uint32_t* a = reinterpret_cast<uint32_t*>(&v.a);
@@ -99,18 +100,21 @@ __device__ __forceinline__ void rotate_piece(Piece& v, const float2 (&cs)[8]) {
 struct Angles {
   float2 cs[8];
   bool have = false;
-  __device__ __forceinline__ void need(const RopeSpec& r, int first, int pos) {
+  // of item `item` of the rotated part
+  template <bool INTER>
+  __device__ __forceinline__ void need(const RopeSpec& r, int item, int pos) {
     if (have) return;
     have = true;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = turn(r, first + i, pos);
+    for (int i = 0; i < 8; ++i)
+      cs[i] = turn(r, INTER ? 4 * item + (i & 3) + (i < 4 ? 0 : r.rot / 4) : 8 * item + i, pos);
   }
 };
 
 // n heads of one piece: rotated, or copied
 template <bool F16, bool INTER>
 __device__ __forceinline__ void walk_heads(const uint16_t* x, long long xh, uint16_t* y, long long yh, int n, int d1,
-                                           bool turned, Angles& a, const RopeSpec& r, int first, int pos) {
+                                           bool turned, Angles& a, const RopeSpec& r, int item, int pos) {
   constexpr int U = kRopeUnroll;
   int h = 0;
 #pragma unroll 1
@@ -119,7 +123,7 @@ __device__ __forceinline__ void walk_heads(const uint16_t* x, long long xh, uint
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = load_piece(x + u * xh, d1);
     if (turned) {
-      a.need(r, first, pos);
+      a.template need<INTER>(r, item, pos);
 #pragma unroll
       for (int u = 0; u < U; ++u) rotate_piece<F16, INTER>(v[u], a.cs);
     }
@@ -132,7 +136,7 @@ __device__ __forceinline__ void walk_heads(const uint16_t* x, long long xh, uint
   for (; h < n; ++h, x += xh, y += yh) {
     Piece v = load_piece(x, d1);
     if (turned) {
-      a.need(r, first, pos);
+      a.template need<INTER>(r, item, pos);
       rotate_piece<F16, INTER>(v, a.cs);
     }
     store_piece(y, d1, v);
@@ -207,14 +211,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
     int d0, d1;
     if constexpr (VEC) {
       turned = item < p.r.rot / 16;
-      d0 = 16 * item;
-      d1 = 8;
-      if (turned) {
-        if (!INTER) {
-          d0 = 8 * item;
-          d1 = p.r.rot / 2;
-        }
-      }
+      d0 = turned ? 8 * item : p.r.rot / 2 + 8 * item;  // behind rot: 8 (item - rot / 16) further
+      d1 = (turned ? p.r.rot : p.D - p.r.rot) / 2;
     } else {
       turned = item < p.r.rot / 2;
       d0 = turned ? (INTER ? 2 * item : item) : item + p.r.rot / 2;
@@ -234,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
       uint16_t* y = a.y + b * a.ys[0] + lo * a.ys[1] + n * a.ys[2];
       if (!turned && x == y) continue;  // in place: nothing to copy
       if constexpr (VEC)
-        walk_heads<F16, INTER>(x + d0, a.xs[1], y + d0, a.ys[1], hi - lo, d1, turned, angles, p.r, 8 * item, pos);
+        walk_heads<F16, INTER>(x + d0, a.xs[1], y + d0, a.ys[1], hi - lo, d1, turned, angles, p.r, item, pos);
       else
         walk_heads_scalar<F16>(x, a.xs[1], y, a.ys[1], hi - lo, d0, d1, turned, angles.cs[0]);
     }
@@ -280,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const __grid_
   const bool turned = item < (VEC ? p.r.rot / 16 : p.r.rot / 2);
   int d0, d1;
   if constexpr (VEC) {
-    d0 = turned && !INTER ? 8 * item : 16 * item;
-    d1 = turned && !INTER ? p.r.rot / 2 : 8;
+    d0 = turned ? 8 * item : p.r.rot / 2 + 8 * item;
+    d1 = (turned ? p.r.rot : p.Dqk - p.r.rot) / 2;
   } else {
     d0 = turned ? (INTER ? 2 * item : item) : item + p.r.rot / 2;
     d1 = INTER ? d0 + 1 : d0 + p.r.rot / 2;
@@ -307,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const __grid_
         }
       } else if (turned || x != y) {
         if constexpr (VEC)
-          walk_heads<F16, INTER>(x + d0, p.qs[1], y + d0, p.qos[1], hi - lo, d1, turned, angles, p.r, 8 * item, static_cast<int>(pos));
+          walk_heads<F16, INTER>(x + d0, p.qs[1], y + d0, p.qos[1], hi - lo, d1, turned, angles, p.r, item, static_cast<int>(pos));
         else
           walk_heads_scalar<F16>(x, p.qs[1], y, p.qos[1], hi - lo, d0, d1, turned, angles.cs[0]);
       }
@@ -320,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const __grid_
       const uint16_t* x = p.k + t * p.ks[0] + lo * p.ks[1];
       uint16_t* y = p.k_pool + page * p.kp[0] + lo * p.kp[1] + slot * p.kp[2];
       if constexpr (VEC)
-        walk_heads<F16, INTER>(x + d0, p.ks[1], y + d0, p.kp[1], hi - lo, d1, turned, angles, p.r, 8 * item, static_cast<int>(pos));
+        walk_heads<F16, INTER>(x + d0, p.ks[1], y + d0, p.kp[1], hi - lo, d1, turned, angles, p.r, item, static_cast<int>(pos));
       else
         walk_heads_scalar<F16>(x, p.ks[1], y, p.kp[1], hi - lo, d0, d1, turned, angles.cs[0]);
     }
@@ -331,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const __grid_
       const uint16_t* x = p.v + t * p.vs[0] + lo * p.vs[1];
       uint16_t* y = p.v_pool + page * p.vp[0] + lo * p.vp[1] + slot * p.vp[2];
       if constexpr (VEC)
-        walk_heads<F16, INTER>(x + 16 * item, p.vs[1], y + 16 * item, p.vp[1], hi - lo, 8, false, angles, p.r, 0, 0);
+        walk_heads<F16, INTER>(x + 8 * item, p.vs[1], y + 8 * item, p.vp[1], hi - lo, p.Dv / 2, false, angles, p.r, 0, 0);
       else
         walk_heads_scalar<F16>(x, p.vs[1], y, p.vp[1], hi - lo, item, item, false, angles.cs[0]);
     }
