@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from array import array
 from typing import Optional
 
 import torch
@@ -74,11 +75,6 @@ class AttnRopeTensor(ctypes.Structure):
                 ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
 
 
-# an array of AttnRopeTensor as 64-bit words, one constructor call instead of
-# nine assignments a tensor (H's upper half is padding; the hosts are little-endian)
-_ROPE_WORDS = [ctypes.c_int64 * (9 * n) for n in range(5)]
-assert ctypes.sizeof(AttnRopeTensor) == 72
-
 
 class AttnRopeFreq(ctypes.Structure):
     _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
@@ -95,6 +91,7 @@ class AttnPagedCache(ctypes.Structure):
 
 
 class AttnPagedNew(ctypes.Structure):
+    # (attn_paged_append below writes it as 64-bit words, in this order)
     _fields_ = [("T", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("k", ctypes.c_void_p),
                 ("v", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("Hq", ctypes.c_int32),
                 ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2), ("q_stride", ctypes.c_int64 * 2),
@@ -164,7 +161,7 @@ def lib() -> ctypes.CDLL:
     L.attn_rope_steps.argtypes = [vp, ctypes.c_int32, vp]
     for f in (L.attn_paged_append, L.attn_paged_append_f16):
         f.restype = i32
-        f.argtypes = [ctypes.POINTER(AttnPagedCache), ctypes.POINTER(AttnPagedNew), ctypes.POINTER(AttnRopeSpec), vp]
+        f.argtypes = [ctypes.POINTER(AttnPagedCache), vp, ctypes.POINTER(AttnRopeSpec), vp]
     L.attn_paged_decode_workspace.restype = sz
     L.attn_paged_decode_workspace.argtypes = [ctypes.POINTER(AttnPagedCache), ctypes.c_int32]
     for f in (L.attn_paged_decode, L.attn_paged_decode_f16):
@@ -577,11 +574,14 @@ def _need_cuda(t: torch.Tensor, name: str, dtype, dev=None):
 def _call_on(dev, fn, *args):
     """fn(*args, stream) with `dev` current; its status raised."""
     i = dev.index
+    # (the handle alone: torch.cuda.current_stream builds an object around it,
+    # at two thirds of the cost of the call)
+    stream = torch._C._cuda_getCurrentRawStream(i)
     if torch.cuda.current_device() == i:
-        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream().cuda_stream)
+            st = fn(*args, stream)
     if st != 0:
         _check(st)
 
@@ -671,36 +671,35 @@ def attn_rope(tensors, rope: Rope, positions: Optional[torch.Tensor] = None, off
         raise ValueError(f"rot_dim {rope.rot_dim} exceeds the head dim {D}")
     if rope.steps.device != dev:
         raise ValueError(f"the rotation is on {rope.steps.device}, the tensors on {dev}")
-    given = out is not None
-    if given:
+    if out is not None:
         out = tuple(out)
         if len(out) != n:
             raise ValueError("out must hold one tensor for each input")
-    else:
-        out = []
-    words = []
-    for i in range(n):
-        x = tensors[i]
-        _need_cuda(x, "every tensor", dt, dev)
-        sx = x.shape
+        for x, y in zip(tensors, out):
+            _need_cuda(y, "out", dt, dev)
+            if y.shape != x.shape:
+                raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(y.shape)}")
+    words = []  # of an array of AttnRopeTensor (H's upper half is padding; the hosts are little-endian)
+    made = []
+    for i, x in enumerate(tensors):
+        xs, sx = x.stride(), x.shape
+        if x.dtype != dt or x.device != dev or dev.type != "cuda" or xs[-1] != 1:
+            _need_cuda(x, "every tensor", dt, dev)
         if len(sx) != nd or sx[-2] != N or sx[-1] != D or (not jagged and sx[0] != B):
             raise ValueError("the tensors must agree in all but their heads")
-        if given:
+        if out is None:
+            y = torch.empty_like(x) if x.is_contiguous() else torch.empty(sx, dtype=dt, device=dev)
+            made.append(y)
+        else:
             y = out[i]
-            _need_cuda(y, "out", dt, dev)
-            if y.shape != sx:
-                raise ValueError(f"out must have shape {tuple(sx)}, got {tuple(y.shape)}")
-        else:
-            y = torch.empty(sx, dtype=dt, device=dev)
-            out.append(y)
-        xs, ys = x.stride(), y.stride()
-        words += (x.data_ptr(), y.data_ptr(), sx[-3])
+        ys = y.stride()
         if jagged:
-            words += (0, xs[0], xs[1], 0, ys[0], ys[1])
+            words += (x.data_ptr(), y.data_ptr(), sx[0], 0, xs[0], xs[1], 0, ys[0], ys[1])
         else:
-            words += (xs[0], xs[1], xs[2], ys[0], ys[1], ys[2])
-    out = tuple(out)
-    arr = _ROPE_WORDS[n](*words)
+            words += (x.data_ptr(), y.data_ptr(), sx[1], xs[0], xs[1], xs[2], ys[0], ys[1], ys[2])
+    if out is None:
+        out = tuple(made)
+    arr = array("q", words)
     pos = ps = off = None
     n_seq = 0
     if positions is not None:
@@ -710,7 +709,8 @@ def attn_rope(tensors, rope: Rope, positions: Optional[torch.Tensor] = None, off
         if tuple(positions.shape) != want:
             raise ValueError(f"positions must have shape {want}, got {tuple(positions.shape)}")
         st = positions.stride()
-        ps = (ctypes.c_int64 * 2)(*(st if len(st) == 2 else (0, st[0])))
+        strides = array("q", st if len(st) == 2 else (0, st[0]))
+        ps = strides.buffer_info()[0]
         pos = positions.data_ptr()
     if jagged:
         _need(offsets, "offsets", torch.int32, dev)
@@ -718,7 +718,7 @@ def attn_rope(tensors, rope: Rope, positions: Optional[torch.Tensor] = None, off
             raise ValueError("offsets must be [B + 1]")
         off, n_seq = offsets.data_ptr(), offsets.numel() - 1
     L = lib()
-    _call_on(dev, L.attn_rope_f16 if dt == torch.float16 else L.attn_rope, B, N, D, rope._ref, arr, n, pos, ps, off,
+    _call_on(dev, L.attn_rope_f16 if dt == torch.float16 else L.attn_rope, B, N, D, rope._ref, arr.buffer_info()[0], n, pos, ps, off,
              n_seq, 1 if inverse else 0)
     return out
 
@@ -759,10 +759,8 @@ class PagedCache:
         self._workspace = {}  # bytes a decode needs, by query heads
 
     def _workspace_bytes(self, Hq: int) -> int:
-        n = self._workspace.get(Hq)
-        if n is None:
-            with torch.cuda.device(self.device):
-                n = self._workspace[Hq] = int(lib().attn_paged_decode_workspace(self._ref, Hq))
+        with torch.cuda.device(self.device):
+            n = self._workspace[Hq] = int(lib().attn_paged_decode_workspace(self._ref, Hq))
         return n
 
 
@@ -780,23 +778,23 @@ def attn_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, rope:
     writes nothing to the cache and zeros to its query row.  Any strides with
     contiguous rows; a jagged [H, T, D] tensor goes in as its transpose(0, 1)."""
     dev, dt = cache.device, cache.dtype
-    _need_cuda(k, "k", dt, dev)
-    _need_cuda(v, "v", dt, dev)
+    for name, t in (("k", k), ("v", v), ("q", q)):
+        if t is not None and (t.dtype != dt or t.device != dev or t.stride(-1) != 1):
+            _need_cuda(t, name, dt, dev)
     T = k.shape[0]
-    if tuple(k.shape) != (T, cache.Hkv, cache.Dqk) or tuple(v.shape) != (T, cache.Hkv, cache.Dv):
+    if k.shape != (T, cache.Hkv, cache.Dqk) or v.shape != (T, cache.Hkv, cache.Dv):
         raise ValueError(f"k must be [T, {cache.Hkv}, {cache.Dqk}] and v [T, {cache.Hkv}, {cache.Dv}]")
-    a = AttnPagedNew()
-    a.T, a.k, a.v = T, k.data_ptr(), v.data_ptr()
-    a.k_stride[:], a.v_stride[:] = k.stride()[:2], v.stride()[:2]
+    off = 0
     if offsets is not None:
         _need(offsets, "offsets", torch.int32, dev)
-        if tuple(offsets.shape) != (cache.B + 1,):
+        if offsets.shape != (cache.B + 1,):
             raise ValueError(f"offsets must be [{cache.B + 1}]")
-        a.offsets = offsets.data_ptr()
+        off = offsets.data_ptr()
     elif T != cache.B:
         raise ValueError(f"without offsets there is one token for each of the {cache.B} sequences, got {T}")
+    ks, vs, qs, os_ = k.stride(), v.stride(), (0, 0), (0, 0)
+    qp = op = Hq = 0
     if q is not None:
-        _need_cuda(q, "q", dt, dev)
         if q.dim() != 3 or q.shape[0] != T or q.shape[2] != cache.Dqk:
             raise ValueError(f"q must be [{T}, Hq, {cache.Dqk}]")
         if out is None:
@@ -805,10 +803,11 @@ def attn_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, rope:
             _need_cuda(out, "out", dt, dev)
             if out.shape != q.shape:
                 raise ValueError(f"out must have shape {tuple(q.shape)}, got {tuple(out.shape)}")
-        a.q, a.q_out, a.Hq = q.data_ptr(), out.data_ptr(), q.shape[1]
-        a.q_stride[:], a.q_out_stride[:] = q.stride()[:2], out.stride()[:2]
+        qp, op, Hq, qs, os_ = q.data_ptr(), out.data_ptr(), q.shape[1], q.stride(), out.stride()
     elif out is not None:
         raise ValueError("out holds the rotated q: there is none without q")
+    a = array("q", (T, off, k.data_ptr(), v.data_ptr(), qp, op, Hq, ks[0], ks[1], vs[0], vs[1], qs[0], qs[1],
+                    os_[0], os_[1]))
     if rope is not None:
         if rope.rot_dim > cache.Dqk:
             raise ValueError(f"rot_dim {rope.rot_dim} exceeds the head dim {cache.Dqk}")
@@ -816,7 +815,7 @@ def attn_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, rope:
             raise ValueError(f"the rotation is on {rope.steps.device}, the cache on {dev}")
     L = lib()
     _call_on(dev, L.attn_paged_append_f16 if dt == torch.float16 else L.attn_paged_append, cache._ref,
-             ctypes.byref(a), rope._ref if rope is not None else None)
+             a.buffer_info()[0], rope._ref if rope is not None else None)
     return out
 
 
@@ -825,11 +824,13 @@ def attn_paged_decode(cache: PagedCache, q: torch.Tensor, sm_scale: Optional[flo
     q [B, Hq, Dqk], Hq a multiple of the cache's key heads (query head h
     reads key head h // (Hq / Hkv)).  Returns (o [B, Hq, Dv], lse [B, Hq]
     float32, natural log).  An idle place (length 0) gets o = 0, lse = -inf."""
-    dev, dt = cache.device, cache.dtype
-    _need_cuda(q, "q", dt, dev)
-    if q.dim() != 3 or q.shape[0] != cache.B or q.shape[2] != cache.Dqk:
-        raise ValueError(f"q must be [{cache.B}, Hq, {cache.Dqk}]")
-    B, Hq = cache.B, q.shape[1]
+    dev, dt, B = cache.device, cache.dtype, cache.B
+    qs = q.stride()
+    if q.dtype != dt or q.device != dev or qs[-1] != 1:
+        _need_cuda(q, "q", dt, dev)
+    if len(qs) != 3 or q.shape[0] != B or q.shape[2] != cache.Dqk:
+        raise ValueError(f"q must be [{B}, Hq, {cache.Dqk}]")
+    Hq = q.shape[1]
     if cache.Hkv == 0 or Hq % cache.Hkv:
         raise ValueError(f"the cache's {cache.Hkv} key heads must divide the {Hq} query heads")
     if out is None:
@@ -839,12 +840,13 @@ def attn_paged_decode(cache: PagedCache, q: torch.Tensor, sm_scale: Optional[flo
         o, lse = out
         _need_out(o, "o", (B, Hq, cache.Dv), dt, dev)
         _need_out(lse, "lse", (B, Hq), torch.float32, dev)
-    n = cache._workspace_bytes(Hq)
+    n = cache._workspace.get(Hq)
+    if n is None:
+        n = cache._workspace_bytes(Hq)
     # of this call alone: a graph's is its own, calls on two streams have two
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    qs = q.stride()
+    strides = array("q", qs)
     L = lib()
     _call_on(dev, L.attn_paged_decode_f16 if dt == torch.float16 else L.attn_paged_decode, cache._ref, Hq,
-             q.data_ptr(), (ctypes.c_int64 * 2)(qs[0], qs[1]), _scale(sm_scale), o.data_ptr(), lse.data_ptr(),
-             ws.data_ptr(), n)
+             q.data_ptr(), strides.buffer_info()[0], _scale(sm_scale), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), n)
     return o, lse
