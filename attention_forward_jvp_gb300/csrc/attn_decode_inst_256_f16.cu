@@ -1,5 +1,5 @@
 // The paged decode kernels of key width 256, f16 storage.
-#include "attn_decode_kernel.cuh"
+#include "attn_decode_tc_kernel.cuh"
 
 namespace attn {
 template cudaError_t launch_decode<256, 64, true>(DecodeParams&, int, int, cudaStream_t);

@@ -109,16 +109,16 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
   return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
 }
 
-// The list of steps cut into ranges: `total` steps over `warps` warps, one
-// more for the first `extra` of them; and the place of this warp's range.
+// The list of steps cut into ranges: `total` steps over `ranges` ranges, one
+// more for the first `extra` of them; and the place of this thread's range.
 struct DecodeRange {
-  long long total, warps, each, extra;
-  long long lo, cta_lo, cta_hi;  // first step of the warp, of its CTA, behind the CTA's last
-  int count;                     // steps of the warp
+  long long total, ranges, each, extra;
+  long long lo, cta_lo, cta_hi;  // first step of the range, of its CTA, behind the CTA's last
+  int count;                     // steps of the range
   int b, hu, t, len;             // sequence, unit and step of lo, the sequence's length
   bool idle;                     // some sequence may be empty
-  __device__ long long start(long long x) const { return x < warps ? each * x + (x < extra ? x : extra) : total; }
-  // the warp that step x falls to
+  __device__ long long start(long long x) const { return x < ranges ? each * x + (x < extra ? x : extra) : total; }
+  // the range that step x falls to
   __device__ long long owner(long long x) const {
     return x < extra * (each + 1) ? divide(x, each + 1) : extra + divide(x - extra * (each + 1), each);
   }
@@ -131,11 +131,13 @@ struct DecodeWords {
 
 // Thread x holds sequence x (and adds up those behind it, a block's width
 // apart): its length, and the steps up to it within its warp.  I: int where
-// no list of this shape can pass 2^31 steps, else long long.
-template <class I, int NW>
+// no list of this shape can pass 2^31 steps, else long long.  BN: keys of a
+// step; NW: warps of a CTA, which has a range for each of them or one.
+template <class I, int BN, int NW, bool PER_WARP>
 __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const DecodeWords& s) {
   constexpr int THREADS = NW * 32;
   constexpr unsigned ALL = 0xffffffffu;
+  constexpr int R = PER_WARP ? NW : 1;  // ranges of a CTA
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const I HU = p.Hkv * p.chunks;
   auto length = [&](int b, bool& odd) {
@@ -153,9 +155,9 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
   };
   bool odd = false;
   int n = tid < p.B ? length(tid, odd) : 0;
-  I inc = scan((n + kDecodeBN - 1) / kDecodeBN), rest = 0;
+  I inc = scan((n + BN - 1) / BN), rest = 0;
   if (p.B > THREADS) {
-    for (int b = tid + THREADS; b < p.B; b += THREADS) rest += (length(b, odd) + kDecodeBN - 1) / kDecodeBN;
+    for (int b = tid + THREADS; b < p.B; b += THREADS) rest += (length(b, odd) + BN - 1) / BN;
 #pragma unroll
     for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(ALL, rest, o);
   }
@@ -174,23 +176,23 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
     for (int o = 16; o; o >>= 1) r += __shfl_xor_sync(ALL, r, o);
     steps += r;
   }
-  const I total = steps * HU, most = static_cast<I>(gridDim.x) * NW;
-  I warps = (total >> kDecodeMinStepsLog) + 1;
-  warps = warps > most ? most : warps;
-  warps = warps > total ? total : warps;
-  warps = warps < 1 ? 1 : warps;
+  const I total = steps * HU, most = static_cast<I>(gridDim.x) * R;
+  I ranges = (total >> kDecodeMinStepsLog) + 1;
+  ranges = ranges > most ? most : ranges;
+  ranges = ranges > total ? total : ranges;
+  ranges = ranges < 1 ? 1 : ranges;
   DecodeRange w;
-  const I each = divide(total, warps);
+  const I each = divide(total, ranges);
   w.idle = idle;
   w.total = total;
-  w.warps = warps;
+  w.ranges = ranges;
   w.each = each;
-  w.extra = total - each * warps;
-  const int first = blockIdx.x * NW;
-  w.lo = w.start(first + warp);
-  w.count = static_cast<int>(w.start(first + warp + 1) - w.lo);
+  w.extra = total - each * ranges;
+  const int first = blockIdx.x * R, mine = first + (PER_WARP ? warp : 0);
+  w.lo = w.start(mine);
+  w.count = static_cast<int>(w.start(mine + 1) - w.lo);
   w.cta_lo = w.start(first);
-  w.cta_hi = w.start(first + NW);
+  w.cta_hi = w.start(first + R);
   if (w.count == 0) w.lo = w.cta_lo;
   w.b = w.hu = w.t = w.len = 0;
   if (w.cta_lo >= total) return w;
@@ -211,7 +213,7 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
       // counts once for every unit
       w.b = b0 + chunk * 32 + k;
       w.len = s.lens[chunk * 32 + k];
-      const int nt = (w.len + kDecodeBN - 1) / kDecodeBN;
+      const int nt = (w.len + BN - 1) / BN;
       const I r = y * HU + (static_cast<I>(w.lo) - x * HU);
       const I hu = divide(r, static_cast<I>(nt));
       w.hu = static_cast<int>(hu);
@@ -221,7 +223,7 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
     b0 += THREADS;
     if (b0 >= p.B || w.cta_hi <= static_cast<long long>(base) * HU) break;
     n = b0 + tid < p.B ? length(b0 + tid, odd) : 0;
-    inc = scan((n + kDecodeBN - 1) / kDecodeBN);
+    inc = scan((n + BN - 1) / BN);
     __syncthreads();
     s.lens[tid] = n;
     s.sums[tid] = static_cast<uint32_t>(inc);
@@ -230,6 +232,28 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
     cum = scan(lane < NW ? static_cast<I>(s.totals[lane]) : 0);
   }
   return w;
+}
+
+// Sequences without keys: O = 0, LSE = -inf
+static __device__ __noinline__ void decode_idle(const DecodeParams& p) {
+  const int Hq = p.Hkv * p.G;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (p.seq_lens[b] > 0 && p.capacity > 0) continue;
+    for (int i = threadIdx.x; i < Hq * (p.dv / 8); i += blockDim.x)
+      reinterpret_cast<uint4*>(p.o + static_cast<long long>(b) * Hq * p.dv)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < Hq; i += blockDim.x) p.lse[static_cast<long long>(b) * Hq + i] = -INFINITY;
+  }
+}
+
+// What joins a unit that begins in range x (of R to a CTA) and has its last
+// step at `end`: the parts of x's CTA from x on (`here` of them), one for each
+// CTA that lies within the unit, and those of the CTA where it ends.
+template <int R>
+__device__ __forceinline__ int4 decode_describe(const DecodeRange& w, int b, int hu, int x, int here, long long end) {
+  const int z = static_cast<int>(w.owner(end)), c = x / R, e = z / R;
+  if (e == c) return make_int4(b, hu, z - x + 1, 0);
+  const bool joined = w.start((e + 1LL) * R) == end + 1;  // CTA e lies within the unit too
+  return make_int4(b, hu, here | (joined ? 1 : z - e * R + 1) << 8, e - c - 1);
 }
 
 // Shared memory and registers of a warp decide how many fit on an SM: three
@@ -265,7 +289,8 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   using P = DecodePlan<DQ, DV, NT>;
   constexpr int BN = P::BN, S = P::S, NW = P::NW, THREADS = NW * 32, PITCH = P::PITCH;
   constexpr int KPITCH = DQ * 2, VPITCH = DV * 2;
-  extern __shared__ __align__(128) char smem[];
+  extern __shared__ __align__(128) char decode_smem[];
+  char* smem = decode_smem;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   char* mine = smem + warp * P::WARP_BYTES;  // this warp's ring, then its Q
   const uint32_t ring = smem_u32(mine);
@@ -326,7 +351,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   // at once
   const int first = blockIdx.x * NW;  // this CTA's first warp
   const int me = first + warp;
-  const DecodeRange w = p.wide ? decode_plan<long long, NW>(p, words) : decode_plan<int, NW>(p, words);
+  const DecodeRange w = p.wide ? decode_plan<long long, BN, NW, true>(p, words) : decode_plan<int, BN, NW, true>(p, words);
   const int count = w.count;
   Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len};  // the step computed next
   Cursor ahead = cur;                                  // the step that `next` is of
@@ -339,24 +364,11 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     }
   }
 
-  // What joins a unit that begins in warp x and has its last step at `end`:
-  // the parts of x's CTA from x on (`here` of them), one for each CTA that
-  // lies within the unit, and those of the CTA where it ends.
-  auto describe = [&](int b, int hu, int x, int here, long long end) -> int4 {
-    const int z = static_cast<int>(w.owner(end)), c = x / NW, e = z / NW;
-    if (e == c) return make_int4(b, hu, z - x + 1, 0);
-    const bool joined = w.start((e + 1LL) * NW) == end + 1;  // CTA e lies within the unit too
-    return make_int4(b, hu, here | (joined ? 1 : z - e * NW + 1) << 8, e - c - 1);
+  auto describe = [&](int b, int hu, int x, int here, long long end) {
+    return decode_describe<NW>(w, b, hu, x, here, end);
   };
 
-  // ---- sequences without keys: O = 0, LSE = -inf
-  for (int b = blockIdx.x; w.idle && b < p.B; b += gridDim.x) {
-    if (length(b) != 0) continue;
-    const int Hq = p.Hkv * p.G;
-    for (int i = tid; i < Hq * (p.dv / 8); i += THREADS)
-      reinterpret_cast<uint4*>(p.o + static_cast<long long>(b) * Hq * p.dv)[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = tid; i < Hq; i += THREADS) p.lse[static_cast<long long>(b) * Hq + i] = -INFINITY;
-  }
+  if (w.idle) decode_idle(p);
   if (p.split && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
   if (w.cta_lo >= w.total) return;
 
@@ -813,16 +825,6 @@ cudaError_t launch_decode_nt(DecodeParams& p, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess || !p.split) return e;
   return decode_launch_one(attn_decode_join<DV, F16>, p, dim3(ctas, (p.rows + p.join_rows - 1) / p.join_rows),
                            kJoinWarps * 32, 0, stream);
-}
-
-template <int DQ, int DV, bool F16>
-cudaError_t launch_decode(DecodeParams& p, int nt, int ctas, cudaStream_t stream) {
-  if (nt == 1) return launch_decode_nt<DQ, DV, F16, 1>(p, ctas, stream);
-  if (nt == 2) return launch_decode_nt<DQ, DV, F16, 2>(p, ctas, stream);
-  if constexpr (decode_max_rows(DV) == 32)
-    return launch_decode_nt<DQ, DV, F16, 4>(p, ctas, stream);
-  else
-    return cudaErrorInvalidValue;
 }
 
 }  // namespace attn

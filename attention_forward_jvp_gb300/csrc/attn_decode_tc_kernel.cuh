@@ -1,0 +1,471 @@
+// The paged decode for many query heads on a key head (17 and more): the same
+// list of steps, ranges and joining as attn_decode_kernel.cuh, with 64-key
+// tiles, a range for each CTA, and the products on tcgen05.
+//
+//   S (128 x 64)   = Q K^T       Q: the unit's heads as rows, from shared memory
+//   O (128 x Dv)  += P V         P: from tensor memory, V as it lies (MN-major)
+//
+// What bounds it: memory up to 128 heads (256 flops a byte, a sixteenth of a
+// tile's time in products).  mma.sync (64 heads, Dqk 256, Dv 128: 140 us)
+// would have to read every key once for 8 heads' columns; here a tile is
+// read once for all of them, and heads short of 128 cost nothing but unused
+// lanes.
+//
+// Warps 0-7 are the softmax: two to a quadrant of 32 lanes (32 heads), each
+// with half of a tile's columns; quadrants behind the last head do nothing.
+// Warps 8-11 bring tiles (16 keys each) by 16-byte asynchronous copies, row
+// by row through the page table, and signal each tile when its copies have
+// landed.  Warp 12 issues the products: S of tile i + 1 before O of tile i.
+// S and P have two buffers each in tensor memory.  P is split into two
+// 16-bit parts there, like the warps' P of the other kernel.
+#pragma once
+#include "attn_decode_kernel.cuh"
+#include "attn_kernel.cuh"
+
+namespace attn {
+
+constexpr int kTcBN = 64, kTcRows = 128;
+
+template <int DQ, int DV>
+struct DecodeTcPlan {
+  static constexpr int NW = 13, THREADS = NW * 32;
+  static constexpr int SUB = kTcBN * 128;                // 64 columns of a tile
+  static constexpr int K_TILE = DQ / 64 * SUB, TILE = K_TILE + DV / 64 * SUB;
+  static constexpr int Q_SUB = kTcRows * 128, Q_TILE = DQ / 64 * Q_SUB;
+  static constexpr int MISC = 8 * THREADS + 2 * 8 * 16 + 2 * 2 * kTcRows * 4 + 256;
+  static constexpr int FIT = 227 * 1024 - MISC - 1024;   // (1024: alignment)
+  static constexpr int NQ = 2 * Q_TILE + 3 * TILE <= FIT ? 2 : 1;
+  static constexpr int S_FIT = (FIT - NQ * Q_TILE) / TILE, S = S_FIT > 6 ? 6 : S_FIT;
+  static constexpr int OFF_RING = NQ * Q_TILE, OFF_MISC = OFF_RING + S * TILE;
+  static constexpr int SMEM = OFF_MISC + MISC + 1024;
+  // barriers
+  static constexpr int B_FULL = 0, B_EMPTY = S, B_SF = 2 * S, B_PF = 2 * S + 2, B_QE = 2 * S + 4, B_OF = 2 * S + 6,
+                       B_OE = 2 * S + 7, B_LS = 2 * S + 8, B_DRAIN = 2 * S + 9, NBAR = 2 * S + 10;
+  // tensor memory columns: S, S, P, P (upper | lower parts), O
+  static constexpr int COL_P = 128, COL_O = 256, TMEM = 512;
+  static_assert(S >= 2 && NBAR * 8 <= 200, "decode plan");
+};
+
+template <int DQ, int DV, bool F16>
+__global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
+    attn_decode_tc_kernel(const __grid_constant__ DecodeParams p) {
+  using P = DecodeTcPlan<DQ, DV>;
+  constexpr int BN = kTcBN, S = P::S, NQ = P::NQ;
+  extern __shared__ __align__(128) char decode_smem[];
+  char* smem = decode_smem + ((1024 - (smem_u32(decode_smem) & 1023)) & 1023);  // swizzle atoms of 1024 bytes
+  const uint32_t base = smem_u32(smem);
+  char* misc = smem + P::OFF_MISC;
+  const DecodeWords words{reinterpret_cast<int*>(misc), reinterpret_cast<uint32_t*>(misc) + P::THREADS,
+                          reinterpret_cast<long long*>(misc + 8 * P::THREADS)};
+  float* lsum = reinterpret_cast<float*>(misc + 8 * P::THREADS + 2 * 8 * 16);  // [2 units][2 halves][row]
+  char* ctl = misc + P::MISC - 256;
+  const uint32_t bar0 = smem_u32(ctl);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(ctl + 208);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + 212);
+  auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int HU = p.Hkv * p.chunks;
+  const int quads = (p.rows + 31) / 32;  // quadrants with heads
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(bar(P::B_FULL + i), 4);
+      mbar_init(bar(P::B_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(P::B_SF + i), 1);
+      mbar_init(bar(P::B_PF + i), 2 * quads);
+      mbar_init(bar(P::B_QE + i), 1);
+    }
+    mbar_init(bar(P::B_OF), 1);
+    mbar_init(bar(P::B_OE), 2 * quads);
+    mbar_init(bar(P::B_LS), 64 * quads);
+    mbar_init(bar(P::B_DRAIN), 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), P::TMEM);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  griddep_wait();
+  griddep_launch_dependents();
+  // (barriers and the tensor-memory address are published by its barrier)
+  const DecodeRange w =
+      p.wide ? decode_plan<long long, BN, P::NW, false>(p, words) : decode_plan<int, BN, P::NW, false>(p, words);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int count = w.count;
+  if (w.idle) decode_idle(p);
+  if (p.split && tid == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+
+  const Waiter W{abort_flag, p.err + 1, p.timeout_ns};
+  auto wait_all = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar(b), parity, W)); };
+  auto wait_sleep = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar_sleep(bar(b), parity, W)); };
+  auto length = [&](int b) {
+    const int n = p.seq_lens[b];
+    return n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
+  };
+  auto steps_of = [](int len) { return (len + BN - 1) / BN; };
+  struct Cursor {
+    int b, hu, t, nt, len;
+  };
+  auto advance = [&](Cursor& a) {
+    if (++a.t < a.nt) return;
+    a.t = 0;
+    if (++a.hu < HU) return;
+    a.hu = 0;
+    while (a.b + 1 < p.B) {
+      ++a.b;
+      a.len = length(a.b);
+      a.nt = steps_of(a.len);
+      if (a.nt > 0) break;
+    }
+  };
+  Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len};
+  auto unit = [&](const Cursor& a, int& h, int& g0, int& n_rows) {
+    h = p.chunks == 1 ? a.hu : a.hu / p.chunks;
+    g0 = (a.hu - h * p.chunks) * p.rows;
+    n_rows = min(p.rows, p.G - g0);
+  };
+
+  if (warp >= 8 && warp < 12 && count > 0) {
+    // ------------------------------------------------------------ producers
+    const int g = lane >> 2, q4 = lane & 3, k0 = (warp - 8) * 16;
+    struct Place {
+      int page[2], slot[2], h;
+    };
+    auto lookup = [&](const Cursor& a) -> Place {
+      Place x;
+      x.h = p.chunks == 1 ? a.hu : a.hu / p.chunks;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int key = a.t * BN + k0 + g + 8 * r;
+        x.page[r] = 0;
+        x.slot[r] = -1;
+        if (key < a.len) {
+          const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+          x.slot[r] = key - e * p.page_size;
+          x.page[r] = p.page_table[a.b * p.table_stride + e];
+        }
+      }
+      return x;
+    };
+    auto issue = [&](const Place& x, int stage) {
+      const uint32_t kd = base + P::OFF_RING + stage * P::TILE + (k0 + g) * 128 + ((q4 ^ g) << 4);
+      const uint32_t vd = kd + P::K_TILE;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const bool live = x.slot[r] >= 0 && x.page[r] >= 0 && x.page[r] < p.n_pages;
+        if (!live && x.slot[r] >= 0) *p.err = 1;
+        const uint16_t* k = live ? p.k + x.page[r] * p.kp[0] + x.h * p.kp[1] + x.slot[r] * p.kp[2] + 8 * q4 : p.q;
+        const uint16_t* v = live ? p.v + x.page[r] * p.vp[0] + x.h * p.vp[1] + x.slot[r] * p.vp[2] + 8 * q4 : p.q;
+#pragma unroll
+        for (int j = 0; j < DQ / 32; ++j) {
+          const bool in = live && 32 * j + 8 * q4 < p.dqk;
+          cp_async16((kd ^ ((j & 1) << 6)) + r * 1024 + (j >> 1) * P::SUB, in ? k + 32 * j : p.q, in);
+        }
+#pragma unroll
+        for (int j = 0; j < DV / 32; ++j) {
+          const bool in = live && 32 * j + 8 * q4 < p.dv;
+          cp_async16((vd ^ ((j & 1) << 6)) + r * 1024 + (j >> 1) * P::SUB, in ? v + 32 * j : p.q, in);
+        }
+      }
+    };
+    // the unit's heads; rows behind them, up to the quadrant's end, are zeros
+    auto issue_q = [&](const Cursor& a, int qb) {
+      int h, g0, n_rows;
+      unit(a, h, g0, n_rows);
+      const uint16_t* q = p.q + a.b * p.qs[0] + (static_cast<long long>(h) * p.G + g0) * p.qs[1];
+      const uint32_t qd = base + qb * P::Q_TILE;
+      constexpr int PIECES = DQ / 8;
+      for (int x = tid - 256; x < quads * 32 * PIECES; x += 128) {
+        const int r = x / PIECES, c = x % PIECES;
+        const bool in = r < n_rows && 8 * c < p.dqk;
+        cp_async16(qd + (c >> 3) * P::Q_SUB + r * 128 + (((c & 7) ^ (r & 7)) << 4), in ? q + r * p.qs[1] + 8 * c : p.q,
+                   in);
+      }
+    };
+    // The oldest tile on its way: wait for this warp's copies of it, make
+    // them visible to the tensor core, count this warp in.
+    int issued = 0, signalled = 0;
+    auto signal_oldest = [&]() {
+      switch (issued - signalled) {
+        case 1: cp_async_wait<0>(); break;
+        case 2: cp_async_wait<1>(); break;
+        case 3: cp_async_wait<2>(); break;
+        case 4: cp_async_wait<3>(); break;
+        case 5: cp_async_wait<4>(); break;
+        default: cp_async_wait<5>(); break;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(P::B_FULL + signalled % S));
+      ++signalled;
+    };
+    bool ok = true;
+    int seg = 0;  // (cur: the tile issued next)
+    Place next = lookup(cur);
+    bool skip = p.skip_first_load && blockIdx.x == 0;
+    for (int j = 0; ok && j < count; ++j) {
+      // the stage is free when the products of tile j - S are done
+      ok = wait_all(P::B_EMPTY + j % S, ((j / S) & 1u) ^ 1u);
+      if (!ok) break;
+      if (j == 0 || cur.t == 0) {
+        if (j > 0) ++seg;
+        // (tiles of the unit before may still wait for this warp's signal)
+        if (seg >= NQ)
+          while (signalled < issued) signal_oldest();
+        ok = wait_all(P::B_QE + seg % NQ, ((seg / NQ) & 1u) ^ 1u);
+        if (!ok) break;
+        issue_q(cur, seg % NQ);
+      }
+      issue(next, j % S);
+      cp_async_commit();
+      ++issued;
+      // S - 1 tiles on their way while the oldest but those is computed
+      if (issued - signalled > S - 2) signal_oldest();
+      if (skip) {  // (failure-detection hook: the first tile never arrives)
+        cp_async_wait<0>();
+        skip = false;
+        signalled = issued;
+      }
+      if (j + 1 < count) {
+        advance(cur);
+        next = lookup(cur);
+      }
+    }
+    if (ok)
+      while (signalled < issued) signal_oldest();
+    cp_async_wait<0>();
+  } else if (warp == 12 && count > 0) {
+    // -------------------------------------------------------------- products
+    const bool leader = elect_one();
+    constexpr uint32_t idesc_s = idesc_16(kTcRows, BN, false, F16), idesc_o = idesc_16(kTcRows, DV, true, F16);
+    constexpr uint32_t kHi = sdesc_hi_sw128(1024);
+    const uint32_t lo_q = sdesc_lo(base, 16), lo_k = sdesc_lo(base + P::OFF_RING, 16);
+    const uint32_t lo_v = sdesc_lo(base + P::OFF_RING + P::K_TILE, P::SUB);
+    bool ok = true;
+    int seg = 0, pv_seg = 0;
+    bool first = true;  // of its unit in this CTA: the tile whose O is next
+    // O of tile j, the last of its unit or not
+    auto products_o = [&](int j, bool last) {
+      ok = wait_all(P::B_PF + (j & 1), (j >> 1) & 1u);
+      // the first product of a unit overwrites O: the unit before has left it
+      if (ok && first) ok = wait_all(P::B_OE, (pv_seg & 1u) ^ 1u);
+      if (!ok) return;
+      tc_fence_after();
+      if (leader) {
+        const uint32_t a = tmem + P::COL_P + (j & 1) * 64, v = lo_v + (j % S) * (P::TILE >> 4);
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk) {
+          const uint64_t d = sdesc_join(v + ((kk * 2048) >> 4), kHi);
+          mma_ts(tmem + P::COL_O, a + 8 * kk, d, idesc_o, first && kk == 0 ? 0u : 1u);
+          mma_ts(tmem + P::COL_O, a + 32 + 8 * kk, d, idesc_o, 1u);
+        }
+        tc_commit(bar(P::B_EMPTY + j % S));
+        if (last) tc_commit(bar(P::B_OF));
+      }
+      __syncwarp();
+      first = last;
+      if (last) ++pv_seg;
+    };
+    bool pending = false, last_before = false;  // O of tile i - 1
+    for (int i = 0; ok && i < count; ++i) {
+      const bool last = cur.t + 1 == cur.nt || i + 1 == count;
+      // S of this tile before O of the one before, unless it has not arrived
+      if (pending && !__all_sync(0xffffffffu, mbar_try_wait(bar(P::B_FULL + i % S), (i / S) & 1u))) {
+        products_o(i - 1, last_before);
+        pending = false;
+        if (!ok) break;
+      }
+      ok = wait_all(P::B_FULL + i % S, (i / S) & 1u);
+      if (!ok) break;
+      tc_fence_after();
+      if (leader) {
+        const uint32_t q = lo_q + (seg % NQ) * (P::Q_TILE >> 4), k = lo_k + (i % S) * (P::TILE >> 4);
+#pragma unroll
+        for (int kk = 0; kk < DQ / 16; ++kk) {
+          const uint32_t oq = ((kk >> 2) * P::Q_SUB + (kk & 3) * 32) >> 4, ok_ = ((kk >> 2) * P::SUB + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + (i & 1) * BN, sdesc_join(q + oq, kHi), sdesc_join(k + ok_, kHi), idesc_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(bar(P::B_SF + (i & 1)));
+        if (last) tc_commit(bar(P::B_QE + seg % NQ));
+      }
+      __syncwarp();
+      if (last) ++seg;
+      if (pending) products_o(i - 1, last_before);
+      pending = true;
+      last_before = last;
+      if (i + 1 < count) advance(cur);
+    }
+    if (ok && pending) products_o(count - 1, last_before);
+    if (leader) {
+      tc_commit(bar(P::B_DRAIN));
+      drain_bar(bar(P::B_DRAIN), 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp < 8 && (warp & 3) < quads && count > 0) {
+    // --------------------------------------------------------------- softmax
+    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    constexpr int DH = DV / 2;  // this warp's columns of O
+    float m = -INFINITY, l = 0.f;
+    bool ok = true, first = true;
+    int seg = 0, t0 = cur.t;
+    for (int i = 0; i < count; ++i) {
+      ok = wait_sleep(P::B_SF + (i & 1), (i >> 1) & 1u);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t x0[32], x1[32];  // this half's columns, the other's
+      tmem_ld_32x32b_x32(tl + (i & 1) * BN + half * 32, x0);
+      tmem_ld_32x32b_x32(tl + (i & 1) * BN + (half ^ 1) * 32, x1);
+      tmem_wait_ld_regs(x0);
+      tmem_regs_ready(x1);
+      const int live = cur.len - cur.t * BN;
+      if (live < BN) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          if (half * 32 + c >= live) x0[c] = 0xff800000u;
+          if ((half ^ 1) * 32 + c >= live) x1[c] = 0xff800000u;
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) top = max3f(top, __uint_as_float(x0[c]), __uint_as_float(x1[c]));
+      top *= p.scale_log2;
+      if (__any_sync(0xffffffffu, top > m + 8.f)) {
+        const float n = fmaxf(m, top), a = exp2_fast(m - (n == -INFINITY ? 0.f : n));
+        m = n;
+        l *= a;
+        if (!first) {
+          // O is at rest once the products of the tile before are done
+          ok = wait_sleep(P::B_EMPTY + (i - 1) % S, ((i - 1) / S) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < DH; c0 += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tl + P::COL_O + half * DH + c0, o);
+            tmem_wait_ld_regs(o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * a);
+            tmem_st_32x32b_x32(tl + P::COL_O + half * DH + c0, o);
+          }
+          tmem_wait_st();
+        }
+      }
+      const float u = m == -INFINITY ? 0.f : m;
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        const float a = exp2_fast(fmaf(__uint_as_float(x0[c]), p.scale_log2, -u));
+        const float b = exp2_fast(fmaf(__uint_as_float(x0[c + 1]), p.scale_log2, -u));
+        l += a + b;
+        split2<F16>(a, b, hi[c / 2], lo[c / 2]);
+      }
+      const uint32_t tp = tl + P::COL_P + (i & 1) * 64 + half * 16;
+      tmem_st_32x32b_x16(tp, hi);
+      tmem_st_32x32b_x16(tp + 32, lo);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(P::B_PF + (i & 1)));
+      first = false;
+
+      const bool ends = cur.t + 1 == cur.nt;
+      if (ends || i + 1 == count) {
+        // ---- the unit's part in this CTA is complete
+        int h, g0, n_rows;
+        unit(cur, h, g0, n_rows);
+        float* ls = lsum + (seg & 1) * 2 * kTcRows;
+        ls[half * kTcRows + row] = l;
+        mbar_arrive(bar(P::B_LS));  // (a bounded wait, unlike a named barrier's)
+        ok = wait_sleep(P::B_LS, seg & 1u) && wait_sleep(P::B_OF, seg & 1u);
+        if (!ok) break;
+        const float sum = ls[row] + ls[kTcRows + row];
+        tc_fence_after();
+        const bool begins = t0 == 0;
+        const bool in = row < n_rows;
+        const long long at = (static_cast<long long>(cur.b) * p.Hkv + h) * p.G + g0 + row;
+        const long long part = (2LL * blockIdx.x + (begins ? 1 : 0)) * p.rows + row;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+        for (int c0 = 0; c0 < DH; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(tl + P::COL_O + half * DH + c0, o);
+          tmem_wait_ld_regs(o);
+          const int col = half * DH + c0;
+          if (in && begins && ends) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                y[e] = pack2<F16>(__uint_as_float(o[c + 2 * e]) * inv, __uint_as_float(o[c + 2 * e + 1]) * inv);
+              if (col + c < p.dv)
+                *reinterpret_cast<uint4*>(p.o + at * p.dv + col + c) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else if (in) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4)
+              *reinterpret_cast<uint4*>(p.part_o + part * DV + col + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+          }
+        }
+        if (in && half == 0) {
+          if (begins && ends) p.lse[at] = sum == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(sum);
+          else p.part_ml[part] = make_float2(m, sum);
+        }
+        if (begins && !ends && tid == 0)
+          p.desc[blockIdx.x] = decode_describe<1>(w, cur.b, cur.hu, blockIdx.x, 1, w.lo + i + (cur.nt - 1 - cur.t));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(P::B_OE));
+        ++seg;
+        first = true;
+        m = -INFINITY;
+        l = 0.f;
+        t0 = 0;
+      }
+      if (i + 1 < count) advance(cur);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, P::TMEM);
+}
+
+template <int DQ, int DV, bool F16>
+cudaError_t launch_decode_tc(DecodeParams& p, int ctas, cudaStream_t stream) {
+  using P = DecodeTcPlan<DQ, DV>;
+  static bool attr_done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_done[dev]) {
+    e = cudaFuncSetAttribute(attn_decode_tc_kernel<DQ, DV, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(attn_decode_join<DV, F16>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  p.cta_warps = 1;
+  p.join_rows = (p.rows + 15) / 16;
+  e = decode_launch_one(attn_decode_tc_kernel<DQ, DV, F16>, p, dim3(ctas), P::THREADS, P::SMEM, stream);
+  if (e != cudaSuccess || !p.split) return e;
+  return decode_launch_one(attn_decode_join<DV, F16>, p, dim3(ctas, (p.rows + p.join_rows - 1) / p.join_rows),
+                           kJoinWarps * 32, 0, stream);
+}
+
+template <int DQ, int DV, bool F16>
+cudaError_t launch_decode(DecodeParams& p, int nt, int ctas, cudaStream_t stream) {
+  if (nt == 1) return launch_decode_nt<DQ, DV, F16, 1>(p, ctas, stream);
+  if (nt == 2) return launch_decode_nt<DQ, DV, F16, 2>(p, ctas, stream);
+  return launch_decode_tc<DQ, DV, F16>(p, ctas, stream);
+}
+
+}  // namespace attn

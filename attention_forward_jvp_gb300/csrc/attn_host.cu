@@ -794,6 +794,8 @@ attn_status noalloc_state(DeviceState* out) {
 
 namespace attn {
 void count_launch(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
+unsigned long long wait_timeout_ns() { return g_timeout_ns.load(); }
+int skip_first_load() { return g_skip_first_load.load(); }
 }  // namespace attn
 
 extern "C" {
@@ -883,14 +885,15 @@ attn_status attn_sync_check(void* stream) {
       timed_out = true;
     }
   }
-  // and the word of the paged cache's entry points
+  // and the words of the paged cache's entry points
   bool bad_page = false;
-  if (int* w = attn::page_error_word(dev)) {
-    int word = 0;
-    if (cudaMemcpy(&word, w, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return ATTN_ERR_CUDA;
-    if (word != 0) {
-      if (cudaMemset(w, 0, sizeof(int)) != cudaSuccess) return ATTN_ERR_CUDA;
-      bad_page = true;
+  if (int* w = attn::page_error_words(dev)) {
+    int word[2] = {0, 0};
+    if (cudaMemcpy(word, w, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (word[0] != 0 || word[1] != 0) {
+      if (cudaMemset(w, 0, sizeof(word)) != cudaSuccess) return ATTN_ERR_CUDA;
+      bad_page = word[0] != 0;
+      timed_out = timed_out || word[1] != 0;
     }
   }
   return timed_out ? ATTN_ERR_TIMEOUT : bad_page ? ATTN_ERR_PAGE : ATTN_OK;

@@ -28,9 +28,10 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-// The word that append and decode set on a bad page number or length: a
-// fixed device variable, so that no call allocates.
-__device__ int g_page_error;
+// The words that append and decode set on a bad page number or length, and
+// on a wait that ran out of time: fixed device variables, so that no call
+// allocates.
+__device__ int g_page_error[2];
 
 std::mutex g_mu;
 struct Device {
@@ -235,7 +236,7 @@ attn_status run_append(const attn_paged_cache* c, const attn_paged_new* n, const
 struct Layout {
   int dq, dv;          // kernel head dims
   int rows, chunks;    // query heads of a unit, units of a key head
-  int nt;              // groups of 8 query heads
+  int nt;              // groups of 8 query heads; 0: more than the warps' kernel takes
   int ctas;
   size_t desc, ml, total;  // workspace: bytes of the first two parts, of all
 };
@@ -243,12 +244,12 @@ Layout layout_of(const attn_paged_cache* c, int Hq, int sms) {
   Layout l;
   l.dq = c->Dqk < 64 ? 64 : c->Dqk;
   l.dv = c->Dv < 64 ? 64 : c->Dv;
-  const int G = Hq / c->Hkv, most = decode_max_rows(l.dv);
-  l.chunks = (G + most - 1) / most;
+  const int G = Hq / c->Hkv;
+  l.chunks = (G + kDecodeMaxRows - 1) / kDecodeMaxRows;
   l.rows = (G + l.chunks - 1) / l.chunks;
-  l.nt = l.rows <= 8 ? 1 : (l.rows <= 16 ? 2 : 4);
+  l.nt = l.rows > kDecodeWarpRows ? 0 : (l.rows + 7) / 8;
   l.ctas = sms;
-  const size_t warps = static_cast<size_t>(sms) * kDecodeMaxWarps;
+  const size_t warps = static_cast<size_t>(sms) * (l.nt == 0 ? 1 : kDecodeMaxWarps);  // ranges
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   l.desc = up(sizeof(int4) * warps);
   l.ml = up(sizeof(float2) * 2 * warps * l.rows);
@@ -326,6 +327,8 @@ attn_status run_decode(const attn_paged_cache* c, int32_t Hq, const void* q, con
   p.part_ml = reinterpret_cast<float2*>(ws + l.desc);
   p.part_o = reinterpret_cast<float*>(ws + l.desc + l.ml);
   p.err = d.err;
+  p.timeout_ns = wait_timeout_ns();
+  p.skip_first_load = skip_first_load();
   p.split = p.capacity > kDecodeBN ? 1 : 0;
   const double steps = (p.capacity / kDecodeBN + 1.0) * p.B * p.Hkv * p.chunks;
   p.wide = steps + l.ctas * kDecodeMaxWarps < 2147483648.0 ? 0 : 1;
@@ -338,7 +341,7 @@ attn_status run_decode(const attn_paged_cache* c, int32_t Hq, const void* q, con
 
 }  // namespace
 
-int* page_error_word(int dev) {
+int* page_error_words(int dev) {
   std::lock_guard<std::mutex> lk(g_mu);
   return dev >= 0 && dev < kMaxDevices ? g_dev[dev].err : nullptr;
 }

@@ -64,8 +64,8 @@ cudaError_t launch_append(const AppendParams& p, bool vec, bool f16, int splits,
 constexpr int kDecodeBN = 16;        // keys of a step
 constexpr int kDecodeMinStepsLog = 1;  // a warp takes two steps at least, where there are two
 constexpr int kDecodeMaxWarps = 16;  // warps of a CTA, at most
-// query heads of a work unit, at most: what the accumulators leave room for
-constexpr int decode_max_rows(int dv) { return dv <= 128 ? 32 : 16; }
+constexpr int kDecodeWarpRows = 16;   // query heads of a unit that a warp takes at most; more go to tcgen05
+constexpr int kDecodeMaxRows = 128;   // query heads of a unit, at most
 
 struct DecodeParams {
   const uint16_t *q, *k, *v;
@@ -85,21 +85,28 @@ struct DecodeParams {
   int4* desc;                  // [warp]: the unit that starts in it and ends in a later one
   float2* part_ml;             // [warp][2][rows]
   float* part_o;               // [warp][2][rows][kernel Dv]
-  int* err;
+  int* err;                    // [0]: bad page or length, [1]: a wait timed out
   int split;                   // 0: no sequence can have more than one step
+  unsigned long long timeout_ns;  // of a wait between the warps of a CTA (err[1])
+  int skip_first_load;         // failure-detection hook
   int wide;                    // 1: the list of steps might pass 2^31
   int cta_warps, join_rows;    // warps of a CTA, heads of a joining block (set by the launch)
 };
 
-// The decode kernel for kernel head dims DQ, DV and nt (1, 2 or 4) groups of
-// 8 query heads, followed, when p.split, by the joining kernel.
+// The decode kernel for kernel head dims DQ, DV and nt (1 or 2) groups of 8
+// query heads to a unit, or (0) more of them, followed, when p.split, by the
+// joining kernel.
 template <int DQ, int DV, bool F16>
 cudaError_t launch_decode(DecodeParams& p, int nt, int ctas, cudaStream_t stream);
 
-// Device word that append and decode set on a bad page number or length;
-// null where no call has set it up on this device.
-int* page_error_word(int dev);
+// Device words that append and decode set: [0] on a bad page number or
+// length, [1] on a wait that ran out of time; null where no call has set them
+// up on this device.
+int* page_error_words(int dev);
 
+// of attn_host.cu: the launch counter, the bound on a wait, the test hook
 void count_launch(int n);
+unsigned long long wait_timeout_ns();
+int skip_first_load();
 
 }  // namespace attn

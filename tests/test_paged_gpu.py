@@ -753,3 +753,34 @@ def test_pool_offsets_pass_32_bits():
         assert torch.equal(k[ids[j], :, :m], small.k[p, :, :m]) and torch.equal(v[ids[j], :, :m], small.v[p, :, :m])
     check_decode(small, q, o, lse)
     assert binding.sync_check() == 0
+
+
+def test_decode_wait_that_runs_out_is_reported():
+    # many heads: the kernel whose warps wait for one another.  A first tile
+    # that never arrives (host-set hook) ends every wait within its bound; the
+    # context and the next call are sound.
+    pool = Pool([300, 70], 1, 128, 64, 16, BF, seed=8)
+    q = randn((2, 40, 128), BF, 8)
+    binding.set_wait_timeout_ns(20_000_000)
+    binding.debug_skip_first_load(True)
+    try:
+        binding.attn_paged_decode(pool.cache, q)
+        assert binding.sync_check() == 5
+    finally:
+        binding.debug_skip_first_load(False)
+        binding.set_wait_timeout_ns(2_000_000_000)
+    assert binding.sync_check() == 0
+    check_decode(pool, q, *binding.attn_paged_decode(pool.cache, q))
+
+
+@pytest.mark.parametrize("B,Hkv,group,lens", [(1, 1, 64, "long"), (2, 1, 17, "mixed"), (40, 2, 33, "short"),
+                                              (30, 3, 100, "random"), (1, 2, 128, "long")])
+def test_decode_many_heads_splits(B, Hkv, group, lens):
+    r = np.random.RandomState(B + group)
+    n = {"long": [9011], "mixed": [5000, 130], "short": list(r.randint(1, 65, B)), "random": list(r.randint(0, 400, B))}[lens]
+    pool = Pool([int(x) for x in n], Hkv, 64, 64, 32, HF if group == 33 else BF, seed=B)
+    q = randn((B, group * Hkv, 64), pool.k.dtype, B, 2.0)
+    o, lse = binding.attn_paged_decode(pool.cache, q)
+    check_decode(pool, q, o, lse)
+    o2, lse2 = binding.attn_paged_decode(pool.cache, q)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
