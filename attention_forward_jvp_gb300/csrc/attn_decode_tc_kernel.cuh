@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
     for (int i = 0; ok && i < count; ++i) {
       const bool last = cur.t + 1 == cur.nt || i + 1 == count;
       // S of this tile before O of the one before, unless it has not arrived
-      if (pending && !__all_sync(0xffffffffu, mbar_try_wait(bar(P::B_FULL + i % S), (i / S) & 1u))) {
+      if (pending && !__all_sync(0xffffffffu, mbar_test_wait(bar(P::B_FULL + i % S), (i / S) & 1u))) {
         products_o(i - 1, last_before);
         pending = false;
         if (!ok) break;
