@@ -41,6 +41,26 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool l
   const int n = live ? 16 : 0;  // 0: the 16 bytes are zeroed, nothing is read
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+// Pieces q4, q4 + 4, .. of one row of D elements (d of them real) into a
+// 128-byte swizzled row: `dst` is where piece q4 goes, STEP bytes lie from one
+// 64-element chunk to the next.  A row that is not live, and what is behind d,
+// becomes zeros.  `any` is an address of D readable elements, or (full
+// false) of one piece.
+template <int D, int STEP>
+__device__ __forceinline__ void copy_row(uint32_t dst, const uint16_t* row, const uint16_t* any, bool live, bool full,
+                                         int q4, int d) {
+  if (full) {  // one address a row, the rest are constants
+    const uint16_t* src = live ? row : any;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) cp_async16((dst ^ ((j & 1) << 6)) + (j >> 1) * STEP, src + 32 * j, live);
+  } else {
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const bool in = live && 32 * j + 8 * q4 < d;
+      cp_async16((dst ^ ((j & 1) << 6)) + (j >> 1) * STEP, in ? row + 32 * j : any, in);
+    }
+  }
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -448,18 +468,11 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
       for (int r = 0; r < 2; ++r) {
         const bool live = x.slot[r] >= 0 && x.page[r] >= 0 && x.page[r] < p.n_pages;
         if (!live && x.slot[r] >= 0) *p.err = 1;
-        const uint16_t* k = live ? p.k + x.page[r] * p.kp[0] + x.h * p.kp[1] + x.slot[r] * p.kp[2] + 8 * q4 : p.q;
-        const uint16_t* v = live ? p.v + x.page[r] * p.vp[0] + x.h * p.vp[1] + x.slot[r] * p.vp[2] + 8 * q4 : p.q;
-#pragma unroll
-        for (int j = 0; j < DQ / 32; ++j) {
-          const bool in = live && 32 * j + 8 * q4 < p.dqk;
-          cp_async16((kd ^ ((j & 1) << 6)) + r * 8 * KPITCH + (j >> 1) * 128, in ? k + 32 * j : p.q, in);
-        }
-#pragma unroll
-        for (int j = 0; j < DV / 32; ++j) {
-          const bool in = live && 32 * j + 8 * q4 < p.dv;
-          cp_async16((vd ^ ((j & 1) << 6)) + r * 8 * VPITCH + (j >> 1) * 128, in ? v + 32 * j : p.q, in);
-        }
+        const long long page = x.page[r], slot = x.slot[r];
+        copy_row<DQ, 128>(kd + r * 8 * KPITCH, p.k + page * p.kp[0] + x.h * p.kp[1] + slot * p.kp[2] + 8 * q4,
+                          (p.full ? p.k : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dqk);
+        copy_row<DV, 128>(vd + r * 8 * VPITCH, p.v + page * p.vp[0] + x.h * p.vp[1] + slot * p.vp[2] + 8 * q4,
+                          (p.full ? p.v : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dv);
       }
     };
     load_q(cur);

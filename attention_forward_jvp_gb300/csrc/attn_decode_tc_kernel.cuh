@@ -36,6 +36,9 @@ struct DecodeTcPlan {
   static constexpr int FIT = 227 * 1024 - MISC - 1024;   // (1024: alignment)
   static constexpr int NQ = 2 * Q_TILE + 3 * TILE <= FIT ? 2 : 1;
   static constexpr int S_FIT = (FIT - NQ * Q_TILE) / TILE, S = S_FIT > 6 ? 6 : S_FIT;
+  // tiles on their way when the oldest is waited for: two of the ring's are
+  // being computed
+  static constexpr int LAG = S > 3 ? S - 3 : (S > 2 ? 1 : 0);
   static constexpr int OFF_RING = NQ * Q_TILE, OFF_MISC = OFF_RING + S * TILE;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   // barriers
@@ -159,18 +162,11 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
       for (int r = 0; r < 2; ++r) {
         const bool live = x.slot[r] >= 0 && x.page[r] >= 0 && x.page[r] < p.n_pages;
         if (!live && x.slot[r] >= 0) *p.err = 1;
-        const uint16_t* k = live ? p.k + x.page[r] * p.kp[0] + x.h * p.kp[1] + x.slot[r] * p.kp[2] + 8 * q4 : p.q;
-        const uint16_t* v = live ? p.v + x.page[r] * p.vp[0] + x.h * p.vp[1] + x.slot[r] * p.vp[2] + 8 * q4 : p.q;
-#pragma unroll
-        for (int j = 0; j < DQ / 32; ++j) {
-          const bool in = live && 32 * j + 8 * q4 < p.dqk;
-          cp_async16((kd ^ ((j & 1) << 6)) + r * 1024 + (j >> 1) * P::SUB, in ? k + 32 * j : p.q, in);
-        }
-#pragma unroll
-        for (int j = 0; j < DV / 32; ++j) {
-          const bool in = live && 32 * j + 8 * q4 < p.dv;
-          cp_async16((vd ^ ((j & 1) << 6)) + r * 1024 + (j >> 1) * P::SUB, in ? v + 32 * j : p.q, in);
-        }
+        const long long page = x.page[r], slot = x.slot[r];
+        copy_row<DQ, P::SUB>(kd + r * 1024, p.k + page * p.kp[0] + x.h * p.kp[1] + slot * p.kp[2] + 8 * q4,
+                             (p.full ? p.k : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dqk);
+        copy_row<DV, P::SUB>(vd + r * 1024, p.v + page * p.vp[0] + x.h * p.vp[1] + slot * p.vp[2] + 8 * q4,
+                             (p.full ? p.v : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dv);
       }
     };
     // the unit's heads; rows behind them, up to the quadrant's end, are zeros
@@ -209,6 +205,9 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
     Place next = lookup(cur);
     bool skip = p.skip_first_load && blockIdx.x == 0;
     for (int j = 0; ok && j < count; ++j) {
+      // LAG tiles stay on their way; those before are handed on as they land,
+      // before the copies of this one are issued
+      if (issued - signalled > P::LAG) signal_oldest();
       // the stage is free when the products of tile j - S are done
       ok = wait_all(P::B_EMPTY + j % S, ((j / S) & 1u) ^ 1u);
       if (!ok) break;
@@ -224,8 +223,6 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
       issue(next, j % S);
       cp_async_commit();
       ++issued;
-      // S - 1 tiles on their way while the oldest but those is computed
-      if (issued - signalled > S - 2) signal_oldest();
       if (skip) {  // (failure-detection hook: the first tile never arrives)
         cp_async_wait<0>();
         skip = false;
@@ -271,11 +268,21 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
       first = last;
       if (last) ++pv_seg;
     };
+    // whether barrier a completes before barrier b (or both have; or neither
+    // does in time: the wait that follows reports it)
+    auto wait_first = [&](int a, uint32_t pa, int b, uint32_t pb) {
+      const uint64_t t0 = globaltimer_ns();
+      for (;;) {
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar(a), pa))) return true;
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar(b), pb))) return false;
+        if (__any_sync(0xffffffffu, *abort_flag != 0 || globaltimer_ns() - t0 > p.timeout_ns)) return true;
+      }
+    };
     bool pending = false, last_before = false;  // O of tile i - 1
     for (int i = 0; ok && i < count; ++i) {
       const bool last = cur.t + 1 == cur.nt || i + 1 == count;
-      // S of this tile before O of the one before, unless it has not arrived
-      if (pending && !__all_sync(0xffffffffu, mbar_test_wait(bar(P::B_FULL + i % S), (i / S) & 1u))) {
+      // S of this tile before O of the one before, unless that is ready first
+      if (pending && !wait_first(P::B_FULL + i % S, (i / S) & 1u, P::B_PF + ((i - 1) & 1), ((i - 1) >> 1) & 1u)) {
         products_o(i - 1, last_before);
         pending = false;
         if (!ok) break;

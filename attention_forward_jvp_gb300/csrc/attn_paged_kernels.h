@@ -79,6 +79,7 @@ struct DecodeParams {
   int Hkv, G;                  // key heads, query heads of each
   int rows, chunks;            // query heads of a work unit, units of a key head
   int dqk, dv;                 // true head dims (<= the kernel's)
+  int full;                    // 1: they are the kernel's, and the pools hold a page
   float scale_log2;
   uint16_t* o;
   float* lse;
