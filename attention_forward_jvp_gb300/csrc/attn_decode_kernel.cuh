@@ -61,6 +61,11 @@ __device__ __forceinline__ void copy_row(uint32_t dst, const uint16_t* row, cons
     }
   }
 }
+// Arrive on `bar` when all copies that this thread has issued have landed
+// (the barrier's count includes this arrival).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {

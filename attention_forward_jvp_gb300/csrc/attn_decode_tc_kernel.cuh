@@ -36,9 +36,6 @@ struct DecodeTcPlan {
   static constexpr int FIT = 227 * 1024 - MISC - 1024;   // (1024: alignment)
   static constexpr int NQ = 2 * Q_TILE + 3 * TILE <= FIT ? 2 : 1;
   static constexpr int S_FIT = (FIT - NQ * Q_TILE) / TILE, S = S_FIT > 6 ? 6 : S_FIT;
-  // tiles on their way when the oldest is waited for: two of the ring's are
-  // being computed
-  static constexpr int LAG = S > 3 ? S - 3 : (S > 2 ? 1 : 0);
   static constexpr int OFF_RING = NQ * Q_TILE, OFF_MISC = OFF_RING + S * TILE;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   // barriers
@@ -72,7 +69,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(bar(P::B_FULL + i), 4);
+      mbar_init(bar(P::B_FULL + i), 128);
       mbar_init(bar(P::B_EMPTY + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -183,58 +180,30 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
                    in);
       }
     };
-    // The oldest tile on its way: wait for this warp's copies of it, make
-    // them visible to the tensor core, count this warp in.
-    int issued = 0, signalled = 0;
-    auto signal_oldest = [&]() {
-      switch (issued - signalled) {
-        case 1: cp_async_wait<0>(); break;
-        case 2: cp_async_wait<1>(); break;
-        case 3: cp_async_wait<2>(); break;
-        case 4: cp_async_wait<3>(); break;
-        case 5: cp_async_wait<4>(); break;
-        default: cp_async_wait<5>(); break;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(P::B_FULL + signalled % S));
-      ++signalled;
-    };
     bool ok = true;
     int seg = 0;  // (cur: the tile issued next)
     Place next = lookup(cur);
-    bool skip = p.skip_first_load && blockIdx.x == 0;
     for (int j = 0; ok && j < count; ++j) {
-      // LAG tiles stay on their way; those before are handed on as they land,
-      // before the copies of this one are issued
-      if (issued - signalled > P::LAG) signal_oldest();
       // the stage is free when the products of tile j - S are done
       ok = wait_all(P::B_EMPTY + j % S, ((j / S) & 1u) ^ 1u);
       if (!ok) break;
       if (j == 0 || cur.t == 0) {
         if (j > 0) ++seg;
-        // (tiles of the unit before may still wait for this warp's signal)
-        if (seg >= NQ)
-          while (signalled < issued) signal_oldest();
         ok = wait_all(P::B_QE + seg % NQ, ((seg / NQ) & 1u) ^ 1u);
         if (!ok) break;
         issue_q(cur, seg % NQ);
       }
       issue(next, j % S);
-      cp_async_commit();
-      ++issued;
-      if (skip) {  // (failure-detection hook: the first tile never arrives)
-        cp_async_wait<0>();
-        skip = false;
-        signalled = issued;
-      }
+      // counts this thread in when its copies so far have landed; the warp
+      // that issues the products makes them visible to the tensor core
+      // (the failure-detection hook: the first tile never arrives)
+      if (j > 0 || !p.skip_first_load || blockIdx.x != 0) cp_async_arrive(bar(P::B_FULL + j % S));
       if (j + 1 < count) {
         advance(cur);
         next = lookup(cur);
       }
     }
-    if (ok)
-      while (signalled < issued) signal_oldest();
+    cp_async_commit();
     cp_async_wait<0>();
   } else if (warp == 12 && count > 0) {
     // -------------------------------------------------------------- products
@@ -289,6 +258,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
       }
       ok = wait_all(P::B_FULL + i % S, (i / S) & 1u);
       if (!ok) break;
+      fence_proxy_async_smem();  // the copies, made by the generic proxy, before the products read them
       tc_fence_after();
       if (leader) {
         const uint32_t q = lo_q + (seg % NQ) * (P::Q_TILE >> 4), k = lo_k + (i % S) * (P::TILE >> 4);
