@@ -207,78 +207,83 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
     cp_async_wait<0>();
   } else if (warp == 12 && count > 0) {
     // -------------------------------------------------------------- products
-    const bool leader = elect_one();
-    constexpr uint32_t idesc_s = idesc_16(kTcRows, BN, false, F16), idesc_o = idesc_16(kTcRows, DV, true, F16);
-    constexpr uint32_t kHi = sdesc_hi_sw128(1024);
-    const uint32_t lo_q = sdesc_lo(base, 16), lo_k = sdesc_lo(base + P::OFF_RING, 16);
-    const uint32_t lo_v = sdesc_lo(base + P::OFF_RING + P::K_TILE, P::SUB);
-    bool ok = true;
-    int seg = 0, pv_seg = 0;
-    bool first = true;  // of its unit in this CTA: the tile whose O is next
-    // O of tile j, the last of its unit or not
-    auto products_o = [&](int j, bool last) {
-      ok = wait_all(P::B_PF + (j & 1), (j >> 1) & 1u);
-      // the first product of a unit overwrites O: the unit before has left it
-      if (ok && first) ok = wait_all(P::B_OE, (pv_seg & 1u) ^ 1u);
-      if (!ok) return;
-      tc_fence_after();
-      if (leader) {
-        const uint32_t a = tmem + P::COL_P + (j & 1) * 64, v = lo_v + (j % S) * (P::TILE >> 4);
+    // One lane alone: its waits and issues are the longest chain of a tile,
+    // and votes between them would lengthen it.
+    if (elect_one()) {
+      constexpr uint32_t idesc_s = idesc_16(kTcRows, BN, false, F16), idesc_o = idesc_16(kTcRows, DV, true, F16);
+      constexpr uint32_t kHi = sdesc_hi_sw128(1024);
+      const uint32_t lo_q = sdesc_lo(base, 16), lo_k = sdesc_lo(base + P::OFF_RING, 16);
+      const uint32_t lo_v = sdesc_lo(base + P::OFF_RING + P::K_TILE, P::SUB);
+      bool ok = true;
+      int seg = 0, pv_seg = 0;
+      bool first = true;                       // of its unit in this CTA: the tile whose O is next
+      int stage_s = 0, stage_o = 0;            // stages of the tiles whose S and O are next
+      uint32_t phase_s = 0;
+      // O of tile j, the last of its unit or not
+      auto products_o = [&](int j, bool last) {
+        ok = wait_bar(bar(P::B_PF + (j & 1)), (j >> 1) & 1u, W);
+        // the first product of a unit overwrites O: the unit before has left it
+        if (ok && first) ok = wait_bar(bar(P::B_OE), (pv_seg & 1u) ^ 1u, W);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t a = tmem + P::COL_P + (j & 1) * 64, v = lo_v + stage_o * (P::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk) {
           const uint64_t d = sdesc_join(v + ((kk * 2048) >> 4), kHi);
           mma_ts(tmem + P::COL_O, a + 8 * kk, d, idesc_o, first && kk == 0 ? 0u : 1u);
           mma_ts(tmem + P::COL_O, a + 32 + 8 * kk, d, idesc_o, 1u);
         }
-        tc_commit(bar(P::B_EMPTY + j % S));
+        tc_commit(bar(P::B_EMPTY + stage_o));
         if (last) tc_commit(bar(P::B_OF));
-      }
-      __syncwarp();
-      first = last;
-      if (last) ++pv_seg;
-    };
-    // whether barrier a completes before barrier b (or both have; or neither
-    // does in time: the wait that follows reports it)
-    auto wait_first = [&](int a, uint32_t pa, int b, uint32_t pb) {
-      const uint64_t t0 = globaltimer_ns();
-      for (;;) {
-        if (__all_sync(0xffffffffu, mbar_test_wait(bar(a), pa))) return true;
-        if (__all_sync(0xffffffffu, mbar_test_wait(bar(b), pb))) return false;
-        if (__any_sync(0xffffffffu, *abort_flag != 0 || globaltimer_ns() - t0 > p.timeout_ns)) return true;
-      }
-    };
-    bool pending = false, last_before = false;  // O of tile i - 1
-    for (int i = 0; ok && i < count; ++i) {
-      const bool last = cur.t + 1 == cur.nt || i + 1 == count;
-      // S of this tile before O of the one before, unless that is ready first
-      if (pending && !wait_first(P::B_FULL + i % S, (i / S) & 1u, P::B_PF + ((i - 1) & 1), ((i - 1) >> 1) & 1u)) {
-        products_o(i - 1, last_before);
-        pending = false;
+        first = last;
+        pv_seg += last ? 1 : 0;
+        stage_o = stage_o + 1 == S ? 0 : stage_o + 1;
+      };
+      // whether barrier a completes before barrier b (or both have; or
+      // neither does in time: the wait that follows reports it)
+      auto wait_first = [&](uint32_t a, uint32_t pa, uint32_t b, uint32_t pb) {
+        if (mbar_test_wait(a, pa)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        for (;;) {
+          if (mbar_test_wait(b, pb)) return false;
+          if (mbar_test_wait(a, pa)) return true;
+          if (*abort_flag != 0 || globaltimer_ns() - t0 > p.timeout_ns) return true;
+        }
+      };
+      bool pending = false, last_before = false;  // O of tile i - 1
+      for (int i = 0; ok && i < count; ++i) {
+        const bool last = cur.t + 1 == cur.nt || i + 1 == count;
+        // S of this tile before O of the one before, unless that is ready first
+        if (pending && !wait_first(bar(P::B_FULL + stage_s), phase_s, bar(P::B_PF + ((i - 1) & 1)), ((i - 1) >> 1) & 1u)) {
+          products_o(i - 1, last_before);
+          pending = false;
+          if (!ok) break;
+        }
+        ok = wait_bar(bar(P::B_FULL + stage_s), phase_s, W);
         if (!ok) break;
-      }
-      ok = wait_all(P::B_FULL + i % S, (i / S) & 1u);
-      if (!ok) break;
-      fence_proxy_async_smem();  // the copies, made by the generic proxy, before the products read them
-      tc_fence_after();
-      if (leader) {
-        const uint32_t q = lo_q + (seg % NQ) * (P::Q_TILE >> 4), k = lo_k + (i % S) * (P::TILE >> 4);
+        fence_proxy_async_smem();  // the copies, made by the generic proxy, before the products read them
+        tc_fence_after();
+        const uint32_t q = lo_q + (seg % NQ) * (P::Q_TILE >> 4), k = lo_k + stage_s * (P::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < DQ / 16; ++kk) {
           const uint32_t oq = ((kk >> 2) * P::Q_SUB + (kk & 3) * 32) >> 4, ok_ = ((kk >> 2) * P::SUB + (kk & 3) * 32) >> 4;
           mma_ss(tmem + (i & 1) * BN, sdesc_join(q + oq, kHi), sdesc_join(k + ok_, kHi), idesc_s, kk > 0 ? 1u : 0u);
         }
         tc_commit(bar(P::B_SF + (i & 1)));
-        if (last) tc_commit(bar(P::B_QE + seg % NQ));
+        if (last) {
+          tc_commit(bar(P::B_QE + seg % NQ));
+          ++seg;
+        }
+        if (++stage_s == S) {
+          stage_s = 0;
+          phase_s ^= 1u;
+        }
+        if (pending) products_o(i - 1, last_before);
+        pending = true;
+        last_before = last;
+        if (i + 1 < count) advance(cur);
       }
-      __syncwarp();
-      if (last) ++seg;
-      if (pending) products_o(i - 1, last_before);
-      pending = true;
-      last_before = last;
-      if (i + 1 < count) advance(cur);
-    }
-    if (ok && pending) products_o(count - 1, last_before);
-    if (leader) {
+      if (ok && pending) products_o(count - 1, last_before);
       tc_commit(bar(P::B_DRAIN));
       drain_bar(bar(P::B_DRAIN), 0, p.timeout_ns);
     }
