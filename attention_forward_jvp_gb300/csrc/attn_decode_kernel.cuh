@@ -25,12 +25,12 @@
 // one list, cut into equal ranges, one for each resident warp, whatever the
 // lengths.  A warp walks its range alone, unit after unit, with a ring of its
 // own in shared memory that it fills by 16-byte asynchronous copies, row by
-// row through the page table: no block-wide barrier until the end.  A unit
-// that lies within one warp is finished there; the warps of a CTA that lies
-// within one unit join their parts in shared memory; parts of the others go
-// to the workspace and attn_decode_join joins them, in order.  Rows behind
-// the sequence's end are filled with zeros, so that whatever a page holds
-// there never enters a product.
+// row through the page table: no block-wide barrier until the end, where the
+// warps of a CTA join what they hold of one unit in shared memory.  A unit
+// that lies within a warp, or within what a CTA joins, is finished there;
+// parts of the others go to the workspace and attn_decode_join joins them, in
+// order.  Rows behind the sequence's end are filled with zeros, so that
+// whatever a page holds there never enters a product.
 #pragma once
 #include "attn_paged_kernels.h"
 #include "ptx.cuh"
@@ -270,15 +270,17 @@ static __device__ __noinline__ void decode_idle(const DecodeParams& p) {
   }
 }
 
-// What joins a unit that begins in range x (of R to a CTA) and has its last
-// step at `end`: the parts of x's CTA from x on (`here` of them), one for each
-// CTA that lies within the unit, and those of the CTA where it ends.
+// Where the parts of a unit are that begins in range x (of R to a CTA) and
+// has its last step at `end`, in another range: in x's part 1; in part 0 of
+// the first range of each CTA behind, that of the end included (z: how many
+// CTAs lie between, -1 when the unit ends in x's own); and, where the range
+// that it ends in goes on to another unit and is not that first one, in part
+// 0 of that (w, else -1).
 template <int R>
-__device__ __forceinline__ int4 decode_describe(const DecodeRange& w, int b, int hu, int x, int here, long long end) {
+__device__ __forceinline__ int4 decode_describe(const DecodeRange& w, int b, int hu, int x, long long end) {
   const int z = static_cast<int>(w.owner(end)), c = x / R, e = z / R;
-  if (e == c) return make_int4(b, hu, z - x + 1, 0);
-  const bool joined = w.start((e + 1LL) * R) == end + 1;  // CTA e lies within the unit too
-  return make_int4(b, hu, here | (joined ? 1 : z - e * R + 1) << 8, e - c - 1);
+  const bool own = w.start(z + 1LL) != end + 1 && (e == c || z != e * R);
+  return make_int4(b, hu, e - c - 1, own ? z : -1);
 }
 
 // Shared memory and registers of a warp decide how many fit on an SM: three
@@ -293,12 +295,13 @@ struct DecodePlan {
   static constexpr int ACC_REGS = DV / 4 * NT, Q_REGS = DQ / 8 * NT;
   static constexpr bool QREG = ACC_REGS + Q_REGS <= 176;
   static constexpr int Q_BYTES = QREG ? 0 : DQ / 16 * NT * 256;
-  static constexpr int MISC_BYTES = 4608;  // words of the planning: 8 bytes a thread, 16 a warp
+  // words of the planning (8 bytes a thread, 16 a warp) and of the joining (a range and 24 a warp)
+  static constexpr int MISC_BYTES = (8 * 32 + 16 + 24 + sizeof(DecodeRange)) * kDecodeMaxWarps;
   static constexpr int FIT = 226 * 1024 - MISC_BYTES;
   static constexpr int S = FIT / (3 * STAGE + Q_BYTES) >= 6 ? 3 : 2;
   static constexpr int WARP_BYTES = S * STAGE + Q_BYTES;
   static constexpr int REGS = ACC_REGS + (QREG ? Q_REGS : 0) + 72;
-  static constexpr int NW_REGS = REGS <= 128 ? 16 : (REGS <= 168 ? 12 : 8);
+  static constexpr int NW_REGS = REGS <= 128 ? 16 : (REGS <= 160 ? 12 : 8);  // 128, 168, 255 registers a thread
   static constexpr int NW_SMEM = FIT / WARP_BYTES;
   static constexpr int NW = NW_SMEM < NW_REGS ? NW_SMEM : NW_REGS;
   static_assert(NW <= kDecodeMaxWarps, "decode plan");
@@ -323,6 +326,11 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   char* misc = smem + NW * P::WARP_BYTES;
   const DecodeWords words{reinterpret_cast<int*>(misc), reinterpret_cast<uint32_t*>(misc) + THREADS,
                           reinterpret_cast<long long*>(misc + 8 * THREADS)};
+  // of each warp at its end: its last unit, whether it begins there, whether
+  // it goes on from the warp before; the unit's last step
+  DecodeRange* ranges = reinterpret_cast<DecodeRange*>(misc + P::MISC_BYTES - (24 + sizeof(DecodeRange)) * kDecodeMaxWarps);
+  int4* held = reinterpret_cast<int4*>(misc + P::MISC_BYTES - 24 * kDecodeMaxWarps);
+  long long* held_end = reinterpret_cast<long long*>(misc + P::MISC_BYTES - 8 * kDecodeMaxWarps);
   const int HU = p.Hkv * p.chunks;  // units of a sequence
 
   griddep_wait();
@@ -376,7 +384,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   // at once
   const int first = blockIdx.x * NW;  // this CTA's first warp
   const int me = first + warp;
-  const DecodeRange w = p.wide ? decode_plan<long long, BN, NW, true>(p, words) : decode_plan<int, BN, NW, true>(p, words);
+  DecodeRange w = p.wide ? decode_plan<long long, BN, NW, true>(p, words) : decode_plan<int, BN, NW, true>(p, words);
   const int count = w.count;
   Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len};  // the step computed next
   Cursor ahead = cur;                                  // the step that `next` is of
@@ -389,21 +397,15 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     }
   }
 
-  auto describe = [&](int b, int hu, int x, int here, long long end) {
-    return decode_describe<NW>(w, b, hu, x, here, end);
-  };
-
   if (w.idle) decode_idle(p);
   if (p.split && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
   if (w.cta_lo >= w.total) return;
+  // (kept in shared memory while the steps need the registers)
+  if (lane == 0) ranges[warp] = w;
 
   float acc[NT][DV / 16][4];
   float m[NT][2], l[NT][2];  // heads 2 q4, 2 q4 + 1 of each group
   uint32_t qr[P::QREG ? DQ / 16 : 1][NT][2];
-  // does the whole CTA lie within one unit?  (a warp without steps has the
-  // place of the CTA's first step)
-  const long long unit_lo = w.lo - w.t;
-  const bool same_unit = unit_lo <= w.cta_lo && w.cta_hi <= unit_lo + cur.nt;
   auto clear = [&]() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
       // ---- the unit ends here, or the range does
       const bool last = i + 1 == count;
       if (cur.t + 1 == cur.nt || last) {
-        const bool begins = t0 == 0, ends = cur.t + 1 == cur.nt;
+        const bool begins = t0 == 0;
         const int h = cur.hu / p.chunks, g0 = (cur.hu - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -600,8 +602,8 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
             l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
             l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
           }
-        if (!same_unit) {
-          const long long part = 2LL * me + (begins ? 1 : 0);
+        if (!last) {  // (the range's last unit is joined with the other warps' below; this one ends here)
+          const long long part = 2LL * me;
           const long long row0 = (static_cast<long long>(cur.b) * p.Hkv + h) * p.G + g0;
           float* scratch = reinterpret_cast<float*>(mine + stage * P::STAGE);  // read; refilled in the next step
 #pragma unroll
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
               const float4 o = *reinterpret_cast<const float4*>(scratch + r * PITCH + 4 * c4);
               const int row = 8 * n + r;
               if (row < n_rows) {
-                if (begins && ends) {
+                if (begins) {
                   write_row(row0 + row, 4 * c4, o, mm, ll);
                 } else {
                   *reinterpret_cast<float4*>(p.part_o + (part * p.rows + row) * DV + 4 * c4) = o;
@@ -627,9 +629,15 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
               }
             }
           }
-          if (begins && !ends && lane == 0) p.desc[me] = describe(cur.b, cur.hu, me, NW - warp, w.lo + i + (cur.nt - 1 - cur.t));
         }
-        if (!last) {
+        if (last) {
+          if (lane == 0) {
+            // goes on where the warp before has left off?
+            const bool goes_on = warp > 0 && i == cur.t - t0 && t0 > 0;
+            held[warp] = make_int4(cur.b, cur.hu, begins ? 1 : 0, goes_on ? 1 : 0);
+            held_end[warp] = ranges[warp].lo + i + (cur.nt - 1 - cur.t);
+          }
+        } else {
           clear();
           advance(cur);
           t0 = 0;
@@ -642,41 +650,52 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     }
   }
 
-  // ---- a CTA within one unit: its warps' parts joined here
-  if (!same_unit) return;
-  float* parts = reinterpret_cast<float*>(mine);
-  cp_async_wait<0>();
-  // statistics of every warp and head, behind its spilled O
+  // ---- what the warps hold of their last units: joined, written
   constexpr int ROWS = NT * 8;
-  float2* my_ml = reinterpret_cast<float2*>(parts + ROWS * PITCH);
+  float* parts = reinterpret_cast<float*>(mine);
+  float2* my_ml = reinterpret_cast<float2*>(parts + ROWS * PITCH);  // behind O
+  cp_async_wait<0>();
   __syncwarp();
+  if (count > 0) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    spill(parts + 8 * n * PITCH, n, 1.f, 1.f);
-    if (g == 0) {
-      my_ml[8 * n + 2 * q4] = make_float2(m[n][0], l[n][0]);
-      my_ml[8 * n + 2 * q4 + 1] = make_float2(m[n][1], l[n][1]);
+    for (int n = 0; n < NT; ++n) {
+      spill(parts + 8 * n * PITCH, n, 1.f, 1.f);
+      if (g == 0) {
+        my_ml[8 * n + 2 * q4] = make_float2(m[n][0], l[n][0]);
+        my_ml[8 * n + 2 * q4 + 1] = make_float2(m[n][1], l[n][1]);
+      }
     }
   }
   __syncthreads();
-  const int nt = steps_of(w.len);
-  const bool begins = unit_lo == w.cta_lo, ends = w.cta_hi == unit_lo + nt;
-  const int h = w.hu / p.chunks, g0 = (w.hu - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
-  const long long part = 2LL * first + (begins ? 1 : 0);
-  const long long row0 = (static_cast<long long>(w.b) * p.Hkv + h) * p.G + g0;
-  for (int y = tid; y < n_rows * (DV / 4); y += THREADS) {
-    const int r = y / (DV / 4), c4 = y % (DV / 4);
+  w = ranges[warp];
+  // groups of warps with parts of one unit, by their first warps
+  const int used = static_cast<int>(min(static_cast<long long>(NW), w.ranges - first));  // warps with steps
+  const unsigned leads = __ballot_sync(0xffffffffu, lane < used && held[lane < used ? lane : 0].w == 0);
+  const int items = p.rows * (DV / 4);
+#pragma unroll 1
+  for (int y = tid; y < __popc(leads) * items; y += THREADS) {
+    const int gi = y / items, r = (y - gi * items) / (DV / 4), c4 = y % (DV / 4);
+    unsigned left = leads;
+    for (int k = 0; k < gi; ++k) left &= left - 1;
+    const int w0 = __ffs(left) - 1;
+    left &= left - 1;
+    const int w1 = left ? __ffs(left) - 1 : used;
+    const int4 u = held[w0];
+    const long long end = held_end[w0];  // the unit's last step
+    const bool begins = u.z != 0, ends = end < w.start(first + w1);
+    const int h = p.chunks == 1 ? u.y : u.y / p.chunks, g0 = (u.y - h * p.chunks) * p.rows;
+    if (r >= min(p.rows, p.G - g0)) continue;
+    const long long part = 2LL * (first + w0) + (begins ? 1 : 0);
     float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-    for (int x = 0; x < NW; ++x)
+    for (int x = w0; x < w1; ++x)
       mm = fmaxf(mm, reinterpret_cast<const float2*>(smem + x * P::WARP_BYTES + ROWS * PITCH * 4)[r].x);
-    const float u = mm == -INFINITY ? 0.f : mm;
+    const float top = mm == -INFINITY ? 0.f : mm;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int x = 0; x < NW; ++x) {
+#pragma unroll 4
+    for (int x = w0; x < w1; ++x) {
       const char* from = smem + x * P::WARP_BYTES;
       const float2 s = reinterpret_cast<const float2*>(from + ROWS * PITCH * 4)[r];
-      const float f = exp2_fast(s.x - u);
+      const float f = exp2_fast(s.x - top);
       const float4 z = *reinterpret_cast<const float4*>(from + (r * PITCH + 4 * c4) * 4);
       ll = fmaf(f, s.y, ll);
       o.x = fmaf(f, z.x, o.x);
@@ -685,13 +704,13 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
       o.w = fmaf(f, z.w, o.w);
     }
     if (begins && ends) {
-      write_row(row0 + r, 4 * c4, o, mm, ll);
+      write_row((static_cast<long long>(u.x) * p.Hkv + h) * p.G + g0 + r, 4 * c4, o, mm, ll);
     } else {
       *reinterpret_cast<float4*>(p.part_o + (part * p.rows + r) * DV + 4 * c4) = o;
       if (c4 == 0) p.part_ml[part * p.rows + r] = make_float2(mm, ll);
+      if (r == 0 && c4 == 0 && begins) p.desc[first + w0] = decode_describe<NW>(w, u.x, u.y, first + w0, end);
     }
   }
-  if (begins && !ends && tid == 0) p.desc[first] = describe(w.b, w.hu, first, 1, unit_lo + nt - 1);
 }
 
 // Joins the parts of the units that several warps of the kernel above share:
@@ -737,11 +756,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
     const int4 d = units[u];
     const int h = p.chunks == 1 ? d.y : d.y / p.chunks, g0 = (d.y - h * p.chunks) * p.rows;
     on = on && g0 + r < p.G;  // (the last units of a key head may have fewer)
-    // parts: here, one of each CTA between, there
-    const int here = d.z & 255, parts = here + d.w + (d.z >> 8);
+    // parts, in order (decode_describe)
+    const int parts = d.z + 2 + (d.w >= 0 ? 1 : 0);
     auto row_of = [&](int i) {
-      const int j = i - here;
-      const int w = j < 0 ? from[u] + i : (blockIdx.x + 1 + min(j, d.w)) * cw + max(j - d.w, 0);
+      const int w = i == 0 ? from[u] : (i <= d.z + 1 ? (blockIdx.x + i) * cw : d.w);
       return (2 * w + (i == 0 ? 1 : 0)) * p.rows + r;
     };
     float m = -INFINITY, l = 0.f, acc[VPL];

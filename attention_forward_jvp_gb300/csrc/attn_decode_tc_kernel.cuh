@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
           else p.part_ml[part] = make_float2(m, sum);
         }
         if (begins && !ends && tid == 0)
-          p.desc[blockIdx.x] = decode_describe<1>(w, cur.b, cur.hu, blockIdx.x, 1, w.lo + i + (cur.nt - 1 - cur.t));
+          p.desc[blockIdx.x] = decode_describe<1>(w, cur.b, cur.hu, blockIdx.x, w.lo + i + (cur.nt - 1 - cur.t));
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(P::B_OE));
