@@ -283,10 +283,11 @@ __device__ __forceinline__ int4 decode_describe(const DecodeRange& w, int b, int
   return make_int4(b, hu, e - c - 1, own ? z : -1);
 }
 
-// Shared memory and registers of a warp decide how many fit on an SM: three
-// stages of 16 keys where that leaves six warps or more (two thirds of the
-// ring in flight while a stage is read), else two; Q in registers unless it
-// and the accumulators would pass 176.
+// Eight warps with as many stages of 16 keys as shared memory holds (up to
+// four), or four where it holds less than two, or more warps of a small head
+// dim: a multiple of four always, since nine warps, three on one of the SM's
+// four parts, were slower than eight (D 128: 198 us for 186).  Q stays in
+// registers unless it and the accumulators would pass 176.
 template <int DQ, int DV, int NT>
 struct DecodePlan {
   static constexpr int BN = kDecodeBN;
@@ -298,17 +299,18 @@ struct DecodePlan {
   // words of the planning (8 bytes a thread, 16 a warp) and of the joining (a range and 24 a warp)
   static constexpr int MISC_BYTES = (8 * 32 + 16 + 24 + sizeof(DecodeRange)) * kDecodeMaxWarps;
   static constexpr int FIT = 226 * 1024 - MISC_BYTES;
-  static constexpr int S = FIT / (3 * STAGE + Q_BYTES) >= 6 ? 3 : 2;
+  static constexpr int S8 = (FIT / 8 - Q_BYTES) / STAGE, S4 = (FIT / 4 - Q_BYTES) / STAGE;
+  static constexpr int S = S8 >= 2 ? (STAGE <= 4096 ? 3 : (S8 > 4 ? 4 : S8)) : S4;
   static constexpr int WARP_BYTES = S * STAGE + Q_BYTES;
   static constexpr int REGS = ACC_REGS + (QREG ? Q_REGS : 0) + 72;
   static constexpr int NW_REGS = REGS <= 128 ? 16 : (REGS <= 160 ? 12 : 8);  // 128, 168, 255 registers a thread
   static constexpr int NW_SMEM = FIT / WARP_BYTES;
-  static constexpr int NW = NW_SMEM < NW_REGS ? NW_SMEM : NW_REGS;
+  static constexpr int NW = (NW_SMEM < NW_REGS ? NW_SMEM : NW_REGS) / 4 * 4;
   static_assert(NW <= kDecodeMaxWarps, "decode plan");
   static constexpr int SMEM = NW * WARP_BYTES + MISC_BYTES;
   // O of 8 heads on its way out, rows padded against bank conflicts
   static constexpr int PITCH = DV + 4;
-  static_assert(NW >= 4 && 8 * PITCH * 4 <= STAGE && NT * 8 * (PITCH * 4 + 8) <= S * STAGE, "decode plan");
+  static_assert(NW >= 4 && S >= 2 && 8 * PITCH * 4 <= STAGE && NT * 8 * (PITCH * 4 + 8) <= S * STAGE, "decode plan");
 };
 
 template <int DQ, int DV, bool F16, int NT>

@@ -14,8 +14,8 @@
 // Warps 0-7 are the softmax: two to a quadrant of 32 lanes (32 heads), each
 // with half of a tile's columns; quadrants behind the last head do nothing.
 // Warps 8-11 bring tiles (16 keys each) by 16-byte asynchronous copies, row
-// by row through the page table, and signal each tile when its copies have
-// landed.  Warp 12 issues the products: S of tile i + 1 before O of tile i.
+// by row through the page table; a tile's barrier counts the copies in as they
+// land.  Warp 12 issues the products: S of tile i + 1 before O of tile i.
 // S and P have two buffers each in tensor memory.  P is split into two
 // 16-bit parts there, like the warps' P of the other kernel.
 #pragma once
@@ -446,7 +446,8 @@ cudaError_t launch_decode_tc(DecodeParams& p, int ctas, cudaStream_t stream) {
 template <int DQ, int DV, bool F16>
 cudaError_t launch_decode(DecodeParams& p, int nt, int ctas, cudaStream_t stream) {
   if (nt == 1) return launch_decode_nt<DQ, DV, F16, 1>(p, ctas, stream);
-  if (nt == 2) return launch_decode_nt<DQ, DV, F16, 2>(p, ctas, stream);
+  if constexpr (decode_warp_rows(DQ, DV) > 8)
+    if (nt == 2) return launch_decode_nt<DQ, DV, F16, 2>(p, ctas, stream);
   return launch_decode_tc<DQ, DV, F16>(p, ctas, stream);
 }
 

@@ -247,7 +247,7 @@ Layout layout_of(const attn_paged_cache* c, int Hq, int sms) {
   const int G = Hq / c->Hkv;
   l.chunks = (G + kDecodeMaxRows - 1) / kDecodeMaxRows;
   l.rows = (G + l.chunks - 1) / l.chunks;
-  l.nt = l.rows > kDecodeWarpRows ? 0 : (l.rows + 7) / 8;
+  l.nt = l.rows > decode_warp_rows(l.dq, l.dv) ? 0 : (l.rows + 7) / 8;
   l.ctas = sms;
   const size_t warps = static_cast<size_t>(sms) * (l.nt == 0 ? 1 : kDecodeMaxWarps);  // ranges
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
