@@ -13,6 +13,11 @@
 //
 // Warps 0-7 are the softmax: two to a quadrant of 32 lanes (32 heads), each
 // with half of a tile's columns; quadrants behind the last head do nothing.
+// Up to 64 heads stand twice in Q, as rows 0-63 and 64-127: the first two
+// quadrants take the even tiles and the others the odd ones (the rows of P
+// that are not a quadrant's stay zero), each with a running maximum, sum and
+// O of its own, joined at the unit's end.  That halves what bounds the kernel
+// otherwise, a tile's softmax (1400 of its 1800 cycles at D 128).
 // Warps 8-11 bring tiles (16 keys each) by 16-byte asynchronous copies, row
 // by row through the page table; a tile's barrier counts the copies in as they
 // land.  Warp 12 issues the products: S of tile i + 1 before O of tile i.
@@ -32,7 +37,10 @@ struct DecodeTcPlan {
   static constexpr int SUB = kTcBN * 128;                // 64 columns of a tile
   static constexpr int K_TILE = DQ / 64 * SUB, TILE = K_TILE + DV / 64 * SUB;
   static constexpr int Q_SUB = kTcRows * 128, Q_TILE = DQ / 64 * Q_SUB;
-  static constexpr int MISC = 8 * THREADS + 2 * 8 * 16 + 2 * 2 * kTcRows * 4 + 256;
+  // words of the planning, sums and maxima of two units, O on its way from
+  // the odd tiles' rows to the even ones' (16 columns of each half), barriers
+  static constexpr int SUMS = 2 * 3 * kTcRows * 4, SWAP = 2 * 64 * 16 * 4;
+  static constexpr int MISC = 8 * THREADS + 2 * 8 * 16 + SUMS + SWAP + 256;
   static constexpr int FIT = 227 * 1024 - MISC - 1024;   // (1024: alignment)
   static constexpr int NQ = 2 * Q_TILE + 3 * TILE <= FIT ? 2 : 1;
   static constexpr int S_FIT = (FIT - NQ * Q_TILE) / TILE, S = S_FIT > 6 ? 6 : S_FIT;
@@ -40,7 +48,7 @@ struct DecodeTcPlan {
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   // barriers
   static constexpr int B_FULL = 0, B_EMPTY = S, B_SF = 2 * S, B_PF = 2 * S + 2, B_QE = 2 * S + 4, B_OF = 2 * S + 6,
-                       B_OE = 2 * S + 7, B_LS = 2 * S + 8, B_DRAIN = 2 * S + 9, NBAR = 2 * S + 10;
+                       B_OE = 2 * S + 7, B_LS = 2 * S + 8, B_XF = 2 * S + 9, B_XE = 2 * S + 10, B_DRAIN = 2 * S + 11, NBAR = 2 * S + 12;
   // tensor memory columns: S, S, P, P (upper | lower parts), O
   static constexpr int COL_P = 128, COL_O = 256, TMEM = 512;
   static_assert(S >= 2 && NBAR * 8 <= 200, "decode plan");
@@ -57,7 +65,8 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
   char* misc = smem + P::OFF_MISC;
   const DecodeWords words{reinterpret_cast<int*>(misc), reinterpret_cast<uint32_t*>(misc) + P::THREADS,
                           reinterpret_cast<long long*>(misc + 8 * P::THREADS)};
-  float* lsum = reinterpret_cast<float*>(misc + 8 * P::THREADS + 2 * 8 * 16);  // [2 units][2 halves][row]
+  float* sums = reinterpret_cast<float*>(misc + 8 * P::THREADS + 2 * 8 * 16);  // [2 units][l, l, m][row]
+  float* swap = sums + P::SUMS / 4;                                            // [2 halves][16 columns][row]
   char* ctl = misc + P::MISC - 256;
   const uint32_t bar0 = smem_u32(ctl);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(ctl + 208);
@@ -66,6 +75,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int HU = p.Hkv * p.chunks;
   const int quads = (p.rows + 31) / 32;  // quadrants with heads
+  const int copies = quads <= 2 ? 2 : 1;
 
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
@@ -78,8 +88,10 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
       mbar_init(bar(P::B_QE + i), 1);
     }
     mbar_init(bar(P::B_OF), 1);
-    mbar_init(bar(P::B_OE), 2 * quads);
-    mbar_init(bar(P::B_LS), 64 * quads);
+    mbar_init(bar(P::B_OE), 2 * quads * copies);
+    mbar_init(bar(P::B_LS), 64 * quads * copies);
+    mbar_init(bar(P::B_XF), 64 * quads);
+    mbar_init(bar(P::B_XE), 64 * quads);
     mbar_init(bar(P::B_DRAIN), 1);
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -97,6 +109,18 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int count = w.count;
+  if (copies == 2) {
+    // each quadrant's rows of the other parity's P, which stay zero
+    if (warp < 8) {
+      const uint32_t z[32] = {};
+      tmem_st_32x32b_x32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + P::COL_P +
+                             ((warp & 2) ? 0 : 64) + (warp >> 2) * 32, z);
+      tmem_wait_st();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
   if (w.idle) decode_idle(p);
   if (p.split && tid == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
@@ -133,12 +157,22 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
   if (warp >= 8 && warp < 12 && count > 0) {
     // ------------------------------------------------------------ producers
     const int g = lane >> 2, q4 = lane & 3, k0 = (warp - 8) * 16;
+    // pages of 16 tokens and more, a power of two of them: the two rows of a
+    // lane, 8 tokens apart, lie in one page
+    const bool one_page = p.page_shift >= 4;
+    const uint16_t *kh = nullptr, *vh = nullptr;  // of the unit: its head's rows, piece q4
+    const int* pages = nullptr;                   // of the sequence
     struct Place {
-      int page[2], slot[2], h;
+      int page[2], slot[2];
+    };
+    auto enter = [&](const Cursor& a) {
+      const int h = p.chunks == 1 ? a.hu : a.hu / p.chunks;
+      kh = p.k + h * p.kp[1] + 8 * q4;
+      vh = p.v + h * p.vp[1] + 8 * q4;
+      pages = p.page_table + a.b * p.table_stride;
     };
     auto lookup = [&](const Cursor& a) -> Place {
       Place x;
-      x.h = p.chunks == 1 ? a.hu : a.hu / p.chunks;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int key = a.t * BN + k0 + g + 8 * r;
@@ -147,23 +181,29 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
         if (key < a.len) {
           const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
           x.slot[r] = key - e * p.page_size;
-          x.page[r] = p.page_table[a.b * p.table_stride + e];
+          x.page[r] = r == 1 && one_page ? x.page[0] : pages[e];
         }
       }
       return x;
     };
-    auto issue = [&](const Place& x, int stage) {
+    auto issue = [&](const Place& x, const uint16_t* kh, const uint16_t* vh, int stage) {
       const uint32_t kd = base + P::OFF_RING + stage * P::TILE + (k0 + g) * 128 + ((q4 ^ g) << 4);
       const uint32_t vd = kd + P::K_TILE;
+      const uint16_t *k = nullptr, *v = nullptr;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const bool live = x.slot[r] >= 0 && x.page[r] >= 0 && x.page[r] < p.n_pages;
         if (!live && x.slot[r] >= 0) *p.err = 1;
-        const long long page = x.page[r], slot = x.slot[r];
-        copy_row<DQ, P::SUB>(kd + r * 1024, p.k + page * p.kp[0] + x.h * p.kp[1] + slot * p.kp[2] + 8 * q4,
-                             (p.full ? p.k : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dqk);
-        copy_row<DV, P::SUB>(vd + r * 1024, p.v + page * p.vp[0] + x.h * p.vp[1] + slot * p.vp[2] + 8 * q4,
-                             (p.full ? p.v : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dv);
+        if (r == 1 && one_page) {
+          k += 8 * p.kp[2];
+          v += 8 * p.vp[2];
+        } else {
+          const long long page = x.page[r], slot = x.slot[r];
+          k = kh + page * p.kp[0] + slot * p.kp[2];
+          v = vh + page * p.vp[0] + slot * p.vp[2];
+        }
+        copy_row<DQ, P::SUB>(kd + r * 1024, k, (p.full ? p.k : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dqk);
+        copy_row<DV, P::SUB>(vd + r * 1024, v, (p.full ? p.v : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dv);
       }
     };
     // the unit's heads; rows behind them, up to the quadrant's end, are zeros
@@ -176,13 +216,17 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
       for (int x = tid - 256; x < quads * 32 * PIECES; x += 128) {
         const int r = x / PIECES, c = x % PIECES;
         const bool in = r < n_rows && 8 * c < p.dqk;
-        cp_async16(qd + (c >> 3) * P::Q_SUB + r * 128 + (((c & 7) ^ (r & 7)) << 4), in ? q + r * p.qs[1] + 8 * c : p.q,
-                   in);
+        const uint32_t to = qd + (c >> 3) * P::Q_SUB + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        const uint16_t* from = in ? q + r * p.qs[1] + 8 * c : p.q;
+        cp_async16(to, from, in);
+        if (copies == 2) cp_async16(to + 64 * 128, from, in);
       }
     };
     bool ok = true;
     int seg = 0;  // (cur: the tile issued next)
+    enter(cur);
     Place next = lookup(cur);
+    const uint16_t *kn = kh, *vn = vh;  // of `next`
     for (int j = 0; ok && j < count; ++j) {
       // the stage is free when the products of tile j - S are done
       ok = wait_all(P::B_EMPTY + j % S, ((j / S) & 1u) ^ 1u);
@@ -193,13 +237,18 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
         if (!ok) break;
         issue_q(cur, seg % NQ);
       }
-      issue(next, j % S);
+      issue(next, kn, vn, j % S);
       // counts this thread in when its copies so far have landed; the warp
       // that issues the products makes them visible to the tensor core
       // (the failure-detection hook: the first tile never arrives)
       if (j > 0 || !p.skip_first_load || blockIdx.x != 0) cp_async_arrive(bar(P::B_FULL + j % S));
       if (j + 1 < count) {
         advance(cur);
+        if (cur.t == 0) {
+          enter(cur);
+          kn = kh;
+          vn = vh;
+        }
         next = lookup(cur);
       }
     }
@@ -288,100 +337,131 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
       drain_bar(bar(P::B_DRAIN), 0, p.timeout_ns);
     }
     __syncwarp();
-  } else if (warp < 8 && (warp & 3) < quads && count > 0) {
+  } else if (warp < 8 && (copies == 2 ? (warp & 1) : (warp & 3)) < quads && count > 0) {
     // --------------------------------------------------------------- softmax
-    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    const int quad = warp & 3, half = warp >> 2, lrow = quad * 32 + lane;
+    const int odd = copies == 2 ? quad >> 1 : 0;  // takes the tiles of this parity
+    const int row = lrow - 64 * odd;              // head
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     constexpr int DH = DV / 2;  // this warp's columns of O
     float m = -INFINITY, l = 0.f;
     bool ok = true, first = true;
     int seg = 0, t0 = cur.t;
+    uint32_t swaps = 0;
     for (int i = 0; i < count; ++i) {
-      ok = wait_sleep(P::B_SF + (i & 1), (i >> 1) & 1u);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t x0[32], x1[32];  // this half's columns, the other's
-      tmem_ld_32x32b_x32(tl + (i & 1) * BN + half * 32, x0);
-      tmem_ld_32x32b_x32(tl + (i & 1) * BN + (half ^ 1) * 32, x1);
-      tmem_wait_ld_regs(x0);
-      tmem_regs_ready(x1);
-      const int live = cur.len - cur.t * BN;
-      if (live < BN) {
+      const bool ends = cur.t + 1 == cur.nt, last = ends || i + 1 == count;
+      if (copies == 1 || (i & 1) == odd) {
+        ok = wait_sleep(P::B_SF + (i & 1), (i >> 1) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x0[32], x1[32];  // this half's columns, the other's
+        tmem_ld_32x32b_x32(tl + (i & 1) * BN + half * 32, x0);
+        tmem_ld_32x32b_x32(tl + (i & 1) * BN + (half ^ 1) * 32, x1);
+        tmem_wait_ld_regs(x0);
+        tmem_regs_ready(x1);
+        const int live = cur.len - cur.t * BN;
+        if (live < BN) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          if (half * 32 + c >= live) x0[c] = 0xff800000u;
-          if ((half ^ 1) * 32 + c >= live) x1[c] = 0xff800000u;
-        }
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 32; ++c) top = max3f(top, __uint_as_float(x0[c]), __uint_as_float(x1[c]));
-      top *= p.scale_log2;
-      if (__any_sync(0xffffffffu, top > m + 8.f)) {
-        const float n = fmaxf(m, top), a = exp2_fast(m - (n == -INFINITY ? 0.f : n));
-        m = n;
-        l *= a;
-        if (!first) {
-          // O is at rest once the products of the tile before are done
-          ok = wait_sleep(P::B_EMPTY + (i - 1) % S, ((i - 1) / S) & 1u);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c0 = 0; c0 < DH; c0 += 32) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(tl + P::COL_O + half * DH + c0, o);
-            tmem_wait_ld_regs(o);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * a);
-            tmem_st_32x32b_x32(tl + P::COL_O + half * DH + c0, o);
+          for (int c = 0; c < 32; ++c) {
+            if (half * 32 + c >= live) x0[c] = 0xff800000u;
+            if ((half ^ 1) * 32 + c >= live) x1[c] = 0xff800000u;
           }
-          tmem_wait_st();
         }
-      }
-      const float u = m == -INFINITY ? 0.f : m;
-      uint32_t hi[16], lo[16];
+        float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        const float a = exp2_fast(fmaf(__uint_as_float(x0[c]), p.scale_log2, -u));
-        const float b = exp2_fast(fmaf(__uint_as_float(x0[c + 1]), p.scale_log2, -u));
-        l += a + b;
-        split2<F16>(a, b, hi[c / 2], lo[c / 2]);
+        for (int c = 0; c < 32; ++c) top = max3f(top, __uint_as_float(x0[c]), __uint_as_float(x1[c]));
+        top *= p.scale_log2;
+        if (__any_sync(0xffffffffu, top > m + 8.f)) {
+          const float n = fmaxf(m, top), a = exp2_fast(m - (n == -INFINITY ? 0.f : n));
+          m = n;
+          l *= a;
+          if (!first) {
+            // O is at rest once the products of the tile before are done
+            ok = wait_sleep(P::B_EMPTY + (i - 1) % S, ((i - 1) / S) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < DH; c0 += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(tl + P::COL_O + half * DH + c0, o);
+              tmem_wait_ld_regs(o);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * a);
+              tmem_st_32x32b_x32(tl + P::COL_O + half * DH + c0, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float u = m == -INFINITY ? 0.f : m;
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const float a = exp2_fast(fmaf(__uint_as_float(x0[c]), p.scale_log2, -u));
+          const float b = exp2_fast(fmaf(__uint_as_float(x0[c + 1]), p.scale_log2, -u));
+          l += a + b;
+          split2<F16>(a, b, hi[c / 2], lo[c / 2]);
+        }
+        const uint32_t tp = tl + P::COL_P + (i & 1) * 64 + half * 16;
+        tmem_st_32x32b_x16(tp, hi);
+        tmem_st_32x32b_x16(tp + 32, lo);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(P::B_PF + (i & 1)));
+        first = false;
       }
-      const uint32_t tp = tl + P::COL_P + (i & 1) * 64 + half * 16;
-      tmem_st_32x32b_x16(tp, hi);
-      tmem_st_32x32b_x16(tp + 32, lo);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(P::B_PF + (i & 1)));
-      first = false;
 
-      const bool ends = cur.t + 1 == cur.nt;
-      if (ends || i + 1 == count) {
+      if (last) {
         // ---- the unit's part in this CTA is complete
         int h, g0, n_rows;
         unit(cur, h, g0, n_rows);
-        float* ls = lsum + (seg & 1) * 2 * kTcRows;
-        ls[half * kTcRows + row] = l;
+        float* ls = sums + (seg & 1) * 3 * kTcRows;
+        ls[half * kTcRows + lrow] = l;
+        if (half == 0) ls[2 * kTcRows + lrow] = m;
         mbar_arrive(bar(P::B_LS));  // (a bounded wait, unlike a named barrier's)
         ok = wait_sleep(P::B_LS, seg & 1u) && wait_sleep(P::B_OF, seg & 1u);
         if (!ok) break;
-        const float sum = ls[row] + ls[kTcRows + row];
         tc_fence_after();
+        float sum = ls[lrow] + ls[kTcRows + lrow], mine = 1.f;  // of all tiles; the factor of this row's O
+        if (copies == 2) {
+          const int other = lrow ^ 64;
+          const float mo = ls[2 * kTcRows + other], n = fmaxf(m, mo), top = n == -INFINITY ? 0.f : n;
+          mine = exp2_fast(m - top);
+          sum = sum * mine + (ls[other] + ls[kTcRows + other]) * exp2_fast(mo - top);
+          m = n;
+        }
         const bool begins = t0 == 0;
         const bool in = row < n_rows;
         const long long at = (static_cast<long long>(cur.b) * p.Hkv + h) * p.G + g0 + row;
         const long long part = (2LL * blockIdx.x + (begins ? 1 : 0)) * p.rows + row;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = begins && ends ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
 #pragma unroll 1
-        for (int c0 = 0; c0 < DH; c0 += 32) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(tl + P::COL_O + half * DH + c0, o);
-          tmem_wait_ld_regs(o);
-          const int col = half * DH + c0;
-          if (in && begins && ends) {
+        for (int c0 = 0; c0 < DH; c0 += 16) {
+          uint32_t o[16];
+          tmem_ld_32x32b_x16(tl + P::COL_O + half * DH + c0, o);
+          tmem_wait_ld16_regs(o);
+          if (copies == 2) {
+            float* x = swap + half * 16 * 64 + row;
+            if (odd) {
+              ok = wait_sleep(P::B_XE, (swaps & 1u) ^ 1u);  // the columns before have been taken
+              if (!ok) break;
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) {
+              for (int c = 0; c < 16; ++c) x[c * 64] = __uint_as_float(o[c]) * mine;
+              mbar_arrive(bar(P::B_XF));
+            } else {
+              ok = wait_sleep(P::B_XF, swaps & 1u);
+              if (!ok) break;
+#pragma unroll
+              for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(fmaf(__uint_as_float(o[c]), mine, x[c * 64]));
+              mbar_arrive(bar(P::B_XE));
+            }
+            ++swaps;
+          }
+          const int col = half * DH + c0;
+          if (!in || odd) continue;
+          if (begins && ends) {
+#pragma unroll
+            for (int c = 0; c < 16; c += 8) {
               uint32_t y[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -389,13 +469,14 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
               if (col + c < p.dv)
                 *reinterpret_cast<uint4*>(p.o + at * p.dv + col + c) = make_uint4(y[0], y[1], y[2], y[3]);
             }
-          } else if (in) {
+          } else {
 #pragma unroll
-            for (int c = 0; c < 32; c += 4)
+            for (int c = 0; c < 16; c += 4)
               *reinterpret_cast<uint4*>(p.part_o + part * DV + col + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
           }
         }
-        if (in && half == 0) {
+        if (!ok) break;
+        if (in && half == 0 && !odd) {
           if (begins && ends) p.lse[at] = sum == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(sum);
           else p.part_ml[part] = make_float2(m, sum);
         }
