@@ -16,16 +16,26 @@
 // Up to 64 heads stand twice in Q, as rows 0-63 and 64-127: the first two
 // quadrants take the even tiles and the others the odd ones (the rows of P
 // that are not a quadrant's stay zero), each with a running maximum, sum and
-// O of its own, joined at the unit's end.  That halves what bounds the kernel
-// otherwise, a tile's softmax (1400 of its 1800 cycles at D 128).
-// Warps 8-11 bring tiles (16 keys each) by 16-byte asynchronous copies, row
-// by row through the page table; a tile's barrier counts the copies in as they
-// land.  Warp 12 issues the products: S of tile i + 1 before O of tile i.
+// O of its own, joined at the unit's end.  (32 sequences of 8192 keys, 64
+// heads, D 64: 203 us with every quadrant at every tile, 171 so.)
+// Warps 8-11 bring tiles (16 keys each) by 16-byte asynchronous copies, row by
+// row through the page table; a tile's barrier counts the copies in as they
+// land.  The last warp issues the products: S of tile i + 1 before O of tile
+// i.  That lane is what bounds the kernel where memory does not (D 128, 64
+// heads: 1700 cycles a tile, of which memory needs 1390): the products
+// themselves, twice those of O because P comes in two parts, and three waits.
+// Both head dims 256: only two tiles fit beside Q, so keys and values have a
+// ring each (a key stage is free again as soon as S is, a tile and a softmax
+// before the values') and two groups of four warps bring the even and the odd
+// tiles: 115 -> 101 us at 24 heads.  At D 128 the second barrier of a tile and
+// the registers of the second group cost more than they give (112 -> 120 us).
 // S and P have two buffers each in tensor memory.  P is split into two
 // 16-bit parts there, like the warps' P of the other kernel.
 #pragma once
 #include "attn_decode_kernel.cuh"
 #include "attn_kernel.cuh"
+
+#include <type_traits>
 
 namespace attn {
 
@@ -33,32 +43,37 @@ constexpr int kTcBN = 64, kTcRows = 128;
 
 template <int DQ, int DV>
 struct DecodeTcPlan {
-  static constexpr int NW = 13, THREADS = NW * 32;
   static constexpr int SUB = kTcBN * 128;                // 64 columns of a tile
-  static constexpr int K_TILE = DQ / 64 * SUB, TILE = K_TILE + DV / 64 * SUB;
+  static constexpr int K_TILE = DQ / 64 * SUB, V_TILE = DV / 64 * SUB, TILE = K_TILE + V_TILE;
+  // a ring and barriers of their own for keys and values, two groups of
+  // producers; else a tile's keys and values share a stage's barriers
+  static constexpr bool SPLIT = TILE > 48 * 1024;
+  static constexpr int GROUPS = SPLIT ? 2 : 1, ISSUER = 8 + 4 * GROUPS, NW = ISSUER + 1, THREADS = NW * 32;
   static constexpr int Q_SUB = kTcRows * 128, Q_TILE = DQ / 64 * Q_SUB;
   // words of the planning, sums and maxima of two units, O on its way from
   // the odd tiles' rows to the even ones' (16 columns of each half), barriers
-  static constexpr int SUMS = 2 * 3 * kTcRows * 4, SWAP = 2 * 64 * 16 * 4;
-  static constexpr int MISC = 8 * THREADS + 2 * 8 * 16 + SUMS + SWAP + 256;
+  static constexpr int SUMS = 2 * 3 * kTcRows * 4, SWAP = 2 * 64 * 16 * 4, CTL = 512;
+  static constexpr int MISC = 8 * THREADS + 2 * 8 * 16 + SUMS + SWAP + CTL;
   static constexpr int FIT = 227 * 1024 - MISC - 1024;   // (1024: alignment)
   static constexpr int NQ = 2 * Q_TILE + 3 * TILE <= FIT ? 2 : 1;
-  static constexpr int S_FIT = (FIT - NQ * Q_TILE) / TILE, S = S_FIT > 6 ? 6 : S_FIT;
-  static constexpr int OFF_RING = NQ * Q_TILE, OFF_MISC = OFF_RING + S * TILE;
+  static constexpr int PAIRS = (FIT - NQ * Q_TILE) / TILE, SV = PAIRS > 8 ? 8 : PAIRS;
+  static constexpr int SK = SPLIT && SV < 8 && FIT - NQ * Q_TILE - SV * TILE >= K_TILE ? SV + 1 : SV;
+  static constexpr int OFF_K = NQ * Q_TILE, OFF_V = OFF_K + SK * K_TILE, OFF_MISC = OFF_V + SV * V_TILE;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   // barriers
-  static constexpr int B_FULL = 0, B_EMPTY = S, B_SF = 2 * S, B_PF = 2 * S + 2, B_QE = 2 * S + 4, B_OF = 2 * S + 6,
-                       B_OE = 2 * S + 7, B_LS = 2 * S + 8, B_XF = 2 * S + 9, B_XE = 2 * S + 10, B_DRAIN = 2 * S + 11, NBAR = 2 * S + 12;
+  static constexpr int B_KF = 0, B_KE = SK, B_VF = SPLIT ? 2 * SK : B_KF, B_VE = SPLIT ? 2 * SK + SV : B_KE, B_SF = 2 * (SK + SV), B_PF = B_SF + 2,
+                       B_QE = B_SF + 4, B_OF = B_SF + 6, B_OE = B_SF + 7, B_LS = B_SF + 8, B_XF = B_SF + 9,
+                       B_XE = B_SF + 10, B_DRAIN = B_SF + 11, NBAR = B_SF + 12;
   // tensor memory columns: S, S, P, P (upper | lower parts), O
   static constexpr int COL_P = 128, COL_O = 256, TMEM = 512;
-  static_assert(S >= 2 && NBAR * 8 <= 200, "decode plan");
+  static_assert(SV >= 2 && NBAR * 8 <= CTL - 16, "decode plan");
 };
 
 template <int DQ, int DV, bool F16>
 __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
     attn_decode_tc_kernel(const __grid_constant__ DecodeParams p) {
   using P = DecodeTcPlan<DQ, DV>;
-  constexpr int BN = kTcBN, S = P::S, NQ = P::NQ;
+  constexpr int BN = kTcBN, SK = P::SK, SV = P::SV, NQ = P::NQ;
   extern __shared__ __align__(128) char decode_smem[];
   char* smem = decode_smem + ((1024 - (smem_u32(decode_smem) & 1023)) & 1023);  // swizzle atoms of 1024 bytes
   const uint32_t base = smem_u32(smem);
@@ -67,10 +82,10 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
                           reinterpret_cast<long long*>(misc + 8 * P::THREADS)};
   float* sums = reinterpret_cast<float*>(misc + 8 * P::THREADS + 2 * 8 * 16);  // [2 units][l, l, m][row]
   float* swap = sums + P::SUMS / 4;                                            // [2 halves][16 columns][row]
-  char* ctl = misc + P::MISC - 256;
+  char* ctl = misc + P::MISC - P::CTL;
   const uint32_t bar0 = smem_u32(ctl);
-  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(ctl + 208);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + 212);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(ctl + P::CTL - 16);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + P::CTL - 12);
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int HU = p.Hkv * p.chunks;
@@ -78,9 +93,13 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
   const int copies = quads <= 2 ? 2 : 1;
 
   if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(bar(P::B_FULL + i), 128);
-      mbar_init(bar(P::B_EMPTY + i), 1);
+    for (int i = 0; i < SK; ++i) {
+      mbar_init(bar(P::B_KF + i), 128);
+      mbar_init(bar(P::B_KE + i), 1);
+    }
+    for (int i = 0; P::SPLIT && i < SV; ++i) {
+      mbar_init(bar(P::B_VF + i), 128);
+      mbar_init(bar(P::B_VE + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(P::B_SF + i), 1);
@@ -96,7 +115,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
     *abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == 12) {
+  if (warp == P::ISSUER) {
     tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), P::TMEM);
     tmem_relinquish();
   }
@@ -154,9 +173,9 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
     n_rows = min(p.rows, p.G - g0);
   };
 
-  if (warp >= 8 && warp < 12 && count > 0) {
+  if (warp >= 8 && warp < P::ISSUER && count > 0) {
     // ------------------------------------------------------------ producers
-    const int g = lane >> 2, q4 = lane & 3, k0 = (warp - 8) * 16;
+    const int g = lane >> 2, q4 = lane & 3, k0 = (warp & 3) * 16;
     // pages of 16 tokens and more, a power of two of them: the two rows of a
     // lane, 8 tokens apart, lie in one page
     const bool one_page = p.page_shift >= 4;
@@ -186,24 +205,19 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
       }
       return x;
     };
-    auto issue = [&](const Place& x, const uint16_t* kh, const uint16_t* vh, int stage) {
-      const uint32_t kd = base + P::OFF_RING + stage * P::TILE + (k0 + g) * 128 + ((q4 ^ g) << 4);
-      const uint32_t vd = kd + P::K_TILE;
-      const uint16_t *k = nullptr, *v = nullptr;
+    // both rows of a tile, of the pool with these strides and D (d) elements
+    auto issue = [&](auto width, const Place& x, const uint16_t* head, const long long (&st)[3], const uint16_t* pool, int d,
+                     uint32_t stage) {
+      constexpr int D = decltype(width)::value;
+      const uint32_t to = stage + (k0 + g) * 128 + ((q4 ^ g) << 4);
+      const uint16_t* row = nullptr;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const bool live = x.slot[r] >= 0 && x.page[r] >= 0 && x.page[r] < p.n_pages;
         if (!live && x.slot[r] >= 0) *p.err = 1;
-        if (r == 1 && one_page) {
-          k += 8 * p.kp[2];
-          v += 8 * p.vp[2];
-        } else {
-          const long long page = x.page[r], slot = x.slot[r];
-          k = kh + page * p.kp[0] + slot * p.kp[2];
-          v = vh + page * p.vp[0] + slot * p.vp[2];
-        }
-        copy_row<DQ, P::SUB>(kd + r * 1024, k, (p.full ? p.k : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dqk);
-        copy_row<DV, P::SUB>(vd + r * 1024, v, (p.full ? p.v : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dv);
+        if (r == 1 && one_page) row += 8 * st[2];
+        else row = head + static_cast<long long>(x.page[r]) * st[0] + static_cast<long long>(x.slot[r]) * st[2];
+        copy_row<D, P::SUB>(to + r * 1024, row, (p.full ? pool : p.q) + 8 * q4 * p.full, live, p.full, q4, d);
       }
     };
     // the unit's heads; rows behind them, up to the quadrant's end, are zeros
@@ -213,7 +227,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
       const uint16_t* q = p.q + a.b * p.qs[0] + (static_cast<long long>(h) * p.G + g0) * p.qs[1];
       const uint32_t qd = base + qb * P::Q_TILE;
       constexpr int PIECES = DQ / 8;
-      for (int x = tid - 256; x < quads * 32 * PIECES; x += 128) {
+      for (int x = tid & 127; x < quads * 32 * PIECES; x += 128) {
         const int r = x / PIECES, c = x % PIECES;
         const bool in = r < n_rows && 8 * c < p.dqk;
         const uint32_t to = qd + (c >> 3) * P::Q_SUB + r * 128 + (((c & 7) ^ (r & 7)) << 4);
@@ -222,110 +236,139 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
         if (copies == 2) cp_async16(to + 64 * 128, from, in);
       }
     };
+    // Every tile, or every second one.  A thread's arrival counts it in when
+    // its copies so far have landed; the warp that issues the products makes
+    // them visible to the tensor core.
     bool ok = true;
-    int seg = 0;  // (cur: the tile issued next)
+    int j = (warp - 8) >> 2, seg = 0;  // (cur: tile j, of unit seg in this CTA)
+    int ks = j, vs = j;
+    uint32_t kp = 1, vp = 1;  // phases of the rings' empty barriers
+    auto step = [&]() {
+      advance(cur);
+      if (cur.t == 0) ++seg;
+    };
+    if (j == 1 && count > 1) step();
     enter(cur);
     Place next = lookup(cur);
-    const uint16_t *kn = kh, *vn = vh;  // of `next`
-    for (int j = 0; ok && j < count; ++j) {
-      // the stage is free when the products of tile j - S are done
-      ok = wait_all(P::B_EMPTY + j % S, ((j / S) & 1u) ^ 1u);
+    while (j < count) {
+      ok = wait_all(P::B_KE + ks, kp);
       if (!ok) break;
       if (j == 0 || cur.t == 0) {
-        if (j > 0) ++seg;
         ok = wait_all(P::B_QE + seg % NQ, ((seg / NQ) & 1u) ^ 1u);
         if (!ok) break;
         issue_q(cur, seg % NQ);
       }
-      issue(next, kn, vn, j % S);
-      // counts this thread in when its copies so far have landed; the warp
-      // that issues the products makes them visible to the tensor core
+      issue(std::integral_constant<int, DQ>(), next, kh, p.kp, p.k, p.dqk, base + P::OFF_K + ks * P::K_TILE);
       // (the failure-detection hook: the first tile never arrives)
-      if (j > 0 || !p.skip_first_load || blockIdx.x != 0) cp_async_arrive(bar(P::B_FULL + j % S));
-      if (j + 1 < count) {
-        advance(cur);
-        if (cur.t == 0) {
-          enter(cur);
-          kn = kh;
-          vn = vh;
-        }
-        next = lookup(cur);
+      const bool arrives = j > 0 || !p.skip_first_load || blockIdx.x != 0;
+      if (P::SPLIT) {
+        if (arrives) cp_async_arrive(bar(P::B_KF + ks));
+        ok = wait_all(P::B_VE + vs, vp);
+        if (!ok) break;
       }
+      issue(std::integral_constant<int, DV>(), next, vh, p.vp, p.v, p.dv, base + P::OFF_V + vs * P::V_TILE);
+      if (P::SPLIT || arrives) cp_async_arrive(bar(P::B_VF + vs));
+      j += P::GROUPS;
+      if (j >= count) break;
+      ks += P::GROUPS;
+      vs += P::GROUPS;
+      if (ks >= SK) {
+        ks -= SK;
+        kp ^= 1u;
+      }
+      if (vs >= SV) {
+        vs -= SV;
+        vp ^= 1u;
+      }
+      const int was = seg;
+      step();
+      if (P::GROUPS == 2) step();
+      if (seg != was) enter(cur);
+      next = lookup(cur);
     }
     cp_async_commit();
     cp_async_wait<0>();
-  } else if (warp == 12 && count > 0) {
+  } else if (warp == P::ISSUER && count > 0) {
     // -------------------------------------------------------------- products
     // One lane alone: its waits and issues are the longest chain of a tile,
     // and votes between them would lengthen it.
     if (elect_one()) {
       constexpr uint32_t idesc_s = idesc_16(kTcRows, BN, false, F16), idesc_o = idesc_16(kTcRows, DV, true, F16);
       constexpr uint32_t kHi = sdesc_hi_sw128(1024);
-      const uint32_t lo_q = sdesc_lo(base, 16), lo_k = sdesc_lo(base + P::OFF_RING, 16);
-      const uint32_t lo_v = sdesc_lo(base + P::OFF_RING + P::K_TILE, P::SUB);
+      const uint32_t lo_q = sdesc_lo(base, 16), lo_k = sdesc_lo(base + P::OFF_K, 16);
+      const uint32_t lo_v = sdesc_lo(base + P::OFF_V, P::SUB);
       bool ok = true;
       int seg = 0, pv_seg = 0;
       bool first = true;                       // of its unit in this CTA: the tile whose O is next
-      int stage_s = 0, stage_o = 0;            // stages of the tiles whose S and O are next
-      uint32_t phase_s = 0;
+      int ks = 0, vs = 0;                      // stages of the tiles whose S and O are next
+      uint32_t kp = 0, vp = 0;
       // O of tile j, the last of its unit or not
       auto products_o = [&](int j, bool last) {
         ok = wait_bar(bar(P::B_PF + (j & 1)), (j >> 1) & 1u, W);
         // the first product of a unit overwrites O: the unit before has left it
         if (ok && first) ok = wait_bar(bar(P::B_OE), (pv_seg & 1u) ^ 1u, W);
+        if (P::SPLIT && ok) ok = wait_bar(bar(P::B_VF + vs), vp, W);
         if (!ok) return;
+        if (P::SPLIT) fence_proxy_async_smem();
         tc_fence_after();
-        const uint32_t a = tmem + P::COL_P + (j & 1) * 64, v = lo_v + stage_o * (P::TILE >> 4);
+        const uint32_t a = tmem + P::COL_P + (j & 1) * 64, v = lo_v + vs * (P::V_TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk) {
           const uint64_t d = sdesc_join(v + ((kk * 2048) >> 4), kHi);
           mma_ts(tmem + P::COL_O, a + 8 * kk, d, idesc_o, first && kk == 0 ? 0u : 1u);
           mma_ts(tmem + P::COL_O, a + 32 + 8 * kk, d, idesc_o, 1u);
         }
-        tc_commit(bar(P::B_EMPTY + stage_o));
+        tc_commit(bar(P::B_VE + vs));
         if (last) tc_commit(bar(P::B_OF));
         first = last;
         pv_seg += last ? 1 : 0;
-        stage_o = stage_o + 1 == S ? 0 : stage_o + 1;
+        if (++vs == SV) {
+          vs = 0;
+          vp ^= 1u;
+        }
       };
-      // whether barrier a completes before barrier b (or both have; or
-      // neither does in time: the wait that follows reports it)
+      // 1: barrier a has completed; 2: barrier b has, and a not yet; 0:
+      // neither in time (the wait that follows reports it)
       auto wait_first = [&](uint32_t a, uint32_t pa, uint32_t b, uint32_t pb) {
-        if (mbar_test_wait(a, pa)) return true;
-        const uint64_t t0 = globaltimer_ns();
-        for (;;) {
-          if (mbar_test_wait(b, pb)) return false;
-          if (mbar_test_wait(a, pa)) return true;
-          if (*abort_flag != 0 || globaltimer_ns() - t0 > p.timeout_ns) return true;
+        uint64_t t0 = 0;
+        for (uint32_t it = 0;; ++it) {
+          if (mbar_test_wait(a, pa)) return 1;
+          if (mbar_test_wait(b, pb)) return 2;
+          if ((it & 7u) != 7u) continue;
+          if (t0 == 0) t0 = globaltimer_ns();
+          else if (*abort_flag != 0 || globaltimer_ns() - t0 > p.timeout_ns) return 0;
         }
       };
       bool pending = false, last_before = false;  // O of tile i - 1
       for (int i = 0; ok && i < count; ++i) {
         const bool last = cur.t + 1 == cur.nt || i + 1 == count;
         // S of this tile before O of the one before, unless that is ready first
-        if (pending && !wait_first(bar(P::B_FULL + stage_s), phase_s, bar(P::B_PF + ((i - 1) & 1)), ((i - 1) >> 1) & 1u)) {
+        const int which =
+            pending ? wait_first(bar(P::B_KF + ks), kp, bar(P::B_PF + ((i - 1) & 1)), ((i - 1) >> 1) & 1u) : 0;
+        if (which == 2) {
           products_o(i - 1, last_before);
           pending = false;
           if (!ok) break;
         }
-        ok = wait_bar(bar(P::B_FULL + stage_s), phase_s, W);
+        if (which != 1) ok = wait_bar(bar(P::B_KF + ks), kp, W);
         if (!ok) break;
         fence_proxy_async_smem();  // the copies, made by the generic proxy, before the products read them
         tc_fence_after();
-        const uint32_t q = lo_q + (seg % NQ) * (P::Q_TILE >> 4), k = lo_k + stage_s * (P::TILE >> 4);
+        const uint32_t q = lo_q + (seg % NQ) * (P::Q_TILE >> 4), k = lo_k + ks * (P::K_TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < DQ / 16; ++kk) {
           const uint32_t oq = ((kk >> 2) * P::Q_SUB + (kk & 3) * 32) >> 4, ok_ = ((kk >> 2) * P::SUB + (kk & 3) * 32) >> 4;
           mma_ss(tmem + (i & 1) * BN, sdesc_join(q + oq, kHi), sdesc_join(k + ok_, kHi), idesc_s, kk > 0 ? 1u : 0u);
         }
         tc_commit(bar(P::B_SF + (i & 1)));
+        if (P::SPLIT) tc_commit(bar(P::B_KE + ks));
         if (last) {
           tc_commit(bar(P::B_QE + seg % NQ));
           ++seg;
         }
-        if (++stage_s == S) {
-          stage_s = 0;
-          phase_s ^= 1u;
+        if (++ks == SK) {
+          ks = 0;
+          kp ^= 1u;
         }
         if (pending) products_o(i - 1, last_before);
         pending = true;
@@ -377,7 +420,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
           l *= a;
           if (!first) {
             // O is at rest once the products of the tile before are done
-            ok = wait_sleep(P::B_EMPTY + (i - 1) % S, ((i - 1) / S) & 1u);
+            ok = wait_sleep(P::B_VE + (i - 1) % SV, ((i - 1) / SV) & 1u);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -497,7 +540,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, P::TMEM);
+  if (warp == P::ISSUER) tmem_dealloc(tmem, P::TMEM);
 }
 
 template <int DQ, int DV, bool F16>
