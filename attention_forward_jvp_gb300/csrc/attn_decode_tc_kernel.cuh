@@ -1,15 +1,16 @@
-// The paged decode for many query heads on a key head (17 and more): the same
-// list of steps, ranges and joining as attn_decode_kernel.cuh, with 64-key
-// tiles, a range for each CTA, and the products on tcgen05.
+// The paged decode for many query heads on a key head (17 and more; 9 and more
+// where both head dims are 256): the same list of steps, ranges and joining as
+// attn_decode_kernel.cuh, with 64-key tiles, a range for each CTA, and the
+// products on tcgen05.
 //
 //   S (128 x 64)   = Q K^T       Q: the unit's heads as rows, from shared memory
 //   O (128 x Dv)  += P V         P: from tensor memory, V as it lies (MN-major)
 //
-// What bounds it: memory up to 128 heads (256 flops a byte, a sixteenth of a
-// tile's time in products).  mma.sync (64 heads, Dqk 256, Dv 128: 140 us)
-// would have to read every key once for 8 heads' columns; here a tile is
-// read once for all of them, and heads short of 128 cost nothing but unused
-// lanes.
+// What has to bound it is memory, up to 128 heads: at D 128 an SM's share of
+// the bandwidth brings a tile in 1400 cycles, and the tensor core multiplies it
+// in 770 whatever the heads (lanes short of 128 are unused).  On mma.sync every
+// 8 heads' columns would read the tile from shared memory again (64 heads, Dqk
+// 256, Dv 128: 140 us; here 88).
 //
 // Warps 0-7 are the softmax: two to a quadrant of 32 lanes (32 heads), each
 // with half of a tile's columns; quadrants behind the last head do nothing.
@@ -22,8 +23,8 @@
 // row through the page table; a tile's barrier counts the copies in as they
 // land.  The last warp issues the products: S of tile i + 1 before O of tile
 // i.  That lane is what bounds the kernel where memory does not (D 128, 64
-// heads: 1700 cycles a tile, of which memory needs 1390): the products
-// themselves, twice those of O because P comes in two parts, and three waits.
+// heads: 1700 cycles a tile): the products, those of O twice because P comes
+// in two parts, and three waits.
 // Both head dims 256: only two tiles fit beside Q, so keys and values have a
 // ring each (a key stage is free again as soon as S is, a tile and a softmax
 // before the values') and two groups of four warps bring the even and the odd

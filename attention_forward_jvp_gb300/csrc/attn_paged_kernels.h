@@ -65,9 +65,9 @@ constexpr int kDecodeBN = 16;        // keys of a step
 constexpr int kDecodeMinStepsLog = 1;  // a warp takes two steps at least, where there are two
 constexpr int kDecodeMaxWarps = 16;  // warps of a CTA, at most
 // Query heads of a unit that a warp takes at most; more go to tcgen05.  At 16
-// heads the two take 101 and 117 us (D 128, 32 sequences of 8192), at 24 the
-// warps' 155 and 117; with Dqk = Dv = 256 a warp has no registers left for a
-// second group of 8: 135 and 115 at 16.
+// heads the two take 103 and 112 us (D 128, 32 sequences of 8192), at 24 the
+// warps' 155 and 112; with Dqk = Dv = 256 a warp has no registers left for a
+// second group of 8: 135 and 100 at 16.
 constexpr int decode_warp_rows(int dq, int dv) { return dq + dv < 512 ? 16 : 8; }
 constexpr int kDecodeMaxRows = 128;   // query heads of a unit, at most
 
