@@ -151,7 +151,7 @@ struct DecodeRange {
 struct DecodeWords {
   int* lens;          // [threads]
   uint32_t* sums;     // [threads]
-  long long* totals;  // [2][16]
+  long long* totals;  // [2][warps]
 };
 
 // Thread x holds sequence x (and adds up those behind it, a block's width
@@ -191,12 +191,12 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
   s.lens[tid] = n;
   s.sums[tid] = static_cast<uint32_t>(inc);
   if (lane == 31) s.totals[warp] = inc;
-  if (lane == 0) s.totals[16 + warp] = rest;
+  if (lane == 0) s.totals[NW + warp] = rest;
   const bool idle = __syncthreads_or((tid < p.B && n == 0) || p.B > THREADS);
   I cum = scan(lane < NW ? static_cast<I>(s.totals[lane]) : 0);  // steps up to warp `lane`
   I steps = __shfl_sync(ALL, cum, NW - 1);
   if (p.B > THREADS) {
-    I r = lane < NW ? static_cast<I>(s.totals[16 + lane]) : 0;
+    I r = lane < NW ? static_cast<I>(s.totals[NW + lane]) : 0;
 #pragma unroll
     for (int o = 16; o; o >>= 1) r += __shfl_xor_sync(ALL, r, o);
     steps += r;

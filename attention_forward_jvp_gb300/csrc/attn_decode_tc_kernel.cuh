@@ -54,34 +54,35 @@ struct DecodeTcPlan {
   // words of the planning, sums and maxima of two units, O on its way from
   // the odd tiles' rows to the even ones' (16 columns of each half), barriers
   static constexpr int SUMS = 2 * 3 * kTcRows * 4, SWAP = 2 * 64 * 16 * 4, CTL = 512;
-  static constexpr int MISC = 8 * THREADS + 2 * 8 * 16 + SUMS + SWAP + CTL;
+  static constexpr int MISC = 8 * THREADS + 16 * NW + SUMS + SWAP + CTL;
   static constexpr int FIT = 227 * 1024 - MISC - 1024;   // (1024: alignment)
-  static constexpr int NQ = 2 * Q_TILE + 3 * TILE <= FIT ? 2 : 1;
-  static constexpr int PAIRS = (FIT - NQ * Q_TILE) / TILE, SV = PAIRS > 8 ? 8 : PAIRS;
-  static constexpr int SK = SPLIT && SV < 8 && FIT - NQ * Q_TILE - SV * TILE >= K_TILE ? SV + 1 : SV;
-  static constexpr int OFF_K = NQ * Q_TILE, OFF_V = OFF_K + SK * K_TILE, OFF_MISC = OFF_V + SV * V_TILE;
+  static constexpr int NQ = !SPLIT && 2 * Q_TILE + 3 * TILE <= FIT ? 2 : 1;
+  static constexpr int S_FIT = (FIT - NQ * Q_TILE) / TILE, S = S_FIT > 8 ? 8 : S_FIT;  // stages
+  static constexpr int OFF_K = NQ * Q_TILE, OFF_V = OFF_K + S * K_TILE, OFF_MISC = OFF_V + S * V_TILE;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   // barriers
-  static constexpr int B_KF = 0, B_KE = SK, B_VF = SPLIT ? 2 * SK : B_KF, B_VE = SPLIT ? 2 * SK + SV : B_KE, B_SF = 2 * (SK + SV), B_PF = B_SF + 2,
-                       B_QE = B_SF + 4, B_OF = B_SF + 6, B_OE = B_SF + 7, B_LS = B_SF + 8, B_XF = B_SF + 9,
-                       B_XE = B_SF + 10, B_DRAIN = B_SF + 11, NBAR = B_SF + 12;
+  static constexpr int B_KF = 0, B_KE = S, B_VF = SPLIT ? 2 * S : B_KF, B_VE = SPLIT ? 3 * S : B_KE, B_SF = 4 * S,
+                       B_PF = B_SF + 2, B_QE = B_SF + 4, B_OF = B_SF + 6, B_OE = B_SF + 7, B_LS = B_SF + 8,
+                       B_XF = B_SF + 9, B_XE = B_SF + 10, B_DRAIN = B_SF + 11, NBAR = B_SF + 12;
   // tensor memory columns: S, S, P, P (upper | lower parts), O
   static constexpr int COL_P = 128, COL_O = 256, TMEM = 512;
-  static_assert(SV >= 2 && NBAR * 8 <= CTL - 16, "decode plan");
+  static_assert(S >= 2 && NBAR * 8 <= CTL - 16, "decode plan");
+  // the stages of a group are its own, whose phases it sees one by one
+  static_assert(S % GROUPS == 0, "decode plan");
 };
 
 template <int DQ, int DV, bool F16>
 __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
     attn_decode_tc_kernel(const __grid_constant__ DecodeParams p) {
   using P = DecodeTcPlan<DQ, DV>;
-  constexpr int BN = kTcBN, SK = P::SK, SV = P::SV, NQ = P::NQ;
+  constexpr int BN = kTcBN, S = P::S, NQ = P::NQ;
   extern __shared__ __align__(128) char decode_smem[];
   char* smem = decode_smem + ((1024 - (smem_u32(decode_smem) & 1023)) & 1023);  // swizzle atoms of 1024 bytes
   const uint32_t base = smem_u32(smem);
   char* misc = smem + P::OFF_MISC;
   const DecodeWords words{reinterpret_cast<int*>(misc), reinterpret_cast<uint32_t*>(misc) + P::THREADS,
                           reinterpret_cast<long long*>(misc + 8 * P::THREADS)};
-  float* sums = reinterpret_cast<float*>(misc + 8 * P::THREADS + 2 * 8 * 16);  // [2 units][l, l, m][row]
+  float* sums = reinterpret_cast<float*>(misc + 8 * P::THREADS + 16 * P::NW);  // [2 units][l, l, m][row]
   float* swap = sums + P::SUMS / 4;                                            // [2 halves][16 columns][row]
   char* ctl = misc + P::MISC - P::CTL;
   const uint32_t bar0 = smem_u32(ctl);
@@ -94,13 +95,13 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
   const int copies = quads <= 2 ? 2 : 1;
 
   if (tid == 0) {
-    for (int i = 0; i < SK; ++i) {
+    for (int i = 0; i < S; ++i) {
       mbar_init(bar(P::B_KF + i), 128);
       mbar_init(bar(P::B_KE + i), 1);
-    }
-    for (int i = 0; P::SPLIT && i < SV; ++i) {
-      mbar_init(bar(P::B_VF + i), 128);
-      mbar_init(bar(P::B_VE + i), 1);
+      if (P::SPLIT) {
+        mbar_init(bar(P::B_VF + i), 128);
+        mbar_init(bar(P::B_VE + i), 1);
+      }
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(P::B_SF + i), 1);
@@ -241,9 +242,10 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
     // its copies so far have landed; the warp that issues the products makes
     // them visible to the tensor core.
     bool ok = true;
-    int j = (warp - 8) >> 2, seg = 0;  // (cur: tile j, of unit seg in this CTA)
-    int ks = j, vs = j;
-    uint32_t kp = 1, vp = 1;  // phases of the rings' empty barriers
+    const int group = (warp - 8) >> 2;
+    int j = group, seg = 0;  // (cur: tile j, of unit seg in this CTA)
+    int stage = j;
+    uint32_t phase = 1, q_phase = 0;
     auto step = [&]() {
       advance(cur);
       if (cur.t == 0) ++seg;
@@ -252,34 +254,36 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
     enter(cur);
     Place next = lookup(cur);
     while (j < count) {
-      ok = wait_all(P::B_KE + ks, kp);
+      ok = wait_all(P::B_KE + stage, phase);
       if (!ok) break;
       if (j == 0 || cur.t == 0) {
-        ok = wait_all(P::B_QE + seg % NQ, ((seg / NQ) & 1u) ^ 1u);
+        // (two groups: the one buffer's barrier of the group that is to fill
+        // it next, which so sees every phase of its own)
+        if (P::GROUPS == 1) {
+          ok = wait_all(P::B_QE + seg % NQ, ((seg / NQ) & 1u) ^ 1u);
+        } else if (j > 0) {
+          ok = wait_all(P::B_QE + group, q_phase);
+          q_phase ^= 1u;
+        }
         if (!ok) break;
         issue_q(cur, seg % NQ);
       }
-      issue(std::integral_constant<int, DQ>(), next, kh, p.kp, p.k, p.dqk, base + P::OFF_K + ks * P::K_TILE);
+      issue(std::integral_constant<int, DQ>(), next, kh, p.kp, p.k, p.dqk, base + P::OFF_K + stage * P::K_TILE);
       // (the failure-detection hook: the first tile never arrives)
       const bool arrives = j > 0 || !p.skip_first_load || blockIdx.x != 0;
       if (P::SPLIT) {
-        if (arrives) cp_async_arrive(bar(P::B_KF + ks));
-        ok = wait_all(P::B_VE + vs, vp);
+        if (arrives) cp_async_arrive(bar(P::B_KF + stage));
+        ok = wait_all(P::B_VE + stage, phase);
         if (!ok) break;
       }
-      issue(std::integral_constant<int, DV>(), next, vh, p.vp, p.v, p.dv, base + P::OFF_V + vs * P::V_TILE);
-      if (P::SPLIT || arrives) cp_async_arrive(bar(P::B_VF + vs));
+      issue(std::integral_constant<int, DV>(), next, vh, p.vp, p.v, p.dv, base + P::OFF_V + stage * P::V_TILE);
+      if (P::SPLIT || arrives) cp_async_arrive(bar(P::B_VF + stage));
       j += P::GROUPS;
       if (j >= count) break;
-      ks += P::GROUPS;
-      vs += P::GROUPS;
-      if (ks >= SK) {
-        ks -= SK;
-        kp ^= 1u;
-      }
-      if (vs >= SV) {
-        vs -= SV;
-        vp ^= 1u;
+      stage += P::GROUPS;
+      if (stage >= S) {
+        stage -= S;
+        phase ^= 1u;
       }
       const int was = seg;
       step();
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
         if (last) tc_commit(bar(P::B_OF));
         first = last;
         pv_seg += last ? 1 : 0;
-        if (++vs == SV) {
+        if (++vs == S) {
           vs = 0;
           vp ^= 1u;
         }
@@ -364,10 +368,10 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
         tc_commit(bar(P::B_SF + (i & 1)));
         if (P::SPLIT) tc_commit(bar(P::B_KE + ks));
         if (last) {
-          tc_commit(bar(P::B_QE + seg % NQ));
+          tc_commit(bar(P::B_QE + (P::GROUPS == 1 ? seg % NQ : (i + 1) & 1)));
           ++seg;
         }
-        if (++ks == SK) {
+        if (++ks == S) {
           ks = 0;
           kp ^= 1u;
         }
@@ -421,7 +425,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
           l *= a;
           if (!first) {
             // O is at rest once the products of the tile before are done
-            ok = wait_sleep(P::B_VE + (i - 1) % SV, ((i - 1) / SV) & 1u);
+            ok = wait_sleep(P::B_VE + (i - 1) % S, ((i - 1) / S) & 1u);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1

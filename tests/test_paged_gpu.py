@@ -784,3 +784,19 @@ def test_decode_many_heads_splits(B, Hkv, group, lens):
     check_decode(pool, q, o, lse)
     o2, lse2 = binding.attn_paged_decode(pool.cache, q)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dims,group", [((256, 256), 12), ((256, 256), 70), ((64, 64), 20)])
+@pytest.mark.parametrize("lens", ["one tile", "random"])
+def test_decode_many_short_sequences(dims, group, lens):
+    # a CTA's units change with every tile or two (both head dims 256: each group of producers skips some), and
+    # there are more sequences than a CTA has threads
+    r = np.random.RandomState(group)
+    B = 700
+    n = list(r.randint(1, 65, B)) if lens == "one tile" else list(r.randint(0, 200, B))
+    pool = Pool([int(x) for x in n], 2, *dims, 16, BF, seed=group)
+    q = randn((B, 2 * group, dims[0]), BF, group)
+    o, lse = binding.attn_paged_decode(pool.cache, q)
+    check_decode(pool, q, o, lse)
+    o2, lse2 = binding.attn_paged_decode(pool.cache, q)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
