@@ -72,6 +72,13 @@ bool take_strides(const int64_t* s, const int64_t* sizes, int n, long long* out)
   }
   return mult8;
 }
+// Whether an array that is written has a stride of 0, elements that share
+// their place (strides as take_strides left them)
+bool shares_places(const int64_t* sizes, int n, const long long* s) {
+  bool any = false;
+  for (int i = 0; i < n; ++i) any = any || (sizes[i] > 1 && s[i] == 0);
+  return any;
+}
 
 attn_status spec_of(const attn_rope_spec* r, int D, bool inverse, RopeSpec* out) {
   if (r->rot_dim <= 0 || r->rot_dim > D || r->rot_dim % 2 != 0 || !std::isfinite(r->out_scale) || r->steps == nullptr)
@@ -93,6 +100,7 @@ int head_splits(long long row_threads, int heads, int sms, int* per_split) {
   const long long want = static_cast<long long>(sms) * 4096;
   long long splits = (want + row_threads - 1) / row_threads;
   if (splits > heads) splits = heads;
+  if (splits > 65535) splits = 65535;  // blockIdx.y
   int per = static_cast<int>((heads + splits - 1) / splits);
   if (per > 1) per = (per + kRopeUnroll - 1) / kRopeUnroll * kRopeUnroll;
   *per_split = per;
@@ -128,6 +136,7 @@ attn_status run_rope(int32_t B, int64_t N, int32_t D, const attn_rope_spec* rope
     const int64_t sizes[3] = {B, t.H, N};
     const bool xs8 = take_strides(t.x_stride, sizes, 3, a.xs), ys8 = take_strides(t.y_stride, sizes, 3, a.ys);
     if (t.x == t.y && std::memcmp(a.xs, a.ys, sizeof(a.xs)) != 0) return ATTN_ERR_INVALID_ARG;
+    if (shares_places(sizes, 3, a.ys)) return ATTN_ERR_INVALID_ARG;
     vec = vec && xs8 && ys8 && aligned16(t.x) && aligned16(t.y);
   }
   if (p.heads == 0) return ATTN_OK;
@@ -148,7 +157,6 @@ attn_status run_rope(int32_t B, int64_t N, int32_t D, const attn_rope_spec* rope
   p.n_seq = n_seq;
   const int items = vec ? D / 16 : D - p.r.rot / 2;
   const int splits = head_splits(p.rows * items, p.heads, d.sms, &p.heads_per_split);
-  if (splits > 65535) return ATTN_ERR_UNSUPPORTED;
   if (launch_rope(p, vec, f16, splits, static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
   count_launch(1);
   return ATTN_OK;
@@ -196,8 +204,11 @@ attn_status run_append(const attn_paged_cache* c, const attn_paged_new* n, const
   if (n->q != nullptr) {
     const bool q8 = take_strides(n->q_stride, q_sizes, 2, p.qs), o8 = take_strides(n->q_out_stride, q_sizes, 2, p.qos);
     if (n->q == n->q_out && std::memcmp(p.qs, p.qos, sizeof(p.qs)) != 0) return ATTN_ERR_INVALID_ARG;
+    if (shares_places(q_sizes, 2, p.qos)) return ATTN_ERR_INVALID_ARG;
     vec = vec && q8 && o8 && aligned16(n->q) && aligned16(n->q_out);
   }
+  const int64_t pool_sizes[3] = {c->n_pages, c->Hkv, c->page_size};
+  if (shares_places(pool_sizes, 3, p.kp) || shares_places(pool_sizes, 3, p.vp)) return ATTN_ERR_INVALID_ARG;
   Device d;
   st = device(&d);
   if (st != ATTN_OK) return st;
@@ -225,7 +236,6 @@ attn_status run_append(const attn_paged_cache* c, const attn_paged_new* n, const
   if (heads > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   const int qk = vec ? p.Dqk / 16 : p.Dqk - p.r.rot / 2, v = vec ? p.Dv / 16 : p.Dv;
   const int splits = head_splits(p.T * (qk > v ? qk : v), static_cast<int>(heads), d.sms, &p.heads_per_split);
-  if (splits > 65535) return ATTN_ERR_UNSUPPORTED;
   if (launch_append(p, vec, f16, splits, static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
   count_launch(1);
   return ATTN_OK;
@@ -376,6 +386,7 @@ attn_status attn_rope_freqs(const attn_rope_freq* f, double* inv_freq) {
   if (kind == ATTN_ROPE_SCALE_BASE) {
     if (f->rot_dim == 2) return ATTN_ERR_INVALID_ARG;  // one frequency, the highest: the base has no say
     base *= std::pow(f->factor, static_cast<double>(f->rot_dim) / (f->rot_dim - 2));
+    if (!(base > 0) || !std::isfinite(base)) return ATTN_ERR_INVALID_ARG;
   }
   if (kind == ATTN_ROPE_SCALE_BY_PARTS &&
       (!(f->orig_len > 0) || !std::isfinite(f->orig_len) || !(f->low_turns >= 0) ||
@@ -390,6 +401,7 @@ attn_status attn_rope_freqs(const attn_rope_freq* f, double* inv_freq) {
       keep = keep < 0 ? 0 : (keep > 1 ? 1 : keep);
       w = w * keep + w / f->factor * (1 - keep);
     }
+    if (!std::isfinite(w)) return ATTN_ERR_INVALID_ARG;
     inv_freq[i] = w;
   }
   return ATTN_OK;

@@ -16,10 +16,11 @@
 // thread owns two 16-byte pieces of one token, half a row (of the rotated
 // part, or of the rest) apart: the pieces that turn together where pairs are
 // half-split, and neighbouring threads on neighbouring pieces in any case.
-// It computes its eight angles once, behind the first loads, and walks over the heads with them in registers,
-// two heads of 16-byte loads in flight and four blocks on an SM (four heads
-// and two blocks were slower: 47 us for 45); a table of cos and sin, the
-// alternative, is a second stream to read and has to end at some position.
+// It computes its eight angles once, behind the first loads, and walks over
+// the heads with them in registers, two heads of 16-byte loads in flight and
+// four blocks on an SM (four heads and two blocks were slower: 47 us for 45);
+// a table of cos and sin, the alternative, is a second stream to read and has
+// to end at some position.
 #include "attn_paged_kernels.h"
 #include "ptx.cuh"
 
@@ -159,8 +160,9 @@ __device__ __forceinline__ void walk_heads_scalar(const uint16_t* x, long long x
 }
 
 // The sequence of packed token t, the last b < n_seq with offsets[b] <= t,
-// for a whole warp whose first lane has its first token: 32 offsets at a
-// time for that token, then step by step.  All lanes take part.
+// for a whole warp: 32 offsets at a time for the first lane's token, then
+// step by step for the others', which lie behind it (or have no part in the
+// answer and lie before).  All lanes take part.
 __device__ __forceinline__ int sequence_of(const int* offsets, int n_seq, long long t) {
   const int lane = threadIdx.x & 31;
   const long long t0 = __shfl_sync(0xffffffffu, t, 0);
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
   const int row_in_block = threadIdx.x / per_row;
   long long row = static_cast<long long>(blockIdx.x) * (kThreads / per_row) + row_in_block;
   const bool idle = row_in_block >= kThreads / per_row || row >= p.rows;
-  if (idle) row = p.rows - 1;  // (takes part in the search)
+  if (idle) row = static_cast<long long>(blockIdx.x) * (kThreads / per_row);  // (takes part in the search)
   const long long b = p.N == p.rows ? 0 : row / p.N;
   const long long n = row - b * p.N;
   int pos = static_cast<int>(n);
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const __grid_
   const int row_in_block = threadIdx.x / per_row;
   long long t = static_cast<long long>(blockIdx.x) * (kThreads / per_row) + row_in_block;
   const bool none = row_in_block >= kThreads / per_row || t >= p.T;
-  if (none) t = p.T - 1;  // (takes part in the search)
+  if (none) t = static_cast<long long>(blockIdx.x) * (kThreads / per_row);  // (takes part in the search)
   const int item = threadIdx.x - row_in_block * per_row;  // items <= 256: every one has its thread
 
   // the token's sequence and position

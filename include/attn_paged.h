@@ -63,9 +63,10 @@ typedef struct {
 /* One tensor: x is read and y written, both [batch, head, token, D] by
  * strides (batch, head, token) in elements, the D elements of a row
  * contiguous.  y == x with equal strides rotates in place; any other
- * overlap is undefined.  Rows that are 16-byte aligned (pointer and
- * strides), with D and rot_dim multiples of 16, move in 16-byte accesses;
- * others element by element. */
+ * overlap is undefined, and a y stride of 0 over more than one element is
+ * refused.  Rows that are 16-byte aligned (pointer and strides), with D and
+ * rot_dim multiples of 16, move in 16-byte accesses; others element by
+ * element. */
 typedef struct {
   const void* x;
   void* y;
@@ -178,7 +179,9 @@ typedef struct {
  * one without a position (more tokens than seq_lens[b]) write nothing to
  * the cache and zeros to q_out; the latter, and a token whose position lies
  * behind the table's row or whose page is not in [0, n_pages), is reported
- * as ATTN_ERR_PAGE.  No two tokens of one call may share a place in the pool. */
+ * as ATTN_ERR_PAGE.  No two tokens of one call may share a place in the
+ * pool; pools or a q_out with a stride of 0 over more than one element are
+ * refused (a decode may read such pools). */
 attn_status attn_paged_append(const attn_paged_cache* cache, const attn_paged_new* tokens,
                               const attn_rope_spec* rope, void* stream);
 attn_status attn_paged_append_f16(const attn_paged_cache* cache, const attn_paged_new* tokens,
@@ -194,10 +197,12 @@ attn_status attn_paged_append_f16(const attn_paged_cache* cache, const attn_page
  *
  * sm_scale: NaN selects Dqk^-1/2, else positive and finite.  An idle place
  * gets O = 0 and LSE = -inf; its q is not read.  Whatever a page holds
- * behind a sequence's last token is never used.  A length outside
- * [0, max_pages * page_size] counts as the nearer bound, and a page not in
- * [0, n_pages) as keys and values of zero; both are reported as
- * ATTN_ERR_PAGE.
+ * behind a sequence's last token is never used.  A NaN among a head's keys
+ * and values gives NaN, an infinite value infinity or NaN (probabilities are
+ * multiplied in two parts, one of which may be 0 or negative); scores of
+ * -inf have no weight, and a head with no others gets 0 and -inf.  A length outside [0, max_pages * page_size]
+ * (2^30 at most) counts as the nearer bound, and a page not in [0, n_pages)
+ * as keys and values of zero; both are reported as ATTN_ERR_PAGE.
  *
  * workspace: 16-byte aligned device memory of attn_paged_decode_workspace()
  * bytes (from the same cache and Hq, on the current device; 0 on an error)

@@ -800,3 +800,40 @@ def test_decode_many_short_sequences(dims, group, lens):
     check_decode(pool, q, o, lse)
     o2, lse2 = binding.attn_paged_decode(pool.cache, q)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("D,rot", [(96, 96), (48, 32), (80, 40)])
+def test_rope_jagged_rows_that_do_not_fill_a_block(D, rot):
+    # threads behind a block's last row; more sequences than a warp's search takes at once
+    r = np.random.RandomState(D)
+    lens = [int(x) for x in r.randint(0, 4, 1500)]
+    T = sum(lens)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    x = randn((2, T, D), BF, D)
+    rope = binding.Rope(rot)
+    (y,) = binding.attn_rope([x], rope, offsets=off)
+    pos = torch.tensor(np.concatenate([np.arange(n) for n in lens]), dtype=torch.int32, device="cuda")
+    (z,) = binding.attn_rope([x[None]], rope, positions=pos)
+    assert torch.equal(y, z[0])
+
+
+@pytest.mark.parametrize("group", [4, 40])
+@pytest.mark.parametrize("bad", ["nan key", "nan value", "inf value"])
+def test_decode_nonfinite_entries_stay_with_their_key_head(group, bad):
+    pool = Pool([200, 90], 2, 64, 64, 16, BF, seed=group)
+    q = randn((2, 2 * group, 64), BF, group)
+    o, lse = binding.attn_paged_decode(pool.cache, q)
+    page = int(pool.table[0, 3])  # sequence 0, tokens 48 .. 63
+    x = pool.k if bad == "nan key" else pool.v
+    x[page, 1, 5, 7] = float("inf") if bad == "inf value" else float("nan")
+    o2, lse2 = binding.attn_paged_decode(pool.cache, q)
+    assert torch.equal(o[1], o2[1]) and torch.equal(o[0, :group], o2[0, :group])
+    assert torch.equal(lse[1], lse2[1]) and torch.equal(lse[0, :group], lse2[0, :group])
+    if bad == "nan key":
+        assert torch.isnan(o2[0, group:]).all() and torch.isnan(lse2[0, group:]).all()
+    else:
+        hit = torch.arange(64, device="cuda") == 7
+        # a probability is the sum of two parts, and the second may have any sign: infinity or NaN
+        assert (torch.isnan(o2[0, group:, hit]) | (torch.isinf(o2[0, group:, hit]) & (bad == "inf value"))).all()
+        assert torch.equal(o2[0, group:][:, ~hit], o[0, group:][:, ~hit])
+        assert torch.equal(lse, lse2)

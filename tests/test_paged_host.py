@@ -95,7 +95,8 @@ def test_frequency_refusals(L):
     assert L.attn_rope_freqs(None, None) == INVALID
     for bad in (dict(rot=0), dict(rot=7), dict(rot=8, base=0.0), dict(rot=8, base=math.inf), dict(rot=8, scaling=4),
                 dict(rot=8, scaling=-1), dict(rot=8, scaling=1, factor=0.0), dict(rot=8, scaling=3, factor=2.0),
-                dict(rot=8, scaling=3, factor=2.0, orig=4096.0, low=4.0, high=4.0)):
+                dict(rot=8, scaling=3, factor=2.0, orig=4096.0, low=4.0, high=4.0),
+                dict(rot=8, scaling=2, base=1e300, factor=1e300), dict(rot=8, scaling=1, factor=5e-324)):
         assert _freqs(L, **bad)[0] == INVALID, bad
 
 
@@ -140,7 +141,9 @@ def _rope_call(L, B=1, N=4, D=64, rot=64, n=1, steps=FAKE, scale=1.0, x=FAKE, y=
     (dict(scale=math.inf), INVALID), (dict(scale=math.nan), INVALID), (dict(x=None), INVALID), (dict(y=None), INVALID),
     (dict(x=FAKE + 1), MISALIGNED), (dict(H=-1), INVALID), (dict(y=FAKE, ys=(512, 64, 128)), INVALID),
     (dict(B=2, offsets=FAKE, n_seq=1), INVALID), (dict(offsets=FAKE, n_seq=-1), INVALID),
-    (dict(offsets=FAKE + 2, n_seq=1), MISALIGNED), (dict(positions=FAKE), INVALID), (dict(N=1 << 31), INVALID)])
+    (dict(offsets=FAKE + 2, n_seq=1), MISALIGNED), (dict(positions=FAKE), INVALID), (dict(N=1 << 31), INVALID),
+    (dict(ys=(512, 0, 64)), INVALID), (dict(ys=(512, 256, 0)), INVALID),
+    (dict(y=FAKE, xs=(512, 0, 64), ys=(512, 0, 64)), INVALID)])
 def test_rope_refuses(L, bad, want):
     assert _rope_call(L, **bad) == want
 
@@ -212,10 +215,17 @@ def test_decode_refuses(L, bad, want):
 @pytest.mark.parametrize("bad,want", [
     (dict(T=-1), INVALID), (dict(T=3), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
     (dict(q_out=None), INVALID), (dict(Hq=-1), INVALID), (dict(k=FAKE + 1), MISALIGNED),
-    (dict(offsets=FAKE + 2), MISALIGNED), (dict(q_out_stride=(512, 64)), INVALID)])
+    (dict(offsets=FAKE + 2), MISALIGNED), (dict(q_out_stride=(512, 64)), INVALID),
+    (dict(q_stride=(256, 0), q_out_stride=(256, 0)), INVALID)])
 def test_append_refuses(L, bad, want):
     assert _append_call(L, None) == INVALID
     assert _append_call(L, _cache(), **bad) == want
+
+
+@pytest.mark.parametrize("strides", [(0, 1024, 64), (2048, 0, 64), (2048, 1024, 0)])
+def test_append_refuses_pools_that_share_places(L, strides):
+    assert _append_call(L, _cache(k_stride=strides)) == INVALID
+    assert _append_call(L, _cache(v_stride=strides)) == INVALID
 
 
 def test_append_refuses_a_wide_rotation(L):
