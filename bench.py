@@ -88,12 +88,14 @@ def kernel_source_hash(backward: bool = False) -> str:
     """Hash of the code a line's kernels are built from: the sources with
     comments and blank lines removed, so an edit of the comments keeps the
     hash (and the profiles recorded for it).  The forward kernels do not
-    include the backward's files."""
+    include the backward's files, and neither those of the rotation and the
+    paged cache."""
     h = hashlib.sha256()
     files = sorted(glob.glob(os.path.join(ROOT, "attention_forward_jvp_gb300", "csrc", "*")))
     if not backward:
         files = [f for f in files if not os.path.basename(f).startswith("attn_bwd")]
     files += sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
+    files = [f for f in files if not os.path.basename(f).startswith(("attn_decode", "attn_paged", "attn_rope"))]
     for f in files:
         with open(f, encoding="utf-8") as fh:
             h.update(os.path.basename(f).encode())
