@@ -75,7 +75,6 @@ class AttnRopeTensor(ctypes.Structure):
                 ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
 
 
-
 class AttnRopeFreq(ctypes.Structure):
     _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
                 ("factor", ctypes.c_double), ("orig_len", ctypes.c_double), ("low_turns", ctypes.c_double),
@@ -577,7 +576,7 @@ def _call_on(dev, fn, *args):
     # (the handle alone: torch.cuda.current_stream builds an object around it,
     # at two thirds of the cost of the call)
     stream = torch._C._cuda_getCurrentRawStream(i)
-    if torch.cuda.current_device() == i:
+    if torch._C._cuda_getDevice() == i:
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -665,8 +664,9 @@ def attn_rope(tensors, rope: Rope, positions: Optional[torch.Tensor] = None, off
     jagged = offsets is not None
     if nd != (3 if jagged else 4):
         raise ValueError("tensors must be [B, H, N, D], or [H, T, D] with offsets")
-    B = 1 if jagged else x0.shape[0]
-    N, D = x0.shape[-2], x0.shape[-1]
+    _need_cuda(x0, "every tensor", dt)
+    s0 = x0.shape
+    B, H0, N, D = (1, *s0) if jagged else s0
     if rope.rot_dim > D:
         raise ValueError(f"rot_dim {rope.rot_dim} exceeds the head dim {D}")
     if rope.steps.device != dev:
@@ -682,21 +682,28 @@ def attn_rope(tensors, rope: Rope, positions: Optional[torch.Tensor] = None, off
     words = []  # of an array of AttnRopeTensor (H's upper half is padding; the hosts are little-endian)
     made = []
     for i, x in enumerate(tensors):
-        xs, sx = x.stride(), x.shape
-        if x.dtype != dt or x.device != dev or dev.type != "cuda" or xs[-1] != 1:
-            _need_cuda(x, "every tensor", dt, dev)
-        if len(sx) != nd or sx[-2] != N or sx[-1] != D or (not jagged and sx[0] != B):
-            raise ValueError("the tensors must agree in all but their heads")
+        xs, H = x.stride(), H0
+        if x is not x0:
+            if x.dtype is not dt or x.device != dev or xs[-1] != 1:
+                _need_cuda(x, "every tensor", dt, dev)
+            sx = x.shape
+            H = sx[nd - 3]
+            if sx != s0 and (len(sx) != nd or sx[-2:] != s0[-2:] or (not jagged and sx[0] != B)):
+                raise ValueError("the tensors must agree in all but their heads")
         if out is None:
-            y = torch.empty_like(x) if x.is_contiguous() else torch.empty(sx, dtype=dt, device=dev)
+            if x.is_contiguous():
+                y, ys = torch.empty_like(x), xs
+            else:
+                y = torch.empty(x.shape, dtype=dt, device=dev)
+                ys = y.stride()
             made.append(y)
         else:
             y = out[i]
-        ys = y.stride()
+            ys = y.stride()
         if jagged:
-            words += (x.data_ptr(), y.data_ptr(), sx[0], 0, xs[0], xs[1], 0, ys[0], ys[1])
+            words += (x.data_ptr(), y.data_ptr(), H, 0, xs[0], xs[1], 0, ys[0], ys[1])
         else:
-            words += (x.data_ptr(), y.data_ptr(), sx[1], xs[0], xs[1], xs[2], ys[0], ys[1], ys[2])
+            words += (x.data_ptr(), y.data_ptr(), H, xs[0], xs[1], xs[2], ys[0], ys[1], ys[2])
     if out is None:
         out = tuple(made)
     arr = array("q", words)
@@ -718,8 +725,8 @@ def attn_rope(tensors, rope: Rope, positions: Optional[torch.Tensor] = None, off
             raise ValueError("offsets must be [B + 1]")
         off, n_seq = offsets.data_ptr(), offsets.numel() - 1
     L = lib()
-    _call_on(dev, L.attn_rope_f16 if dt == torch.float16 else L.attn_rope, B, N, D, rope._ref, arr.buffer_info()[0], n, pos, ps, off,
-             n_seq, 1 if inverse else 0)
+    _call_on(dev, L.attn_rope_f16 if dt == torch.float16 else L.attn_rope, B, N, D, rope._ref, arr.buffer_info()[0],
+             n, pos, ps, off, n_seq, 1 if inverse else 0)
     return out
 
 
@@ -779,7 +786,7 @@ def attn_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, rope:
     contiguous rows; a jagged [H, T, D] tensor goes in as its transpose(0, 1)."""
     dev, dt = cache.device, cache.dtype
     for name, t in (("k", k), ("v", v), ("q", q)):
-        if t is not None and (t.dtype != dt or t.device != dev or t.stride(-1) != 1):
+        if t is not None and (t.dtype is not dt or t.device != dev or t.stride(-1) != 1):
             _need_cuda(t, name, dt, dev)
     T = k.shape[0]
     if k.shape != (T, cache.Hkv, cache.Dqk) or v.shape != (T, cache.Hkv, cache.Dv):
@@ -825,12 +832,12 @@ def attn_paged_decode(cache: PagedCache, q: torch.Tensor, sm_scale: Optional[flo
     reads key head h // (Hq / Hkv)).  Returns (o [B, Hq, Dv], lse [B, Hq]
     float32, natural log).  An idle place (length 0) gets o = 0, lse = -inf."""
     dev, dt, B = cache.device, cache.dtype, cache.B
-    qs = q.stride()
-    if q.dtype != dt or q.device != dev or qs[-1] != 1:
+    qs, sq = q.stride(), q.shape
+    if q.dtype is not dt or q.device != dev or qs[-1] != 1:
         _need_cuda(q, "q", dt, dev)
-    if len(qs) != 3 or q.shape[0] != B or q.shape[2] != cache.Dqk:
+    if len(sq) != 3 or sq[0] != B or sq[2] != cache.Dqk:
         raise ValueError(f"q must be [{B}, Hq, {cache.Dqk}]")
-    Hq = q.shape[1]
+    Hq = sq[1]
     if cache.Hkv == 0 or Hq % cache.Hkv:
         raise ValueError(f"the cache's {cache.Hkv} key heads must divide the {Hq} query heads")
     if out is None:

@@ -161,6 +161,14 @@ def test_rope_jagged(lens, T, inter, given):
         assert b[:, n:].isnan().all()
 
 
+def test_rope_of_tensors_given_twice():
+    r = binding.Rope(64)
+    q, k = randn((2, 6, 9, 64), BF, 0), randn((2, 2, 9, 64), BF, 1)
+    (a,), (b,) = binding.attn_rope([q], r), binding.attn_rope([k], r)
+    for x, want in zip(binding.attn_rope([q, k, q, k], r), (a, b, a, b)):
+        assert torch.equal(x, want)
+
+
 def test_rope_inverse_transposes():
     # <R x, g> = <x, R^T g>: each side sums products whose rounded factor is
     # off by u relative (2^-11)
