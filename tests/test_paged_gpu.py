@@ -845,3 +845,30 @@ def test_decode_nonfinite_entries_stay_with_their_key_head(group, bad):
         assert (torch.isnan(o2[0, group:, hit]) | (torch.isinf(o2[0, group:, hit]) & (bad == "inf value"))).all()
         assert torch.equal(o2[0, group:][:, ~hit], o[0, group:][:, ~hit])
         assert torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("group", [2, 20])
+def test_decode_of_a_table_whose_steps_pass_31_bits(group):
+    # the rows of the table are as long as the struct says only where a length reaches: planned in 64 bits, the
+    # same ranges and results
+    r = np.random.RandomState(group)
+    pool = Pool([int(x) for x in r.randint(0, 300, 40)], 2, 64, 64, 16, BF, seed=group)
+    q = randn((40, 2 * group, 64), BF, group)
+    o, lse = binding.attn_paged_decode(pool.cache, q)
+    pool.cache._struct.max_pages = 1 << 26
+    o2, lse2 = binding.attn_paged_decode(pool.cache, q)
+    check_decode(pool, q, o2, lse2)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("group", [2, 20])
+def test_decode_of_an_empty_pool(group):
+    k = torch.empty((0, 2, 16, 64), dtype=BF, device="cuda")
+    table, lens = torch.zeros((3, 4), dtype=torch.int32, device="cuda"), [50, 0, 7]
+    cache = binding.PagedCache(k, k, table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    o, lse = binding.attn_paged_decode(cache, randn((3, 2 * group, 64), BF, 0))
+    assert binding.sync_check() == 6
+    assert (o == 0).all()
+    for b, n in enumerate(lens):  # keys of zero: every score is 0
+        want = np.log(n) if n else -np.inf
+        assert (f64(lse[b]) == want).all() if n == 0 else (np.abs(f64(lse[b]) - want) <= 2.0**-20).all()
