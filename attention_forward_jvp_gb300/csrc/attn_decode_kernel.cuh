@@ -41,23 +41,59 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool l
   const int n = live ? 16 : 0;  // 0: the 16 bytes are zeroed, nothing is read
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-// Pieces q4, q4 + 4, .. of one row of D elements (d of them real) into a
-// 128-byte swizzled row: `dst` is where piece q4 goes, STEP bytes lie from one
-// 64-element chunk to the next.  A row that is not live, and what is behind d,
-// becomes zeros.  `any` is an address of D readable elements, or (full
-// false) of one piece.
-template <int D, int STEP>
-__device__ __forceinline__ void copy_row(uint32_t dst, const uint16_t* row, const uint16_t* any, bool live, bool full,
-                                         int q4, int d) {
-  if (full) {  // one address a row, the rest are constants
-    const uint16_t* src = live ? row : any;
+// 16 neighbouring tokens of a sequence, of which n are live.  Where pages hold
+// a multiple of 16 tokens (`whole`) they lie in one page, from slot `slot` on;
+// else lanes r and r + 16 have the page and slot of token r.
+struct DecodePlace {
+  int page, slot, n;
+};
+__device__ __forceinline__ DecodePlace decode_lookup(const DecodeParams& p, bool whole, const int* pages, int first, int len) {
+  DecodePlace x;
+  const int key = whole ? first : first + (threadIdx.x & 15);
+  x.n = len - first;
+  x.page = x.slot = 0;
+  if (key < len) {
+    const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+    x.slot = key - e * p.page_size;
+    x.page = pages[e];
+  }
+  return x;
+}
+// Reports a page out of range (apart from the look-up, whose load is on its way)
+__device__ __forceinline__ void decode_report(const DecodeParams& p, bool whole, const DecodePlace& x) {
+  const int row = whole ? 0 : threadIdx.x & 15;
+  if (row < x.n && static_cast<unsigned>(x.page) >= static_cast<unsigned>(p.n_pages)) *p.err = 1;
+}
+// Their rows of D elements (d of them real) of one pool, by a warp, into
+// 128-byte swizzled rows PITCH bytes apart (64-element chunks CHUNK apart).
+// Rows that are not live or have no page, and what is behind d, become zeros.
+// An instruction moves whole rows, so that every request is for a full line:
+// with 64 bytes of 8 rows to an instruction instead, the same traffic took 2
+// to 5 % longer (64 sequences of up to 8192: 191 us for 186.5).
+template <int D, int PITCH, int CHUNK>
+__device__ __forceinline__ void copy_rows(const DecodeParams& p, bool whole, const DecodePlace& x,
+                                          const uint16_t* head, const long long (&st)[3], int d, uint32_t to) {
+  constexpr int L = D / 8 < 32 ? D / 8 : 32, R = 32 / L;  // lanes of a row, rows of an instruction
+  const int lane = threadIdx.x & 31, lr = lane / L, c = lane % L;
+  to += (c >> 3) * CHUNK + lr * PITCH + (((c & 7) ^ lr) << 4);
+  const bool has = static_cast<unsigned>(x.page) < static_cast<unsigned>(p.n_pages);
+  if (whole) {
+    const int n = has && 8 * c < d ? x.n : 0;
+    const uint16_t* from = head + x.page * st[0] + (x.slot + lr) * st[2] + 8 * c;
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) cp_async16((dst ^ ((j & 1) << 6)) + (j >> 1) * STEP, src + 32 * j, live);
+    for (int i = 0; i < 16; i += R) {
+      const bool live = i + lr < n;
+      cp_async16((to ^ ((i & 7) << 4)) + i * PITCH, live ? from : p.q, live);
+      from += R * st[2];
+    }
   } else {
+    const unsigned rows = __ballot_sync(0xffffffffu, has && (lane & 15) < x.n) >> lr;
+    const long long at = x.page * st[0] + x.slot * st[2];
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      const bool in = live && 32 * j + 8 * q4 < d;
-      cp_async16((dst ^ ((j & 1) << 6)) + (j >> 1) * STEP, in ? row + 32 * j : any, in);
+    for (int i = 0; i < 16; i += R) {
+      const long long row = __shfl_sync(0xffffffffu, at, i + lr);
+      const bool live = (rows >> i & 1u) && 8 * c < d;
+      cp_async16((to ^ ((i & 7) << 4)) + i * PITCH, live ? head + row + 8 * c : p.q, live);
     }
   }
 }
@@ -313,7 +349,9 @@ struct DecodePlan {
   static_assert(NW >= 4 && S >= 2 && 8 * PITCH * 4 <= STAGE && NT * 8 * (PITCH * 4 + 8) <= S * STAGE, "decode plan");
 };
 
-template <int DQ, int DV, bool F16, int NT>
+// WHOLE: pages of a multiple of 16 tokens (a choice made in the loop instead
+// costs what whole rows gain).
+template <int DQ, int DV, bool F16, int NT, bool WHOLE>
 __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     attn_decode_kernel(const __grid_constant__ DecodeParams p) {
   using P = DecodePlan<DQ, DV, NT>;
@@ -360,26 +398,13 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     }
   };
   const int mi = lane >> 3, l8 = lane & 7, g = lane >> 2, q4 = lane & 3;
-  // where rows g and g + 8 of a step lie: page, token in it (-1: behind the
-  // end of the sequence), key head
-  struct Place {
-    int page[2], slot[2], h;
+  // where the tokens of a step lie, and its key head
+  struct Place : DecodePlace {
+    int h;
   };
   auto lookup = [&](const Cursor& a) -> Place {
-    Place x;
-    x.h = p.chunks == 1 ? a.hu : a.hu / p.chunks;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int key = a.t * BN + g + 8 * r;
-      x.page[r] = 0;
-      x.slot[r] = -1;
-      if (key < a.len) {
-        const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-        x.slot[r] = key - e * p.page_size;
-        x.page[r] = p.page_table[a.b * p.table_stride + e];
-      }
-    }
-    return x;
+    return {decode_lookup(p, WHOLE, p.page_table + a.b * p.table_stride, a.t * BN, a.len),
+            p.chunks == 1 ? a.hu : a.hu / p.chunks};
   };
 
   // ---- this warp's range, and the places of its first steps, looked up all
@@ -467,22 +492,11 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
 
   clear();
   if (count > 0) {
-    // ---- copies: a lane brings 16-byte pieces q4, q4 + 4, .. of rows g and
-    // g + 8 of a step, so that one instruction moves 64 bytes of 8 rows
-    // (a row behind the end of the sequence has slot -1)
     auto issue = [&](const Place& x, int stage) {
-      const uint32_t kd = ring + stage * P::STAGE + g * KPITCH + ((q4 ^ g) << 4);
-      const uint32_t vd = ring + stage * P::STAGE + P::K_BYTES + g * VPITCH + ((q4 ^ g) << 4);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const bool live = x.slot[r] >= 0 && x.page[r] >= 0 && x.page[r] < p.n_pages;
-        if (!live && x.slot[r] >= 0) *p.err = 1;
-        const long long page = x.page[r], slot = x.slot[r];
-        copy_row<DQ, 128>(kd + r * 8 * KPITCH, p.k + page * p.kp[0] + x.h * p.kp[1] + slot * p.kp[2] + 8 * q4,
-                          (p.full ? p.k : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dqk);
-        copy_row<DV, 128>(vd + r * 8 * VPITCH, p.v + page * p.vp[0] + x.h * p.vp[1] + slot * p.vp[2] + 8 * q4,
-                          (p.full ? p.v : p.q) + 8 * q4 * p.full, live, p.full, q4, p.dv);
-      }
+      const uint32_t to = ring + stage * P::STAGE;
+      decode_report(p, WHOLE, x);
+      copy_rows<DQ, KPITCH, 128>(p, WHOLE, x, p.k + x.h * p.kp[1], p.kp, p.dqk, to);
+      copy_rows<DV, VPITCH, 128>(p, WHOLE, x, p.v + x.h * p.vp[1], p.vp, p.dv, to + P::K_BYTES);
     };
     load_q(cur);
 #pragma unroll
@@ -839,7 +853,7 @@ cudaError_t decode_launch_one(K kernel, const DecodeParams& p, dim3 grid, int th
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int DQ, int DV, bool F16, int NT>
+template <int DQ, int DV, bool F16, int NT, bool WHOLE>
 cudaError_t launch_decode_nt(DecodeParams& p, int ctas, cudaStream_t stream) {
   using P = DecodePlan<DQ, DV, NT>;
   static bool attr_done[64] = {};
@@ -848,7 +862,7 @@ cudaError_t launch_decode_nt(DecodeParams& p, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(attn_decode_kernel<DQ, DV, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
+    e = cudaFuncSetAttribute(attn_decode_kernel<DQ, DV, F16, NT, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
     if (e != cudaSuccess) return e;
     // the same division of the SM's memory as the kernel before it: changing
     // it would have to wait for the SM to drain
@@ -859,7 +873,7 @@ cudaError_t launch_decode_nt(DecodeParams& p, int ctas, cudaStream_t stream) {
   }
   p.cta_warps = P::NW;
   p.join_rows = (p.rows + 7) / 8;  // eight blocks at most share the heads of a CTA's units
-  e = decode_launch_one(attn_decode_kernel<DQ, DV, F16, NT>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
+  e = decode_launch_one(attn_decode_kernel<DQ, DV, F16, NT, WHOLE>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
   if (e != cudaSuccess || !p.split) return e;
   return decode_launch_one(attn_decode_join<DV, F16>, p, dim3(ctas, (p.rows + p.join_rows - 1) / p.join_rows),
                            kJoinWarps * 32, 0, stream);

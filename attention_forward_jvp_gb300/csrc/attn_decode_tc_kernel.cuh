@@ -36,8 +36,6 @@
 #include "attn_decode_kernel.cuh"
 #include "attn_kernel.cuh"
 
-#include <type_traits>
-
 namespace attn {
 
 constexpr int kTcBN = 64, kTcRows = 128;
@@ -196,51 +194,16 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
 
   if (warp >= 8 && warp < P::ISSUER && count > 0) {
     // ------------------------------------------------------------ producers
-    const int g = lane >> 2, q4 = lane & 3, k0 = (warp & 3) * 16;
-    // pages of 16 tokens and more, a power of two of them: the two rows of a
-    // lane, 8 tokens apart, lie in one page
-    const bool one_page = p.page_shift >= 4;
-    const uint16_t *kh = nullptr, *vh = nullptr;  // of the unit: its head's rows, piece q4
+    const int k0 = (warp & 3) * 16;  // this warp's rows of a tile
+    const uint16_t *kh = nullptr, *vh = nullptr;  // of the unit's key head
     const int* pages = nullptr;                   // of the sequence
-    struct Place {
-      int page[2], slot[2];
-    };
     auto enter = [&](const Cursor& a) {
       const int h = p.chunks == 1 ? a.hu : a.hu / p.chunks;
-      kh = p.k + h * p.kp[1] + 8 * q4;
-      vh = p.v + h * p.vp[1] + 8 * q4;
+      kh = p.k + h * p.kp[1];
+      vh = p.v + h * p.vp[1];
       pages = p.page_table + a.b * p.table_stride;
     };
-    auto lookup = [&](const Cursor& a) -> Place {
-      Place x;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int key = a.t * BN + k0 + g + 8 * r;
-        x.page[r] = 0;
-        x.slot[r] = -1;
-        if (key < a.len) {
-          const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-          x.slot[r] = key - e * p.page_size;
-          x.page[r] = r == 1 && one_page ? x.page[0] : pages[e];
-        }
-      }
-      return x;
-    };
-    // both rows of a tile, of the pool with these strides and D (d) elements
-    auto issue = [&](auto width, const Place& x, const uint16_t* head, const long long (&st)[3], const uint16_t* pool, int d,
-                     uint32_t stage) {
-      constexpr int D = decltype(width)::value;
-      const uint32_t to = stage + (k0 + g) * 128 + ((q4 ^ g) << 4);
-      const uint16_t* row = nullptr;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const bool live = x.slot[r] >= 0 && x.page[r] >= 0 && x.page[r] < p.n_pages;
-        if (!live && x.slot[r] >= 0) *p.err = 1;
-        if (r == 1 && one_page) row += 8 * st[2];
-        else row = head + static_cast<long long>(x.page[r]) * st[0] + static_cast<long long>(x.slot[r]) * st[2];
-        copy_row<D, P::SUB>(to + r * 1024, row, (p.full ? pool : p.q) + 8 * q4 * p.full, live, p.full, q4, d);
-      }
-    };
+    auto lookup = [&](const Cursor& a) { return decode_lookup(p, p.whole, pages, a.t * BN + k0, a.len); };
     // the unit's heads; rows behind them, up to the quadrant's end, are zeros
     auto issue_q = [&](const Cursor& a, int qb) {
       int h, g0, n_rows;
@@ -271,7 +234,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
     };
     if (j == 1 && count > 1) step();
     enter(cur);
-    Place next = lookup(cur);
+    DecodePlace next = lookup(cur);
     while (j < count) {
       ok = wait_all(P::B_KE + stage, phase);
       if (!ok) break;
@@ -287,7 +250,8 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
         if (!ok) break;
         issue_q(cur, seg % NQ);
       }
-      issue(std::integral_constant<int, DQ>(), next, kh, p.kp, p.k, p.dqk, base + P::OFF_K + stage * P::K_TILE);
+      decode_report(p, p.whole, next);
+      copy_rows<DQ, 128, P::SUB>(p, p.whole, next, kh, p.kp, p.dqk, base + P::OFF_K + stage * P::K_TILE + k0 * 128);
       // (the failure-detection hook: the first tile never arrives)
       const bool arrives = j > 0 || !p.skip_first_load || blockIdx.x != 0;
       if (P::SPLIT) {
@@ -295,7 +259,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
         ok = wait_all(P::B_VE + stage, phase);
         if (!ok) break;
       }
-      issue(std::integral_constant<int, DV>(), next, vh, p.vp, p.v, p.dv, base + P::OFF_V + stage * P::V_TILE);
+      copy_rows<DV, 128, P::SUB>(p, p.whole, next, vh, p.vp, p.dv, base + P::OFF_V + stage * P::V_TILE + k0 * 128);
       if (P::SPLIT || arrives) cp_async_arrive(bar(P::B_VF + stage));
       j += P::GROUPS;
       if (j >= count) break;
@@ -593,9 +557,13 @@ cudaError_t launch_decode_tc(DecodeParams& p, int ctas, cudaStream_t stream) {
 
 template <int DQ, int DV, bool F16>
 cudaError_t launch_decode(DecodeParams& p, int nt, int ctas, cudaStream_t stream) {
-  if (nt == 1) return launch_decode_nt<DQ, DV, F16, 1>(p, ctas, stream);
+  if (nt == 1)
+    return p.whole ? launch_decode_nt<DQ, DV, F16, 1, true>(p, ctas, stream)
+                   : launch_decode_nt<DQ, DV, F16, 1, false>(p, ctas, stream);
   if constexpr (decode_warp_rows(DQ, DV) > 8)
-    if (nt == 2) return launch_decode_nt<DQ, DV, F16, 2>(p, ctas, stream);
+    if (nt == 2)
+      return p.whole ? launch_decode_nt<DQ, DV, F16, 2, true>(p, ctas, stream)
+                     : launch_decode_nt<DQ, DV, F16, 2, false>(p, ctas, stream);
   return launch_decode_tc<DQ, DV, F16>(p, ctas, stream);
 }
 

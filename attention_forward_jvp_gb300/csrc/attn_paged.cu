@@ -328,7 +328,7 @@ attn_status run_decode(const attn_paged_cache* c, int32_t Hq, const void* q, con
   p.chunks = l.chunks;
   p.dqk = c->Dqk;
   p.dv = c->Dv;
-  p.full = c->Dqk == l.dq && c->Dv == l.dv && c->n_pages > 0 ? 1 : 0;
+  p.whole = c->page_size % kDecodeBN == 0 ? 1 : 0;
   const float scale = std::isnan(sm_scale) ? 1.0f / std::sqrt(static_cast<float>(c->Dqk)) : sm_scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.o = static_cast<uint16_t*>(o);

@@ -83,7 +83,7 @@ struct DecodeParams {
   int Hkv, G;                  // key heads, query heads of each
   int rows, chunks;            // query heads of a work unit, units of a key head
   int dqk, dv;                 // true head dims (<= the kernel's)
-  int full;                    // 1: they are the kernel's, and the pools hold a page
+  int whole;                   // 1: pages hold a multiple of 16 tokens
   float scale_log2;
   uint16_t* o;
   float* lse;
