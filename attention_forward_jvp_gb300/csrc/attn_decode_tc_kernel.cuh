@@ -1,7 +1,7 @@
-// The paged decode for many query heads on a key head (17 and more; 9 and more
-// where both head dims are 256): the same list of steps, ranges and joining as
-// attn_decode_kernel.cuh, with 64-key tiles, a range for each CTA, and the
-// products on tcgen05.
+// The paged decode for many query heads on a key head (more than
+// decode_warp_rows: 9 to 33 and more, by the head dims): the same list of
+// steps, ranges and joining as attn_decode_kernel.cuh, with 64-key tiles, a
+// range for each CTA, and the products on tcgen05.
 //
 //   S (128 x 64)   = Q K^T       Q: the unit's heads as rows, from shared memory
 //   O (128 x Dv)  += P V         P: from tensor memory, V as it lies (MN-major)
@@ -555,15 +555,17 @@ cudaError_t launch_decode_tc(DecodeParams& p, int ctas, cudaStream_t stream) {
                            kJoinWarps * 32, 0, stream);
 }
 
+template <int DQ, int DV, bool F16, int NT = 1>
+cudaError_t launch_decode_warps(DecodeParams& p, int nt, int ctas, cudaStream_t stream) {
+  if constexpr (8 * NT < decode_warp_rows(DQ, DV))
+    if (nt > NT) return launch_decode_warps<DQ, DV, F16, NT + 1>(p, nt, ctas, stream);
+  return p.whole ? launch_decode_nt<DQ, DV, F16, NT, true>(p, ctas, stream)
+                 : launch_decode_nt<DQ, DV, F16, NT, false>(p, ctas, stream);
+}
+
 template <int DQ, int DV, bool F16>
 cudaError_t launch_decode(DecodeParams& p, int nt, int ctas, cudaStream_t stream) {
-  if (nt == 1)
-    return p.whole ? launch_decode_nt<DQ, DV, F16, 1, true>(p, ctas, stream)
-                   : launch_decode_nt<DQ, DV, F16, 1, false>(p, ctas, stream);
-  if constexpr (decode_warp_rows(DQ, DV) > 8)
-    if (nt == 2)
-      return p.whole ? launch_decode_nt<DQ, DV, F16, 2, true>(p, ctas, stream)
-                     : launch_decode_nt<DQ, DV, F16, 2, false>(p, ctas, stream);
+  if (nt > 0) return launch_decode_warps<DQ, DV, F16>(p, nt, ctas, stream);
   return launch_decode_tc<DQ, DV, F16>(p, ctas, stream);
 }
 

@@ -64,11 +64,16 @@ cudaError_t launch_append(const AppendParams& p, bool vec, bool f16, int splits,
 constexpr int kDecodeBN = 16;        // keys of a step
 constexpr int kDecodeMinStepsLog = 1;  // a warp takes two steps at least, where there are two
 constexpr int kDecodeMaxWarps = 16;  // warps of a CTA, at most
-// Query heads of a unit that a warp takes at most; more go to tcgen05.  At 16
-// heads the two take 103 and 112 us (D 128, 32 sequences of 8192), at 24 the
-// warps' 155 and 112; with Dqk = Dv = 256 a warp has no registers left for a
-// second group of 8: 135 and 100 at 16.
-constexpr int decode_warp_rows(int dq, int dv) { return dq + dv < 512 ? 16 : 8; }
+// Query heads of a unit that a warp takes at most, in groups of 8; more go to
+// tcgen05.  Every group is another pass of mma.sync over a step and takes
+// registers by the head dims, so the limit falls with them.  On either side of
+// it, the warps' kernel and tcgen05 (32 sequences of 8192, us, at that many
+// heads): 64/64 119 and 152, 128/64 103 and 113 at 32; 256/64 93 and 98, 64/128
+// 98 and 115, 128/128 106 and 110 at 24; 256/128 93 and 82 at 24; 256/256 135
+// and 100 at 16.
+constexpr int decode_warp_rows(int dq, int dv) {
+  return dv == 64 ? (dq <= 128 ? 32 : 24) : (dv == 128 ? (dq <= 128 ? 24 : 16) : (dq < 256 ? 16 : 8));
+}
 constexpr int kDecodeMaxRows = 128;   // query heads of a unit, at most
 
 struct DecodeParams {
@@ -98,8 +103,8 @@ struct DecodeParams {
   int cta_warps, join_rows;    // warps of a CTA, heads of a joining block (set by the launch)
 };
 
-// The decode kernel for kernel head dims DQ, DV and nt (1 or 2) groups of 8
-// query heads to a unit, or (0) more of them, followed, when p.split, by the
+// The decode kernel for kernel head dims DQ, DV and nt groups of 8 query heads
+// to a unit, or (0) more of them than the warps' kernel takes, followed, when p.split, by the
 // joining kernel.
 template <int DQ, int DV, bool F16>
 cudaError_t launch_decode(DecodeParams& p, int nt, int ctas, cudaStream_t stream);

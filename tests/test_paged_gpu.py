@@ -872,3 +872,26 @@ def test_decode_of_an_empty_pool(group):
     for b, n in enumerate(lens):  # keys of zero: every score is 0
         want = np.log(n) if n else -np.inf
         assert (f64(lse[b]) == want).all() if n == 0 else (np.abs(f64(lse[b]) - want) <= 2.0**-20).all()
+
+
+@pytest.mark.parametrize("dims,group", [((64, 64), 24), ((64, 64), 32), ((128, 64), 30), ((256, 64), 23), ((64, 128), 20),
+                                        ((128, 128), 24), ((32, 16), 29), ((16, 128), 18)])
+@pytest.mark.parametrize("page", [16, 24])
+def test_decode_three_and_four_groups_of_heads(dims, group, page):
+    # lengths about the ends of steps and ranges, one long one; pages of whole steps and not
+    pool = Pool([1, 16, 17, 0, 63, 300, 5000], 2, *dims, page, HF, seed=group + page)
+    q = randn((7, 2 * group, dims[0]), HF, group, 1.5)
+    o, lse = binding.attn_paged_decode(pool.cache, q)
+    check_decode(pool, q, o, lse)
+    o2, lse2 = binding.attn_paged_decode(pool.cache, q)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_decode_of_sequences_that_share_pages():
+    pool = Pool([200, 90, 33], 2, 64, 64, 16, BF, seed=1)
+    pool.table[1] = pool.table[0]
+    pool.table[2, :2] = pool.table[0, :2]
+    pool.table[2, 2] = pool.table[0, 2]
+    for group in (3, 40):
+        q = randn((3, 2 * group, 64), BF, group)
+        check_decode(pool, q, *binding.attn_paged_decode(pool.cache, q))
