@@ -303,6 +303,9 @@ static __device__ __noinline__ void decode_idle(const DecodeParams& p) {
     for (int i = threadIdx.x; i < Hq * (p.dv / 8); i += blockDim.x)
       reinterpret_cast<uint4*>(p.o + static_cast<long long>(b) * Hq * p.dv)[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = threadIdx.x; i < Hq; i += blockDim.x) p.lse[static_cast<long long>(b) * Hq + i] = -INFINITY;
+    if (p.by_unit)
+      for (int i = threadIdx.x; i < p.Hkv * p.chunks; i += blockDim.x)
+        p.desc[b * p.Hkv * p.chunks + i] = make_int4(-1, 0, 0, 0);
   }
 }
 
@@ -311,12 +314,18 @@ static __device__ __noinline__ void decode_idle(const DecodeParams& p) {
 // the first range of each CTA behind, that of the end included (z: how many
 // CTAs lie between, -1 when the unit ends in x's own); and, where the range
 // that it ends in goes on to another unit and is not that first one, in part
-// 0 of that (w, else -1).
+// 0 of that (w, else -1).  `desc` has this by units, with x before (-1: the
+// unit is complete), or by ranges, with the unit before.
+__device__ __forceinline__ void decode_complete(const DecodeParams& p, int b, int hu) {
+  if (p.by_unit) p.desc[b * p.Hkv * p.chunks + hu] = make_int4(-1, 0, 0, 0);
+}
 template <int R>
-__device__ __forceinline__ int4 decode_describe(const DecodeRange& w, int b, int hu, int x, long long end) {
+__device__ __forceinline__ void decode_describe(const DecodeParams& p, const DecodeRange& w, int b, int hu, int x,
+                                                long long end) {
   const int z = static_cast<int>(w.owner(end)), c = x / R, e = z / R;
   const bool own = w.start(z + 1LL) != end + 1 && (e == c || z != e * R);
-  return make_int4(b, hu, e - c - 1, own ? z : -1);
+  if (p.by_unit) p.desc[b * p.Hkv * p.chunks + hu] = make_int4(x, 0, e - c - 1, own ? z : -1);
+  else p.desc[x] = make_int4(b, hu, e - c - 1, own ? z : -1);
 }
 
 // Eight warps with as many stages of 16 keys as shared memory holds (up to
@@ -425,7 +434,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   }
 
   if (w.idle) decode_idle(p);
-  if (p.split && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
+  if (p.split && !p.by_unit && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
   if (w.cta_lo >= w.total) return;
   // (kept in shared memory while the steps need the registers)
   if (lane == 0) ranges[warp] = w;
@@ -621,6 +630,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
         if (!last) {  // (the range's last unit is joined with the other warps' below; this one ends here)
           const long long part = 2LL * me;
           const long long row0 = (static_cast<long long>(cur.b) * p.Hkv + h) * p.G + g0;
+          if (begins && lane == 0) decode_complete(p, cur.b, cur.hu);
           float* scratch = reinterpret_cast<float*>(mine + stage * P::STAGE);  // read; refilled in the next step
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -721,17 +731,19 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     }
     if (begins && ends) {
       write_row((static_cast<long long>(u.x) * p.Hkv + h) * p.G + g0 + r, 4 * c4, o, mm, ll);
+      if (r == 0 && c4 == 0) decode_complete(p, u.x, u.y);
     } else {
       *reinterpret_cast<float4*>(p.part_o + (part * p.rows + r) * DV + 4 * c4) = o;
       if (c4 == 0) p.part_ml[part * p.rows + r] = make_float2(mm, ll);
-      if (r == 0 && c4 == 0 && begins) p.desc[first + w0] = decode_describe<NW>(w, u.x, u.y, first + w0, end);
+      if (r == 0 && c4 == 0 && begins) decode_describe<NW>(p, w, u.x, u.y, first + w0, end);
     }
   }
 }
 
-// Joins the parts of the units that several warps of the kernel above share:
-// block (c, y) takes some heads (the y-th part of them) of the units that
-// begin in CTA c and end in another warp.  A warp takes a head of one unit,
+// Joins the parts of the units that several ranges of the kernels above share:
+// block (c, y) takes some heads (the y-th part of them) of unit c, or, where
+// there are more units than CTAs, of those that begin in CTA c and end in
+// another range.  A warp takes a head of one unit,
 // or its parts together with other warps when there are fewer heads than
 // warps; U parts' rows are on their way at a time.
 constexpr int kJoinWarps = 8;
@@ -750,7 +762,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
   const int r0 = blockIdx.y * p.join_rows, rows = min(p.join_rows, p.rows - r0);
   griddep_wait();
   griddep_launch_dependents();
-  if (warp == 0) {
+  if (p.by_unit) {
+    if (threadIdx.x == 0) {
+      const int4 d = p.desc[blockIdx.x];
+      const int hu = p.Hkv * p.chunks, b = blockIdx.x / hu;
+      // (a wait that ran out of time may have left it unwritten)
+      const bool sound = d.x >= 0 && d.x < p.ranges && d.z >= -1 && d.z + 1 < p.ranges / cw - d.x / cw && d.w >= -1 &&
+                         d.w < p.ranges;
+      units[0] = make_int4(b, blockIdx.x - b * hu, d.z, d.w);
+      from[0] = d.x;
+      n_units = sound ? 1 : 0;
+    }
+  } else if (warp == 0) {
     int4 d = make_int4(-1, 0, 0, 0);
     if (lane < cw) d = p.desc[blockIdx.x * cw + lane];
     const unsigned have = __ballot_sync(ALL, d.x >= 0);
@@ -773,9 +796,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
     const int h = p.chunks == 1 ? d.y : d.y / p.chunks, g0 = (d.y - h * p.chunks) * p.rows;
     on = on && g0 + r < p.G;  // (the last units of a key head may have fewer)
     // parts, in order (decode_describe)
-    const int parts = d.z + 2 + (d.w >= 0 ? 1 : 0);
+    const int parts = d.z + 2 + (d.w >= 0 ? 1 : 0), c0 = on ? from[u] / cw : 0;
     auto row_of = [&](int i) {
-      const int w = i == 0 ? from[u] : (i <= d.z + 1 ? (blockIdx.x + i) * cw : d.w);
+      const int w = i == 0 ? from[u] : (i <= d.z + 1 ? (c0 + i) * cw : d.w);
       return (2 * w + (i == 0 ? 1 : 0)) * p.rows + r;
     };
     float m = -INFINITY, l = 0.f, acc[VPL];
@@ -853,6 +876,22 @@ cudaError_t decode_launch_one(K kernel, const DecodeParams& p, dim3 grid, int th
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// Blocks of the join: about two an SM, which are resident at a time (eight for
+// each CTA, most of them without a unit, took four rounds: 32 sequences of
+// 8192, D 128, 8 heads 95.7 us for 90, 64 heads 118 for 109).
+inline void plan_join(DecodeParams& p, int ctas) {
+  const long long units = static_cast<long long>(p.B) * p.Hkv * p.chunks;
+  p.ranges = ctas * p.cta_warps;
+  p.by_unit = p.split && units <= ctas ? 1 : 0;
+  const int blocks = 2 * ctas / static_cast<int>(p.by_unit ? units : ctas);  // for the heads of a unit
+  p.join_rows = (p.rows + blocks - 1) / blocks;
+}
+template <int DV, bool F16>
+cudaError_t launch_join(const DecodeParams& p, int ctas, cudaStream_t stream) {
+  const dim3 grid(p.by_unit ? p.B * p.Hkv * p.chunks : ctas, (p.rows + p.join_rows - 1) / p.join_rows);
+  return decode_launch_one(attn_decode_join<DV, F16>, p, grid, kJoinWarps * 32, 0, stream);
+}
+
 template <int DQ, int DV, bool F16, int NT, bool WHOLE>
 cudaError_t launch_decode_nt(DecodeParams& p, int ctas, cudaStream_t stream) {
   using P = DecodePlan<DQ, DV, NT>;
@@ -872,11 +911,10 @@ cudaError_t launch_decode_nt(DecodeParams& p, int ctas, cudaStream_t stream) {
     attr_done[dev] = true;
   }
   p.cta_warps = P::NW;
-  p.join_rows = (p.rows + 7) / 8;  // eight blocks at most share the heads of a CTA's units
+  plan_join(p, ctas);
   e = decode_launch_one(attn_decode_kernel<DQ, DV, F16, NT, WHOLE>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
   if (e != cudaSuccess || !p.split) return e;
-  return decode_launch_one(attn_decode_join<DV, F16>, p, dim3(ctas, (p.rows + p.join_rows - 1) / p.join_rows),
-                           kJoinWarps * 32, 0, stream);
+  return launch_join<DV, F16>(p, ctas, stream);
 }
 
 }  // namespace attn

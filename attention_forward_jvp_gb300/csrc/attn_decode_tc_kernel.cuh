@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
     tc_fence_after();
   }
   if (w.idle) decode_idle(p);
-  if (p.split && tid == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (p.split && !p.by_unit && tid == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
   const Waiter W{abort_flag, p.err + 1, p.timeout_ns};
   auto wait_all = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar(b), parity, W)); };
@@ -511,8 +511,10 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
           if (begins && ends) p.lse[at] = sum == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(sum);
           else p.part_ml[part] = make_float2(m, sum);
         }
-        if (begins && !ends && tid == 0)
-          p.desc[blockIdx.x] = decode_describe<1>(w, cur.b, cur.hu, blockIdx.x, w.lo + i + (cur.nt - 1 - cur.t));
+        if (begins && tid == 0) {
+          if (ends) decode_complete(p, cur.b, cur.hu);
+          else decode_describe<1>(p, w, cur.b, cur.hu, blockIdx.x, w.lo + i + (cur.nt - 1 - cur.t));
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(P::B_OE));
@@ -548,11 +550,10 @@ cudaError_t launch_decode_tc(DecodeParams& p, int ctas, cudaStream_t stream) {
     attr_done[dev] = true;
   }
   p.cta_warps = 1;
-  p.join_rows = (p.rows + 15) / 16;
+  plan_join(p, ctas);
   e = decode_launch_one(attn_decode_tc_kernel<DQ, DV, F16>, p, dim3(ctas), P::THREADS, P::SMEM, stream);
   if (e != cudaSuccess || !p.split) return e;
-  return decode_launch_one(attn_decode_join<DV, F16>, p, dim3(ctas, (p.rows + p.join_rows - 1) / p.join_rows),
-                           kJoinWarps * 32, 0, stream);
+  return launch_join<DV, F16>(p, ctas, stream);
 }
 
 template <int DQ, int DV, bool F16, int NT = 1>

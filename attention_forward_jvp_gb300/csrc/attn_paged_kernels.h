@@ -92,7 +92,7 @@ struct DecodeParams {
   float scale_log2;
   uint16_t* o;
   float* lse;
-  int4* desc;                  // [warp]: the unit that starts in it and ends in a later one
+  int4* desc;                  // by range, or by unit: the unit that starts in it and ends in a later one
   float2* part_ml;             // [warp][2][rows]
   float* part_o;               // [warp][2][rows][kernel Dv]
   int* err;                    // [0]: bad page or length, [1]: a wait timed out
@@ -100,7 +100,9 @@ struct DecodeParams {
   unsigned long long timeout_ns;  // of a wait between the warps of a CTA (err[1])
   int skip_first_load;         // failure-detection hook
   int wide;                    // 1: the list of steps might pass 2^31
-  int cta_warps, join_rows;    // warps of a CTA, heads of a joining block (set by the launch)
+  // set by the launch: ranges of a CTA, of all; whether `desc` and the joining blocks go
+  // by units; heads of a joining block
+  int cta_warps, ranges, by_unit, join_rows;
 };
 
 // The decode kernel for kernel head dims DQ, DV and nt groups of 8 query heads
