@@ -47,7 +47,8 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool l
 struct DecodePlace {
   int page, slot, n;
 };
-__device__ __forceinline__ DecodePlace decode_lookup(const DecodeParams& p, bool whole, const int* pages, int first, int len) {
+__device__ __forceinline__ DecodePlace decode_lookup(const DecodeParams& p, bool whole, const int* pages, int first,
+                                                     int len) {
   DecodePlace x;
   const int key = whole ? first : first + (threadIdx.x & 15);
   x.n = len - first;

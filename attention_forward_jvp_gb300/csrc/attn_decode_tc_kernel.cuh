@@ -10,7 +10,7 @@
 // the bandwidth brings a tile in 1400 cycles, and the tensor core multiplies it
 // in 770 whatever the heads (lanes short of 128 are unused).  On mma.sync every
 // 8 heads' columns would read the tile from shared memory again (64 heads, Dqk
-// 256, Dv 128: 140 us; here 88).
+// 256, Dv 128: 140 us; here 80).
 //
 // Warps 0-7 are the softmax: two to a quadrant of 32 lanes (32 heads), each
 // with half of a tile's columns; quadrants behind the last head do nothing.
@@ -18,7 +18,8 @@
 // quadrants take the even tiles and the others the odd ones (the rows of P
 // that are not a quadrant's stay zero), each with a running maximum, sum and
 // O of its own, joined at the unit's end.  (32 sequences of 8192 keys, 64
-// heads, D 64: 203 us with every quadrant at every tile, 171 so.)
+// heads, D 64: 203 us with every quadrant at every tile, 169 so; 154 since
+// copies move whole rows.)
 // Warps 8-11 bring tiles (16 keys each) by 16-byte asynchronous copies, row by
 // row through the page table; a tile's barrier counts the copies in as they
 // land.  The last warp issues the products: S of tile i + 1 before O of tile
@@ -28,8 +29,9 @@
 // Both head dims 256: only two tiles fit beside Q, so keys and values have a
 // ring each (a key stage is free again as soon as S is, a tile and a softmax
 // before the values') and two groups of four warps bring the even and the odd
-// tiles: 115 -> 101 us at 24 heads.  At D 128 the second barrier of a tile and
-// the registers of the second group cost more than they give (112 -> 120 us).
+// tiles: 115 -> 101 us at 24 heads (95 since).  At D 128 the second barrier
+// of a tile and the registers of the second group cost more than they give
+// (112 -> 120 us).
 // S and P have two buffers each in tensor memory.  P is split into two
 // 16-bit parts there, like the warps' P of the other kernel.
 #pragma once

@@ -67,10 +67,10 @@ constexpr int kDecodeMaxWarps = 16;  // warps of a CTA, at most
 // Query heads of a unit that a warp takes at most, in groups of 8; more go to
 // tcgen05.  Every group is another pass of mma.sync over a step and takes
 // registers by the head dims, so the limit falls with them.  On either side of
-// it, the warps' kernel and tcgen05 (32 sequences of 8192, us, at that many
-// heads): 64/64 119 and 152, 128/64 103 and 113 at 32; 256/64 93 and 98, 64/128
-// 98 and 115, 128/128 106 and 110 at 24; 256/128 93 and 82 at 24; 256/256 135
-// and 100 at 16.
+// it, the warps' kernel and tcgen05 with one head more (32 sequences of 8192,
+// us): 64/64 123 and 151, 128/64 107 and 112 at 32; 256/64 90 and 95, 64/128 96
+// and 107, 128/128 99 and 101 at 24; 256/128 75 and 74, 64/256 93 and 91 at 16.
+// (One group more: 256/128 93 for 82 at 24; 256/256 135 for 100 at 16.)
 constexpr int decode_warp_rows(int dq, int dv) {
   return dv == 64 ? (dq <= 128 ? 32 : 24) : (dv == 128 ? (dq <= 128 ? 24 : 16) : (dq < 256 ? 16 : 8));
 }
