@@ -895,3 +895,10 @@ def test_decode_of_sequences_that_share_pages():
     for group in (3, 40):
         q = randn((3, 2 * group, 64), BF, group)
         check_decode(pool, q, *binding.attn_paged_decode(pool.cache, q))
+
+
+@pytest.mark.parametrize("lens,Hkv", [([5], 1), ([77], 2), ([33, 0, 48], 1), ([112], 1), ([128], 2), ([0], 2)])
+def test_decode_of_lists_about_as_long_as_one_block_holds(lens, Hkv):
+    pool = Pool(lens, Hkv, 128, 64, 16, BF, seed=len(lens), extra=0)
+    q = randn((len(lens), 5 * Hkv, 128), BF, 3)
+    check_decode(pool, q, *binding.attn_paged_decode(pool.cache, q))
