@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
         const float inv = begins && ends ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
 #pragma unroll 1
         for (int c0 = 0; c0 < DH; c0 += 16) {
+          __syncwarp();  // rows of a quadrant behind the unit's heads have no part in the stores below
           uint32_t o[16];
           tmem_ld_32x32b_x16(tl + P::COL_O + half * DH + c0, o);
           tmem_wait_ld16_regs(o);
@@ -491,21 +492,23 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
             ++swaps;
           }
           const int col = half * DH + c0;
-          if (!in || odd) continue;
-          if (begins && ends) {
+          if (in && !odd) {
+            if (begins && ends) {
 #pragma unroll
-            for (int c = 0; c < 16; c += 8) {
-              uint32_t y[4];
+              for (int c = 0; c < 16; c += 8) {
+                uint32_t y[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                y[e] = pack2<F16>(__uint_as_float(o[c + 2 * e]) * inv, __uint_as_float(o[c + 2 * e + 1]) * inv);
-              if (col + c < p.dv)
-                *reinterpret_cast<uint4*>(p.o + at * p.dv + col + c) = make_uint4(y[0], y[1], y[2], y[3]);
+                for (int e = 0; e < 4; ++e)
+                  y[e] = pack2<F16>(__uint_as_float(o[c + 2 * e]) * inv, __uint_as_float(o[c + 2 * e + 1]) * inv);
+                if (col + c < p.dv)
+                  *reinterpret_cast<uint4*>(p.o + at * p.dv + col + c) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 16; c += 4)
+                *reinterpret_cast<uint4*>(p.part_o + part * DV + col + c) =
+                    make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 16; c += 4)
-              *reinterpret_cast<uint4*>(p.part_o + part * DV + col + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
           }
         }
         if (!ok) break;

@@ -1,0 +1,105 @@
+"""Paged decode on the GPU where its arithmetic and its refusals are thinnest,
+against the float64 definition of oracle.paged_ref.
+
+Tolerances, from the arithmetic (u = half a step of the output type,
+torch.finfo(t).eps / 2):
+
+  scores   d = (Dqk + 4) 2^-22 s max_j sum |q| |k_j|: fp32 sums, a rounding
+           and a truncation each
+  O        u |O| + (2 d + 2^-15) sum_j w_j |V_j|: a weight is off by its own
+           score's error and the others', by exp2's (2^-22) and by what P's
+           two parts leave (bf16 2^-18, fp16 2^-22 of it), and the sum by its
+           accumulation
+  LSE      d + (n + 8) 2^-24 + 2^-21 |LSE|
+"""
+import numpy as np
+import pytest
+import torch
+
+from attention_forward_jvp_gb300 import binding, build
+from oracle import paged_ref
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build.build()
+    binding.lib()
+
+
+@pytest.fixture(autouse=True)
+def _clean(_lib):
+    assert binding.sync_check() == 0
+    yield
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def randn(shape, dtype, seed, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std).to(dtype)
+
+
+class Pool:
+    """Keys and values [pages, Hkv, page, d] of the CPU, a shuffled page table
+    (entries behind a sequence's last page are out of range), and the cache of
+    them on the GPU.  Every slot of every page is finite."""
+
+    def __init__(self, lens, Hkv, Dqk, Dv, page, dtype, seed=0, width=None):
+        need = [-(-n // page) for n in lens]
+        width = width or max(need + [1])
+        self.lens, self.page, count = list(lens), page, sum(need) + 2
+        self.k, self.v = (randn((count, Hkv, page, d), dtype, seed + i) for i, d in enumerate((Dqk, Dv)))
+        order = torch.randperm(count, generator=torch.Generator().manual_seed(seed))
+        self.table = torch.full((len(lens), width), -7, dtype=torch.int32)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n].int()
+            at += n
+
+    def rows(self, x, b, h):
+        """Rows of a pool's key head in the order of sequence b."""
+        j = torch.arange(self.lens[b])
+        return x[self.table[b, j // self.page].long(), h, j % self.page]
+
+    def cache(self, table=None, lens=None):
+        table = self.table if table is None else table
+        lens = torch.tensor(self.lens if lens is None else lens, dtype=torch.int32)
+        return binding.PagedCache(self.k.cuda(), self.v.cuda(), table.cuda(), lens.cuda())
+
+
+def check(pool, q, o, lse, sm_scale=None):
+    Q, K, V = f64(q), f64(pool.k), f64(pool.v)
+    want, wl = paged_ref.decode(Q, K, V, pool.table.numpy(), pool.lens, sm_scale)
+    O, L, u = f64(o), f64(lse), torch.finfo(o.dtype).eps / 2
+    group, Dqk = Q.shape[1] // K.shape[1], Q.shape[2]
+    s = Dqk**-0.5 if sm_scale is None else sm_scale
+    assert np.isfinite(O).all() and not np.isnan(L).any()
+    for b, n in enumerate(pool.lens):
+        if n == 0:
+            assert (O[b] == 0).all() and np.isneginf(L[b]).all()
+            continue
+        for h in range(Q.shape[1]):
+            k, v = f64(pool.rows(pool.k, b, h // group)), f64(pool.rows(pool.v, b, h // group))
+            w = np.exp(s * (k @ Q[b, h]) - wl[b, h])
+            d = (Dqk + 4) * 2.0**-22 * s * (np.abs(k) @ np.abs(Q[b, h])).max()
+            tol = u * np.abs(want[b, h]) + (2 * d + 2.0**-15) * (w @ np.abs(v))
+            tol += torch.finfo(o.dtype).smallest_normal * 2 * u
+            e = np.abs(O[b, h] - want[b, h])
+            assert (e <= tol).all(), f"O of {b}, {h}: {e.max():.3e}, {np.max(e - tol):.3e} over its bound"
+            assert abs(L[b, h] - wl[b, h]) <= d + (n + 8) * 2.0**-24 + 2.0**-21 * abs(wl[b, h]), f"LSE of {b}, {h}"
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (64, 256), (256, 128), (256, 256)])
+@pytest.mark.parametrize("group", [33, 65, 95, 97, 127])
+def test_heads_that_end_inside_a_quadrant(dims, group):
+    # (33 stand twice, the others once; units that end in a CTA and that several share)
+    pool = Pool([1, 64, 65, 0, 1500], 1, *dims, 16, BF if group % 4 == 1 else HF, seed=group)
+    q = randn((5, group, dims[0]), pool.k.dtype, group)
+    check(pool, q, *binding.attn_paged_decode(pool.cache(), q.cuda()))
