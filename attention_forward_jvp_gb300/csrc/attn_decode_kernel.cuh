@@ -5,8 +5,9 @@
 // sum l per head: P = exp2(S' - m), O <- O exp2(m_old - m) + P V,
 // l <- l exp2(m_old - m) + sum(P), with S' = S log2(e).  m moves only when a
 // score passes it by more than 8 (P then stays below 2^8), so that most steps
-// need neither the maximum over the lanes nor the rescale.  Parts of a
-// sequence are joined by the same rule.
+// need neither the maximum over the lanes nor the rescale; for fp16 storage m
+// lies below the maximum and moves sooner (DecodeReference).  Parts of a
+// sequence are joined by the same rule, whatever their m.
 //
 // What bounds it: memory.  Every key and value is read once and used by G
 // query heads, G flops a byte; tcgen05's 64 or 128 rows would be padding but
@@ -139,9 +140,26 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Where the reference m of the probabilities P = exp2(S' - m) lies: `below` the
+// maximum when it moves, and it moves when a score is more than `room` above it.
+// A bf16 part of P has fp32's exponents, so m is the maximum.  Parts in fp16 end
+// at 2^-24, and at 65504: with m 11 below and 15 of room P goes up to 2^15, the
+// largest probability of a part is 2^11 or more, and 2^-25, the most that its
+// parts drop of any other, is 2^-36 of it.  (m at the maximum dropped 2^-25 of
+// it: a key that outweighs a long even tail by 2^25 hid the tail from O, though
+// not from l.)  What lies between the two is how far the maximum may rise
+// without a rescale: 4 cost what 8 do where scores are N(0, 1.5^2) (64 heads,
+// D 64, 32 sequences of 8192: 151.5 us for 151.2), and 4 % on tcgen05 where they
+// are N(0, 3^2) (157.9 for 151.9); 2 cost as much at the former and 9 % there,
+// and 8, with m 7 below, leave an even tail 16 times the error.
+template <bool F16>
+struct DecodeReference {
+  static constexpr float below = F16 ? 11.f : 0.f, room = F16 ? 15.f : 8.f;
+};
 // x, y rounded to the operand type (hi) and what the rounding left (lo), each
-// packed: hi + lo holds 16 or more bits of a probability, so that rounding P
-// costs the output nothing next to its own rounding.
+// packed: hi + lo holds 16 bits of a probability in bf16, 22 in fp16 above
+// 2^-14 and 2^-25 of absolute error below, so that rounding P costs the output
+// nothing next to its own rounding.
 template <bool F16>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = pack2<F16>(x, y);
@@ -565,7 +583,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
           if constexpr (CH == 2) s[0][n][e] += s[1][n][e];
           s[0][n][e] *= p.scale_log2;
           if (g + (e >> 1) * 8 >= live) s[0][n][e] = -INFINITY;
-          grows = grows || s[0][n][e] > m[n][e & 1] + 8.f;
+          grows = grows || s[0][n][e] > m[n][e & 1] + DecodeReference<F16>::room;
         }
       }
       if (__any_sync(0xffffffffu, grows)) {
@@ -577,7 +595,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            x = fmaxf(x, m[n][e]);
+            x = fmaxf(x - DecodeReference<F16>::below, m[n][e]);
             const float a = exp2_fast(m[n][e] - (x == -INFINITY ? 0.f : x));
             m[n][e] = x;
             l[n][e] *= a;

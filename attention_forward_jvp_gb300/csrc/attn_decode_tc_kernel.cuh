@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c) top = max3f(top, __uint_as_float(x0[c]), __uint_as_float(x1[c]));
         top *= p.scale_log2;
-        if (__any_sync(0xffffffffu, top > m + 8.f)) {
-          const float n = fmaxf(m, top), a = exp2_fast(m - (n == -INFINITY ? 0.f : n));
+        if (__any_sync(0xffffffffu, top > m + DecodeReference<F16>::room)) {
+          const float n = fmaxf(m, top - DecodeReference<F16>::below), a = exp2_fast(m - (n == -INFINITY ? 0.f : n));
           m = n;
           l *= a;
           if (!first) {

@@ -103,3 +103,51 @@ def test_heads_that_end_inside_a_quadrant(dims, group):
     pool = Pool([1, 64, 65, 0, 1500], 1, *dims, 16, BF if group % 4 == 1 else HF, seed=group)
     q = randn((5, group, dims[0]), pool.k.dtype, group)
     check(pool, q, *binding.attn_paged_decode(pool.cache(), q.cuda()))
+
+
+@pytest.mark.parametrize("dims,group", [((64, 64), 1), ((64, 64), 24), ((128, 128), 8), ((256, 256), 5), ((64, 64), 40),
+                                        ((128, 64), 70), ((256, 256), 12)])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_one_key_that_outweighs_an_even_tail(dims, group, dt):
+    """In every 16 keys one of value 0 that outweighs each of the others by
+    2^6 to 2^28, by the head: O is the tail's, and LSE has both.  The tail's
+    weights are all alike, so that what the parts of P drop adds up.  Beside
+    the module's bound only that: fp16 parts drop up to 2^-25 of a weight
+    that is 2^-11 of the largest or more, each 2^-36 of the large key's."""
+    Dqk, Dv = dims
+    lens = [16, 64, 1000, 5, 3000]
+    pool = Pool(lens, 1, Dqk, Dv, 16, dt, seed=group)
+    pool.k.zero_()
+    pool.k[:, :, 3, 0] = 8.0
+    pool.v.copy_((torch.rand(pool.v.shape, generator=torch.Generator().manual_seed(1)) + 0.5) * 2.0**13)
+    pool.v[:, :, 3] = 0.0
+    q = randn((5, group, Dqk), dt, group)
+    gap = torch.linspace(6.0, 28.0, group) if group > 1 else torch.tensor([24.7])
+    q[:, :, 0] = (gap * np.log(2.0) * Dqk**0.5 / 8.0).to(dt)  # score of the large key over the others' 0
+    o, lse = binding.attn_paged_decode(pool.cache(), q.cuda())
+    u, O, L = torch.finfo(dt).eps / 2, f64(o), f64(lse)
+    for b, n in enumerate(lens):
+        v, big = f64(pool.rows(pool.v, b, 0)), np.arange(n) % 16 == 3
+        for h in range(group):
+            z = float(q[b, h, 0].double()) * 8.0 * Dqk**-0.5
+            total = big.sum() * np.exp(z) + (~big).sum()
+            want, d = v.sum(0) / total, (Dqk + 4) * 2.0**-22 * z
+            drop = 2.0**-36 * np.exp(z) * v.sum(0) / total if dt == HF else 0.0
+            tol = (u + 2 * d + 2.0**-15) * want + drop + (2.0**-25 if dt == HF else 0.0)
+            e = np.abs(O[b, h] - want)
+            assert (e <= tol).all(), f"O of {b}, gap 2^{z / np.log(2.0):.1f}: {np.max(e / want):.2e} of it"
+            assert abs(L[b, h] - np.log(total)) <= d + (n + 8) * 2.0**-24 + 2.0**-21 * np.log(total)
+
+
+def test_large_keys_that_come_late():
+    # the maximum rises by 2^3 to 2^14 from one 64 keys to the next: the reference moves, and with it what was added up
+    for dt in (BF, HF):
+        for dims, group in (((64, 64), 3), ((64, 128), 30), ((128, 128), 70)):
+            pool = Pool([700, 65, 3001], 1, *dims, 16, dt, seed=group)
+            for b, n in enumerate(pool.lens):
+                j = torch.arange(n)
+                step = [3.0, 14.0, 0.4][b]
+                pool.k[pool.table[b, j // 16].long(), 0, j % 16, 0] += (j // 64 * step).to(dt)
+            q = randn((3, group, dims[0]), dt, group)
+            q[:, :, 0] = dims[0] ** 0.5
+            check(pool, q, *binding.attn_paged_decode(pool.cache(), q.cuda()))
