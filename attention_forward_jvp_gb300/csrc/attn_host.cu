@@ -885,16 +885,16 @@ attn_status attn_sync_check(void* stream) {
       timed_out = true;
     }
   }
-  // and the words of the paged cache's entry points
+  // and the words of the paged cache's entry points; a page error beside a
+  // timeout stays for the next check
   bool bad_page = false;
   if (int* w = attn::page_error_words(dev)) {
     int word[2] = {0, 0};
     if (cudaMemcpy(word, w, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return ATTN_ERR_CUDA;
-    if (word[0] != 0 || word[1] != 0) {
-      if (cudaMemset(w, 0, sizeof(word)) != cudaSuccess) return ATTN_ERR_CUDA;
-      bad_page = word[0] != 0;
-      timed_out = timed_out || word[1] != 0;
-    }
+    timed_out = timed_out || word[1] != 0;
+    bad_page = word[0] != 0 && !timed_out;
+    if (word[1] != 0 && cudaMemset(w + 1, 0, sizeof(int)) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (bad_page && cudaMemset(w, 0, sizeof(int)) != cudaSuccess) return ATTN_ERR_CUDA;
   }
   return timed_out ? ATTN_ERR_TIMEOUT : bad_page ? ATTN_ERR_PAGE : ATTN_OK;
 }

@@ -273,7 +273,8 @@ attn_status attn_bwd_stages(const attn_shape* shape,
  * up (nothing is allocated here), and the word of attn_paged.h's entry
  * points.  Returns ATTN_ERR_TIMEOUT if a launch since the last check
  * reported a timed-out wait, else ATTN_ERR_PAGE if one met a page, length
- * or position out of range, ATTN_ERR_CUDA on a CUDA error, else ATTN_OK. */
+ * or position out of range (beside a timeout that is left for the next
+ * check), ATTN_ERR_CUDA on a CUDA error, else ATTN_OK. */
 attn_status attn_sync_check(void* stream);
 
 /* Static description of a status code; never NULL. */

@@ -151,3 +151,23 @@ def test_large_keys_that_come_late():
             q = randn((3, group, dims[0]), dt, group)
             q[:, :, 0] = dims[0] ** 0.5
             check(pool, q, *binding.attn_paged_decode(pool.cache(), q.cuda()))
+
+
+def test_bad_page_beside_a_wait_that_runs_out_is_reported_next():
+    # a first tile that never arrives (host-set hook), and a page out of range in it: both are told, one after the other
+    pool = Pool([300, 70], 1, 128, 64, 16, BF, seed=8)
+    q = randn((2, 40, 128), BF, 8).cuda()
+    bad = pool.table.clone()
+    bad[0, 1] = -1
+    cache = pool.cache(table=bad)
+    binding.set_wait_timeout_ns(20_000_000)
+    binding.debug_skip_first_load(True)
+    try:
+        binding.attn_paged_decode(cache, q)
+        assert [binding.sync_check() for _ in range(3)] == [5, 6, 0]
+    finally:
+        binding.debug_skip_first_load(False)
+        binding.set_wait_timeout_ns(2_000_000_000)
+    binding.attn_paged_decode(cache, q)
+    assert [binding.sync_check() for _ in range(2)] == [6, 0]
+    check(pool, q, *binding.attn_paged_decode(pool.cache(), q))
