@@ -171,3 +171,35 @@ def test_bad_page_beside_a_wait_that_runs_out_is_reported_next():
     binding.attn_paged_decode(cache, q)
     assert [binding.sync_check() for _ in range(2)] == [6, 0]
     check(pool, q, *binding.attn_paged_decode(pool.cache(), q))
+
+
+@pytest.mark.parametrize("group,dims", [(2, (64, 64)), (40, (64, 64)), (70, (128, 128)), (12, (256, 256)), (6, (16, 32))])
+@pytest.mark.parametrize("page", [16, 24])
+@pytest.mark.parametrize("bad", [-1, 2**31 - 1, None])
+def test_bad_pages_count_as_zeros(group, dims, page, bad):
+    # keys and values of zero among good ones, in a page that ends inside a step and in the last one
+    pool = Pool([100, 64, 500], 2, *dims, page, HF, seed=group)
+    q = randn((3, 2 * group, dims[0]), HF, group)
+    table = pool.table.clone()
+    for b, e in ((0, 1), (2, 4), (2, int((pool.table[2] >= 0).sum()) - 1)):
+        table[b, e] = pool.k.shape[0] if bad is None else bad
+        pool.k[pool.table[b, e].long()] = 0
+        pool.v[pool.table[b, e].long()] = 0
+    o, lse = binding.attn_paged_decode(pool.cache(table=table), q.cuda())
+    assert binding.sync_check() == 6
+    check(pool, q, o, lse)
+    o2, lse2 = binding.attn_paged_decode(pool.cache(), q.cuda())
+    assert binding.sync_check() == 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("group,dims", [(2, (64, 64)), (40, (64, 64)), (70, (128, 128))])
+@pytest.mark.parametrize("page", [16, 24])
+def test_lengths_out_of_range_count_as_the_nearer_bound(group, dims, page):
+    lens = [13 * page, 50, 0]
+    pool = Pool(lens, 2, *dims, page, BF, seed=group, width=13)
+    q = randn((3, 2 * group, dims[0]), BF, group).cuda()
+    for long in (13 * page + 1, 2**31 - 1):
+        o, lse = binding.attn_paged_decode(pool.cache(lens=[long, 50, -3]), q)
+        assert binding.sync_check() == 6
+        check(pool, q, o, lse)
