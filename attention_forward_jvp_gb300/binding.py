@@ -653,8 +653,8 @@ def attn_rope(tensors, rope: Rope, positions: Optional[torch.Tensor] = None, off
     written.  Any strides with contiguous rows of D (a transposed view of a
     [B, N, H, D] projection); rows on 16-byte boundaries with D and rot_dim
     multiples of 16 run at speed, others element by element.  ``out``: one
-    tensor for each, the input itself to rotate in place; by default new
-    contiguous ones."""
+    tensor for each, of its own, or the input itself to rotate in place (a
+    tensor given twice then is refused); by default new contiguous ones."""
     tensors = tuple(tensors)
     n = len(tensors)
     if not 1 <= n <= 4:

@@ -137,6 +137,8 @@ attn_status run_rope(int32_t B, int64_t N, int32_t D, const attn_rope_spec* rope
     const bool xs8 = take_strides(t.x_stride, sizes, 3, a.xs), ys8 = take_strides(t.y_stride, sizes, 3, a.ys);
     if (t.x == t.y && std::memcmp(a.xs, a.ys, sizeof(a.xs)) != 0) return ATTN_ERR_INVALID_ARG;
     if (shares_places(sizes, 3, a.ys)) return ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j + 1 < p.n_tensors; ++j)
+      if (a.y == p.t[j].y || a.y == p.t[j].x || a.x == p.t[j].y) return ATTN_ERR_INVALID_ARG;
     vec = vec && xs8 && ys8 && aligned16(t.x) && aligned16(t.y);
   }
   if (p.heads == 0) return ATTN_OK;
@@ -205,10 +207,12 @@ attn_status run_append(const attn_paged_cache* c, const attn_paged_new* n, const
     const bool q8 = take_strides(n->q_stride, q_sizes, 2, p.qs), o8 = take_strides(n->q_out_stride, q_sizes, 2, p.qos);
     if (n->q == n->q_out && std::memcmp(p.qs, p.qos, sizeof(p.qs)) != 0) return ATTN_ERR_INVALID_ARG;
     if (shares_places(q_sizes, 2, p.qos)) return ATTN_ERR_INVALID_ARG;
+    if (n->Hq > 0 && (n->q_out == n->k || n->q_out == n->v)) return ATTN_ERR_INVALID_ARG;
     vec = vec && q8 && o8 && aligned16(n->q) && aligned16(n->q_out);
   }
   const int64_t pool_sizes[3] = {c->n_pages, c->Hkv, c->page_size};
   if (shares_places(pool_sizes, 3, p.kp) || shares_places(pool_sizes, 3, p.vp)) return ATTN_ERR_INVALID_ARG;
+  if (c->n_pages > 0 && c->k == c->v) return ATTN_ERR_INVALID_ARG;
   Device d;
   st = device(&d);
   if (st != ATTN_OK) return st;

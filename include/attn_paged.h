@@ -63,8 +63,8 @@ typedef struct {
 /* One tensor: x is read and y written, both [batch, head, token, D] by
  * strides (batch, head, token) in elements, the D elements of a row
  * contiguous.  y == x with equal strides rotates in place; any other
- * overlap is undefined, and a y stride of 0 over more than one element is
- * refused.  Rows that are 16-byte aligned (pointer and strides), with D and
+ * overlap is undefined, and refused where it shows: a y that is also another
+ * tensor's x or y, a y stride of 0 over more than one element.  Rows that are 16-byte aligned (pointer and strides), with D and
  * rot_dim multiples of 16, move in 16-byte accesses; others element by
  * element. */
 typedef struct {
@@ -180,8 +180,9 @@ typedef struct {
  * the cache and zeros to q_out; the latter, and a token whose position lies
  * behind the table's row or whose page is not in [0, n_pages), is reported
  * as ATTN_ERR_PAGE.  No two tokens of one call may share a place in the
- * pool; pools or a q_out with a stride of 0 over more than one element are
- * refused (a decode may read such pools). */
+ * pool; pools or a q_out with a stride of 0 over more than one element, one
+ * pool for keys and values (a decode may read such pools) and a q_out that is
+ * k or v are refused. */
 attn_status attn_paged_append(const attn_paged_cache* cache, const attn_paged_new* tokens,
                               const attn_rope_spec* rope, void* stream);
 attn_status attn_paged_append_f16(const attn_paged_cache* cache, const attn_paged_new* tokens,
