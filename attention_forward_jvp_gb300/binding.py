@@ -566,6 +566,8 @@ def _need_cuda(t: torch.Tensor, name: str, dtype, dev=None):
         raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have dimensions, got a single number")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
@@ -684,12 +686,12 @@ def attn_rope(tensors, rope: Rope, positions: Optional[torch.Tensor] = None, off
     for i, x in enumerate(tensors):
         xs, H = x.stride(), H0
         if x is not x0:
-            if x.dtype is not dt or x.device != dev or xs[-1] != 1:
+            if x.dtype is not dt or x.device != dev or xs[-1:] != (1,):
                 _need_cuda(x, "every tensor", dt, dev)
             sx = x.shape
-            H = sx[nd - 3]
             if sx != s0 and (len(sx) != nd or sx[-2:] != s0[-2:] or (not jagged and sx[0] != B)):
                 raise ValueError("the tensors must agree in all but their heads")
+            H = sx[nd - 3]
         if out is None:
             if x.is_contiguous():
                 y, ys = torch.empty_like(x), xs
@@ -786,7 +788,7 @@ def attn_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, rope:
     contiguous rows; a jagged [H, T, D] tensor goes in as its transpose(0, 1)."""
     dev, dt = cache.device, cache.dtype
     for name, t in (("k", k), ("v", v), ("q", q)):
-        if t is not None and (t.dtype is not dt or t.device != dev or t.stride(-1) != 1):
+        if t is not None and (t.dtype is not dt or t.device != dev or t.stride()[-1:] != (1,)):
             _need_cuda(t, name, dt, dev)
     T = k.shape[0]
     if k.shape != (T, cache.Hkv, cache.Dqk) or v.shape != (T, cache.Hkv, cache.Dv):
@@ -833,7 +835,7 @@ def attn_paged_decode(cache: PagedCache, q: torch.Tensor, sm_scale: Optional[flo
     float32, natural log).  An idle place (length 0) gets o = 0, lse = -inf."""
     dev, dt, B = cache.device, cache.dtype, cache.B
     qs, sq = q.stride(), q.shape
-    if q.dtype is not dt or q.device != dev or qs[-1] != 1:
+    if q.dtype is not dt or q.device != dev or qs[-1:] != (1,):
         _need_cuda(q, "q", dt, dev)
     if len(sq) != 3 or sq[0] != B or sq[2] != cache.Dqk:
         raise ValueError(f"q must be [{B}, Hq, {cache.Dqk}]")

@@ -203,3 +203,22 @@ def test_lengths_out_of_range_count_as_the_nearer_bound(group, dims, page):
         o, lse = binding.attn_paged_decode(pool.cache(lens=[long, 50, -3]), q)
         assert binding.sync_check() == 6
         check(pool, q, o, lse)
+
+
+@pytest.mark.parametrize("shape", [(), (64,), (2, 64), (1, 2, 3, 4, 64)])
+def test_tensors_of_other_dimensions_are_refused(shape):
+    pool = Pool([40, 3], 2, 64, 64, 16, BF)
+    c, r, bad = pool.cache(), binding.Rope(64), torch.zeros(shape, dtype=BF, device="cuda")
+    x, q, k = (randn(s, BF, 0).cuda() for s in ((1, 2, 4, 64), (2, 4, 64), (2, 2, 64)))
+    calls = [lambda: binding.attn_rope([bad], r), lambda: binding.attn_rope([x, bad], r),
+             lambda: binding.attn_rope([x], r, out=[bad]), lambda: binding.attn_paged_append(c, bad, k),
+             lambda: binding.attn_paged_append(c, k, bad), lambda: binding.attn_paged_append(c, k, k, q=bad),
+             lambda: binding.attn_paged_append(c, k, k, q=q, out=bad), lambda: binding.attn_paged_decode(c, bad),
+             lambda: binding.PagedCache(bad, c.v, c.page_table, c.seq_lens),
+             lambda: binding.PagedCache(c.k, bad, c.page_table, c.seq_lens),
+             lambda: binding.PagedCache(c.k, c.v, c.page_table, bad.int())]
+    if bad.dim() != 2:
+        calls.append(lambda: binding.PagedCache(c.k, c.v, bad.int(), c.seq_lens))
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
