@@ -62,7 +62,10 @@ cudaError_t launch_append(const AppendParams& p, bool vec, bool f16, int splits,
 
 // -------------------------------------------------------------------- decode
 constexpr int kDecodeBN = 16;        // keys of a step
-constexpr int kDecodeMinStepsLog = 1;  // a warp takes two steps at least, where there are two
+// A list of n steps is cut into n / 2 + 1 ranges at most: most take two steps,
+// and one or two of a list that is cut so finely take one (n / 2 ranges would
+// leave a third step to one of them where n is odd).
+constexpr int kDecodeMinStepsLog = 1;
 constexpr int kDecodeMaxWarps = 16;  // warps of a CTA, at most
 // Query heads of a unit that a warp takes at most, in groups of 8; more go to
 // tcgen05.  Every group is another pass of mma.sync over a step and takes
