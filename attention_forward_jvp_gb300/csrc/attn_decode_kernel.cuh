@@ -157,9 +157,9 @@ struct DecodeReference {
   static constexpr float below = F16 ? 11.f : 0.f, room = F16 ? 15.f : 8.f;
 };
 // x, y rounded to the operand type (hi) and what the rounding left (lo), each
-// packed: hi + lo holds 16 bits of a probability in bf16, 22 in fp16 above
-// 2^-14 and 2^-25 of absolute error below, so that rounding P costs the output
-// nothing next to its own rounding.
+// packed: hi + lo holds 16 bits of a probability in bf16; in fp16 it is off by at
+// most 2^-23 of one above 2^-2, and by 2^-25 below.  Rounding P so costs the
+// output nothing next to its own rounding.
 template <bool F16>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = pack2<F16>(x, y);
