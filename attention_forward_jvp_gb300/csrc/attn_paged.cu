@@ -212,7 +212,8 @@ attn_status run_append(const attn_paged_cache* c, const attn_paged_new* n, const
   }
   const int64_t pool_sizes[3] = {c->n_pages, c->Hkv, c->page_size};
   if (shares_places(pool_sizes, 3, p.kp) || shares_places(pool_sizes, 3, p.vp)) return ATTN_ERR_INVALID_ARG;
-  if (c->n_pages > 0 && c->k == c->v) return ATTN_ERR_INVALID_ARG;
+  // one pool for both holds what both write only where that is the same
+  if (c->n_pages > 0 && c->k == c->v && (rope != nullptr || n->k != n->v)) return ATTN_ERR_INVALID_ARG;
   Device d;
   st = device(&d);
   if (st != ATTN_OK) return st;

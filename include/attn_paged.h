@@ -181,8 +181,8 @@ typedef struct {
  * behind the table's row or whose page is not in [0, n_pages), is reported
  * as ATTN_ERR_PAGE.  No two tokens of one call may share a place in the
  * pool; pools or a q_out with a stride of 0 over more than one element, one
- * pool for keys and values (a decode may read such pools) and a q_out that is
- * k or v are refused. */
+ * pool for keys and values (a decode may read such pools) unless k is v and
+ * nothing is rotated, and a q_out that is k or v are refused. */
 attn_status attn_paged_append(const attn_paged_cache* cache, const attn_paged_new* tokens,
                               const attn_rope_spec* rope, void* stream);
 attn_status attn_paged_append_f16(const attn_paged_cache* cache, const attn_paged_new* tokens,

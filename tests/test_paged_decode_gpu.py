@@ -222,3 +222,21 @@ def test_tensors_of_other_dimensions_are_refused(shape):
     for call in calls:
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (128, 64)])
+def test_one_pool_for_keys_and_values(dims):
+    # values that are the first elements of the keys, in their place: written as both, read as both
+    pool = Pool([40, 3], 2, dims[0], dims[1], 16, BF, seed=2)
+    k, kn = pool.k.cuda(), randn((2, 2, dims[0]), BF, 1).cuda()
+    c = binding.PagedCache(k, k[..., :dims[1]], pool.table.cuda(), torch.tensor(pool.lens, dtype=torch.int32).cuda())
+    binding.attn_paged_append(c, kn, kn[..., :dims[1]])
+    for b, n in enumerate(pool.lens):
+        pool.k[pool.table[b, (n - 1) // 16].long(), :, (n - 1) % 16] = kn[b].cpu()
+    assert torch.equal(k.cpu(), pool.k)
+    pool.v = pool.k[..., :dims[1]]
+    q = randn((2, 6, dims[0]), BF, 3)
+    check(pool, q, *binding.attn_paged_decode(c, q.cuda()))
+    for bad in (dict(rope=binding.Rope(64)), dict(v=kn[..., :dims[1]].clone())):
+        with pytest.raises(binding.AttnError):
+            binding.attn_paged_append(c, kn, bad.pop("v", kn[..., :dims[1]]), **bad)
