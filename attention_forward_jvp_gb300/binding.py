@@ -1,11 +1,11 @@
-"""ctypes binding of the C ABI in include/attn_jvp.h and include/attn_paged.h.
+"""ctypes binding of the C ABI in include/attn_jvp.h, attn_paged.h and attn_cache.h.
 
 Argument marshalling only: shapes, strides and raw pointers of torch
 tensors are handed to ``libattn_jvp.so``; every arithmetic step runs in its
 CUDA kernels.  Outputs are allocated with torch (device memory plumbing).
 CPU (host) inputs of the attention entry points are staged through the
 device: the host->device copies, the kernel and the device->host copies all
-run on the current stream.  (The rotation and the paged cache take CUDA
+run on the current stream.  (The rotation and the paged caches take CUDA
 tensors only.)
 
 There is no fallback: if the library is missing or the GPU is absent the
@@ -47,6 +47,21 @@ EXPORTS = (
     "attn_paged_decode",
     "attn_paged_decode_f16",
     "attn_paged_decode_workspace",
+    "attn_paged_append4",
+    "attn_paged_append4_f16",
+    "attn_paged_decode4",
+    "attn_paged_decode4_f16",
+    "attn_paged_decode4_workspace",
+    "attn_paged_gather",
+    "attn_paged_gather4",
+    "attn_paged_gather4_f16",
+    "attn_paged_weights",
+    "attn_paged_weights_f16",
+    "attn_paged_weights4",
+    "attn_paged_weights4_f16",
+    "attn_paged_evict",
+    "attn_paged_evict4",
+    "attn_paged_evict_workspace",
 )
 
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED",
@@ -95,6 +110,29 @@ class AttnPagedNew(ctypes.Structure):
                 ("v", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("Hq", ctypes.c_int32),
                 ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2), ("q_stride", ctypes.c_int64 * 2),
                 ("q_out_stride", ctypes.c_int64 * 2)]
+
+
+class AttnPagedCache4(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("Dqk", ctypes.c_int32),
+                ("Dv", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("k_scale_stride", ctypes.c_int64 * 3),
+                ("v_scale_stride", ctypes.c_int64 * 3), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p)]
+
+
+class AttnPagedWeight(ctypes.Structure):
+    _fields_ = [("lse", ctypes.c_void_p), ("w", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("w_stride", ctypes.c_int64 * 2), ("out_stride", ctypes.c_int64 * 2), ("decay", ctypes.c_float)]
+
+
+class AttnPagedEviction(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("w_out", ctypes.c_void_p), ("w_stride", ctypes.c_int64 * 2),
+                ("w_out_stride", ctypes.c_int64 * 2), ("keep", ctypes.c_void_p), ("keep_all", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("recent", ctypes.c_int32), ("pages", ctypes.c_void_p),
+                ("pages_stride", ctypes.c_int64), ("n_new", ctypes.c_int32), ("table_out", ctypes.c_void_p),
+                ("table_out_stride", ctypes.c_int64), ("lens_out", ctypes.c_void_p)]
 
 
 class AttnError(RuntimeError):
@@ -166,6 +204,27 @@ def lib() -> ctypes.CDLL:
     for f in (L.attn_paged_decode, L.attn_paged_decode_f16):
         f.restype = i32
         f.argtypes = [ctypes.POINTER(AttnPagedCache), ctypes.c_int32, vp, vp, f32, vp, vp, vp, sz, vp]
+    for f in (L.attn_paged_append4, L.attn_paged_append4_f16):
+        f.restype = i32
+        f.argtypes = [ctypes.POINTER(AttnPagedCache4), vp, ctypes.POINTER(AttnRopeSpec), vp]
+    L.attn_paged_decode4_workspace.restype = sz
+    L.attn_paged_decode4_workspace.argtypes = [ctypes.POINTER(AttnPagedCache4), ctypes.c_int32]
+    for f in (L.attn_paged_decode4, L.attn_paged_decode4_f16):
+        f.restype = i32
+        f.argtypes = [ctypes.POINTER(AttnPagedCache4), ctypes.c_int32, vp, vp, f32, vp, vp, vp, sz, vp]
+    for f in (L.attn_paged_gather, L.attn_paged_gather4, L.attn_paged_gather4_f16):
+        f.restype = i32
+        cache = AttnPagedCache if f is L.attn_paged_gather else AttnPagedCache4
+        f.argtypes = [ctypes.POINTER(cache), i64, vp, vp, vp, vp, vp, vp]
+    for f, cache in ((L.attn_paged_weights, AttnPagedCache), (L.attn_paged_weights_f16, AttnPagedCache),
+                     (L.attn_paged_weights4, AttnPagedCache4), (L.attn_paged_weights4_f16, AttnPagedCache4)):
+        f.restype = i32
+        f.argtypes = [ctypes.POINTER(cache), ctypes.c_int32, vp, vp, f32, ctypes.POINTER(AttnPagedWeight), vp]
+    L.attn_paged_evict_workspace.restype = sz
+    L.attn_paged_evict_workspace.argtypes = [ctypes.c_int32] * 4
+    for f, cache in ((L.attn_paged_evict, AttnPagedCache), (L.attn_paged_evict4, AttnPagedCache4)):
+        f.restype = i32
+        f.argtypes = [ctypes.POINTER(cache), ctypes.POINTER(AttnPagedEviction), vp, sz, vp]
     _LIB = L
     return L
 
@@ -766,6 +825,7 @@ class PagedCache:
         c.page_table, c.table_stride, c.seq_lens = page_table.data_ptr(), page_table.stride(0), seq_lens.data_ptr()
         self._struct, self._ref = c, ctypes.byref(c)
         self._workspace = {}  # bytes a decode needs, by query heads
+        self._calls = _paged_calls("", dt)
 
     def _workspace_bytes(self, Hq: int) -> int:
         with torch.cuda.device(self.device):
@@ -773,12 +833,79 @@ class PagedCache:
         return n
 
 
-def attn_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, rope: Optional[Rope] = None,
+class PagedCache4:
+    """A paged key-value cache that holds 4 bits an element: of 64 neighbouring
+    elements of a row (32 where the head has no more) a least value m and a step
+    s in float16, and of each element a whole number n of 0 .. 15; the element
+    is m + n s.
+
+    ``k``, ``v``: uint8 pools [pages, Hkv, page_size, D / 2], element 2i in the
+    low half of byte i; ``k_scale``, ``v_scale``: float16 [pages, Hkv,
+    page_size, 2, groups], a row's steps, then its least values, groups =
+    max(1, D / 64).  Head dims 32, 64, 128, 256; any strides with contiguous
+    rows, as for PagedCache, bytes in multiples of 16.  ``dtype`` is the type of
+    what goes in (new keys, values, queries) and comes out.  Everything else is
+    as in PagedCache, and the same calls take either."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 page_table: torch.Tensor, seq_lens: torch.Tensor, dtype: torch.dtype = torch.bfloat16):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
+        dev = k.device
+        _need_cuda(k, "k", torch.uint8)
+        _need_cuda(v, "v", torch.uint8, dev)
+        _need_cuda(k_scale, "k_scale", torch.float16, dev)
+        _need_cuda(v_scale, "v_scale", torch.float16, dev)
+        _need_cuda(page_table, "page_table", torch.int32, dev)
+        _need_cuda(seq_lens, "seq_lens", torch.int32, dev)
+        if k.dim() != 4 or v.dim() != 4 or k.shape[:3] != v.shape[:3]:
+            raise ValueError("k must be [pages, Hkv, page_size, Dqk / 2] and v [pages, Hkv, page_size, Dv / 2]")
+        for name, t, scale in (("k", k, k_scale), ("v", v, v_scale)):
+            groups = max(1, t.shape[3] // 32)
+            if scale.shape != (*t.shape[:3], 2, groups):
+                raise ValueError(f"{name}_scale must have shape {(*t.shape[:3], 2, groups)}, got {tuple(scale.shape)}")
+            if scale.stride(3) != groups and scale.numel() > 0:
+                raise ValueError(f"{name}_scale must be contiguous in its last two dimensions")
+        if page_table.dim() != 2 or seq_lens.dim() != 1 or seq_lens.shape[0] != page_table.shape[0]:
+            raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_table, self.seq_lens = page_table, seq_lens
+        self.B, self.max_pages = page_table.shape
+        self.n_pages, self.Hkv, self.page_size = k.shape[:3]
+        self.Dqk, self.Dv = 2 * k.shape[3], 2 * v.shape[3]
+        self.device, self.dtype = dev, dtype
+        c = AttnPagedCache4()
+        c.B, c.max_pages, c.n_pages, c.page_size = self.B, self.max_pages, self.n_pages, self.page_size
+        c.Hkv, c.Dqk, c.Dv = self.Hkv, self.Dqk, self.Dv
+        c.k, c.v, c.k_scale, c.v_scale = k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()
+        c.k_stride[:], c.v_stride[:] = k.stride()[:3], v.stride()[:3]
+        c.k_scale_stride[:], c.v_scale_stride[:] = k_scale.stride()[:3], v_scale.stride()[:3]
+        c.page_table, c.table_stride, c.seq_lens = page_table.data_ptr(), page_table.stride(0), seq_lens.data_ptr()
+        self._struct, self._ref = c, ctypes.byref(c)
+        self._workspace = {}
+        self._calls = _paged_calls("4", dtype)
+
+    def _workspace_bytes(self, Hq: int) -> int:
+        with torch.cuda.device(self.device):
+            n = self._workspace[Hq] = int(lib().attn_paged_decode4_workspace(self._ref, Hq))
+        return n
+
+
+def _paged_calls(bits: str, dtype) -> dict:
+    """The library's entry points for a cache of this kind and type."""
+    L, f16 = lib(), "_f16" if dtype == torch.float16 else ""
+    calls = {name: getattr(L, f"attn_paged_{name}{bits}{f16}") for name in ("append", "decode", "weights")}
+    calls["gather"] = getattr(L, f"attn_paged_gather{bits}{f16 if bits else ''}")
+    calls["evict"] = getattr(L, f"attn_paged_evict{bits}")
+    return calls
+
+
+def attn_paged_append(cache, k: torch.Tensor, v: torch.Tensor, rope: Optional[Rope] = None,
                       q: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
                       out: Optional[torch.Tensor] = None):
     """Write the keys k [T, Hkv, Dqk] and values v [T, Hkv, Dv] of new tokens
-    into their pages, the keys rotated to their positions by ``rope``, and
-    return the queries q [T, Hq, Dqk] rotated beside them (in ``out``, which
+    into their pages of a PagedCache, or rounded to 4 bits of a PagedCache4, the
+    keys rotated to their positions by ``rope``, and return the queries q [T, Hq, Dqk] rotated beside them (in ``out``, which
     may be q itself; None without q).
 
     Without ``offsets`` T = B and token b is the last of sequence b; with
@@ -822,15 +949,13 @@ def attn_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, rope:
             raise ValueError(f"rot_dim {rope.rot_dim} exceeds the head dim {cache.Dqk}")
         if rope.steps.device != dev:
             raise ValueError(f"the rotation is on {rope.steps.device}, the cache on {dev}")
-    L = lib()
-    _call_on(dev, L.attn_paged_append_f16 if dt == torch.float16 else L.attn_paged_append, cache._ref,
-             a.buffer_info()[0], rope._ref if rope is not None else None)
+    _call_on(dev, cache._calls["append"], cache._ref, a.buffer_info()[0], rope._ref if rope is not None else None)
     return out
 
 
-def attn_paged_decode(cache: PagedCache, q: torch.Tensor, sm_scale: Optional[float] = None, out=None):
-    """Attention of one query token per sequence over the paged cache:
-    q [B, Hq, Dqk], Hq a multiple of the cache's key heads (query head h
+def attn_paged_decode(cache, q: torch.Tensor, sm_scale: Optional[float] = None, out=None):
+    """Attention of one query token per sequence over a PagedCache or
+    PagedCache4: q [B, Hq, Dqk], Hq a multiple of the cache's key heads (query head h
     reads key head h // (Hq / Hkv)).  Returns (o [B, Hq, Dv], lse [B, Hq]
     float32, natural log).  An idle place (length 0) gets o = 0, lse = -inf."""
     dev, dt, B = cache.device, cache.dtype, cache.B
@@ -855,7 +980,134 @@ def attn_paged_decode(cache: PagedCache, q: torch.Tensor, sm_scale: Optional[flo
     # of this call alone: a graph's is its own, calls on two streams have two
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
     strides = array("q", qs)
-    L = lib()
-    _call_on(dev, L.attn_paged_decode_f16 if dt == torch.float16 else L.attn_paged_decode, cache._ref, Hq,
-             q.data_ptr(), strides.buffer_info()[0], _scale(sm_scale), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), n)
+    _call_on(dev, cache._calls["decode"], cache._ref, Hq, q.data_ptr(), strides.buffer_info()[0], _scale(sm_scale),
+             o.data_ptr(), lse.data_ptr(), ws.data_ptr(), n)
     return o, lse
+
+
+def attn_paged_gather(cache, offsets: torch.Tensor, T: int, out=None):
+    """The last tokens of each sequence of a PagedCache or PagedCache4 as dense
+    jagged tensors (k [Hkv, T, Dqk], v [Hkv, T, Dv]), as attn_fwd takes them:
+    of sequence b its last offsets[b + 1] - offsets[b], int32 ``offsets``
+    [B + 1], offsets[0] = 0.  Rows at offsets[B] and behind are not written (of
+    new outputs they are undefined).  ``out``: the two tensors, any strides with
+    contiguous rows."""
+    dev, dt = cache.device, cache.dtype
+    _need(offsets, "offsets", torch.int32, dev)
+    if offsets.shape != (cache.B + 1,):
+        raise ValueError(f"offsets must be [{cache.B + 1}]")
+    T = int(T)
+    if T < 0:
+        raise ValueError("T must not be negative")
+    sk, sv = (cache.Hkv, T, cache.Dqk), (cache.Hkv, T, cache.Dv)
+    if out is None:
+        k, v = torch.empty(sk, dtype=dt, device=dev), torch.empty(sv, dtype=dt, device=dev)
+    else:
+        k, v = out
+        for name, t, shape in (("k", k, sk), ("v", v, sv)):
+            _need_cuda(t, f"out's {name}", dt, dev)
+            if t.shape != shape:
+                raise ValueError(f"out's {name} must have shape {shape}, got {tuple(t.shape)}")
+    if T > 0:
+        ks, vs = k.stride(), v.stride()
+        strides = array("q", (ks[0], ks[1], vs[0], vs[1]))
+        at = strides.buffer_info()[0]
+        _call_on(dev, cache._calls["gather"], cache._ref, T, offsets.data_ptr(), k.data_ptr(), at, v.data_ptr(), at + 16)
+    return k, v
+
+
+def _need_weights(cache, w: torch.Tensor, name: str):
+    _need_cuda(w, name, torch.float32, cache.device)
+    shape = (cache.B, cache.Hkv, cache.max_pages * cache.page_size)
+    if w.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(w.shape)}")
+
+
+def attn_paged_weights(cache, q: torch.Tensor, lse: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                       sm_scale: Optional[float] = None, decay: float = 1.0, out: Optional[torch.Tensor] = None):
+    """The attention weight of each key, added up over the steps: returns
+    ``decay`` * weights + the sum over the query heads of a key head of
+    exp(sm_scale q k - lse), float32 [B, Hkv, max_pages * page_size], for every
+    key of a sequence; entries behind its last token are those of ``weights``.
+
+    q [B, Hq, Dqk] and ``lse`` [B, Hq] are those of the step's
+    attn_paged_decode; ``weights`` None stands for zeros; ``out`` may be
+    ``weights`` itself.  At ``decay`` 0 (of 0 .. 1) only this step counts."""
+    dev, dt, B = cache.device, cache.dtype, cache.B
+    _need_cuda(q, "q", dt, dev)
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != cache.Dqk:
+        raise ValueError(f"q must be [{B}, Hq, {cache.Dqk}]")
+    Hq = q.shape[1]
+    if cache.Hkv == 0 or Hq % cache.Hkv:
+        raise ValueError(f"the cache's {cache.Hkv} key heads must divide the {Hq} query heads")
+    _need_out(lse, "lse", (B, Hq), torch.float32, dev)
+    if weights is not None:
+        _need_weights(cache, weights, "weights")
+    if out is None:
+        out = torch.empty((B, cache.Hkv, cache.max_pages * cache.page_size), dtype=torch.float32, device=dev)
+    else:
+        _need_weights(cache, out, "out")
+    a = AttnPagedWeight()
+    a.lse, a.out, a.decay = lse.data_ptr(), out.data_ptr(), decay
+    a.out_stride[:] = out.stride()[:2]
+    if weights is not None:
+        a.w = weights.data_ptr()
+        a.w_stride[:] = weights.stride()[:2]
+    strides = array("q", q.stride())
+    _call_on(dev, cache._calls["weights"], cache._ref, Hq, q.data_ptr(), strides.buffer_info()[0], _scale(sm_scale),
+             ctypes.byref(a))
+    return out
+
+
+def attn_paged_evict(cache, weights: torch.Tensor, keep, pages: torch.Tensor, sinks: int = 0, recent: int = 0,
+                     out=None):
+    """Cut the sequences of a PagedCache or PagedCache4 that hold more than
+    ``keep`` tokens (a number, or int32 [B]) down to that many: the last
+    ``recent``, the first ``sinks``, and for each key head by itself those of
+    the others with the largest ``weights`` (attn_paged_weights; of equal ones
+    the earliest), copied in their order into the pages ``pages`` [B, n] (int32;
+    pages that no sequence uses).  Returns (page_table, seq_lens, weights) as
+    they are afterwards, new ones or ``out``; weights behind a shortened
+    sequence are 0, sequences within their budget stay as they are.
+
+    The cache's own table and lengths do not change: copy the results into them
+    (cache.page_table.copy_(...), cache.seq_lens.copy_(...)) and the old pages
+    are free.  Keys stay rotated as they are; a later token's position is no
+    longer its place, so rotate it with attn_rope and its positions, and append
+    it without ``rope``."""
+    dev, B = cache.device, cache.B
+    _need_weights(cache, weights, "weights")
+    _need_cuda(pages, "pages", torch.int32, dev)
+    if pages.dim() != 2 or pages.shape[0] != B or pages.shape[1] > cache.max_pages:
+        raise ValueError(f"pages must be [{B}, at most {cache.max_pages}]")
+    a = AttnPagedEviction()
+    if isinstance(keep, torch.Tensor):
+        _need(keep, "keep", torch.int32, dev)
+        if keep.shape != (B,):
+            raise ValueError(f"keep must be a number or [{B}]")
+        a.keep = keep.data_ptr()
+    else:
+        a.keep_all = min(max(int(keep), 0), 0x7FFFFFFF)
+    if sinks < 0 or recent < 0:
+        raise ValueError("sinks and recent must not be negative")
+    if out is None:
+        table = torch.empty((B, cache.max_pages), dtype=torch.int32, device=dev)
+        lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        w = torch.empty(weights.shape, dtype=torch.float32, device=dev)
+    else:
+        table, lens, w = out
+        _need_cuda(table, "out's page_table", torch.int32, dev)
+        if table.shape != (B, cache.max_pages):
+            raise ValueError(f"out's page_table must be [{B}, {cache.max_pages}]")
+        _need_out(lens, "out's seq_lens", (B,), torch.int32, dev)
+        _need_weights(cache, w, "out's weights")
+    a.w, a.w_out = weights.data_ptr(), w.data_ptr()
+    a.w_stride[:], a.w_out_stride[:] = weights.stride()[:2], w.stride()[:2]
+    a.sinks, a.recent = min(int(sinks), 0x7FFFFFFF), min(int(recent), 0x7FFFFFFF)
+    a.pages, a.pages_stride, a.n_new = pages.data_ptr(), pages.stride(0), pages.shape[1]
+    a.table_out, a.table_out_stride, a.lens_out = table.data_ptr(), table.stride(0), lens.data_ptr()
+    n = int(lib().attn_paged_evict_workspace(B, cache.Hkv, cache.page_size, pages.shape[1]))
+    # of this call alone, as a decode's
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _call_on(dev, cache._calls["evict"], cache._ref, ctypes.byref(a), ws.data_ptr(), n)
+    return table, lens, w

@@ -347,6 +347,73 @@ __device__ __forceinline__ void decode_describe(const DecodeParams& p, const Dec
   else p.desc[x] = make_int4(b, hu, e - c - 1, own ? z : -1);
 }
 
+// Four columns of a row that is complete
+template <bool F16>
+__device__ __forceinline__ void decode_write_row(const DecodeParams& p, long long row, int col, float4 o, float mm,
+                                                 float ll) {
+  const float inv = ll == 0.f ? 0.f : 1.f / ll;
+  if (col < p.dv)
+    *reinterpret_cast<uint2*>(p.o + row * p.dv + col) =
+        make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
+  if (col == 0) p.lse[row] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
+}
+
+// What a CTA's warps hold of their last units: joined, and written by `write`
+// or to the workspace.  The parts of warp x lie at smem + x * WARP_BYTES: ROWS
+// rows of O, PITCH floats apart, then their (m, l).  held, held_end: of each
+// warp its unit (x, y), whether it begins there (z), whether it goes on from
+// the warp before (w), and the unit's last step.
+template <int DV, int NW, int WARP_BYTES, int ROWS, int PITCH, class Write>
+__device__ __forceinline__ void decode_join_held(const DecodeParams& p, const DecodeRange w, const char* smem,
+                                                 const int4* held, const long long* held_end, Write write) {
+  constexpr int THREADS = NW * 32;
+  const int tid = threadIdx.x, lane = tid & 31, first = blockIdx.x * NW;
+  // groups of warps with parts of one unit, by their first warps
+  const int used = static_cast<int>(min(static_cast<long long>(NW), w.ranges - first));  // warps with steps
+  const unsigned leads = __ballot_sync(0xffffffffu, lane < used && held[lane < used ? lane : 0].w == 0);
+  const int items = p.rows * (DV / 4);
+#pragma unroll 1
+  for (int y = tid; y < __popc(leads) * items; y += THREADS) {
+    const int gi = y / items, r = (y - gi * items) / (DV / 4), c4 = y % (DV / 4);
+    unsigned left = leads;
+    for (int k = 0; k < gi; ++k) left &= left - 1;
+    const int w0 = __ffs(left) - 1;
+    left &= left - 1;
+    const int w1 = left ? __ffs(left) - 1 : used;
+    const int4 u = held[w0];
+    const long long end = held_end[w0];  // the unit's last step
+    const bool begins = u.z != 0, ends = end < w.start(first + w1);
+    const int h = p.chunks == 1 ? u.y : u.y / p.chunks, g0 = (u.y - h * p.chunks) * p.rows;
+    if (r >= min(p.rows, p.G - g0)) continue;
+    const long long part = 2LL * (first + w0) + (begins ? 1 : 0);
+    float mm = -INFINITY, ll = 0.f;
+    for (int x = w0; x < w1; ++x)
+      mm = fmaxf(mm, reinterpret_cast<const float2*>(smem + x * WARP_BYTES + ROWS * PITCH * 4)[r].x);
+    const float top = mm == -INFINITY ? 0.f : mm;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = w0; x < w1; ++x) {
+      const char* from = smem + x * WARP_BYTES;
+      const float2 s = reinterpret_cast<const float2*>(from + ROWS * PITCH * 4)[r];
+      const float f = exp2_fast(s.x - top);
+      const float4 z = *reinterpret_cast<const float4*>(from + (r * PITCH + 4 * c4) * 4);
+      ll = fmaf(f, s.y, ll);
+      o.x = fmaf(f, z.x, o.x);
+      o.y = fmaf(f, z.y, o.y);
+      o.z = fmaf(f, z.z, o.z);
+      o.w = fmaf(f, z.w, o.w);
+    }
+    if (begins && ends) {
+      write((static_cast<long long>(u.x) * p.Hkv + h) * p.G + g0 + r, 4 * c4, o, mm, ll);
+      if (r == 0 && c4 == 0) decode_complete(p, u.x, u.y);
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (part * p.rows + r) * DV + 4 * c4) = o;
+      if (c4 == 0) p.part_ml[part * p.rows + r] = make_float2(mm, ll);
+      if (r == 0 && c4 == 0 && begins) decode_describe<NW>(p, w, u.x, u.y, first + w0, end);
+    }
+  }
+}
+
 // Eight warps with as many stages of 16 keys as shared memory holds (up to
 // four), or four where it holds less than two, or more warps of a small head
 // dim: a multiple of four always, since nine warps, three on one of the SM's
@@ -509,15 +576,6 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
       x[PITCH + 8] = acc[n][d][3] * f1;
     }
   };
-  // four columns of a row that is complete
-  auto write_row = [&](long long row, int col, float4 o, float mm, float ll) {
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    if (col < p.dv)
-      *reinterpret_cast<uint2*>(p.o + row * p.dv + col) =
-          make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
-    if (col == 0) p.lse[row] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
-  };
-
   clear();
   if (count > 0) {
     auto issue = [&](const Place& x, int stage) {
@@ -666,7 +724,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
               const int row = 8 * n + r;
               if (row < n_rows) {
                 if (begins) {
-                  write_row(row0 + row, 4 * c4, o, mm, ll);
+                  decode_write_row<F16>(p, row0 + row, 4 * c4, o, mm, ll);
                 } else {
                   *reinterpret_cast<float4*>(p.part_o + (part * p.rows + row) * DV + 4 * c4) = o;
                   if (c4 == 0) p.part_ml[part * p.rows + row] = make_float2(mm, ll);
@@ -712,51 +770,9 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     }
   }
   __syncthreads();
-  w = ranges[warp];
-  // groups of warps with parts of one unit, by their first warps
-  const int used = static_cast<int>(min(static_cast<long long>(NW), w.ranges - first));  // warps with steps
-  const unsigned leads = __ballot_sync(0xffffffffu, lane < used && held[lane < used ? lane : 0].w == 0);
-  const int items = p.rows * (DV / 4);
-#pragma unroll 1
-  for (int y = tid; y < __popc(leads) * items; y += THREADS) {
-    const int gi = y / items, r = (y - gi * items) / (DV / 4), c4 = y % (DV / 4);
-    unsigned left = leads;
-    for (int k = 0; k < gi; ++k) left &= left - 1;
-    const int w0 = __ffs(left) - 1;
-    left &= left - 1;
-    const int w1 = left ? __ffs(left) - 1 : used;
-    const int4 u = held[w0];
-    const long long end = held_end[w0];  // the unit's last step
-    const bool begins = u.z != 0, ends = end < w.start(first + w1);
-    const int h = p.chunks == 1 ? u.y : u.y / p.chunks, g0 = (u.y - h * p.chunks) * p.rows;
-    if (r >= min(p.rows, p.G - g0)) continue;
-    const long long part = 2LL * (first + w0) + (begins ? 1 : 0);
-    float mm = -INFINITY, ll = 0.f;
-    for (int x = w0; x < w1; ++x)
-      mm = fmaxf(mm, reinterpret_cast<const float2*>(smem + x * P::WARP_BYTES + ROWS * PITCH * 4)[r].x);
-    const float top = mm == -INFINITY ? 0.f : mm;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int x = w0; x < w1; ++x) {
-      const char* from = smem + x * P::WARP_BYTES;
-      const float2 s = reinterpret_cast<const float2*>(from + ROWS * PITCH * 4)[r];
-      const float f = exp2_fast(s.x - top);
-      const float4 z = *reinterpret_cast<const float4*>(from + (r * PITCH + 4 * c4) * 4);
-      ll = fmaf(f, s.y, ll);
-      o.x = fmaf(f, z.x, o.x);
-      o.y = fmaf(f, z.y, o.y);
-      o.z = fmaf(f, z.z, o.z);
-      o.w = fmaf(f, z.w, o.w);
-    }
-    if (begins && ends) {
-      write_row((static_cast<long long>(u.x) * p.Hkv + h) * p.G + g0 + r, 4 * c4, o, mm, ll);
-      if (r == 0 && c4 == 0) decode_complete(p, u.x, u.y);
-    } else {
-      *reinterpret_cast<float4*>(p.part_o + (part * p.rows + r) * DV + 4 * c4) = o;
-      if (c4 == 0) p.part_ml[part * p.rows + r] = make_float2(mm, ll);
-      if (r == 0 && c4 == 0 && begins) decode_describe<NW>(p, w, u.x, u.y, first + w0, end);
-    }
-  }
+  decode_join_held<DV, NW, P::WARP_BYTES, ROWS, PITCH>(
+      p, ranges[warp], smem, held, held_end,
+      [&](long long row, int col, float4 o, float mm, float ll) { decode_write_row<F16>(p, row, col, o, mm, ll); });
 }
 
 // Joins the parts of the units that several ranges of the kernels above share:
@@ -880,8 +896,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_decode_join(const __grid
   }
 }
 
-template <class K>
-cudaError_t decode_launch_one(K kernel, const DecodeParams& p, dim3 grid, int threads, int smem, cudaStream_t stream) {
+template <class K, class P>
+cudaError_t decode_launch_one(K kernel, const P& p, dim3 grid, int threads, int smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));

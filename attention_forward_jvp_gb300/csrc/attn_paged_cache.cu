@@ -1,0 +1,523 @@
+// Host side of attn_cache.h: argument validation, dispatch.
+#include "attn_cache.h"
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "attn_paged_cache_kernels.h"
+#include "attn_paged_host.h"
+
+namespace attn {
+
+#define ATTN_DECODE4_DECL(DQ)                                                                 \
+  extern template cudaError_t launch_decode4<DQ, 64>(Decode4Params&, int, int, cudaStream_t);  \
+  extern template cudaError_t launch_decode4<DQ, 128>(Decode4Params&, int, int, cudaStream_t); \
+  extern template cudaError_t launch_decode4<DQ, 256>(Decode4Params&, int, int, cudaStream_t);
+ATTN_DECODE4_DECL(64)
+ATTN_DECODE4_DECL(128)
+ATTN_DECODE4_DECL(256)
+
+namespace {
+
+bool dim4_ok(int d) { return d == 32 || d == 64 || d == 128 || d == 256; }
+
+// A pool's strides; whether it is aligned
+bool take_pool(void* codes, void* scales, const int64_t* st, const int64_t* ss, int D, const int64_t (&sizes)[3],
+               Pool4* out) {
+  out->codes = static_cast<uint8_t*>(codes);
+  out->scales = static_cast<uint16_t*>(scales);
+  take_strides(st, sizes, 3, out->st);
+  take_strides(ss, sizes, 3, out->ss);
+  const int row = 2 * groups4(D);
+  bool ok = aligned16(codes) && aligned(scales, 2 * row);
+  for (int i = 0; i < 3; ++i) ok = ok && out->st[i] % 16 == 0 && out->ss[i] % row == 0;
+  return ok;
+}
+
+// The checks that all calls on a cache in 4 bits share; its pools
+attn_status check_cache4(const attn_paged_cache4* c, Pool4* k, Pool4* v) {
+  if (c == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (c->B < 0 || c->max_pages < 0 || c->n_pages < 0 || c->page_size < 1 || c->Hkv < 1) return ATTN_ERR_INVALID_ARG;
+  if (!dim4_ok(c->Dqk) || !dim4_ok(c->Dv)) return ATTN_ERR_UNSUPPORTED;
+  if (c->B == 0) return ATTN_OK;
+  if (c->seq_lens == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (c->max_pages > 0 && c->page_table == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (c->n_pages > 0 && (c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(c->seq_lens, 4) || !aligned(c->page_table, 4)) return ATTN_ERR_MISALIGNED;
+  const int64_t sizes[3] = {c->n_pages, c->Hkv, c->page_size};
+  const bool ok_k = take_pool(c->k, c->k_scale, c->k_stride, c->k_scale_stride, c->Dqk, sizes, k);
+  const bool ok_v = take_pool(c->v, c->v_scale, c->v_stride, c->v_scale_stride, c->Dv, sizes, v);
+  return ok_k && ok_v ? ATTN_OK : ATTN_ERR_MISALIGNED;
+}
+// Whether pools of this cache that are written share places
+template <class C>
+bool pools_share(const C* c, const Pool4& k, const Pool4& v) {
+  const int64_t sizes[3] = {c->n_pages, c->Hkv, c->page_size};
+  if (shares_places(sizes, 3, k.st) || shares_places(sizes, 3, k.ss) || shares_places(sizes, 3, v.st) ||
+      shares_places(sizes, 3, v.ss))
+    return true;
+  const void* at[4] = {c->k, c->v, c->k_scale, c->v_scale};
+  for (int i = 0; c->n_pages > 0 && i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (at[i] == at[j]) return true;
+  return false;
+}
+
+// The keys that a row of a table of n pages can hold
+template <class C>
+int capacity_of(const C* c, int n) {
+  const int64_t keys = static_cast<int64_t>(n) * c->page_size;
+  return static_cast<int>(keys < (1 << 30) ? keys : (1 << 30));
+}
+
+// What the kernels that walk over the pages of sequences take of a cache
+template <class C>
+void take_cache(const C* c, const Device& d, DecodeParams* p) {
+  p->page_table = c->page_table;
+  p->table_stride = c->table_stride;
+  p->seq_lens = c->seq_lens;
+  p->B = c->B;
+  p->n_pages = c->n_pages;
+  p->page_size = c->page_size;
+  p->page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (c->page_size == 1 << s) p->page_shift = s;
+  p->capacity = capacity_of(c, c->max_pages);
+  p->Hkv = c->Hkv;
+  p->dqk = c->Dqk;
+  p->dv = c->Dv;
+  p->err = d.err;
+}
+
+attn_status take_scale(float sm_scale, int D, float* log2_scale) {
+  if (!std::isnan(sm_scale) && !(sm_scale > 0.f && std::isfinite(sm_scale))) return ATTN_ERR_INVALID_ARG;
+  *log2_scale = (std::isnan(sm_scale) ? 1.0f / std::sqrt(static_cast<float>(D)) : sm_scale) * 1.4426950408889634f;
+  return ATTN_OK;
+}
+
+template <class C>
+attn_status check_query(const C* c, int32_t Hq) {
+  return Hq >= 0 && Hq % c->Hkv == 0 ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+// ------------------------------------------------------------------- append
+attn_status run_append4(const attn_paged_cache4* c, const attn_paged_new* n, const attn_rope_spec* rope, void* stream,
+                        bool f16) {
+  Append4Params p4;
+  std::memset(&p4, 0, sizeof(p4));
+  AppendParams& p = p4.a;
+  attn_status st = check_cache4(c, &p4.k, &p4.v);
+  if (st != ATTN_OK) return st;
+  if (n == nullptr || n->T < 0 || n->T > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  if (n->offsets == nullptr && n->T != c->B) return ATTN_ERR_INVALID_ARG;
+  if (n->q != nullptr && (n->Hq < 0 || n->q_out == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (rope != nullptr) {
+    st = spec_of(rope, c->Dqk, false, &p.r);
+    if (st != ATTN_OK) return st;
+  }
+  if (c->B == 0 || n->T == 0) return ATTN_OK;
+  if (n->k == nullptr || n->v == nullptr) return ATTN_ERR_INVALID_ARG;
+  for (const void* x : {n->k, n->v, n->q, static_cast<const void*>(n->q_out)})
+    if (!aligned(x, 2)) return ATTN_ERR_MISALIGNED;
+  if (!aligned(n->offsets, 4)) return ATTN_ERR_MISALIGNED;
+  const int64_t kv_sizes[2] = {n->T, c->Hkv}, q_sizes[2] = {n->T, n->Hq};
+  const bool k8 = take_strides(n->k_stride, kv_sizes, 2, p.ks), v8 = take_strides(n->v_stride, kv_sizes, 2, p.vs);
+  bool vec = p.r.rot % 16 == 0 && k8 && v8 && aligned16(n->k) && aligned16(n->v);
+  if (n->q != nullptr) {
+    const bool q8 = take_strides(n->q_stride, q_sizes, 2, p.qs), o8 = take_strides(n->q_out_stride, q_sizes, 2, p.qos);
+    if (n->q == n->q_out && std::memcmp(p.qs, p.qos, sizeof(p.qs)) != 0) return ATTN_ERR_INVALID_ARG;
+    if (shares_places(q_sizes, 2, p.qos)) return ATTN_ERR_INVALID_ARG;
+    if (n->Hq > 0 && (n->q_out == n->k || n->q_out == n->v)) return ATTN_ERR_INVALID_ARG;
+    vec = vec && q8 && o8 && aligned16(n->q) && aligned16(n->q_out);
+  }
+  if (pools_share(c, p4.k, p4.v)) return ATTN_ERR_INVALID_ARG;
+  Device d;
+  st = device(&d);
+  if (st != ATTN_OK) return st;
+  p.k = static_cast<const uint16_t*>(n->k);
+  p.v = static_cast<const uint16_t*>(n->v);
+  p.q = static_cast<const uint16_t*>(n->q);
+  p.q_out = static_cast<uint16_t*>(n->q_out);
+  p.Hq = n->q != nullptr ? n->Hq : 0;
+  p.Hkv = c->Hkv;
+  p.Dqk = c->Dqk;
+  p.Dv = c->Dv;
+  p.T = n->T;
+  p.offsets = n->offsets;
+  p.page_table = c->page_table;
+  p.table_stride = c->table_stride;
+  p.seq_lens = c->seq_lens;
+  p.B = c->B;
+  p.max_pages = c->max_pages;
+  p.n_pages = c->n_pages;
+  p.page_size = c->page_size;
+  p.err = d.err;
+  const int64_t heads = static_cast<int64_t>(p.Hq) + 2 * static_cast<int64_t>(p.Hkv);
+  if (heads > 0x7fffffffLL - 64) return ATTN_ERR_INVALID_ARG;
+  // a warp for as many heads as it takes at once, or more where the tokens alone fill the card
+  const int at_once = 256 / (p.Dqk < p.Dv ? p.Dqk : p.Dv);
+  const int64_t want = (static_cast<int64_t>(d.sms) * 64 + p.T - 1) / p.T;
+  int64_t per = (heads + want - 1) / want;
+  per = (per + at_once - 1) / at_once * at_once;
+  if ((heads + per - 1) / per > 65535) per = (heads + 65534) / 65535;  // blockIdx.y
+  p.heads_per_split = static_cast<int>(per);
+  const int splits = static_cast<int>((heads + per - 1) / per);
+  if (launch_append4(p4, vec, f16, splits, static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
+  count_launch(1);
+  return ATTN_OK;
+}
+
+// ------------------------------------------------------------------- decode
+// How the kernel runs a cache's head dims and Hq query heads
+struct Layout4 {
+  int dq, dv;              // kernel head dims
+  int rows, chunks;        // query heads of a unit, units of a key head
+  size_t desc, ml, total;  // workspace: bytes of the first two parts, of all
+};
+Layout4 layout4_of(const attn_paged_cache4* c, int Hq, int sms) {
+  Layout4 l;
+  l.dq = c->Dqk < 64 ? 64 : c->Dqk;
+  l.dv = c->Dv < 64 ? 64 : c->Dv;
+  const int G = Hq / c->Hkv, most = decode4_rows(l.dv);
+  l.chunks = (G + most - 1) / most;
+  l.rows = (G + l.chunks - 1) / l.chunks;
+  const size_t warps = static_cast<size_t>(sms) * kDecodeMaxWarps;  // ranges
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  l.desc = up(sizeof(int4) * warps);
+  l.ml = up(sizeof(float2) * 2 * warps * l.rows);
+  l.total = l.desc + l.ml + sizeof(float) * 2 * warps * static_cast<size_t>(l.rows) * l.dv;
+  return l;
+}
+
+cudaError_t dispatch_decode4(const Layout4& l, Decode4Params& p, int ctas, cudaStream_t s) {
+  const int nt = (l.rows + 7) / 8;
+  switch (l.dq * 1000 + l.dv) {
+    case 64064: return launch_decode4<64, 64>(p, nt, ctas, s);
+    case 64128: return launch_decode4<64, 128>(p, nt, ctas, s);
+    case 64256: return launch_decode4<64, 256>(p, nt, ctas, s);
+    case 128064: return launch_decode4<128, 64>(p, nt, ctas, s);
+    case 128128: return launch_decode4<128, 128>(p, nt, ctas, s);
+    case 128256: return launch_decode4<128, 256>(p, nt, ctas, s);
+    case 256064: return launch_decode4<256, 64>(p, nt, ctas, s);
+    case 256128: return launch_decode4<256, 128>(p, nt, ctas, s);
+    case 256256: return launch_decode4<256, 256>(p, nt, ctas, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+attn_status run_decode4(const attn_paged_cache4* c, int32_t Hq, const void* q, const int64_t* q_stride, float sm_scale,
+                        void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream, bool f16) {
+  Decode4Params p4;
+  std::memset(&p4, 0, sizeof(p4));
+  DecodeParams& p = p4.d;
+  attn_status st = check_cache4(c, &p4.k, &p4.v);
+  if (st == ATTN_OK) st = check_query(c, Hq);
+  if (st == ATTN_OK) st = take_scale(sm_scale, c->Dqk, &p.scale_log2);
+  if (st != ATTN_OK) return st;
+  if (c->B == 0 || Hq == 0) return ATTN_OK;
+  if (q == nullptr || q_stride == nullptr || o == nullptr || lse == nullptr || workspace == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  const int64_t q_sizes[2] = {c->B, Hq};
+  if (!take_strides(q_stride, q_sizes, 2, p.qs) || !aligned16(q) || !aligned16(o) || !aligned(lse, 4) ||
+      !aligned16(workspace))
+    return ATTN_ERR_MISALIGNED;
+  Device d;
+  st = device(&d);
+  if (st != ATTN_OK) return st;
+  const Layout4 l = layout4_of(c, Hq, d.sms);
+  if (workspace_bytes < l.total) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(c->Hkv) * l.chunks > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  take_cache(c, d, &p);
+  p4.f16 = f16 ? 1 : 0;
+  p.q = static_cast<const uint16_t*>(q);
+  p.G = Hq / c->Hkv;
+  p.rows = l.rows;
+  p.chunks = l.chunks;
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  p.desc = reinterpret_cast<int4*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + l.desc);
+  p.part_o = reinterpret_cast<float*>(ws + l.desc + l.ml);
+  p.split = p.capacity > kDecode4BN ? 1 : 0;
+  const double steps = (p.capacity / kDecode4BN + 1.0) * p.B * p.Hkv * p.chunks;
+  p.wide = steps + d.sms * kDecodeMaxWarps < 2147483648.0 ? 0 : 1;
+  if (dispatch_decode4(l, p4, d.sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
+  count_launch(1 + p.split);
+  return ATTN_OK;
+}
+
+// ------------------------------------------------------------------- gather
+template <class C>
+attn_status run_gather(const C* c, GatherParams& p, int bits, int64_t T, const int32_t* offsets, void* k,
+                       const int64_t* k_stride, void* v, const int64_t* v_stride, void* stream, bool f16) {
+  if (T < 0 || T > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  if (c->B == 0 || T == 0) return ATTN_OK;
+  if (offsets == nullptr || k == nullptr || v == nullptr || k_stride == nullptr || v_stride == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  const int64_t sizes[2] = {c->Hkv, T};
+  const bool k8 = take_strides(k_stride, sizes, 2, p.ko), v8 = take_strides(v_stride, sizes, 2, p.vo);
+  if (!k8 || !v8 || !aligned16(k) || !aligned16(v) || !aligned(offsets, 4)) return ATTN_ERR_MISALIGNED;
+  if (shares_places(sizes, 2, p.ko) || shares_places(sizes, 2, p.vo) || k == v || k == c->k || k == c->v || v == c->k ||
+      v == c->v)
+    return ATTN_ERR_INVALID_ARG;
+  Device d;
+  const attn_status st = device(&d);
+  if (st != ATTN_OK) return st;
+  p.k_out = static_cast<uint16_t*>(k);
+  p.v_out = static_cast<uint16_t*>(v);
+  p.Hkv = c->Hkv;
+  p.Dqk = c->Dqk;
+  p.Dv = c->Dv;
+  p.T = T;
+  p.offsets = offsets;
+  p.page_table = c->page_table;
+  p.table_stride = c->table_stride;
+  p.seq_lens = c->seq_lens;
+  p.B = c->B;
+  p.max_pages = c->max_pages;
+  p.n_pages = c->n_pages;
+  p.page_size = c->page_size;
+  p.err = d.err;
+  const int items = (p.Dqk > p.Dv ? p.Dqk : p.Dv) / 8;
+  const int splits = head_splits(T * items, p.Hkv, d.sms, &p.heads_per_split);
+  if (launch_gather(p, bits, f16, splits, static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
+  count_launch(1);
+  return ATTN_OK;
+}
+attn_status run_gather4(const attn_paged_cache4* c, int64_t T, const int32_t* offsets, void* k, const int64_t* k_stride,
+                        void* v, const int64_t* v_stride, void* stream, bool f16) {
+  GatherParams p;
+  std::memset(&p, 0, sizeof(p));
+  const attn_status st = check_cache4(c, &p.k, &p.v);
+  if (st != ATTN_OK) return st;
+  return run_gather(c, p, 4, T, offsets, k, k_stride, v, v_stride, stream, f16);
+}
+
+// ------------------------------------------------------------------ weights
+template <class C>
+attn_status run_weights(const C* c, WeightParams& p, int bits, int32_t Hq, const void* q, const int64_t* q_stride,
+                        float sm_scale, const attn_paged_weight* w, void* stream, bool f16) {
+  attn_status st = check_query(c, Hq);
+  if (st == ATTN_OK) st = take_scale(sm_scale, c->Dqk, &p.d.scale_log2);
+  if (st != ATTN_OK) return st;
+  if (w == nullptr || !(w->decay >= 0.f && w->decay <= 1.f)) return ATTN_ERR_INVALID_ARG;
+  if (c->B == 0 || c->max_pages == 0) return ATTN_OK;
+  if (w->out == nullptr || (Hq > 0 && (q == nullptr || q_stride == nullptr || w->lse == nullptr)))
+    return ATTN_ERR_INVALID_ARG;
+  const int64_t sizes[2] = {c->B, c->Hkv}, q_sizes[2] = {c->B, Hq};
+  take_strides(w->w_stride, sizes, 2, p.ws);
+  take_strides(w->out_stride, sizes, 2, p.os);
+  if (!aligned(w->lse, 4) || !aligned(w->w, 4) || !aligned(w->out, 4)) return ATTN_ERR_MISALIGNED;
+  if (Hq > 0 && (!take_strides(q_stride, q_sizes, 2, p.d.qs) || !aligned16(q))) return ATTN_ERR_MISALIGNED;
+  if (shares_places(sizes, 2, p.os)) return ATTN_ERR_INVALID_ARG;
+  if (w->out == w->w && std::memcmp(p.ws, p.os, sizeof(p.ws)) != 0) return ATTN_ERR_INVALID_ARG;
+  Device d;
+  st = device(&d);
+  if (st != ATTN_OK) return st;
+  take_cache(c, d, &p.d);
+  p.d.q = static_cast<const uint16_t*>(q);
+  p.d.G = Hq / c->Hkv;
+  p.d.rows = p.d.G;
+  p.d.chunks = 1;
+  p.d.whole = c->page_size % kDecodeBN == 0 ? 1 : 0;
+  p.f16 = f16 ? 1 : 0;
+  p.lse = w->lse;
+  p.w = w->w;
+  p.out = w->out;
+  p.decay = w->decay;
+  p.places = static_cast<long long>(c->max_pages) * c->page_size;
+  const double steps = (p.d.capacity / kDecodeBN + 1.0) * c->B * c->Hkv;
+  p.d.wide = steps + d.sms * kDecodeMaxWarps < 2147483648.0 ? 0 : 1;
+  if (launch_weights(p, c->Dqk < 64 ? 64 : c->Dqk, bits, d.sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  count_launch(1);
+  return ATTN_OK;
+}
+attn_status run_weights16(const attn_paged_cache* c, int32_t Hq, const void* q, const int64_t* q_stride, float sm_scale,
+                          const attn_paged_weight* w, void* stream, bool f16) {
+  WeightParams p;
+  std::memset(&p, 0, sizeof(p));
+  const attn_status st = check_cache(c, p.d.kp, p.d.vp);
+  if (st != ATTN_OK) return st;
+  p.d.k = static_cast<const uint16_t*>(c->k);
+  return run_weights(c, p, 16, Hq, q, q_stride, sm_scale, w, stream, f16);
+}
+attn_status run_weights4(const attn_paged_cache4* c, int32_t Hq, const void* q, const int64_t* q_stride, float sm_scale,
+                         const attn_paged_weight* w, void* stream, bool f16) {
+  WeightParams p;
+  std::memset(&p, 0, sizeof(p));
+  Pool4 v;
+  const attn_status st = check_cache4(c, &p.k, &v);
+  if (st != ATTN_OK) return st;
+  return run_weights(c, p, 4, Hq, q, q_stride, sm_scale, w, stream, f16);
+}
+
+// ----------------------------------------------------------------- eviction
+size_t evict_workspace(int32_t B, int32_t Hkv, int32_t page_size, int32_t n_new) {
+  if (B < 0 || Hkv < 1 || page_size < 1 || n_new < 0) return 0;
+  const int64_t keys = static_cast<int64_t>(n_new) * page_size;
+  return sizeof(int32_t) * static_cast<size_t>(B) * Hkv * (keys < (1 << 30) ? keys : (1 << 30));
+}
+
+template <class C>
+attn_status run_evict(const C* c, EvictParams& p, int bits, const attn_paged_eviction* a, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  if (a == nullptr || a->sinks < 0 || a->recent < 0 || a->n_new < 0 || a->n_new > c->max_pages)
+    return ATTN_ERR_INVALID_ARG;
+  if (c->B == 0) return ATTN_OK;
+  if (a->lens_out == nullptr || (c->max_pages > 0 && (a->w == nullptr || a->w_out == nullptr || a->table_out == nullptr)) ||
+      (a->n_new > 0 && (a->pages == nullptr || workspace == nullptr)))
+    return ATTN_ERR_INVALID_ARG;
+  const int64_t sizes[2] = {c->B, c->Hkv}, rows[2] = {c->B, c->max_pages};
+  take_strides(a->w_stride, sizes, 2, p.ws);
+  take_strides(a->w_out_stride, sizes, 2, p.wos);
+  if (!aligned(a->w, 4) || !aligned(a->w_out, 4) || !aligned(a->keep, 4) || !aligned(a->pages, 4) ||
+      !aligned(a->table_out, 4) || !aligned(a->lens_out, 4) || !aligned16(workspace))
+    return ATTN_ERR_MISALIGNED;
+  const int64_t row_stride[2] = {a->table_out_stride, 1};
+  long long table[2];
+  take_strides(row_stride, rows, 2, table);
+  if (shares_places(sizes, 2, p.wos) || shares_places(rows, 2, table)) return ATTN_ERR_INVALID_ARG;
+  if (a->lens_out == c->seq_lens || a->lens_out == a->keep) return ATTN_ERR_INVALID_ARG;
+  if (c->max_pages > 0 && (a->w == a->w_out || a->table_out == c->page_table || a->table_out == a->pages ||
+                           a->table_out == a->lens_out))
+    return ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < evict_workspace(c->B, c->Hkv, c->page_size, a->n_new)) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(c->B) * c->Hkv > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  Device d;
+  const attn_status st = device(&d);
+  if (st != ATTN_OK) return st;
+  p.B = c->B;
+  p.Hkv = c->Hkv;
+  p.max_pages = c->max_pages;
+  p.n_pages = c->n_pages;
+  p.page_size = c->page_size;
+  p.n_new = a->n_new;
+  p.capacity = capacity_of(c, c->max_pages);
+  p.new_capacity = capacity_of(c, a->n_new);
+  p.page_table = c->page_table;
+  p.table_stride = c->table_stride;
+  p.seq_lens = c->seq_lens;
+  p.keep = a->keep;
+  p.keep_all = a->keep_all;
+  p.sinks = a->sinks;
+  p.recent = a->recent;
+  p.pages = a->pages;
+  p.pages_stride = a->pages_stride;
+  p.table_out = a->table_out;
+  p.table_out_stride = a->table_out_stride;
+  p.lens_out = a->lens_out;
+  p.w = a->w;
+  p.w_out = a->w_out;
+  p.places = static_cast<long long>(c->max_pages) * c->page_size;
+  p.index = static_cast<int*>(workspace);
+  p.Dqk = c->Dqk;
+  p.Dv = c->Dv;
+  p.err = d.err;
+  int launches = 0;
+  if (launch_evict(p, bits, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess) return ATTN_ERR_CUDA;
+  count_launch(launches);
+  return ATTN_OK;
+}
+
+}  // namespace
+
+}  // namespace attn
+
+extern "C" {
+
+attn_status attn_paged_append4(const attn_paged_cache4* cache, const attn_paged_new* tokens, const attn_rope_spec* rope,
+                               void* stream) {
+  return attn::run_append4(cache, tokens, rope, stream, false);
+}
+attn_status attn_paged_append4_f16(const attn_paged_cache4* cache, const attn_paged_new* tokens,
+                                   const attn_rope_spec* rope, void* stream) {
+  return attn::run_append4(cache, tokens, rope, stream, true);
+}
+
+size_t attn_paged_decode4_workspace(const attn_paged_cache4* cache, int32_t Hq) {
+  attn::Pool4 k, v;
+  if (attn::check_cache4(cache, &k, &v) != ATTN_OK || attn::check_query(cache, Hq) != ATTN_OK || cache->B == 0 || Hq == 0)
+    return 0;
+  attn::Device d;
+  if (attn::device(&d) != ATTN_OK) return 0;
+  return attn::layout4_of(cache, Hq, d.sms).total;
+}
+attn_status attn_paged_decode4(const attn_paged_cache4* cache, int32_t Hq, const void* q, const int64_t q_stride[2],
+                               float sm_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  return attn::run_decode4(cache, Hq, q, q_stride, sm_scale, o, lse, workspace, workspace_bytes, stream, false);
+}
+attn_status attn_paged_decode4_f16(const attn_paged_cache4* cache, int32_t Hq, const void* q, const int64_t q_stride[2],
+                                   float sm_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  return attn::run_decode4(cache, Hq, q, q_stride, sm_scale, o, lse, workspace, workspace_bytes, stream, true);
+}
+
+attn_status attn_paged_gather(const attn_paged_cache* cache, int64_t T, const int32_t* offsets, void* k,
+                              const int64_t k_stride[2], void* v, const int64_t v_stride[2], void* stream) {
+  attn::GatherParams p;
+  std::memset(&p, 0, sizeof(p));
+  const attn_status st = attn::check_cache(cache, p.kp, p.vp);
+  if (st != ATTN_OK) return st;
+  p.k16 = static_cast<const uint16_t*>(cache->k);
+  p.v16 = static_cast<const uint16_t*>(cache->v);
+  return attn::run_gather(cache, p, 16, T, offsets, k, k_stride, v, v_stride, stream, false);
+}
+attn_status attn_paged_gather4(const attn_paged_cache4* cache, int64_t T, const int32_t* offsets, void* k,
+                               const int64_t k_stride[2], void* v, const int64_t v_stride[2], void* stream) {
+  return attn::run_gather4(cache, T, offsets, k, k_stride, v, v_stride, stream, false);
+}
+attn_status attn_paged_gather4_f16(const attn_paged_cache4* cache, int64_t T, const int32_t* offsets, void* k,
+                                   const int64_t k_stride[2], void* v, const int64_t v_stride[2], void* stream) {
+  return attn::run_gather4(cache, T, offsets, k, k_stride, v, v_stride, stream, true);
+}
+
+attn_status attn_paged_weights(const attn_paged_cache* cache, int32_t Hq, const void* q, const int64_t q_stride[2],
+                               float sm_scale, const attn_paged_weight* weight, void* stream) {
+  return attn::run_weights16(cache, Hq, q, q_stride, sm_scale, weight, stream, false);
+}
+attn_status attn_paged_weights_f16(const attn_paged_cache* cache, int32_t Hq, const void* q, const int64_t q_stride[2],
+                                   float sm_scale, const attn_paged_weight* weight, void* stream) {
+  return attn::run_weights16(cache, Hq, q, q_stride, sm_scale, weight, stream, true);
+}
+attn_status attn_paged_weights4(const attn_paged_cache4* cache, int32_t Hq, const void* q, const int64_t q_stride[2],
+                                float sm_scale, const attn_paged_weight* weight, void* stream) {
+  return attn::run_weights4(cache, Hq, q, q_stride, sm_scale, weight, stream, false);
+}
+attn_status attn_paged_weights4_f16(const attn_paged_cache4* cache, int32_t Hq, const void* q, const int64_t q_stride[2],
+                                    float sm_scale, const attn_paged_weight* weight, void* stream) {
+  return attn::run_weights4(cache, Hq, q, q_stride, sm_scale, weight, stream, true);
+}
+
+size_t attn_paged_evict_workspace(int32_t B, int32_t Hkv, int32_t page_size, int32_t n_new) {
+  return attn::evict_workspace(B, Hkv, page_size, n_new);
+}
+attn_status attn_paged_evict(const attn_paged_cache* cache, const attn_paged_eviction* evict, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  attn::EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  const attn_status st = attn::check_cache(cache, p.kp, p.vp);
+  if (st != ATTN_OK) return st;
+  const int64_t sizes[3] = {cache->n_pages, cache->Hkv, cache->page_size};
+  if (cache->B > 0 && (attn::shares_places(sizes, 3, p.kp) || attn::shares_places(sizes, 3, p.vp)))
+    return ATTN_ERR_INVALID_ARG;
+  p.k16 = static_cast<uint16_t*>(cache->k);
+  p.v16 = static_cast<uint16_t*>(cache->v);
+  return attn::run_evict(cache, p, 16, evict, workspace, workspace_bytes, stream);
+}
+attn_status attn_paged_evict4(const attn_paged_cache4* cache, const attn_paged_eviction* evict, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  attn::EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  const attn_status st = attn::check_cache4(cache, &p.k, &p.v);
+  if (st != ATTN_OK) return st;
+  if (cache->B > 0 && attn::pools_share(cache, p.k, p.v)) return ATTN_ERR_INVALID_ARG;
+  return attn::run_evict(cache, p, 4, evict, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,107 @@
+// The cache in 4 bits, reading back, weights and eviction: what the host side
+// (attn_paged_cache.cu) hands to the kernels.
+#pragma once
+#include "attn_paged_kernels.h"
+
+namespace attn {
+
+// groups of a row of d elements that share a step and a least value
+__host__ __device__ constexpr int groups4(int d) { return d < 64 ? 1 : d / 64; }
+
+// Keys or values of a cache in 4 bits, by (page, head, token)
+struct Pool4 {
+  uint8_t* codes;
+  uint16_t* scales;  // fp16: a row's steps, then its least values
+  long long st[3];   // bytes
+  long long ss[3];   // elements
+};
+
+// The pools of a 16-bit cache are in `a`; those of one in 4 bits here
+struct Append4Params {
+  AppendParams a;
+  Pool4 k, v;
+};
+
+struct GatherParams {
+  const uint16_t *k16, *v16;  // 16 bits
+  long long kp[3], vp[3];
+  Pool4 k, v;                 // 4 bits
+  uint16_t *k_out, *v_out;
+  long long ko[2], vo[2];     // head, token
+  int Hkv, Dqk, Dv;
+  int heads_per_split;
+  long long T;
+  const int* offsets;
+  const int* page_table;
+  long long table_stride;
+  const int* seq_lens;
+  int B, max_pages, n_pages, page_size;
+  int* err;
+};
+
+cudaError_t launch_append4(const Append4Params& p, bool vec, bool f16, int splits, cudaStream_t stream);
+// bits: 16 or 4; f16: the type that 4 bits become
+cudaError_t launch_gather(const GatherParams& p, int bits, bool f16, int splits, cudaStream_t stream);
+
+// ------------------------------------------------------------------ decode
+constexpr int kDecode4BN = 32;  // keys of a step
+
+// Query heads of a unit at most, in groups of 8: each takes DV / 4 registers of
+// accumulators and more for the corrections.  More heads are units of their
+// own, which read the key head's pages again, at 4.5 bits an element.
+constexpr int decode4_rows(int dv) { return dv == 64 ? 32 : (dv == 128 ? 24 : 16); }
+
+struct Decode4Params {
+  DecodeParams d;  // (its 16-bit pools unused)
+  Pool4 k, v;
+  int f16;         // the type of q and o
+};
+
+// The decode kernel over a cache in 4 bits for kernel head dims DQ, DV and nt
+// groups of 8 query heads to a unit, followed, when p.d.split, by the join
+template <int DQ, int DV>
+cudaError_t launch_decode4(Decode4Params& p, int nt, int ctas, cudaStream_t stream);
+
+// ----------------------------------------------------------------- weights
+struct WeightParams {
+  DecodeParams d;     // (no values, workspace or outputs)
+  Pool4 k;            // of a cache in 4 bits
+  int f16;            // the type of q
+  const float* lse;   // [B, Hkv * G]
+  const float* w;     // or null
+  float* out;
+  long long ws[2], os[2];  // sequence, head
+  float decay;
+  long long places;   // of a row
+};
+// dq: kernel head dim; bits: 16 or 4
+cudaError_t launch_weights(const WeightParams& p, int dq, int bits, int ctas, cudaStream_t stream);
+
+// ---------------------------------------------------------------- eviction
+struct EvictParams {
+  int B, Hkv, max_pages, n_pages, page_size, n_new;
+  int capacity, new_capacity;  // keys of a row of the old table, of the new pages
+  const int* page_table;
+  long long table_stride;
+  const int* seq_lens;
+  const int* keep;             // or null
+  int keep_all, sinks, recent;
+  const int* pages;
+  long long pages_stride;
+  int* table_out;
+  long long table_out_stride;
+  int* lens_out;
+  const float* w;
+  float* w_out;
+  long long ws[2], wos[2], places;
+  int* index;                  // [B][Hkv][new_capacity]: the kept tokens of a head
+  uint16_t *k16, *v16;
+  long long kp[3], vp[3];
+  Pool4 k, v;
+  int Dqk, Dv;
+  int* err;
+};
+// launches: how many kernels it came to
+cudaError_t launch_evict(const EvictParams& p, int bits, cudaStream_t stream, int* launches);
+
+}  // namespace attn

@@ -1,0 +1,466 @@
+// Attention of one query token per sequence over a paged cache in 4 bits.
+//
+// Mathematics: that of attn_decode_kernel.cuh, with keys and values m + n s (n
+// whole, a step s and a least value m for each row's group of 64 elements):
+//
+//   S_hj  = sum_g s_jg (q_h n_j)_g + m_jg sum(q_h)_g        (scores4)
+//   O_hd  = sum_j P_hj m_jg + 8 sum_j P_hj s_jg + sum_j P'_hjg (n_jd - 8),
+//           P' = fp16(P s)
+//
+// With n - 8 the rounding of P' meets numbers about zero: the output is off by
+// 2^-12 of each key's part, not of 2.6 times it.  n itself is the operand (a
+// subnormal, attn_paged_values4.cuh); the sum of P' 8 comes from a product of
+// its own, the sums of P m and P s, and of P as it was rounded, from another
+// (a row each).  P is rounded to fp16 once and O normalised by the sum of the
+// rounded P, so that this rounding costs only where keys differ; the LSE takes
+// the sum in fp32.
+//
+// P s must not pass 65504: the reference of the probabilities lies 11 below
+// the maximum and P goes up to 2^15 (DecodeReference), less as many powers of
+// two as the steps of the values seen go above 1.
+//
+// What bounds it: memory, 0.5625 bytes an element, read once; but 3.6 times as
+// many elements a byte as in 16 bits, so that the instructions count: a row's
+// words become operands in two and a half instructions for four elements, and
+// a step takes 32 keys.  The list of steps, the ranges, the ring of a warp's
+// own, and the joins are those of attn_decode_kernel.cuh.
+#pragma once
+#include "attn_paged_values4.cuh"
+
+namespace attn {
+
+template <int DQ, int DV, int NT>
+struct Decode4Plan {
+  static constexpr int BN = kDecode4BN, GQ = groups4(DQ), GV = groups4(DV);
+  static constexpr int K_BYTES = BN * DQ / 2, V_BYTES = BN * DV / 2, KS_BYTES = BN * 4 * GQ, VS_BYTES = BN * 4 * GV;
+  static constexpr int STAGE = K_BYTES + V_BYTES + KS_BYTES + VS_BYTES;
+  static constexpr int MISC_BYTES = (8 * 32 + 16 + 24 + sizeof(DecodeRange)) * kDecodeMaxWarps;
+  static constexpr int FIT = 226 * 1024 - MISC_BYTES;
+  // O, its corrections and statistics; Q
+  static constexpr int REGS = (DV / 4 + 4 * GV + 4) * NT + (DQ / 8 + 4) * NT + 80;
+  static constexpr int NW_REGS = REGS <= 128 ? 16 : (REGS <= 160 ? 12 : 8);
+  static constexpr int S = FIT / NW_REGS / STAGE >= 4 ? 4 : (FIT / NW_REGS / STAGE >= 3 ? 3 : 2);
+  static constexpr int PITCH = DV + 4;
+  static constexpr int PARTS = NT * 8 * (PITCH * 4 + 8);  // what a warp leaves at the end
+  static constexpr int SPILL = 8 * PITCH * 4;             // eight heads of O on their way out
+  static constexpr int RING = (S * STAGE > PARTS ? S * STAGE : PARTS) + (SPILL > STAGE ? SPILL : 0);
+  static constexpr int WARP_BYTES = (RING + 127) / 128 * 128;
+  static constexpr int NW_SMEM = FIT / WARP_BYTES / 4 * 4;
+  static constexpr int NW = NW_SMEM < NW_REGS ? NW_SMEM : NW_REGS;
+  static_assert(NW >= 4 && NW <= kDecodeMaxWarps, "decode plan");
+  static constexpr int SMEM = NW * WARP_BYTES + MISC_BYTES;
+};
+
+template <int DQ, int DV, int NT>
+__global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
+    attn_paged_decode4_kernel(const __grid_constant__ Decode4Params p4) {
+  using P = Decode4Plan<DQ, DV, NT>;
+  constexpr int BN = P::BN, S = P::S, NW = P::NW, THREADS = NW * 32, PITCH = P::PITCH, GV = P::GV;
+  constexpr unsigned ALL = 0xffffffffu;
+  const DecodeParams& p = p4.d;
+  extern __shared__ __align__(128) char decode_smem[];
+  char* smem = decode_smem;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  char* mine = smem + warp * P::WARP_BYTES;
+  const uint32_t ring = smem_u32(mine);
+  char* misc = smem + NW * P::WARP_BYTES;
+  const DecodeWords words{reinterpret_cast<int*>(misc), reinterpret_cast<uint32_t*>(misc) + THREADS,
+                          reinterpret_cast<long long*>(misc + 8 * THREADS)};
+  // of each warp at its end (decode_join_held)
+  DecodeRange* ranges = reinterpret_cast<DecodeRange*>(misc + P::MISC_BYTES - (24 + sizeof(DecodeRange)) * kDecodeMaxWarps);
+  int4* held = reinterpret_cast<int4*>(misc + P::MISC_BYTES - 24 * kDecodeMaxWarps);
+  long long* held_end = reinterpret_cast<long long*>(misc + P::MISC_BYTES - 8 * kDecodeMaxWarps);
+  const int HU = p.Hkv * p.chunks;  // units of a sequence
+
+  griddep_wait();
+  griddep_launch_dependents();
+
+  auto length = [&](int b) {
+    const int n = p.seq_lens[b];
+    return n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
+  };
+  auto steps_of = [](int len) { return (len + BN - 1) / BN; };
+  struct Cursor {
+    int b, hu, t, nt, len;
+  };
+  // the next step of the list (the caller knows that there is one)
+  auto advance = [&](Cursor& a) {
+    if (++a.t < a.nt) return;
+    a.t = 0;
+    if (++a.hu < HU) return;
+    a.hu = 0;
+    while (a.b + 1 < p.B) {
+      ++a.b;
+      a.len = length(a.b);
+      a.nt = steps_of(a.len);
+      if (a.nt > 0) break;
+    }
+  };
+  auto lookup = [&](const Cursor& a) {
+    return lookup4(p, p.page_table + a.b * p.table_stride, a.t * BN, a.len, p.chunks == 1 ? a.hu : a.hu / p.chunks);
+  };
+
+  // ---- this warp's range, and the places of its first steps
+  const int me = blockIdx.x * NW + warp;
+  DecodeRange w = p.wide ? decode_plan<long long, BN, NW, true>(p, words) : decode_plan<int, BN, NW, true>(p, words);
+  const int count = w.count;
+  Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len};  // the step computed next
+  Cursor ahead = cur;                                  // the step that `next` is of
+  Place4 next, now[S - 1];
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    if (j < count) {
+      (j < S - 1 ? now[j < S - 1 ? j : 0] : next) = lookup(ahead);
+      if (j + 1 < count && j + 1 < S) advance(ahead);
+    }
+  }
+  if (w.idle) decode_idle(p);
+  if (p.split && !p.by_unit && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
+  if (w.cta_lo >= w.total) return;
+  if (lane == 0) ranges[warp] = w;
+
+  float acc[NT][GV][4][4];  // [64 columns][product]: columns 8 g + 2 i of heads 2 t, 2 t + 1, then 8 g + 2 i + 1 (16-fold)
+  float eight[NT][GV][4];   // sum P' 8, the same in every row
+  float stat[NT][4];        // rows 0 .. GV - 1: sum P m, 4: sum P; rows 8 ..: sum P s
+  float m[NT][2], l[NT][2];
+  Query4<DQ, NT> q;
+  int top = 0;              // the steps of the values seen are at most 2^top
+  auto clear = [&]() {
+    top = 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        stat[n][e] = 0.f;
+#pragma unroll
+        for (int b = 0; b < GV; ++b) {
+          eight[n][b][e] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][b][i][e] = 0.f;
+        }
+      }
+    }
+  };
+  auto load_q = [&](const Cursor& a) {
+    const int h = a.hu / p.chunks, g0 = (a.hu - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
+    const uint16_t* base = p.q + a.b * p.qs[0] + (static_cast<long long>(h) * p.G + g0) * p.qs[1];
+    if (p4.f16) q.template load<true>(base, p.qs[1], n_rows, p.dqk, p.scale_log2);
+    else q.template load<false>(base, p.qs[1], n_rows, p.dqk, p.scale_log2);
+  };
+  auto write_row = [&](long long row, int col, float4 o, float mm, float ll) {
+    if (p4.f16) decode_write_row<true>(p, row, col, o, mm, ll);
+    else decode_write_row<false>(p, row, col, o, mm, ll);
+  };
+  // l over the lanes; O of group n from its sums, times l by the sum of the
+  // rounded P, to [head][DV] in shared memory
+  auto finish = [&](int n, float* to) {
+    float f[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(ALL, l[n][e], o);
+      const float sum = __shfl_sync(ALL, stat[n][e], 16 + t);
+      f[e] = sum == 0.f ? 0.f : l[n][e] / sum;
+    }
+#pragma unroll
+    for (int b = 0; b < GV; ++b) {
+      float base[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        base[e] = __shfl_sync(ALL, stat[n][e], 4 * b + t) + 8.f * __shfl_sync(ALL, stat[n][2 + e], 4 * b + t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = (acc[n][b][i][e] - eight[n][b][e]) * 16777216.f + base[e];
+          const float y = (acc[n][b][i][2 + e] * 0.0625f - eight[n][b][e]) * 16777216.f + base[e];
+          *reinterpret_cast<float2*>(to + (2 * t + e) * PITCH + 64 * b + 8 * g + 2 * i) = make_float2(x * f[e], y * f[e]);
+        }
+    }
+  };
+
+  clear();
+  if (count > 0) {
+    auto issue = [&](Place4& x, int stage) {
+      const uint32_t to = ring + stage * P::STAGE;
+      report4(p, x);
+      copy_rows4<DQ, true>(p4.k, x, p.dqk, to, to + P::K_BYTES + P::V_BYTES);
+      copy_rows4<DV, false>(p4.v, x, p.dv, to + P::K_BYTES, to + P::K_BYTES + P::V_BYTES + P::KS_BYTES);
+    };
+    load_q(cur);
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j) {
+      if (j < count) issue(now[j], j);
+      cp_async_commit();
+    }
+
+    int t0 = cur.t;  // first step of the unit in this warp
+    int stage = 0;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      // refill the stage of the step before this one, which every lane has read
+      __syncwarp();
+      if (i + S - 1 < count) {
+        issue(next, stage == 0 ? S - 1 : stage - 1);
+        if (i + S < count) {
+          advance(ahead);
+          next = lookup(ahead);
+        }
+      }
+      cp_async_commit();
+      cp_async_wait<S - 1>();
+      __syncwarp();
+
+      const uint32_t sk = ring + stage * P::STAGE, sv = sk + P::K_BYTES, sks = sv + P::V_BYTES, svs = sks + P::KS_BYTES;
+      const int live = cur.len - cur.t * BN;  // keys of this step
+      float s[2][NT][4];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) scores4<DQ, NT>(q, sk, sks, 16 * kt, s[kt]);
+      // the largest step of the values of key `lane`
+      uint32_t steps[GV];
+      lds_row<GV>(svs + lane * (4 * GV), steps);
+      float most = fabsf(half_at<GV>(steps, 0));
+#pragma unroll
+      for (int b = 1; b < GV; ++b) most = fmaxf(most, fabsf(half_at<GV>(steps, b)));
+      bool grows = most > __int_as_float((127 + top) << 23);
+      float room = DecodeReference<true>::room - top;
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float& x = s[kt][n][e];
+            x *= q.scale[n][e & 1];
+            if (16 * kt + g + (e >> 1) * 8 >= live) x = -INFINITY;
+            grows = grows || x > m[n][e & 1] + room;
+          }
+      if (__any_sync(ALL, grows)) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(ALL, most, o));
+        // (2^-126 .. 2^16: the exponent above the step's, none of an infinite one)
+        const int up = (__float_as_int(most) >> 23) - 126;
+        top = most > __int_as_float((127 + top) << 23) ? min(up, 16) : top;
+        room = DecodeReference<true>::room - top;
+        const float below = DecodeReference<true>::below - top;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+            x = fmaxf(x, __shfl_xor_sync(ALL, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(ALL, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(ALL, x, 16));
+            x = fmaxf(x - below, m[n][e]);
+            const float a = exp2_fast(m[n][e] - (x == -INFINITY ? 0.f : x));
+            m[n][e] = x;
+            l[n][e] *= a;
+            stat[n][e] *= a;
+            stat[n][2 + e] *= a;
+#pragma unroll
+            for (int b = 0; b < GV; ++b) {
+              eight[n][b][e] *= a;
+              eight[n][b][2 + e] *= a;
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                acc[n][b][d][e] *= a;
+                acc[n][b][d][2 + e] *= a;
+              }
+            }
+          }
+      }
+      uint32_t ph[2][NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        // a head whose scores are all -inf keeps weights of 0
+        const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0], u1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float a = exp2_fast(s[kt][n][2 * e] - u0), b = exp2_fast(s[kt][n][2 * e + 1] - u1);
+            l[n][0] += a;
+            l[n][1] += b;
+            ph[kt][n][e] = movmatrix_t(pack2<true>(a, b));
+          }
+      }
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        // the steps and least values of keys 2 t, 2 t + 1 and 8 further on
+        uint32_t step[GV][2], a[4];
+        {
+          uint32_t row[2][2][GV];
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) lds_row<GV>(svs + (16 * kt + 8 * o + 2 * t + e) * (4 * GV), row[o][e]);
+          // half i of both keys' rows
+          auto both = [&](int o, int i) {
+            return __byte_perm(row[o][0][i >> 1], row[o][1][i >> 1], i & 1 ? 0x7632 : 0x5410);
+          };
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            uint32_t least = 0u, each = 0u;
+#pragma unroll
+            for (int b = 0; b < GV; ++b) {
+              step[b][o] = both(o, b);
+              const uint32_t x = both(o, GV + b);
+              least = g == b ? x : least;
+              each = g == b ? step[b][o] : each;
+            }
+            a[2 * o] = g == 4 ? 0x3c003c00u : least;  // row 4: ones
+            a[2 * o + 1] = each;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816<true>(stat[n], a, ph[kt][n][0], ph[kt][n][1]);
+#pragma unroll
+        for (int b = 0; b < GV; ++b) {
+          uint32_t ps[NT][2];
+          const uint32_t eights[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};  // 8 2^-24
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            ps[n][0] = mul_half2(ph[kt][n][0], step[b][0]);
+            ps[n][1] = mul_half2(ph[kt][n][1], step[b][1]);
+            mma16816<true>(eight[n][b], eights, ps[n][0], ps[n][1]);
+          }
+          uint32_t word[2][2];  // of keys 2 t + e, and 8 further on
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = 16 * kt + 8 * o + 2 * t + e;
+              word[o][e] = lds32(sv + value_row<DV>(key) * (DV / 2) + value_slot<DV>(key, b) * 32 + 4 * g);
+            }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {  // elements 4 c .. 4 c + 3 of the word's eight
+            uint32_t r[2][4];
+            nibbles(__byte_perm(word[0][0], word[0][1], c ? 0x7632 : 0x5410), r[0]);
+            nibbles(__byte_perm(word[1][0], word[1][1], c ? 0x7632 : 0x5410), r[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t v[4] = {r[0][2 * i], r[0][2 * i + 1], r[1][2 * i], r[1][2 * i + 1]};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma16816<true>(acc[n][b][2 * c + i], v, ps[n][0], ps[n][1]);
+            }
+          }
+        }
+      }
+
+      // ---- the unit ends here, or the range does
+      const bool last = i + 1 == count;
+      if (cur.t + 1 == cur.nt || last) {
+        const bool begins = t0 == 0;
+        if (!last) {  // (the range's last unit is joined with the other warps' below; this one ends here)
+          const int h = cur.hu / p.chunks, g0 = (cur.hu - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
+          const long long part = 2LL * me;
+          const long long row0 = (static_cast<long long>(cur.b) * p.Hkv + h) * p.G + g0;
+          if (begins && lane == 0) decode_complete(p, cur.b, cur.hu);
+          // this step's stage, which has been read and is refilled in the next step; where eight heads are larger, a place apart
+          float* scratch = reinterpret_cast<float*>(P::SPILL > P::STAGE ? mine + P::WARP_BYTES - P::SPILL : mine + stage * P::STAGE);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            __syncwarp();
+            finish(n, scratch);
+            __syncwarp();
+#pragma unroll
+            for (int x = lane; x < 8 * (DV / 4); x += 32) {
+              const int r = x / (DV / 4), c4 = x % (DV / 4);
+              const float ma = __shfl_sync(ALL, m[n][0], r >> 1), mb = __shfl_sync(ALL, m[n][1], r >> 1);
+              const float la = __shfl_sync(ALL, l[n][0], r >> 1), lb = __shfl_sync(ALL, l[n][1], r >> 1);
+              const float mm = r & 1 ? mb : ma, ll = r & 1 ? lb : la;
+              const float4 o = *reinterpret_cast<const float4*>(scratch + r * PITCH + 4 * c4);
+              const int row = 8 * n + r;
+              if (row < n_rows) {
+                if (begins) {
+                  write_row(row0 + row, 4 * c4, o, mm, ll);
+                } else {
+                  *reinterpret_cast<float4*>(p.part_o + (part * p.rows + row) * DV + 4 * c4) = o;
+                  if (c4 == 0) p.part_ml[part * p.rows + row] = make_float2(mm, ll);
+                }
+              }
+            }
+          }
+        }
+        if (last) {
+          if (lane == 0) {
+            // goes on where the warp before has left off?
+            const bool goes_on = warp > 0 && i == cur.t - t0 && t0 > 0;
+            held[warp] = make_int4(cur.b, cur.hu, begins ? 1 : 0, goes_on ? 1 : 0);
+            held_end[warp] = ranges[warp].lo + i + (cur.nt - 1 - cur.t);
+          }
+        } else {
+          clear();
+          advance(cur);
+          t0 = 0;
+          load_q(cur);
+        }
+      } else {
+        ++cur.t;
+      }
+      stage = stage + 1 == S ? 0 : stage + 1;
+    }
+  }
+
+  // ---- what the warps hold of their last units: joined, written
+  constexpr int ROWS = NT * 8;
+  float* parts = reinterpret_cast<float*>(mine);
+  float2* my_ml = reinterpret_cast<float2*>(parts + ROWS * PITCH);  // behind O
+  cp_async_wait<0>();
+  __syncwarp();
+  if (count > 0) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      finish(n, parts + 8 * n * PITCH);
+      if (g == 0) {
+        my_ml[8 * n + 2 * t] = make_float2(m[n][0], l[n][0]);
+        my_ml[8 * n + 2 * t + 1] = make_float2(m[n][1], l[n][1]);
+      }
+    }
+  }
+  __syncthreads();
+  decode_join_held<DV, NW, P::WARP_BYTES, ROWS, PITCH>(p, ranges[warp], smem, held, held_end, write_row);
+}
+
+template <int DQ, int DV, int NT>
+cudaError_t launch_decode4_nt(Decode4Params& p, int ctas, cudaStream_t stream) {
+  using P = Decode4Plan<DQ, DV, NT>;
+  static bool attr_done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_done[dev]) {
+    e = cudaFuncSetAttribute(attn_paged_decode4_kernel<DQ, DV, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
+    // (as in launch_decode_nt)
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(attn_decode_join<DV, false>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(attn_decode_join<DV, true>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  p.d.cta_warps = P::NW;
+  plan_join(p.d, ctas);
+  e = decode_launch_one(attn_paged_decode4_kernel<DQ, DV, NT>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
+  if (e != cudaSuccess || !p.d.split) return e;
+  return p.f16 ? launch_join<DV, true>(p.d, ctas, stream) : launch_join<DV, false>(p.d, ctas, stream);
+}
+
+template <int DQ, int DV>
+cudaError_t launch_decode4(Decode4Params& p, int nt, int ctas, cudaStream_t stream) {
+  constexpr int MOST = decode4_rows(DV) / 8;
+  if (nt == 1) return launch_decode4_nt<DQ, DV, 1>(p, ctas, stream);
+  if (nt == 2) return launch_decode4_nt<DQ, DV, 2>(p, ctas, stream);
+  if constexpr (MOST >= 3)
+    if (nt == 3) return launch_decode4_nt<DQ, DV, 3>(p, ctas, stream);
+  if constexpr (MOST >= 4)
+    if (nt == 4) return launch_decode4_nt<DQ, DV, 4>(p, ctas, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace attn

@@ -1,0 +1,85 @@
+// What the host sides of the rotation and the paged caches (attn_paged.cu,
+// attn_paged_cache.cu) share: argument checks, the device's words.
+#pragma once
+#include <cmath>
+
+#include "attn_paged.h"
+#include "attn_paged_kernels.h"
+
+namespace attn {
+
+struct Device {
+  int* err = nullptr;  // the words of page_error_words
+  int sms = 0;
+};
+// The current device's error word and SM count, looked up once
+attn_status device(Device* out);
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// The strides of an array; that of a dimension of one element, which is
+// never stepped, counts as 0.  Returns whether all are multiples of 8
+// elements (16 bytes).
+inline bool take_strides(const int64_t* s, const int64_t* sizes, int n, long long* out) {
+  bool mult8 = true;
+  for (int i = 0; i < n; ++i) {
+    out[i] = sizes[i] > 1 ? s[i] : 0;
+    mult8 = mult8 && out[i] % 8 == 0;
+  }
+  return mult8;
+}
+// Whether an array that is written has a stride of 0, elements that share
+// their place (strides as take_strides left them)
+inline bool shares_places(const int64_t* sizes, int n, const long long* s) {
+  bool any = false;
+  for (int i = 0; i < n; ++i) any = any || (sizes[i] > 1 && s[i] == 0);
+  return any;
+}
+
+inline attn_status spec_of(const attn_rope_spec* r, int D, bool inverse, RopeSpec* out) {
+  if (r->rot_dim <= 0 || r->rot_dim > D || r->rot_dim % 2 != 0 || !std::isfinite(r->out_scale) || r->steps == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(r->steps, 8)) return ATTN_ERR_MISALIGNED;
+  out->steps = reinterpret_cast<const unsigned long long*>(r->steps);
+  out->rot = r->rot_dim;
+  out->interleaved = r->interleaved ? 1 : 0;
+  out->scale = r->out_scale;
+  out->inverse = inverse ? 1 : 0;
+  return ATTN_OK;
+}
+
+// Into how many blockIdx.y the heads are split: four rounds of threads over
+// the card while there are heads to give them, so that the last round is a
+// small share (one round: 48 us where four take 45; eight: the angles, taken
+// once for a thread's heads, tell); whole batches of heads for each.
+inline int head_splits(long long row_threads, int heads, int sms, int* per_split) {
+  const long long want = static_cast<long long>(sms) * 4096;
+  long long splits = (want + row_threads - 1) / row_threads;
+  if (splits > heads) splits = heads;
+  if (splits > 65535) splits = 65535;  // blockIdx.y
+  int per = static_cast<int>((heads + splits - 1) / splits);
+  if (per > 1) per = (per + kRopeUnroll - 1) / kRopeUnroll * kRopeUnroll;
+  *per_split = per;
+  return (heads + per - 1) / per;
+}
+
+inline bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128 || d == 256; }
+
+// The checks that all calls on a 16-bit cache share; the pools' strides
+inline attn_status check_cache(const attn_paged_cache* c, long long (&kp)[3], long long (&vp)[3]) {
+  if (c == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (c->B < 0 || c->max_pages < 0 || c->n_pages < 0 || c->page_size < 1 || c->Hkv < 1) return ATTN_ERR_INVALID_ARG;
+  if (!dim_ok(c->Dqk) || !dim_ok(c->Dv)) return ATTN_ERR_UNSUPPORTED;
+  if (c->B == 0) return ATTN_OK;
+  if (c->seq_lens == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (c->max_pages > 0 && c->page_table == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (c->n_pages > 0 && (c->k == nullptr || c->v == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(c->seq_lens, 4) || !aligned(c->page_table, 4)) return ATTN_ERR_MISALIGNED;
+  const int64_t sizes[3] = {c->n_pages, c->Hkv, c->page_size};
+  const bool k8 = take_strides(c->k_stride, sizes, 3, kp), v8 = take_strides(c->v_stride, sizes, 3, vp);
+  if (!aligned16(c->k) || !aligned16(c->v) || !k8 || !v8) return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+}  // namespace attn

@@ -1,0 +1,282 @@
+// The cache in 4 bits in registers: how tiles of it lie in shared memory and
+// become operands of mma.sync (attn_paged_decode4_kernel.cuh,
+// attn_paged_weights.cu).
+//
+// A whole number n of 0 .. 15 in the low bits of a half is the fp16 subnormal
+// n 2^-24, which a product of fp16 operands takes exactly: one AND makes two
+// operands of a word, with no conversion.  x & 0x000f000f is the pair (element
+// 0, element 4) of its eight; x & 0x00f000f0 the pair (1, 5), 16 times as
+// large, which the other operand's 1/16 (exact) or a final factor undoes; the
+// same of x >> 8 gives (2, 6) and (3, 7).  Two and a half instructions for
+// four elements.
+#pragma once
+#include "attn_decode_kernel.cuh"
+#include "attn_paged_cache_kernels.h"
+
+namespace attn {
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+// the words of a row's steps and least values (2 G halves)
+template <int G>
+__device__ __forceinline__ void lds_row(uint32_t a, uint32_t (&w)[G]) {
+  if constexpr (G == 1) {
+    w[0] = lds32(a);
+  } else if constexpr (G == 2) {
+    const uint2 v = lds64(a);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(a)
+                 : "memory");
+  }
+}
+// N bytes (4, 8 or 16), or zeros
+template <int N>
+__device__ __forceinline__ void cp_async_n(uint32_t dst, const void* src, bool live) {
+  const int n = live ? N : 0;
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half(w & 0xffffu)); }
+__device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ushort_as_half(w >> 16)); }
+// half i (a constant) of a row's words
+template <int G>
+__device__ __forceinline__ float half_at(const uint32_t (&w)[G], int i) {
+  return i & 1 ? half_hi(w[i >> 1]) : half_lo(w[i >> 1]);
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// the four operands of a word of eight elements, as above
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&r)[4]) {
+  r[0] = w & 0x000f000fu;
+  r[1] = w & 0x00f000f0u;
+  w >>= 8;
+  r[2] = w & 0x000f000fu;
+  r[3] = w & 0x00f000f0u;
+}
+
+// Where the 32-byte slots (64 elements) of a tile's rows lie, so that neither
+// the copies nor the reads meet twice in a bank.  Keys: eight lanes of a read
+// take 64 bits each of eight neighbouring rows' slots.
+template <int D>
+__device__ __forceinline__ uint32_t key_slot(int key, int slot) {
+  return D == 256 ? slot ^ (key & 3) : (D == 128 ? slot ^ (key >> 1 & 1) : slot);
+}
+// Values: a read takes whole slots of every other row of eight.
+template <int D>
+__device__ __forceinline__ uint32_t value_row(int key) {
+  return D == 64 ? (key & ~7) | (key & 7) >> 1 | (key & 1) << 2
+                 : (D == 128 ? (key & ~3) | (key & 1) << 1 | (key >> 1 & 1) : key);
+}
+template <int D>
+__device__ __forceinline__ uint32_t value_slot(int key, int slot) {
+  return D == 256 ? slot ^ (key >> 1 & 3) : (D == 128 ? slot ^ (key >> 2 & 1) : slot);
+}
+
+// 32 neighbouring tokens of a sequence: lane r has the page and slot of token
+// r, and whether it is live (within the length, its page within the pool).
+struct Place4 {
+  int page, slot, h;
+  bool live;
+};
+__device__ __forceinline__ Place4 lookup4(const DecodeParams& p, const int* pages, int first, int len, int h) {
+  Place4 x;
+  const int key = first + (threadIdx.x & 31);
+  x.page = x.slot = 0;
+  x.h = h;
+  x.live = key < len;
+  if (x.live) {
+    const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+    x.slot = key - e * p.page_size;
+    x.page = pages[e];
+  }
+  return x;
+}
+// Tells of a page out of range, whose rows become zeros (apart from the
+// look-up, whose load is on its way)
+__device__ __forceinline__ void report4(const DecodeParams& p, Place4& x) {
+  if (static_cast<unsigned>(x.page) >= static_cast<unsigned>(p.n_pages)) {
+    if (x.live) *p.err = 1;
+    x.live = false;
+  }
+}
+
+// Their rows of D elements (d of them real) into a tile by a warp, and their
+// steps and least values behind one another.  KEYS: laid out as keys.
+template <int D, bool KEYS>
+__device__ __forceinline__ void copy_rows4(const Pool4& pool, const Place4& x, int d, uint32_t to, uint32_t scales) {
+  constexpr int L = D / 32, R = 32 / L;  // 16-byte lanes of a row, rows of an instruction
+  const int lane = threadIdx.x & 31, lr = lane / L, c = lane % L;
+  const long long at = x.live ? x.page * pool.st[0] + x.h * pool.st[1] + x.slot * pool.st[2] : -1;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const long long row = __shfl_sync(0xffffffffu, at, i * R + lr);
+    const int key = i * R + lr;
+    const bool live = row >= 0 && 32 * c < d;
+    const uint32_t place = KEYS ? key * (D / 2) + key_slot<D>(key, c >> 1) * 32
+                                : value_row<D>(key) * (D / 2) + value_slot<D>(key, c >> 1) * 32;
+    cp_async_n<16>(to + place + (c & 1) * 16, live ? pool.codes + row + 16 * c : pool.codes, live);
+  }
+  constexpr int N = 4 * groups4(D);
+  cp_async_n<N>(scales + lane * N,
+                x.live ? pool.scales + x.page * pool.ss[0] + x.h * pool.ss[1] + x.slot * pool.ss[2] : pool.scales,
+                x.live);
+}
+
+// Q^T of up to NT groups of 8 heads as the products' second operand, to go
+// with K's rows: each head times a power of two that brings its largest
+// element to [2^8, 2^9), so that fp16 holds the elements, a sixteenth of them,
+// and the sums of 64.
+template <int DQ, int NT>
+struct Query4 {
+  static constexpr int GQ = groups4(DQ);
+  uint32_t q[GQ][4][NT][2];  // of products j: elements 16 t + (0, 4), (1, 5), ... of a group
+  uint32_t sum[NT][2];       // the groups' sums in two parts, for the least values
+  float scale[NT][2];        // of the scores of heads 2 t, 2 t + 1 of each group of heads
+
+  // rows n_rows .. are zero; base: the first head's row, d: real elements
+  template <bool F16>
+  __device__ __forceinline__ void load(const uint16_t* base, long long stride, int n_rows, int d, float scale_log2) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const bool in = 8 * n + g < n_rows;
+      const uint16_t* row = base + (in ? 8 * n + g : 0) * stride;
+      float most = 0.f;
+      uint4 w[GQ][2];
+#pragma unroll
+      for (int b = 0; b < GQ; ++b) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int at = 64 * b + 16 * t + 8 * e;
+          w[b][e] = in && at < d ? *reinterpret_cast<const uint4*>(row + at) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t u[4] = {w[b][e].x, w[b][e].y, w[b][e].z, w[b][e].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = widen2<F16>(u[i]);
+            most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+      }
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      const int ex = __float_as_int(most) >> 23;
+      const int f = ex == 0 ? 127 : min(262 - ex, 252);
+      const float up = __int_as_float(f << 23), down = __int_as_float((254 - f) << 23);
+      float sums[GQ];
+#pragma unroll
+      for (int b = 0; b < GQ; ++b) {
+        sums[b] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t u[4] = {w[b][e].x, w[b][e].y, w[b][e].z, w[b][e].w};
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 y = widen2<F16>(u[i]);
+            x[2 * i] = y.x * up;
+            x[2 * i + 1] = y.y * up;
+          }
+          q[b][2 * e][n][0] = pack2<true>(x[0], x[4]);
+          q[b][2 * e][n][1] = pack2<true>(x[1] * 0.0625f, x[5] * 0.0625f);
+          q[b][2 * e + 1][n][0] = pack2<true>(x[2], x[6]);
+          q[b][2 * e + 1][n][1] = pack2<true>(x[3] * 0.0625f, x[7] * 0.0625f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sums[b] += x[i];
+        }
+        sums[b] += __shfl_xor_sync(0xffffffffu, sums[b], 1);
+        sums[b] += __shfl_xor_sync(0xffffffffu, sums[b], 2);
+      }
+      // rows 2 t, 2 t + 1 of the operand are groups 2 t, 2 t + 1; 8 further on their second parts
+      const float s0 = t == 0 ? sums[0] : (GQ > 2 && t == 1 ? sums[GQ > 2 ? 2 : 0] : 0.f);
+      const float s1 = GQ > 1 && t == 0 ? sums[GQ > 1 ? 1 : 0] : (GQ > 2 && t == 1 ? sums[GQ > 2 ? 3 : 0] : 0.f);
+      split2<true>(s0, s1, sum[n][0], sum[n][1]);
+      const float back = down * scale_log2;
+      scale[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      scale[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    }
+  }
+  template <bool F16>
+  static __device__ __forceinline__ float2 widen2(uint32_t w) {
+    if constexpr (F16) return make_float2(half_lo(w), half_hi(w));
+    else return make_float2(bf16_lo(w), bf16_hi(w));
+  }
+};
+
+// S^T (16 keys x 8 heads, NT groups) of keys key0 .. key0 + 15 of a tile, in
+// units of Query4's scale: sum over the groups of s (n q) + m sum(q), with n q
+// by products of n 2^-24 and the sums of a row's least values by one more.
+template <int DQ, int NT>
+__device__ __forceinline__ void scores4(const Query4<DQ, NT>& q, uint32_t tile, uint32_t scales, int key0,
+                                        float (&s)[NT][4]) {
+  constexpr int GQ = groups4(DQ);
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint32_t row[2][GQ];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) lds_row<GQ>(scales + (key0 + 8 * i + g) * (4 * GQ), row[i]);
+  {
+    uint32_t a[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t least;
+      if constexpr (GQ == 1) least = t == 0 ? row[i][0] >> 16 : 0u;
+      else if constexpr (GQ == 2) least = t == 0 ? row[i][1] : 0u;
+      else least = t == 0 ? row[i][2] : (t == 1 ? row[i][3] : 0u);
+      a[i] = a[2 + i] = least;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      mma16816<true>(s[n], a, q.sum[n][0], q.sum[n][1]);
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < GQ; ++b) {
+    uint32_t r[2][2][4];  // row g or g + 8, word
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int key = 8 * i + g;
+      const uint2 w = lds64(tile + (key0 + key) * (DQ / 2) + key_slot<DQ>(key, b) * 32 + 8 * t);
+      nibbles(w.x, r[i][0]);
+      nibbles(w.y, r[i][1]);
+    }
+    float x[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a[4] = {r[0][j >> 1][2 * (j & 1)], r[1][j >> 1][2 * (j & 1)], r[0][j >> 1][2 * (j & 1) + 1],
+                             r[1][j >> 1][2 * (j & 1) + 1]};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma16816<true>(x[n], a, q.q[b][j][n][0], q.q[b][j][n][1]);
+    }
+    const float s0 = half_at<GQ>(row[0], b) * 16777216.f, s1 = half_at<GQ>(row[1], b) * 16777216.f;  // 2^24
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      s[n][0] = fmaf(x[n][0], s0, s[n][0]);
+      s[n][1] = fmaf(x[n][1], s0, s[n][1]);
+      s[n][2] = fmaf(x[n][2], s1, s[n][2]);
+      s[n][3] = fmaf(x[n][3], s1, s[n][3]);
+    }
+  }
+}
+
+}  // namespace attn

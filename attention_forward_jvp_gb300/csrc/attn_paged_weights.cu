@@ -1,0 +1,278 @@
+// The attention weight of each key (attn_paged_weights, attn_paged_weights4):
+//
+//   out_j = decay w_j + sum over the query heads of exp(s q k_j - lse)
+//
+// One pass over the keys: the scores by mma.sync with 16 keys as the rows and
+// 8 heads as the columns, as in the decode kernels, then exp2 of their distance
+// to the LSE and a sum over the columns.  No maximum and nothing to join: the
+// LSE is given, and a key's sum is one warp's, in one order.
+//
+// What bounds it: memory, the keys once.  The list of steps, its cut into
+// ranges and the rings are those of the decode (attn_decode_kernel.cuh): 16
+// keys to a step in 16 bits, 32 in 4 bits.  The heads of a key head that are
+// more than registers hold go over the same step in turn, their queries read
+// again from L1.
+#include "attn_paged_values4.cuh"
+
+namespace attn {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kWarps = 16;
+
+template <int DQ, int BITS, int NT>
+struct WeightPlan {
+  static constexpr int BN = BITS == 4 ? kDecode4BN : kDecodeBN;
+  static constexpr int K_BYTES = BN * DQ * BITS / 8;
+  static constexpr int STAGE = K_BYTES + (BITS == 4 ? BN * 4 * groups4(DQ) : 0);
+  static constexpr int MISC_BYTES = (8 * 32 + 16) * kDecodeMaxWarps;
+  static constexpr int FIT = 226 * 1024 - MISC_BYTES;
+  static constexpr int REGS = (DQ / 8 + 8) * NT + 72;
+  static constexpr int NW_REGS = REGS <= 128 ? 16 : (REGS <= 160 ? 12 : 8);
+  static constexpr int NW = FIT / NW_REGS / STAGE >= 3 ? NW_REGS : 8;
+  static constexpr int S = FIT / NW / STAGE >= 6 ? 6 : FIT / NW / STAGE;
+  static constexpr int SMEM = NW * S * STAGE + MISC_BYTES;
+  static_assert(S >= 2 && NW <= kWarps, "weight plan");
+};
+
+template <int DQ, int BITS, bool F16, int NT>
+__global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
+    weights_kernel(const __grid_constant__ WeightParams pw) {
+  using P = WeightPlan<DQ, BITS, NT>;
+  constexpr int BN = P::BN, S = P::S, NW = P::NW, THREADS = NW * 32, TILES = BN / 16;
+  const DecodeParams& p = pw.d;
+  extern __shared__ __align__(128) char weight_smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_u32(weight_smem + warp * S * P::STAGE);
+  char* misc = weight_smem + NW * S * P::STAGE;
+  const DecodeWords words{reinterpret_cast<int*>(misc), reinterpret_cast<uint32_t*>(misc) + THREADS,
+                          reinterpret_cast<long long*>(misc + 8 * THREADS)};
+  griddep_wait();
+  griddep_launch_dependents();
+
+  auto length = [&](int b) {
+    const int n = p.seq_lens[b];
+    return n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
+  };
+  // behind the lengths
+  if (pw.out != pw.w) {
+    constexpr long long PIECE = 4096;
+    const long long pieces = (pw.places + PIECE - 1) / PIECE, all = pieces * p.B * p.Hkv;
+    for (long long x = blockIdx.x; x < all; x += gridDim.x) {
+      const long long row = x / pieces, at = (x - row * pieces) * PIECE;
+      const int b = static_cast<int>(row / p.Hkv), h = static_cast<int>(row - static_cast<long long>(b) * p.Hkv);
+      const long long end = min(at + PIECE, pw.places);
+      float* to = pw.out + b * pw.os[0] + h * pw.os[1];
+      const float* from = pw.w == nullptr ? nullptr : pw.w + b * pw.ws[0] + h * pw.ws[1];
+      for (long long j = max(at, static_cast<long long>(length(b))) + tid; j < end; j += THREADS)
+        to[j] = from == nullptr ? 0.f : from[j];
+    }
+  }
+
+  struct Cursor {
+    int b, h, t, nt, len;
+  };
+  auto steps_of = [](int len) { return (len + BN - 1) / BN; };
+  auto advance = [&](Cursor& a) {
+    if (++a.t < a.nt) return;
+    a.t = 0;
+    if (++a.h < p.Hkv) return;
+    a.h = 0;
+    while (a.b + 1 < p.B) {
+      ++a.b;
+      a.len = length(a.b);
+      a.nt = steps_of(a.len);
+      if (a.nt > 0) break;
+    }
+  };
+  struct Place16 : DecodePlace {
+    int h;
+  };
+  using Place = typename std::conditional<BITS == 4, Place4, Place16>::type;
+  auto lookup = [&](const Cursor& a) -> Place {
+    const int* pages = p.page_table + a.b * p.table_stride;
+    if constexpr (BITS == 4) return lookup4(p, pages, a.t * BN, a.len, a.h);
+    else return {decode_lookup(p, p.whole, pages, a.t * BN, a.len), a.h};
+  };
+  auto issue = [&](Place& x, int stage) {
+    const uint32_t to = ring + stage * P::STAGE;
+    if constexpr (BITS == 4) {
+      report4(p, x);
+      copy_rows4<DQ, true>(pw.k, x, p.dqk, to, to + P::K_BYTES);
+    } else {
+      decode_report(p, p.whole, x);
+      copy_rows<DQ, DQ * 2, 128>(p, p.whole, x, p.k + x.h * p.kp[1], p.kp, p.dqk, to);
+    }
+  };
+
+  const DecodeRange w = p.wide ? decode_plan<long long, BN, NW, true>(p, words) : decode_plan<int, BN, NW, true>(p, words);
+  const int count = w.count;
+  if (count == 0) return;
+  Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len}, ahead = cur;
+#pragma unroll 1
+  for (int j = 0; j < S - 1; ++j) {
+    if (j < count) {
+      Place x = lookup(ahead);
+      issue(x, j);
+      if (j + 1 < count) advance(ahead);
+    }
+    cp_async_commit();
+  }
+  Place next = lookup(ahead);
+
+  // queries and LSEs of 8 NT heads
+  constexpr float kLog2e = 1.4426950408889634f;
+  Query4<DQ, BITS == 4 ? NT : 1> q4;
+  uint32_t q16[BITS == 16 ? DQ / 16 : 1][NT][2];
+  float lse[NT][2];  // of heads 2 t, 2 t + 1, times log2(e)
+  auto load_heads = [&](const Cursor& a, int g0) {
+    const long long head = static_cast<long long>(a.h) * p.G + g0;
+    const uint16_t* base = p.q + a.b * p.qs[0] + head * p.qs[1];
+    const int n_rows = p.G - g0;
+    if constexpr (BITS == 4) {
+      if (pw.f16) q4.template load<true>(base, p.qs[1], n_rows, p.dqk, p.scale_log2);
+      else q4.template load<false>(base, p.qs[1], n_rows, p.dqk, p.scale_log2);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const bool in = 8 * n + g < n_rows;
+        const uint16_t* row = base + (in ? 8 * n + g : 0) * p.qs[1];
+#pragma unroll
+        for (int ks = 0; ks < DQ / 16; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int d = 16 * ks + 8 * e + 2 * t;
+            q16[ks][n][e] = in && d < p.dqk ? *reinterpret_cast<const uint32_t*>(row + d) : 0u;
+          }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e;
+        float x = INFINITY;  // (a head that is none, or without keys: no weight)
+        if (r < n_rows) {
+          x = pw.lse[static_cast<long long>(a.b) * p.Hkv * p.G + head + r] * kLog2e;
+          if (x == -INFINITY) x = INFINITY;
+        }
+        lse[n][e] = x;
+      }
+  };
+  const bool once = p.G <= 8 * NT;  // the heads stay for a whole unit
+  if (once) load_heads(cur, 0);
+
+  int stage = 0;
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    __syncwarp();
+    if (i + S - 1 < count) {
+      issue(next, stage == 0 ? S - 1 : stage - 1);
+      if (i + S < count) {
+        advance(ahead);
+        next = lookup(ahead);
+      }
+    }
+    cp_async_commit();
+    // lane (g, t) has key 8 t + g of the step
+    const long long key = static_cast<long long>(cur.t) * BN + 8 * t + g;
+    const bool mine = 8 * t < BN && key < cur.len;
+    float old = 0.f;
+    if (mine && pw.w != nullptr && pw.decay != 0.f) old = pw.w[cur.b * pw.ws[0] + cur.h * pw.ws[1] + key];
+    cp_async_wait<S - 1>();
+    __syncwarp();
+
+    const uint32_t sk = ring + stage * P::STAGE;
+    float sum[TILES][2];
+#pragma unroll
+    for (int kt = 0; kt < TILES; ++kt) sum[kt][0] = sum[kt][1] = 0.f;
+#pragma unroll 1
+    for (int g0 = 0; g0 < p.G; g0 += 8 * NT) {
+      if (!once) load_heads(cur, g0);
+#pragma unroll
+      for (int kt = 0; kt < TILES; ++kt) {
+        float s[NT][4];
+        if constexpr (BITS == 4) {
+          scores4<DQ, NT>(q4, sk, sk + P::K_BYTES, 16 * kt, s);
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+          const int mi = lane >> 3, l8 = lane & 7;
+          const uint32_t k_row = sk + ((mi & 1) * 8 + l8) * (DQ * 2);
+#pragma unroll
+          for (int ks = 0; ks < DQ / 16; ++ks) {
+            uint32_t ka[4];
+            ldsm4(ka, k_row + (((2 * ks + (mi >> 1)) ^ l8) << 4));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<F16>(s[n], ka, q16[ks][n][0], q16[ks][n][1]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float scale = BITS == 4 ? q4.scale[BITS == 4 ? n : 0][e & 1] : p.scale_log2;
+            sum[kt][e >> 1] += exp2_fast(fmaf(s[n][e], scale, -lse[n][e & 1]));
+          }
+      }
+    }
+    float mineOf = 0.f;
+#pragma unroll
+    for (int kt = 0; kt < TILES; ++kt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float x = sum[kt][r];
+        x += __shfl_xor_sync(kAll, x, 1);
+        x += __shfl_xor_sync(kAll, x, 2);
+        if (t == 2 * kt + r) mineOf = x;
+      }
+    if (mine) pw.out[cur.b * pw.os[0] + cur.h * pw.os[1] + key] = fmaf(pw.decay, old, mineOf);
+
+    if (i + 1 < count) {
+      const bool ends = cur.t + 1 == cur.nt;
+      advance(cur);
+      if (ends && once) load_heads(cur, 0);
+    }
+    stage = stage + 1 == S ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
+}
+
+template <int DQ, int BITS, bool F16, int NT>
+cudaError_t launch_nt(const WeightParams& p, int ctas, cudaStream_t stream) {
+  using P = WeightPlan<DQ, BITS, NT>;
+  static bool attr_done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_done[dev]) {
+    e = cudaFuncSetAttribute(weights_kernel<DQ, BITS, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  return decode_launch_one(weights_kernel<DQ, BITS, F16, NT>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
+}
+
+// groups of 8 heads in registers: one, two or four (two at head dim 256)
+template <int DQ, int BITS, bool F16>
+cudaError_t launch_dq(const WeightParams& p, int ctas, cudaStream_t stream) {
+  if (p.d.G <= 8) return launch_nt<DQ, BITS, F16, 1>(p, ctas, stream);
+  if (p.d.G <= 16 || DQ == 256) return launch_nt<DQ, BITS, F16, 2>(p, ctas, stream);
+  return launch_nt<DQ, BITS, F16, DQ == 256 ? 2 : 4>(p, ctas, stream);
+}
+template <int BITS, bool F16>
+cudaError_t launch_bits(const WeightParams& p, int dq, int ctas, cudaStream_t stream) {
+  if (dq == 64) return launch_dq<64, BITS, F16>(p, ctas, stream);
+  return dq == 128 ? launch_dq<128, BITS, F16>(p, ctas, stream) : launch_dq<256, BITS, F16>(p, ctas, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_weights(const WeightParams& p, int dq, int bits, int ctas, cudaStream_t stream) {
+  if (bits == 4) return launch_bits<4, true>(p, dq, ctas, stream);
+  return p.f16 ? launch_bits<16, true>(p, dq, ctas, stream) : launch_bits<16, false>(p, dq, ctas, stream);
+}
+
+}  // namespace attn

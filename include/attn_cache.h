@@ -1,0 +1,206 @@
+/*
+ * attn_cache.h -- a paged key-value cache made smaller, and read back.  Part
+ * of the library of attn_jvp.h; the cache of 16-bit values, its conventions,
+ * positions and new tokens are those of attn_paged.h.
+ *
+ *   attn_paged_append4  appends new tokens to a cache that holds 4 bits an
+ *                       element, rotating keys and queries on the way
+ *   attn_paged_decode4  attention of one query token per sequence over it
+ *   attn_paged_gather   the last tokens of each sequence as the dense jagged
+ *   attn_paged_gather4  tensors that attn_fwd takes, of either cache
+ *   attn_paged_weights  the attention weight that the step's query heads gave
+ *   attn_paged_weights4 each key, added up beside the cache
+ *   attn_paged_evict    keeps the keys with the largest such weights, the
+ *   attn_paged_evict4   first and the last, copied into fewer pages
+ *
+ * Types: queries, new tokens and outputs are bf16; the *_f16 entry points
+ * take fp16.  Every product, sum, angle and softmax statistic is fp32 or
+ * wider; the weights are fp32.
+ *
+ * Calls are asynchronous on `stream`, allocate no device memory and may be
+ * captured, like those of attn_paged.h; argument errors are returned
+ * synchronously and launch nothing, and a page number or a length out of
+ * range is refused on the device: nothing outside the pools is touched, and
+ * the next attn_sync_check on the device returns ATTN_ERR_PAGE.
+ */
+#ifndef ATTN_CACHE_H
+#define ATTN_CACHE_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "attn_jvp.h"
+#include "attn_paged.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ------------------------------------------------------- cache in 4 bits
+ *
+ * A row of D elements is cut into D / 64 groups of 64 (one of 32 where
+ * D = 32).  Of a group the cache holds a least value m and a step s, fp16,
+ * and for each element a whole number n of 0 .. 15: the element is m + n s.
+ *
+ *   m = fp16(min x)    s = fp16((max x - m) / 15)    n = round((x - m) / s)
+ *
+ * all to nearest even, the differences and quotients in fp32, n limited to
+ * 0 .. 15 and 0 where s is not above 0; x beyond +-65504 counts as that, and a group
+ * with an infinite or NaN element is NaN as a whole (m = s = NaN, n = 0).
+ *
+ * k, v: pools of bytes [page, head, token in page, D / 2], element 2i in the
+ * low half of byte i and 2i + 1 in the high half; strides (page, head, token)
+ * in bytes.  k_scale, v_scale: fp16 [page, head, token in page, 2, groups],
+ * the steps of a row, then its least values; strides in elements.  Rows are
+ * contiguous.  Byte pools: 16-byte aligned, strides multiples of 16.  Scales:
+ * a row (4 groups bytes) is aligned to its size, strides multiples of
+ * 2 groups.  Dqk, Dv each in {32, 64, 128, 256}.  The rest as in
+ * attn_paged_cache. */
+typedef struct {
+  int32_t B, max_pages, n_pages, page_size;
+  int32_t Hkv, Dqk, Dv;
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t k_scale_stride[3];
+  int64_t v_scale_stride[3];
+  const int32_t* page_table;  /* device [B, max_pages] */
+  int64_t table_stride;
+  const int32_t* seq_lens;    /* device [B] */
+} attn_paged_cache4;
+
+/* attn_paged_append, rounding keys (after their rotation) and values as
+ * above.  The same tokens are refused or left out.  A pool that is another
+ * pool too, or shares places within itself, is refused. */
+attn_status attn_paged_append4(const attn_paged_cache4* cache, const attn_paged_new* tokens,
+                               const attn_rope_spec* rope, void* stream);
+attn_status attn_paged_append4_f16(const attn_paged_cache4* cache, const attn_paged_new* tokens,
+                                   const attn_rope_spec* rope, void* stream);
+
+/* attn_paged_decode over the values m + n s.  q is multiplied as fp16 after
+ * a power of two of its row (2^-29 of the row's largest element and less is
+ * lost); a q with an infinite element gives NaN. */
+size_t attn_paged_decode4_workspace(const attn_paged_cache4* cache, int32_t Hq);
+attn_status attn_paged_decode4(const attn_paged_cache4* cache, int32_t Hq, const void* q, const int64_t q_stride[2],
+                               float sm_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream);
+attn_status attn_paged_decode4_f16(const attn_paged_cache4* cache, int32_t Hq, const void* q,
+                                   const int64_t q_stride[2], float sm_scale, void* o, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- gather
+ *
+ * Of each sequence b its last offsets[b + 1] - offsets[b] tokens: keys to k
+ * [Hkv, T, Dqk] and values to v [Hkv, T, Dv] by strides (head, token), rows
+ * contiguous and 16-byte aligned; offsets: device int32 [B + 1] as in
+ * attn_paged_new; rows >= offsets[B] are left as they were.  A token without
+ * a position (more of them than seq_lens[b]) or with a page out of range
+ * gives zeros and ATTN_ERR_PAGE.  attn_paged_gather copies bf16 or fp16;
+ * attn_paged_gather4 writes m + n s rounded to bf16, its twin to fp16.
+ * Pools are read, never written: k and v must be apart from them and from
+ * each other. */
+attn_status attn_paged_gather(const attn_paged_cache* cache, int64_t T, const int32_t* offsets, void* k,
+                              const int64_t k_stride[2], void* v, const int64_t v_stride[2], void* stream);
+attn_status attn_paged_gather4(const attn_paged_cache4* cache, int64_t T, const int32_t* offsets, void* k,
+                               const int64_t k_stride[2], void* v, const int64_t v_stride[2], void* stream);
+attn_status attn_paged_gather4_f16(const attn_paged_cache4* cache, int64_t T, const int32_t* offsets, void* k,
+                                   const int64_t k_stride[2], void* v, const int64_t v_stride[2], void* stream);
+
+/* --------------------------------------------------------------- weights
+ *
+ * For every sequence b, key head h and key j < seq_lens[b], over the query
+ * heads of h:
+ *
+ *   out[b, h, j] = decay w[b, h, j] + sum_heads exp(sm_scale q k_j - lse)
+ *
+ *   q, q_stride, sm_scale  as in attn_paged_decode
+ *   lse   [B, Hq] fp32, as attn_paged_decode wrote it (-inf: no weight)
+ *   w     fp32 [B, Hkv, places] by strides (sequence, head), the places of a
+ *         row contiguous, places = max_pages * page_size; NULL: zeros
+ *   out   the same, w itself allowed (with equal strides)
+ *   decay 0 .. 1; at 0 w is not read where j < seq_lens[b]
+ *
+ * Entries at seq_lens[b] and behind are copied (left alone when out is w,
+ * zero without w).  A page out of range counts as keys of zero. */
+typedef struct {
+  const float* lse;
+  const float* w;
+  float* out;
+  int64_t w_stride[2];
+  int64_t out_stride[2];
+  float decay;
+} attn_paged_weight;
+attn_status attn_paged_weights(const attn_paged_cache* cache, int32_t Hq, const void* q, const int64_t q_stride[2],
+                               float sm_scale, const attn_paged_weight* weight, void* stream);
+attn_status attn_paged_weights_f16(const attn_paged_cache* cache, int32_t Hq, const void* q,
+                                   const int64_t q_stride[2], float sm_scale, const attn_paged_weight* weight,
+                                   void* stream);
+attn_status attn_paged_weights4(const attn_paged_cache4* cache, int32_t Hq, const void* q, const int64_t q_stride[2],
+                                float sm_scale, const attn_paged_weight* weight, void* stream);
+attn_status attn_paged_weights4_f16(const attn_paged_cache4* cache, int32_t Hq, const void* q,
+                                    const int64_t q_stride[2], float sm_scale, const attn_paged_weight* weight,
+                                    void* stream);
+
+/* -------------------------------------------------------------- eviction
+ *
+ * A sequence of n = seq_lens[b] > K tokens, K = keep[b], is cut down to K:
+ * its last min(recent, K) tokens, its first min(sinks, K - those), and of
+ * the others, for each key head by itself, those with the largest weights
+ * (of equal ones the earliest; NaN counts as the largest).  The kept tokens
+ * of a head are copied, in their order, to the places 0 .. K - 1 of the pages
+ * `pages[b]`, keys, values and scales bit for bit.  Then
+ *
+ *   lens_out[b]  = K
+ *   table_out[b] = the table's row, its first n_new entries from pages[b]
+ *   w_out[b, h]  = the kept tokens' weights, zeros behind
+ *
+ * A sequence with n <= K stays where it is: its length, row and weights are
+ * copied.  The call changes neither the old table and lengths nor the old
+ * pages: they are the caller's to give back once table_out and lens_out have
+ * taken their place.  Keys keep their rotation; a later token's position is
+ * no longer its place: rotate it with attn_rope's positions and append it
+ * without a rotation.
+ *
+ *   w, w_out     as w in attn_paged_weights; apart from one another
+ *   keep         device int32 [B], or NULL: keep_all for every sequence.
+ *                Below 0 counts as 0; above n_new * page_size as that,
+ *                reported as ATTN_ERR_PAGE where n is larger still
+ *   pages        device int32 [B, n_new], pages_stride elements from row to
+ *                row, n_new <= max_pages: pages that no sequence uses and
+ *                that are given once.  Out of range: what would go there is
+ *                dropped, ATTN_ERR_PAGE.  (A page that is read too, or given
+ *                twice, holds either token.)
+ *   table_out    [B, max_pages], table_out_stride; lens_out [B]; apart from
+ *                the cache's own table and lengths
+ *   workspace    16-byte aligned, attn_paged_evict_workspace() bytes, as for
+ *                attn_paged_decode
+ *
+ * Token places out of range in the old table read as zeros, ATTN_ERR_PAGE. */
+typedef struct {
+  const float* w;
+  float* w_out;
+  int64_t w_stride[2];
+  int64_t w_out_stride[2];
+  const int32_t* keep;
+  int32_t keep_all, sinks, recent;
+  const int32_t* pages;
+  int64_t pages_stride;
+  int32_t n_new;
+  int32_t* table_out;
+  int64_t table_out_stride;
+  int32_t* lens_out;
+} attn_paged_eviction;
+size_t attn_paged_evict_workspace(int32_t B, int32_t Hkv, int32_t page_size, int32_t n_new);
+attn_status attn_paged_evict(const attn_paged_cache* cache, const attn_paged_eviction* evict, void* workspace,
+                             size_t workspace_bytes, void* stream);
+attn_status attn_paged_evict4(const attn_paged_cache4* cache, const attn_paged_eviction* evict, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* ATTN_CACHE_H */

@@ -1,0 +1,970 @@
+"""The smaller paged cache on the GPU (4-bit pages, reading back, attention
+weights, eviction) against the float64 definitions of oracle.cache_ref.
+
+Tolerances, from the arithmetic (u = half a step of the output type,
+torch.finfo(t).eps / 2):
+
+  append4  without a rotation, nothing: n, s and m are functions of the input
+           by IEEE operations.  With one, the key is off by e = 1e-6 (|a| + |b|)
+           before it is rounded (the rotation's bound), so the value held by
+           half a step and e, m and s by another 2^-11 of themselves.
+  gather   nothing in 16 bits; in 4 bits m + n s in fp32 (n s exact), rounded
+           to the type.
+  decode4  scores: d = (Dqk / 8 + 16) 2^-22 s sum |q| (n |s| + |m|) (fp32 sums
+           and a truncation in each product of 16).  O: 2 d and 2^-16 (exp2)
+           of sum w |x|; P rounded to fp16, O divided by the rounded sum: 2^-12
+           (sum w |x| + |O|); P s rounded: 2^-12 sum w |s (n - 8)|, or 2^-25
+           of a P that is 2^11 and more, 8 of it a key; the products' sums
+           (keys / 16 + 8) 2^-22 sum w (|m| + 15 |s|); u |O|.
+           LSE: d + (keys + 8) 2^-24 + 2^-21 |LSE|.
+  weights  sum p (d + 2^-22 |LSE| + 2^-20), d in 16 bits (Dqk + 4) 2^-22 s sum
+           |q| |k|; 2^-23 of the result.
+  evict    nothing: a choice by comparisons, rows bit for bit.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from attention_forward_jvp_gb300 import binding, build
+from oracle import cache_ref, paged_ref
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build.build()
+    binding.lib()
+
+
+@pytest.fixture(autouse=True)
+def _clean(_lib):
+    assert binding.sync_check() == 0
+    yield
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def ints(*x):
+    return torch.tensor(*x, dtype=torch.int32).cuda()
+
+
+def randn(shape, dtype, seed, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std).to(dtype).cuda()
+
+
+def bits(t):
+    """A copy that torch.equal compares bit for bit."""
+    return t.contiguous().clone().view(torch.uint8 if t.dtype == torch.uint8 else torch.int16)
+
+
+class Pool:
+    """Pages in random order: `four` with random numbers, steps and least values,
+    else 16-bit values; NaN behind the sequences and in pages of nobody."""
+
+    def __init__(self, lens, Hkv, Dqk, Dv, page, dt=BF, seed=0, head_major=True, four=True, extra=1, spare=3, std=1.0):
+        r = np.random.RandomState(seed)
+        self.lens, self.page, self.four, self.dt, self.Hkv = lens, page, four, dt, Hkv
+        per = [-(-n // page) for n in lens]
+        count = sum(per) + spare
+        order = r.permutation(count)
+        table = np.zeros((len(lens), max(per + [0]) + extra), dtype=np.int32)
+        at = 0
+        for b, m in enumerate(per):
+            table[b, :m] = order[at:at + m]
+            at += m
+        self.spare = order[at:]
+        lead = (count, Hkv, page) if head_major else (count, page, Hkv)
+        held = np.zeros((count, page), dtype=bool)
+        for b, n in enumerate(lens):
+            for j in range(per[b]):
+                held[table[b, j], : min(page, n - j * page)] = True
+        held = held[:, None] if head_major else held[:, :, None]
+        self.parts = []
+        for d in (Dqk, Dv):
+            if four:
+                groups = max(1, d // 64)
+                codes = r.randint(0, 256, (*lead, d // 2)).astype(np.uint8)
+                s = (r.rand(*lead, 1, groups) * 0.3 + 0.05) * std
+                m = -7.5 * s + r.randn(*lead, 1, groups) * 0.3 * std
+                scale = np.concatenate([s, m], -2).astype(np.float16)
+                scale[~np.broadcast_to(held, lead)] = np.nan
+                parts = [torch.from_numpy(codes), torch.from_numpy(scale)]
+            else:
+                x = (r.randn(*lead, d) * std).astype(np.float32)
+                x[~np.broadcast_to(held, lead)] = np.nan
+                parts = [torch.from_numpy(x).to(dt)]
+            self.parts.append([t.cuda() if head_major else t.cuda().transpose(1, 2) for t in parts])
+        self.table, self.seq_lens = torch.from_numpy(table).cuda(), ints(list(lens))
+        self.cache = self.make(self.table, self.seq_lens)
+
+    def make(self, table, seq_lens):
+        k, v = self.parts
+        if self.four:
+            return binding.PagedCache4(k[0], v[0], k[1], v[1], table, seq_lens, dtype=self.dt)
+        return binding.PagedCache(k[0], v[0], table, seq_lens)
+
+    def values(self, which):
+        """[pages, Hkv, page, D] in float64."""
+        p = self.parts[which]
+        if not self.four:
+            return f64(p[0])
+        s = f64(p[1])
+        return cache_ref.values4(cache_ref.unpack4(p[0].cpu().numpy()), s[..., 0, :], s[..., 1, :])
+
+    def bits(self):
+        return [bits(t) for p in self.parts for t in p]
+
+    def rows(self, which, b, h, n):
+        """n keys or values of a sequence's head, and their sizes n |s|, |m|, s."""
+        t = self.table.cpu().numpy()[b]
+        pages, slots = [int(t[p // self.page]) for p in range(n)], [p % self.page for p in range(n)]
+        p = self.parts[which]
+        x = f64(p[0][pages, h, slots]) if not self.four else None
+        if not self.four:
+            return x, None, None, None
+        num = cache_ref.unpack4(p[0][pages, h, slots].cpu().numpy())
+        sc = f64(p[1][pages, h, slots])
+        size = cache_ref.group_of(num.shape[-1])
+        s, m = np.repeat(sc[:, 0], size, -1), np.repeat(sc[:, 1], size, -1)
+        return m + num * s, num, np.abs(s), np.abs(m)
+
+
+def check_decode4(pool, q, o, lse, sm_scale=None, lens=None):
+    B, Hq, D = q.shape
+    s = D**-0.5 if sm_scale is None else sm_scale
+    Q, O, Lse = f64(q), f64(o), f64(lse)
+    u = torch.finfo(o.dtype).eps / 2
+    for b, n in enumerate(pool.lens if lens is None else lens):
+        if n == 0:
+            assert (O[b] == 0).all() and np.isneginf(Lse[b]).all()
+            continue
+        for h in range(Hq):
+            k, kn, ks, km = pool.rows(0, b, h // (Hq // pool.Hkv), n)
+            v, vn, vs, vm = pool.rows(1, b, h // (Hq // pool.Hkv), n)
+            z = s * (k @ Q[b, h])
+            top = z.max()
+            w = np.exp(z - top)
+            want_lse = top + math.log(w.sum())
+            w /= w.sum()
+            want = w @ v
+            d = (D / 8 + 16) * 2.0**-22 * s * float(((kn * ks + km) @ np.abs(Q[b, h])).max())
+            mean = w @ np.abs(v)
+            step = np.minimum(w[:, None] * vs, 1e30)
+            tol = u * np.abs(want) + (2 * d + 2.0**-16) * mean + 2.0**-12 * (mean + np.abs(want))
+            tol += 2.0**-12 * (step * np.abs(vn - 8)).sum(0) + n * 8 * 2.0**-36
+            tol += (n / 16 + 8) * 2.0**-22 * (w @ (vm + 15 * vs)) + 2.0**-25
+            err = np.abs(O[b, h] - want)
+            assert (err <= tol).all(), f"sequence {b} head {h}: off by {err.max():.3e}, {np.max(err / tol):.2f} of its bound"
+            assert abs(Lse[b, h] - want_lse) <= d + (n + 8) * 2.0**-24 + 2.0**-21 * abs(want_lse), (b, h)
+
+
+def decode4(pool, q, **kw):
+    o, lse = binding.attn_paged_decode(pool.cache, q, **kw)
+    assert binding.sync_check() == 0
+    return o, lse
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("page,head_major", [(1, True), (5, False), (16, True), (64, False)])
+@pytest.mark.parametrize("dims,dt", [((64, 64), BF), ((128, 64), HF), ((32, 128), BF), ((256, 32), BF), ((64, 256), HF)])
+@pytest.mark.parametrize("jagged", [False, True])
+def test_append_rounds_as_defined(page, head_major, dims, dt, jagged):
+    lens = [0, 1, 7, 64, 65, 130, 33]
+    new = [0, 1, 7, 3, 0, 100, 2] if jagged else [1] * len(lens)
+    pool = Pool(lens, 3, *dims, page, dt, seed=page, head_major=head_major)
+    T = sum(new) + (5 if jagged else 0)  # rows behind the last sequence
+    k, v, q = (randn((T, h, d), dt, h + d, 2.0) for h, d in ((3, dims[0]), (3, dims[1]), (6, dims[0])))
+    before = [t.clone() for p in pool.parts for t in p]
+    out = torch.full_like(q, 9.0)
+    off = ints([0] + new).cumsum(0).int() if jagged else None
+    assert binding.attn_paged_append(pool.cache, k, v, q=q, offsets=off, out=out) is out
+    assert binding.sync_check() == 0
+    want = [cache_ref.round4(f64(x)) for x in (k, v)]
+    table, t = pool.table.cpu(), 0
+    for b, m in enumerate(new):
+        for j in range(m):
+            p = lens[b] - m + j
+            if p < 0:
+                assert (out[t] == 0).all()  # idle
+            else:
+                assert torch.equal(out[t], q[t])
+                pg, sl = int(table[b, p // page]), p % page
+                for i, (codes, scale) in enumerate(pool.parts):
+                    n, s, least = (x[t] for x in want[i])
+                    assert (codes[pg, :, sl].cpu().numpy() == cache_ref.pack4(n)).all()
+                    assert (scale[pg, :, sl].cpu().numpy() == np.stack([s, least], 1)).all()
+                    codes[pg, :, sl], scale[pg, :, sl] = before[2 * i][pg, :, sl], before[2 * i + 1][pg, :, sl]
+            t += 1
+    assert all(torch.equal(a, bits(b)) for a, b in zip(pool.bits(), before))  # everything else as it was
+    assert (out[t:] == 9).all()
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_append_rounds_odd_groups(dt):
+    most = float(torch.finfo(dt).max)
+    rows = torch.zeros(12, 1, 128)
+    rows[1] = 0.1
+    rows[2, 0, 5] = math.inf
+    rows[3, 0, 70] = -math.inf
+    rows[4, 0, 64] = math.nan
+    rows[5] = torch.linspace(-most, most, 128)
+    rows[6] = most
+    rows[7] = torch.linspace(-1e-6, 1e-6, 128)
+    rows[8] = torch.linspace(5.0, 5.001, 128)
+    rows[9, 0, ::2] = -0.0
+    rows[10] = torch.linspace(-7.5, 7.5, 64).repeat(2)
+    rows[11] = -65504.0
+    x = rows.to(dt).cuda()
+    pool = Pool([1] * 12, 1, 128, 128, 4, dt)
+    binding.attn_paged_append(pool.cache, x, x)
+    n, s, least = cache_ref.round4(f64(x))
+    for b in range(12):
+        for codes, scale in pool.parts:
+            assert (codes[pool.table[b, 0].item(), 0, 0].cpu().numpy() == cache_ref.pack4(n[b, 0])).all(), b
+            np.testing.assert_array_equal(scale[pool.table[b, 0].item(), 0, 0].cpu().numpy(), np.stack([s[b, 0], least[b, 0]]))
+
+
+@pytest.mark.parametrize("dims,rot,inter,dt", [
+    ((64, 64), 64, False, BF), ((128, 64), 32, True, HF), ((128, 128), 128, False, HF), ((32, 32), 6, True, BF),
+    ((256, 64), 252, False, BF), ((64, 64), 28, False, HF), ((256, 256), 256, True, BF), ((128, 32), 2, False, BF)])
+@pytest.mark.parametrize("place", ["new", "in place", "unaligned"])
+def test_append_rotates(dims, rot, inter, dt, place):
+    lens, Hkv = [70000, 3, 0, 40], 2
+    r = binding.Rope(rot, interleaved=inter, out_scale=1.25)
+    D = dims[0]
+    pool = Pool([3, 3, 0, 40], Hkv, *dims, 8, dt, seed=rot)
+    table = torch.zeros((4, 8800), dtype=torch.int32)
+    table[:, : pool.table.shape[1]] = pool.table.cpu()
+    table[0, 70000 // 8 - 1] = pool.table[0, 0].item()
+    pool.table, pool.seq_lens = table.cuda(), ints(lens)
+    cache = pool.make(pool.table, pool.seq_lens)
+    shift = 3 if place == "unaligned" else 0
+    k, v, q = (torch.empty((4, h, d + 2 * shift), dtype=dt, device="cuda") for h, d in ((Hkv, D), (Hkv, dims[1]), (5, D)))
+    k, v, q = (t[..., shift : t.shape[-1] - shift].copy_(randn((*t.shape[:2], t.shape[2] - 2 * shift), dt, i))
+               for i, t in enumerate((k, v, q)))
+    before = q.clone()
+    got = binding.attn_paged_append(cache, k, v, rope=r, q=q, out=q if place == "in place" else None)
+    assert binding.sync_check() == 0 and (place == "in place" or torch.equal(q, before))
+    half = rot // 2
+    i = np.arange(half)
+    a, b2 = (2 * i, 2 * i + 1) if inter else (i, i + half)
+    K, V = pool.values(0), pool.values(1)
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert (got[b] == 0).all()
+            continue
+        pg, sl = int(table[b, (n - 1) // 8]), (n - 1) % 8
+        for x, y, is_key in ((before[b], f64(got[b]), False), (k[b], K[pg, :, sl], True)):
+            X = f64(x)
+            want = paged_ref.rope(X[:, None], [n - 1], f64(r.inv_freq), inter, 1.25)[:, 0]
+            size = np.zeros_like(X)
+            size[..., a] = size[..., b2] = np.abs(X[..., a]) + np.abs(X[..., b2])
+            e = 1e-6 * 1.25 * size
+            if is_key:
+                _, s, least = cache_ref.round4(want)
+                g = cache_ref.group_of(D)
+                s, least = np.repeat(f64(torch.from_numpy(s)), g, -1), np.repeat(f64(torch.from_numpy(least)), g, -1)
+                tol = e + e.max() + s * (0.5 + 16 * 2.0**-11) + (np.abs(least) + 15 * s) * 2.0**-10 + 2.0**-24
+            else:
+                tol = torch.finfo(dt).eps / 2 * np.abs(want) + e + (2.0**-25 if dt == HF else 2.0**-130)
+            assert (np.abs(y - want) <= tol).all(), (b, is_key)
+        n4, s, least = cache_ref.round4(f64(v[b]))
+        assert np.array_equal(V[pg, :, sl], cache_ref.values4(n4, s, least))
+
+
+@pytest.mark.parametrize("what", ["page", "table", "length"])
+def test_append_bad_places_are_reported_and_left_out(what):
+    k, v, q = randn((2, 1, 64), BF, 1), randn((2, 1, 64), BF, 2), randn((2, 2, 64), BF, 3)
+    pool = Pool([40, 3], 1, 64, 64, 16, seed=2, extra=0)
+    off = None
+    if what == "page":
+        pool.table[0, 2] = pool.parts[0][0].shape[0]
+    elif what == "table":
+        pool.seq_lens[0] = 16 * pool.table.shape[1] + 1
+    else:
+        pool.seq_lens[0] = 1  # two tokens, one place
+        off = ints([0, 2, 2])
+    before = pool.bits()
+    y = binding.attn_paged_append(pool.cache, k, v, q=q, offsets=off)
+    assert binding.sync_check() == 6 and binding.sync_check() == 0
+    p, slot = (int(pool.table[0, 0]), 0) if what == "length" else (int(pool.table[1, 0]), 2)
+    n, s, m = cache_ref.round4(f64(v[1]))
+    assert (pool.parts[1][0][p, :, slot].cpu().numpy() == cache_ref.pack4(n)).all()
+    changed = [(a != b).nonzero() for a, b in zip(before, pool.bits())]
+    assert all((c[:, 0] == p).all() and (c[:, 2] == slot).all() for c in changed)
+    assert (y[0] == 0).all() if what == "length" else torch.equal(y, q)
+
+
+# ------------------------------------------------------------------ gather
+@pytest.mark.parametrize("four,dims,dt", [(True, (64, 64), BF), (True, (128, 32), HF), (True, (32, 256), BF),
+                                          (True, (256, 128), HF), (False, (16, 64), BF), (False, (128, 256), HF)])
+@pytest.mark.parametrize("page,head_major", [(1, True), (7, False), (16, False), (64, True)])
+def test_gather(four, dims, dt, page, head_major):
+    lens = [0, 1, 70, 33, 130, 16, 5]
+    take = [0, 1, 70, 10, 129, 0, 5]
+    pool = Pool(lens, 5, *dims, page, dt, seed=page, head_major=head_major, four=four)
+    off, T = ints([0] + take).cumsum(0).int(), sum(take) + 4
+    k0, v0 = (torch.full((5, T + 1, d + 8), 7.0, dtype=dt, device="cuda") for d in dims)
+    k, v = k0[:, :T, : dims[0]], v0[:, 1:, : dims[1]]
+    got = binding.attn_paged_gather(pool.cache, off, T, out=(k, v))
+    assert got[0] is k and got[1] is v and binding.sync_check() == 0
+    for which, y in ((0, k), (1, v)):
+        t = 0
+        for b, m in enumerate(take):
+            for h in range(5):
+                want = pool.rows(which, b, h, lens[b])[0][lens[b] - m :]
+                assert torch.equal(y[h, t : t + m].cpu(), torch.from_numpy(want).float().to(dt)), (which, b, h)
+            t += m
+        assert (y[:, t:] == 7).all()
+    assert (k0[:, T:] == 7).all() and (k0[..., dims[0]:] == 7).all() and (v0[:, 0] == 7).all() and (v0[..., dims[1]:] == 7).all()
+    k2, v2 = binding.attn_paged_gather(pool.cache, off, sum(take))
+    assert torch.equal(k2, k[:, : sum(take)]) and torch.equal(v2, v[:, : sum(take)])
+
+
+@pytest.mark.parametrize("four", [True, False])
+def test_gather_bad_places_are_zeros_and_reported(four):
+    pool = Pool([40, 3, 20], 2, 64, 64, 16, seed=2, extra=0, four=four)
+    off = ints([0, 40, 43, 63])
+    good = binding.attn_paged_gather(pool.cache, off, 63)
+    for bad in (-1, pool.parts[0][0].shape[0], 2**31 - 1, -2**31):
+        old = pool.table[0, 1].item()
+        pool.table[0, 1] = bad
+        got = binding.attn_paged_gather(pool.cache, off, 63)
+        assert binding.sync_check() == 6 and binding.sync_check() == 0
+        pool.table[0, 1] = old
+        for x, y in zip(good, got):
+            assert (y[:, 16:32] == 0).all()
+            assert torch.equal(x[:, :16], y[:, :16]) and torch.equal(x[:, 32:], y[:, 32:])
+    pool.seq_lens[1] = 1  # three rows, one token
+    got = binding.attn_paged_gather(pool.cache, off, 63)
+    assert binding.sync_check() == 6
+    assert (got[0][:, 40:42] == 0).all() and torch.equal(got[0][:, 42], good[0][:, 40])
+    pool.seq_lens[1] = 1000
+    got = binding.attn_paged_gather(pool.cache, off, 63)
+    assert binding.sync_check() == 6 and (got[1][:, 40:43] == 0).all()
+
+
+# ------------------------------------------------------------------ decode
+@pytest.mark.parametrize("dims", [(32, 32), (64, 64), (128, 128), (256, 256), (128, 64), (64, 128), (256, 64), (32, 256)])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_decode_dims_and_edge_lengths(dims, dt):
+    pool = Pool([0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 200], 2, *dims, 16, dt, seed=dims[0])
+    q = randn((12, 6, dims[0]), dt, 3, 1.5)
+    check_decode4(pool, q, *decode4(pool, q))
+
+
+@pytest.mark.parametrize("group", [1, 2, 7, 8, 9, 16, 17, 24, 25, 32, 33, 50])
+@pytest.mark.parametrize("dims,dt", [((64, 64), BF), ((128, 128), HF), ((256, 256), BF), ((64, 128), HF)])
+def test_decode_head_groups(group, dims, dt):
+    pool = Pool([70, 1, 200], 2, *dims, 32, dt, seed=group, head_major=False)
+    q = randn((3, 2 * group, dims[0]), dt, group)
+    check_decode4(pool, q, *decode4(pool, q))
+
+
+@pytest.mark.parametrize("page", [1, 3, 8, 24, 64, 100, 256])
+@pytest.mark.parametrize("head_major", [True, False])
+def test_decode_pages(page, head_major):
+    pool = Pool([257, 64, 5, 1000], 3, 128, 64, page, BF, seed=page, head_major=head_major)
+    q = randn((4, 3, 128), BF, page)
+    check_decode4(pool, q, *decode4(pool, q))
+
+
+@pytest.mark.parametrize("B,Hkv,group,lens", [(1, 1, 1, "long"), (1, 4, 8, "long"), (3, 2, 3, "mixed"), (200, 1, 2, "short"),
+                                              (150, 8, 1, "one"), (600, 2, 1, "random")])
+def test_decode_splits(B, Hkv, group, lens):
+    # one sequence over all CTAs; many sequences in one CTA; units that end in the middle of a CTA's range
+    r = np.random.RandomState(B)
+    n = {"long": [20011], "mixed": [9000, 1, 700], "short": list(r.randint(1, 65, B)), "one": [1] * B,
+         "random": list(r.randint(0, 200, B))}[lens]
+    pool = Pool([int(x) for x in n], Hkv, 64, 64, 64, BF, seed=B)
+    q = randn((B, group * Hkv, 64), BF, B)
+    o, lse = decode4(pool, q)
+    check_decode4(pool, q, o, lse)
+    o2, lse2 = decode4(pool, q)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_decode_scale_sharp_scores_and_strided_q():
+    pool = Pool([300, 40, 1], 2, 128, 128, 16, BF, seed=3, std=2.0)
+    q = randn((3, 9, 128), BF, 9, 3.0)[:, 1:5]
+    check_decode4(pool, q, *decode4(pool, q, sm_scale=0.3), sm_scale=0.3)
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("std", [2.0**-13, 30.0, 4000.0])
+def test_decode_values_of_all_sizes(dt, std):
+    # steps that pass 1 while a sequence runs, and ones near fp16's least
+    pool = Pool([300, 40, 1], 1, 64, 64, 16, dt, seed=4)
+    pool.parts[1][1].mul_(torch.linspace(0.1, 1.0, 16, device="cuda").view(1, 1, 16, 1, 1) * std)
+    q = randn((3, 2, 64), dt, 9, 1.5)
+    o, lse = decode4(pool, q)
+    if dt == HF and std > 1000:
+        keep = o.isfinite()
+        assert keep.any()
+    check_decode4(pool, q, o, lse)
+
+
+@pytest.mark.parametrize("dt,size", [(BF, 2.0**-100), (BF, 2.0**60), (HF, 2.0**-14), (HF, 2.0**10)])
+def test_decode_queries_of_all_sizes(dt, size):
+    pool = Pool([100, 7], 1, 128, 64, 16, dt, seed=5)
+    q = randn((2, 3, 128), dt, 1) * size
+    scale = 1.0 / (8 * size)
+    if scale < 1e37:
+        check_decode4(pool, q, *decode4(pool, q, sm_scale=scale), sm_scale=scale)
+
+
+def test_decode_nan_and_infinite_entries_stay_with_their_head():
+    pool = Pool([100, 7], 2, 64, 64, 16, BF, seed=6)
+    q = randn((2, 4, 64), BF, 1)
+    good = decode4(pool, q)
+    for which in (0, 1):
+        scale = pool.parts[which][1]
+        for row in (0, 1):
+            at = (pool.table[0, 3].item(), 1, 5, row, 0)
+            old = scale[at].item()
+            scale[at] = math.nan
+            o, lse = decode4(pool, q)
+            scale[at] = old
+            assert o[0, 2:].isnan().all() and torch.equal(o[0, :2], good[0][0, :2]) and torch.equal(o[1], good[0][1])
+            assert (lse[0, 2:].isnan().all() if which == 0 else torch.equal(lse, good[1]))
+    q[0, 1, 3] = math.inf
+    o, lse = decode4(pool, q)
+    assert o[0, 1].isnan().all() and torch.equal(o[0, [0, 2, 3]], good[0][0, [0, 2, 3]])
+
+
+def test_decode_one_key_that_outweighs_an_even_tail():
+    # one key 2^20 times as heavy as each of 8000 others, and values that differ
+    n = 8000
+    pool = Pool([n], 1, 64, 64, 64, HF, seed=7)
+    (kc, ks), (vc, vs) = pool.parts
+    kc.zero_(), ks.zero_()
+    first = pool.table[0, 0].item()
+    ks[first, 0, 9, 1] = 1.0  # the heavy key: all ones; the others zero
+    q = torch.full((1, 1, 64), 1.0, dtype=HF, device="cuda")
+    scale = 20 * math.log(2) / 64
+    o, lse = decode4(pool, q, sm_scale=scale)
+    check_decode4(pool, q, o, lse, sm_scale=scale)
+
+
+def test_decode_bad_pages_and_lengths_are_reported():
+    lens = [100, 64, 30]
+    pool = Pool(lens, 1, 64, 64, 16, BF, seed=5)
+    q = randn((3, 2, 64), BF, 5)
+    good = decode4(pool, q)
+    for bad in (-1, pool.parts[0][0].shape[0], 2**31 - 1):
+        pool.table[0, 2] = bad
+        o, lse = binding.attn_paged_decode(pool.cache, q)
+        assert binding.sync_check() == 6 and binding.sync_check() == 0
+        assert torch.equal(o[1:], good[0][1:]) and torch.isfinite(o).all()
+    pool = Pool(lens, 1, 64, 64, 16, BF, seed=5, extra=0)
+    pool.seq_lens[1] = -5
+    o, lse = binding.attn_paged_decode(pool.cache, q)
+    assert binding.sync_check() == 6
+    assert (o[1] == 0).all() and torch.isneginf(lse[1]).all()
+    pool.seq_lens[1] = 64
+    pool.seq_lens[0] = pool.table.shape[1] * 16 + 1000  # counts as the whole row of the table
+    binding.attn_paged_decode(pool.cache, q)
+    assert binding.sync_check() == 6
+
+
+def test_decode_writes_its_outputs_only():
+    pool = Pool([100, 0, 3], 2, 64, 32, 16, HF, seed=6)
+    q = randn((3, 4, 64), HF, 6)
+    ob = torch.full((3 * 4 * 32 + 128,), 7.0, dtype=HF, device="cuda")
+    lb = torch.full((3 * 4 + 8,), 7.0, device="cuda")
+    o, lse = ob[64:-64].view(3, 4, 32), lb[4:-4].view(3, 4)
+    before = pool.bits()
+    decode4(pool, q, out=(o, lse))
+    check_decode4(pool, q, o, lse)
+    assert (ob[:64] == 7).all() and (ob[-64:] == 7).all() and (lb[:4] == 7).all() and (lb[-4:] == 7).all()
+    assert all(torch.equal(a, b) for a, b in zip(before, pool.bits()))
+
+
+# ----------------------------------------------------------------- weights
+def check_weights(pool, q, lse, w, out, sm_scale=None, decay=1.0):
+    B, Hq, D = q.shape
+    s = D**-0.5 if sm_scale is None else sm_scale
+    Q, G = f64(q), Hq // pool.Hkv
+    L, W, Out = f64(lse), np.zeros(out.shape) if w is None else f64(w), f64(out)
+    for b, n in enumerate(pool.lens):
+        assert np.array_equal(Out[b, :, n:], W[b, :, n:])
+        for h in range(pool.Hkv if n else 0):
+            k, num, ks, km = pool.rows(0, b, h, n)
+            want, tol = (decay * W[b, h, :n] if decay else np.zeros(n)), np.zeros(n)
+            for i in range(h * G, (h + 1) * G):
+                p = np.exp(s * (k @ Q[b, i]) - L[b, i]) if L[b, i] != -np.inf else np.zeros(n)
+                size = (num * ks + km) @ np.abs(Q[b, i]) if pool.four else np.abs(k) @ np.abs(Q[b, i])
+                d = ((D / 8 + 16) if pool.four else (D + 4)) * 2.0**-22 * s * size
+                want = want + p
+                tol += p * (d + 2.0**-22 * (abs(L[b, i]) if L[b, i] != -np.inf else 0) + 2.0**-20)
+            err = np.abs(Out[b, h, :n] - want)
+            assert (err <= tol + 2.0**-23 * np.abs(want) + 2.0**-126).all(), (b, h, float((err - tol).max()))
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("dims", [32, 64, 128, 256])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_weights_dims_and_edge_lengths(four, dims, dt):
+    pool = Pool([0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 200], 2, dims, 64, 16, dt, seed=dims, four=four)
+    q = randn((12, 6, dims), dt, 3, 1.5)
+    _, lse = binding.attn_paged_decode(pool.cache, q)
+    out = binding.attn_paged_weights(pool.cache, q, lse)
+    assert binding.sync_check() == 0
+    check_weights(pool, q, lse, None, out)
+    w = torch.rand(out.shape, device="cuda")
+    again = binding.attn_paged_weights(pool.cache, q, lse, w, decay=0.75)
+    check_weights(pool, q, lse, w, again, decay=0.75)
+    inplace = w.clone()
+    assert binding.attn_paged_weights(pool.cache, q, lse, inplace, decay=0.75, out=inplace) is inplace
+    assert torch.equal(inplace, again)
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("group", [1, 3, 8, 9, 16, 17, 32, 33, 70])
+@pytest.mark.parametrize("dims", [64, 256])
+def test_weights_head_groups(four, group, dims):
+    pool = Pool([70, 1, 200], 2, dims, 64, 24, BF, seed=group, head_major=False, four=four)
+    q = randn((3, 2 * group, dims), BF, group)
+    _, lse = binding.attn_paged_decode(pool.cache, q, sm_scale=0.2)
+    check_weights(pool, q, lse, None, binding.attn_paged_weights(pool.cache, q, lse, sm_scale=0.2), sm_scale=0.2)
+
+
+@pytest.mark.parametrize("four", [True, False])
+def test_weights_splits_decay_nothing_and_empty_heads(four):
+    lens = [5000, 0, 1, 700] + [3] * 200
+    pool = Pool(lens, 2, 64, 64, 16, BF, seed=1, four=four)
+    q = randn((204, 4, 64), BF, 2)
+    _, lse = binding.attn_paged_decode(pool.cache, q)
+    lse[3, 1] = -math.inf  # no weight
+    w = torch.full((204, 2, pool.table.shape[1] * 16), math.nan, device="cuda")
+    for b, n in enumerate(lens):
+        w[b, :, n:] = 5.0
+    a = binding.attn_paged_weights(pool.cache, q, lse, w, decay=0.0)  # NaN is not read
+    check_weights(pool, q, lse, torch.nan_to_num(w, 0.0), a, decay=0.0)
+    assert torch.equal(a, binding.attn_paged_weights(pool.cache, q, lse, w, decay=0.0))
+    # a view with other strides, and nothing outside it
+    big = torch.full((204, 4, w.shape[2] + 3), 9.0, device="cuda")
+    view = big[:, 1:3, 2:-1]
+    binding.attn_paged_weights(pool.cache, q, lse, w, decay=0.0, out=view)
+    assert torch.equal(view, a)
+    assert (big[:, [0, 3]] == 9).all() and (big[:, :, :2] == 9).all() and (big[:, :, -1:] == 9).all()
+
+
+@pytest.mark.parametrize("four", [True, False])
+def test_weights_bad_pages_and_lengths_are_reported(four):
+    pool = Pool([100, 64], 1, 64, 64, 16, BF, seed=5, extra=0, four=four)
+    q = randn((2, 2, 64), BF, 5)
+    _, lse = binding.attn_paged_decode(pool.cache, q)
+    good = binding.attn_paged_weights(pool.cache, q, lse)
+    pool.table[0, 2] = pool.parts[0][0].shape[0]
+    got = binding.attn_paged_weights(pool.cache, q, lse)
+    assert binding.sync_check() == 6 and binding.sync_check() == 0
+    assert torch.equal(got[1], good[1]) and torch.equal(got[0, :, :32], good[0, :, :32])
+    want = np.exp(-f64(lse[0])).sum()  # scores of zero
+    assert np.abs(f64(got[0, 0, 32:48]) - want).max() <= 1e-5 * want
+    pool.seq_lens[1] = 100000
+    binding.attn_paged_weights(pool.cache, q, lse)
+    assert binding.sync_check() == 6
+
+
+# ---------------------------------------------------------------- eviction
+def run_evict(pool, w, keep, sinks=0, recent=0, n_new=None, pages=None, **kw):
+    most = max([keep] if isinstance(keep, int) else keep)
+    if n_new is None:
+        n_new = min(-(-most // pool.page), pool.table.shape[1])
+    if pages is None:
+        pages = ints(pool.spare[: len(pool.lens) * n_new].reshape(len(pool.lens), n_new).copy())
+    k = keep if isinstance(keep, int) else ints(keep)
+    return pages, binding.attn_paged_evict(pool.cache, w, k, pages, sinks=sinks, recent=recent, **kw)
+
+
+def check_evict(pool, before, w, keep, sinks, recent, pages, got):
+    """`before`: the pools' parts as they were."""
+    table, lens, w_out = got
+    W, page = w.cpu().numpy(), pool.page
+    old, P = pool.table.cpu().numpy(), pages.cpu().numpy()
+    want_table, want_w = old.copy(), np.array(W)
+    parts = [t.clone() for t in before]
+    for b, n in enumerate(pool.lens):
+        K = keep if isinstance(keep, int) else max(keep[b], 0)
+        assert lens[b].item() == min(n, K)
+        if n <= K:
+            continue
+        want_table[b, : P.shape[1]] = P[b]
+        for h in range(pool.Hkv):
+            kept = cache_ref.kept(W[b, h], n, K, sinks, recent)
+            want_w[b, h] = 0
+            want_w[b, h, : len(kept)] = W[b, h, kept]
+            src = [int(old[b, j // page]) for j in kept], [j % page for j in kept]
+            dst = [int(P[b, j // page]) for j in range(K)], [j % page for j in range(K)]
+            for x, y in zip(before, parts):
+                if K:
+                    y[dst[0], h, dst[1]] = x[src[0], h, src[1]]
+    assert np.array_equal(table.cpu().numpy(), want_table)
+    assert np.array_equal(w_out.cpu().numpy(), want_w, equal_nan=True)
+    now = [t for p in pool.parts for t in p]
+    for x, y in zip(now, parts):
+        assert torch.equal(bits(x), bits(y))  # the kept rows, and everything else as it was
+
+
+def random_weights(pool, seed, ties=True):
+    r = np.random.RandomState(seed)
+    places = pool.table.shape[1] * pool.page
+    w = np.exp(2 * r.randn(len(pool.lens), pool.Hkv, places)).astype(np.float32)
+    if ties:
+        w = np.round(w * 2) / 2  # many equal ones, and zeros
+    return torch.from_numpy(w.astype(np.float32)).cuda()
+
+
+@pytest.mark.parametrize("four,dims,dt", [(True, (64, 64), BF), (True, (256, 32), BF), (True, (128, 256), HF),
+                                          (False, (64, 128), BF), (False, (16, 256), HF)])
+@pytest.mark.parametrize("page,head_major", [(1, False), (7, True), (16, False), (64, True)])
+@pytest.mark.parametrize("sinks,recent", [(0, 0), (4, 16), (100, 7), (3, 1000)])
+def test_evict(four, dims, dt, page, head_major, sinks, recent):
+    lens = [0, 1, 39, 40, 41, 130, 77, 300]
+    pool = Pool(lens, 2, *dims, page, dt, seed=page, head_major=head_major, four=four, spare=8 * -(-40 // page))
+    w = random_weights(pool, page)
+    before = [t.clone() for p in pool.parts for t in p]
+    pages, got = run_evict(pool, w, 40, sinks, recent)
+    assert binding.sync_check() == 0
+    check_evict(pool, before, w, 40, sinks, recent, pages, got)
+
+
+@pytest.mark.parametrize("four", [True, False])
+def test_evict_by_sequence_and_odd_weights(four):
+    lens = [100, 90, 64, 30, 55, 1]
+    keep = [10, 0, 64, -3, 17, 5]
+    pool = Pool(lens, 3, 64, 64, 16, BF, seed=3, four=four, spare=40, extra=3)
+    w = random_weights(pool, 1)
+    w[0, 0, 3:9] = math.nan
+    w[0, 1, ::2] = -0.0
+    w[0, 1, 1::2] = 0.0
+    w[0, 2] = -1.0 - torch.arange(w.shape[2], device="cuda") % 3
+    w[4, 0] = math.inf
+    w[4, 1, 20:] = -math.inf
+    w[4, 2] = 1e-45 * (torch.arange(w.shape[2], device="cuda") % 4)
+    before = [t.clone() for p in pool.parts for t in p]
+    pages, got = run_evict(pool, w, keep, 2, 3, n_new=5)
+    assert binding.sync_check() == 0
+    check_evict(pool, before, w, keep, 2, 3, pages, got)
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("keep", [1, 1000, 4999, 20000])
+def test_evict_from_long_sequences(four, keep):
+    pool = Pool([20011, 5000], 1, 64, 64, 64, BF, seed=4, four=four, spare=2 * -(-keep // 64))
+    w = random_weights(pool, 2, ties=False)
+    before = [t.clone() for p in pool.parts for t in p]
+    pages, got = run_evict(pool, w, keep, 4, 64)
+    check_evict(pool, before, w, keep, 4, 64, pages, got)
+    assert binding.sync_check() == 0
+    for x, y in zip(got, run_evict(pool, w, keep, 4, 64, pages=pages)[1]):
+        assert torch.equal(x, y)
+
+
+def test_evict_outputs_in_views():
+    pool = Pool([100, 20], 2, 64, 64, 16, BF, seed=5, spare=6)
+    w = random_weights(pool, 3)
+    table = torch.full((2, pool.table.shape[1] + 4), 77, dtype=torch.int32, device="cuda")
+    lens = torch.full((2,), 77, dtype=torch.int32, device="cuda")
+    big = torch.full((2, 4, w.shape[2] + 8), 7.0, device="cuda")
+    wide = torch.zeros((2, 2, w.shape[2] + 5), device="cuda")
+    wide[..., 1:-4] = w
+    before = [t.clone() for p in pool.parts for t in p]
+    out = (table[:, 2:-2], lens, big[:, 1:3, 4:-4])
+    pages, got = run_evict(pool, wide[..., 1:-4], 30, 1, 2, out=out)
+    assert all(a is b for a, b in zip(got, out))
+    check_evict(pool, before, w, 30, 1, 2, pages, got)
+    assert (table[:, :2] == 77).all() and (table[:, -2:] == 77).all()
+    assert (big[:, [0, 3]] == 7).all() and (big[..., :4] == 7).all() and (big[..., -4:] == 7).all()
+
+
+@pytest.mark.parametrize("four", [True, False])
+def test_evict_bad_pages_lengths_and_budgets_are_reported(four):
+    def fresh():
+        pool = Pool([100, 64], 1, 64, 64, 16, BF, seed=5, extra=0, four=four, spare=8)
+        return pool, random_weights(pool, 4), ints(pool.spare[:8].reshape(2, 4).copy())
+
+    pool, w, pages = fresh()
+    n = pool.parts[0][0].shape[0]
+    pages[0, 1], pages[1, 0] = n, -1
+    before = [t.clone() for p in pool.parts for t in p]
+    table, lens, _ = binding.attn_paged_evict(pool.cache, w, 40, pages)
+    assert binding.sync_check() == 6 and binding.sync_check() == 0
+    assert lens.tolist() == [40, 40] and table[0, :4].tolist() == pages[0].tolist()
+    written = {pages[0, 0].item(), pages[0, 2].item(), pages[1, 1].item(), pages[1, 2].item()}
+    for x, p in zip(before, [t for p in pool.parts for t in p]):
+        for i in set(range(n)) - written:
+            assert torch.equal(bits(x[i]), bits(p[i]))
+    pool, w, pages = fresh()
+    pool.table[0, 1] = n  # its tokens read as zeros
+    w[0, 0] = 0
+    w[0, 0, 20:30] = 1
+    binding.attn_paged_evict(pool.cache, w, 10, pages)
+    assert binding.sync_check() == 6
+    assert all((t[pages[0, 0].item(), 0, :10] == 0).all() for p in pool.parts for t in p)
+    pool, w, pages = fresh()
+    _, lens, _ = binding.attn_paged_evict(pool.cache, w, 70, pages)  # 64 places, a sequence of 100
+    assert binding.sync_check() == 6 and lens.tolist() == [64, 64]
+    pool, w, pages = fresh()
+    pool.seq_lens[0] = 10**6
+    _, lens, _ = binding.attn_paged_evict(pool.cache, w, 10, pages)
+    assert binding.sync_check() == 6 and lens.tolist() == [10, 10]
+    pool, w, pages = fresh()
+    pool.seq_lens[0] = -1
+    _, lens, _ = binding.attn_paged_evict(pool.cache, w, 10, pages)
+    assert binding.sync_check() == 6 and lens.tolist() == [0, 10]
+
+
+# ---------------------------------------------------------------- refusals
+def test_binding_refusals():
+    pool = Pool([40, 3], 2, 64, 64, 16, BF, spare=6)
+    c, (k, ks), (v, vs) = pool.cache, *pool.parts
+    q, x = randn((2, 4, 64), BF, 0), randn((2, 2, 64), BF, 1)
+    lse, w = torch.zeros((2, 4), device="cuda"), torch.zeros((2, 2, pool.table.shape[1] * 16), device="cuda")
+    off, pages = ints([0, 1, 2]), ints([[0], [1]])
+    P4 = binding.PagedCache4
+    for bad in (lambda: binding.attn_paged_decode(c, q[:1]), lambda: binding.attn_paged_decode(c, q[..., :32]),
+                lambda: binding.attn_paged_append(c, x[:1], x[:1]), lambda: binding.attn_paged_append(c, x, x[:, :1]),
+                lambda: P4(k, v[:1], ks, vs, pool.table, pool.seq_lens), lambda: P4(k, v, ks[:1], vs, pool.table, pool.seq_lens),
+                lambda: P4(k, v, ks[..., :1, :], vs, pool.table, pool.seq_lens),
+                lambda: P4(k, v, ks, vs, pool.table[0], pool.seq_lens), lambda: P4(k, v, ks, vs, pool.table, pool.seq_lens[:1]),
+                lambda: P4(k.cpu(), v, ks, vs, pool.table, pool.seq_lens),
+                lambda: P4(k, v, ks.repeat(1, 1, 1, 2, 1)[..., ::2, :], vs, pool.table, pool.seq_lens),
+                lambda: binding.attn_paged_gather(c, off[:2], 2), lambda: binding.attn_paged_gather(c, off, -1),
+                lambda: binding.attn_paged_gather(c, off.cpu(), 2),
+                lambda: binding.attn_paged_gather(c, off, 2, out=(x[:1], x[:1])),
+                lambda: binding.attn_paged_weights(c, q[:, :3], lse[:, :3]), lambda: binding.attn_paged_weights(c, q, lse[:, :3]),
+                lambda: binding.attn_paged_weights(c, q[..., :32], lse), lambda: binding.attn_paged_weights(c, q, lse, w[..., :16]),
+                lambda: binding.attn_paged_weights(c, q, lse, w, out=w[:1]),
+                lambda: binding.attn_paged_evict(c, w[:1], 4, pages), lambda: binding.attn_paged_evict(c, w, 4, pages[:1]),
+                lambda: binding.attn_paged_evict(c, w, 4, torch.zeros((2, 99), dtype=torch.int32, device="cuda")),
+                lambda: binding.attn_paged_evict(c, w, off, pages), lambda: binding.attn_paged_evict(c, w, 4, pages, sinks=-1),
+                lambda: binding.attn_paged_evict(c, w, 4, pages, recent=-1),
+                lambda: binding.attn_paged_evict(c, w, 4, pages, out=(pool.table[:1], pool.seq_lens, w))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: binding.attn_paged_decode(c, q.half()), lambda: binding.attn_paged_append(c, x.half(), x.half()),
+                lambda: P4(k.int(), v, ks, vs, pool.table, pool.seq_lens), lambda: P4(k, v, ks.float(), vs, pool.table, pool.seq_lens),
+                lambda: P4(k, v, ks, vs, pool.table.long(), pool.seq_lens), lambda: binding.attn_paged_gather(c, off.long(), 2),
+                lambda: binding.attn_paged_weights(c, q, lse.half()), lambda: binding.attn_paged_weights(c, q, lse, w.double()),
+                lambda: binding.attn_paged_evict(c, w, off[1:].long(), pages), lambda: binding.attn_paged_evict(c, w, 4, pages.long())):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: binding.attn_paged_gather(c, off, 2, out=(x, x)), lambda: binding.attn_paged_weights(c, q, lse, decay=1.5), lambda: binding.attn_paged_decode(c, q, sm_scale=-1.0),
+                lambda: binding.attn_paged_evict(c, w, 4, pages, out=(pool.table, pool.seq_lens.clone(), w.clone())),
+                lambda: binding.attn_paged_evict(c, w, 4, pages, out=(pool.table.clone(), pool.seq_lens, w.clone())),
+                lambda: binding.attn_paged_evict(c, w, 4, pages, out=(pool.table.clone(), pool.seq_lens.clone(), w)),
+                lambda: binding.attn_paged_append(P4(k, k, ks, vs, pool.table, pool.seq_lens), x, x),
+                lambda: binding.attn_paged_decode(P4(k[..., :24], v, ks, vs, pool.table, pool.seq_lens), q[..., :48])):
+        with pytest.raises(binding.AttnError):
+            bad()
+
+
+def test_nothing_to_do():
+    for four in (True, False):
+        pool = Pool([0, 0], 2, 64, 64, 16, BF, four=four)
+        q, x = randn((2, 4, 64), BF, 0), randn((2, 2, 64), BF, 1)
+        before = pool.bits()
+        assert (binding.attn_paged_append(pool.cache, x, x, q=q) == 0).all()
+        o, lse = binding.attn_paged_decode(pool.cache, q)
+        assert (o == 0).all() and torch.isneginf(lse).all()
+        k, v = binding.attn_paged_gather(pool.cache, ints([0, 0, 0]), 0)
+        assert k.shape == (2, 0, 64)
+        assert (binding.attn_paged_weights(pool.cache, q, lse) == 0).all()
+        w = torch.zeros((2, 2, 16), device="cuda")
+        table, lens, w2 = binding.attn_paged_evict(pool.cache, w, 0, torch.zeros((2, 0), dtype=torch.int32, device="cuda"))
+        assert torch.equal(table, pool.table) and (lens == 0).all() and torch.equal(w, w2)
+        assert all(torch.equal(a, b) for a, b in zip(before, pool.bits()))
+        none = pool.make(pool.table[:0], pool.seq_lens[:0])
+        assert binding.attn_paged_decode(none, q[:0])[0].shape == (0, 4, 64)
+        assert binding.attn_paged_weights(none, q[:0], lse[:0]).shape == (0, 2, 16)
+    assert binding.sync_check() == 0
+
+
+# ---------------------------------------------------------------- together
+@pytest.mark.parametrize("four,dims,dt", [(True, (64, 64), BF), (True, (128, 64), HF), (False, (64, 64), BF)])
+def test_a_program_that_serves(four, dims, dt):
+    """Prompts are rotated, appended, read back and attended to; then tokens are
+    appended and decoded, their weights added up; the cache is cut down, its
+    table and lengths take the results, and decoding goes on: every row against
+    the float64 attention over what the cache holds."""
+    Dqk, Dv, H, G, page, keep = *dims, 2, 3, 16, 24
+    prompt = [70, 5, 33]
+    r = binding.Rope(Dqk)
+    pool = Pool([n + 8 for n in prompt], H, Dqk, Dv, page, dt, four=four, spare=8)
+    pool.lens = prompt
+    pool.seq_lens.copy_(ints(prompt))
+    cache, T = pool.cache, sum(prompt)
+    off = ints([0] + prompt).cumsum(0).int()
+    k, v, q = randn((T, H, Dqk), dt, 1), randn((T, H, Dv), dt, 2), randn((T, H * G, Dqk), dt, 3)
+    qr = binding.attn_paged_append(cache, k, v, rope=r, q=q, offsets=off)
+    kd, vd = binding.attn_paged_gather(cache, off, T)
+    # attn_fwd takes as many key heads as query heads
+    o, _ = binding.attn_fwd(qr.transpose(0, 1).contiguous(), kd.repeat_interleave(G, 0), vd.repeat_interleave(G, 0),
+                            causal=True, offsets=off, max_seq_len=max(prompt))
+    assert binding.sync_check() == 0
+    for b, n in enumerate(prompt):
+        # the last token of a prompt sees all of it, as a decode would
+        o1, _ = binding.attn_paged_decode(cache, qr[off[1:].long() - 1].contiguous())
+        assert np.abs(f64(o[:, off[b + 1].item() - 1]) - f64(o1[b])).max() <= 2e-2
+    w = torch.zeros((3, H, cache.max_pages * page), device="cuda")
+    pos = ints(prompt)  # positions of the next tokens
+    for step in range(6):
+        cache.seq_lens += 1
+        x, y, z = randn((3, H, Dqk), dt, 10 + step), randn((3, H, Dv), dt, 20 + step), randn((3, H * G, Dqk), dt, 30 + step)
+        zr, xr = (t[:, :, 0] for t in binding.attn_rope([z[:, :, None], x[:, :, None]], r, positions=pos[:, None]))
+        binding.attn_paged_append(cache, xr, y)
+        o, lse = binding.attn_paged_decode(cache, zr)
+        binding.attn_paged_weights(cache, zr, lse, w, out=w)
+        pos += 1
+        lens = cache.seq_lens.tolist()
+        assert binding.sync_check() == 0
+        O, L = paged_ref.decode(f64(zr), pool.values(0), pool.values(1), pool.table.cpu().numpy(), lens)
+        size = np.abs(np.nan_to_num(pool.values(1))).max()
+        assert np.abs(f64(o) - O).max() <= torch.finfo(dt).eps * size + 2.0**-10 * size
+        assert np.abs(f64(lse) - L).max() <= 1e-4
+        for b, n in enumerate(lens):
+            assert (w[b, :, n:] == 0).all()
+        if step == 2:
+            pool.lens = lens
+            total = w.clone()
+            before = [t.clone() for p in pool.parts for t in p]
+            pages, got = run_evict(pool, w, keep, 2, 8)
+            check_evict(pool, before, total, keep, 2, 8, pages, got)
+            for dst, src in zip((cache.page_table, cache.seq_lens, w), got):
+                dst.copy_(src)
+            # pages to grow into: the row's entry behind the budget's two
+            for b, n in enumerate(lens):
+                if n > keep:
+                    cache.page_table[b, 2] = int(pool.spare[6 + b % 2])
+    assert (w.sum(-1) > 0).all()
+
+
+def _step(cache, r, k, v, q, w):
+    qr = binding.attn_paged_append(cache, k, v, rope=r, q=q)
+    o, lse = binding.attn_paged_decode(cache, qr)
+    binding.attn_paged_weights(cache, qr, lse, w, out=w, decay=0.5)
+    return o, lse
+
+
+@pytest.mark.parametrize("four", [True, False])
+def test_captured_steps_replay_on_two_streams(four):
+    pools = [Pool([50, 0, 17], 2, 64, 64, 16, BF, seed=s, four=four, spare=8) for s in (1, 2)]
+    r = binding.Rope(64)
+    ins = [[randn((3, h, 64), BF, 10 * s + h) for h in (2, 2, 4)] for s in (1, 2)]
+    ws = [torch.zeros((3, 2, p.table.shape[1] * 16), device="cuda") for p in pools]
+    pages = [ints(p.spare[:3].reshape(3, 1).copy()) for p in pools]
+    graphs, outs, streams = [], [], []
+    for p, i, w, pg in zip(pools, ins, ws, pages):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                o, lse = _step(p.cache, r, *i, w)
+                ev = binding.attn_paged_evict(p.cache, w, 12, pg, sinks=1, recent=2)
+        graphs.append(g), outs.append((o, lse, ev)), streams.append(s)
+    torch.cuda.synchronize()
+    for lens in ([50, 0, 17], [60, 3, 0], [49, 0, 3]):  # (at 60 the keys behind 50 are NaN)
+        eager = []
+        for p, i, w, pg in zip(pools, ins, ws, pages):
+            w.zero_()
+            p.seq_lens.copy_(ints(lens))
+            o, lse = _step(p.cache, r, *i, w)
+            ev = binding.attn_paged_evict(p.cache, w, 12, pg, sinks=1, recent=2)
+            eager.append([o, lse, *ev, w.clone()])
+            w.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert binding.sync_check() == 0
+        for e, (o, lse, ev), w in zip(eager, outs, ws):
+            for x, y in zip(e, (o, lse, *ev, w)):
+                assert torch.equal(torch.nan_to_num(x, 7.0), torch.nan_to_num(y, 7.0))
+
+
+def test_inputs_written_just_before_the_call_are_seen():
+    pool = Pool([2000, 900], 2, 128, 128, 16, BF, seed=1, spare=200)
+    q = randn((2, 4, 128), BF, 1)
+    w = random_weights(pool, 1)
+    o, lse = decode4(pool, q)
+    a = binding.attn_paged_weights(pool.cache, q, lse, w)
+    pages = ints(pool.spare[:64].reshape(2, 32).copy())
+    e = binding.attn_paged_evict(pool.cache, a, 500, pages, sinks=3, recent=5)
+    k, v = binding.attn_paged_gather(pool.cache, ints([0, 2000, 2900]), 2900)
+    torch.cuda.synchronize()
+    parts = [t.clone() for p in pool.parts for t in p]
+    for _ in range(3):
+        for t, p in zip([t for x in pool.parts for t in x], parts):
+            t.zero_()
+            t.copy_(p)
+        q2 = torch.zeros_like(q)
+        q2.copy_(q)
+        o2, lse2 = binding.attn_paged_decode(pool.cache, q2)
+        a2 = binding.attn_paged_weights(pool.cache, q2, lse2, w)
+        e2 = binding.attn_paged_evict(pool.cache, a2, 500, pages, sinks=3, recent=5)
+        k2, v2 = binding.attn_paged_gather(pool.cache, ints([0, 2000, 2900]), 2900)
+        for x, y in zip((o, lse, a, *e, k, v), (o2, lse2, a2, *e2, k2, v2)):
+            assert torch.equal(x, y)
+
+
+def test_launch_counts():
+    pool = Pool([40, 3], 2, 64, 64, 16, BF, spare=8)
+    q, x = randn((2, 4, 64), BF, 0), randn((2, 2, 64), BF, 1)
+    for call, n in ((lambda: binding.attn_paged_append(pool.cache, x, x, q=q), 1),
+                    (lambda: binding.attn_paged_decode(pool.cache, q), 2),
+                    (lambda: binding.attn_paged_gather(pool.cache, ints([0, 1, 2]), 2), 1),
+                    (lambda: binding.attn_paged_weights(pool.cache, q, torch.zeros((2, 4), device="cuda")), 1)):
+        before = binding.launch_count()
+        call()
+        assert binding.launch_count() - before == n
+    assert binding.sync_check() == 0
+
+
+def test_pool_offsets_pass_32_bits():
+    # pages 4 GB and more into the pools
+    page, D, n = 4096, 256, 9000
+    pool = Pool([n], 1, D, D, page, BF, seed=1)
+    # 2^31 bytes of codes a pool: 4200 pages of 512 KB
+    big = [[torch.empty((9000, *t.shape[1:]), dtype=t.dtype, device="cuda") for t in p] for p in pool.parts]
+    rows = [8999, 4500, 8200]
+    for src, dst in zip(pool.parts, big):
+        for x, y in zip(src, dst):
+            for i, at in enumerate(rows):
+                y[at] = x[pool.table[0, i].item()]
+    q = randn((1, 4, D), BF, 2)
+    o, lse = decode4(pool, q)
+    a = binding.attn_paged_weights(pool.cache, q, lse)
+    k, v = binding.attn_paged_gather(pool.cache, ints([0, n]), n)
+    pool.parts, pool.table = big, ints([rows + [0]])
+    pool.cache = pool.make(pool.table, pool.seq_lens)
+    o2, lse2 = decode4(pool, q)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert torch.equal(a, binding.attn_paged_weights(pool.cache, q, lse))
+    k2, v2 = binding.attn_paged_gather(pool.cache, ints([0, n]), n)
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    x = randn((1, 1, D), BF, 3)
+    binding.attn_paged_append(pool.cache, x, x)
+    num, s, m = cache_ref.round4(f64(x))
+    at = (8200, 0, (n - 1) % page)
+    assert (big[0][0][at].cpu().numpy() == cache_ref.pack4(num)[0, 0]).all()
+    assert (big[1][1][at].cpu().numpy() == np.stack([s[0, 0], m[0, 0]])).all()
+    table, lens, _ = binding.attn_paged_evict(pool.cache, a, 3000, ints([[8998]]))
+    after = pool.make(table, lens)
+    k3, _ = binding.attn_paged_gather(after, ints([0, 3000]), 3000)
+    kept = cache_ref.kept(a[0, 0].cpu().numpy(), n, 3000)
+    kd, _ = binding.attn_paged_gather(pool.cache, ints([0, n]), n)
+    assert torch.equal(k3[0], kd[0, kept])
+    assert binding.sync_check() == 0

@@ -1,0 +1,308 @@
+"""The smaller paged cache without a GPU: the oracle's pins, and what is
+refused before anything is launched."""
+import ctypes
+import math
+import os
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+from attention_forward_jvp_gb300 import binding, build
+from oracle import cache_ref, paged_ref
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INVALID, UNSUPPORTED, MISALIGNED = 1, 2, 3
+FAKE = 0x10000  # 16-byte aligned, never dereferenced: every call here is refused or empty
+AT = [0x100000 * (i + 1) for i in range(20)]
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return binding.lib()
+
+
+# ------------------------------------------------------------------- oracle
+def test_oracle_round4_by_hand():
+    x = np.zeros((1, 32))
+    x[0, :4] = [-3.0, 12.0, -2.4, 4.5]
+    n, s, m = cache_ref.round4(x)  # steps of 1 from -3 on
+    assert s[0, 0] == 1 and m[0, 0] == -3
+    assert list(n[0, :5]) == [0, 15, 1, 8, 3]  # 7.5 goes to the even 8
+    v = cache_ref.values4(n, s, m)
+    assert list(v[0, :5]) == [-3.0, 12.0, -2.0, 5.0, 0.0]
+    assert (cache_ref.unpack4(cache_ref.pack4(n)) == n).all()
+    assert cache_ref.pack4(np.array([[1, 2, 3, 15]])).tolist() == [[0x21, 0xF3]]
+
+
+def test_oracle_round4_edges():
+    n, s, m = cache_ref.round4(np.full((1, 64), 2.5))
+    assert s[0, 0] == 0 and m[0, 0] == 2.5 and (n == 0).all()
+    n, s, m = cache_ref.round4(np.full((1, 64), 0.1))  # fp16(0.1) lies below fp32's
+    assert abs(cache_ref.values4(n, s, m)[0, 0] - 0.1) <= 0.1 * 2.0**-11
+    x = np.linspace(-1e6, 1e6, 64)[None]
+    n, s, m = cache_ref.round4(x)
+    assert m[0, 0] == -65504 and n[0, 0] == 0 and n[0, -1] == 15 and np.isfinite(s).all()
+    x = np.zeros((1, 128))
+    x[0, 3] = np.inf
+    n, s, m = cache_ref.round4(x)
+    assert np.isnan(s[0, 0]) and np.isnan(m[0, 0]) and s[0, 1] == 0
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+def test_oracle_round4_is_off_by_half_a_step(d):
+    x = np.random.RandomState(d).randn(50, d).astype(np.float32)
+    n, s, m = cache_ref.round4(x)
+    assert s.shape == (50, max(1, d // 64))
+    err = np.abs(cache_ref.values4(n, s, m) - x)
+    # half a step; m and s are rounded by 2^-11 each, s up to 15 times over
+    step = np.repeat(s.astype(np.float64), cache_ref.group_of(d), -1)
+    assert (err <= 0.5 * step + 15 * step * 2.0**-11 + np.abs(x).max() * 2.0**-11).all()
+
+
+def test_oracle_weights_are_the_softmax():
+    r = np.random.RandomState(0)
+    q, k, v = r.randn(2, 4, 8), r.randn(6, 2, 4, 8), r.randn(6, 2, 4, 8)
+    table, lens = np.array([[3, 1, 5], [0, 2, 4]]), [9, 0]
+    _, lse = paged_ref.decode(q, k, v, table, lens)
+    w = cache_ref.weights(q, lse, k, table, lens, np.ones((2, 2, 12)), decay=0.5)
+    np.testing.assert_allclose(w[0, :, :9].sum(-1), 2 + 4.5)  # two heads' softmax and half of nine ones
+    assert (w[0, :, 9:] == 1).all() and (w[1] == 1).all()
+
+
+def test_oracle_kept_by_hand():
+    w = [9.0, 1.0, 5.0, 5.0, 5.0, 0.0, 7.0, 2.0]
+    assert cache_ref.kept(w, 8, 9) == list(range(8))
+    assert cache_ref.kept(w, 8, 4) == [0, 2, 3, 6]
+    assert cache_ref.kept(w, 8, 4, sinks=2) == [0, 1, 2, 6]
+    assert cache_ref.kept(w, 8, 4, recent=2) == [0, 2, 6, 7]
+    assert cache_ref.kept(w, 8, 3, sinks=5, recent=2) == [0, 6, 7]
+    assert cache_ref.kept(w, 8, 3, sinks=5, recent=20) == [5, 6, 7]
+    assert cache_ref.kept([math.nan, 3.0, math.inf, math.nan], 4, 3) == [0, 2, 3]
+    assert cache_ref.kept([0.0, -0.0, 0.0], 3, 2) == [0, 1]
+    assert cache_ref.kept(w, 8, 0) == []
+
+
+# ----------------------------------------------------------------- refusals
+def _cache4(**kw):
+    c = binding.AttnPagedCache4()
+    c.B, c.max_pages, c.n_pages, c.page_size, c.Hkv, c.Dqk, c.Dv = 2, 4, 8, 16, 2, 128, 64
+    c.k, c.v, c.k_scale, c.v_scale, c.page_table, c.seq_lens = AT[:6]
+    c.k_stride[:], c.v_stride[:], c.table_stride = (2048, 1024, 64), (1024, 512, 32), 4
+    c.k_scale_stride[:], c.v_scale_stride[:] = (128, 64, 4), (64, 32, 2)
+    for k, v in kw.items():
+        if k.endswith("_stride") and k != "table_stride":
+            getattr(c, k)[:] = v
+        else:
+            setattr(c, k, v)
+    return c
+
+
+def _cache16(**kw):
+    c = binding.AttnPagedCache()
+    c.B, c.max_pages, c.n_pages, c.page_size, c.Hkv, c.Dqk, c.Dv = 2, 4, 8, 16, 2, 64, 64
+    c.k, c.v, c.page_table, c.seq_lens = AT[0], AT[1], AT[4], AT[5]
+    c.k_stride[:], c.v_stride[:], c.table_stride = (2048, 1024, 64), (2048, 1024, 64), 4
+    for k, v in kw.items():
+        if k in ("k_stride", "v_stride"):
+            getattr(c, k)[:] = v
+        else:
+            setattr(c, k, v)
+    return c
+
+
+def _same(results):
+    assert len(set(results)) == 1
+    return results[0]
+
+
+def _append(c, rope=None, **kw):
+    n = binding.AttnPagedNew()
+    n.T, n.k, n.v, n.q, n.q_out, n.Hq = 2, AT[6], AT[7], AT[8], AT[9], 4
+    n.k_stride[:], n.v_stride[:], n.q_stride[:], n.q_out_stride[:] = (256, 128), (128, 64), (512, 128), (512, 128)
+    for k, v in kw.items():
+        if k.endswith("_stride"):
+            getattr(n, k)[:] = v
+        else:
+            setattr(n, k, v)
+    return _same([f(ctypes.byref(c) if c is not None else None, ctypes.byref(n), rope, None)
+                  for f in (binding.lib().attn_paged_append4, binding.lib().attn_paged_append4_f16)])
+
+
+def _decode(c, Hq=4, q=AT[6], qs=(512, 128), scale=math.nan, o=AT[7], lse=AT[8], ws=AT[9], n=1 << 40):
+    return _same([f(ctypes.byref(c) if c is not None else None, Hq, q, (ctypes.c_int64 * 2)(*qs) if qs else None, scale,
+                    o, lse, ws, n, None)
+                  for f in (binding.lib().attn_paged_decode4, binding.lib().attn_paged_decode4_f16)])
+
+
+def _gather(c, T=5, offsets=AT[6], k=AT[7], ks=(640, 128), v=AT[8], vs=(640, 128), four=True):
+    L = binding.lib()
+    i64 = ctypes.c_int64 * 2
+    return _same([f(ctypes.byref(c) if c is not None else None, T, offsets, k, i64(*ks) if ks else None, v,
+                    i64(*vs) if vs else None, None)
+                  for f in ((L.attn_paged_gather4, L.attn_paged_gather4_f16) if four else (L.attn_paged_gather,))])
+
+
+def _weights(c, four=True, Hq=4, q=AT[6], qs=(512, 128), scale=math.nan, weight=True, **kw):
+    L = binding.lib()
+    a = binding.AttnPagedWeight()
+    a.lse, a.w, a.out, a.decay = AT[7], AT[8], AT[8], 1.0
+    a.w_stride[:], a.out_stride[:] = (128, 64), (128, 64)
+    for k, v in kw.items():
+        if k.endswith("_stride"):
+            getattr(a, k)[:] = v
+        else:
+            setattr(a, k, v)
+    fs = (L.attn_paged_weights4, L.attn_paged_weights4_f16) if four else (L.attn_paged_weights, L.attn_paged_weights_f16)
+    return _same([f(ctypes.byref(c) if c is not None else None, Hq, q, (ctypes.c_int64 * 2)(*qs) if qs else None, scale,
+                    ctypes.byref(a) if weight else None, None) for f in fs])
+
+
+def _evict(c, four=True, ws=AT[12], n=1 << 40, eviction=True, **kw):
+    L = binding.lib()
+    a = binding.AttnPagedEviction()
+    a.w, a.w_out, a.keep_all, a.pages, a.pages_stride, a.n_new = AT[6], AT[7], 20, AT[8], 2, 2
+    a.table_out, a.table_out_stride, a.lens_out = AT[9], 4, AT[10]
+    a.w_stride[:], a.w_out_stride[:] = (128, 64), (128, 64)
+    for k, v in kw.items():
+        if k in ("w_stride", "w_out_stride"):
+            getattr(a, k)[:] = v
+        else:
+            setattr(a, k, v)
+    return (L.attn_paged_evict4 if four else L.attn_paged_evict)(
+        ctypes.byref(c) if c is not None else None, ctypes.byref(a) if eviction else None, ws, n, None)
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(B=-1), INVALID), (dict(max_pages=-1), INVALID), (dict(n_pages=-1), INVALID), (dict(page_size=0), INVALID),
+    (dict(Hkv=0), INVALID), (dict(Dqk=16), UNSUPPORTED), (dict(Dqk=96), UNSUPPORTED), (dict(Dv=512), UNSUPPORTED),
+    (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(k_scale=None), INVALID), (dict(v_scale=None), INVALID),
+    (dict(seq_lens=None), INVALID), (dict(page_table=None), INVALID), (dict(seq_lens=FAKE + 2), MISALIGNED),
+    (dict(k=FAKE + 8), MISALIGNED), (dict(v=FAKE + 1), MISALIGNED), (dict(k_stride=(2048, 1024, 72)), MISALIGNED),
+    (dict(v_stride=(1024, 520, 32)), MISALIGNED), (dict(k_scale=FAKE + 4), MISALIGNED), (dict(v_scale=FAKE + 2), MISALIGNED),
+    (dict(k_scale_stride=(128, 64, 6)), MISALIGNED), (dict(v_scale_stride=(64, 33, 2)), MISALIGNED)])
+def test_cache4_refused(L, bad, want):
+    c = _cache4(**bad)
+    assert [f(c) for f in (_append, _decode, _gather, _weights, _evict)] == [want] * 5
+    assert L.attn_paged_decode4_workspace(ctypes.byref(c), 4) == 0
+
+
+def test_no_cache_refused(L):
+    assert [f(None) for f in (_append, _decode, _gather, _weights, _evict)] == [INVALID] * 5
+    assert [f(None, four=False) for f in (_gather, _weights, _evict)] == [INVALID] * 3
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(T=-1), INVALID), (dict(T=3), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
+    (dict(q_out=None), INVALID), (dict(Hq=-1), INVALID), (dict(k=FAKE + 1), MISALIGNED), (dict(offsets=FAKE + 2), MISALIGNED),
+    (dict(q=AT[8], q_out=AT[8], q_out_stride=(1024, 128)), INVALID), (dict(q_out=AT[6]), INVALID), (dict(q_out=AT[7]), INVALID),
+    (dict(q_out_stride=(512, 0)), INVALID)])
+def test_append4_refuses(L, bad, want):
+    assert _append(_cache4(), **bad) == want
+
+
+@pytest.mark.parametrize("bad", [
+    dict(v=AT[0]), dict(v_scale=AT[2]), dict(k_scale=AT[0]), dict(v=AT[2]), dict(k_stride=(2048, 0, 64)),
+    dict(v_stride=(0, 512, 32)), dict(k_scale_stride=(128, 64, 0)), dict(v_scale_stride=(0, 32, 2))])
+def test_pools_that_share_places_are_not_written(L, bad):
+    assert _append(_cache4(**bad)) == INVALID
+    assert _evict(_cache4(**bad)) == INVALID
+
+
+def test_append4_refuses_a_wide_rotation(L):
+    s = binding.AttnRopeSpec(FAKE, 130, 0, 1.0)
+    assert _append(_cache4(), ctypes.byref(s)) == INVALID
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(Hq=-1), INVALID), (dict(Hq=3), INVALID), (dict(q=None), INVALID), (dict(qs=None), INVALID),
+    (dict(o=None), INVALID), (dict(lse=None), INVALID), (dict(ws=None), INVALID), (dict(scale=0.0), INVALID),
+    (dict(scale=-1.0), INVALID), (dict(scale=math.inf), INVALID), (dict(q=FAKE + 8), MISALIGNED),
+    (dict(qs=(512, 132)), MISALIGNED), (dict(o=FAKE + 8), MISALIGNED), (dict(lse=FAKE + 2), MISALIGNED),
+    (dict(ws=FAKE + 8), MISALIGNED)])
+def test_decode4_refuses(L, bad, want):
+    assert _decode(_cache4(), **bad) == want
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("bad,want", [
+    (dict(T=-1), INVALID), (dict(T=1 << 31), INVALID), (dict(offsets=None), INVALID), (dict(k=None), INVALID),
+    (dict(v=None), INVALID), (dict(ks=None), INVALID), (dict(vs=None), INVALID), (dict(k=FAKE + 8), MISALIGNED),
+    (dict(v=FAKE + 2), MISALIGNED), (dict(ks=(640, 132)), MISALIGNED), (dict(offsets=FAKE + 2), MISALIGNED),
+    (dict(ks=(0, 128)), INVALID), (dict(vs=(640, 0)), INVALID), (dict(k=AT[8]), INVALID), (dict(k=AT[0]), INVALID),
+    (dict(v=AT[1]), INVALID)])
+def test_gather_refuses(L, four, bad, want):
+    assert _gather(_cache4() if four else _cache16(), four=four, **bad) == want
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("bad,want", [
+    (dict(Hq=-1), INVALID), (dict(Hq=3), INVALID), (dict(q=None), INVALID), (dict(qs=None), INVALID),
+    (dict(weight=False), INVALID), (dict(lse=None), INVALID), (dict(out=None), INVALID), (dict(scale=0.0), INVALID),
+    (dict(decay=-0.5), INVALID), (dict(decay=1.5), INVALID), (dict(decay=math.nan), INVALID), (dict(q=FAKE + 8), MISALIGNED),
+    (dict(lse=FAKE + 2), MISALIGNED), (dict(w=FAKE + 2), MISALIGNED), (dict(out=FAKE + 1), MISALIGNED),
+    (dict(out_stride=(0, 64)), INVALID), (dict(out_stride=(128, 0)), INVALID), (dict(out_stride=(256, 64)), INVALID)])
+def test_weights_refuses(L, four, bad, want):
+    assert _weights(_cache4() if four else _cache16(), four=four, **bad) == want
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("bad,want", [
+    (dict(eviction=False), INVALID), (dict(sinks=-1), INVALID), (dict(recent=-1), INVALID), (dict(n_new=-1), INVALID),
+    (dict(n_new=5), INVALID), (dict(w=None), INVALID), (dict(w_out=None), INVALID), (dict(pages=None), INVALID),
+    (dict(table_out=None), INVALID), (dict(lens_out=None), INVALID), (dict(ws=None), INVALID), (dict(n=255), INVALID),
+    (dict(w=FAKE + 2), MISALIGNED), (dict(w_out=FAKE + 1), MISALIGNED), (dict(keep=FAKE + 2), MISALIGNED),
+    (dict(pages=FAKE + 2), MISALIGNED), (dict(table_out=FAKE + 2), MISALIGNED), (dict(lens_out=FAKE + 2), MISALIGNED),
+    (dict(ws=FAKE + 8), MISALIGNED), (dict(w_out=AT[6]), INVALID), (dict(w_out_stride=(0, 64)), INVALID),
+    (dict(table_out=AT[4]), INVALID), (dict(lens_out=AT[5]), INVALID), (dict(table_out=AT[8]), INVALID),
+    (dict(table_out=AT[10]), INVALID), (dict(table_out_stride=0), INVALID), (dict(keep=AT[10]), INVALID)])
+def test_evict_refuses(L, four, bad, want):
+    assert _evict(_cache4() if four else _cache16(), four=four, **bad) == want
+
+
+def test_evict_does_not_write_16_bit_pools_that_share_places(L):
+    assert _evict(_cache16(k_stride=(2048, 0, 64)), four=False) == INVALID
+    assert _evict(_cache16(v_stride=(0, 1024, 64)), four=False) == INVALID
+
+
+def test_evict_workspace(L):
+    assert L.attn_paged_evict_workspace(3, 2, 16, 5) == 4 * 3 * 2 * 80
+    assert L.attn_paged_evict_workspace(1, 1, 1, 0) == 0
+    assert L.attn_paged_evict_workspace(-1, 1, 1, 1) == 0
+    assert L.attn_paged_evict_workspace(1, 1, 0x7FFFFFFF, 0x7FFFFFFF) == 4 << 30
+
+
+def test_empty_calls_touch_nothing(L):
+    none = _cache4(B=0, seq_lens=None)
+    assert _append(none, T=0, k=None) == 0 and _append(_cache4(), T=0, offsets=FAKE, k=None) == 0
+    assert _decode(none, q=None, o=None) == 0 and _decode(_cache4(), Hq=0, q=None, o=None) == 0
+    assert _gather(none, offsets=None) == 0 and _gather(_cache4(), T=0, k=None) == 0
+    assert _weights(none, out=None) == 0 and _weights(_cache4(max_pages=0, page_table=None), out=None) == 0
+    assert _evict(none, w=None) == 0
+    none = _cache16(B=0, seq_lens=None)
+    assert _gather(none, offsets=None, four=False) == 0 and _evict(none, four=False, w=None) == 0
+
+
+def test_binding_refuses_cpu_tensors():
+    z, s = torch.zeros(1, 1, 16, 32, dtype=torch.uint8), torch.zeros(1, 1, 16, 2, 1, dtype=torch.float16)
+    i = torch.zeros(1, 1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        binding.PagedCache4(z, z, s, s, i, i[0])
+    with pytest.raises(TypeError):
+        binding.PagedCache4(z.half(), z, s, s, i, i[0])
+    with pytest.raises(TypeError):
+        binding.PagedCache4(z, z, s, s, i, i[0], dtype=torch.float32)
+
+
+def test_abi_from_c(tmp_path):
+    """A C99 caller through attn_cache.h; it prints its failed checks."""
+    build.build()
+    exe = tmp_path / "cache_from_c"
+    libdir = os.path.dirname(build.LIB_PATH)
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"),
+                    os.path.join(ROOT, "tests", "c", "cache_from_c.c"), "-o", str(exe), "-L", libdir, "-lattn_jvp",
+                    f"-Wl,-rpath,{libdir}", "-lm"], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
