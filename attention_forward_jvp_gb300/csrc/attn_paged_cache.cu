@@ -11,13 +11,16 @@
 
 namespace attn {
 
-#define ATTN_DECODE4_DECL(DQ)                                                                 \
-  extern template cudaError_t launch_decode4<DQ, 64>(Decode4Params&, int, int, cudaStream_t);  \
-  extern template cudaError_t launch_decode4<DQ, 128>(Decode4Params&, int, int, cudaStream_t); \
-  extern template cudaError_t launch_decode4<DQ, 256>(Decode4Params&, int, int, cudaStream_t);
-ATTN_DECODE4_DECL(64)
-ATTN_DECODE4_DECL(128)
-ATTN_DECODE4_DECL(256)
+#define ATTN_DECODE4_DECL(DQ, F16)                                                                 \
+  extern template cudaError_t launch_decode4<DQ, 64, F16>(Decode4Params&, int, int, cudaStream_t);  \
+  extern template cudaError_t launch_decode4<DQ, 128, F16>(Decode4Params&, int, int, cudaStream_t); \
+  extern template cudaError_t launch_decode4<DQ, 256, F16>(Decode4Params&, int, int, cudaStream_t);
+ATTN_DECODE4_DECL(64, false)
+ATTN_DECODE4_DECL(128, false)
+ATTN_DECODE4_DECL(256, false)
+ATTN_DECODE4_DECL(64, true)
+ATTN_DECODE4_DECL(128, true)
+ATTN_DECODE4_DECL(256, true)
 
 namespace {
 
@@ -33,6 +36,14 @@ bool take_pool(void* codes, void* scales, const int64_t* st, const int64_t* ss, 
   const int row = 2 * groups4(D);
   bool ok = aligned16(codes) && aligned(scales, 2 * row);
   for (int i = 0; i < 3; ++i) ok = ok && out->st[i] % 16 == 0 && out->ss[i] % row == 0;
+  return ok;
+}
+
+// Whether its strides fit 32 bits
+bool narrow(const Pool4& p) {
+  bool ok = true;
+  for (int i = 0; i < 3; ++i)
+    ok = ok && p.st[i] >= 0 && p.st[i] <= 0x7fffffffLL && p.ss[i] >= 0 && p.ss[i] <= 0x7fffffffLL;
   return ok;
 }
 
@@ -86,6 +97,7 @@ void take_cache(const C* c, const Device& d, DecodeParams* p) {
   for (int s = 0; s < 31; ++s)
     if (c->page_size == 1 << s) p->page_shift = s;
   p->capacity = capacity_of(c, c->max_pages);
+  p->whole = c->page_size % 16 == 0 ? 1 : 0;
   p->Hkv = c->Hkv;
   p->dqk = c->Dqk;
   p->dv = c->Dv;
@@ -192,18 +204,19 @@ Layout4 layout4_of(const attn_paged_cache4* c, int Hq, int sms) {
   return l;
 }
 
+template <bool F16>
 cudaError_t dispatch_decode4(const Layout4& l, Decode4Params& p, int ctas, cudaStream_t s) {
   const int nt = (l.rows + 7) / 8;
   switch (l.dq * 1000 + l.dv) {
-    case 64064: return launch_decode4<64, 64>(p, nt, ctas, s);
-    case 64128: return launch_decode4<64, 128>(p, nt, ctas, s);
-    case 64256: return launch_decode4<64, 256>(p, nt, ctas, s);
-    case 128064: return launch_decode4<128, 64>(p, nt, ctas, s);
-    case 128128: return launch_decode4<128, 128>(p, nt, ctas, s);
-    case 128256: return launch_decode4<128, 256>(p, nt, ctas, s);
-    case 256064: return launch_decode4<256, 64>(p, nt, ctas, s);
-    case 256128: return launch_decode4<256, 128>(p, nt, ctas, s);
-    case 256256: return launch_decode4<256, 256>(p, nt, ctas, s);
+    case 64064: return launch_decode4<64, 64, F16>(p, nt, ctas, s);
+    case 64128: return launch_decode4<64, 128, F16>(p, nt, ctas, s);
+    case 64256: return launch_decode4<64, 256, F16>(p, nt, ctas, s);
+    case 128064: return launch_decode4<128, 64, F16>(p, nt, ctas, s);
+    case 128128: return launch_decode4<128, 128, F16>(p, nt, ctas, s);
+    case 128256: return launch_decode4<128, 256, F16>(p, nt, ctas, s);
+    case 256064: return launch_decode4<256, 64, F16>(p, nt, ctas, s);
+    case 256128: return launch_decode4<256, 128, F16>(p, nt, ctas, s);
+    case 256256: return launch_decode4<256, 256, F16>(p, nt, ctas, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -231,7 +244,7 @@ attn_status run_decode4(const attn_paged_cache4* c, int32_t Hq, const void* q, c
   if (workspace_bytes < l.total) return ATTN_ERR_INVALID_ARG;
   if (static_cast<int64_t>(c->Hkv) * l.chunks > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   take_cache(c, d, &p);
-  p4.f16 = f16 ? 1 : 0;
+  p4.narrow = p.whole && narrow(p4.k) && narrow(p4.v) && c->Dqk >= 64 && c->Dv >= 64 ? 1 : 0;
   p.q = static_cast<const uint16_t*>(q);
   p.G = Hq / c->Hkv;
   p.rows = l.rows;
@@ -245,7 +258,9 @@ attn_status run_decode4(const attn_paged_cache4* c, int32_t Hq, const void* q, c
   p.split = p.capacity > kDecode4BN ? 1 : 0;
   const double steps = (p.capacity / kDecode4BN + 1.0) * p.B * p.Hkv * p.chunks;
   p.wide = steps + d.sms * kDecodeMaxWarps < 2147483648.0 ? 0 : 1;
-  if (dispatch_decode4(l, p4, d.sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
+  const cudaError_t e = f16 ? dispatch_decode4<true>(l, p4, d.sms, static_cast<cudaStream_t>(stream))
+                            : dispatch_decode4<false>(l, p4, d.sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return ATTN_ERR_CUDA;
   count_launch(1 + p.split);
   return ATTN_OK;
 }
@@ -323,7 +338,7 @@ attn_status run_weights(const C* c, WeightParams& p, int bits, int32_t Hq, const
   p.d.G = Hq / c->Hkv;
   p.d.rows = p.d.G;
   p.d.chunks = 1;
-  p.d.whole = c->page_size % kDecodeBN == 0 ? 1 : 0;
+  p.narrow = bits == 4 && p.d.whole && narrow(p.k) && c->Dqk >= 64 ? 1 : 0;
   p.f16 = f16 ? 1 : 0;
   p.lse = w->lse;
   p.w = w->w;

@@ -54,18 +54,19 @@ constexpr int decode4_rows(int dv) { return dv == 64 ? 32 : (dv == 128 ? 24 : 16
 struct Decode4Params {
   DecodeParams d;  // (its 16-bit pools unused)
   Pool4 k, v;
-  int f16;         // the type of q and o
+  int narrow;      // copy_tokens4
 };
 
 // The decode kernel over a cache in 4 bits for kernel head dims DQ, DV and nt
 // groups of 8 query heads to a unit, followed, when p.d.split, by the join
-template <int DQ, int DV>
+template <int DQ, int DV, bool F16>
 cudaError_t launch_decode4(Decode4Params& p, int nt, int ctas, cudaStream_t stream);
 
 // ----------------------------------------------------------------- weights
 struct WeightParams {
   DecodeParams d;     // (no values, workspace or outputs)
   Pool4 k;            // of a cache in 4 bits
+  int narrow;         // copy_tokens4
   int f16;            // the type of q
   const float* lse;   // [B, Hkv * G]
   const float* w;     // or null

@@ -13,7 +13,9 @@
 // its own, the sums of P m and P s, and of P as it was rounded, from another
 // (a row each).  P is rounded to fp16 once and O normalised by the sum of the
 // rounded P, so that this rounding costs only where keys differ; the LSE takes
-// the sum in fp32.
+// the sum in fp32.  That is a quarter of what rounding O to bf16 costs.  Beside
+// the rounding to fp16 it would tell, so there P and P s are multiplied in two
+// parts each (22 bits), n as it is, and nothing is left to correct.
 //
 // P s must not pass 65504: the reference of the probabilities lies 11 below
 // the maximum and P goes up to 2^15 (DecodeReference), less as many powers of
@@ -37,7 +39,7 @@ struct Decode4Plan {
   static constexpr int MISC_BYTES = (8 * 32 + 16 + 24 + sizeof(DecodeRange)) * kDecodeMaxWarps;
   static constexpr int FIT = 226 * 1024 - MISC_BYTES;
   // O, its corrections and statistics; Q
-  static constexpr int REGS = (DV / 4 + 4 * GV + 4) * NT + (DQ / 8 + 4) * NT + 80;
+  static constexpr int REGS = (DV / 4 + 4 * GV + 4) * NT + (DQ / 8 + 4) * NT + 64;
   static constexpr int NW_REGS = REGS <= 128 ? 16 : (REGS <= 160 ? 12 : 8);
   static constexpr int S = FIT / NW_REGS / STAGE >= 4 ? 4 : (FIT / NW_REGS / STAGE >= 3 ? 3 : 2);
   static constexpr int PITCH = DV + 4;
@@ -51,7 +53,7 @@ struct Decode4Plan {
   static constexpr int SMEM = NW * WARP_BYTES + MISC_BYTES;
 };
 
-template <int DQ, int DV, int NT>
+template <int DQ, int DV, bool F16, int NT>
 __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
     attn_paged_decode4_kernel(const __grid_constant__ Decode4Params p4) {
   using P = Decode4Plan<DQ, DV, NT>;
@@ -120,23 +122,24 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
   if (lane == 0) ranges[warp] = w;
 
   float acc[NT][GV][4][4];  // [64 columns][product]: columns 8 g + 2 i of heads 2 t, 2 t + 1, then 8 g + 2 i + 1 (16-fold)
-  float eight[NT][GV][4];   // sum P' 8, the same in every row
-  float stat[NT][4];        // rows 0 .. GV - 1: sum P m, 4: sum P; rows 8 ..: sum P s
+  float eight[F16 ? 1 : NT][F16 ? 1 : GV][4];  // sum P' 8, the same in every row (bf16)
+  float stat[NT][4];        // rows 0 .. GV - 1: sum P m, 4: sum P; rows 8 ..: sum P s (of no use in fp16)
   float m[NT][2], l[NT][2];
   Query4<DQ, NT> q;
   int top = 0;              // the steps of the values seen are at most 2^top
+  constexpr float kNone = -3.402823466e38f;  // below every score: the first one moves the reference
   auto clear = [&]() {
     top = 0;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = kNone;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         stat[n][e] = 0.f;
 #pragma unroll
         for (int b = 0; b < GV; ++b) {
-          eight[n][b][e] = 0.f;
+          if constexpr (!F16) eight[n][b][e] = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[n][b][i][e] = 0.f;
         }
@@ -146,12 +149,10 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
   auto load_q = [&](const Cursor& a) {
     const int h = a.hu / p.chunks, g0 = (a.hu - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
     const uint16_t* base = p.q + a.b * p.qs[0] + (static_cast<long long>(h) * p.G + g0) * p.qs[1];
-    if (p4.f16) q.template load<true>(base, p.qs[1], n_rows, p.dqk, p.scale_log2);
-    else q.template load<false>(base, p.qs[1], n_rows, p.dqk, p.scale_log2);
+    q.template load<F16>(base, p.qs[1], n_rows, p.dqk, p.scale_log2);
   };
   auto write_row = [&](long long row, int col, float4 o, float mm, float ll) {
-    if (p4.f16) decode_write_row<true>(p, row, col, o, mm, ll);
-    else decode_write_row<false>(p, row, col, o, mm, ll);
+    decode_write_row<F16>(p, row, col, o, mm, ll);
   };
   // l over the lanes; O of group n from its sums, times l by the sum of the
   // rounded P, to [head][DV] in shared memory
@@ -162,20 +163,26 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(ALL, l[n][e], o);
       const float sum = __shfl_sync(ALL, stat[n][e], 16 + t);
-      f[e] = sum == 0.f ? 0.f : l[n][e] / sum;
+      f[e] = F16 ? 1.f : (sum == 0.f ? 0.f : l[n][e] / sum);
     }
 #pragma unroll
     for (int b = 0; b < GV; ++b) {
-      float base[2];
+      float base[2], less[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        base[e] = __shfl_sync(ALL, stat[n][e], 4 * b + t) + 8.f * __shfl_sync(ALL, stat[n][2 + e], 4 * b + t);
+      for (int e = 0; e < 2; ++e) {
+        base[e] = __shfl_sync(ALL, stat[n][e], 4 * b + t);
+        less[e] = 0.f;
+        if constexpr (!F16) {
+          base[e] += 8.f * __shfl_sync(ALL, stat[n][2 + e], 4 * b + t);
+          less[e] = eight[n][b][e];
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float x = (acc[n][b][i][e] - eight[n][b][e]) * 16777216.f + base[e];
-          const float y = (acc[n][b][i][2 + e] * 0.0625f - eight[n][b][e]) * 16777216.f + base[e];
+          const float x = (acc[n][b][i][e] - less[e]) * 16777216.f + base[e];
+          const float y = (acc[n][b][i][2 + e] * 0.0625f - less[e]) * 16777216.f + base[e];
           *reinterpret_cast<float2*>(to + (2 * t + e) * PITCH + 64 * b + 8 * g + 2 * i) = make_float2(x * f[e], y * f[e]);
         }
     }
@@ -183,11 +190,18 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
 
   clear();
   if (count > 0) {
-    auto issue = [&](Place4& x, int stage) {
+    auto issue = [&](const Place4& x, int stage) {
       const uint32_t to = ring + stage * P::STAGE;
-      report4(p, x);
-      copy_rows4<DQ, true>(p4.k, x, p.dqk, to, to + P::K_BYTES + P::V_BYTES);
-      copy_rows4<DV, false>(p4.v, x, p.dv, to + P::K_BYTES, to + P::K_BYTES + P::V_BYTES + P::KS_BYTES);
+      const uint32_t tv = to + P::K_BYTES, ks = tv + P::V_BYTES, vs = ks + P::KS_BYTES;
+      copy_tokens4(p, p4.narrow, x, [&](auto whole, const Place4& y, bool live) {
+        if constexpr (decltype(whole)::value) {
+          copy_rows4_whole<DQ, true>(p4.k, y, to, ks);
+          copy_rows4_whole<DV, false>(p4.v, y, tv, vs);
+        } else {
+          copy_rows4<DQ, true>(p4.k, y, live, p.dqk, to, ks);
+          copy_rows4<DV, false>(p4.v, y, live, p.dv, tv, vs);
+        }
+      });
     };
     load_q(cur);
 #pragma unroll
@@ -218,32 +232,53 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
       float s[2][NT][4];
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) scores4<DQ, NT>(q, sk, sks, 16 * kt, s[kt]);
-      // the largest step of the values of key `lane`
-      uint32_t steps[GV];
-      lds_row<GV>(svs + lane * (4 * GV), steps);
-      float most = fabsf(half_at<GV>(steps, 0));
+      // S' - m, and whether one passes the room above the reference, or a step
+      // of the values of key `lane` the largest so far
+      bool grows = false;
+      {
+        uint32_t steps[GV];
+        lds_row<GV>(svs + lane * (4 * GV), steps);
+        const uint32_t most = 0x3c003c00u + top * 0x04000400u;  // 2^top
+        if constexpr (GV == 1) grows = above_half2(steps[0] & 0xffffu, most);
+        if constexpr (GV >= 2) grows = above_half2(steps[0], most);
+        if constexpr (GV == 4) grows = grows || above_half2(steps[1], most);
+      }
+      if (live < BN) {
 #pragma unroll
-      for (int b = 1; b < GV; ++b) most = fmaxf(most, fabsf(half_at<GV>(steps, b)));
-      bool grows = most > __int_as_float((127 + top) << 23);
-      float room = DecodeReference<true>::room - top;
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (16 * kt + g + (e >> 1) * 8 >= live) s[kt][n][e] = -INFINITY;
+      }
+      float y[2][NT][4];
+      auto less_m = [&]() {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[kt][n][e] = fmaf(s[kt][n][e], q.scale[n][e & 1], -m[n][e & 1]);
+      };
+      less_m();
+      const float room = DecodeReference<true>::room - top;
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float& x = s[kt][n][e];
-            x *= q.scale[n][e & 1];
-            if (16 * kt + g + (e >> 1) * 8 >= live) x = -INFINITY;
-            grows = grows || x > m[n][e & 1] + room;
-          }
+          for (int e = 0; e < 4; ++e) grows = grows || y[kt][n][e] > room;
       if (__any_sync(ALL, grows)) {
+        uint32_t steps[GV];
+        lds_row<GV>(svs + lane * (4 * GV), steps);
+        float most = fabsf(half_at<GV>(steps, 0));
+#pragma unroll
+        for (int b = 1; b < GV; ++b) most = fmaxf(most, fabsf(half_at<GV>(steps, b)));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(ALL, most, o));
-        // (2^-126 .. 2^16: the exponent above the step's, none of an infinite one)
-        const int up = (__float_as_int(most) >> 23) - 126;
-        top = most > __int_as_float((127 + top) << 23) ? min(up, 16) : top;
-        room = DecodeReference<true>::room - top;
+        // (the exponent above the step's; fp16 has none above 16, infinity apart)
+        top = most > __int_as_float((127 + top) << 23) ? min((__float_as_int(most) >> 23) - 126, 16) : top;
         const float below = DecodeReference<true>::below - top;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -253,16 +288,18 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
             x = fmaxf(x, __shfl_xor_sync(ALL, x, 4));
             x = fmaxf(x, __shfl_xor_sync(ALL, x, 8));
             x = fmaxf(x, __shfl_xor_sync(ALL, x, 16));
-            x = fmaxf(x - below, m[n][e]);
-            const float a = exp2_fast(m[n][e] - (x == -INFINITY ? 0.f : x));
+            x = fmaxf(x * q.scale[n][e] - below, m[n][e]);
+            const float a = exp2_fast(m[n][e] - x);
             m[n][e] = x;
             l[n][e] *= a;
             stat[n][e] *= a;
             stat[n][2 + e] *= a;
 #pragma unroll
             for (int b = 0; b < GV; ++b) {
-              eight[n][b][e] *= a;
-              eight[n][b][2 + e] *= a;
+              if constexpr (!F16) {
+                eight[n][b][e] *= a;
+                eight[n][b][2 + e] *= a;
+              }
 #pragma unroll
               for (int d = 0; d < 4; ++d) {
                 acc[n][b][d][e] *= a;
@@ -270,61 +307,74 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
               }
             }
           }
+        less_m();
       }
-      uint32_t ph[2][NT][2];
+      uint32_t ph[2][NT][2], pl[F16 ? 2 : 1][F16 ? NT : 1][2];  // P, and what rounding left of it
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        // a head whose scores are all -inf keeps weights of 0
-        const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0], u1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float a = exp2_fast(s[kt][n][2 * e] - u0), b = exp2_fast(s[kt][n][2 * e + 1] - u1);
+            const float a = exp2_fast(y[kt][n][2 * e]), b = exp2_fast(y[kt][n][2 * e + 1]);
             l[n][0] += a;
             l[n][1] += b;
-            ph[kt][n][e] = movmatrix_t(pack2<true>(a, b));
+            if constexpr (F16) {
+              split2<true>(a, b, ph[kt][n][e], pl[kt][n][e]);
+              pl[kt][n][e] = movmatrix_t(pl[kt][n][e]);
+            } else {
+              ph[kt][n][e] = pack2<true>(a, b);
+            }
+            ph[kt][n][e] = movmatrix_t(ph[kt][n][e]);
           }
-      }
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
         // the steps and least values of keys 2 t, 2 t + 1 and 8 further on
         uint32_t step[GV][2], a[4];
-        {
-          uint32_t row[2][2][GV];
 #pragma unroll
-          for (int o = 0; o < 2; ++o)
+        for (int o = 0; o < 2; ++o) {
+          uint32_t row[2][GV];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) lds_row<GV>(svs + (16 * kt + 8 * o + 2 * t + e) * (4 * GV), row[o][e]);
-          // half i of both keys' rows
-          auto both = [&](int o, int i) {
-            return __byte_perm(row[o][0][i >> 1], row[o][1][i >> 1], i & 1 ? 0x7632 : 0x5410);
-          };
+          for (int e = 0; e < 2; ++e) lds_row<GV>(svs + (16 * kt + 8 * o + 2 * t + e) * (4 * GV), row[e]);
 #pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            uint32_t least = 0u, each = 0u;
-#pragma unroll
-            for (int b = 0; b < GV; ++b) {
-              step[b][o] = both(o, b);
-              const uint32_t x = both(o, GV + b);
-              least = g == b ? x : least;
-              each = g == b ? step[b][o] : each;
-            }
-            a[2 * o] = g == 4 ? 0x3c003c00u : least;  // row 4: ones
-            a[2 * o + 1] = each;
+          for (int b = 0; b < GV; ++b)
+            step[b][o] = __byte_perm(row[0][b >> 1], row[1][b >> 1], b & 1 ? 0x7632 : 0x5410);
+          // row g of the statistics' operand: the least values of group g, ones in row 4; row g + 8: its steps.
+          // (What stands in the other rows is of no use.)
+          uint32_t least, each;
+          if constexpr (GV == 1) {
+            least = __byte_perm(row[0][0], row[1][0], 0x7632);
+            each = step[0][o];
+          } else {
+            const int half = g & 1 ? 0x7632 : 0x5410;
+            const uint32_t m0 = GV == 4 && (g & 2) ? row[0][GV - 1] : row[0][GV / 2];
+            const uint32_t m1 = GV == 4 && (g & 2) ? row[1][GV - 1] : row[1][GV / 2];
+            least = __byte_perm(m0, m1, half);
+            each = g & 1 ? step[1][o] : step[0][o];
+            if constexpr (GV == 4) each = g & 2 ? (g & 1 ? step[GV - 1][o] : step[GV - 2][o]) : each;
           }
+          a[2 * o] = g == 4 ? 0x3c003c00u : least;
+          a[2 * o + 1] = F16 ? 0u : each;
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816<true>(stat[n], a, ph[kt][n][0], ph[kt][n][1]);
+        for (int n = 0; n < NT; ++n) {
+          mma16816<true>(stat[n], a, ph[kt][n][0], ph[kt][n][1]);
+          if constexpr (F16) mma16816<true>(stat[n], a, pl[kt][n][0], pl[kt][n][1]);
+        }
 #pragma unroll
         for (int b = 0; b < GV; ++b) {
-          uint32_t ps[NT][2];
+          uint32_t ps[NT][2], less[F16 ? NT : 1][2];
           const uint32_t eights[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};  // 8 2^-24
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            ps[n][0] = mul_half2(ph[kt][n][0], step[b][0]);
-            ps[n][1] = mul_half2(ph[kt][n][1], step[b][1]);
-            mma16816<true>(eight[n][b], eights, ps[n][0], ps[n][1]);
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              ps[n][o] = mul_half2(ph[kt][n][o], step[b][o]);
+              if constexpr (F16)  // (the product's rounding is exact in fp16)
+                less[n][o] = fma_half2(pl[kt][n][o], step[b][o],
+                                       fma_half2(ph[kt][n][o], step[b][o], ps[n][o] ^ 0x80008000u));
+            }
+            if constexpr (!F16) mma16816<true>(eight[n][b], eights, ps[n][0], ps[n][1]);
           }
           uint32_t word[2][2];  // of keys 2 t + e, and 8 further on
 #pragma unroll
@@ -343,7 +393,10 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
             for (int i = 0; i < 2; ++i) {
               const uint32_t v[4] = {r[0][2 * i], r[0][2 * i + 1], r[1][2 * i], r[1][2 * i + 1]};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816<true>(acc[n][b][2 * c + i], v, ps[n][0], ps[n][1]);
+              for (int n = 0; n < NT; ++n) {
+                mma16816<true>(acc[n][b][2 * c + i], v, ps[n][0], ps[n][1]);
+                if constexpr (F16) mma16816<true>(acc[n][b][2 * c + i], v, less[n][0], less[n][1]);
+              }
             }
           }
         }
@@ -424,7 +477,7 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
   decode_join_held<DV, NW, P::WARP_BYTES, ROWS, PITCH>(p, ranges[warp], smem, held, held_end, write_row);
 }
 
-template <int DQ, int DV, int NT>
+template <int DQ, int DV, bool F16, int NT>
 cudaError_t launch_decode4_nt(Decode4Params& p, int ctas, cudaStream_t stream) {
   using P = Decode4Plan<DQ, DV, NT>;
   static bool attr_done[64] = {};
@@ -433,33 +486,29 @@ cudaError_t launch_decode4_nt(Decode4Params& p, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(attn_paged_decode4_kernel<DQ, DV, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
-    // (as in launch_decode_nt)
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attn_decode_join<DV, false>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attn_decode_join<DV, true>, cudaFuncAttributePreferredSharedMemoryCarveout,
+    e = cudaFuncSetAttribute(attn_paged_decode4_kernel<DQ, DV, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             P::SMEM);
+    if (e == cudaSuccess)  // (as in launch_decode_nt)
+      e = cudaFuncSetAttribute(attn_decode_join<DV, F16>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
   p.d.cta_warps = P::NW;
   plan_join(p.d, ctas);
-  e = decode_launch_one(attn_paged_decode4_kernel<DQ, DV, NT>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
-  if (e != cudaSuccess || !p.d.split) return e;
-  return p.f16 ? launch_join<DV, true>(p.d, ctas, stream) : launch_join<DV, false>(p.d, ctas, stream);
+  e = decode_launch_one(attn_paged_decode4_kernel<DQ, DV, F16, NT>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
+  return e != cudaSuccess || !p.d.split ? e : launch_join<DV, F16>(p.d, ctas, stream);
 }
 
-template <int DQ, int DV>
+template <int DQ, int DV, bool F16>
 cudaError_t launch_decode4(Decode4Params& p, int nt, int ctas, cudaStream_t stream) {
   constexpr int MOST = decode4_rows(DV) / 8;
-  if (nt == 1) return launch_decode4_nt<DQ, DV, 1>(p, ctas, stream);
-  if (nt == 2) return launch_decode4_nt<DQ, DV, 2>(p, ctas, stream);
+  if (nt == 1) return launch_decode4_nt<DQ, DV, F16, 1>(p, ctas, stream);
+  if (nt == 2) return launch_decode4_nt<DQ, DV, F16, 2>(p, ctas, stream);
   if constexpr (MOST >= 3)
-    if (nt == 3) return launch_decode4_nt<DQ, DV, 3>(p, ctas, stream);
+    if (nt == 3) return launch_decode4_nt<DQ, DV, F16, 3>(p, ctas, stream);
   if constexpr (MOST >= 4)
-    if (nt == 4) return launch_decode4_nt<DQ, DV, 4>(p, ctas, stream);
+    if (nt == 4) return launch_decode4_nt<DQ, DV, F16, 4>(p, ctas, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -10,6 +10,8 @@
 // same of x >> 8 gives (2, 6) and (3, 7).  Two and a half instructions for
 // four elements.
 #pragma once
+#include <type_traits>
+
 #include "attn_decode_kernel.cuh"
 #include "attn_paged_cache_kernels.h"
 
@@ -63,6 +65,17 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// whether a half of w is larger than that of `most`, regardless of signs
+__device__ __forceinline__ bool above_half2(uint32_t w, uint32_t most) {
+  uint32_t d;
+  asm("set.gt.u32.f16x2 %0, %1, %2;" : "=r"(d) : "r"(w & 0x7fff7fffu), "r"(most));
+  return d != 0u;
+}
 
 // the four operands of a word of eight elements, as above
 __device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&r)[4]) {
@@ -91,54 +104,93 @@ __device__ __forceinline__ uint32_t value_slot(int key, int slot) {
   return D == 256 ? slot ^ (key >> 1 & 3) : (D == 128 ? slot ^ (key >> 2 & 1) : slot);
 }
 
-// 32 neighbouring tokens of a sequence: lane r has the page and slot of token
-// r, and whether it is live (within the length, its page within the pool).
+// 32 neighbouring tokens of a sequence, from `first` on, n of them or more
+// live.  Where pages hold a multiple of 16 tokens (`whole`) each half of them
+// lies in one page, and a lane has the page and slot of the first token of its
+// half; else those of token `lane`.
 struct Place4 {
-  int page, slot, h;
-  bool live;
+  int page, slot, h, n;
 };
 __device__ __forceinline__ Place4 lookup4(const DecodeParams& p, const int* pages, int first, int len, int h) {
   Place4 x;
-  const int key = first + (threadIdx.x & 31);
+  const int key = first + (threadIdx.x & (p.whole ? 16 : 31));
   x.page = x.slot = 0;
   x.h = h;
-  x.live = key < len;
-  if (x.live) {
+  x.n = len - first;
+  if (key < len) {
     const int e = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
     x.slot = key - e * p.page_size;
     x.page = pages[e];
   }
   return x;
 }
-// Tells of a page out of range, whose rows become zeros (apart from the
-// look-up, whose load is on its way)
-__device__ __forceinline__ void report4(const DecodeParams& p, Place4& x) {
-  if (static_cast<unsigned>(x.page) >= static_cast<unsigned>(p.n_pages)) {
-    if (x.live) *p.err = 1;
-    x.live = false;
-  }
-}
 
-// Their rows of D elements (d of them real) into a tile by a warp, and their
-// steps and least values behind one another.  KEYS: laid out as keys.
+// The rows of D elements (d of them real) of those tokens into a tile by a
+// warp, 16 bytes a lane, and their steps and least values behind one another.
+// KEYS: laid out as keys.  A half of the warp copies a half of the tokens.
+template <int D>
+struct Rows4 {
+  static constexpr int L = D / 32, R = 16 / L;  // lanes of a row, rows of an instruction in each half
+  static constexpr int N = 4 * groups4(D);      // bytes of a row's steps and least values
+};
 template <int D, bool KEYS>
-__device__ __forceinline__ void copy_rows4(const Pool4& pool, const Place4& x, int d, uint32_t to, uint32_t scales) {
-  constexpr int L = D / 32, R = 32 / L;  // 16-byte lanes of a row, rows of an instruction
-  const int lane = threadIdx.x & 31, lr = lane / L, c = lane % L;
-  const long long at = x.live ? x.page * pool.st[0] + x.h * pool.st[1] + x.slot * pool.st[2] : -1;
+__device__ __forceinline__ uint32_t row_place4(int i) {
+  using X = Rows4<D>;
+  const int lane = threadIdx.x & 31, lr = (lane & 15) / X::L, c = lane % X::L, key = (lane & 16) + i * X::R + lr;
+  return (KEYS ? key * (D / 2) + key_slot<D>(key, c >> 1) * 32
+               : value_row<D>(key) * (D / 2) + value_slot<D>(key, c >> 1) * 32) + (c & 1) * 16;
+}
+// all of them live, their halves in one page each, strides below 2^31
+template <int D, bool KEYS>
+__device__ __forceinline__ void copy_rows4_whole(const Pool4& pool, const Place4& x, uint32_t to, uint32_t scales) {
+  using X = Rows4<D>;
+  const int lane = threadIdx.x & 31, lr = (lane & 15) / X::L, c = lane % X::L;
+  const int s1 = static_cast<int>(pool.st[1]), s0 = static_cast<int>(pool.st[0]), s2 = static_cast<int>(pool.st[2]);
+  const uint8_t* from = pool.codes + static_cast<long long>(x.h) * s1 + static_cast<long long>(x.page) * s0 +
+                        static_cast<long long>(x.slot + lr) * s2 + 16 * c;
 #pragma unroll
-  for (int i = 0; i < L; ++i) {
-    const long long row = __shfl_sync(0xffffffffu, at, i * R + lr);
-    const int key = i * R + lr;
-    const bool live = row >= 0 && 32 * c < d;
-    const uint32_t place = KEYS ? key * (D / 2) + key_slot<D>(key, c >> 1) * 32
-                                : value_row<D>(key) * (D / 2) + value_slot<D>(key, c >> 1) * 32;
-    cp_async_n<16>(to + place + (c & 1) * 16, live ? pool.codes + row + 16 * c : pool.codes, live);
+  for (int i = 0; i < X::L; ++i) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + row_place4<D, KEYS>(i)), "l"(from) : "memory");
+    from += static_cast<long long>(X::R) * s2;
   }
-  constexpr int N = 4 * groups4(D);
-  cp_async_n<N>(scales + lane * N,
-                x.live ? pool.scales + x.page * pool.ss[0] + x.h * pool.ss[1] + x.slot * pool.ss[2] : pool.scales,
-                x.live);
+  const int t1 = static_cast<int>(pool.ss[1]), t0 = static_cast<int>(pool.ss[0]), t2 = static_cast<int>(pool.ss[2]);
+  cp_async_n<X::N>(scales + lane * X::N,
+                   pool.scales + (static_cast<long long>(x.h) * t1 + static_cast<long long>(x.page) * t0 +
+                                  static_cast<long long>(x.slot + (lane & 15)) * t2),
+                   true);
+}
+// in any case: x has the place of token `lane`; those that are not live become zeros
+template <int D, bool KEYS>
+__device__ __forceinline__ void copy_rows4(const Pool4& pool, const Place4& x, bool live, int d, uint32_t to,
+                                           uint32_t scales) {
+  using X = Rows4<D>;
+  const int lane = threadIdx.x & 31, lr = (lane & 15) / X::L, c = lane % X::L;
+  const long long at = live ? x.page * pool.st[0] + x.h * pool.st[1] + x.slot * pool.st[2] : -1;
+#pragma unroll
+  for (int i = 0; i < X::L; ++i) {
+    const long long row = __shfl_sync(0xffffffffu, at, (lane & 16) + i * X::R + lr);
+    const bool in = row >= 0 && 32 * c < d;
+    cp_async_n<16>(to + row_place4<D, KEYS>(i), in ? pool.codes + row + 16 * c : pool.codes, in);
+  }
+  cp_async_n<X::N>(scales + lane * X::N,
+                   live ? pool.scales + x.page * pool.ss[0] + x.h * pool.ss[1] + x.slot * pool.ss[2] : pool.scales, live);
+}
+// `copy` with what the places allow: (true, x, true) for copy_rows4_whole, else
+// (false, x of this lane's token, live) for copy_rows4.  Tells of a page out of
+// range, whose rows become zeros (apart from the look-up, whose load is on its
+// way).  narrow: pages of a multiple of 16 tokens, strides below 2^31, rows as
+// wide as the kernel's head dims.
+template <class Copy>
+__device__ __forceinline__ void copy_tokens4(const DecodeParams& p, bool narrow, Place4 x, Copy copy) {
+  const bool has = static_cast<unsigned>(x.page) < static_cast<unsigned>(p.n_pages);
+  const int lane = threadIdx.x & 31;
+  if (__all_sync(0xffffffffu, has && x.n >= 32) && narrow) {
+    copy(std::true_type(), x, true);
+  } else {
+    if (p.whole) x.slot += lane & 15;
+    if (lane < x.n && !has) *p.err = 1;
+    copy(std::false_type(), x, lane < x.n && has);
+  }
 }
 
 // Q^T of up to NT groups of 8 heads as the products' second operand, to go

@@ -98,8 +98,10 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
   auto issue = [&](Place& x, int stage) {
     const uint32_t to = ring + stage * P::STAGE;
     if constexpr (BITS == 4) {
-      report4(p, x);
-      copy_rows4<DQ, true>(pw.k, x, p.dqk, to, to + P::K_BYTES);
+      copy_tokens4(p, pw.narrow, x, [&](auto whole, const Place4& y, bool live) {
+        if constexpr (decltype(whole)::value) copy_rows4_whole<DQ, true>(pw.k, y, to, to + P::K_BYTES);
+        else copy_rows4<DQ, true>(pw.k, y, live, p.dqk, to, to + P::K_BYTES);
+      });
     } else {
       decode_report(p, p.whole, x);
       copy_rows<DQ, DQ * 2, 128>(p, p.whole, x, p.k + x.h * p.kp[1], p.kp, p.dqk, to);
