@@ -212,12 +212,11 @@ struct DecodeWords {
 // Thread x holds sequence x (and adds up those behind it, a block's width
 // apart): its length, and the steps up to it within its warp.  I: int where
 // no list of this shape can pass 2^31 steps, else long long.  BN: keys of a
-// step; NW: warps of a CTA, which has a range for each of them or one.
-template <class I, int BN, int NW, bool PER_WARP>
-__device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const DecodeWords& s) {
+// step; NW: warps of a CTA, which has R ranges, the warp's the one numbered own.
+template <class I, int BN, int NW>
+__device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const DecodeWords& s, int R, int own) {
   constexpr int THREADS = NW * 32;
   constexpr unsigned ALL = 0xffffffffu;
-  constexpr int R = PER_WARP ? NW : 1;  // ranges of a CTA
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const I HU = p.Hkv * p.chunks;
   auto length = [&](int b, bool& odd) {
@@ -268,7 +267,7 @@ __device__ __forceinline__ DecodeRange decode_plan(const DecodeParams& p, const 
   w.ranges = ranges;
   w.each = each;
   w.extra = total - each * ranges;
-  const int first = blockIdx.x * R, mine = first + (PER_WARP ? warp : 0);
+  const int first = blockIdx.x * R, mine = first + own;
   w.lo = w.start(mine);
   w.count = static_cast<int>(w.start(mine + 1) - w.lo);
   w.cta_lo = w.start(first);
@@ -338,9 +337,8 @@ static __device__ __noinline__ void decode_idle(const DecodeParams& p) {
 __device__ __forceinline__ void decode_complete(const DecodeParams& p, int b, int hu) {
   if (p.by_unit) p.desc[b * p.Hkv * p.chunks + hu] = make_int4(-1, 0, 0, 0);
 }
-template <int R>
-__device__ __forceinline__ void decode_describe(const DecodeParams& p, const DecodeRange& w, int b, int hu, int x,
-                                                long long end) {
+__device__ __forceinline__ void decode_describe(const DecodeParams& p, const DecodeRange& w, int R, int b, int hu,
+                                                int x, long long end) {
   const int z = static_cast<int>(w.owner(end)), c = x / R, e = z / R;
   const bool own = w.start(z + 1LL) != end + 1 && (e == c || z != e * R);
   if (p.by_unit) p.desc[b * p.Hkv * p.chunks + hu] = make_int4(x, 0, e - c - 1, own ? z : -1);
@@ -358,22 +356,21 @@ __device__ __forceinline__ void decode_write_row(const DecodeParams& p, long lon
   if (col == 0) p.lse[row] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
 }
 
-// What a CTA's warps hold of their last units: joined, and written by `write`
-// or to the workspace.  The parts of warp x lie at smem + x * WARP_BYTES: ROWS
-// rows of O, PITCH floats apart, then their (m, l).  held, held_end: of each
-// warp its unit (x, y), whether it begins there (z), whether it goes on from
-// the warp before (w), and the unit's last step.
-template <int DV, int NW, int WARP_BYTES, int ROWS, int PITCH, class Write>
-__device__ __forceinline__ void decode_join_held(const DecodeParams& p, const DecodeRange w, const char* smem,
-                                                 const int4* held, const long long* held_end, Write write) {
-  constexpr int THREADS = NW * 32;
-  const int tid = threadIdx.x, lane = tid & 31, first = blockIdx.x * NW;
-  // groups of warps with parts of one unit, by their first warps
-  const int used = static_cast<int>(min(static_cast<long long>(NW), w.ranges - first));  // warps with steps
+// What a CTA's R ranges hold of their last units: joined, and written by
+// `write` or to the workspace.  part(x, r): row r (of p.rows) of range x's O in
+// shared memory, stat(x, r) its (m, l).  held, held_end: of each range its unit
+// (x, y), whether it begins there (z), whether it goes on from the range before
+// (w), and the unit's last step.
+template <int DV, class Part, class Stat, class Write>
+__device__ __forceinline__ void decode_join_held(const DecodeParams& p, const DecodeRange w, int R, const int4* held,
+                                                 const long long* held_end, Part part_of, Stat stat_of, Write write) {
+  const int tid = threadIdx.x, lane = tid & 31, first = blockIdx.x * R;
+  // groups of ranges with parts of one unit, by their first ones
+  const int used = static_cast<int>(min(static_cast<long long>(R), w.ranges - first));  // ranges with steps
   const unsigned leads = __ballot_sync(0xffffffffu, lane < used && held[lane < used ? lane : 0].w == 0);
   const int items = p.rows * (DV / 4);
 #pragma unroll 1
-  for (int y = tid; y < __popc(leads) * items; y += THREADS) {
+  for (int y = tid; y < __popc(leads) * items; y += blockDim.x) {
     const int gi = y / items, r = (y - gi * items) / (DV / 4), c4 = y % (DV / 4);
     unsigned left = leads;
     for (int k = 0; k < gi; ++k) left &= left - 1;
@@ -388,15 +385,14 @@ __device__ __forceinline__ void decode_join_held(const DecodeParams& p, const De
     const long long part = 2LL * (first + w0) + (begins ? 1 : 0);
     float mm = -INFINITY, ll = 0.f;
     for (int x = w0; x < w1; ++x)
-      mm = fmaxf(mm, reinterpret_cast<const float2*>(smem + x * WARP_BYTES + ROWS * PITCH * 4)[r].x);
+      mm = fmaxf(mm, stat_of(x, r).x);
     const float top = mm == -INFINITY ? 0.f : mm;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int x = w0; x < w1; ++x) {
-      const char* from = smem + x * WARP_BYTES;
-      const float2 s = reinterpret_cast<const float2*>(from + ROWS * PITCH * 4)[r];
+      const float2 s = stat_of(x, r);
       const float f = exp2_fast(s.x - top);
-      const float4 z = *reinterpret_cast<const float4*>(from + (r * PITCH + 4 * c4) * 4);
+      const float4 z = *reinterpret_cast<const float4*>(part_of(x, r) + 4 * c4);
       ll = fmaf(f, s.y, ll);
       o.x = fmaf(f, z.x, o.x);
       o.y = fmaf(f, z.y, o.y);
@@ -409,7 +405,7 @@ __device__ __forceinline__ void decode_join_held(const DecodeParams& p, const De
     } else {
       *reinterpret_cast<float4*>(p.part_o + (part * p.rows + r) * DV + 4 * c4) = o;
       if (c4 == 0) p.part_ml[part * p.rows + r] = make_float2(mm, ll);
-      if (r == 0 && c4 == 0 && begins) decode_describe<NW>(p, w, u.x, u.y, first + w0, end);
+      if (r == 0 && c4 == 0 && begins) decode_describe(p, w, R, u.x, u.y, first + w0, end);
     }
   }
 }
@@ -506,7 +502,7 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
   // at once
   const int first = blockIdx.x * NW;  // this CTA's first warp
   const int me = first + warp;
-  DecodeRange w = p.wide ? decode_plan<long long, BN, NW, true>(p, words) : decode_plan<int, BN, NW, true>(p, words);
+  DecodeRange w = p.wide ? decode_plan<long long, BN, NW>(p, words, NW, warp) : decode_plan<int, BN, NW>(p, words, NW, warp);
   const int count = w.count;
   Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len};  // the step computed next
   Cursor ahead = cur;                                  // the step that `next` is of
@@ -770,8 +766,10 @@ __global__ void __launch_bounds__(DecodePlan<DQ, DV, NT>::NW * 32, 1)
     }
   }
   __syncthreads();
-  decode_join_held<DV, NW, P::WARP_BYTES, ROWS, PITCH>(
-      p, ranges[warp], smem, held, held_end,
+  decode_join_held<DV>(
+      p, ranges[warp], NW, held, held_end,
+      [&](int x, int r) { return reinterpret_cast<const float*>(smem + x * P::WARP_BYTES) + r * PITCH; },
+      [&](int x, int r) { return reinterpret_cast<const float2*>(smem + x * P::WARP_BYTES + ROWS * PITCH * 4)[r]; },
       [&](long long row, int col, float4 o, float mm, float ll) { decode_write_row<F16>(p, row, col, o, mm, ll); });
 }
 

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
   griddep_launch_dependents();
   // (barriers and the tensor-memory address are published by its barrier)
   const DecodeRange w =
-      p.wide ? decode_plan<long long, BN, P::NW, false>(p, words) : decode_plan<int, BN, P::NW, false>(p, words);
+      p.wide ? decode_plan<long long, BN, P::NW>(p, words, 1, 0) : decode_plan<int, BN, P::NW>(p, words, 1, 0);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int count = w.count;
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(DecodeTcPlan<DQ, DV>::THREADS, 1)
         }
         if (begins && tid == 0) {
           if (ends) decode_complete(p, cur.b, cur.hu);
-          else decode_describe<1>(p, w, cur.b, cur.hu, blockIdx.x, w.lo + i + (cur.nt - 1 - cur.t));
+          else decode_describe(p, w, 1, cur.b, cur.hu, blockIdx.x, w.lo + i + (cur.nt - 1 - cur.t));
         }
         tc_fence_before();
         __syncwarp();

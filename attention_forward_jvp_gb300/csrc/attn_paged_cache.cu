@@ -77,6 +77,13 @@ bool pools_share(const C* c, const Pool4& k, const Pool4& v) {
   return false;
 }
 
+// log2 of a power of two, else -1
+int page_shift_of(int page_size) {
+  for (int s = 0; s < 31; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
 // The keys that a row of a table of n pages can hold
 template <class C>
 int capacity_of(const C* c, int n) {
@@ -93,9 +100,7 @@ void take_cache(const C* c, const Device& d, DecodeParams* p) {
   p->B = c->B;
   p->n_pages = c->n_pages;
   p->page_size = c->page_size;
-  p->page_shift = -1;
-  for (int s = 0; s < 31; ++s)
-    if (c->page_size == 1 << s) p->page_shift = s;
+  p->page_shift = page_shift_of(c->page_size);
   p->capacity = capacity_of(c, c->max_pages);
   p->whole = c->page_size % 16 == 0 ? 1 : 0;
   p->Hkv = c->Hkv;
@@ -186,7 +191,7 @@ attn_status run_append4(const attn_paged_cache4* c, const attn_paged_new* n, con
 // How the kernel runs a cache's head dims and Hq query heads
 struct Layout4 {
   int dq, dv;              // kernel head dims
-  int rows, chunks;        // query heads of a unit, units of a key head
+  int rows, chunks;        // query heads of a warp, warps that a key head's take
   size_t desc, ml, total;  // workspace: bytes of the first two parts, of all
 };
 Layout4 layout4_of(const attn_paged_cache4* c, int Hq, int sms) {
@@ -247,7 +252,7 @@ attn_status run_decode4(const attn_paged_cache4* c, int32_t Hq, const void* q, c
   p4.narrow = p.whole && narrow(p4.k) && narrow(p4.v) && c->Dqk >= 64 && c->Dv >= 64 ? 1 : 0;
   p.q = static_cast<const uint16_t*>(q);
   p.G = Hq / c->Hkv;
-  p.rows = l.rows;
+  p4.sub_rows = l.rows;
   p.chunks = l.chunks;
   p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
@@ -375,7 +380,7 @@ attn_status run_weights4(const attn_paged_cache4* c, int32_t Hq, const void* q, 
 size_t evict_workspace(int32_t B, int32_t Hkv, int32_t page_size, int32_t n_new) {
   if (B < 0 || Hkv < 1 || page_size < 1 || n_new < 0) return 0;
   const int64_t keys = static_cast<int64_t>(n_new) * page_size;
-  return sizeof(int32_t) * static_cast<size_t>(B) * Hkv * (keys < (1 << 30) ? keys : (1 << 30));
+  return sizeof(int2) * static_cast<size_t>(B) * Hkv * (keys < (1 << 30) ? keys : (1 << 30));
 }
 
 template <class C>
@@ -429,12 +434,13 @@ attn_status run_evict(const C* c, EvictParams& p, int bits, const attn_paged_evi
   p.w = a->w;
   p.w_out = a->w_out;
   p.places = static_cast<long long>(c->max_pages) * c->page_size;
-  p.index = static_cast<int*>(workspace);
+  p.index = static_cast<int2*>(workspace);
+  p.page_shift = page_shift_of(c->page_size);
   p.Dqk = c->Dqk;
   p.Dv = c->Dv;
   p.err = d.err;
   int launches = 0;
-  if (launch_evict(p, bits, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (launch_evict(p, bits, d.sms, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess) return ATTN_ERR_CUDA;
   count_launch(launches);
   return ATTN_OK;
 }

@@ -3,11 +3,13 @@
 //
 // Append: of a group of 64 neighbouring elements (32 where D = 32), after the
 // rotation, m = fp16(min), s = fp16((max - m) / 15), n = round((x - m) / s) in
-// 0 .. 15; the divisions are IEEE's, so that n is a function of x alone.  Eight
+// 0 .. 15, with the quotients of IEEE's division, so that n is a function of x
+// alone: x - m times 1 / s rounds to the same n unless it lies within 10^-4 of
+// a half (it is off by 4 10^-6 at most), and is divided where it does.  Eight
 // elements to a thread, the row of a head to D / 8 neighbouring lanes of one
 // warp: the group's extremes come from three exchanges between lanes, and the
 // element that x turns with from another lane of the row.  A warp takes heads
-// of one token, whose angles it computes once.
+// of one token, whose angles it computes once, the rows of several on their way.
 //
 // Gather: a thread owns eight elements of one token and walks over the heads,
 // several loads in flight.
@@ -25,23 +27,27 @@ namespace attn {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWarps = 8;
+constexpr int kWarps = 8, kAppendUnroll = 4;
 
-// eight neighbouring elements, of which VEC says that they are one 16-byte word
-template <bool F16, bool VEC>
-__device__ __forceinline__ void load8(const uint16_t* x, bool live, float (&f)[8]) {
-  if constexpr (VEC) {
-    const uint4 w = live ? *reinterpret_cast<const uint4*>(x) : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// eight neighbouring elements: VEC says that they are one 16-byte word
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const uint16_t* x, bool live) {
+  uint4 w = make_uint4(0u, 0u, 0u, 0u);
+  if (!live) return w;
+  if constexpr (VEC) return *reinterpret_cast<const uint4*>(x);
+  uint32_t* u = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = unpack2<F16>(u[i]);
-      f[2 * i] = v.x;
-      f[2 * i + 1] = v.y;
-    }
-  } else {
+  for (int i = 0; i < 4; ++i) u[i] = x[2 * i] | static_cast<uint32_t>(x[2 * i + 1]) << 16;
+  return w;
+}
+template <bool F16>
+__device__ __forceinline__ void widen8(const uint4& w, float (&f)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = live ? widen<F16>(x[i]) : 0.f;
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack2<F16>(u[i]);
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
   }
 }
 template <bool F16, bool VEC>
@@ -73,9 +79,12 @@ struct Turn8 {
       }
     }
   }
-  // f: this lane's elements; x: the row in memory.  All lanes take part.
+  // f: the elements w; x: the row in memory.  All lanes take part.
   template <bool F16, bool VEC>
-  __device__ __forceinline__ void apply(const RopeSpec& r, int d0, const uint16_t* x, bool live, float (&f)[8]) const {
+  __device__ __forceinline__ void apply(const RopeSpec& r, int d0, const uint16_t* x, bool live, const uint4& w,
+                                        float (&f)[8]) const {
+    widen8<F16>(w, f);
+    if (r.rot == 0) return;
     float o[8];
     if constexpr (VEC) {  // rot a multiple of 16: a lane's elements turn with another lane's, or with one another
       if (r.interleaved) {
@@ -84,8 +93,9 @@ struct Turn8 {
       } else {
         const int shift = d0 < r.rot / 2 ? r.rot / 16 : (d0 < r.rot ? -(r.rot / 16) : 0);
         const int from = (threadIdx.x & 31) + shift;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(kAll, f[j], from);
+        widen8<F16>(make_uint4(__shfl_sync(kAll, w.x, from), __shfl_sync(kAll, w.y, from), __shfl_sync(kAll, w.z, from),
+                               __shfl_sync(kAll, w.w, from)),
+                    o);
       }
     } else {
 #pragma unroll
@@ -135,11 +145,22 @@ __device__ __forceinline__ void store_row4(const Pool4& pool, long long page, in
   if (odds) {
     m = s = __ushort_as_half(0x7fff);
   } else if (sf > 0.f) {
+    const float inv = __frcp_rn(sf);  // (finite: s is 2^-24 or more)
+    bool near = false;
+    float n[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float n = fminf(fmaxf(rintf(__fdiv_rn(f[j] - mf, sf)), 0.f), 15.f);
-      word |= static_cast<uint32_t>(n) << (4 * j);
+      const float y = (f[j] - mf) * inv;
+      n[j] = rintf(y);
+      near = near || fabsf(y - n[j]) > 0.4999f;
     }
+    if (near) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) n[j] = rintf(__fdiv_rn(f[j] - mf, sf));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)  // (2^23 + n: n in the low bits)
+      word |= (__float_as_uint(fminf(fmaxf(n[j], 0.f), 15.f) + 8388608.f) & 15u) << (4 * j);
   }
   uint8_t* codes = pool.codes + page * pool.st[0] + h * pool.st[1] + slot * pool.st[2];
   *reinterpret_cast<uint32_t*>(codes + d0 / 2) = word;
@@ -180,45 +201,57 @@ __global__ void __launch_bounds__(kWarps * 32) append4_kernel(const __grid_const
   const bool placed = page >= 0 && page < p.n_pages;
   if (!placed && !idle && lane == 0 && blockIdx.y == 0) *p.err = 1;
 
-  // heads of q, of k and of v, one after the other
+  // heads of q, of k and of v, one after the other: `use` for each row that
+  // this lane has eight elements of, those of U rows on their way
+  constexpr int U = VEC ? kAppendUnroll : 1;
   const int first = blockIdx.y * p.heads_per_split;
   const int last = min(first + p.heads_per_split, p.Hq + 2 * p.Hkv);
-  {
-    const int L = p.Dqk / 8, R = 32 / L, d0 = 8 * (lane & (L - 1)), r = lane / L;
-    Turn8 turned;
-    if (first < p.Hq + p.Hkv && pos >= 0) turned.angles(p.r, d0, static_cast<int>(pos));
-    for (int h = first + r, end = min(last, p.Hq); h - r < end; h += R) {
-      const bool live = h < end;
-      const uint16_t* x = p.q + t * p.qs[0] + (live ? h : first) * p.qs[1];
-      uint16_t* y = p.q_out + t * p.qos[0] + (live ? h : first) * p.qos[1];
-      float f[8] = {};
-      if (pos >= 0) {
-        load8<F16, VEC>(x + d0, live, f);
-        turned.apply<F16, VEC>(p.r, d0, x, live, f);
-        __syncwarp();  // in place: the row has been read
+  auto heads = [&](const uint16_t* base, long long stride, int D, int lo, int hi, auto use) {
+    const int L = D / 8, R = 32 / L, d0 = 8 * (lane & (L - 1)), r = lane / L;
+#pragma unroll 1
+    for (int h0 = lo; h0 < hi; h0 += R * U) {
+      uint4 w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * R + r;
+        w[u] = load8<VEC>(base + (h < hi ? h : lo) * stride + d0, h < hi);
       }
-      if (live) store8<F16, VEC>(y + d0, f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * R + r;
+        if (h0 + u * R < hi) use(w[u], base + (h < hi ? h : lo) * stride, h, h < hi, d0);
+      }
     }
-    if (!placed) return;
-    for (int h = max(first - p.Hq, 0) + r, end = min(last - p.Hq, p.Hkv); h - r < end; h += R) {
-      const bool live = h < end;
-      const uint16_t* x = p.k + t * p.ks[0] + (live ? h : 0) * p.ks[1];
-      float f[8];
-      load8<F16, VEC>(x + d0, live, f);
-      turned.apply<F16, VEC>(p.r, d0, x, live, f);
-      store_row4(p4.k, page, h, slot, p.Dqk, d0, live, f);
-    }
+  };
+  Turn8 turned;
+  if (first < p.Hq + p.Hkv && pos >= 0) turned.angles(p.r, 8 * (lane & (p.Dqk / 8 - 1)), static_cast<int>(pos));
+  if (pos >= 0) {
+    heads(p.q + t * p.qs[0], p.qs[1], p.Dqk, first, min(last, p.Hq),
+          [&](const uint4& w, const uint16_t* x, int h, bool live, int d0) {
+            float f[8];
+            turned.apply<F16, VEC>(p.r, d0, x, live, w, f);
+            __syncwarp();  // in place: the row has been read
+            if (live) store8<F16, VEC>(p.q_out + t * p.qos[0] + h * p.qos[1] + d0, f);
+          });
+  } else {  // no position: zeros
+    const float zero[8] = {};
+    const int L = p.Dqk / 8;
+    for (int h = first + lane / L; h < min(last, p.Hq); h += 32 / L)
+      store8<F16, VEC>(p.q_out + t * p.qos[0] + h * p.qos[1] + 8 * (lane & (L - 1)), zero);
   }
-  {
-    const int L = p.Dv / 8, R = 32 / L, d0 = 8 * (lane & (L - 1)), r = lane / L;
-    for (int h = max(first - p.Hq - p.Hkv, 0) + r, end = min(last - p.Hq - p.Hkv, p.Hkv); h - r < end; h += R) {
-      const bool live = h < end;
-      const uint16_t* x = p.v + t * p.vs[0] + (live ? h : 0) * p.vs[1];
-      float f[8];
-      load8<F16, VEC>(x + d0, live, f);
-      store_row4(p4.v, page, h, slot, p.Dv, d0, live, f);
-    }
-  }
+  if (!placed) return;
+  heads(p.k + t * p.ks[0], p.ks[1], p.Dqk, max(first - p.Hq, 0), min(last - p.Hq, p.Hkv),
+        [&](const uint4& w, const uint16_t* x, int h, bool live, int d0) {
+          float f[8];
+          turned.apply<F16, VEC>(p.r, d0, x, live, w, f);
+          store_row4(p4.k, page, h, slot, p.Dqk, d0, live, f);
+        });
+  heads(p.v + t * p.vs[0], p.vs[1], p.Dv, max(first - p.Hq - p.Hkv, 0), min(last - p.Hq - p.Hkv, p.Hkv),
+        [&](const uint4& w, const uint16_t*, int h, bool live, int d0) {
+          float f[8];
+          widen8<F16>(w, f);
+          store_row4(p4.v, page, h, slot, p.Dv, d0, live, f);
+        });
 }
 
 // ------------------------------------------------------------------- gather
@@ -248,12 +281,18 @@ struct Held4 {
   }
   template <bool F16>
   __device__ __forceinline__ uint4 value() const {
-    const float sf = __half2float(__ushort_as_half(s)), mf = __half2float(__ushort_as_half(m));
+    // n in the low bits of a half is the subnormal n 2^-24, 16 n that of an odd
+    // element; n s is exact (15 bits)
+    const float m1 = __half2float(__ushort_as_half(m)), s1 = __half2float(__ushort_as_half(s)) * 16777216.f;
+    const float s16 = s1 * 0.0625f;
     uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // (n s is exact: 15 bits)
-      u[i] = pack2<F16>(fmaf(static_cast<float>(w >> (8 * i) & 15u), sf, mf),
-                        fmaf(static_cast<float>(w >> (8 * i + 4) & 15u), sf, mf));
+    for (int i = 0; i < 2; ++i) {  // elements 2 i, 2 i + 1 and 4 further on
+      const uint32_t a = w >> (8 * i) & 0x000f000fu, b = w >> (8 * i) & 0x00f000f0u;
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+      u[i] = pack2<F16>(fmaf(x.x, s1, m1), fmaf(y.x, s16, m1));
+      u[2 + i] = pack2<F16>(fmaf(x.y, s1, m1), fmaf(y.y, s16, m1));
+    }
     return make_uint4(u[0], u[1], u[2], u[3]);
   }
 };

@@ -46,15 +46,19 @@ cudaError_t launch_gather(const GatherParams& p, int bits, bool f16, int splits,
 // ------------------------------------------------------------------ decode
 constexpr int kDecode4BN = 32;  // keys of a step
 
-// Query heads of a unit at most, in groups of 8: each takes DV / 4 registers of
-// accumulators and more for the corrections.  More heads are units of their
-// own, which read the key head's pages again, at 4.5 bits an element.
+// Query heads of a warp at most, in groups of 8: each takes DV / 4 registers of
+// accumulators and more for the corrections.  More heads go to more warps, which
+// walk over the same steps at the same time.
 constexpr int decode4_rows(int dv) { return dv == 64 ? 32 : (dv == 128 ? 24 : 16); }
 
 struct Decode4Params {
-  DecodeParams d;  // (its 16-bit pools unused)
+  DecodeParams d;  // (its 16-bit pools unused; Hkv, G, rows, chunks by the launch)
   Pool4 k, v;
   int narrow;      // copy_tokens4
+  int sub_rows;    // query heads of a warp
+  // set by the launch: warps of a range, each with heads of its own; the key
+  // heads that they are of, 1 or all different
+  int subs, heads;
 };
 
 // The decode kernel over a cache in 4 bits for kernel head dims DQ, DV and nt
@@ -95,7 +99,8 @@ struct EvictParams {
   const float* w;
   float* w_out;
   long long ws[2], wos[2], places;
-  int* index;                  // [B][Hkv][new_capacity]: the kept tokens of a head
+  int page_shift;              // log2 of page_size, or -1
+  int2* index;                 // [B][Hkv][new_capacity]: page and slot of a head's kept tokens
   uint16_t *k16, *v16;
   long long kp[3], vp[3];
   Pool4 k, v;
@@ -103,6 +108,6 @@ struct EvictParams {
   int* err;
 };
 // launches: how many kernels it came to
-cudaError_t launch_evict(const EvictParams& p, int bits, cudaStream_t stream, int* launches);
+cudaError_t launch_evict(const EvictParams& p, int bits, int sms, cudaStream_t stream, int* launches);
 
 }  // namespace attn

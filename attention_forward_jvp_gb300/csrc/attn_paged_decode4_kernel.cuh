@@ -39,7 +39,7 @@ struct Decode4Plan {
   static constexpr int MISC_BYTES = (8 * 32 + 16 + 24 + sizeof(DecodeRange)) * kDecodeMaxWarps;
   static constexpr int FIT = 226 * 1024 - MISC_BYTES;
   // O, its corrections and statistics; Q
-  static constexpr int REGS = (DV / 4 + 4 * GV + 4) * NT + (DQ / 8 + 4) * NT + 64;
+  static constexpr int REGS = (DV / 4 + 4 * GV + 4) * NT + (DQ / 8 + 4) * NT + 80;
   static constexpr int NW_REGS = REGS <= 128 ? 16 : (REGS <= 160 ? 12 : 8);
   static constexpr int S = FIT / NW_REGS / STAGE >= 4 ? 4 : (FIT / NW_REGS / STAGE >= 3 ? 3 : 2);
   static constexpr int PITCH = DV + 4;
@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
   int4* held = reinterpret_cast<int4*>(misc + P::MISC_BYTES - 24 * kDecodeMaxWarps);
   long long* held_end = reinterpret_cast<long long*>(misc + P::MISC_BYTES - 8 * kDecodeMaxWarps);
   const int HU = p.Hkv * p.chunks;  // units of a sequence
+  // this warp's part of a unit: heads g0 + sub * sub_rows ..; its range's place in the CTA
+  const int R = NW / p4.subs, own = warp / p4.subs, sub = warp - own * p4.subs;
 
   griddep_wait();
   griddep_launch_dependents();
@@ -99,12 +101,13 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
     }
   };
   auto lookup = [&](const Cursor& a) {
-    return lookup4(p, p.page_table + a.b * p.table_stride, a.t * BN, a.len, p.chunks == 1 ? a.hu : a.hu / p.chunks);
+    const int h = p.chunks == 1 ? a.hu : a.hu / p.chunks;
+    return lookup4(p, p.page_table + a.b * p.table_stride, a.t * BN, a.len, p4.heads > 1 ? h * p4.heads + sub : h);
   };
 
   // ---- this warp's range, and the places of its first steps
-  const int me = blockIdx.x * NW + warp;
-  DecodeRange w = p.wide ? decode_plan<long long, BN, NW, true>(p, words) : decode_plan<int, BN, NW, true>(p, words);
+  const int me = blockIdx.x * R + own;
+  DecodeRange w = p.wide ? decode_plan<long long, BN, NW>(p, words, R, own) : decode_plan<int, BN, NW>(p, words, R, own);
   const int count = w.count;
   Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len};  // the step computed next
   Cursor ahead = cur;                                  // the step that `next` is of
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
     }
   }
   if (w.idle) decode_idle(p);
-  if (p.split && !p.by_unit && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
+  if (p.split && !p.by_unit && sub == 0 && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
   if (w.cta_lo >= w.total) return;
   if (lane == 0) ranges[warp] = w;
 
@@ -147,7 +150,8 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
     }
   };
   auto load_q = [&](const Cursor& a) {
-    const int h = a.hu / p.chunks, g0 = (a.hu - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
+    const int h = a.hu / p.chunks, g0 = (a.hu - h * p.chunks) * p.rows + sub * p4.sub_rows;
+    const int n_rows = min(p4.sub_rows, p.G - g0);
     const uint16_t* base = p.q + a.b * p.qs[0] + (static_cast<long long>(h) * p.G + g0) * p.qs[1];
     q.template load<F16>(base, p.qs[1], n_rows, p.dqk, p.scale_log2);
   };
@@ -189,17 +193,22 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
   };
 
   clear();
+  Rows4<DQ, true> k_rows;
+  Rows4<DV, false> v_rows;
+  k_rows.init(p4.k);
+  v_rows.init(p4.v);
+  const uint32_t key_at = key_read<DQ>(), value_at = value_read<DV>();
   if (count > 0) {
     auto issue = [&](const Place4& x, int stage) {
       const uint32_t to = ring + stage * P::STAGE;
       const uint32_t tv = to + P::K_BYTES, ks = tv + P::V_BYTES, vs = ks + P::KS_BYTES;
       copy_tokens4(p, p4.narrow, x, [&](auto whole, const Place4& y, bool live) {
         if constexpr (decltype(whole)::value) {
-          copy_rows4_whole<DQ, true>(p4.k, y, to, ks);
-          copy_rows4_whole<DV, false>(p4.v, y, tv, vs);
+          k_rows.copy_whole(p4.k, y, to, ks);
+          v_rows.copy_whole(p4.v, y, tv, vs);
         } else {
-          copy_rows4<DQ, true>(p4.k, y, live, p.dqk, to, ks);
-          copy_rows4<DV, false>(p4.v, y, live, p.dv, tv, vs);
+          k_rows.copy(p4.k, y, live, p.dqk, to, ks);
+          v_rows.copy(p4.v, y, live, p.dv, tv, vs);
         }
       });
     };
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
       const int live = cur.len - cur.t * BN;  // keys of this step
       float s[2][NT][4];
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) scores4<DQ, NT>(q, sk, sks, 16 * kt, s[kt]);
+      for (int kt = 0; kt < 2; ++kt) scores4<DQ, NT>(q, sk + key_at, sks + g * (4 * P::GQ), 16 * kt, s[kt]);
       // S' - m, and whether one passes the room above the reference, or a step
       // of the values of key `lane` the largest so far
       bool grows = false;
@@ -381,8 +390,8 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
           for (int o = 0; o < 2; ++o)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int key = 16 * kt + 8 * o + 2 * t + e;
-              word[o][e] = lds32(sv + value_row<DV>(key) * (DV / 2) + value_slot<DV>(key, b) * 32 + 4 * g);
+              const int row = 16 * kt + 8 * o + e * (DV == 64 ? 4 : (DV == 128 ? 2 : 1));  // value_row
+              word[o][e] = lds32(((sv + value_at) ^ (b << 5)) + row * (DV / 2));
             }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {  // elements 4 c .. 4 c + 3 of the word's eight
@@ -407,10 +416,11 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
       if (cur.t + 1 == cur.nt || last) {
         const bool begins = t0 == 0;
         if (!last) {  // (the range's last unit is joined with the other warps' below; this one ends here)
-          const int h = cur.hu / p.chunks, g0 = (cur.hu - h * p.chunks) * p.rows, n_rows = min(p.rows, p.G - g0);
-          const long long part = 2LL * me;
+          const int h = cur.hu / p.chunks, g0 = (cur.hu - h * p.chunks) * p.rows + sub * p4.sub_rows;
+          const int n_rows = min(p4.sub_rows, p.G - g0);
+          const long long part0 = 2LL * me * p.rows + sub * p4.sub_rows;
           const long long row0 = (static_cast<long long>(cur.b) * p.Hkv + h) * p.G + g0;
-          if (begins && lane == 0) decode_complete(p, cur.b, cur.hu);
+          if (begins && sub == 0 && lane == 0) decode_complete(p, cur.b, cur.hu);
           // this step's stage, which has been read and is refilled in the next step; where eight heads are larger, a place apart
           float* scratch = reinterpret_cast<float*>(P::SPILL > P::STAGE ? mine + P::WARP_BYTES - P::SPILL : mine + stage * P::STAGE);
 #pragma unroll
@@ -430,19 +440,19 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
                 if (begins) {
                   write_row(row0 + row, 4 * c4, o, mm, ll);
                 } else {
-                  *reinterpret_cast<float4*>(p.part_o + (part * p.rows + row) * DV + 4 * c4) = o;
-                  if (c4 == 0) p.part_ml[part * p.rows + row] = make_float2(mm, ll);
+                  *reinterpret_cast<float4*>(p.part_o + (part0 + row) * DV + 4 * c4) = o;
+                  if (c4 == 0) p.part_ml[part0 + row] = make_float2(mm, ll);
                 }
               }
             }
           }
         }
         if (last) {
-          if (lane == 0) {
-            // goes on where the warp before has left off?
-            const bool goes_on = warp > 0 && i == cur.t - t0 && t0 > 0;
-            held[warp] = make_int4(cur.b, cur.hu, begins ? 1 : 0, goes_on ? 1 : 0);
-            held_end[warp] = ranges[warp].lo + i + (cur.nt - 1 - cur.t);
+          if (sub == 0 && lane == 0) {
+            // goes on where the range before has left off?
+            const bool goes_on = own > 0 && i == cur.t - t0 && t0 > 0;
+            held[own] = make_int4(cur.b, cur.hu, begins ? 1 : 0, goes_on ? 1 : 0);
+            held_end[own] = ranges[warp].lo + i + (cur.nt - 1 - cur.t);
           }
         } else {
           clear();
@@ -474,7 +484,23 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
     }
   }
   __syncthreads();
-  decode_join_held<DV, NW, P::WARP_BYTES, ROWS, PITCH>(p, ranges[warp], smem, held, held_end, write_row);
+  // row r of a range's unit, where the warp that has it left it
+  auto left_by = [&](int x, int& r) {
+    const int k = p4.subs == 1 ? 0 : r / p4.sub_rows;
+    r -= k * p4.sub_rows;
+    return smem + (x * p4.subs + k) * P::WARP_BYTES;
+  };
+  decode_join_held<DV>(
+      p, ranges[warp], R, held, held_end,
+      [&](int x, int r) {
+        const char* from = left_by(x, r);
+        return reinterpret_cast<const float*>(from) + r * PITCH;
+      },
+      [&](int x, int r) {
+        const char* from = left_by(x, r);
+        return reinterpret_cast<const float2*>(from + ROWS * PITCH * 4)[r];
+      },
+      write_row);
 }
 
 template <int DQ, int DV, bool F16, int NT>
@@ -494,8 +520,27 @@ cudaError_t launch_decode4_nt(Decode4Params& p, int ctas, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
-  p.d.cta_warps = P::NW;
-  plan_join(p.d, ctas);
+  // Warps that take neighbouring key heads of the same tokens, or the heads of
+  // one that are too many for a warp, go together.  Where a page lies token by
+  // token, the steps and least values of up to eight heads share 64 bytes, the
+  // least that memory gives: on their own, heads read them again and again
+  // (64 sequences of up to 8192, D 128, eight heads: 610 MB for 322).
+  DecodeParams& d = p.d;
+  int subs = 1;
+  if (d.chunks == 1) {
+    while (subs < 8 && P::NW % (2 * subs) == 0 && d.Hkv % (2 * subs) == 0) subs *= 2;
+    p.heads = subs;
+    d.Hkv /= subs;
+    d.G *= subs;
+  } else {
+    while (subs < d.chunks && subs < 8 && P::NW % (2 * subs) == 0) subs *= 2;
+    p.heads = 1;
+    d.chunks = (d.chunks + subs - 1) / subs;
+  }
+  p.subs = subs;
+  d.rows = subs * p.sub_rows;
+  d.cta_warps = P::NW / subs;
+  plan_join(d, ctas);
   e = decode_launch_one(attn_paged_decode4_kernel<DQ, DV, F16, NT>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
   return e != cudaSuccess || !p.d.split ? e : launch_join<DV, F16>(p.d, ctas, stream);
 }

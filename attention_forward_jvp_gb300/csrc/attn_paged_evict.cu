@@ -2,16 +2,18 @@
 // sequence that is longer than it may stay, the tokens with the largest
 // weights, the first and the last, copied in their order into fewer pages.
 //
-// Two kernels.  `select` has a block for each (sequence, key head): a radix
-// selection of the M-th largest weight, in four passes of eight bits over
-// weights turned to whole numbers of the same order, then the numbers of the
-// kept tokens in order, each warp counting what a stretch of the row keeps
-// before all write.  Ties go by the same order, so that the choice is a
-// function of the weights alone.  `move` copies the rows of the kept tokens,
-// 16 bytes a thread, several rows on their way.
+// Two kernels.  `select` has a block for each (sequence, key head), or a cluster
+// of up to eight where there are few: a radix selection of the M-th largest
+// weight in three passes (12, 10 and 10 bits) over weights turned to whole
+// numbers of the same order, which stay in registers while a warp's stretch of
+// the row is no longer than 512; the blocks of a cluster add up their histograms
+// from one another's shared memory.  Then the places of the kept tokens in
+// order, each warp counting what its stretch keeps before all write.  Ties go by
+// the same order, so that the choice is a function of the weights alone.
+// `move` copies the rows of the kept tokens: a warp looks up 32 of them at once,
+// then moves whole rows, 16 bytes a lane, several of them on their way.
 //
-// What bounds it: memory, the kept rows read and written once; the selection
-// reads a head's weights six times, from L2 after the first.
+// What bounds it: memory, the kept rows read and written once.
 #include "attn_paged_cache_kernels.h"
 #include "ptx.cuh"
 
@@ -50,16 +52,44 @@ __device__ __forceinline__ Share share_of(const EvictParams& p, int b) {
   return s;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the word at `p`, of this block's shared memory, in that of another block of the cluster
+__device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
+  uint32_t at;
+  int v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+constexpr int kKept = 16;             // weights that a lane keeps
+constexpr int kStretch = 32 * kKept;  // and a warp
+
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int histogram[256];
-  __shared__ int found[2];                      // the digit, the numbers above it
+  __shared__ int histogram[4096 + 1024 + 1024];  // one for each pass
+  __shared__ int found[2];                       // the digit, the numbers above it
+  __shared__ int sums[kSelectWarps];
   __shared__ int counts[2][kSelectWarps];
+  __shared__ int totals[2];
   griddep_wait();
   griddep_launch_dependents();
-  const int b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv;
+  const int C = cluster_size(), rank = cluster_rank();
+  const int bh = blockIdx.x / C, b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Share s = share_of(p, b);
-  if (h == 0) {
+  if (h == 0 && rank == 0) {
     if (s.odd && tid == 0) *p.err = 1;
     if (tid == 0) p.lens_out[b] = min(s.n, s.keep);
     for (int i = tid; i < p.max_pages; i += kSelectThreads)
@@ -68,11 +98,40 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
   }
   const float* w = p.w + b * p.ws[0] + h * p.ws[1];
   float* to = p.w_out + b * p.wos[0] + h * p.wos[1];
+  const int step = C * kSelectThreads, first = rank * kSelectThreads + tid;
   if (!s.over) {
-    for (long long i = tid; i < p.places; i += kSelectThreads) to[i] = w[i];
+    for (long long i = first; i < p.places; i += step) to[i] = w[i];
     return;
   }
-  for (long long i = s.keep + tid; i < p.places; i += kSelectThreads) to[i] = 0.f;
+  for (int i = tid; i < (4096 + 1024 + 1024) / 4; i += kSelectThreads)
+    reinterpret_cast<int4*>(histogram)[i] = make_int4(0, 0, 0, 0);
+  for (long long i = s.keep + static_cast<long long>(first); i < p.places; i += step) to[i] = 0.f;
+
+  // this warp's stretch of the row
+  const int warps = C * kSelectWarps;
+  const long long stretch = ((s.n + warps - 1LL) / warps + 31) / 32 * 32;
+  const int from = static_cast<int>(min((rank * kSelectWarps + warp) * stretch, static_cast<long long>(s.n)));
+  const int end = static_cast<int>(min(from + stretch, static_cast<long long>(s.n)));
+  const bool stays = stretch <= kStretch;
+  float x[kKept];
+  auto load = [&](int at) {
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      const int j = at + 32 * k + lane;
+      x[k] = j < end ? w[j] : 0.f;
+    }
+  };
+  if (stays) load(from);
+  // use(j, weight) for the stretch's tokens j, 32 neighbouring ones at a time; all lanes take part
+  auto each = [&](auto use) {
+#pragma unroll 1
+    for (int at = from; at < end; at += kStretch) {
+      if (!stays) load(at);
+#pragma unroll
+      for (int k = 0; k < kKept; ++k)
+        if (at + 32 * k < end) use(at + 32 * k + lane, x[k]);
+    }
+  };
 
   // the others' weights lie in [lo, hi); `most` of them are kept
   const int lo = s.sinks, hi = s.n - s.recent, most = s.keep - s.sinks - s.recent;
@@ -80,70 +139,107 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
   int ties = 0;        // how many that are equal to it
   if (most > 0) {
     int left = most;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) histogram[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bits = pass == 0 ? 12 : 10, shift = pass == 0 ? 20 : (pass == 1 ? 10 : 0);
+      int* bins = histogram + (pass == 0 ? 0 : (pass == 1 ? 4096 : 5120));
+      each([&](int j, float v) {
+        const uint32_t u = ordered(v);
+        const bool in = j >= lo && j < hi && j < end && (pass == 0 || u >> (shift + bits) == least);
+        const unsigned all = __ballot_sync(kAll, in);
+        if (all == 0) return;
+        const int bin = u >> shift & ((1 << bits) - 1);
+        const int one = __shfl_sync(kAll, bin, __ffs(all) - 1);
+        // (the same bin for all: one addition, where a row of equal weights would take 32)
+        if (__ballot_sync(kAll, in && bin == one) == all) {
+          if (lane == 0) atomicAdd(&bins[one], __popc(all));
+        } else if (in) {
+          atomicAdd(&bins[bin], 1);
+        }
+      });
+      if (C > 1) cluster_sync();
+      else __syncthreads();
+      // the digits from the largest on, four or one to a thread
+      constexpr int kMost = 4;
+      const int mine = pass == 0 ? kMost : 1, top = (1 << bits) - 1 - mine * tid;
+      int c[kMost], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        c[i] = 0;
+        if (i < mine) {
+          for (int r = 0; r < C; ++r) c[i] += C > 1 ? peer_word(&bins[top - i], r) : bins[top - i];
+        }
+        sum += c[i];
+      }
+      int above = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kAll, above, o);
+        if (lane >= o) above += y;
+      }
+      if (lane == 31) sums[warp] = above;
       __syncthreads();
-      for (int i = lo + tid; i < hi; i += kSelectThreads) {
-        const uint32_t u = ordered(w[i]);
-        if (shift == 24 || u >> (shift + 8) == least) atomicAdd(&histogram[u >> shift & 255], 1);
+      int before = lane < warp ? sums[lane] : 0;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(kAll, before, o);
+      above += before - sum;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        if (i < mine && above < left && above + c[i] >= left) {
+          found[0] = top - i;
+          found[1] = above;
+        }
+        above += c[i];
       }
       __syncthreads();
-      if (warp == 0) {  // the digits from the largest on, eight to a lane
-        int c[8], sum = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += c[j] = histogram[255 - 8 * lane - j];
-        int above = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(kAll, above, o);
-          if (lane >= o) above += y;
-        }
-        above -= sum;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (above < left && above + c[j] >= left) {
-            found[0] = 255 - 8 * lane - j;
-            found[1] = above;
-          }
-          above += c[j];
-        }
-      }
-      __syncthreads();
-      least = least << 8 | static_cast<uint32_t>(found[0]);
+      least = least << bits | static_cast<uint32_t>(found[0]);
       left -= found[1];
     }
     ties = left;
   }
-  // each warp's stretch of the row: what it keeps for its weight, its ties
-  const int each = ((s.n + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-  const int from = min(warp * each, s.n), end = min(from + each, s.n);
+  // what the stretch keeps for its weight, and its ties
   int above = 0, equal = 0;
-  for (int i = from; i < end; i += 32) {
-    const int j = i + lane;
+  each([&](int j, float v) {
     const bool in = j < end, sure = in && (j < lo || j >= hi);
-    const uint32_t u = in ? ordered(w[j]) : 0u;
+    const uint32_t u = ordered(v);
     above += __popc(__ballot_sync(kAll, sure || (in && most > 0 && u > least)));
     equal += __popc(__ballot_sync(kAll, in && !sure && most > 0 && u == least));
-  }
+  });
   if (lane == 0) {
     counts[0][warp] = above;
     counts[1][warp] = equal;
   }
   __syncthreads();
-  int equals = lane < warp ? counts[1][lane] : 0, aboves = lane < warp ? counts[0][lane] : 0;
+  if (warp == 0) {
+    int a = counts[0][lane], e = counts[1][lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      a += __shfl_xor_sync(kAll, a, o);
+      e += __shfl_xor_sync(kAll, e, o);
+    }
+    if (lane == 0) {
+      totals[0] = a;
+      totals[1] = e;
+    }
+  }
+  if (C > 1) cluster_sync();
+  int aboves = lane < warp ? counts[0][lane] : 0, equals = lane < warp ? counts[1][lane] : 0;
+  if (lane < rank) {
+    aboves += peer_word(&totals[0], lane);
+    equals += peer_word(&totals[1], lane);
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
-    equals += __shfl_xor_sync(kAll, equals, o);
     aboves += __shfl_xor_sync(kAll, aboves, o);
+    equals += __shfl_xor_sync(kAll, equals, o);
   }
   // places of the stretch: behind what the warps before it keep
   int at = aboves + min(equals, ties);
-  int* index = p.index + static_cast<long long>(blockIdx.x) * p.new_capacity;
-  for (int i = from; i < end; i += 32) {
-    const int j = i + lane;
+  int2* index = p.index + static_cast<long long>(bh) * p.new_capacity;
+  each([&](int j, float v) {
     const bool in = j < end, sure = in && (j < lo || j >= hi);
-    const float x = in ? w[j] : 0.f;
-    const uint32_t u = in ? ordered(x) : 0u;
+    const uint32_t u = ordered(v);
     const bool tie = in && !sure && most > 0 && u == least;
     const unsigned all_ties = __ballot_sync(kAll, tie);
     const bool keep = sure || (in && most > 0 && u > least) ||
@@ -151,18 +247,19 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     const unsigned kept = __ballot_sync(kAll, keep);
     if (keep) {
       const int k = at + __popc(kept & ((1u << lane) - 1));
-      index[k] = j;
-      to[k] = x;
+      const int e = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+      index[k] = make_int2(p.page_table[b * p.table_stride + e], j - e * p.page_size);
+      to[k] = v;
     }
     at += __popc(kept);
     equals += __popc(all_ties);
-  }
+  });
+  if (C > 1) cluster_sync();  // a block's shared memory stays until the others have read it
 }
 
-constexpr int kMoveThreads = 256, kMoveUnroll = 4;
+constexpr int kMoveThreads = 256, kMoveUnroll = 8;
 
-// Rows of keys (blockIdx.y 0) or values, 16 bytes a thread; the first thread of
-// a row of 4 bits takes its steps and least values too.
+// Rows of keys (blockIdx.y 0) or values, 32 tokens of a head to a warp
 template <int BITS>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictParams p, int chunks,
                                                             long long blocks) {
@@ -170,91 +267,93 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   griddep_wait();
   griddep_launch_dependents();
   const bool values = blockIdx.y != 0;
-  const int d = values ? p.Dv : p.Dqk;
+  const int d = values ? p.Dv : p.Dqk, lane = threadIdx.x & 31;
   const Pool4& pool = values ? p.v : p.k;
   const long long* st = BITS == 4 ? pool.st : (values ? p.vp : p.kp);
   char* base = BITS == 4 ? reinterpret_cast<char*>(pool.codes) : reinterpret_cast<char*>(values ? p.v16 : p.k16);
-  const int items = d * BITS / 128;  // a power of two
-  const int rows = kMoveThreads / items, item = threadIdx.x & (items - 1);
+  const int L = d * BITS / 128, R = 32 / L;  // lanes of a row, rows at once: powers of two
+  const int item = lane & (L - 1), lr = lane / L;
   constexpr int E = BITS == 4 ? 1 : 2;  // bytes of a unit of the strides
   for (long long x = blockIdx.x; x < blocks; x += gridDim.x) {
     const int bh = static_cast<int>(x / chunks), chunk = static_cast<int>(x - static_cast<long long>(bh) * chunks);
     const int b = bh / p.Hkv, h = bh - b * p.Hkv;
     const Share s = share_of(p, b);
-    const long long first = static_cast<long long>(chunk) * rows * U;
+    const int first = chunk * kMoveThreads + (threadIdx.x & ~31);
     if (!s.over || first >= s.keep) continue;
-    const int* index = p.index + static_cast<long long>(bh) * p.new_capacity;
-    uint4 v[U], sc[U];
-    long long to[U], to_scale[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long j = first + u * rows + threadIdx.x / items;
-      to[u] = to_scale[u] = -1;
-      v[u] = sc[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (j < s.keep) {
-        const int i = index[j], k = static_cast<int>(j);
-        const int src_e = i / p.page_size, dst_e = k / p.page_size;
-        const int src_slot = i - src_e * p.page_size, dst_slot = k - dst_e * p.page_size;
-        const int src = p.page_table[b * p.table_stride + src_e], dst = p.pages[b * p.pages_stride + dst_e];
-        const bool from = static_cast<unsigned>(src) < static_cast<unsigned>(p.n_pages);
-        const bool there = static_cast<unsigned>(dst) < static_cast<unsigned>(p.n_pages);
-        if (!(from && there) && item == 0) *p.err = 1;
-        if (there) to[u] = E * (dst * st[0] + h * st[1] + dst_slot * st[2]) + 16 * item;
-        if (from) v[u] = *reinterpret_cast<const uint4*>(base + E * (src * st[0] + h * st[1] + src_slot * st[2]) + 16 * item);
-        if (BITS == 4 && item == 0) {
-          const uint16_t* a = pool.scales + src * pool.ss[0] + h * pool.ss[1] + src_slot * pool.ss[2];
-          if (there) to_scale[u] = dst * pool.ss[0] + h * pool.ss[1] + dst_slot * pool.ss[2];
-          if (from) {
-            if (d <= 64) sc[u].x = *reinterpret_cast<const uint32_t*>(a);
-            else if (d == 128) *reinterpret_cast<uint2*>(&sc[u]) = *reinterpret_cast<const uint2*>(a);
-            else sc[u] = *reinterpret_cast<const uint4*>(a);
-          }
-        }
+    // the places of token `lane` of the 32, in bytes from the pool's start; -1: none
+    long long from = -1, to = -1;
+    const int k = first + lane;
+    if (k < s.keep) {
+      const int2 src = p.index[static_cast<long long>(bh) * p.new_capacity + k];
+      const int e = p.page_shift >= 0 ? k >> p.page_shift : k / p.page_size, slot = k - e * p.page_size;
+      const int dst = p.pages[b * p.pages_stride + e];
+      const bool has = static_cast<unsigned>(src.x) < static_cast<unsigned>(p.n_pages);
+      const bool there = static_cast<unsigned>(dst) < static_cast<unsigned>(p.n_pages);
+      if (!(has && there)) *p.err = 1;
+      if (has) from = E * (src.x * st[0] + h * st[1] + src.y * st[2]);
+      if (there) to = E * (dst * st[0] + h * st[1] + slot * st[2]);
+      if (BITS == 4 && there) {
+        uint16_t* y = pool.scales + dst * pool.ss[0] + h * pool.ss[1] + slot * pool.ss[2];
+        const uint16_t* a = pool.scales + (has ? src.x * pool.ss[0] + h * pool.ss[1] + src.y * pool.ss[2] : 0);
+        if (d <= 64) *reinterpret_cast<uint32_t*>(y) = has ? *reinterpret_cast<const uint32_t*>(a) : 0u;
+        else if (d == 128) *reinterpret_cast<uint2*>(y) = has ? *reinterpret_cast<const uint2*>(a) : make_uint2(0u, 0u);
+        else *reinterpret_cast<uint4*>(y) = has ? *reinterpret_cast<const uint4*>(a) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
+    const int rows = min(32, s.keep - first);
+    for (int r0 = 0; r0 < rows; r0 += U * R) {
+      uint4 v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (to[u] >= 0) *reinterpret_cast<uint4*>(base + to[u]) = v[u];
-      if (BITS == 4 && to_scale[u] >= 0) {
-        uint16_t* a = pool.scales + to_scale[u];
-        if (d <= 64) *reinterpret_cast<uint32_t*>(a) = sc[u].x;
-        else if (d == 128) *reinterpret_cast<uint2*>(a) = make_uint2(sc[u].x, sc[u].y);
-        else *reinterpret_cast<uint4*>(a) = sc[u];
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * R + lr;
+        const long long at = __shfl_sync(kAll, from, r & 31);
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows && at >= 0) v[u] = *reinterpret_cast<const uint4*>(base + at + 16 * item);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * R + lr;
+        const long long at = __shfl_sync(kAll, to, r & 31);
+        if (r < rows && at >= 0) *reinterpret_cast<uint4*>(base + at + 16 * item) = v[u];
       }
     }
   }
 }
 
-template <class K, class... A>
-cudaError_t launch(K kernel, dim3 grid, int threads, cudaStream_t stream, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace
 
-cudaError_t launch_evict(const EvictParams& p, int bits, cudaStream_t stream, int* launches) {
+cudaError_t launch_evict(const EvictParams& p, int bits, int sms, cudaStream_t stream, int* launches) {
   *launches = 1;
-  cudaError_t e = launch(select_kernel, dim3(static_cast<unsigned>(p.B * p.Hkv)), kSelectThreads, stream, p);
-  if (e != cudaSuccess || p.new_capacity == 0) return e;
-  const int most = p.Dqk > p.Dv ? p.Dqk : p.Dv;
-  const int fewest = kMoveThreads / (most * bits / 128) * kMoveUnroll;  // rows of a block, of the wider pool
-  const int kept = p.keep == nullptr && p.keep_all < p.new_capacity ? (p.keep_all < 0 ? 0 : p.keep_all) : p.new_capacity;
-  const int chunks = (kept + fewest - 1) / fewest;
-  if (chunks == 0) return cudaSuccess;
-  const long long blocks = static_cast<long long>(chunks) * p.B * p.Hkv;
+  // A cluster of blocks for each head where heads are few and rows long: four
+  // rows of 131072 took 150 us with a block each.
+  const long long heads = static_cast<long long>(p.B) * p.Hkv;
+  int cluster = 1;
+  while (cluster < 8 && 2 * cluster * heads <= 2LL * sms && p.capacity > 2048 * cluster) cluster *= 2;
+  if (heads * cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(heads * cluster));
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, p);
+  if (e != cudaSuccess) return e;
+  const int kept = p.keep == nullptr ? (p.keep_all < p.new_capacity ? p.keep_all : p.new_capacity) : p.new_capacity;
+  if (kept <= 0) return cudaSuccess;
+  const int chunks = (kept + kMoveThreads - 1) / kMoveThreads;
+  const long long blocks = chunks * heads;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)), 2);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.numAttrs = 1;
   *launches = 2;
-  const dim3 grid(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)), 2);
-  return bits == 4 ? launch(move_kernel<4>, grid, kMoveThreads, stream, p, chunks, blocks)
-                   : launch(move_kernel<16>, grid, kMoveThreads, stream, p, chunks, blocks);
+  return bits == 4 ? cudaLaunchKernelEx(&cfg, move_kernel<4>, p, chunks, blocks)
+                   : cudaLaunchKernelEx(&cfg, move_kernel<16>, p, chunks, blocks);
 }
 
 }  // namespace attn

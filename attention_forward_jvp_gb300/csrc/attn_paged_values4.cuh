@@ -53,8 +53,20 @@ __device__ __forceinline__ void cp_async_n(uint32_t dst, const void* src, bool l
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
 }
 
-__device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half(w & 0xffffu)); }
-__device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ushort_as_half(w >> 16)); }
+__device__ __forceinline__ __half2 as_half2(uint32_t w) {
+  __half2 h;
+  *reinterpret_cast<uint32_t*>(&h) = w;
+  return h;
+}
+__device__ __forceinline__ float half_lo(uint32_t w) { return __low2float(as_half2(w)); }
+__device__ __forceinline__ float half_hi(uint32_t w) { return __high2float(as_half2(w)); }
+// D (16 x 8, fp32) = A (16 x 16) B (16 x 8), fp16
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // half i (a constant) of a row's words
 template <int G>
 __device__ __forceinline__ float half_at(const uint32_t (&w)[G], int i) {
@@ -125,58 +137,74 @@ __device__ __forceinline__ Place4 lookup4(const DecodeParams& p, const int* page
   return x;
 }
 
-// The rows of D elements (d of them real) of those tokens into a tile by a
-// warp, 16 bytes a lane, and their steps and least values behind one another.
-// KEYS: laid out as keys.  A half of the warp copies a half of the tokens.
-template <int D>
+// Keeps a value as it is: what a lane's addresses are made of is otherwise
+// computed again from its number in every step, for want of registers (D 128,
+// 777 instructions a step for 610).
+__device__ __forceinline__ void keep(uint32_t& x) { asm volatile("" : "+r"(x)); }
+__device__ __forceinline__ void keep(const void*& x) { asm volatile("" : "+l"(x)); }
+
+// What a lane copies of the rows of D elements of 32 tokens, 16 bytes at a
+// time, into a tile (KEYS: laid out as keys).  A half of the warp copies a half
+// of the tokens: row i R + lr of it.
+template <int D, bool KEYS>
 struct Rows4 {
   static constexpr int L = D / 32, R = 16 / L;  // lanes of a row, rows of an instruction in each half
   static constexpr int N = 4 * groups4(D);      // bytes of a row's steps and least values
+  uint32_t place;        // of row lr in a tile
+  const void* codes;     // of token lr, head 0, page 0
+  const void* scales;    // of token lane & 15, head 0, page 0
+
+  static __device__ __forceinline__ int lr() { return (threadIdx.x & 15) / L; }
+  static __device__ __forceinline__ int c() { return threadIdx.x % L; }
+  __device__ __forceinline__ void init(const Pool4& pool) {
+    const int key = (threadIdx.x & 16) + lr();
+    place = (KEYS ? key * (D / 2) + key_slot<D>(key, c() >> 1) * 32
+                  : value_row<D>(key) * (D / 2) + value_slot<D>(key, c() >> 1) * 32) + (c() & 1) * 16;
+    codes = pool.codes + lr() * pool.st[2] + 16 * c();
+    scales = pool.scales + (threadIdx.x & 15) * pool.ss[2];
+    keep(place);
+    keep(codes);
+    keep(scales);
+  }
+  // row i R + lr, in a tile at `at - place` (128-byte aligned)
+  static __device__ __forceinline__ uint32_t row_at(uint32_t at, int i) {
+    const int flip = D == 64 ? 0 : (KEYS ? (D == 256 ? (i & 1) << 6 : 0) : (D == 256 ? (i & 3) << 5 : (i & 1) << 5));
+    return (at ^ flip) + i * R * (D / 2);
+  }
+  // all tokens live, the halves in one page each, strides below 2^31
+  __device__ __forceinline__ void copy_whole(const Pool4& pool, const Place4& x, uint32_t tile, uint32_t to_scales) const {
+    const int s1 = static_cast<int>(pool.st[1]), s0 = static_cast<int>(pool.st[0]), s2 = static_cast<int>(pool.st[2]);
+    const char* page = static_cast<const char*>(codes) + static_cast<long long>(x.h) * s1 + static_cast<long long>(x.page) * s0;
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(row_at(tile + place, i)),
+                   "l"(page + static_cast<long long>(x.slot + i * R) * s2)
+                   : "memory");
+    const int t1 = static_cast<int>(pool.ss[1]), t0 = static_cast<int>(pool.ss[0]), t2 = static_cast<int>(pool.ss[2]);
+    cp_async_n<N>(to_scales + (threadIdx.x & 31) * N,
+                  static_cast<const uint16_t*>(scales) + (static_cast<long long>(x.h) * t1 +
+                                                          static_cast<long long>(x.page) * t0 +
+                                                          static_cast<long long>(x.slot) * t2),
+                  true);
+  }
+  // in any case: x has the place of token `lane`; those that are not live become
+  // zeros, as what is behind the d real elements of a row
+  __device__ __forceinline__ void copy(const Pool4& pool, const Place4& x, bool live, int d, uint32_t tile,
+                                       uint32_t to_scales) const {
+    const int lane = threadIdx.x & 31;
+    const long long at = live ? x.page * pool.st[0] + x.h * pool.st[1] + x.slot * pool.st[2] : -1;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const long long row = __shfl_sync(0xffffffffu, at, (lane & 16) + i * R + lr());
+      const bool in = row >= 0 && 32 * c() < d;
+      cp_async_n<16>(row_at(tile + place, i), in ? pool.codes + row + 16 * c() : pool.codes, in);
+    }
+    cp_async_n<N>(to_scales + lane * N,
+                  live ? pool.scales + x.page * pool.ss[0] + x.h * pool.ss[1] + x.slot * pool.ss[2] : pool.scales, live);
+  }
 };
-template <int D, bool KEYS>
-__device__ __forceinline__ uint32_t row_place4(int i) {
-  using X = Rows4<D>;
-  const int lane = threadIdx.x & 31, lr = (lane & 15) / X::L, c = lane % X::L, key = (lane & 16) + i * X::R + lr;
-  return (KEYS ? key * (D / 2) + key_slot<D>(key, c >> 1) * 32
-               : value_row<D>(key) * (D / 2) + value_slot<D>(key, c >> 1) * 32) + (c & 1) * 16;
-}
-// all of them live, their halves in one page each, strides below 2^31
-template <int D, bool KEYS>
-__device__ __forceinline__ void copy_rows4_whole(const Pool4& pool, const Place4& x, uint32_t to, uint32_t scales) {
-  using X = Rows4<D>;
-  const int lane = threadIdx.x & 31, lr = (lane & 15) / X::L, c = lane % X::L;
-  const int s1 = static_cast<int>(pool.st[1]), s0 = static_cast<int>(pool.st[0]), s2 = static_cast<int>(pool.st[2]);
-  const uint8_t* from = pool.codes + static_cast<long long>(x.h) * s1 + static_cast<long long>(x.page) * s0 +
-                        static_cast<long long>(x.slot + lr) * s2 + 16 * c;
-#pragma unroll
-  for (int i = 0; i < X::L; ++i) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + row_place4<D, KEYS>(i)), "l"(from) : "memory");
-    from += static_cast<long long>(X::R) * s2;
-  }
-  const int t1 = static_cast<int>(pool.ss[1]), t0 = static_cast<int>(pool.ss[0]), t2 = static_cast<int>(pool.ss[2]);
-  cp_async_n<X::N>(scales + lane * X::N,
-                   pool.scales + (static_cast<long long>(x.h) * t1 + static_cast<long long>(x.page) * t0 +
-                                  static_cast<long long>(x.slot + (lane & 15)) * t2),
-                   true);
-}
-// in any case: x has the place of token `lane`; those that are not live become zeros
-template <int D, bool KEYS>
-__device__ __forceinline__ void copy_rows4(const Pool4& pool, const Place4& x, bool live, int d, uint32_t to,
-                                           uint32_t scales) {
-  using X = Rows4<D>;
-  const int lane = threadIdx.x & 31, lr = (lane & 15) / X::L, c = lane % X::L;
-  const long long at = live ? x.page * pool.st[0] + x.h * pool.st[1] + x.slot * pool.st[2] : -1;
-#pragma unroll
-  for (int i = 0; i < X::L; ++i) {
-    const long long row = __shfl_sync(0xffffffffu, at, (lane & 16) + i * X::R + lr);
-    const bool in = row >= 0 && 32 * c < d;
-    cp_async_n<16>(to + row_place4<D, KEYS>(i), in ? pool.codes + row + 16 * c : pool.codes, in);
-  }
-  cp_async_n<X::N>(scales + lane * X::N,
-                   live ? pool.scales + x.page * pool.ss[0] + x.h * pool.ss[1] + x.slot * pool.ss[2] : pool.scales, live);
-}
-// `copy` with what the places allow: (true, x, true) for copy_rows4_whole, else
-// (false, x of this lane's token, live) for copy_rows4.  Tells of a page out of
+// `copy` with what the places allow: (true, x, true) for Rows4's copy_whole, else
+// (false, x of this lane's token, live) for its copy.  Tells of a page out of
 // range, whose rows become zeros (apart from the look-up, whose load is on its
 // way).  narrow: pages of a multiple of 16 tokens, strides below 2^31, rows as
 // wide as the kernel's head dims.
@@ -273,52 +301,68 @@ struct Query4 {
   }
 };
 
-// S^T (16 keys x 8 heads, NT groups) of keys key0 .. key0 + 15 of a tile, in
-// units of Query4's scale: sum over the groups of s (n q) + m sum(q), with n q
+// Where a lane reads the keys of a tile: row g, its 64 bits of slot 0 (the
+// slots' numbers are bits 5 and 6 of an address)
+template <int DQ>
+__device__ __forceinline__ uint32_t key_read() {
+  const int g = threadIdx.x >> 2 & 7;
+  uint32_t at = g * (DQ / 2) + key_slot<DQ>(g, 0) * 32 + 8 * (threadIdx.x & 3);
+  keep(at);
+  return at;
+}
+// and the values: row 2 t, word g of slot 0
+template <int DV>
+__device__ __forceinline__ uint32_t value_read() {
+  const int t = threadIdx.x & 3;
+  uint32_t at = value_row<DV>(2 * t) * (DV / 2) + value_slot<DV>(2 * t, 0) * 32 + 4 * (threadIdx.x >> 2 & 7);
+  keep(at);
+  return at;
+}
+
+// S^T (16 keys x 8 heads, NT groups) of keys key0 .. key0 + 15 of a tile (at:
+// its address + key_read; rows: that of its steps + 4 G g), in units of
+// Query4's scale: sum over the groups of s (n q) + m sum(q), with n q
 // by products of n 2^-24 and the sums of a row's least values by one more.
 template <int DQ, int NT>
-__device__ __forceinline__ void scores4(const Query4<DQ, NT>& q, uint32_t tile, uint32_t scales, int key0,
+__device__ __forceinline__ void scores4(const Query4<DQ, NT>& q, uint32_t at, uint32_t rows, int key0,
                                         float (&s)[NT][4]) {
   constexpr int GQ = groups4(DQ);
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint32_t row[2][GQ];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) lds_row<GQ>(scales + (key0 + 8 * i + g) * (4 * GQ), row[i]);
+  for (int i = 0; i < 2; ++i) lds_row<GQ>(rows + (key0 + 8 * i) * (4 * GQ), row[i]);
   {
     uint32_t a[4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      // (columns behind the groups meet zeros: q.sum)
       uint32_t least;
-      if constexpr (GQ == 1) least = t == 0 ? row[i][0] >> 16 : 0u;
-      else if constexpr (GQ == 2) least = t == 0 ? row[i][1] : 0u;
-      else least = t == 0 ? row[i][2] : (t == 1 ? row[i][3] : 0u);
+      if constexpr (GQ == 1) least = row[i][0] >> 16;
+      else if constexpr (GQ == 2) least = row[i][1];
+      else least = threadIdx.x & 1 ? row[i][3] : row[i][2];
       a[i] = a[2 + i] = least;
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-      mma16816<true>(s[n], a, q.sum[n][0], q.sum[n][1]);
-    }
+    for (int n = 0; n < NT; ++n) mma16816_first(s[n], a, q.sum[n][0], q.sum[n][1]);
   }
 #pragma unroll
   for (int b = 0; b < GQ; ++b) {
     uint32_t r[2][2][4];  // row g or g + 8, word
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int key = 8 * i + g;
-      const uint2 w = lds64(tile + (key0 + key) * (DQ / 2) + key_slot<DQ>(key, b) * 32 + 8 * t);
+      const uint2 w = lds64((at ^ (b << 5)) + (key0 + 8 * i) * (DQ / 2));
       nibbles(w.x, r[i][0]);
       nibbles(w.y, r[i][1]);
     }
     float x[NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
-#pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t a[4] = {r[0][j >> 1][2 * (j & 1)], r[1][j >> 1][2 * (j & 1)], r[0][j >> 1][2 * (j & 1) + 1],
                              r[1][j >> 1][2 * (j & 1) + 1]};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma16816<true>(x[n], a, q.q[b][j][n][0], q.q[b][j][n][1]);
+      for (int n = 0; n < NT; ++n) {
+        if (j == 0) mma16816_first(x[n], a, q.q[b][j][n][0], q.q[b][j][n][1]);
+        else mma16816<true>(x[n], a, q.q[b][j][n][0], q.q[b][j][n][1]);
+      }
     }
     const float s0 = half_at<GQ>(row[0], b) * 16777216.f, s1 = half_at<GQ>(row[1], b) * 16777216.f;  // 2^24
 #pragma unroll

@@ -95,12 +95,18 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
     if constexpr (BITS == 4) return lookup4(p, pages, a.t * BN, a.len, a.h);
     else return {decode_lookup(p, p.whole, pages, a.t * BN, a.len), a.h};
   };
+  Rows4<BITS == 4 ? DQ : 64, true> rows;
+  uint32_t key_at = 0;
+  if constexpr (BITS == 4) {
+    rows.init(pw.k);
+    key_at = key_read<DQ>();
+  }
   auto issue = [&](Place& x, int stage) {
     const uint32_t to = ring + stage * P::STAGE;
     if constexpr (BITS == 4) {
       copy_tokens4(p, pw.narrow, x, [&](auto whole, const Place4& y, bool live) {
-        if constexpr (decltype(whole)::value) copy_rows4_whole<DQ, true>(pw.k, y, to, to + P::K_BYTES);
-        else copy_rows4<DQ, true>(pw.k, y, live, p.dqk, to, to + P::K_BYTES);
+        if constexpr (decltype(whole)::value) rows.copy_whole(pw.k, y, to, to + P::K_BYTES);
+        else rows.copy(pw.k, y, live, p.dqk, to, to + P::K_BYTES);
       });
     } else {
       decode_report(p, p.whole, x);
@@ -108,7 +114,7 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
     }
   };
 
-  const DecodeRange w = p.wide ? decode_plan<long long, BN, NW, true>(p, words) : decode_plan<int, BN, NW, true>(p, words);
+  const DecodeRange w = p.wide ? decode_plan<long long, BN, NW>(p, words, NW, warp) : decode_plan<int, BN, NW>(p, words, NW, warp);
   const int count = w.count;
   if (count == 0) return;
   Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len}, ahead = cur;
@@ -165,9 +171,20 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
   const bool once = p.G <= 8 * NT;  // the heads stay for a whole unit
   if (once) load_heads(cur, 0);
 
+  // lane (g, t) has key 8 t + g of a step; its older weight is loaded a step ahead
+  auto mine = [&](const Cursor& a) { return 8 * t < BN && a.t * BN + 8 * t + g < a.len; };
+  const bool adds = pw.w != nullptr && pw.decay != 0.f;
+  auto older = [&](const Cursor& a) {
+    return adds && mine(a) ? pw.w[a.b * pw.ws[0] + a.h * pw.ws[1] + (a.t * BN + 8 * t + g)] : 0.f;
+  };
+  float old = older(cur);
+
   int stage = 0;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
+    Cursor then = cur;
+    if (i + 1 < count) advance(then);
+    const float next_old = i + 1 < count ? older(then) : 0.f;
     __syncwarp();
     if (i + S - 1 < count) {
       issue(next, stage == 0 ? S - 1 : stage - 1);
@@ -177,11 +194,6 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
       }
     }
     cp_async_commit();
-    // lane (g, t) has key 8 t + g of the step
-    const long long key = static_cast<long long>(cur.t) * BN + 8 * t + g;
-    const bool mine = 8 * t < BN && key < cur.len;
-    float old = 0.f;
-    if (mine && pw.w != nullptr && pw.decay != 0.f) old = pw.w[cur.b * pw.ws[0] + cur.h * pw.ws[1] + key];
     cp_async_wait<S - 1>();
     __syncwarp();
 
@@ -196,7 +208,7 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
       for (int kt = 0; kt < TILES; ++kt) {
         float s[NT][4];
         if constexpr (BITS == 4) {
-          scores4<DQ, NT>(q4, sk, sk + P::K_BYTES, 16 * kt, s);
+          scores4<DQ, NT>(q4, sk + key_at, sk + P::K_BYTES + g * (4 * groups4(DQ)), 16 * kt, s);
         } else {
 #pragma unroll
           for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
@@ -219,7 +231,7 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
           }
       }
     }
-    float mineOf = 0.f;
+    float sum_of_mine = 0.f;
 #pragma unroll
     for (int kt = 0; kt < TILES; ++kt)
 #pragma unroll
@@ -227,15 +239,15 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
         float x = sum[kt][r];
         x += __shfl_xor_sync(kAll, x, 1);
         x += __shfl_xor_sync(kAll, x, 2);
-        if (t == 2 * kt + r) mineOf = x;
+        if (t == 2 * kt + r) sum_of_mine = x;
       }
-    if (mine) pw.out[cur.b * pw.os[0] + cur.h * pw.os[1] + key] = fmaf(pw.decay, old, mineOf);
+    if (mine(cur))
+      pw.out[cur.b * pw.os[0] + cur.h * pw.os[1] + (cur.t * BN + 8 * t + g)] = fmaf(pw.decay, old, sum_of_mine);
+    old = next_old;
 
-    if (i + 1 < count) {
-      const bool ends = cur.t + 1 == cur.nt;
-      advance(cur);
-      if (ends && once) load_heads(cur, 0);
-    }
+    const bool ends = then.b != cur.b || then.h != cur.h;
+    cur = then;
+    if (ends && once) load_heads(cur, 0);
     stage = stage + 1 == S ? 0 : stage + 1;
   }
   cp_async_wait<0>();

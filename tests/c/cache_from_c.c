@@ -39,7 +39,7 @@ int main(void) {
   expect("eviction from nothing", attn_paged_evict4(&c, &e, NULL, 0, NULL), ATTN_OK);
   e.sinks = -1;
   expect("sinks -1", attn_paged_evict(&d, &e, NULL, 0, NULL), ATTN_ERR_INVALID_ARG);
-  if (attn_paged_evict_workspace(2, 3, 4, 5) != 2 * 3 * 4 * 5 * 4) ++fails;
+  if (attn_paged_evict_workspace(2, 3, 4, 5) != 2 * 3 * 4 * 5 * 8) ++fails;
   if (attn_paged_decode4_workspace(NULL, 1) != 0) ++fails;
   printf("%d\n", fails);
   return fails != 0;

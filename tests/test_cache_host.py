@@ -252,7 +252,7 @@ def test_weights_refuses(L, four, bad, want):
 @pytest.mark.parametrize("bad,want", [
     (dict(eviction=False), INVALID), (dict(sinks=-1), INVALID), (dict(recent=-1), INVALID), (dict(n_new=-1), INVALID),
     (dict(n_new=5), INVALID), (dict(w=None), INVALID), (dict(w_out=None), INVALID), (dict(pages=None), INVALID),
-    (dict(table_out=None), INVALID), (dict(lens_out=None), INVALID), (dict(ws=None), INVALID), (dict(n=255), INVALID),
+    (dict(table_out=None), INVALID), (dict(lens_out=None), INVALID), (dict(ws=None), INVALID), (dict(n=1023), INVALID),
     (dict(w=FAKE + 2), MISALIGNED), (dict(w_out=FAKE + 1), MISALIGNED), (dict(keep=FAKE + 2), MISALIGNED),
     (dict(pages=FAKE + 2), MISALIGNED), (dict(table_out=FAKE + 2), MISALIGNED), (dict(lens_out=FAKE + 2), MISALIGNED),
     (dict(ws=FAKE + 8), MISALIGNED), (dict(w_out=AT[6]), INVALID), (dict(w_out_stride=(0, 64)), INVALID),
@@ -268,10 +268,10 @@ def test_evict_does_not_write_16_bit_pools_that_share_places(L):
 
 
 def test_evict_workspace(L):
-    assert L.attn_paged_evict_workspace(3, 2, 16, 5) == 4 * 3 * 2 * 80
+    assert L.attn_paged_evict_workspace(3, 2, 16, 5) == 8 * 3 * 2 * 80
     assert L.attn_paged_evict_workspace(1, 1, 1, 0) == 0
     assert L.attn_paged_evict_workspace(-1, 1, 1, 1) == 0
-    assert L.attn_paged_evict_workspace(1, 1, 0x7FFFFFFF, 0x7FFFFFFF) == 4 << 30
+    assert L.attn_paged_evict_workspace(1, 1, 0x7FFFFFFF, 0x7FFFFFFF) == 8 << 30
 
 
 def test_empty_calls_touch_nothing(L):
