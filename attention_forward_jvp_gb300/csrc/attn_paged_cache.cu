@@ -302,9 +302,21 @@ attn_status run_gather(const C* c, GatherParams& p, int bits, int64_t T, const i
   p.n_pages = c->n_pages;
   p.page_size = c->page_size;
   p.err = d.err;
-  const int items = (p.Dqk > p.Dv ? p.Dqk : p.Dv) / 8;
-  const int splits = head_splits(T * items, p.Hkv, d.sms, &p.heads_per_split);
-  if (launch_gather(p, bits, f16, splits, static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
+  const int items = (p.Dqk > p.Dv ? p.Dqk : p.Dv) / 16;
+  // the heads go to more threads only while these do not fill the card once:
+  // each looks its token's place up
+  const int64_t want = (static_cast<int64_t>(d.sms) * 768 + T * items - 1) / (T * items);
+  int splits = static_cast<int>(want < p.Hkv ? want : p.Hkv);
+  splits = splits > 65535 ? 65535 : splits;  // blockIdx.y
+  p.heads_per_split = (p.Hkv + splits - 1) / splits;
+  splits = (p.Hkv + p.heads_per_split - 1) / p.heads_per_split;
+  auto on32 = [](const void* x, const long long* st, int n) {
+    bool ok = aligned(x, 32);
+    for (int i = 0; i < n; ++i) ok = ok && st[i] % 16 == 0;
+    return ok;
+  };
+  const bool wide = on32(k, p.ko, 2) && on32(v, p.vo, 2) && (bits == 4 || (on32(p.k16, p.kp, 3) && on32(p.v16, p.vp, 3)));
+  if (launch_gather(p, bits, f16, wide, splits, static_cast<cudaStream_t>(stream)) != cudaSuccess) return ATTN_ERR_CUDA;
   count_launch(1);
   return ATTN_OK;
 }
@@ -343,7 +355,9 @@ attn_status run_weights(const C* c, WeightParams& p, int bits, int32_t Hq, const
   p.d.G = Hq / c->Hkv;
   p.d.rows = p.d.G;
   p.d.chunks = 1;
-  p.narrow = bits == 4 && p.d.whole && narrow(p.k) && c->Dqk >= 64 ? 1 : 0;
+  bool below = true;
+  for (int i = 0; i < 3; ++i) below = below && p.d.kp[i] >= 0 && p.d.kp[i] < (1 << 30);
+  p.narrow = p.d.whole && (bits == 4 ? narrow(p.k) : below) && c->Dqk >= 64 ? 1 : 0;
   p.f16 = f16 ? 1 : 0;
   p.lse = w->lse;
   p.w = w->w;

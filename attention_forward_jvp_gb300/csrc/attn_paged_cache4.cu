@@ -11,8 +11,10 @@
 // element that x turns with from another lane of the row.  A warp takes heads
 // of one token, whose angles it computes once, the rows of several on their way.
 //
-// Gather: a thread owns eight elements of one token and walks over the heads,
-// several loads in flight.
+// Gather: a thread owns sixteen elements of one token and walks over the heads,
+// the loads of several on their way; what it writes is a whole 32-byte sector.
+// (A warp that looks up 32 tokens and moves their rows one after the other has
+// fewer bytes on their way: 43 us for 37, a prefix of 30001 tokens.)
 //
 // Both are bound by memory: a new token's row is read in 16 bits and written in
 // 4.5, the gather's read in 4.5 or 16 and written in 16.
@@ -27,7 +29,7 @@ namespace attn {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWarps = 8, kAppendUnroll = 4;
+constexpr int kWarps = 8, kAppendUnroll = 2;
 
 // eight neighbouring elements: VEC says that they are one 16-byte word
 template <bool VEC>
@@ -61,60 +63,69 @@ __device__ __forceinline__ void store8(uint16_t* y, const float (&f)[8]) {
   }
 }
 
-// The rotation of a row of which this lane holds elements d0 .. d0 + 7
+// How pairs lie in a row: none turns, element i with i + rot / 2, neighbours
+enum { kStill, kHalves, kNeighbours };
+
+// The rotation of a row of which this lane holds elements d0 .. d0 + 7.  VEC:
+// the rotated width is a multiple of 16, so that all of a lane's elements turn,
+// with another lane's or with one another, or none.
+template <bool F16, bool VEC, int PAIRS>
 struct Turn8 {
   float2 cs[8];
+  int rot, d0;
+  bool any;  // some of this lane's elements turn
 
-  __device__ __forceinline__ void angles(const RopeSpec& r, int d0, int pos) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int d = d0 + j;
-      if (d < r.rot) {
-        const int pair = r.interleaved ? d >> 1 : (d < r.rot / 2 ? d : d - r.rot / 2);
-        cs[j] = turn(r, pair, pos);
-        const bool first = r.interleaved ? !(d & 1) : d < r.rot / 2;
-        if (first) cs[j].y = -cs[j].y;  // x cos - other sin; the second of a pair x cos + other sin
-      } else {
-        cs[j] = make_float2(1.f, 0.f);
-      }
-    }
-  }
-  // f: the elements w; x: the row in memory.  All lanes take part.
-  template <bool F16, bool VEC>
-  __device__ __forceinline__ void apply(const RopeSpec& r, int d0, const uint16_t* x, bool live, const uint4& w,
-                                        float (&f)[8]) const {
-    widen8<F16>(w, f);
-    if (r.rot == 0) return;
-    float o[8];
-    if constexpr (VEC) {  // rot a multiple of 16: a lane's elements turn with another lane's, or with one another
-      if (r.interleaved) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = f[j ^ 1];
-      } else {
-        const int shift = d0 < r.rot / 2 ? r.rot / 16 : (d0 < r.rot ? -(r.rot / 16) : 0);
-        const int from = (threadIdx.x & 31) + shift;
-        widen8<F16>(make_uint4(__shfl_sync(kAll, w.x, from), __shfl_sync(kAll, w.y, from), __shfl_sync(kAll, w.z, from),
-                               __shfl_sync(kAll, w.w, from)),
-                    o);
-      }
-    } else {
+  __device__ __forceinline__ void angles(const RopeSpec& r, int first, int pos) {
+    if constexpr (PAIRS != kStill) {
+      rot = r.rot;
+      d0 = first;
+      any = d0 < rot;
+      const int half = rot / 2;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int d = d0 + j;
-        o[j] = 0.f;
-        if (live && d < r.rot)
-          o[j] = widen<F16>(x[r.interleaved ? d ^ 1 : (d < r.rot / 2 ? d + r.rot / 2 : d - r.rot / 2)]);
+        cs[j] = make_float2(1.f, 0.f);
+        if (d < rot) {
+          cs[j] = turn(r, PAIRS == kNeighbours ? d >> 1 : (d < half ? d : d - half), pos);
+          // x cos - other sin; the second of a pair x cos + other sin
+          if (PAIRS == kNeighbours ? !(j & 1) : d < half) cs[j].y = -cs[j].y;
+        }
       }
     }
+  }
+  // f: the elements w, turned; x: the row in memory.  All lanes take part.
+  __device__ __forceinline__ void apply(const uint16_t* x, bool live, const uint4& w, float (&f)[8]) const {
+    widen8<F16>(w, f);
+    if constexpr (PAIRS != kStill) {
+      float o[8];
+      if constexpr (VEC && PAIRS == kNeighbours) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = d0 + j < r.rot ? f[j] * cs[j].x + o[j] * cs[j].y : f[j];
+        for (int j = 0; j < 8; ++j) o[j] = f[j ^ 1];
+      } else if constexpr (VEC) {
+        const int from = (threadIdx.x & 31) + (any ? (d0 < rot / 2 ? rot / 16 : -(rot / 16)) : 0);
+        widen8<F16>(make_uint4(__shfl_sync(kAll, w.x, from), __shfl_sync(kAll, w.y, from), __shfl_sync(kAll, w.z, from),
+                               __shfl_sync(kAll, w.w, from)),
+                    o);
+      } else {
+        const int half = rot / 2;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int d = d0 + j;
+          o[j] = live && d < rot ? widen<F16>(x[PAIRS == kNeighbours ? d ^ 1 : (d < half ? d + half : d - half)]) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float y = f[j] * cs[j].x + o[j] * cs[j].y;
+        f[j] = (VEC ? any : d0 + j < rot) ? y : f[j];
+      }
+    }
   }
 };
 
-// Rounds a row whose elements d0 .. d0 + 7 this lane holds, and stores it.
-// All lanes take part; d: elements of the row.
-__device__ __forceinline__ void store_row4(const Pool4& pool, long long page, int h, long long slot, int d, int d0,
-                                           bool live, float (&f)[8]) {
+// Rounds a row whose elements d0 .. d0 + 7 this lane holds, and stores it: codes
+// to those of d0, scales to the row's.  All lanes take part; d: its elements.
+__device__ __forceinline__ void store_row4(uint8_t* codes, uint16_t* scales, int d, int d0, bool live, float (&f)[8]) {
   const int lane = threadIdx.x & 31;
   const int lanes = d < 64 ? 4 : 8;  // of a group
   constexpr float kMost = 65504.f;
@@ -136,44 +147,40 @@ __device__ __forceinline__ void store_row4(const Pool4& pool, long long page, in
     }
   }
   const unsigned odds = __ballot_sync(kAll, odd) >> (lane & ~(lanes - 1)) & ((1u << lanes) - 1);
-  if (!live) return;
   __half m = __float2half_rn(lo);
   const float mf = __half2float(m);
   __half s = __float2half_rn(__fdiv_rn(hi - mf, 15.f));
   const float sf = __half2float(s);
-  uint32_t word = 0;
-  if (odds) {
-    m = s = __ushort_as_half(0x7fff);
-  } else if (sf > 0.f) {
-    const float inv = __frcp_rn(sf);  // (finite: s is 2^-24 or more)
-    bool near = false;
-    float n[8];
+  const float inv = __frcp_rn(sf > 0.f ? sf : 1.f);  // (s is 2^-24 or more)
+  bool near = false;
+  float n[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float y = (f[j] - mf) * inv;
-      n[j] = rintf(y);
-      near = near || fabsf(y - n[j]) > 0.4999f;
-    }
-    if (near) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) n[j] = rintf(__fdiv_rn(f[j] - mf, sf));
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)  // (2^23 + n: n in the low bits)
-      word |= (__float_as_uint(fminf(fmaxf(n[j], 0.f), 15.f) + 8388608.f) & 15u) << (4 * j);
+  for (int j = 0; j < 8; ++j) {
+    const float y = (f[j] - mf) * inv;
+    n[j] = rintf(y);
+    near = near || fabsf(y - n[j]) > 0.4999f;
   }
-  uint8_t* codes = pool.codes + page * pool.st[0] + h * pool.st[1] + slot * pool.st[2];
-  *reinterpret_cast<uint32_t*>(codes + d0 / 2) = word;
+  if (near) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) n[j] = rintf(__fdiv_rn(f[j] - mf, sf > 0.f ? sf : 1.f));
+  }
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)  // (2^23 + n: n in the low bits)
+    word |= (__float_as_uint(fminf(fmaxf(n[j], 0.f), 15.f) + 8388608.f) & 15u) << (4 * j);
+  if (odds) m = s = __ushort_as_half(0x7fff);
+  if (odds || !(sf > 0.f)) word = 0;
+  if (!live) return;
+  *reinterpret_cast<uint32_t*>(codes) = word;
   if ((lane & (lanes - 1)) == 0) {
-    uint16_t* to = pool.scales + page * pool.ss[0] + h * pool.ss[1] + slot * pool.ss[2];
     const int g = d0 / 64;
-    to[g] = __half_as_ushort(s);
-    to[groups4(d) + g] = __half_as_ushort(m);
+    scales[g] = __half_as_ushort(s);
+    scales[groups4(d) + g] = __half_as_ushort(m);
   }
 }
 
-template <bool F16, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32) append4_kernel(const __grid_constant__ Append4Params p4) {
+template <bool F16, bool VEC, int PAIRS>
+__global__ void __launch_bounds__(kWarps * 32, 4) append4_kernel(const __grid_constant__ Append4Params p4) {
   griddep_wait();
   griddep_launch_dependents();
   const AppendParams& p = p4.a;
@@ -202,112 +209,167 @@ __global__ void __launch_bounds__(kWarps * 32) append4_kernel(const __grid_const
   if (!placed && !idle && lane == 0 && blockIdx.y == 0) *p.err = 1;
 
   // heads of q, of k and of v, one after the other: `use` for each row that
-  // this lane has eight elements of, those of U rows on their way
+  // this lane has eight elements of, those of U rows on their way; R rows at a
+  // time, in steps of `each` elements
   constexpr int U = VEC ? kAppendUnroll : 1;
   const int first = blockIdx.y * p.heads_per_split;
   const int last = min(first + p.heads_per_split, p.Hq + 2 * p.Hkv);
-  auto heads = [&](const uint16_t* base, long long stride, int D, int lo, int hi, auto use) {
+  auto heads = [&](const uint16_t* x, long long each, int D, int n, auto use) {
     const int L = D / 8, R = 32 / L, d0 = 8 * (lane & (L - 1)), r = lane / L;
+    x += r * each;
+    each *= R;
 #pragma unroll 1
-    for (int h0 = lo; h0 < hi; h0 += R * U) {
+    for (int h = r; h - r < n; h += R * U) {
       uint4 w[U];
+      const uint16_t* y = x;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * R + r;
-        w[u] = load8<VEC>(base + (h < hi ? h : lo) * stride + d0, h < hi);
+        w[u] = load8<VEC>(y + d0, h + u * R < n);
+        y += each;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * R + r;
-        if (h0 + u * R < hi) use(w[u], base + (h < hi ? h : lo) * stride, h, h < hi, d0);
+        use(w[u], x, h + u * R < n, d0);
+        x += each;
       }
     }
   };
-  Turn8 turned;
-  if (first < p.Hq + p.Hkv && pos >= 0) turned.angles(p.r, 8 * (lane & (p.Dqk / 8 - 1)), static_cast<int>(pos));
-  if (pos >= 0) {
-    heads(p.q + t * p.qs[0], p.qs[1], p.Dqk, first, min(last, p.Hq),
-          [&](const uint4& w, const uint16_t* x, int h, bool live, int d0) {
-            float f[8];
-            turned.apply<F16, VEC>(p.r, d0, x, live, w, f);
-            __syncwarp();  // in place: the row has been read
-            if (live) store8<F16, VEC>(p.q_out + t * p.qos[0] + h * p.qos[1] + d0, f);
-          });
-  } else {  // no position: zeros
-    const float zero[8] = {};
-    const int L = p.Dqk / 8;
-    for (int h = first + lane / L; h < min(last, p.Hq); h += 32 / L)
-      store8<F16, VEC>(p.q_out + t * p.qos[0] + h * p.qos[1] + 8 * (lane & (L - 1)), zero);
+  // of the first row of this lane
+  const int Lk = p.Dqk / 8, rk = lane / Lk, dk = 8 * (lane & (Lk - 1)), Lv = p.Dv / 8, rv = lane / Lv, dv = 8 * (lane & (Lv - 1));
+  Turn8<F16, VEC, PAIRS> turned;
+  if (first < p.Hq + p.Hkv) turned.angles(p.r, dk, static_cast<int>(pos));
+  {
+    const int lo = first, n = min(last, p.Hq) - lo;
+    uint16_t* y = p.q_out + t * p.qos[0] + (lo + rk) * p.qos[1] + dk;
+    const long long each = p.qos[1] * (32 / Lk);
+    if (pos >= 0) {
+      heads(p.q + t * p.qs[0] + lo * p.qs[1], p.qs[1], p.Dqk, n, [&](const uint4& w, const uint16_t* x, bool live, int) {
+        float f[8];
+        turned.apply(x, live, w, f);
+        if constexpr (!VEC) __syncwarp();  // in place: the row has been read
+        if (live) store8<F16, VEC>(y, f);
+        y += each;
+      });
+    } else {  // no position: zeros
+      const float zero[8] = {};
+      for (int h = rk; h < n; h += 32 / Lk, y += each) store8<F16, VEC>(y, zero);
+    }
   }
   if (!placed) return;
-  heads(p.k + t * p.ks[0], p.ks[1], p.Dqk, max(first - p.Hq, 0), min(last - p.Hq, p.Hkv),
-        [&](const uint4& w, const uint16_t* x, int h, bool live, int d0) {
-          float f[8];
-          turned.apply<F16, VEC>(p.r, d0, x, live, w, f);
-          store_row4(p4.k, page, h, slot, p.Dqk, d0, live, f);
-        });
-  heads(p.v + t * p.vs[0], p.vs[1], p.Dv, max(first - p.Hq - p.Hkv, 0), min(last - p.Hq - p.Hkv, p.Hkv),
-        [&](const uint4& w, const uint16_t*, int h, bool live, int d0) {
-          float f[8];
-          widen8<F16>(w, f);
-          store_row4(p4.v, page, h, slot, p.Dv, d0, live, f);
-        });
+  {
+    const int lo = max(first - p.Hq, 0), n = min(last - p.Hq, p.Hkv) - lo;
+    uint8_t* codes = p4.k.codes + page * p4.k.st[0] + (lo + rk) * p4.k.st[1] + slot * p4.k.st[2] + dk / 2;
+    uint16_t* scales = p4.k.scales + page * p4.k.ss[0] + (lo + rk) * p4.k.ss[1] + slot * p4.k.ss[2];
+    const long long each = p4.k.st[1] * (32 / Lk), each_scale = p4.k.ss[1] * (32 / Lk);
+    heads(p.k + t * p.ks[0] + lo * p.ks[1], p.ks[1], p.Dqk, n, [&](const uint4& w, const uint16_t* x, bool live, int d0) {
+      float f[8];
+      turned.apply(x, live, w, f);
+      store_row4(codes, scales, p.Dqk, d0, live, f);
+      codes += each;
+      scales += each_scale;
+    });
+  }
+  {
+    const int lo = max(first - p.Hq - p.Hkv, 0), n = min(last - p.Hq - p.Hkv, p.Hkv) - lo;
+    uint8_t* codes = p4.v.codes + page * p4.v.st[0] + (lo + rv) * p4.v.st[1] + slot * p4.v.st[2] + dv / 2;
+    uint16_t* scales = p4.v.scales + page * p4.v.ss[0] + (lo + rv) * p4.v.ss[1] + slot * p4.v.ss[2];
+    const long long each = p4.v.st[1] * (32 / Lv), each_scale = p4.v.ss[1] * (32 / Lv);
+    heads(p.v + t * p.vs[0] + lo * p.vs[1], p.vs[1], p.Dv, n, [&](const uint4& w, const uint16_t*, bool live, int d0) {
+      float f[8];
+      widen8<F16>(w, f);
+      store_row4(codes, scales, p.Dv, d0, live, f);
+      codes += each;
+      scales += each_scale;
+    });
+  }
 }
 
 // ------------------------------------------------------------------- gather
 constexpr int kGatherThreads = 256, kGatherUnroll = 4;
 
-// eight elements of a row in 16 bits
-struct Held16 {
-  uint4 w;
-  __device__ __forceinline__ void load(const uint16_t* pool, const long long (&st)[3], long long page, int h,
-                                       long long slot, int d0) {
-    w = *reinterpret_cast<const uint4*>(pool + page * st[0] + h * st[1] + slot * st[2] + d0);
+// m + n s of the eight elements of a word, rounded
+template <bool F16>
+__device__ __forceinline__ uint4 values8(uint32_t w, float s, float m) {
+  // n in the low bits of a half is the subnormal n 2^-24, 16 n that of an odd
+  // element; n s is exact (15 bits)
+  const float s1 = s * 16777216.f, s16 = s * 1048576.f;
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // elements 2 i, 2 i + 1 and 4 further on
+    const uint32_t a = w >> (8 * i) & 0x000f000fu, b = w >> (8 * i) & 0x00f000f0u;
+    const float2 x = unpack2<true>(a), y = unpack2<true>(b);
+    u[i] = pack2<F16>(fmaf(x.x, s1, m), fmaf(y.x, s16, m));
+    u[2 + i] = pack2<F16>(fmaf(x.y, s1, m), fmaf(y.y, s16, m));
   }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// sixteen elements on their way out
+struct Sixteen {
+  uint4 a, b;
+};
+// WIDE: at a 32-byte boundary
+template <bool WIDE>
+__device__ __forceinline__ Sixteen load16(const uint16_t* x) {
+  Sixteen v;
+  if constexpr (WIDE) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w), "=r"(v.b.x), "=r"(v.b.y), "=r"(v.b.z), "=r"(v.b.w)
+                 : "l"(x));
+  } else {
+    v.a = reinterpret_cast<const uint4*>(x)[0];
+    v.b = reinterpret_cast<const uint4*>(x)[1];
+  }
+  return v;
+}
+template <bool WIDE>
+__device__ __forceinline__ void store16(uint16_t* y, const Sixteen& v) {
+  if constexpr (WIDE) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(y), "r"(v.a.x), "r"(v.a.y), "r"(v.a.z),
+                 "r"(v.a.w), "r"(v.b.x), "r"(v.b.y), "r"(v.b.z), "r"(v.b.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(y)[0] = v.a;
+    reinterpret_cast<uint4*>(y)[1] = v.b;
+  }
+}
+// sixteen elements of a row in 16 bits
+template <bool WIDE>
+struct Held16 {
+  Sixteen v;
+  __device__ __forceinline__ void load(const uint16_t* row, int) { v = load16<WIDE>(row); }
   template <bool F16>
-  __device__ __forceinline__ uint4 value() const {
-    return w;
+  __device__ __forceinline__ Sixteen value() const {
+    return v;
   }
 };
-// eight elements of a row in 4 bits
+// and in 4 bits
 struct Held4 {
-  uint32_t w;
+  uint2 w;
   uint16_t s, m;
-  __device__ __forceinline__ void load(const Pool4& pool, long long page, int h, long long slot, int d, int d0) {
-    w = *reinterpret_cast<const uint32_t*>(pool.codes + page * pool.st[0] + h * pool.st[1] + slot * pool.st[2] + d0 / 2);
-    const uint16_t* at = pool.scales + page * pool.ss[0] + h * pool.ss[1] + slot * pool.ss[2] + d0 / 64;
-    s = at[0];
-    m = at[groups4(d)];
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint16_t* scales, int groups) {
+    w = *reinterpret_cast<const uint2*>(codes);
+    s = scales[0];
+    m = scales[groups];
   }
   template <bool F16>
-  __device__ __forceinline__ uint4 value() const {
-    // n in the low bits of a half is the subnormal n 2^-24, 16 n that of an odd
-    // element; n s is exact (15 bits)
-    const float m1 = __half2float(__ushort_as_half(m)), s1 = __half2float(__ushort_as_half(s)) * 16777216.f;
-    const float s16 = s1 * 0.0625f;
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {  // elements 2 i, 2 i + 1 and 4 further on
-      const uint32_t a = w >> (8 * i) & 0x000f000fu, b = w >> (8 * i) & 0x00f000f0u;
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-      u[i] = pack2<F16>(fmaf(x.x, s1, m1), fmaf(y.x, s16, m1));
-      u[2 + i] = pack2<F16>(fmaf(x.y, s1, m1), fmaf(y.y, s16, m1));
-    }
-    return make_uint4(u[0], u[1], u[2], u[3]);
+  __device__ __forceinline__ Sixteen value() const {
+    const float a = widen<true>(s), b = widen<true>(m);
+    return {values8<F16>(w.x, a, b), values8<F16>(w.y, a, b)};
   }
 };
 
-template <int BITS, bool F16>
+template <int BITS, bool F16, bool WIDE>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_constant__ GatherParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int items = max(p.Dqk, p.Dv) / 8;  // a power of two, at most 32
-  const int row_in_block = threadIdx.x / items, d0 = 8 * (threadIdx.x & (items - 1));
+  const int items = max(p.Dqk, p.Dv) / 16;  // a power of two, at most 16
+  const int row_in_block = threadIdx.x / items, d0 = 16 * (threadIdx.x & (items - 1));
   const long long t0 = static_cast<long long>(blockIdx.x) * (kGatherThreads / items);
   long long t = t0 + row_in_block;
   const bool none = t >= p.T;
   if (none) t = t0;  // (takes part in the search)
-  const long long b = sequence_of(p.offsets, p.B, t);
+  const int b = sequence_of(p.offsets, p.B, t);
   if (none || t >= p.offsets[p.B]) return;
   const long long pos = p.seq_lens[b] - static_cast<long long>(p.offsets[b + 1]) + t;
   long long page = -1, slot = 0;
@@ -323,34 +385,42 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
   uint16_t* ko = p.k_out + t * p.ko[1] + d0;
   uint16_t* vo = p.v_out + t * p.vo[1] + d0;
   if (!placed) {
+    const Sixteen zero = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
     for (int h = first; h < last; ++h) {
-      if (in_k) *reinterpret_cast<uint4*>(ko + h * p.ko[0]) = make_uint4(0u, 0u, 0u, 0u);
-      if (in_v) *reinterpret_cast<uint4*>(vo + h * p.vo[0]) = make_uint4(0u, 0u, 0u, 0u);
+      if (in_k) store16<WIDE>(ko + h * p.ko[0], zero);
+      if (in_v) store16<WIDE>(vo + h * p.vo[0], zero);
     }
     return;
   }
-  constexpr int U = kGatherUnroll;
-  using Held = typename std::conditional<BITS == 4, Held4, Held16>::type;
+  // K and V of head 0
+  const uint16_t* k16 = p.k16 + page * p.kp[0] + slot * p.kp[2] + d0;
+  const uint16_t* v16 = p.v16 + page * p.vp[0] + slot * p.vp[2] + d0;
+  const uint8_t* k4 = p.k.codes + page * p.k.st[0] + slot * p.k.st[2] + d0 / 2;
+  const uint8_t* v4 = p.v.codes + page * p.v.st[0] + slot * p.v.st[2] + d0 / 2;
+  const uint16_t* ks = p.k.scales + page * p.k.ss[0] + slot * p.k.ss[2] + d0 / 64;
+  const uint16_t* vs = p.v.scales + page * p.v.ss[0] + slot * p.v.ss[2] + d0 / 64;
+  constexpr int U = BITS == 4 ? kGatherUnroll : kGatherUnroll / 2;
+  using Held = typename std::conditional<BITS == 4, Held4, Held16<WIDE>>::type;
 #pragma unroll 1
   for (int h0 = first; h0 < last; h0 += U) {
     Held k[U], v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u < last ? h0 + u : h0;
+      const long long h = h0 + u < last ? h0 + u : h0;
       if constexpr (BITS == 4) {
-        if (in_k) k[u].load(p.k, page, h, slot, p.Dqk, d0);
-        if (in_v) v[u].load(p.v, page, h, slot, p.Dv, d0);
+        if (in_k) k[u].load(k4 + h * p.k.st[1], ks + h * p.k.ss[1], groups4(p.Dqk));
+        if (in_v) v[u].load(v4 + h * p.v.st[1], vs + h * p.v.ss[1], groups4(p.Dv));
       } else {
-        if (in_k) k[u].load(p.k16, p.kp, page, h, slot, d0);
-        if (in_v) v[u].load(p.v16, p.vp, page, h, slot, d0);
+        if (in_k) k[u].load(k16 + h * p.kp[1], 0);
+        if (in_v) v[u].load(v16 + h * p.vp[1], 0);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u;
+      const long long h = h0 + u;
       if (h >= last) break;
-      if (in_k) *reinterpret_cast<uint4*>(ko + h * p.ko[0]) = k[u].template value<F16>();
-      if (in_v) *reinterpret_cast<uint4*>(vo + h * p.vo[0]) = v[u].template value<F16>();
+      if (in_k) store16<WIDE>(ko + h * p.ko[0], k[u].template value<F16>());
+      if (in_v) store16<WIDE>(vo + h * p.vo[0], v[u].template value<F16>());
     }
   }
 }
@@ -374,15 +444,24 @@ cudaError_t launch(void (*kernel)(P), const P& p, dim3 grid, int threads, cudaSt
 cudaError_t launch_append4(const Append4Params& p, bool vec, bool f16, int splits, cudaStream_t stream) {
   const long long blocks = (p.a.T + kWarps - 1) / kWarps;
   const dim3 grid(static_cast<unsigned>(blocks), splits);
-  if (f16) return launch(vec ? append4_kernel<true, true> : append4_kernel<true, false>, p, grid, kWarps * 32, stream);
-  return launch(vec ? append4_kernel<false, true> : append4_kernel<false, false>, p, grid, kWarps * 32, stream);
+  const int pairs = p.a.r.rot == 0 ? kStill : (p.a.r.interleaved ? kNeighbours : kHalves);
+  auto pick = [&](auto half, auto words) {
+    constexpr bool F16 = decltype(half)::value, VEC = decltype(words)::value;
+    if (pairs == kStill) return launch(append4_kernel<F16, VEC, kStill>, p, grid, kWarps * 32, stream);
+    if (pairs == kHalves) return launch(append4_kernel<F16, VEC, kHalves>, p, grid, kWarps * 32, stream);
+    return launch(append4_kernel<F16, VEC, kNeighbours>, p, grid, kWarps * 32, stream);
+  };
+  if (f16) return vec ? pick(std::true_type(), std::true_type()) : pick(std::true_type(), std::false_type());
+  return vec ? pick(std::false_type(), std::true_type()) : pick(std::false_type(), std::false_type());
 }
 
-cudaError_t launch_gather(const GatherParams& p, int bits, bool f16, int splits, cudaStream_t stream) {
-  const int rows = kGatherThreads / ((p.Dqk > p.Dv ? p.Dqk : p.Dv) / 8);
+cudaError_t launch_gather(const GatherParams& p, int bits, bool f16, bool wide, int splits, cudaStream_t stream) {
+  const int rows = kGatherThreads / ((p.Dqk > p.Dv ? p.Dqk : p.Dv) / 16);
   const dim3 grid(static_cast<unsigned>((p.T + rows - 1) / rows), splits);
-  if (bits == 16) return launch(gather_kernel<16, false>, p, grid, kGatherThreads, stream);
-  return launch(f16 ? gather_kernel<4, true> : gather_kernel<4, false>, p, grid, kGatherThreads, stream);
+  if (bits == 16)
+    return launch(wide ? gather_kernel<16, false, true> : gather_kernel<16, false, false>, p, grid, kGatherThreads, stream);
+  if (f16) return launch(wide ? gather_kernel<4, true, true> : gather_kernel<4, true, false>, p, grid, kGatherThreads, stream);
+  return launch(wide ? gather_kernel<4, false, true> : gather_kernel<4, false, false>, p, grid, kGatherThreads, stream);
 }
 
 }  // namespace attn

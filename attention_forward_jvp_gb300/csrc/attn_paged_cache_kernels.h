@@ -40,8 +40,8 @@ struct GatherParams {
 };
 
 cudaError_t launch_append4(const Append4Params& p, bool vec, bool f16, int splits, cudaStream_t stream);
-// bits: 16 or 4; f16: the type that 4 bits become
-cudaError_t launch_gather(const GatherParams& p, int bits, bool f16, int splits, cudaStream_t stream);
+// bits: 16 or 4; f16: the type that 4 bits become; wide: rows on 32-byte boundaries
+cudaError_t launch_gather(const GatherParams& p, int bits, bool f16, bool wide, int splits, cudaStream_t stream);
 
 // ------------------------------------------------------------------ decode
 constexpr int kDecode4BN = 32;  // keys of a step
@@ -71,6 +71,7 @@ struct WeightParams {
   DecodeParams d;     // (no values, workspace or outputs)
   Pool4 k;            // of a cache in 4 bits
   int narrow;         // copy_tokens4
+  int subs;           // set by the launch: warps of a range, each with a key head of its own
   int f16;            // the type of q
   const float* lse;   // [B, Hkv * G]
   const float* w;     // or null

@@ -53,6 +53,11 @@ struct Decode4Plan {
   static constexpr int SMEM = NW * WARP_BYTES + MISC_BYTES;
 };
 
+template <int BN, int NW>
+__device__ __noinline__ DecodeRange decode_plan_wide(const DecodeParams& p, const DecodeWords& s, int R, int own) {
+  return decode_plan<long long, BN, NW>(p, s, R, own);
+}
+
 template <int DQ, int DV, bool F16, int NT>
 __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
     attn_paged_decode4_kernel(const __grid_constant__ Decode4Params p4) {
@@ -107,7 +112,7 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
 
   // ---- this warp's range, and the places of its first steps
   const int me = blockIdx.x * R + own;
-  DecodeRange w = p.wide ? decode_plan<long long, BN, NW>(p, words, R, own) : decode_plan<int, BN, NW>(p, words, R, own);
+  DecodeRange w = p.wide ? decode_plan_wide<BN, NW>(p, words, R, own) : decode_plan<int, BN, NW>(p, words, R, own);
   const int count = w.count;
   Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len};  // the step computed next
   Cursor ahead = cur;                                  // the step that `next` is of
@@ -125,7 +130,8 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
   if (lane == 0) ranges[warp] = w;
 
   float acc[NT][GV][4][4];  // [64 columns][product]: columns 8 g + 2 i of heads 2 t, 2 t + 1, then 8 g + 2 i + 1 (16-fold)
-  float eight[F16 ? 1 : NT][F16 ? 1 : GV][4];  // sum P' 8, the same in every row (bf16)
+  // sum P' 8 (bf16): that of groups 2 k, in every row of the first eight, and 2 k + 1
+  float eight[F16 ? 1 : NT][F16 ? 1 : (GV + 1) / 2][4];
   float stat[NT][4];        // rows 0 .. GV - 1: sum P m, 4: sum P; rows 8 ..: sum P s (of no use in fp16)
   float m[NT][2], l[NT][2];
   Query4<DQ, NT> q;
@@ -142,7 +148,7 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
         stat[n][e] = 0.f;
 #pragma unroll
         for (int b = 0; b < GV; ++b) {
-          if constexpr (!F16) eight[n][b][e] = 0.f;
+          if constexpr (!F16) eight[n][b / 2][e] = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[n][b][i][e] = 0.f;
         }
@@ -178,7 +184,7 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
         less[e] = 0.f;
         if constexpr (!F16) {
           base[e] += 8.f * __shfl_sync(ALL, stat[n][2 + e], 4 * b + t);
-          less[e] = eight[n][b][e];
+          less[e] = eight[n][b / 2][2 * (b & 1) + e];
         }
       }
 #pragma unroll
@@ -192,7 +198,6 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
     }
   };
 
-  clear();
   Rows4<DQ, true> k_rows;
   Rows4<DV, false> v_rows;
   k_rows.init(p4.k);
@@ -207,22 +212,26 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
           k_rows.copy_whole(p4.k, y, to, ks);
           v_rows.copy_whole(p4.v, y, tv, vs);
         } else {
-          k_rows.copy(p4.k, y, live, p.dqk, to, ks);
-          v_rows.copy(p4.v, y, live, p.dv, tv, vs);
+          k_rows.copy(p4.k, y, live, p.dqk, to + k_rows.place, ks);
+          v_rows.copy(p4.v, y, live, p.dv, tv + v_rows.place, vs);
         }
       });
     };
-    load_q(cur);
 #pragma unroll
     for (int j = 0; j < S - 1; ++j) {
       if (j < count) issue(now[j], j);
       cp_async_commit();
     }
 
-    int t0 = cur.t;  // first step of the unit in this warp
+    int t0 = -1;  // first step of the unit in this warp; -1: this one
     int stage = 0;
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
+      if (t0 < 0) {
+        t0 = cur.t;
+        clear();
+        load_q(cur);
+      }
       // refill the stage of the step before this one, which every lane has read
       __syncwarp();
       if (i + S - 1 < count) {
@@ -239,8 +248,12 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
       const uint32_t sk = ring + stage * P::STAGE, sv = sk + P::K_BYTES, sks = sv + P::V_BYTES, svs = sks + P::KS_BYTES;
       const int live = cur.len - cur.t * BN;  // keys of this step
       float s[2][NT][4];
+      if constexpr (NT == 1 && DQ <= 128) {
+        scores4<DQ, NT, 2>(q, sk + key_at, sks + g * (4 * P::GQ), 0, s);
+      } else {
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) scores4<DQ, NT>(q, sk + key_at, sks + g * (4 * P::GQ), 16 * kt, s[kt]);
+        for (int kt = 0; kt < 2; ++kt) scores4<DQ, NT, 1>(q, sk + key_at, sks + g * (4 * P::GQ), 16 * kt, s + kt);
+      }
       // S' - m, and whether one passes the room above the reference, or a step
       // of the values of key `lane` the largest so far
       bool grows = false;
@@ -305,10 +318,7 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
             stat[n][2 + e] *= a;
 #pragma unroll
             for (int b = 0; b < GV; ++b) {
-              if constexpr (!F16) {
-                eight[n][b][e] *= a;
-                eight[n][b][2 + e] *= a;
-              }
+              if constexpr (!F16) eight[n][b / 2][2 * (b & 1) + e] *= a;
 #pragma unroll
               for (int d = 0; d < 4; ++d) {
                 acc[n][b][d][e] *= a;
@@ -367,13 +377,14 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma16816<true>(stat[n], a, ph[kt][n][0], ph[kt][n][1]);
-          if constexpr (F16) mma16816<true>(stat[n], a, pl[kt][n][0], pl[kt][n][1]);
+          mma4(stat[n], a, ph[kt][n][0], ph[kt][n][1]);
+          if constexpr (F16) mma4(stat[n], a, pl[kt][n][0], pl[kt][n][1]);
         }
 #pragma unroll
         for (int b = 0; b < GV; ++b) {
           uint32_t ps[NT][2], less[F16 ? NT : 1][2];
-          const uint32_t eights[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};  // 8 2^-24
+          constexpr uint32_t E = 0x00080008u;  // 8 2^-24
+          const uint32_t eights[4] = {b & 1 ? 0u : E, b & 1 ? E : 0u, b & 1 ? 0u : E, b & 1 ? E : 0u};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -383,7 +394,7 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
                 less[n][o] = fma_half2(pl[kt][n][o], step[b][o],
                                        fma_half2(ph[kt][n][o], step[b][o], ps[n][o] ^ 0x80008000u));
             }
-            if constexpr (!F16) mma16816<true>(eight[n][b], eights, ps[n][0], ps[n][1]);
+            if constexpr (!F16) mma4(eight[n][b / 2], eights, ps[n][0], ps[n][1]);
           }
           uint32_t word[2][2];  // of keys 2 t + e, and 8 further on
 #pragma unroll
@@ -403,8 +414,8 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
               const uint32_t v[4] = {r[0][2 * i], r[0][2 * i + 1], r[1][2 * i], r[1][2 * i + 1]};
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                mma16816<true>(acc[n][b][2 * c + i], v, ps[n][0], ps[n][1]);
-                if constexpr (F16) mma16816<true>(acc[n][b][2 * c + i], v, less[n][0], less[n][1]);
+                mma4(acc[n][b][2 * c + i], v, ps[n][0], ps[n][1]);
+                if constexpr (F16) mma4(acc[n][b][2 * c + i], v, less[n][0], less[n][1]);
               }
             }
           }
@@ -428,7 +439,7 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
             __syncwarp();
             finish(n, scratch);
             __syncwarp();
-#pragma unroll
+#pragma unroll 1
             for (int x = lane; x < 8 * (DV / 4); x += 32) {
               const int r = x / (DV / 4), c4 = x % (DV / 4);
               const float ma = __shfl_sync(ALL, m[n][0], r >> 1), mb = __shfl_sync(ALL, m[n][1], r >> 1);
@@ -455,10 +466,8 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
             held_end[own] = ranges[warp].lo + i + (cur.nt - 1 - cur.t);
           }
         } else {
-          clear();
           advance(cur);
-          t0 = 0;
-          load_q(cur);
+          t0 = -1;
         }
       } else {
         ++cur.t;

@@ -5,13 +5,15 @@
 // Two kernels.  `select` has a block for each (sequence, key head), or a cluster
 // of up to eight where there are few: a radix selection of the M-th largest
 // weight in three passes (12, 10 and 10 bits) over weights turned to whole
-// numbers of the same order, which stay in registers while a warp's stretch of
-// the row is no longer than 512; the blocks of a cluster add up their histograms
-// from one another's shared memory.  Then the places of the kept tokens in
-// order, each warp counting what its stretch keeps before all write.  Ties go by
-// the same order, so that the choice is a function of the weights alone.
-// `move` copies the rows of the kept tokens: a warp looks up 32 of them at once,
-// then moves whole rows, 16 bytes a lane, several of them on their way.
+// numbers of the same order, held in shared memory where they fit; the blocks of
+// a cluster add up their histograms from one another's shared memory.  Then the
+// places of the kept tokens in order, each warp counting what its stretch of the
+// row keeps before all write.  Ties go by the same order, so that the choice is
+// a function of the weights alone.  (With the numbers in registers and the
+// passes unrolled the same took twice as long: instructions that are run once
+// are read from memory once each.)  `move` copies the rows of the kept tokens: a
+// warp looks up 32 of them at once, then moves whole rows, 16 bytes a lane,
+// several of them on their way.
 //
 // What bounds it: memory, the kept rows read and written once.
 #include "attn_paged_cache_kernels.h"
@@ -22,7 +24,8 @@ namespace attn {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectMost = 1536;  // numbers that a warp holds, at most: a multiple of 256
 
 // whole numbers in the order of the weights: -0 as 0, NaN above all
 __device__ __forceinline__ uint32_t ordered(float w) {
@@ -74,12 +77,18 @@ __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
   return v;
 }
 
-constexpr int kKept = 16;             // weights that a lane keeps
-constexpr int kStretch = 32 * kKept;  // and a warp
+__device__ __forceinline__ void set_peer_word(int* p, uint32_t rank, int v) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
 
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int histogram[4096 + 1024 + 1024];  // one for each pass
-  __shared__ int found[2];                       // the digit, the numbers above it
+// `room`: numbers that a warp's part of the shared memory holds
+__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_constant__ EvictParams p, int room) {
+  extern __shared__ __align__(16) uint32_t numbers[];
+  __shared__ __align__(16) int histogram[4096 + 1024 + 1024];  // one for each pass
+  __shared__ int total[4096];                                  // of a cluster's blocks
+  __shared__ int found[2];                                     // the digit, the numbers above it
   __shared__ int sums[kSelectWarps];
   __shared__ int counts[2][kSelectWarps];
   __shared__ int totals[2];
@@ -89,6 +98,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
   const int bh = blockIdx.x / C, b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Share s = share_of(p, b);
+  const float* w = p.w + b * p.ws[0] + h * p.ws[1];
+  float* to = p.w_out + b * p.wos[0] + h * p.wos[1];
+  const int step = C * kSelectThreads, first = rank * kSelectThreads + tid;
   if (h == 0 && rank == 0) {
     if (s.odd && tid == 0) *p.err = 1;
     if (tid == 0) p.lens_out[b] = min(s.n, s.keep);
@@ -96,82 +108,103 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
       p.table_out[b * p.table_out_stride + i] =
           s.over && i < p.n_new ? p.pages[b * p.pages_stride + i] : p.page_table[b * p.table_stride + i];
   }
-  const float* w = p.w + b * p.ws[0] + h * p.ws[1];
-  float* to = p.w_out + b * p.wos[0] + h * p.wos[1];
-  const int step = C * kSelectThreads, first = rank * kSelectThreads + tid;
   if (!s.over) {
+#pragma unroll 4
     for (long long i = first; i < p.places; i += step) to[i] = w[i];
     return;
   }
-  for (int i = tid; i < (4096 + 1024 + 1024) / 4; i += kSelectThreads)
-    reinterpret_cast<int4*>(histogram)[i] = make_int4(0, 0, 0, 0);
-  for (long long i = s.keep + static_cast<long long>(first); i < p.places; i += step) to[i] = 0.f;
-
-  // this warp's stretch of the row
-  const int warps = C * kSelectWarps;
-  const long long stretch = ((s.n + warps - 1LL) / warps + 31) / 32 * 32;
-  const int from = static_cast<int>(min((rank * kSelectWarps + warp) * stretch, static_cast<long long>(s.n)));
-  const int end = static_cast<int>(min(from + stretch, static_cast<long long>(s.n)));
-  const bool stays = stretch <= kStretch;
-  float x[kKept];
-  auto load = [&](int at) {
+  // This warp's stretch of the row.  Of its tokens shared memory has the numbers,
+  // all of them or (`pieces`) as many as fit, taken again for each pass: 1 of one
+  // that is kept whatever its weight (no weight's number is below 2^22), 0 behind
+  // the stretch.  The others, of which `most` are kept, lie in [lo, hi).
+  const int lo = s.sinks, hi = s.n - s.recent, most = s.keep - s.sinks - s.recent;
+  const int stretch = static_cast<int>(((s.n + C * kSelectWarps - 1LL) / (C * kSelectWarps) + 31) / 32 * 32);
+  const int start = static_cast<int>(
+      min((static_cast<long long>(rank) * kSelectWarps + warp) * stretch, static_cast<long long>(s.n)));
+  const int count = min(stretch, s.n - start);
+  const bool pieces = count > room;
+  uint32_t* const mine = numbers + warp * room;
+  constexpr int EACH = 8;  // numbers of a lane at a time
+  auto take = [&](int c0) {
+    __syncwarp();
+    const int n = min(count - c0, room);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 32 * EACH) {
+      float x[EACH];
 #pragma unroll
-    for (int k = 0; k < kKept; ++k) {
-      const int j = at + 32 * k + lane;
-      x[k] = j < end ? w[j] : 0.f;
+      for (int c = 0; c < EACH; ++c) {
+        const int i = i0 + 32 * c + lane;
+        x[c] = i < n ? w[start + c0 + i] : 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < EACH; ++c) {
+        const int i = i0 + 32 * c + lane, j = start + c0 + i;
+        const uint32_t u = j < lo || j >= hi ? 1u : ordered(x[c]);
+        mine[i] = i < n ? u : 0u;
+      }
     }
+    __syncwarp();
   };
-  if (stays) load(from);
-  // use(j, weight) for the stretch's tokens j, 32 neighbouring ones at a time; all lanes take part
+  if (!pieces) take(0);
+  // use(j, numbers of tokens j, j + 32, ...) for the stretch; all lanes take part
   auto each = [&](auto use) {
 #pragma unroll 1
-    for (int at = from; at < end; at += kStretch) {
-      if (!stays) load(at);
+    for (int c0 = 0; c0 < count; c0 += room) {
+      if (pieces) take(c0);
+      const int n = min(count - c0, room);
+#pragma unroll 1
+      for (int i0 = 0; i0 < n; i0 += 32 * EACH) {
+        uint32_t u[EACH];
 #pragma unroll
-      for (int k = 0; k < kKept; ++k)
-        if (at + 32 * k < end) use(at + 32 * k + lane, x[k]);
+        for (int c = 0; c < EACH; ++c) u[c] = mine[i0 + 32 * c + lane];
+        use(start + c0 + i0 + lane, u);
+      }
     }
   };
+  for (int i = tid; i < (4096 + 1024 + 1024) / 4; i += kSelectThreads)
+    reinterpret_cast<int4*>(histogram)[i] = make_int4(0, 0, 0, 0);
+  __syncthreads();
 
-  // the others' weights lie in [lo, hi); `most` of them are kept
-  const int lo = s.sinks, hi = s.n - s.recent, most = s.keep - s.sinks - s.recent;
-  uint32_t least = 0;  // the smallest kept number
-  int ties = 0;        // how many that are equal to it
+  uint32_t least = 0xffffffffu;  // the smallest kept number
+  int ties = 0;                  // how many that are equal to it
   if (most > 0) {
     int left = most;
-    __syncthreads();
-#pragma unroll
+    least = 0;
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass == 0 ? 12 : 10, shift = pass == 0 ? 20 : (pass == 1 ? 10 : 0);
       int* bins = histogram + (pass == 0 ? 0 : (pass == 1 ? 4096 : 5120));
-      each([&](int j, float v) {
-        const uint32_t u = ordered(v);
-        const bool in = j >= lo && j < hi && j < end && (pass == 0 || u >> (shift + bits) == least);
-        const unsigned all = __ballot_sync(kAll, in);
-        if (all == 0) return;
-        const int bin = u >> shift & ((1 << bits) - 1);
-        const int one = __shfl_sync(kAll, bin, __ffs(all) - 1);
-        // (the same bin for all: one addition, where a row of equal weights would take 32)
-        if (__ballot_sync(kAll, in && bin == one) == all) {
-          if (lane == 0) atomicAdd(&bins[one], __popc(all));
-        } else if (in) {
-          atomicAdd(&bins[bin], 1);
+      each([&](int, const uint32_t (&u)[EACH]) {
+#pragma unroll
+        for (int c = 0; c < EACH; ++c) {
+          const bool in = pass == 0 || u[c] >> (shift + bits) == least;  // (0 and 1: bin 0, which no other number has)
+          const unsigned all = __ballot_sync(kAll, in);
+          const int bin = u[c] >> shift & ((1 << bits) - 1), leader = __ffs(all) - 1;
+          const int one = __shfl_sync(kAll, bin, leader);
+          const unsigned same = __ballot_sync(kAll, in && bin == one);
+          // (one addition for all that are in the first one's bin: equal weights would take 32)
+          const int more = bin == one ? (lane == leader ? __popc(same) : 0) : 1;
+          if (in && more) atomicAdd(&bins[bin], more);
         }
       });
-      if (C > 1) cluster_sync();
-      else __syncthreads();
-      // the digits from the largest on, four or one to a thread
-      constexpr int kMost = 4;
-      const int mine = pass == 0 ? kMost : 1, top = (1 << bits) - 1 - mine * tid;
-      int c[kMost], sum = 0;
-#pragma unroll
-      for (int i = 0; i < kMost; ++i) {
-        c[i] = 0;
-        if (i < mine) {
-          for (int r = 0; r < C; ++r) c[i] += C > 1 ? peer_word(&bins[top - i], r) : bins[top - i];
+      if (C > 1) {  // each block adds up its part of the bins, for all of them
+        cluster_sync();
+        const int part = (1 << bits) / C;
+        for (int i = tid; i < part; i += kSelectThreads) {
+          int c = 0;
+          for (int r = 0; r < C; ++r) c += peer_word(&bins[rank * part + i], r);
+          for (int r = 0; r < C; ++r) set_peer_word(&total[rank * part + i], r, c);
         }
-        sum += c[i];
+        cluster_sync();
+        bins = total;
+      } else {
+        __syncthreads();
       }
+      // the digits from the largest on, eight or two to a thread
+      const int mine = pass == 0 ? 8 : 2, top = (1 << bits) - 1 - mine * tid;
+      int sum = 0;
+#pragma unroll 2
+      for (int i = 0; i < mine; ++i) sum += bins[top - i];
       int above = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -180,17 +213,17 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
       }
       if (lane == 31) sums[warp] = above;
       __syncthreads();
-      int before = lane < warp ? sums[lane] : 0;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(kAll, before, o);
-      above += before - sum;
-#pragma unroll
-      for (int i = 0; i < kMost; ++i) {
-        if (i < mine && above < left && above + c[i] >= left) {
-          found[0] = top - i;
-          found[1] = above;
+      above += __reduce_add_sync(kAll, lane < warp ? sums[lane] : 0) - sum;
+      if (above < left && above + sum >= left) {  // the digit is one of this thread's
+#pragma unroll 1
+        for (int i = 0; i < mine; ++i) {
+          const int c = bins[top - i];
+          if (above < left && above + c >= left) {
+            found[0] = top - i;
+            found[1] = above;
+          }
+          above += c;
         }
-        above += c[i];
       }
       __syncthreads();
       least = least << bits | static_cast<uint32_t>(found[0]);
@@ -198,26 +231,25 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     }
     ties = left;
   }
-  // what the stretch keeps for its weight, and its ties
+  // what the warp's stretch keeps for its weight, and its ties
   int above = 0, equal = 0;
-  each([&](int j, float v) {
-    const bool in = j < end, sure = in && (j < lo || j >= hi);
-    const uint32_t u = ordered(v);
-    above += __popc(__ballot_sync(kAll, sure || (in && most > 0 && u > least)));
-    equal += __popc(__ballot_sync(kAll, in && !sure && most > 0 && u == least));
+  each([&](int, const uint32_t (&u)[EACH]) {
+#pragma unroll
+    for (int c = 0; c < EACH; ++c) {
+      above += u[c] == 1u || u[c] > least ? 1 : 0;
+      equal += u[c] == least ? 1 : 0;
+    }
   });
+  above = __reduce_add_sync(kAll, above);
+  equal = __reduce_add_sync(kAll, equal);
   if (lane == 0) {
     counts[0][warp] = above;
     counts[1][warp] = equal;
   }
   __syncthreads();
   if (warp == 0) {
-    int a = counts[0][lane], e = counts[1][lane];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      a += __shfl_xor_sync(kAll, a, o);
-      e += __shfl_xor_sync(kAll, e, o);
-    }
+    const int a = __reduce_add_sync(kAll, lane < kSelectWarps ? counts[0][lane] : 0);
+    const int e = __reduce_add_sync(kAll, lane < kSelectWarps ? counts[1][lane] : 0);
     if (lane == 0) {
       totals[0] = a;
       totals[1] = e;
@@ -229,31 +261,42 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     aboves += peer_word(&totals[0], lane);
     equals += peer_word(&totals[1], lane);
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    aboves += __shfl_xor_sync(kAll, aboves, o);
-    equals += __shfl_xor_sync(kAll, equals, o);
-  }
+  aboves = __reduce_add_sync(kAll, aboves);
+  equals = __reduce_add_sync(kAll, equals);
   // places of the stretch: behind what the warps before it keep
   int at = aboves + min(equals, ties);
   int2* index = p.index + static_cast<long long>(bh) * p.new_capacity;
-  each([&](int j, float v) {
-    const bool in = j < end, sure = in && (j < lo || j >= hi);
-    const uint32_t u = ordered(v);
-    const bool tie = in && !sure && most > 0 && u == least;
-    const unsigned all_ties = __ballot_sync(kAll, tie);
-    const bool keep = sure || (in && most > 0 && u > least) ||
-                      (tie && equals + __popc(all_ties & ((1u << lane) - 1)) < ties);
-    const unsigned kept = __ballot_sync(kAll, keep);
-    if (keep) {
-      const int k = at + __popc(kept & ((1u << lane) - 1));
-      const int e = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
-      index[k] = make_int2(p.page_table[b * p.table_stride + e], j - e * p.page_size);
-      to[k] = v;
+  const int* pages = p.page_table + b * p.table_stride;
+  const unsigned before = (1u << lane) - 1;
+  each([&](int j0, const uint32_t (&u)[EACH]) {
+    int k[EACH], page[EACH];  // k: the place that a token goes to, or -1
+    float x[EACH];
+#pragma unroll
+    for (int c = 0; c < EACH; ++c) {
+      const unsigned all_ties = __ballot_sync(kAll, u[c] == least);
+      const bool keep = u[c] == 1u || u[c] > least || (u[c] == least && equals + __popc(all_ties & before) < ties);
+      const unsigned kept = __ballot_sync(kAll, keep);
+      k[c] = keep ? at + __popc(kept & before) : -1;
+      at += __popc(kept);
+      equals += __popc(all_ties);
     }
-    at += __popc(kept);
-    equals += __popc(all_ties);
+#pragma unroll
+    for (int c = 0; c < EACH; ++c) {  // (the loads of all on their way)
+      const int j = j0 + 32 * c;
+      page[c] = k[c] >= 0 ? pages[p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size] : 0;
+      x[c] = k[c] >= 0 ? w[j] : 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < EACH; ++c) {
+      const int j = j0 + 32 * c;
+      if (k[c] >= 0) {
+        index[k[c]] = make_int2(page[c], p.page_shift >= 0 ? j & (p.page_size - 1) : j % p.page_size);
+        to[k[c]] = x[c];
+      }
+    }
   });
+#pragma unroll 4
+  for (long long i = s.keep + static_cast<long long>(first); i < p.places; i += step) to[i] = 0.f;
   if (C > 1) cluster_sync();  // a block's shared memory stays until the others have read it
 }
 
@@ -330,9 +373,23 @@ cudaError_t launch_evict(const EvictParams& p, int bits, int sms, cudaStream_t s
   int cluster = 1;
   while (cluster < 8 && 2 * cluster * heads <= 2LL * sms && p.capacity > 2048 * cluster) cluster *= 2;
   if (heads * cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long part = static_cast<long long>(p.capacity) / (cluster * kSelectWarps) + 33;  // of a warp, at most
+  const int room = static_cast<int>(part < kSelectMost ? (part + 255) / 256 * 256 : kSelectMost);
+  static bool attr_done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_done[dev]) {
+    e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             4 * kSelectMost * kSelectWarps);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(heads * cluster));
   cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = 4 * static_cast<size_t>(room) * kSelectWarps;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -342,7 +399,7 @@ cudaError_t launch_evict(const EvictParams& p, int bits, int sms, cudaStream_t s
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, p);
+  e = cudaLaunchKernelEx(&cfg, select_kernel, p, room);
   if (e != cudaSuccess) return e;
   const int kept = p.keep == nullptr ? (p.keep_all < p.new_capacity ? p.keep_all : p.new_capacity) : p.new_capacity;
   if (kept <= 0) return cudaSuccess;
@@ -350,6 +407,7 @@ cudaError_t launch_evict(const EvictParams& p, int bits, int sms, cudaStream_t s
   const long long blocks = chunks * heads;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)), 2);
   cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   *launches = 2;
   return bits == 4 ? cudaLaunchKernelEx(&cfg, move_kernel<4>, p, chunks, blocks)

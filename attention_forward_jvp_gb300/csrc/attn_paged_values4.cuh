@@ -60,9 +60,15 @@ __device__ __forceinline__ __half2 as_half2(uint32_t w) {
 }
 __device__ __forceinline__ float half_lo(uint32_t w) { return __low2float(as_half2(w)); }
 __device__ __forceinline__ float half_hi(uint32_t w) { return __high2float(as_half2(w)); }
-// D (16 x 8, fp32) = A (16 x 16) B (16 x 8), fp16
-__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16; in any order among others
+__device__ __forceinline__ void mma4(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// D = A B
+__device__ __forceinline__ void mma4_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
@@ -188,16 +194,17 @@ struct Rows4 {
                   true);
   }
   // in any case: x has the place of token `lane`; those that are not live become
-  // zeros, as what is behind the d real elements of a row
-  __device__ __forceinline__ void copy(const Pool4& pool, const Place4& x, bool live, int d, uint32_t tile,
-                                       uint32_t to_scales) const {
+  // zeros, as what is behind the d real elements of a row.  (Out of line, once
+  // for all: a kernel's instructions come from memory too.)
+  __device__ __noinline__ static void copy(const Pool4& pool, Place4 x, bool live, int d, uint32_t row0,
+                                           uint32_t to_scales) {
     const int lane = threadIdx.x & 31;
     const long long at = live ? x.page * pool.st[0] + x.h * pool.st[1] + x.slot * pool.st[2] : -1;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const long long row = __shfl_sync(0xffffffffu, at, (lane & 16) + i * R + lr());
       const bool in = row >= 0 && 32 * c() < d;
-      cp_async_n<16>(row_at(tile + place, i), in ? pool.codes + row + 16 * c() : pool.codes, in);
+      cp_async_n<16>(row_at(row0, i), in ? pool.codes + row + 16 * c() : pool.codes, in);
     }
     cp_async_n<N>(to_scales + lane * N,
                   live ? pool.scales + x.page * pool.ss[0] + x.h * pool.ss[1] + x.slot * pool.ss[2] : pool.scales, live);
@@ -319,60 +326,74 @@ __device__ __forceinline__ uint32_t value_read() {
   return at;
 }
 
-// S^T (16 keys x 8 heads, NT groups) of keys key0 .. key0 + 15 of a tile (at:
-// its address + key_read; rows: that of its steps + 4 G g), in units of
-// Query4's scale: sum over the groups of s (n q) + m sum(q), with n q
-// by products of n 2^-24 and the sums of a row's least values by one more.
-template <int DQ, int NT>
+// S^T (16 keys x 8 heads, NT groups) of the TILES times 16 keys of a tile from
+// key0 on (at: its address + key_read; rows: that of its steps + 4 G g), in
+// units of Query4's scale: sum over the groups of s (n q) + m sum(q), with n q
+// by products of n 2^-24 and the sums of a row's least values by one more.  The
+// products of all groups and tiles take turns: four of one group depend on one
+// another.
+template <int DQ, int NT, int TILES>
 __device__ __forceinline__ void scores4(const Query4<DQ, NT>& q, uint32_t at, uint32_t rows, int key0,
-                                        float (&s)[NT][4]) {
+                                        float (*s)[NT][4]) {
   constexpr int GQ = groups4(DQ);
-  uint32_t row[2][GQ];
+  uint32_t row[TILES][2][GQ];
+  uint2 w[TILES][2][GQ];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) lds_row<GQ>(rows + (key0 + 8 * i) * (4 * GQ), row[i]);
-  {
+  for (int k = 0; k < TILES; ++k)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lds_row<GQ>(rows + (key0 + 16 * k + 8 * i) * (4 * GQ), row[k][i]);
+#pragma unroll
+      for (int b = 0; b < GQ; ++b) w[k][i][b] = lds64((at ^ (b << 5)) + (key0 + 16 * k + 8 * i) * (DQ / 2));
+    }
+#pragma unroll
+  for (int k = 0; k < TILES; ++k) {
     uint32_t a[4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // (columns behind the groups meet zeros: q.sum)
       uint32_t least;
-      if constexpr (GQ == 1) least = row[i][0] >> 16;
-      else if constexpr (GQ == 2) least = row[i][1];
-      else least = threadIdx.x & 1 ? row[i][3] : row[i][2];
+      if constexpr (GQ == 1) least = row[k][i][0] >> 16;
+      else if constexpr (GQ == 2) least = row[k][i][1];
+      else least = threadIdx.x & 1 ? row[k][i][3] : row[k][i][2];
       a[i] = a[2 + i] = least;
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) mma16816_first(s[n], a, q.sum[n][0], q.sum[n][1]);
+    for (int n = 0; n < NT; ++n) mma4_first(s[k][n], a, q.sum[n][0], q.sum[n][1]);
   }
+  float x[TILES][GQ][NT][4];
 #pragma unroll
-  for (int b = 0; b < GQ; ++b) {
-    uint32_t r[2][2][4];  // row g or g + 8, word
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint2 w = lds64((at ^ (b << 5)) + (key0 + 8 * i) * (DQ / 2));
-      nibbles(w.x, r[i][0]);
-      nibbles(w.y, r[i][1]);
-    }
-    float x[NT][4];
+    for (int k = 0; k < TILES; ++k)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t a[4] = {r[0][j >> 1][2 * (j & 1)], r[1][j >> 1][2 * (j & 1)], r[0][j >> 1][2 * (j & 1) + 1],
-                             r[1][j >> 1][2 * (j & 1) + 1]};
+      for (int b = 0; b < GQ; ++b) {
+        uint32_t a[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t word = j < 2 ? w[k][i][b].x : w[k][i][b].y, y = j & 1 ? word >> 8 : word;
+          a[i] = y & 0x000f000fu;
+          a[2 + i] = y & 0x00f000f0u;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (j == 0) mma4_first(x[k][b][n], a, q.q[b][j][n][0], q.q[b][j][n][1]);
+          else mma4(x[k][b][n], a, q.q[b][j][n][0], q.q[b][j][n][1]);
+        }
+      }
+#pragma unroll
+  for (int k = 0; k < TILES; ++k)
+#pragma unroll
+    for (int b = 0; b < GQ; ++b) {
+      const float s0 = half_at<GQ>(row[k][0], b) * 16777216.f, s1 = half_at<GQ>(row[k][1], b) * 16777216.f;  // 2^24
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (j == 0) mma16816_first(x[n], a, q.q[b][j][n][0], q.q[b][j][n][1]);
-        else mma16816<true>(x[n], a, q.q[b][j][n][0], q.q[b][j][n][1]);
+        s[k][n][0] = fmaf(x[k][b][n][0], s0, s[k][n][0]);
+        s[k][n][1] = fmaf(x[k][b][n][1], s0, s[k][n][1]);
+        s[k][n][2] = fmaf(x[k][b][n][2], s1, s[k][n][2]);
+        s[k][n][3] = fmaf(x[k][b][n][3], s1, s[k][n][3]);
       }
     }
-    const float s0 = half_at<GQ>(row[0], b) * 16777216.f, s1 = half_at<GQ>(row[1], b) * 16777216.f;  // 2^24
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      s[n][0] = fmaf(x[n][0], s0, s[n][0]);
-      s[n][1] = fmaf(x[n][1], s0, s[n][1]);
-      s[n][2] = fmaf(x[n][2], s1, s[n][2]);
-      s[n][3] = fmaf(x[n][3], s1, s[n][3]);
-    }
-  }
 }
 
 }  // namespace attn

@@ -21,6 +21,36 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 16;
 
+// What a lane copies of 16 rows of D 16-bit elements, as copy_rows lays them out
+template <int D>
+struct Rows16 {
+  static constexpr int L = D / 8 < 32 ? D / 8 : 32, R = 32 / L;  // lanes of a row, rows of an instruction
+  uint32_t place;      // of row lr in a tile
+  const void* from;    // of token lr, head 0, page 0
+  __device__ __forceinline__ void init(const DecodeParams& p) {
+    const int lane = threadIdx.x & 31, lr = lane / L, c = lane % L;
+    place = (c >> 3) * 128 + lr * (2 * D) + (((c & 7) ^ lr) << 4);
+    from = p.k + lr * p.kp[2] + 8 * c;
+    keep(place);
+    keep(from);
+  }
+  // all live, in one page, strides below 2^30 elements
+  __device__ __forceinline__ void copy_whole(const DecodeParams& p, int page, int h, int slot, uint32_t tile) const {
+    const int s0 = static_cast<int>(p.kp[0]), s1 = static_cast<int>(p.kp[1]), s2 = 2 * static_cast<int>(p.kp[2]);
+    const char* x = static_cast<const char*>(from) + 2 * (static_cast<long long>(h) * s1 + static_cast<long long>(page) * s0);
+#pragma unroll
+    for (int i = 0; i < 16; i += R)
+      asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(((tile + place) ^ ((i & 7) << 4)) + i * (2 * D)),
+                   "l"(x + static_cast<long long>(slot + i) * s2)
+                   : "memory");
+  }
+};
+// (out of line, once for all calls)
+template <int D>
+__device__ __noinline__ void copy_rows_any(const DecodeParams& p, DecodePlace x, int h, uint32_t tile) {
+  copy_rows<D, D * 2, 128>(p, p.whole, x, p.k + h * p.kp[1], p.kp, p.dqk, tile);
+}
+
 template <int DQ, int BITS, int NT>
 struct WeightPlan {
   static constexpr int BN = BITS == 4 ? kDecode4BN : kDecodeBN;
@@ -28,7 +58,7 @@ struct WeightPlan {
   static constexpr int STAGE = K_BYTES + (BITS == 4 ? BN * 4 * groups4(DQ) : 0);
   static constexpr int MISC_BYTES = (8 * 32 + 16) * kDecodeMaxWarps;
   static constexpr int FIT = 226 * 1024 - MISC_BYTES;
-  static constexpr int REGS = (DQ / 8 + 8) * NT + 72;
+  static constexpr int REGS = (DQ / 8 + 8) * NT + (BITS == 16 && DQ <= 128 ? DQ / 4 : 0) + 64;
   static constexpr int NW_REGS = REGS <= 128 ? 16 : (REGS <= 160 ? 12 : 8);
   static constexpr int NW = FIT / NW_REGS / STAGE >= 3 ? NW_REGS : 8;
   static constexpr int S = FIT / NW / STAGE >= 6 ? 6 : FIT / NW / STAGE;
@@ -41,6 +71,10 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
     weights_kernel(const __grid_constant__ WeightParams pw) {
   using P = WeightPlan<DQ, BITS, NT>;
   constexpr int BN = P::BN, S = P::S, NW = P::NW, THREADS = NW * 32, TILES = BN / 16;
+  // The keys of a step of 16 bits go to registers at once, so that its stage is
+  // filled again before the products: 192 KB on their way to an SM for 128.
+  constexpr bool EARLY = BITS == 16 && DQ <= 128;
+  constexpr int AHEAD = EARLY ? S : S - 1;  // steps on their way
   const DecodeParams& p = pw.d;
   extern __shared__ __align__(128) char weight_smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -48,6 +82,8 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
   char* misc = weight_smem + NW * S * P::STAGE;
   const DecodeWords words{reinterpret_cast<int*>(misc), reinterpret_cast<uint32_t*>(misc) + THREADS,
                           reinterpret_cast<long long*>(misc + 8 * THREADS)};
+  // warps of a range, with neighbouring key heads of the same tokens; this one's
+  const int R = NW / pw.subs, own = warp / pw.subs, sub = warp - own * pw.subs;
   griddep_wait();
   griddep_launch_dependents();
 
@@ -55,20 +91,35 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
     const int n = p.seq_lens[b];
     return n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
   };
-  // behind the lengths
-  if (pw.out != pw.w) {
-    constexpr long long PIECE = 4096;
-    const long long pieces = (pw.places + PIECE - 1) / PIECE, all = pieces * p.B * p.Hkv;
-    for (long long x = blockIdx.x; x < all; x += gridDim.x) {
-      const long long row = x / pieces, at = (x - row * pieces) * PIECE;
-      const int b = static_cast<int>(row / p.Hkv), h = static_cast<int>(row - static_cast<long long>(b) * p.Hkv);
-      const long long end = min(at + PIECE, pw.places);
-      float* to = pw.out + b * pw.os[0] + h * pw.os[1];
-      const float* from = pw.w == nullptr ? nullptr : pw.w + b * pw.ws[0] + h * pw.ws[1];
-      for (long long j = max(at, static_cast<long long>(length(b))) + tid; j < end; j += THREADS)
-        to[j] = from == nullptr ? 0.f : from[j];
+  // What is behind the lengths, copied while the first keys are on their way.
+  // (512 rows of 8208 places before them, or by the warps that are done: 10 and
+  // 20 us more.)
+  auto copy_rest = [&]() {
+    if (pw.out == pw.w) return;
+    constexpr int EACH = 16, PIECE = 32 * EACH;
+    const int heads = p.Hkv * pw.subs;
+    const long long pieces = (pw.places + PIECE - 1) / PIECE, all = pieces * p.B * heads;
+#pragma unroll 1
+    for (long long x = blockIdx.x + static_cast<long long>(gridDim.x) * warp; x < all; x += static_cast<long long>(gridDim.x) * NW) {
+      const long long row = x / pieces, at = (x - row * pieces) * PIECE + lane;
+      const int b = static_cast<int>(row / heads), h = static_cast<int>(row - static_cast<long long>(b) * heads);
+      const int len = length(b);
+      if (at - lane + PIECE <= len) continue;
+      float* to = pw.out + b * pw.os[0] + h * pw.os[1] + at;
+      const float* from = pw.w == nullptr ? nullptr : pw.w + b * pw.ws[0] + h * pw.ws[1] + at;
+      float v[EACH];
+#pragma unroll
+      for (int k = 0; k < EACH; ++k) {
+        const long long j = at + 32 * k;
+        v[k] = from != nullptr && j >= len && j < pw.places ? from[32 * k] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < EACH; ++k) {
+        const long long j = at + 32 * k;
+        if (j >= len && j < pw.places) to[32 * k] = v[k];
+      }
     }
-  }
+  };
 
   struct Cursor {
     int b, h, t, nt, len;
@@ -92,42 +143,53 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
   using Place = typename std::conditional<BITS == 4, Place4, Place16>::type;
   auto lookup = [&](const Cursor& a) -> Place {
     const int* pages = p.page_table + a.b * p.table_stride;
-    if constexpr (BITS == 4) return lookup4(p, pages, a.t * BN, a.len, a.h);
-    else return {decode_lookup(p, p.whole, pages, a.t * BN, a.len), a.h};
+    if constexpr (BITS == 4) return lookup4(p, pages, a.t * BN, a.len, a.h * pw.subs + sub);
+    else return {decode_lookup(p, p.whole, pages, a.t * BN, a.len), a.h * pw.subs + sub};
   };
   Rows4<BITS == 4 ? DQ : 64, true> rows;
+  Rows16<DQ> rows16;
   uint32_t key_at = 0;
   if constexpr (BITS == 4) {
     rows.init(pw.k);
     key_at = key_read<DQ>();
+  } else {
+    rows16.init(p);
   }
-  auto issue = [&](Place& x, int stage) {
+  auto issue = [&](const Place& x, int stage) {
     const uint32_t to = ring + stage * P::STAGE;
     if constexpr (BITS == 4) {
       copy_tokens4(p, pw.narrow, x, [&](auto whole, const Place4& y, bool live) {
         if constexpr (decltype(whole)::value) rows.copy_whole(pw.k, y, to, to + P::K_BYTES);
-        else rows.copy(pw.k, y, live, p.dqk, to, to + P::K_BYTES);
+        else rows.copy(pw.k, y, live, p.dqk, to + rows.place, to + P::K_BYTES);
       });
     } else {
       decode_report(p, p.whole, x);
-      copy_rows<DQ, DQ * 2, 128>(p, p.whole, x, p.k + x.h * p.kp[1], p.kp, p.dqk, to);
+      // (of a whole page all lanes have the place of the first token)
+      if (pw.narrow && x.n >= 16 && static_cast<unsigned>(x.page) < static_cast<unsigned>(p.n_pages))
+        rows16.copy_whole(p, x.page, x.h, x.slot, to);
+      else
+        copy_rows_any<DQ>(p, x, x.h, to);
     }
   };
 
-  const DecodeRange w = p.wide ? decode_plan<long long, BN, NW>(p, words, NW, warp) : decode_plan<int, BN, NW>(p, words, NW, warp);
+  const DecodeRange w = p.wide ? decode_plan<long long, BN, NW>(p, words, R, own) : decode_plan<int, BN, NW>(p, words, R, own);
   const int count = w.count;
-  if (count == 0) return;
   Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len}, ahead = cur;
-#pragma unroll 1
-  for (int j = 0; j < S - 1; ++j) {
+  Place next, now[AHEAD];
+#pragma unroll
+  for (int j = 0; j <= AHEAD; ++j) {
     if (j < count) {
-      Place x = lookup(ahead);
-      issue(x, j);
-      if (j + 1 < count) advance(ahead);
+      (j < AHEAD ? now[j < AHEAD ? j : 0] : next) = lookup(ahead);
+      if (j + 1 < count && j < AHEAD) advance(ahead);
     }
+  }
+#pragma unroll
+  for (int j = 0; j < AHEAD; ++j) {
+    if (j < count) issue(now[j], j);
     cp_async_commit();
   }
-  Place next = lookup(ahead);
+  copy_rest();
+  if (count == 0) return;
 
   // queries and LSEs of 8 NT heads
   constexpr float kLog2e = 1.4426950408889634f;
@@ -135,7 +197,7 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
   uint32_t q16[BITS == 16 ? DQ / 16 : 1][NT][2];
   float lse[NT][2];  // of heads 2 t, 2 t + 1, times log2(e)
   auto load_heads = [&](const Cursor& a, int g0) {
-    const long long head = static_cast<long long>(a.h) * p.G + g0;
+    const long long head = (static_cast<long long>(a.h) * pw.subs + sub) * p.G + g0;
     const uint16_t* base = p.q + a.b * p.qs[0] + head * p.qs[1];
     const int n_rows = p.G - g0;
     if constexpr (BITS == 4) {
@@ -162,42 +224,67 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
         const int r = 8 * n + 2 * t + e;
         float x = INFINITY;  // (a head that is none, or without keys: no weight)
         if (r < n_rows) {
-          x = pw.lse[static_cast<long long>(a.b) * p.Hkv * p.G + head + r] * kLog2e;
+          x = pw.lse[static_cast<long long>(a.b) * p.Hkv * pw.subs * p.G + head + r] * kLog2e;
           if (x == -INFINITY) x = INFINITY;
         }
         lse[n][e] = x;
       }
   };
   const bool once = p.G <= 8 * NT;  // the heads stay for a whole unit
-  if (once) load_heads(cur, 0);
 
   // lane (g, t) has key 8 t + g of a step; its older weight is loaded a step ahead
-  auto mine = [&](const Cursor& a) { return 8 * t < BN && a.t * BN + 8 * t + g < a.len; };
   const bool adds = pw.w != nullptr && pw.decay != 0.f;
-  auto older = [&](const Cursor& a) {
-    return adds && mine(a) ? pw.w[a.b * pw.ws[0] + a.h * pw.ws[1] + (a.t * BN + 8 * t + g)] : 0.f;
+  const float* w_row;
+  float* out_row;  // of the unit's key 8 t + g
+  auto rows_of = [&](const Cursor& a) {
+    const int h = a.h * pw.subs + sub;
+    w_row = adds ? pw.w + a.b * pw.ws[0] + h * pw.ws[1] + (8 * t + g) : nullptr;
+    out_row = pw.out + a.b * pw.os[0] + h * pw.os[1] + (8 * t + g);
   };
+  auto mine = [&](const Cursor& a) { return 8 * t < BN && a.t * BN + 8 * t + g < a.len; };
+  auto older = [&](const Cursor& a) { return adds && mine(a) ? w_row[a.t * BN] : 0.f; };
+  rows_of(cur);
   float old = older(cur);
+  bool fresh = true;  // the unit's heads are to be loaded
 
   int stage = 0;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
+    if (fresh && once) load_heads(cur, 0);
     Cursor then = cur;
     if (i + 1 < count) advance(then);
+    fresh = then.h != cur.h || then.b != cur.b;
+    float* const out = out_row;
+    if (fresh) rows_of(then);
     const float next_old = i + 1 < count ? older(then) : 0.f;
-    __syncwarp();
-    if (i + S - 1 < count) {
-      issue(next, stage == 0 ? S - 1 : stage - 1);
-      if (i + S < count) {
-        advance(ahead);
-        next = lookup(ahead);
-      }
-    }
-    cp_async_commit();
-    cp_async_wait<S - 1>();
-    __syncwarp();
-
     const uint32_t sk = ring + stage * P::STAGE;
+    auto refill = [&](int to) {
+      if (i + AHEAD < count) {
+        issue(next, to);
+        if (i + AHEAD + 1 < count) {
+          advance(ahead);
+          next = lookup(ahead);
+        }
+      }
+      cp_async_commit();
+    };
+    const uint32_t k_row = sk + ((lane >> 3 & 1) * 8 + (lane & 7)) * (DQ * 2);
+    auto k16 = [&](int ks, uint32_t (&a)[4]) { ldsm4(a, k_row + (((2 * ks + (lane >> 4)) ^ (lane & 7)) << 4)); };
+    uint32_t ka[EARLY ? DQ / 16 : 1][4];
+    if constexpr (EARLY) {
+      cp_async_wait<S - 1>();
+      __syncwarp();
+#pragma unroll
+      for (int ks = 0; ks < DQ / 16; ++ks) k16(ks, ka[ks]);
+      __syncwarp();
+      refill(stage);
+    } else {
+      __syncwarp();
+      refill(stage == 0 ? S - 1 : stage - 1);
+      cp_async_wait<S - 1>();
+      __syncwarp();
+    }
+
     float sum[TILES][2];
 #pragma unroll
     for (int kt = 0; kt < TILES; ++kt) sum[kt][0] = sum[kt][1] = 0.f;
@@ -208,18 +295,17 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
       for (int kt = 0; kt < TILES; ++kt) {
         float s[NT][4];
         if constexpr (BITS == 4) {
-          scores4<DQ, NT>(q4, sk + key_at, sk + P::K_BYTES + g * (4 * groups4(DQ)), 16 * kt, s);
+          scores4<DQ, NT, 1>(q4, sk + key_at, sk + P::K_BYTES + g * (4 * groups4(DQ)), 16 * kt, &s);
         } else {
 #pragma unroll
           for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-          const int mi = lane >> 3, l8 = lane & 7;
-          const uint32_t k_row = sk + ((mi & 1) * 8 + l8) * (DQ * 2);
 #pragma unroll
           for (int ks = 0; ks < DQ / 16; ++ks) {
-            uint32_t ka[4];
-            ldsm4(ka, k_row + (((2 * ks + (mi >> 1)) ^ l8) << 4));
+            uint32_t now[4];
+            if constexpr (!EARLY) k16(ks, now);
+            const uint32_t (&a)[4] = EARLY ? ka[EARLY ? ks : 0] : now;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<F16>(s[n], ka, q16[ks][n][0], q16[ks][n][1]);
+            for (int n = 0; n < NT; ++n) mma16816<F16>(s[n], a, q16[ks][n][0], q16[ks][n][1]);
           }
         }
 #pragma unroll
@@ -241,21 +327,22 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
         x += __shfl_xor_sync(kAll, x, 2);
         if (t == 2 * kt + r) sum_of_mine = x;
       }
-    if (mine(cur))
-      pw.out[cur.b * pw.os[0] + cur.h * pw.os[1] + (cur.t * BN + 8 * t + g)] = fmaf(pw.decay, old, sum_of_mine);
+    if (mine(cur)) out[cur.t * BN] = fmaf(pw.decay, old, sum_of_mine);
     old = next_old;
-
-    const bool ends = then.b != cur.b || then.h != cur.h;
     cur = then;
-    if (ends && once) load_heads(cur, 0);
     stage = stage + 1 == S ? 0 : stage + 1;
   }
   cp_async_wait<0>();
 }
 
 template <int DQ, int BITS, bool F16, int NT>
-cudaError_t launch_nt(const WeightParams& p, int ctas, cudaStream_t stream) {
+cudaError_t launch_nt(WeightParams p, int ctas, cudaStream_t stream) {
   using P = WeightPlan<DQ, BITS, NT>;
+  p.subs = 1;  // as in the decode over 4 bits
+  while (p.subs < 8 && P::NW % (2 * p.subs) == 0 && p.d.Hkv % 2 == 0) {
+    p.subs *= 2;
+    p.d.Hkv /= 2;
+  }
   static bool attr_done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
