@@ -198,7 +198,7 @@ Layout4 layout4_of(const attn_paged_cache4* c, int Hq, int sms) {
   Layout4 l;
   l.dq = c->Dqk < 64 ? 64 : c->Dqk;
   l.dv = c->Dv < 64 ? 64 : c->Dv;
-  const int G = Hq / c->Hkv, most = decode4_rows(l.dv);
+  const int G = Hq / c->Hkv, most = decode4_rows(l.dv, G);
   l.chunks = (G + most - 1) / most;
   l.rows = (G + l.chunks - 1) / l.chunks;
   const size_t warps = static_cast<size_t>(sms) * kDecodeMaxWarps;  // ranges

@@ -46,10 +46,14 @@ cudaError_t launch_gather(const GatherParams& p, int bits, bool f16, bool wide, 
 // ------------------------------------------------------------------ decode
 constexpr int kDecode4BN = 32;  // keys of a step
 
-// Query heads of a warp at most, in groups of 8: each takes DV / 4 registers of
-// accumulators and more for the corrections.  More heads go to more warps, which
-// walk over the same steps at the same time.
-constexpr int decode4_rows(int dv) { return dv == 64 ? 32 : (dv == 128 ? 24 : 16); }
+// Query heads of a warp at most, for G on a key head, in groups of 8: a second
+// group shares the making of operands with the first and takes registers from
+// it, so that fewer warps are resident.  More heads go to more warps, which walk
+// over the same steps at the same time.  16 sequences of up to 32768 on two key
+// heads, one group a warp and two (us): 256/256, 16 heads 91 and 123; 256/128 64
+// and 70, with 32 heads 111 and 99; 64/64 41.5 and 39.4, with 32 heads 64 and 58
+// (four groups).
+constexpr int decode4_rows(int dv, int G) { return dv == 256 || (dv == 128 && G <= 16) ? 8 : 16; }
 
 struct Decode4Params {
   DecodeParams d;  // (its 16-bit pools unused; Hkv, G, rows, chunks by the launch)
@@ -61,7 +65,7 @@ struct Decode4Params {
   int subs, heads;
 };
 
-// The decode kernel over a cache in 4 bits for kernel head dims DQ, DV and nt
+// The decode kernel over a cache in 4 bits for kernel head dims DQ, DV and nt (1, 2)
 // groups of 8 query heads to a unit, followed, when p.d.split, by the join
 template <int DQ, int DV, bool F16>
 cudaError_t launch_decode4(Decode4Params& p, int nt, int ctas, cudaStream_t stream);

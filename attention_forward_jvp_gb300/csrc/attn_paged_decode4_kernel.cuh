@@ -36,10 +36,10 @@ struct Decode4Plan {
   static constexpr int BN = kDecode4BN, GQ = groups4(DQ), GV = groups4(DV);
   static constexpr int K_BYTES = BN * DQ / 2, V_BYTES = BN * DV / 2, KS_BYTES = BN * 4 * GQ, VS_BYTES = BN * 4 * GV;
   static constexpr int STAGE = K_BYTES + V_BYTES + KS_BYTES + VS_BYTES;
-  static constexpr int MISC_BYTES = (8 * 32 + 16 + 24 + sizeof(DecodeRange)) * kDecodeMaxWarps;
+  static constexpr int MISC_BYTES = (8 * 32 + 16 + 16 + 24 + sizeof(DecodeRange)) * kDecodeMaxWarps;
   static constexpr int FIT = 226 * 1024 - MISC_BYTES;
   // O, its corrections and statistics; Q
-  static constexpr int REGS = (DV / 4 + 4 * GV + 4) * NT + (DQ / 8 + 4) * NT + 80;
+  static constexpr int REGS = (DV / 4 + 4 * GV + 4) * NT + (DQ / 8 + 4) * NT + 64;
   static constexpr int NW_REGS = REGS <= 128 ? 16 : (REGS <= 160 ? 12 : 8);
   static constexpr int S = FIT / NW_REGS / STAGE >= 4 ? 4 : (FIT / NW_REGS / STAGE >= 3 ? 3 : 2);
   static constexpr int PITCH = DV + 4;
@@ -77,6 +77,8 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
   DecodeRange* ranges = reinterpret_cast<DecodeRange*>(misc + P::MISC_BYTES - (24 + sizeof(DecodeRange)) * kDecodeMaxWarps);
   int4* held = reinterpret_cast<int4*>(misc + P::MISC_BYTES - 24 * kDecodeMaxWarps);
   long long* held_end = reinterpret_cast<long long*>(misc + P::MISC_BYTES - 8 * kDecodeMaxWarps);
+  // of this warp's unit: sequence, number, first step, how many steps of the range went before it: 0 or some
+  int4* unit = reinterpret_cast<int4*>(misc + P::MISC_BYTES - (16 + 24 + sizeof(DecodeRange)) * kDecodeMaxWarps) + warp;
   const int HU = p.Hkv * p.chunks;  // units of a sequence
   // this warp's part of a unit: heads g0 + sub * sub_rows ..; its range's place in the CTA
   const int R = NW / p4.subs, own = warp / p4.subs, sub = warp - own * p4.subs;
@@ -88,34 +90,38 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
     const int n = p.seq_lens[b];
     return n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
   };
-  auto steps_of = [](int len) { return (len + BN - 1) / BN; };
   struct Cursor {
-    int b, hu, t, nt, len;
+    int b, hu, t, len;
   };
   // the next step of the list (the caller knows that there is one)
-  auto advance = [&](Cursor& a) {
-    if (++a.t < a.nt) return;
+  auto next_unit = [&](Cursor& a) {
     a.t = 0;
     if (++a.hu < HU) return;
     a.hu = 0;
     while (a.b + 1 < p.B) {
       ++a.b;
       a.len = length(a.b);
-      a.nt = steps_of(a.len);
-      if (a.nt > 0) break;
+      if (a.len > 0) break;
     }
   };
-  auto lookup = [&](const Cursor& a) {
+  auto advance = [&](Cursor& a) {
+    ++a.t;
+    if (a.t * BN >= a.len) next_unit(a);
+  };
+  auto head_of = [&](const Cursor& a) {
     const int h = p.chunks == 1 ? a.hu : a.hu / p.chunks;
-    return lookup4(p, p.page_table + a.b * p.table_stride, a.t * BN, a.len, p4.heads > 1 ? h * p4.heads + sub : h);
+    return p4.heads > 1 ? h * p4.heads + sub : h;
+  };
+  auto lookup = [&](const Cursor& a) {
+    return lookup4(p, p.page_table + a.b * p.table_stride, a.t * BN, a.len, head_of(a));
   };
 
   // ---- this warp's range, and the places of its first steps
   const int me = blockIdx.x * R + own;
   DecodeRange w = p.wide ? decode_plan_wide<BN, NW>(p, words, R, own) : decode_plan<int, BN, NW>(p, words, R, own);
   const int count = w.count;
-  Cursor cur{w.b, w.hu, w.t, steps_of(w.len), w.len};  // the step computed next
-  Cursor ahead = cur;                                  // the step that `next` is of
+  Cursor ahead{w.b, w.hu, w.t, w.len};  // the step that `next` is of
+  int left = w.len - w.t * BN;          // keys of the unit from the step computed next on
   Place4 next, now[S - 1];
 #pragma unroll
   for (int j = 0; j < S; ++j) {
@@ -127,7 +133,10 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
   if (w.idle) decode_idle(p);
   if (p.split && !p.by_unit && sub == 0 && lane == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
   if (w.cta_lo >= w.total) return;
-  if (lane == 0) ranges[warp] = w;
+  if (lane == 0) {
+    ranges[warp] = w;
+    *unit = make_int4(w.b, w.hu, w.t, 0);
+  }
 
   float acc[NT][GV][4][4];  // [64 columns][product]: columns 8 g + 2 i of heads 2 t, 2 t + 1, then 8 g + 2 i + 1 (16-fold)
   // sum P' 8 (bf16): that of groups 2 k, in every row of the first eight, and 2 k + 1
@@ -155,10 +164,10 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
       }
     }
   };
-  auto load_q = [&](const Cursor& a) {
-    const int h = a.hu / p.chunks, g0 = (a.hu - h * p.chunks) * p.rows + sub * p4.sub_rows;
+  auto load_q = [&](const int4& a) {
+    const int h = a.y / p.chunks, g0 = (a.y - h * p.chunks) * p.rows + sub * p4.sub_rows;
     const int n_rows = min(p4.sub_rows, p.G - g0);
-    const uint16_t* base = p.q + a.b * p.qs[0] + (static_cast<long long>(h) * p.G + g0) * p.qs[1];
+    const uint16_t* base = p.q + a.x * p.qs[0] + (static_cast<long long>(h) * p.G + g0) * p.qs[1];
     q.template load<F16>(base, p.qs[1], n_rows, p.dqk, p.scale_log2);
   };
   auto write_row = [&](long long row, int col, float4 o, float mm, float ll) {
@@ -204,8 +213,7 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
   v_rows.init(p4.v);
   const uint32_t key_at = key_read<DQ>(), value_at = value_read<DV>();
   if (count > 0) {
-    auto issue = [&](const Place4& x, int stage) {
-      const uint32_t to = ring + stage * P::STAGE;
+    auto issue = [&](const Place4& x, uint32_t to) {
       const uint32_t tv = to + P::K_BYTES, ks = tv + P::V_BYTES, vs = ks + P::KS_BYTES;
       copy_tokens4(p, p4.narrow, x, [&](auto whole, const Place4& y, bool live) {
         if constexpr (decltype(whole)::value) {
@@ -219,24 +227,27 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
     };
 #pragma unroll
     for (int j = 0; j < S - 1; ++j) {
-      if (j < count) issue(now[j], j);
+      if (j < count) issue(now[j], ring + j * P::STAGE);
       cp_async_commit();
     }
 
-    int t0 = -1;  // first step of the unit in this warp; -1: this one
-    int stage = 0;
+    bool fresh = true;  // the step is the first of its unit here
+    uint32_t sk = ring;
 #pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-      if (t0 < 0) {
-        t0 = cur.t;
+    for (int steps = count; steps > 0; --steps) {  // left, this one among them
+      if (fresh) {
+        __syncwarp();
         clear();
-        load_q(cur);
+        load_q(*unit);
       }
       // refill the stage of the step before this one, which every lane has read
       __syncwarp();
-      if (i + S - 1 < count) {
-        issue(next, stage == 0 ? S - 1 : stage - 1);
-        if (i + S < count) {
+      if (steps >= S) {
+        // (the head and the length again: two registers less from step to step)
+        next.h = head_of(ahead);
+        next.n = ahead.len - ahead.t * BN;
+        issue(next, sk == ring ? ring + (S - 1) * P::STAGE : sk - P::STAGE);
+        if (steps > S) {
           advance(ahead);
           next = lookup(ahead);
         }
@@ -245,8 +256,7 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
       cp_async_wait<S - 1>();
       __syncwarp();
 
-      const uint32_t sk = ring + stage * P::STAGE, sv = sk + P::K_BYTES, sks = sv + P::V_BYTES, svs = sks + P::KS_BYTES;
-      const int live = cur.len - cur.t * BN;  // keys of this step
+      const uint32_t sv = sk + P::K_BYTES, sks = sv + P::V_BYTES, svs = sks + P::KS_BYTES;
       float s[2][NT][4];
       if constexpr (NT == 1 && DQ <= 128) {
         scores4<DQ, NT, 2>(q, sk + key_at, sks + g * (4 * P::GQ), 0, s);
@@ -265,14 +275,14 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
         if constexpr (GV >= 2) grows = above_half2(steps[0], most);
         if constexpr (GV == 4) grows = grows || above_half2(steps[1], most);
       }
-      if (live < BN) {
+      if (left < BN) {
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (16 * kt + g + (e >> 1) * 8 >= live) s[kt][n][e] = -INFINITY;
+              if (16 * kt + g + (e >> 1) * 8 >= left) s[kt][n][e] = -INFINITY;
       }
       float y[2][NT][4];
       auto less_m = [&]() {
@@ -423,17 +433,19 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
       }
 
       // ---- the unit ends here, or the range does
-      const bool last = i + 1 == count;
-      if (cur.t + 1 == cur.nt || last) {
-        const bool begins = t0 == 0;
+      const bool last = steps == 1;
+      fresh = left <= BN;
+      if (fresh || last) {
+        const int4 u = *unit;
+        const bool begins = u.z == 0;
         if (!last) {  // (the range's last unit is joined with the other warps' below; this one ends here)
-          const int h = cur.hu / p.chunks, g0 = (cur.hu - h * p.chunks) * p.rows + sub * p4.sub_rows;
+          const int h = u.y / p.chunks, g0 = (u.y - h * p.chunks) * p.rows + sub * p4.sub_rows;
           const int n_rows = min(p4.sub_rows, p.G - g0);
           const long long part0 = 2LL * me * p.rows + sub * p4.sub_rows;
-          const long long row0 = (static_cast<long long>(cur.b) * p.Hkv + h) * p.G + g0;
-          if (begins && sub == 0 && lane == 0) decode_complete(p, cur.b, cur.hu);
+          const long long row0 = (static_cast<long long>(u.x) * p.Hkv + h) * p.G + g0;
+          if (begins && sub == 0 && lane == 0) decode_complete(p, u.x, u.y);
           // this step's stage, which has been read and is refilled in the next step; where eight heads are larger, a place apart
-          float* scratch = reinterpret_cast<float*>(P::SPILL > P::STAGE ? mine + P::WARP_BYTES - P::SPILL : mine + stage * P::STAGE);
+          float* scratch = reinterpret_cast<float*>(P::SPILL > P::STAGE ? mine + P::WARP_BYTES - P::SPILL : mine + (sk - ring));
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             __syncwarp();
@@ -461,18 +473,19 @@ __global__ void __launch_bounds__(Decode4Plan<DQ, DV, NT>::NW * 32, 1)
         if (last) {
           if (sub == 0 && lane == 0) {
             // goes on where the range before has left off?
-            const bool goes_on = own > 0 && i == cur.t - t0 && t0 > 0;
-            held[own] = make_int4(cur.b, cur.hu, begins ? 1 : 0, goes_on ? 1 : 0);
-            held_end[own] = ranges[warp].lo + i + (cur.nt - 1 - cur.t);
+            held[own] = make_int4(u.x, u.y, begins ? 1 : 0, own > 0 && u.w == 0 && !begins ? 1 : 0);
+            held_end[own] = ranges[warp].lo + count - 1 + (left - 1) / BN;
           }
         } else {
-          advance(cur);
-          t0 = -1;
+          Cursor cur{u.x, u.y, 0, length(u.x)};
+          next_unit(cur);
+          left = cur.len + BN;  // (and this step's)
+          __syncwarp();
+          if (lane == 0) *unit = make_int4(cur.b, cur.hu, 0, 1);
         }
-      } else {
-        ++cur.t;
       }
-      stage = stage + 1 == S ? 0 : stage + 1;
+      left -= BN;
+      sk = sk == ring + (S - 1) * P::STAGE ? ring : sk + P::STAGE;
     }
   }
 
@@ -537,7 +550,7 @@ cudaError_t launch_decode4_nt(Decode4Params& p, int ctas, cudaStream_t stream) {
   DecodeParams& d = p.d;
   int subs = 1;
   if (d.chunks == 1) {
-    while (subs < 8 && P::NW % (2 * subs) == 0 && d.Hkv % (2 * subs) == 0) subs *= 2;
+    while (subs < 4 && P::NW % (2 * subs) == 0 && d.Hkv % (2 * subs) == 0) subs *= 2;
     p.heads = subs;
     d.Hkv /= subs;
     d.G *= subs;
@@ -556,13 +569,9 @@ cudaError_t launch_decode4_nt(Decode4Params& p, int ctas, cudaStream_t stream) {
 
 template <int DQ, int DV, bool F16>
 cudaError_t launch_decode4(Decode4Params& p, int nt, int ctas, cudaStream_t stream) {
-  constexpr int MOST = decode4_rows(DV) / 8;
   if (nt == 1) return launch_decode4_nt<DQ, DV, F16, 1>(p, ctas, stream);
-  if (nt == 2) return launch_decode4_nt<DQ, DV, F16, 2>(p, ctas, stream);
-  if constexpr (MOST >= 3)
-    if (nt == 3) return launch_decode4_nt<DQ, DV, F16, 3>(p, ctas, stream);
-  if constexpr (MOST >= 4)
-    if (nt == 4) return launch_decode4_nt<DQ, DV, F16, 4>(p, ctas, stream);
+  if constexpr (DV < 256)
+    if (nt == 2) return launch_decode4_nt<DQ, DV, F16, 2>(p, ctas, stream);
   return cudaErrorInvalidValue;
 }
 

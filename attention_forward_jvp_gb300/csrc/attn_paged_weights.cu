@@ -356,12 +356,14 @@ cudaError_t launch_nt(WeightParams p, int ctas, cudaStream_t stream) {
   return decode_launch_one(weights_kernel<DQ, BITS, F16, NT>, p, dim3(ctas), P::NW * 32, P::SMEM, stream);
 }
 
-// groups of 8 heads in registers: one, two or four (two at head dim 256)
+// groups of 8 heads in registers: one, two, or four (two at head dim 256 and of
+// a cache in 4 bits, whose operands take the rest)
 template <int DQ, int BITS, bool F16>
 cudaError_t launch_dq(const WeightParams& p, int ctas, cudaStream_t stream) {
+  constexpr int MOST = DQ == 256 || BITS == 4 ? 2 : 4;
   if (p.d.G <= 8) return launch_nt<DQ, BITS, F16, 1>(p, ctas, stream);
-  if (p.d.G <= 16 || DQ == 256) return launch_nt<DQ, BITS, F16, 2>(p, ctas, stream);
-  return launch_nt<DQ, BITS, F16, DQ == 256 ? 2 : 4>(p, ctas, stream);
+  if (p.d.G <= 16 || MOST == 2) return launch_nt<DQ, BITS, F16, 2>(p, ctas, stream);
+  return launch_nt<DQ, BITS, F16, MOST>(p, ctas, stream);
 }
 template <int BITS, bool F16>
 cudaError_t launch_bits(const WeightParams& p, int dq, int ctas, cudaStream_t stream) {
