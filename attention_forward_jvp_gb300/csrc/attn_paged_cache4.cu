@@ -180,7 +180,7 @@ __device__ __forceinline__ void store_row4(uint8_t* codes, uint16_t* scales, int
 }
 
 template <bool F16, bool VEC, int PAIRS>
-__global__ void __launch_bounds__(kWarps * 32, 4) append4_kernel(const __grid_constant__ Append4Params p4) {
+__global__ void __launch_bounds__(kWarps * 32, 3) append4_kernel(const __grid_constant__ Append4Params p4) {
   griddep_wait();
   griddep_launch_dependents();
   const AppendParams& p = p4.a;
@@ -218,20 +218,27 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append4_kernel(const __grid_co
     const int L = D / 8, R = 32 / L, d0 = 8 * (lane & (L - 1)), r = lane / L;
     x += r * each;
     each *= R;
-#pragma unroll 1
-    for (int h = r; h - r < n; h += R * U) {
-      uint4 w[U];
-      const uint16_t* y = x;
+    uint4 w[U];
+    auto load = [&](int h, const uint16_t* y) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         w[u] = load8<VEC>(y + d0, h + u * R < n);
         y += each;
       }
+    };
+    load(r, x);
+#pragma unroll 1
+    for (int h = r; h - r < n; h += R * U) {
+      uint4 now[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) now[u] = w[u];
+      if (VEC) load(h + R * U, x + U * each);  // the next ones, on their way meanwhile
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        use(w[u], x, h + u * R < n, d0);
+        use(now[u], x, h + u * R < n, d0);
         x += each;
       }
+      if (!VEC) load(h + R * U, x);
     }
   };
   // of the first row of this lane

@@ -368,36 +368,44 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 cudaError_t launch_evict(const EvictParams& p, int bits, int sms, cudaStream_t stream, int* launches) {
   *launches = 1;
   // A cluster of blocks for each head where heads are few and rows long: four
-  // rows of 131072 took 150 us with a block each.
-  const long long heads = static_cast<long long>(p.B) * p.Hkv;
-  int cluster = 1;
-  while (cluster < 8 && 2 * cluster * heads <= 2LL * sms && p.capacity > 2048 * cluster) cluster *= 2;
-  if (heads * cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const long long part = static_cast<long long>(p.capacity) / (cluster * kSelectWarps) + 33;  // of a warp, at most
-  const int room = static_cast<int>(part < kSelectMost ? (part + 255) / 256 * 256 : kSelectMost);
-  static bool attr_done[64] = {};
+  // rows of 131072 took 150 us with a block each.  Sixteen blocks (where the
+  // device can place them at all) for eight: 27 us for 36.
+  static int most[64] = {};  // blocks of a cluster, at most; 0: not looked up
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64) return cudaErrorInvalidDevice;
-  if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             4 * kSelectMost * kSelectWarps);
-    if (e != cudaSuccess) return e;
-    attr_done[dev] = true;
-  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(heads * cluster));
   cfg.blockDim = dim3(kSelectThreads);
-  cfg.dynamicSmemBytes = 4 * static_cast<size_t>(room) * kSelectWarps;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 16;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  constexpr size_t kNumber = 4 * kSelectWarps;  // bytes of a number of each warp
+  if (most[dev] == 0) {
+    e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNumber * kSelectMost);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(16);
+    cfg.dynamicSmemBytes = kNumber * kSelectMost;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    const bool fits = cudaOccupancyMaxActiveClusters(&clusters, select_kernel, &cfg) == cudaSuccess && clusters > 0;
+    most[dev] = fits ? 16 : 8;
+  }
+  const long long heads = static_cast<long long>(p.B) * p.Hkv;
+  int cluster = 1;
+  while (cluster < most[dev] && 2 * cluster * heads <= 2LL * sms && p.capacity > 2048 * cluster) cluster *= 2;
+  if (heads * cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long part = static_cast<long long>(p.capacity) / (cluster * kSelectWarps) + 33;  // of a warp, at most
+  const int room = static_cast<int>(part < kSelectMost ? (part + 255) / 256 * 256 : kSelectMost);
+  cfg.gridDim = dim3(static_cast<unsigned>(heads * cluster));
+  cfg.dynamicSmemBytes = kNumber * room;
+  attr[0].val.clusterDim.x = cluster;
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, select_kernel, p, room);
   if (e != cudaSuccess) return e;
@@ -408,6 +416,7 @@ cudaError_t launch_evict(const EvictParams& p, int bits, int sms, cudaStream_t s
   cfg.gridDim = dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)), 2);
   cfg.blockDim = dim3(kMoveThreads);
   cfg.dynamicSmemBytes = 0;
+  cfg.attrs = attr + 1;  // (no clusters)
   cfg.numAttrs = 1;
   *launches = 2;
   return bits == 4 ? cudaLaunchKernelEx(&cfg, move_kernel<4>, p, chunks, blocks)
