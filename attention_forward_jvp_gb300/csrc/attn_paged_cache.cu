@@ -359,6 +359,7 @@ attn_status run_weights(const C* c, WeightParams& p, int bits, int32_t Hq, const
   for (int i = 0; i < 3; ++i) below = below && p.d.kp[i] >= 0 && p.d.kp[i] < (1 << 30);
   p.narrow = p.d.whole && (bits == 4 ? narrow(p.k) : below) && c->Dqk >= 64 ? 1 : 0;
   p.f16 = f16 ? 1 : 0;
+  p.scale = std::isnan(sm_scale) ? 1.0f / std::sqrt(static_cast<float>(c->Dqk)) : sm_scale;
   p.lse = w->lse;
   p.w = w->w;
   p.out = w->out;

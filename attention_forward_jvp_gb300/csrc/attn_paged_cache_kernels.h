@@ -77,6 +77,7 @@ struct WeightParams {
   int narrow;         // copy_tokens4
   int subs;           // set by the launch: warps of a range, each with a key head of its own
   int f16;            // the type of q
+  float scale;        // of the scores
   const float* lse;   // [B, Hkv * G]
   const float* w;     // or null
   float* out;

@@ -241,7 +241,7 @@ struct Query4 {
 
   // rows n_rows .. are zero; base: the first head's row, d: real elements
   template <bool F16>
-  __device__ __forceinline__ void load(const uint16_t* base, long long stride, int n_rows, int d, float scale_log2) {
+  __device__ __forceinline__ void load(const uint16_t* base, long long stride, int n_rows, int d, float scale_all) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -296,7 +296,7 @@ struct Query4 {
       const float s0 = t == 0 ? sums[0] : (GQ > 2 && t == 1 ? sums[GQ > 2 ? 2 : 0] : 0.f);
       const float s1 = GQ > 1 && t == 0 ? sums[GQ > 1 ? 1 : 0] : (GQ > 2 && t == 1 ? sums[GQ > 2 ? 3 : 0] : 0.f);
       split2<true>(s0, s1, sum[n][0], sum[n][1]);
-      const float back = down * scale_log2;
+      const float back = down * scale_all;
       scale[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
       scale[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }

@@ -3,8 +3,9 @@
 //   out_j = decay w_j + sum over the query heads of exp(s q k_j - lse)
 //
 // One pass over the keys: the scores by mma.sync with 16 keys as the rows and
-// 8 heads as the columns, as in the decode kernels, then exp2 of their distance
-// to the LSE and a sum over the columns.  No maximum and nothing to join: the
+// 8 heads as the columns, as in the decode kernels, then the exponential of their
+// distance to the LSE and a sum over the columns.  (The distance is taken before
+// log2(e) is: scores of 30 times a rounded factor are off by 2^-19.)  No maximum and nothing to join: the
 // LSE is given, and a key's sum is one warp's, in one order.
 //
 // What bounds it: memory, the keys once.  The list of steps, its cut into
@@ -195,25 +196,26 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
   constexpr float kLog2e = 1.4426950408889634f;
   Query4<DQ, BITS == 4 ? NT : 1> q4;
   uint32_t q16[BITS == 16 ? DQ / 16 : 1][NT][2];
-  float lse[NT][2];  // of heads 2 t, 2 t + 1, times log2(e)
+  float lse[NT][2];  // of heads 2 t, 2 t + 1
   auto load_heads = [&](const Cursor& a, int g0) {
     const long long head = (static_cast<long long>(a.h) * pw.subs + sub) * p.G + g0;
     const uint16_t* base = p.q + a.b * p.qs[0] + head * p.qs[1];
     const int n_rows = p.G - g0;
     if constexpr (BITS == 4) {
-      if (pw.f16) q4.template load<true>(base, p.qs[1], n_rows, p.dqk, p.scale_log2);
-      else q4.template load<false>(base, p.qs[1], n_rows, p.dqk, p.scale_log2);
+      if (pw.f16) q4.template load<true>(base, p.qs[1], n_rows, p.dqk, pw.scale);
+      else q4.template load<false>(base, p.qs[1], n_rows, p.dqk, pw.scale);
     } else {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const bool in = 8 * n + g < n_rows;
-        const uint16_t* row = base + (in ? 8 * n + g : 0) * p.qs[1];
+        // (behind the last head the first again, without weight: zeros would make
+        // NaN of an infinite key)
+        const uint16_t* row = base + (8 * n + g < n_rows ? 8 * n + g : 0) * p.qs[1];
 #pragma unroll
         for (int ks = 0; ks < DQ / 16; ++ks)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int d = 16 * ks + 8 * e + 2 * t;
-            q16[ks][n][e] = in && d < p.dqk ? *reinterpret_cast<const uint32_t*>(row + d) : 0u;
+            q16[ks][n][e] = n_rows > 0 && d < p.dqk ? *reinterpret_cast<const uint32_t*>(row + d) : 0u;
           }
       }
     }
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
         const int r = 8 * n + 2 * t + e;
         float x = INFINITY;  // (a head that is none, or without keys: no weight)
         if (r < n_rows) {
-          x = pw.lse[static_cast<long long>(a.b) * p.Hkv * pw.subs * p.G + head + r] * kLog2e;
+          x = pw.lse[static_cast<long long>(a.b) * p.Hkv * pw.subs * p.G + head + r];
           if (x == -INFINITY) x = INFINITY;
         }
         lse[n][e] = x;
@@ -312,8 +314,8 @@ __global__ void __launch_bounds__(WeightPlan<DQ, BITS, NT>::NW * 32, 1)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float scale = BITS == 4 ? q4.scale[BITS == 4 ? n : 0][e & 1] : p.scale_log2;
-            sum[kt][e >> 1] += exp2_fast(fmaf(s[n][e], scale, -lse[n][e & 1]));
+            const float scale = BITS == 4 ? q4.scale[BITS == 4 ? n : 0][e & 1] : pw.scale;
+            sum[kt][e >> 1] += exp2_fast(fmaf(s[n][e], scale, -lse[n][e & 1]) * kLog2e);
           }
       }
     }

@@ -559,6 +559,25 @@ def test_weights_splits_decay_nothing_and_empty_heads(four):
     assert (big[:, [0, 3]] == 9).all() and (big[:, :, :2] == 9).all() and (big[:, :, -1:] == 9).all()
 
 
+@pytest.mark.parametrize("dims", [64, 256])
+@pytest.mark.parametrize("group", [1, 5, 8])
+def test_weights_of_keys_with_infinite_scores(dims, group):
+    """A key whose score is -inf has no weight and leaves the others as they are,
+    in whatever number of heads."""
+    pool = Pool([40], 1, dims, 64, 16, BF, seed=group, four=False)
+    q = randn((1, group, dims), BF, 1).abs() + 0.5
+    for at in (0, 17, 39):  # positive queries
+        page, slot = int(pool.table[0, at // 16]), at % 16
+        pool.parts[0][0][page, 0, slot, 3 * at % dims] = -math.inf
+    _, lse = binding.attn_paged_decode(pool.cache, q)
+    out = binding.attn_paged_weights(pool.cache, q, lse)
+    assert torch.isfinite(lse).all() and torch.isfinite(out).all()
+    assert (out[0, 0, [0, 17, 39]] == 0).all()
+    # each head's weights add up to 1: 40 of 2^-24 each, the score's products and the LSE's rounding
+    d = (dims + 8) * 2.0**-22 * dims**-0.5 * float((q.double()[0].abs().sum(-1) * 6).max()) + 2.0**-18
+    assert abs(float(out[0, 0, :40].double().sum()) - group) <= group * d
+
+
 @pytest.mark.parametrize("four", [True, False])
 def test_weights_bad_pages_and_lengths_are_reported(four):
     pool = Pool([100, 64], 1, 64, 64, 16, BF, seed=5, extra=0, four=four)
