@@ -8,8 +8,11 @@
 // a half (it is off by 4 10^-6 at most), and is divided where it does.  Eight
 // elements to a thread, the row of a head to D / 8 neighbouring lanes of one
 // warp: the group's extremes come from three exchanges between lanes, and the
-// element that x turns with from another lane of the row.  A warp takes heads
-// of one token, whose angles it computes once, the rows of several on their way.
+// element that x turns with from another lane of the row.  A warp takes heads of
+// one token.  Its rows go to L2 while the place is looked up; each of its angles is
+// worked out by one lane and shared (by every lane that needs it: 65 us for 61,
+// 10360 tokens of 16 + 8 heads, 256/128, with the gather behind it; half the heads
+// to a warp then takes 63, four blocks an SM, with fewer registers, 65).
 //
 // Gather: a thread owns sixteen elements of one token and walks over the heads,
 // the loads of several on their way; what it writes is a whole 32-byte sector.
@@ -75,18 +78,22 @@ struct Turn8 {
   int rot, d0;
   bool any;  // some of this lane's elements turn
 
-  __device__ __forceinline__ void angles(const RopeSpec& r, int first, int pos) {
+  // table: of the warp, for the row's pairs (each is worked out once; all lanes take part)
+  __device__ __forceinline__ void angles(const RopeSpec& r, int first, int pos, float2* table) {
     if constexpr (PAIRS != kStill) {
       rot = r.rot;
       d0 = first;
       any = d0 < rot;
       const int half = rot / 2;
+#pragma unroll 1
+      for (int i = threadIdx.x & 31; i < half; i += 32) table[i] = turn_close(r, i, pos);
+      __syncwarp();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int d = d0 + j;
         cs[j] = make_float2(1.f, 0.f);
         if (d < rot) {
-          cs[j] = turn(r, PAIRS == kNeighbours ? d >> 1 : (d < half ? d : d - half), pos);
+          cs[j] = table[PAIRS == kNeighbours ? d >> 1 : (d < half ? d : d - half)];
           // x cos - other sin; the second of a pair x cos + other sin
           if (PAIRS == kNeighbours ? !(j & 1) : d < half) cs[j].y = -cs[j].y;
         }
@@ -181,70 +188,86 @@ __device__ __forceinline__ void store_row4(uint8_t* codes, uint16_t* scales, int
 
 template <bool F16, bool VEC, int PAIRS>
 __global__ void __launch_bounds__(kWarps * 32, 3) append4_kernel(const __grid_constant__ Append4Params p4) {
+  __shared__ float2 table[kWarps][PAIRS == kStill ? 1 : 128];  // cos and sin of each warp's token
   griddep_wait();
   griddep_launch_dependents();
   const AppendParams& p = p4.a;
   const int lane = threadIdx.x & 31;
   const long long t = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (t >= p.T) return;
-  // the token's sequence and position
-  long long b = t, pos = 0;
-  bool idle = false;
-  if (p.offsets != nullptr) {
-    if (t >= p.offsets[p.B]) return;
-    b = sequence_of(p.offsets, p.B, t);
-    pos = p.seq_lens[b] - static_cast<long long>(p.offsets[b + 1]) + t;
-  } else {
-    pos = static_cast<long long>(p.seq_lens[b]) - 1;
-    idle = pos == -1;
+  const int first = blockIdx.y * p.heads_per_split;
+  const int last = min(first + p.heads_per_split, p.Hq + 2 * p.Hkv);
+  if constexpr (VEC) {  // the rows to L2, while the token's place is looked up
+    for (int h = first + lane; h < last; h += 32) {
+      const bool q = h < p.Hq, k = h < p.Hq + p.Hkv;
+      const uint16_t* row = q ? p.q + t * p.qs[0] + h * p.qs[1]
+                              : (k ? p.k + t * p.ks[0] + (h - p.Hq) * p.ks[1]
+                                   : p.v + t * p.vs[0] + (h - p.Hq - p.Hkv) * p.vs[1]);
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row), "r"(2 * (k ? p.Dqk : p.Dv)) : "memory");
+    }
   }
-  // its place in the pool
-  long long page = -1, slot = 0;
+  // the token's sequence, position and page
+  int b, pos;
+  if (p.offsets != nullptr) {
+    int n = p.B, end = 0x7fffffff, len = 0;
+    const int all = p.offsets[p.B];
+    b = 0;  // the one sought is in [b, b + n)
+    while (n > 32) {
+      const int k = (n + 31) / 32;
+      const bool below = lane * k < n && p.offsets[b + lane * k] <= t;
+      const int c = max(__popc(__ballot_sync(kAll, below)) - 1, 0);
+      b += c * k;
+      n = min(k, n - c * k);
+    }
+    if (lane < n) {  // (ends and lengths in one round)
+      end = p.offsets[b + lane + 1];
+      len = p.seq_lens[b + lane];
+    }
+    const int c = min(__popc(__ballot_sync(kAll, end <= t)), n - 1);
+    if (t >= all) return;
+    b += c;
+    const long long x = __shfl_sync(kAll, len, c) - static_cast<long long>(__shfl_sync(kAll, end, c)) + t;
+    pos = static_cast<int>(max(min(x, 0x7fffffffLL), -2LL));
+  } else {
+    b = static_cast<int>(t);
+    pos = max(p.seq_lens[b], -1) - 1;
+  }
+  const bool idle = p.offsets == nullptr && pos == -1;
+  int page = -1, slot = 0;
   if (pos >= 0 && pos < static_cast<long long>(p.max_pages) * p.page_size) {
-    const int e = static_cast<int>(pos / p.page_size);
-    slot = pos - static_cast<long long>(e) * p.page_size;
+    const int e = pos / p.page_size;
+    slot = pos - e * p.page_size;
     page = p.page_table[b * p.table_stride + e];
   }
-  const bool placed = page >= 0 && page < p.n_pages;
-  if (!placed && !idle && lane == 0 && blockIdx.y == 0) *p.err = 1;
 
   // heads of q, of k and of v, one after the other: `use` for each row that
   // this lane has eight elements of, those of U rows on their way; R rows at a
   // time, in steps of `each` elements
   constexpr int U = VEC ? kAppendUnroll : 1;
-  const int first = blockIdx.y * p.heads_per_split;
-  const int last = min(first + p.heads_per_split, p.Hq + 2 * p.Hkv);
   auto heads = [&](const uint16_t* x, long long each, int D, int n, auto use) {
     const int L = D / 8, R = 32 / L, d0 = 8 * (lane & (L - 1)), r = lane / L;
     x += r * each;
     each *= R;
-    uint4 w[U];
-    auto load = [&](int h, const uint16_t* y) {
+#pragma unroll 1
+    for (int h = r; h - r < n; h += R * U) {
+      uint4 w[U];
+      const uint16_t* y = x;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         w[u] = load8<VEC>(y + d0, h + u * R < n);
         y += each;
       }
-    };
-    load(r, x);
-#pragma unroll 1
-    for (int h = r; h - r < n; h += R * U) {
-      uint4 now[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) now[u] = w[u];
-      if (VEC) load(h + R * U, x + U * each);  // the next ones, on their way meanwhile
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        use(now[u], x, h + u * R < n, d0);
+        use(w[u], x, h + u * R < n, d0);
         x += each;
       }
-      if (!VEC) load(h + R * U, x);
     }
   };
   // of the first row of this lane
   const int Lk = p.Dqk / 8, rk = lane / Lk, dk = 8 * (lane & (Lk - 1)), Lv = p.Dv / 8, rv = lane / Lv, dv = 8 * (lane & (Lv - 1));
   Turn8<F16, VEC, PAIRS> turned;
-  if (first < p.Hq + p.Hkv) turned.angles(p.r, dk, static_cast<int>(pos));
+  if (first < p.Hq + p.Hkv) turned.angles(p.r, dk, pos, table[threadIdx.x >> 5]);
   {
     const int lo = first, n = min(last, p.Hq) - lo;
     uint16_t* y = p.q_out + t * p.qos[0] + (lo + rk) * p.qos[1] + dk;
@@ -262,6 +285,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) append4_kernel(const __grid_co
       for (int h = rk; h < n; h += 32 / Lk, y += each) store8<F16, VEC>(y, zero);
     }
   }
+  const bool placed = page >= 0 && page < p.n_pages;
+  if (!placed && !idle && lane == 0 && blockIdx.y == 0) *p.err = 1;
   if (!placed) return;
   {
     const int lo = max(first - p.Hq, 0), n = min(last - p.Hq, p.Hkv) - lo;
@@ -381,8 +406,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
   const long long pos = p.seq_lens[b] - static_cast<long long>(p.offsets[b + 1]) + t;
   long long page = -1, slot = 0;
   if (pos >= 0 && pos < static_cast<long long>(p.max_pages) * p.page_size) {
-    const int e = static_cast<int>(pos / p.page_size);
-    slot = pos - static_cast<long long>(e) * p.page_size;
+    const int e = static_cast<int>(pos) / p.page_size;
+    slot = static_cast<int>(pos) - e * p.page_size;
     page = p.page_table[b * p.table_stride + e];
   }
   const bool placed = page >= 0 && page < p.n_pages;

@@ -39,6 +39,22 @@ __device__ __forceinline__ float2 turn(const RopeSpec& r, int pair, int pos) {
   return make_float2(c * r.scale, s * r.scale);
 }
 
+// The same to the last bits, for a rounding to 4 bits, which has steps that
+// __sincosf's error takes one more time in 10^5 to the wrong side of: the nearest
+// quarter of a turn in whole numbers, and CUDA's sincospif of what is left.
+__device__ __forceinline__ float2 turn_close(const RopeSpec& r, int pair, int pos) {
+  const unsigned long long ph =
+      r.steps[pair] * static_cast<unsigned long long>(static_cast<long long>(pos));
+  const uint32_t at = static_cast<uint32_t>(ph >> 32), quarter = (at + 0x20000000u) >> 30;
+  float s, c;
+  sincospif(static_cast<float>(static_cast<int>(at - (quarter << 30))) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+  const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
+  c = (quarter + 1) & 2 ? -x : x;
+  s = quarter & 2 ? -y : y;
+  if (r.inverse) s = -s;
+  return make_float2(c * r.scale, s * r.scale);
+}
+
 // The sequence of packed token t, the last b < n_seq with offsets[b] <= t,
 // for a whole warp: 32 offsets at a time for the first lane's token, then
 // step by step for the others', which lie behind it (or have no part in the
