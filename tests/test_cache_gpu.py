@@ -304,6 +304,48 @@ def test_append_bad_places_are_reported_and_left_out(what):
     assert (y[0] == 0).all() if what == "length" else torch.equal(y, q)
 
 
+@pytest.mark.parametrize("B", [1, 32, 33, 100, 1100])
+def test_append_and_gather_find_a_token_among_many_sequences(B):
+    r = np.random.RandomState(B)
+    lens = [int(n) for n in r.randint(0, 7, B)]
+    lens[-1] = 3 if B % 2 else 0
+    new = [int(r.randint(0, n + 1)) if r.rand() < 0.7 else 0 for n in lens]
+    new[0] = lens[0] = 2  # some at the first sequence, and a stretch of empty ones
+    new[B // 3 + 1 : B // 2] = [0] * len(new[B // 3 + 1 : B // 2])
+    pool = Pool(lens, 1, 64, 32, 4, BF, seed=B)
+    T = sum(new)
+    k, v, q = (randn((T, h, d), BF, d + h) for h, d in ((1, 64), (1, 32), (2, 64)))
+    off = ints([0] + new).cumsum(0).int()
+    rope = binding.Rope(64)
+    y = binding.attn_paged_append(pool.cache, k, v, rope=rope, q=q, offsets=off)
+    assert binding.sync_check() == 0
+    pos = [n - m + j for n, m in zip(lens, new) for j in range(m)]
+    seq = [b for b, m in enumerate(new) for _ in range(m)]
+    Q, i = f64(q), np.arange(32)
+    a = np.array(pos)[:, None, None] * f64(rope.inv_freq)
+    c, s = np.cos(a), np.sin(a)
+    turned = np.concatenate([Q[..., i] * c - Q[..., 32 + i] * s, Q[..., 32 + i] * c + Q[..., i] * s], -1)
+    size = np.tile(np.abs(Q[..., :32]) + np.abs(Q[..., 32:]), 2)
+    assert (np.abs(f64(y) - turned) <= torch.finfo(BF).eps / 2 * np.abs(turned) + 1e-6 * size + 2.0**-130).all()
+    n, st, least = cache_ref.round4(f64(v))
+    table, (codes, scale) = pool.table.cpu().numpy(), pool.parts[1]
+    pages, slots = [int(table[b, p // 4]) for b, p in zip(seq, pos)], [p % 4 for p in pos]
+    assert (codes[pages, 0, slots].cpu().numpy() == cache_ref.pack4(n)[:, 0]).all()
+    assert (scale[pages, 0, slots].cpu().numpy() == np.stack([st, least], 2)[:, 0]).all()
+    _, gv = binding.attn_paged_gather(pool.cache, off, T)
+    assert torch.equal(gv[0].cpu(), torch.from_numpy(cache_ref.values4(n, st, least)[:, 0]).float().to(BF))
+
+
+def test_append_of_negative_lengths_is_reported():
+    pool = Pool([3, 3, 3], 1, 64, 64, 4, seed=1)
+    pool.seq_lens.copy_(ints([-1, 0, -2**31]))
+    x = randn((3, 1, 64), BF, 1)
+    before = pool.bits()
+    assert (binding.attn_paged_append(pool.cache, x, x, q=x.clone()) == 0).all()
+    assert binding.sync_check() == 6
+    assert all(torch.equal(a, b) for a, b in zip(before, pool.bits()))
+
+
 # ------------------------------------------------------------------ gather
 @pytest.mark.parametrize("four,dims,dt", [(True, (64, 64), BF), (True, (128, 32), HF), (True, (32, 256), BF),
                                           (True, (256, 128), HF), (False, (16, 64), BF), (False, (128, 256), HF)])
