@@ -19,8 +19,10 @@
 // (A warp that looks up 32 tokens and moves their rows one after the other has
 // fewer bytes on their way: 43 us for 37, a prefix of 30001 tokens.)
 //
-// Both are bound by memory: a new token's row is read in 16 bits and written in
-// 4.5, the gather's read in 4.5 or 16 and written in 16.
+// The gather is bound by memory, its rows read in 4.5 or 16 bits and written in 16:
+// 71202 tokens of eight heads of 128 in 16 bits 86 us (6.8 TB/s), 30001 out of 4
+// bits 29 us (5.5).  The append, read in 16 bits and written in 4.5, takes 58 % of
+// the issue slots: the 10360 tokens 51 us (4.1 TB/s).
 #include <type_traits>
 
 #include "attn_paged_cache_kernels.h"

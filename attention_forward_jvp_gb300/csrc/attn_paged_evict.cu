@@ -3,7 +3,7 @@
 // weights, the first and the last, copied in their order into fewer pages.
 //
 // Two kernels.  `select` has a block for each (sequence, key head), or a cluster
-// of up to eight where there are few: a radix selection of the M-th largest
+// of up to sixteen where there are few: a radix selection of the M-th largest
 // weight in three passes (12, 10 and 10 bits) over weights turned to whole
 // numbers of the same order, held in shared memory where they fit; the blocks of
 // a cluster add up their histograms from one another's shared memory.  Then the
@@ -15,7 +15,10 @@
 // warp looks up 32 of them at once, then moves whole rows, 16 bytes a lane,
 // several of them on their way.
 //
-// What bounds it: memory, the kept rows read and written once.
+// What bounds it: memory, the kept rows read and written once, and before it the
+// selection's chain of passes and barriers.  32 sequences of up to 8192 to 2048,
+// eight heads of 128 in 16 bits: select 22 us, move 68 (403 MB); one of 131071 to
+// 32768, four heads in 4 bits: 26 and 16.
 #include "attn_paged_cache_kernels.h"
 #include "ptx.cuh"
 
